@@ -21,7 +21,10 @@ EXPORTED = ("gdn_opts_init", "gdn_chunk_fwd", "gdn_chunk_fwd_workspace_size", "g
             "gdn_chunk_fwd_noalloc", "gdn_causal_conv1d_fwd", "gdn_causal_conv1d_step",
             "gdn_recurrent_bwd", "gdn_recurrent_bwd_workspace_size", "gdn_causal_conv1d_fwd_qkv",
             "gdn_causal_conv1d_step_qkv", "gdn_output_gate_fwd", "gdn_output_gate_bwd",
-            "gdn_output_gate_bwd_workspace_size", "gdn_causal_conv1d_bwd", "gdn_causal_conv1d_bwd_workspace_size")
+            "gdn_output_gate_bwd_workspace_size", "gdn_causal_conv1d_bwd", "gdn_causal_conv1d_bwd_workspace_size",
+            "gdn_decay_attn_fwd", "gdn_decay_attn_fwd_workspace_size", "gdn_decay_attn_step", "gdn_decay_attn_bwd",
+            "gdn_decay_attn_bwd_workspace_size", "gdn_block_norm_fwd", "gdn_block_norm_bwd",
+            "gdn_block_norm_bwd_workspace_size")
 
 
 class GdnOpts(ctypes.Structure):
@@ -100,6 +103,22 @@ def load(path: str = LIB_PATH):
     lib.gdn_chunk_fwd_workspace_size.restype = ctypes.c_size_t
     lib.gdn_recurrent_step.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, opts_p]
     lib.gdn_recurrent_step.restype = i
+    lib.gdn_decay_attn_fwd.argtypes = [vp, ll, vp, ll, vp, ll, vp, vp, vp, vp, i, i, i, i, i, i, opts_p]
+    lib.gdn_decay_attn_fwd.restype = i
+    lib.gdn_decay_attn_step.argtypes = [vp, ll, vp, ll, vp, ll, vp, vp, vp, i, vp, i, i, i, i, i, opts_p]
+    lib.gdn_decay_attn_step.restype = i
+    lib.gdn_decay_attn_bwd.argtypes = [vp, ll, vp, ll, vp, ll, vp, vp, vp, vp, vp, ll, vp, ll, vp, ll, vp,
+                                       i, i, i, i, i, i, opts_p]
+    lib.gdn_decay_attn_bwd.restype = i
+    for size in (lib.gdn_decay_attn_fwd_workspace_size, lib.gdn_decay_attn_bwd_workspace_size):
+        size.argtypes = [i, i, i, i, i, i, opts_p]
+        size.restype = ctypes.c_size_t
+    lib.gdn_block_norm_fwd.argtypes = [vp, vp, vp, i, vp, vp, vp, vp, vp, ll, i, opts_p]
+    lib.gdn_block_norm_fwd.restype = i
+    lib.gdn_block_norm_bwd.argtypes = [vp, vp, vp, i] + [vp] * 11 + [ll, i, opts_p]
+    lib.gdn_block_norm_bwd.restype = i
+    lib.gdn_block_norm_bwd_workspace_size.argtypes = [ll, i, opts_p]
+    lib.gdn_block_norm_bwd_workspace_size.restype = ctypes.c_size_t
     lib.gdn_check_device_status.argtypes = [vp]
     lib.gdn_check_device_status.restype = i
     lib.gdn_status_string.argtypes = [i]

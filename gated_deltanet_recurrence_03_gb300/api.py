@@ -512,3 +512,234 @@ def gdn_output_gate_bwd(o: torch.Tensor, z: torch.Tensor, norm_weight: torch.Ten
         del keep
         L.check(lib, st)
     return go, gz, gw
+
+
+def _token_rows(name, t, lead):
+    """Elements between consecutive token rows of t ([*lead, heads, features] with contiguous heads, token
+    rows evenly strided: a dense tensor or a slice of a packed projection)."""
+    d, H = t.shape[-1], t.shape[-2]
+    ok = t.stride(-1) == 1 and (H == 1 or t.stride(-2) == d)
+    row = t.stride(-3) if t.shape[-3] > 1 else (t.stride(0) if lead == 2 and t.shape[0] > 1 else H * d)
+    if ok and lead == 2 and t.shape[0] > 1:
+        ok = t.stride(0) == t.shape[1] * row
+    if t.numel() and not ok:
+        raise ValueError(f"{name} must have contiguous heads and evenly strided token rows")
+    return row if t.numel() else H * d
+
+
+def _decay_inputs(q, k, v, log_decay, lead):
+    """Shapes and row strides of the decayed attention's inputs (``lead`` leading dimensions)."""
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
+        if t.dim() != lead + 2:
+            raise ValueError(f"{name} must be {lead + 2}-D [{'B, T' if lead == 2 else 'N'}, H, d]")
+    dev, dt = q.device, q.dtype
+    if dt not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
+    if k.shape != q.shape:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected {tuple(q.shape)}")
+    if v.shape[:lead] != q.shape[:lead]:
+        raise ValueError(f"v has shape {tuple(v.shape)}, expected leading {tuple(q.shape[:lead])}")
+    for name, t in (("k", k), ("v", v)):
+        if t.device != dev or t.dtype != dt:
+            raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {dt} on {dev}")
+    Hqk, dk = q.shape[-2:]
+    Hv, dv = v.shape[-2:]
+    _need("log_decay", log_decay, torch.float32, dev, (Hv,))
+    return dev, dt, Hqk, Hv, dk, dv, tuple(_token_rows(n, t, lead) for n, t in (("q", q), ("k", k), ("v", v)))
+
+
+def _scratch(o, need, workspace, dev):
+    """Point the options at a workspace of at least ``need`` bytes; returns the tensor to keep alive."""
+    if not need:
+        return None
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    o.workspace = workspace.data_ptr()
+    o.workspace_bytes = workspace.numel() * workspace.element_size()
+    return workspace
+
+
+def _packed(o, cu_seqlens, B, dev):
+    """Number of sequences; a packed call's offsets go into the options."""
+    if cu_seqlens is None:
+        return B
+    if cu_seqlens.dim() != 1:
+        raise ValueError("cu_seqlens must be 1-D")
+    nseq = int(cu_seqlens.numel()) - 1
+    _need("cu_seqlens", cu_seqlens, torch.int32, dev, (nseq + 1,))
+    o.cu_seqlens = cu_seqlens.data_ptr()
+    o.num_seqs = nseq
+    return nseq
+
+
+def gdn_decay_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                       S0: Optional[torch.Tensor] = None, *, scale: float = 1.0,
+                       cu_seqlens: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                       S_final: Optional[torch.Tensor] = None, output_final_state: bool = True,
+                       workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                       events: Optional[Sequence[int]] = None):
+    """Linear attention with a decay for each value head, over whole sequences: S <- exp(log_decay[h]) S +
+    k v^T, out = scale S^T q.  q, k [B, T, Hqk, dk]; v [B, T, Hv, dv] (bf16 or fp32; slices of a packed
+    projection are taken as they are); log_decay fp32 [Hv] (<= 0); S0 [nseq, Hv, dk, dv] fp32 or None.  With
+    ``cu_seqlens`` (int32 device tensor of nseq+1 offsets) B must be 1.  Returns (out [B, T, Hv, dv],
+    S_final or None)."""
+    lib = L.load()
+    dev, dt, Hqk, Hv, dk, dv, strides = _decay_inputs(q, k, v, log_decay, 2)
+    B, T = q.shape[:2]
+    with torch.cuda.device(dev):
+        o, keep = _opts(lib, dt, scale, 64, False, stream, dev, events)
+        nseq = _packed(o, cu_seqlens, B, dev)
+        if S0 is not None:
+            _need("S0", S0, torch.float32, dev, (nseq, Hv, dk, dv))
+        if out is None:
+            out = torch.empty((B, T, Hv, dv), dtype=dt, device=dev)
+        else:
+            _need("out", out, dt, dev, (B, T, Hv, dv))
+        if S_final is not None:
+            _need("S_final", S_final, torch.float32, dev, (nseq, Hv, dk, dv))
+        elif output_final_state:
+            S_final = torch.empty((nseq, Hv, dk, dv), dtype=torch.float32, device=dev)
+        workspace = _scratch(o, int(lib.gdn_decay_attn_fwd_workspace_size(B, T, Hqk, Hv, dk, dv, ctypes.byref(o))),
+                             workspace, dev)
+        st = lib.gdn_decay_attn_fwd(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], _ptr(log_decay),
+                                    _ptr(S0), _ptr(out), _ptr(S_final), B, T, Hqk, Hv, dk, dv, ctypes.byref(o))
+        del keep
+        L.check(lib, st)
+    return out, S_final
+
+
+def gdn_decay_attn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, S: torch.Tensor,
+                        *, slots: Optional[torch.Tensor] = None, scale: float = 1.0,
+                        out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                        events: Optional[Sequence[int]] = None) -> torch.Tensor:
+    """One token for each of N rows through gdn_decay_attn_fwd's recurrence.  q, k [N, Hqk, dk]; v [N, Hv, dv];
+    S [pool, Hv, dk, dv] fp32, updated in place.  ``slots`` (int32 [N]) names each row's state in the pool
+    (None: row n, state n); a row whose slot is outside the pool (-1, say) is idle and gets zeros.  Returns
+    out [N, Hv, dv]."""
+    lib = L.load()
+    dev, dt, Hqk, Hv, dk, dv, strides = _decay_inputs(q, k, v, log_decay, 1)
+    N = q.shape[0]
+    pool = S.shape[0] if slots is not None and S.dim() == 4 else N
+    _need("S", S, torch.float32, dev, (pool, Hv, dk, dv))
+    if slots is not None:
+        _need("slots", slots, torch.int32, dev, (N,))
+    if out is None:
+        out = torch.empty((N, Hv, dv), dtype=dt, device=dev)
+    else:
+        _need("out", out, dt, dev, (N, Hv, dv))
+    with torch.cuda.device(dev):
+        o, keep = _opts(lib, dt, scale, 64, False, stream, dev, events)
+        st = lib.gdn_decay_attn_step(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], _ptr(log_decay),
+                                     _ptr(S), _ptr(slots), pool, _ptr(out), N, Hqk, Hv, dk, dv, ctypes.byref(o))
+        del keep
+        L.check(lib, st)
+    return out
+
+
+def gdn_decay_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                       S0: Optional[torch.Tensor], grad_out: torch.Tensor,
+                       grad_S_final: Optional[torch.Tensor] = None, *, scale: float = 1.0,
+                       cu_seqlens: Optional[torch.Tensor] = None, want_grad_S0: bool = True,
+                       grads: Optional[Sequence[torch.Tensor]] = None, workspace: Optional[torch.Tensor] = None,
+                       stream: Optional[torch.cuda.Stream] = None, events: Optional[Sequence[int]] = None):
+    """Gradients of a loss on (out, S_final) of gdn_decay_attn_fwd with respect to q, k, v and S0.  Inputs as
+    there; grad_out like out (dense); grad_S_final fp32 like S_final or None.  ``grads`` = (grad_q, grad_k,
+    grad_v) receives the three where given (slices of one packed tensor, say, as the convolution's backward
+    takes them).  Returns (grad_q, grad_k, grad_v in the inputs' type, grad_S0 fp32 or None)."""
+    lib = L.load()
+    dev, dt, Hqk, Hv, dk, dv, strides = _decay_inputs(q, k, v, log_decay, 2)
+    B, T = q.shape[:2]
+    _need("grad_out", grad_out, dt, dev, (B, T, Hv, dv))
+    if grads is None:
+        grads = tuple(torch.empty(t.shape, dtype=dt, device=dev) for t in (q, k, v))
+    for name, g, t in zip(("grad_q", "grad_k", "grad_v"), grads, (q, k, v)):
+        if g.shape != t.shape or g.dtype != dt or g.device != dev:
+            raise ValueError(f"{name} must be {dt} of shape {tuple(t.shape)} on {dev}")
+    gstrides = tuple(_token_rows(n, g, 2) for n, g in zip(("grad_q", "grad_k", "grad_v"), grads))
+    with torch.cuda.device(dev):
+        o, keep = _opts(lib, dt, scale, 64, False, stream, dev, events)
+        nseq = _packed(o, cu_seqlens, B, dev)
+        for name, t in (("S0", S0), ("grad_S_final", grad_S_final)):
+            if t is not None:
+                _need(name, t, torch.float32, dev, (nseq, Hv, dk, dv))
+        gS0 = torch.empty((nseq, Hv, dk, dv), dtype=torch.float32, device=dev) if want_grad_S0 else None
+        workspace = _scratch(o, int(lib.gdn_decay_attn_bwd_workspace_size(B, T, Hqk, Hv, dk, dv, ctypes.byref(o))),
+                             workspace, dev)
+        st = lib.gdn_decay_attn_bwd(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], _ptr(log_decay),
+                                    _ptr(S0), _ptr(grad_out), _ptr(grad_S_final), _ptr(grads[0]), gstrides[0],
+                                    _ptr(grads[1]), gstrides[1], _ptr(grads[2]), gstrides[2], _ptr(gS0), B, T, Hqk, Hv,
+                                    dk, dv, ctypes.byref(o))
+        del keep
+        L.check(lib, st)
+    return grads[0], grads[1], grads[2], gS0
+
+
+def _block_norm_inputs(x, b, post_weight, pre_weight, gate, res_scale):
+    dev, dt = x.device, x.dtype
+    if dt not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    shape, D = tuple(x.shape), int(x.shape[-1])
+    _need("x", x, dt, dev, shape)
+    _need("b", b, dt, dev, shape)
+    _need("post_weight", post_weight, torch.float32, dev, (D,))
+    _need("pre_weight", pre_weight, torch.float32, dev, (D,))
+    if res_scale is not None:
+        _need("res_scale", res_scale, torch.float32, dev, (D,))
+    if gate is not None:
+        _need("gate", gate, dt, dev, shape if gate.shape[-1:] == x.shape[-1:] else shape[:-1] + (1,))
+    return dev, dt, shape, D, (x.numel() // D if D else 0), (0 if gate is None else int(gate.shape[-1]))
+
+
+def gdn_block_norm_fwd(x: torch.Tensor, b: torch.Tensor, post_weight: torch.Tensor, pre_weight: torch.Tensor, *,
+                       gate: Optional[torch.Tensor] = None, res_scale: Optional[torch.Tensor] = None,
+                       eps: float = 1e-6, out: Optional[Sequence[torch.Tensor]] = None,
+                       stream: Optional[torch.cuda.Stream] = None, events: Optional[Sequence[int]] = None):
+    """What surrounds a layer's block, in one pass: y = RMSNorm(b) post_weight, r = x + res_scale sigmoid(gate) y,
+    n = RMSNorm(r) pre_weight.  x (residual stream) and b (the block's output) [..., D] (bf16 or fp32,
+    contiguous); gate: logits like x, or [..., 1], or None (no gate); post_weight, pre_weight and res_scale
+    (None: 1) fp32 [D].  ``out`` = (r, n) receives the results where given (r may be x, n may be b).
+    Returns (r, n)."""
+    lib = L.load()
+    dev, dt, shape, D, rows, cols = _block_norm_inputs(x, b, post_weight, pre_weight, gate, res_scale)
+    r, n = (torch.empty_like(x), torch.empty_like(x)) if out is None else out
+    _need("r", r, dt, dev, shape)
+    _need("n", n, dt, dev, shape)
+    with torch.cuda.device(dev):
+        o, keep = _opts(lib, dt, 1.0, 64, False, stream, dev, events)
+        o.norm_eps = float(eps)
+        st = lib.gdn_block_norm_fwd(_ptr(x), _ptr(b), _ptr(gate), cols, _ptr(res_scale), _ptr(post_weight),
+                                    _ptr(pre_weight), _ptr(r), _ptr(n), rows, D, ctypes.byref(o))
+        del keep
+        L.check(lib, st)
+    return r, n
+
+
+def gdn_block_norm_bwd(x: torch.Tensor, b: torch.Tensor, post_weight: torch.Tensor, pre_weight: torch.Tensor,
+                       grad_r: torch.Tensor, grad_n: torch.Tensor, *, gate: Optional[torch.Tensor] = None,
+                       res_scale: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                       stream: Optional[torch.cuda.Stream] = None, events: Optional[Sequence[int]] = None):
+    """Gradients through gdn_block_norm_fwd, from its inputs and grad_r, grad_n (like x).  Returns (grad_x,
+    grad_b in x's type, grad_post_weight, grad_pre_weight fp32 [D], grad_gate like gate or None,
+    grad_res_scale fp32 [D] or None)."""
+    lib = L.load()
+    dev, dt, shape, D, rows, cols = _block_norm_inputs(x, b, post_weight, pre_weight, gate, res_scale)
+    _need("grad_r", grad_r, dt, dev, shape)
+    _need("grad_n", grad_n, dt, dev, shape)
+    gx, gb = torch.empty_like(x), torch.empty_like(x)
+    gg = None if gate is None else torch.empty_like(gate)
+    sums = torch.empty((3 if res_scale is not None else 2, D), dtype=torch.float32, device=dev)
+    gs = sums[2] if res_scale is not None else None
+    with torch.cuda.device(dev):
+        o, keep = _opts(lib, dt, 1.0, 64, False, stream, dev, events)
+        o.norm_eps = float(eps)
+        ws = _scratch(o, int(lib.gdn_block_norm_bwd_workspace_size(rows, D, ctypes.byref(o))), None, dev)
+        st = lib.gdn_block_norm_bwd(_ptr(x), _ptr(b), _ptr(gate), cols, _ptr(res_scale), _ptr(post_weight),
+                                    _ptr(pre_weight), _ptr(grad_r), _ptr(grad_n), _ptr(gx), _ptr(gb), _ptr(gg),
+                                    _ptr(sums[0]), _ptr(sums[1]), _ptr(gs), rows, D, ctypes.byref(o))
+        del keep, ws
+        L.check(lib, st)
+    return gx, gb, sums[0], sums[1], gg, gs

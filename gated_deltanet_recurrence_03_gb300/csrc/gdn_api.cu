@@ -1,9 +1,11 @@
 // C ABI of libgdn (declared in include/gdn.h): argument validation, kernel selection, device
 // status word, error reporting.  Every check that can fail does so on the host before anything is
 // enqueued.
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "gdn_internal.cuh"
@@ -599,6 +601,314 @@ gdn_status_t gdn_output_gate_bwd(const void* o, const void* z, const float* norm
                                                  grad_norm_weight, op.workspace, rows, dv, op.dtype, s);
     if (e != cudaSuccess) return cuda_fail(e, "output gate backward launch");
     record(op, 1, s);
+    return GDN_OK;
+}
+
+// ---------------------------------------------------------------- linear attention with a decay per head
+}  // extern "C"
+
+namespace {
+
+// Checks shared by the decayed attention's entry points; strides of 0 become the dense ones.
+gdn_status_t decay_common(int Hqk, int Hv, int dk, int dv, const gdn_opts_t& o, const float* log_decay,
+                          long long* q_stride, long long* k_stride, long long* v_stride) {
+    gdn_status_t st = check_common(Hqk, Hv, dk, dv, o);
+    if (st != GDN_OK) return st;
+    if (o.flags) return fail(GDN_ERR_INVALID_ARG, "flags 0x%x: the decayed attention takes none", o.flags);
+    if (log_decay && !aligned_to(log_decay, 4)) return fail(GDN_ERR_INVALID_ARG, "log_decay is not 4-byte aligned");
+    struct { const char* name; long long* stride; long long width; } rows[] = {
+        {"q", q_stride, (long long)Hqk * dk}, {"k", k_stride, (long long)Hqk * dk}, {"v", v_stride, (long long)Hv * dv}};
+    const int per16 = o.dtype == GDN_BF16 ? 8 : 4;   // elements in 16 bytes: rows must stay 16-byte aligned
+    for (auto& r : rows) {
+        if (*r.stride == 0) *r.stride = r.width;
+        if (*r.stride < r.width || *r.stride % per16 != 0 || *r.stride > INT32_MAX)
+            return fail(GDN_ERR_INVALID_ARG, "%s stride %lld must be >= %lld, a multiple of %d and below 2^31", r.name,
+                        *r.stride, r.width, per16);
+    }
+    return GDN_OK;
+}
+
+gdn_status_t need_aligned16(std::initializer_list<const void*> ptrs) {
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return fail(GDN_ERR_INVALID_ARG, "pointer %p is not 16-byte aligned", p);
+    return GDN_OK;
+}
+
+gdn_status_t need_workspace(const gdn_opts_t& o, size_t need) {
+    if (!need) return GDN_OK;
+    if (!o.workspace || o.workspace_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                    o.workspace ? o.workspace_bytes : (size_t)0);
+    if ((reinterpret_cast<uintptr_t>(o.workspace) & 255u) != 0)
+        return fail(GDN_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    return GDN_OK;
+}
+
+// Sequences and packing of a call over whole sequences; false (with *st set) on an argument error.
+bool decay_sequences(int B, int T, const gdn_opts_t& o, int* nseq, gdn_status_t* st) {
+    *st = GDN_OK;
+    if (B < 0 || T < 0) *st = fail(GDN_ERR_INVALID_ARG, "B=%d T=%d must be >= 0", B, T);
+    else if (o.cu_seqlens && (B != 1 || o.num_seqs < 1))
+        *st = fail(GDN_ERR_INVALID_ARG, "cu_seqlens needs B == 1 and num_seqs >= 1 (B=%d num_seqs=%d)", B, o.num_seqs);
+    else if (o.cu_seqlens && !aligned_to(o.cu_seqlens, 4))
+        *st = fail(GDN_ERR_INVALID_ARG, "cu_seqlens must be 4-byte aligned");
+    else if ((long long)B * T > INT32_MAX) *st = fail(GDN_ERR_INVALID_ARG, "more than 2^31 - 1 tokens");
+    *nseq = o.cu_seqlens ? o.num_seqs : B;
+    return *st == GDN_OK;
+}
+
+// Byte offsets of the backward's workspace: the per-value-head parts of grad_q and grad_k where query/key
+// heads are shared, then the scans' own scratch.
+struct DecayBwdLayout {
+    size_t dq, dk, scan, total;
+};
+DecayBwdLayout decay_bwd_layout(int dtype, long long tokens, int Hqk, int Hv, int dk, int dv, int nseq) {
+    DecayBwdLayout l{};
+    const size_t part = Hv > Hqk ? ((size_t)tokens * Hv * dk * 4 + 255) / 256 * 256 : 0;
+    l.dk = part;
+    l.scan = 2 * part;
+    const size_t scan = dk == dv ? decay_scan_workspace_bytes(dtype, dk, dv, Hv, nseq, tokens, 3)
+                                 : std::max(decay_scan_workspace_bytes(dtype, dv, dk, Hv, nseq, tokens, 2),
+                                            decay_scan_workspace_bytes(dtype, dk, dv, Hv, nseq, tokens, 1));
+    l.total = l.scan + scan;
+    return l;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_decay_attn_fwd_workspace_size(int B, int T, int Hqk, int Hv, int dk, int dv, const gdn_opts_t* opts) {
+    const gdn_opts_t o = resolve(opts);
+    if (B <= 0 || T <= 0 || Hqk <= 0 || Hv <= 0 || Hv % Hqk || !dim_ok(dk) || !dim_ok(dv)) return 0;
+    const int nseq = o.cu_seqlens ? o.num_seqs : B;
+    return nseq > 0 ? decay_scan_workspace_bytes(o.dtype, dk, dv, Hv, nseq, (long long)B * T, 1) : 0;
+}
+
+gdn_status_t gdn_decay_attn_fwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                                long long v_stride, const float* log_decay, const float* S0, void* out, float* S_final,
+                                int B, int T, int Hqk, int Hv, int dk, int dv, const gdn_opts_t* opts) {
+    t_last_error[0] = 0;
+    const gdn_opts_t o = resolve(opts);
+    gdn_status_t st;
+    int nseq;
+    if (!decay_sequences(B, T, o, &nseq, &st)) return st;
+    if ((st = decay_common(Hqk, Hv, dk, dv, o, log_decay, &q_stride, &k_stride, &v_stride)) != GDN_OK) return st;
+    const bool have_tokens = (long long)B * T > 0;
+    if (have_tokens && (!q || !k || !v || !log_decay || !out))
+        return fail(GDN_ERR_INVALID_ARG, "null input/output pointer");
+    if ((st = need_aligned16({q, k, v, S0, out, S_final})) != GDN_OK) return st;
+    if (nseq == 0) return GDN_OK;
+    const size_t need = have_tokens ? decay_scan_workspace_bytes(o.dtype, dk, dv, Hv, nseq, (long long)B * T, 1) : 0;
+    if ((st = need_workspace(o, need)) != GDN_OK) return st;
+    unsigned* status = nullptr;
+    if ((st = device_ready(&status)) != GDN_OK) return st;
+    cudaStream_t stream = static_cast<cudaStream_t>(o.stream);
+    record(o, 0, stream);
+    cudaError_t e = cudaSuccess;
+    if (!have_tokens) {   // no tokens: the final states are the initial ones
+        const size_t bytes = (size_t)nseq * Hv * dk * dv * sizeof(float);
+        if (S_final && S_final != S0)
+            e = S0 ? cudaMemcpyAsync(S_final, S0, bytes, cudaMemcpyDeviceToDevice, stream)
+                   : cudaMemsetAsync(S_final, 0, bytes, stream);
+    } else {
+        DecayArgs a{};
+        a.scan[0] = DecayScan{q, k, v, q_stride, k_stride, v_stride, Hv / Hqk, Hv / Hqk, 1, S0, S_final, out,
+                              (long long)Hv * dv, 0, 0, 0, o.scale, 1.f};
+        a.num_scans = 1;
+        a.log_decay = log_decay;
+        a.T = T; a.Hv = Hv; a.dk = dk; a.dv = dv; a.dtype = o.dtype;
+        a.cu = o.cu_seqlens; a.nseq = nseq; a.tokens = B * T;
+        a.workspace = o.workspace; a.stream = stream; a.status = status;
+        e = launch_decay_scan(a);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "decayed attention launch");
+    record(o, 1, stream);
+    return GDN_OK;
+}
+
+gdn_status_t gdn_decay_attn_step(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                                 long long v_stride, const float* log_decay, float* S, const int32_t* slots,
+                                 int num_slots, void* out, int N, int Hqk, int Hv, int dk, int dv,
+                                 const gdn_opts_t* opts) {
+    t_last_error[0] = 0;
+    const gdn_opts_t o = resolve(opts);
+    if (N < 0 || num_slots < 0) return fail(GDN_ERR_INVALID_ARG, "N=%d num_slots=%d must be >= 0", N, num_slots);
+    gdn_status_t st = decay_common(Hqk, Hv, dk, dv, o, log_decay, &q_stride, &k_stride, &v_stride);
+    if (st != GDN_OK) return st;
+    if (!slots && num_slots < N) return fail(GDN_ERR_INVALID_ARG, "%d states for %d rows without slots", num_slots, N);
+    if (N == 0) return GDN_OK;
+    if (!q || !k || !v || !log_decay || (!S && num_slots > 0) || !out) return fail(GDN_ERR_INVALID_ARG, "null pointer");
+    if ((long long)N * Hv > INT32_MAX / 4) return fail(GDN_ERR_INVALID_ARG, "N=%d rows of %d heads are too many", N, Hv);
+    if ((st = need_aligned16({q, k, v, S, out})) != GDN_OK) return st;
+    if (slots && !aligned_to(slots, 4)) return fail(GDN_ERR_INVALID_ARG, "slots is not 4-byte aligned");
+    unsigned* status = nullptr;
+    if ((st = device_ready(&status)) != GDN_OK) return st;
+    DecayStepArgs a{q, k, v, q_stride, k_stride, v_stride, log_decay, S, slots, num_slots, out, N, Hqk, Hv, dk, dv,
+                    o.dtype, o.scale, static_cast<cudaStream_t>(o.stream)};
+    record(o, 0, a.stream);
+    const cudaError_t e = launch_decay_step(a);
+    if (e != cudaSuccess) return cuda_fail(e, "decayed attention step launch");
+    record(o, 1, a.stream);
+    return GDN_OK;
+}
+
+size_t gdn_decay_attn_bwd_workspace_size(int B, int T, int Hqk, int Hv, int dk, int dv, const gdn_opts_t* opts) {
+    const gdn_opts_t o = resolve(opts);
+    if (B <= 0 || T <= 0 || Hqk <= 0 || Hv <= 0 || Hv % Hqk || !dim_ok(dk) || !dim_ok(dv)) return 0;
+    const int nseq = o.cu_seqlens ? o.num_seqs : B;
+    return nseq > 0 ? decay_bwd_layout(o.dtype, (long long)B * T, Hqk, Hv, dk, dv, nseq).total : 0;
+}
+
+gdn_status_t gdn_decay_attn_bwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                                long long v_stride, const float* log_decay, const float* S0, const void* grad_out,
+                                const float* grad_S_final, void* grad_q, long long gq_stride, void* grad_k,
+                                long long gk_stride, void* grad_v, long long gv_stride, float* grad_S0, int B, int T,
+                                int Hqk, int Hv, int dk, int dv, const gdn_opts_t* opts) {
+    t_last_error[0] = 0;
+    const gdn_opts_t o = resolve(opts);
+    gdn_status_t st;
+    int nseq;
+    if (!decay_sequences(B, T, o, &nseq, &st)) return st;
+    if ((st = decay_common(Hqk, Hv, dk, dv, o, log_decay, &q_stride, &k_stride, &v_stride)) != GDN_OK) return st;
+    if ((st = decay_common(Hqk, Hv, dk, dv, o, log_decay, &gq_stride, &gk_stride, &gv_stride)) != GDN_OK) return st;
+    const bool have_tokens = (long long)B * T > 0;
+    if (have_tokens && (!q || !k || !v || !log_decay || !grad_out || !grad_q || !grad_k || !grad_v))
+        return fail(GDN_ERR_INVALID_ARG, "null input/output pointer");
+    if ((st = need_aligned16({q, k, v, S0, grad_out, grad_S_final, grad_q, grad_k, grad_v, grad_S0})) != GDN_OK) return st;
+    if (nseq == 0) return GDN_OK;
+    const long long tokens = (long long)B * T;
+    const DecayBwdLayout l = have_tokens ? decay_bwd_layout(o.dtype, tokens, Hqk, Hv, dk, dv, nseq) : DecayBwdLayout{};
+    if ((st = need_workspace(o, l.total)) != GDN_OK) return st;
+    unsigned* status = nullptr;
+    if ((st = device_ready(&status)) != GDN_OK) return st;
+    cudaStream_t stream = static_cast<cudaStream_t>(o.stream);
+    record(o, 0, stream);
+    cudaError_t e = cudaSuccess;
+    if (!have_tokens) {   // no tokens: the initial states' gradient is the final ones'
+        const size_t bytes = (size_t)nseq * Hv * dk * dv * sizeof(float);
+        if (grad_S0 && grad_S0 != grad_S_final)
+            e = grad_S_final ? cudaMemcpyAsync(grad_S0, grad_S_final, bytes, cudaMemcpyDeviceToDevice, stream)
+                             : cudaMemsetAsync(grad_S0, 0, bytes, stream);
+    } else {
+        const int G = Hv / Hqk;
+        const long long do_stride = (long long)Hv * dv, part_stride = (long long)Hv * dk;
+        uint8_t* ws = static_cast<uint8_t*>(o.workspace);
+        void* dq = G > 1 ? static_cast<void*>(ws + l.dq) : grad_q;
+        void* dkk = G > 1 ? static_cast<void*>(ws + l.dk) : grad_k;
+        const int f32 = G > 1 ? 1 : 0;
+        const DecayScan scan_q{grad_out, v, k, do_stride, v_stride, k_stride, 1, 1, G, S0, nullptr, dq,
+                               G > 1 ? part_stride : gq_stride, 1, f32, 0, o.scale, 1.f};
+        const DecayScan scan_k{v, grad_out, q, v_stride, do_stride, q_stride, 1, 1, G, grad_S_final, nullptr, dkk,
+                               G > 1 ? part_stride : gk_stride, 1, f32, 1, 1.f, o.scale};
+        const DecayScan scan_v{k, q, grad_out, k_stride, q_stride, do_stride, G, G, 1, grad_S_final, grad_S0, grad_v,
+                               gv_stride, 0, 0, 1, 1.f, o.scale};
+        DecayArgs a{};
+        a.log_decay = log_decay;
+        a.T = T; a.Hv = Hv; a.dtype = o.dtype;
+        a.cu = o.cu_seqlens; a.nseq = nseq; a.tokens = (int)tokens;
+        a.workspace = ws ? ws + l.scan : nullptr; a.stream = stream; a.status = status;
+        a.scan[0] = scan_q;
+        a.scan[1] = scan_k;
+        a.scan[2] = scan_v;
+        a.dk = dv; a.dv = dk;
+        a.num_scans = dk == dv ? 3 : 2;   // scans of one shape share a launch
+        e = launch_decay_scan(a);
+        if (e == cudaSuccess && dk != dv) {
+            a.scan[0] = scan_v;
+            a.dk = dk; a.dv = dv;
+            a.num_scans = 1;
+            e = launch_decay_scan(a);
+        }
+        if (e == cudaSuccess && G > 1)
+            e = launch_head_sum(static_cast<const float*>(dq), grad_q, gq_stride, tokens, Hqk, G, dk, o.dtype, stream);
+        if (e == cudaSuccess && G > 1)
+            e = launch_head_sum(static_cast<const float*>(dkk), grad_k, gk_stride, tokens, Hqk, G, dk, o.dtype, stream);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "decayed attention backward launch");
+    record(o, 1, stream);
+    return GDN_OK;
+}
+
+// ---------------------------------------------------------------- block norm
+static gdn_status_t block_norm_common(const gdn_opts_t& o, long long rows, int D, const void* gate, int gate_cols,
+                                      const float* post_w, const float* pre_w, const float* res_scale) {
+    if (rows < 0 || rows > INT32_MAX) return fail(GDN_ERR_INVALID_ARG, "rows=%lld not in 0..2^31 - 1", rows);
+    if (o.dtype != GDN_F32 && o.dtype != GDN_BF16) return fail(GDN_ERR_INVALID_ARG, "unknown dtype %d", o.dtype);
+    if (o.flags) return fail(GDN_ERR_INVALID_ARG, "flags 0x%x: the block norm takes none", o.flags);
+    if (!(o.norm_eps >= 0.f)) return fail(GDN_ERR_INVALID_ARG, "norm_eps must be >= 0");
+    if (o.num_events < 0 || (o.num_events > 0 && !o.events)) return fail(GDN_ERR_INVALID_ARG, "bad event list");
+    if (D <= 0 || D % 8 != 0) return fail(GDN_ERR_INVALID_ARG, "D=%d must be a positive multiple of 8", D);
+    if (D > kBlockNormMaxD) return fail(GDN_ERR_UNSUPPORTED, "D=%d is above %d", D, kBlockNormMaxD);
+    if (gate && gate_cols != 1 && gate_cols != D)
+        return fail(GDN_ERR_INVALID_ARG, "gate_cols=%d must be 1 or D", gate_cols);
+    if (!post_w || !pre_w) return fail(GDN_ERR_INVALID_ARG, "null weight");
+    const gdn_status_t st = need_aligned16({post_w, pre_w, res_scale, gate && gate_cols > 1 ? gate : nullptr});
+    if (st != GDN_OK) return st;
+    if (gate && !aligned_to(gate, elem_bytes(o.dtype))) return fail(GDN_ERR_INVALID_ARG, "gate is not element aligned");
+    return GDN_OK;
+}
+
+gdn_status_t gdn_block_norm_fwd(const void* x, const void* b, const void* gate, int gate_cols, const float* res_scale,
+                                const float* post_weight, const float* pre_weight, void* r, void* n, long long rows,
+                                int D, const gdn_opts_t* opts) {
+    t_last_error[0] = 0;
+    const gdn_opts_t o = resolve(opts);
+    gdn_status_t st = block_norm_common(o, rows, D, gate, gate_cols, post_weight, pre_weight, res_scale);
+    if (st != GDN_OK) return st;
+    if (rows == 0) return GDN_OK;
+    if (!x || !b || !r || !n) return fail(GDN_ERR_INVALID_ARG, "null x, b, r or n");
+    if ((st = need_aligned16({x, b, r, n})) != GDN_OK) return st;
+    unsigned* status = nullptr;
+    if ((st = device_ready(&status)) != GDN_OK) return st;
+    BlockNormArgs a{};
+    a.x = x; a.b = b; a.gate = gate; a.gate_cols = gate_cols; a.res_scale = res_scale;
+    a.post_w = post_weight; a.pre_w = pre_weight; a.eps = o.norm_eps; a.r = r; a.n = n;
+    a.rows = rows; a.D = D; a.dtype = o.dtype; a.stream = static_cast<cudaStream_t>(o.stream);
+    record(o, 0, a.stream);
+    const cudaError_t e = launch_block_norm_fwd(a);
+    if (e != cudaSuccess) return cuda_fail(e, "block norm launch");
+    record(o, 1, a.stream);
+    return GDN_OK;
+}
+
+size_t gdn_block_norm_bwd_workspace_size(long long rows, int D, const gdn_opts_t* opts) {
+    (void)opts;
+    if (rows < 0 || D <= 0 || D % 8 || D > kBlockNormMaxD) return 0;
+    return block_norm_bwd_workspace_bytes(rows, D);
+}
+
+gdn_status_t gdn_block_norm_bwd(const void* x, const void* b, const void* gate, int gate_cols, const float* res_scale,
+                                const float* post_weight, const float* pre_weight, const void* grad_r,
+                                const void* grad_n, void* grad_x, void* grad_b, void* grad_gate, float* grad_post,
+                                float* grad_pre, float* grad_res_scale, long long rows, int D, const gdn_opts_t* opts) {
+    t_last_error[0] = 0;
+    const gdn_opts_t o = resolve(opts);
+    gdn_status_t st = block_norm_common(o, rows, D, gate, gate_cols, post_weight, pre_weight, res_scale);
+    if (st != GDN_OK) return st;
+    const bool sums = grad_post || grad_pre || grad_res_scale;
+    if (rows > 0 && (!x || !b || !grad_r || !grad_n || !grad_x || !grad_b))
+        return fail(GDN_ERR_INVALID_ARG, "null x, b, grad_r, grad_n, grad_x or grad_b");
+    if (rows > 0 && gate && !grad_gate) return fail(GDN_ERR_INVALID_ARG, "a gate needs grad_gate");
+    if ((st = need_aligned16({x, b, grad_r, grad_n, grad_x, grad_b, gate_cols > 1 ? grad_gate : nullptr, grad_post,
+                              grad_pre, grad_res_scale})) != GDN_OK)
+        return st;
+    if (grad_gate && !aligned_to(grad_gate, elem_bytes(o.dtype)))
+        return fail(GDN_ERR_INVALID_ARG, "grad_gate is not element aligned");
+    if (rows == 0 && !sums) return GDN_OK;
+    if (sums && (st = need_workspace(o, block_norm_bwd_workspace_bytes(rows, D))) != GDN_OK) return st;
+    unsigned* status = nullptr;
+    if ((st = device_ready(&status)) != GDN_OK) return st;
+    BlockNormArgs a{};
+    a.x = x; a.b = b; a.gate = gate; a.gate_cols = gate_cols; a.res_scale = res_scale;
+    a.post_w = post_weight; a.pre_w = pre_weight; a.eps = o.norm_eps;
+    a.gr = grad_r; a.gn = grad_n; a.gx = grad_x; a.gb = grad_b; a.ggate = grad_gate;
+    a.g_post = grad_post; a.g_pre = grad_pre; a.g_scale = grad_res_scale; a.workspace = o.workspace;
+    a.rows = rows; a.D = D; a.dtype = o.dtype; a.stream = static_cast<cudaStream_t>(o.stream);
+    record(o, 0, a.stream);
+    const cudaError_t e = launch_block_norm_bwd(a);
+    if (e != cudaSuccess) return cuda_fail(e, "block norm backward launch");
+    record(o, 1, a.stream);
     return GDN_OK;
 }
 

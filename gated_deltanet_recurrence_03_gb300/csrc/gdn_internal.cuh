@@ -158,6 +158,101 @@ cudaError_t launch_bwd_state_adj_tc(const void* q, const void* k, const void* do
 size_t chunked_prefill_workspace_bytes(int B, int T, int Hv, int dk, int dv, int nseq, bool packed);
 cudaError_t launch_chunked_prefill(const PrefillArgs& a);
 
+// ---------------------------------------------------------------- linear attention with a decay per head
+// One decayed scan over the tokens of every sequence, per value head h with a = exp(max(log_decay[h], -100)):
+//     forward:  S <- a S + su k_t v_t^T,   out_t = so S^T q_t           (t ascending, S starts at `init`)
+//     reverse:  S <- S + su k_t v_t^T,     out_t = so S^T q_t,  S <- a S   (t descending)
+// `final` gets the last S.  The operator's forward is one such scan; its three gradients are the scans
+// dq = F(do, v, k), dv = R(k, q, do), dk = R(v, do, q), whose states are S^T, lam and lam^T (lam the adjoint
+// of S): the names q, k, v below are the scan's roles, each with its own row stride and head sharing.
+struct DecayScan {
+    const void* q;              // [tokens][head h / q_div][dk], rows q_stride elements apart
+    const void* k;              // [tokens][head h / k_div][dk]
+    const void* v;              // [tokens][head h / v_div][dv]
+    long long q_stride, k_stride, v_stride;
+    int q_div, k_div, v_div;
+    const float* init;          // [nseq][Hv][dk][dv] ([dv][dk] when init_t), or nullptr (zeros)
+    float* final;               // [nseq][Hv][dk][dv], or nullptr (not wanted)
+    void* out;                  // [tokens][head h][dv], rows out_stride elements apart
+    long long out_stride;
+    int init_t;
+    int out_f32;                // out is float (a partial sum over shared heads), else the inputs' type
+    int reverse;
+    float so, su;
+};
+constexpr int kMaxScans = 3;
+struct DecayArgs {
+    DecayScan scan[kMaxScans];
+    int num_scans;
+    const float* log_decay;     // [Hv]
+    int T, Hv, dk, dv;          // dk, dv of the scans (the same for all scans of one launch)
+    int dtype;
+    const int32_t* cu;
+    int nseq;
+    int tokens;                 // all tokens of the call
+    void* workspace;
+    cudaStream_t stream;
+    unsigned* status;
+};
+// Floor of the log decay: exp(-100) is 0 to fp32 products of ordinary size, while -inf would turn the
+// differences of exponents into NaN.
+constexpr float kMinLogDecay = -100.f;
+// Device scratch of one launch_decay_scan call, and the launch.
+size_t decay_scan_workspace_bytes(int dtype, int dk, int dv, int Hv, int nseq, long long tokens, int num_scans);
+cudaError_t launch_decay_scan(const DecayArgs& a);
+// out[t][hk] = sum over the G value heads of query/key head hk of part[t][hk G + i] (fp32 [tokens][Hqk G][d]),
+// rounded once to the output type, rows out_stride elements apart.
+cudaError_t launch_head_sum(const float* part, void* out, long long out_stride, long long tokens, int Hqk, int G, int d,
+                            int dtype, cudaStream_t stream);
+
+struct DecayStepArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    long long q_stride, k_stride, v_stride;
+    const float* log_decay;
+    float* S;                   // [num_slots][Hv][dk][dv]
+    const int32_t* slots;       // [N], or nullptr (row n uses state n)
+    int num_slots;
+    void* out;                  // [N][Hv][dv]
+    int N, Hqk, Hv, dk, dv;
+    int dtype;
+    float scale;
+    cudaStream_t stream;
+};
+cudaError_t launch_decay_step(const DecayStepArgs& a);
+
+// ---------------------------------------------------------------- block norm
+struct BlockNormArgs {
+    const void* x;              // [rows][D] residual stream
+    const void* b;              // [rows][D] the block's output
+    const void* gate;           // [rows][gate_cols] logits, or nullptr
+    int gate_cols;              // 1 or D
+    const float* res_scale;     // [D] or nullptr (1)
+    const float* post_w;        // [D]
+    const float* pre_w;         // [D]
+    float eps;
+    void* r;                    // forward outputs
+    void* n;
+    const void* gr;             // backward inputs
+    const void* gn;
+    void* gx;                   // backward outputs
+    void* gb;
+    void* ggate;
+    float* g_post;              // [D] or nullptr (not wanted)
+    float* g_pre;
+    float* g_scale;
+    void* workspace;
+    long long rows;
+    int D;
+    int dtype;
+    cudaStream_t stream;
+};
+constexpr int kBlockNormMaxD = 16384;
+cudaError_t launch_block_norm_fwd(const BlockNormArgs& a);
+size_t block_norm_bwd_workspace_bytes(long long rows, int D);
+cudaError_t launch_block_norm_bwd(const BlockNormArgs& a);
+
 // The CUDA driver's cuTensorMapEncodeTiled (looked up once), or nullptr when the CUDA driver lacks it.
 void* tensor_map_encoder();
 

@@ -332,6 +332,101 @@ gdn_status_t gdn_output_gate_bwd(const void* o, const void* z, const float* norm
                                  float* grad_o, float* grad_z, float* grad_norm_weight, long long rows, int dv,
                                  const gdn_opts_t* opts);
 
+/*
+ * gdn_decay_attn_fwd -- linear attention with a decay for each value head: the rung of the update-rule
+ * table (learn-llm page "linear attention") below the delta rule, plain writes into a decaying state,
+ * with the decay a constant of the head (a_h = exp(log_decay[h])):
+ *     S_t = a_h S_{t-1} + k_t v_t^T,     o_t = scale * S_t^T q_t
+ * over whole sequences.  Value head h reads query/key head floor(h / (Hv / Hqk)).
+ *   q, k        [B, T, Hqk, dk] dtype, token rows q_stride / k_stride elements apart (0 = dense: Hqk dk)
+ *   v           [B, T, Hv, dv] dtype, rows v_stride apart (0 = Hv dv).  Slices of one packed q | k | v
+ *               projection can be passed directly; strides are multiples of 16 bytes
+ *   log_decay   [Hv] float, <= 0 (values below -100, -inf among them, act as -100: exp(-100) leaves nothing)
+ *   S0          [nseq, Hv, dk, dv] float or NULL (zero states); nseq = B, or num_seqs when packed
+ *   out         [B, T, Hv, dv] dtype, dense; must not overlap any input
+ *   S_final     [nseq, Hv, dk, dv] float or NULL (not written); may equal S0 (in-place update)
+ * Supported: dk, dv in {32, 64, 128}; Hv a multiple of Hqk; B, T >= 0, sequences of no tokens included
+ * (their S_final is S0, or zeros).  States, sums and decays are fp32.  A value (a NaN, say) in one
+ * sequence's tokens never reaches another sequence's results.  opts->workspace: 256-byte aligned, of
+ * gdn_decay_attn_fwd_workspace_size bytes (GDN_ERR_WORKSPACE if that is not 0 and it is missing or too
+ * small).  opts->flags must be 0; dtype, scale, cu_seqlens, num_seqs, stream and events[0] / [1] (around
+ * the kernels) are used.  Errors otherwise as for gdn_chunk_fwd.
+ */
+size_t gdn_decay_attn_fwd_workspace_size(int B, int T, int Hqk, int Hv, int dk, int dv, const gdn_opts_t* opts);
+gdn_status_t gdn_decay_attn_fwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                                long long v_stride, const float* log_decay, const float* S0, void* out, float* S_final,
+                                int B, int T, int Hqk, int Hv, int dk, int dv, const gdn_opts_t* opts);
+
+/*
+ * gdn_decay_attn_step -- one token for each of N rows through the same recurrence, the states updated in
+ * place: q, k [N, Hqk, dk], v [N, Hv, dv] dtype (row strides as above), out [N, Hv, dv] dtype, dense.
+ *   S       [num_slots, Hv, dk, dv] float: a pool of states
+ *   slots   [N] int32 DEVICE or NULL: row n uses state slots[n] (NULL: state n, num_slots >= N).  A row
+ *           whose slot is outside 0 .. num_slots - 1 (-1, say) is idle: its out row is zeros, no state is
+ *           touched.  Two rows must not name the same state.
+ * Each state is read once and written once.  opts->flags must be 0; cu_seqlens and workspace are ignored.
+ */
+gdn_status_t gdn_decay_attn_step(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                                 long long v_stride, const float* log_decay, float* S, const int32_t* slots,
+                                 int num_slots, void* out, int N, int Hqk, int Hv, int dk, int dv,
+                                 const gdn_opts_t* opts);
+
+/*
+ * gdn_decay_attn_bwd -- gradients of a loss on (out, S_final) of gdn_decay_attn_fwd with respect to q, k,
+ * v and S0 (the decays are constants of the heads and have none).  With lam = dL/dS, walked backwards
+ * from grad_S_final:
+ *     lam += scale q_t do_t^T;  dq_t = scale S_t do_t;  dk_t = lam v_t;  dv_t = lam^T k_t;  lam <- a lam;
+ *     dS0 = lam at the start
+ *   q, k, v and their strides, log_decay, S0, B, T, Hqk, Hv, dk, dv: as gdn_decay_attn_fwd
+ *   grad_out       [B, T, Hv, dv] dtype, dense
+ *   grad_S_final   [nseq, Hv, dk, dv] float or NULL (no loss on the final states)
+ *   grad_q, grad_k [B, T, Hqk, dk] dtype, grad_v [B, T, Hv, dv] dtype: the inputs' type, as the backward
+ *                  of the convolution that feeds q, k, v takes them; rows gq_stride / gk_stride / gv_stride
+ *                  elements apart (0 = dense), so the three can be slices of one packed tensor.  Sums over
+ *                  the value heads that share a query/key head are fp32, rounded once
+ *   grad_S0        [nseq, Hv, dk, dv] float or NULL (not written)
+ * Deterministic.  opts->workspace: 256-byte aligned, gdn_decay_attn_bwd_workspace_size bytes.
+ */
+size_t gdn_decay_attn_bwd_workspace_size(int B, int T, int Hqk, int Hv, int dk, int dv, const gdn_opts_t* opts);
+gdn_status_t gdn_decay_attn_bwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                                long long v_stride, const float* log_decay, const float* S0, const void* grad_out,
+                                const float* grad_S_final, void* grad_q, long long gq_stride, void* grad_k,
+                                long long gk_stride, void* grad_v, long long gv_stride, float* grad_S0, int B, int T,
+                                int Hqk, int Hv, int dk, int dv, const gdn_opts_t* opts);
+
+/*
+ * gdn_block_norm_fwd -- what surrounds a layer's block, in one pass over the rows: the norm after the
+ * block, its gate and residual scale, the residual add, and the norm before the next block.  Per row of D
+ * values, with b the block's output and x the residual stream:
+ *     y = b / sqrt(mean(b^2) + eps) * post_weight
+ *     r = x + res_scale * sigmoid(gate) * y            (the new residual stream)
+ *     n = r / sqrt(mean(r^2) + eps) * pre_weight       (the next block's input; r before its rounding)
+ *   x, b, r, n               [rows, D] dtype, 16-byte aligned; r may equal x and n may equal b (in place)
+ *   gate                     logits [rows, D] (gate_cols = D) or [rows] (gate_cols = 1) dtype, or NULL (no gate)
+ *   res_scale                [D] float or NULL (1)
+ *   post_weight, pre_weight  [D] float
+ * Supported: D a multiple of 8 up to 16384, rows >= 0.  eps = opts->norm_eps; opts->flags must be 0.
+ */
+gdn_status_t gdn_block_norm_fwd(const void* x, const void* b, const void* gate, int gate_cols, const float* res_scale,
+                                const float* post_weight, const float* pre_weight, void* r, void* n, long long rows,
+                                int D, const gdn_opts_t* opts);
+
+/*
+ * gdn_block_norm_bwd -- gradients through gdn_block_norm_fwd given grad_r = dL/dr and grad_n = dL/dn, from
+ * the forward's inputs (r is formed again, so nothing of the forward has to be kept).
+ *   grad_x, grad_b           [rows, D] dtype, 16-byte aligned
+ *   grad_gate                like gate, dtype (required with a gate)
+ *   grad_post, grad_pre, grad_res_scale   [D] float, each may be NULL (not computed): sums over the rows in
+ *                            a fixed order through opts->workspace (256-byte aligned,
+ *                            gdn_block_norm_bwd_workspace_size bytes; needed if one of them is wanted)
+ * Deterministic.  Errors and options as for gdn_block_norm_fwd.
+ */
+size_t gdn_block_norm_bwd_workspace_size(long long rows, int D, const gdn_opts_t* opts);
+gdn_status_t gdn_block_norm_bwd(const void* x, const void* b, const void* gate, int gate_cols, const float* res_scale,
+                                const float* post_weight, const float* pre_weight, const void* grad_r,
+                                const void* grad_n, void* grad_x, void* grad_b, void* grad_gate, float* grad_post,
+                                float* grad_pre, float* grad_res_scale, long long rows, int D, const gdn_opts_t* opts);
+
 /* Synchronise `stream` (cudaStream_t, NULL = legacy), then read and clear the device status word
  * that kernels set when a bounded wait runs out.  GDN_OK if clear, GDN_ERR_TIMEOUT if set,
  * GDN_ERR_CUDA if the synchronisation itself failed. */
