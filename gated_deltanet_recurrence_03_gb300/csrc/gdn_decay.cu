@@ -108,6 +108,7 @@ cudaError_t launch_serial(const DecayArgs& a) {
 size_t decay_scan_workspace_bytes(int, int, int, int, int, long long, int) { return 0; }
 
 cudaError_t launch_decay_scan(const DecayArgs& a) {
+    if (a.dtype == GDN_BF16 && a.dk == 128 && a.dv == 128) return launch_decay_scan_tc(a);
     return a.dtype == GDN_BF16 ? launch_serial<__nv_bfloat16>(a) : launch_serial<float>(a);
 }
 

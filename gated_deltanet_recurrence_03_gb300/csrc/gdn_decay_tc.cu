@@ -1,0 +1,528 @@
+// The decayed scan (gdn_internal.cuh, DecayScan) on the tcgen05 tensor cores: bf16, 128-wide heads.
+//
+// Inside a chunk of C = 128 tokens, n of them valid, with w_d = a^d and S the state at the chunk's first
+// visited end (its start; its end in a reverse scan), in token order r, j = 0 .. n - 1:
+//   forward   out_r = so (w_{r+1} q_r S + su sum_{j<=r} w_{r-j} (q_r.k_j) v_j),  S <- w_n S + su sum_j w_{n-1-j} k_j v_j^T
+//   reverse   out_r = so (w_{n-1-r} q_r S + su sum_{j>=r} w_{j-r} (q_r.k_j) v_j), S <- w_n S + su sum_j w_{j+1} k_j v_j^T
+//
+// One CTA walks one sequence (or one segment of it) of one value head for 64 of the 128 value columns, so
+// that a head keeps two SMs busy; the two read the same q and k tiles, the second time from L2.  Per chunk
+// four products (M = 128 each):
+//   QK [128 x 128] = Q K^T;   PV [128 x 64] = P V, P = the decayed, masked QK as the bf16 A operand in TMEM;
+//   QS [128 x 64] = Q S_bf16;   KV [dk x 64] = K^T V~, V~ = V scaled by su w and split into three bf16 parts.
+// The state is kept in registers in fp32 (64 columns of one row a thread), so the products of a chunk wait for
+// the state only in QS: KV goes to a fresh accumulator, and S <- w_n S + KV is one FMA per element (with w_n in
+// two floats: one rounding of it would compound over the head's memory).  V~'s three parts hold its fp32 value
+// exactly, K is exact, so the states that leave the kernel have fp32 accuracy; P and the state's copy in QS are
+// rounded to bf16, each 2^-9 of terms whose sum is rounded to bf16 anyway.
+//
+// Warps: 0-7 form P; 8-11 scale and split V and write the outputs; 12-15 keep the state; 16 issues the MMAs,
+// 17 the copies.  Hand-overs are mbarriers; every wait is bounded.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "gdn_internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace tc;
+using bf16 = __nv_bfloat16;
+
+constexpr int kC = 128;       // tokens of a chunk
+constexpr int kD = 128;       // head dims
+constexpr int kHalf = 64;     // value columns of a CTA
+constexpr int kParts = 3;     // bf16 parts of the scaled V
+
+// Shared memory (bytes from the 1024-aligned base).  Panels: 128 rows x 64 bf16, 128-byte swizzle.
+constexpr uint32_t kPanel = 16384;
+constexpr uint32_t S_Q = 0;                          // 2 stages x 2 panels
+constexpr uint32_t S_K = S_Q + 2 * 2 * kPanel;       // 2 stages x 2 panels
+constexpr uint32_t S_V = S_K + 2 * 2 * kPanel;       // 2 stages x 1 panel; then the chunk's outputs
+constexpr uint32_t S_VP = S_V + 2 * kPanel;          // the three parts of the scaled V
+constexpr uint32_t S_SB = S_VP + kParts * kPanel;    // the state in bf16: 128 dk rows
+constexpr uint32_t S_BAR = S_SB + kPanel;
+constexpr uint32_t kBarBytes = 256;
+constexpr uint32_t S_PW = S_BAR + kBarBytes;         // w_0 .. w_128
+constexpr uint32_t S_PR = S_PW + 132 * 4;            // w_31 .. w_0
+constexpr uint32_t kSmem = S_PR + 32 * 4 + 1024;
+
+enum Bar : uint32_t {
+    B_FULLQK = 0,   // 2: q and k tiles of a stage have landed
+    B_FULLV = 2,    // 2: the v tile
+    B_QK = 4,       // QK is complete
+    B_QKFREE = 5,   // QK has been read
+    B_P = 6,        // P is in TMEM
+    B_VP = 7,       // V's parts are in shared memory
+    B_KV = 8,       // 2: KV is complete
+    B_KVFREE = 10,  // 2: KV has been read
+    B_S = 12,       // the state's bf16 copy is in shared memory
+    B_O = 13,       // QS and PV are complete
+    B_OFREE = 14,   // QS and PV have been read
+    B_FREE = 15,    // 2: every product of the chunk in a stage is complete
+    B_OST = 17,     // 2: the outputs are staged in (or past) a stage's v tile
+    B_GAMMA = 19,   // w_n in two floats
+    B_DRAIN = 20,
+    B_COUNT = 21
+};
+
+// TMEM columns
+constexpr uint32_t T_QK = 0, T_P = 128, T_QS = 192, T_PV = 256, T_KV = 320;   // KV: 2 x 64
+constexpr uint32_t kTmemCols = 512;
+
+constexpr int kThreads = 18 * 32;
+
+struct Maps {
+    CUtensorMap q, k, v, out;
+};
+struct TcArgs {
+    Maps maps[kMaxScans];
+    DecayArgs a;
+};
+
+// x = h + m + l, three bf16 values whose sum is x to 2^-26 (each difference is exact in fp32).
+__device__ __forceinline__ void split3(float x0, float x1, uint32_t& h, uint32_t& m, uint32_t& l) {
+    h = pack_bf16(x0, x1);
+    x0 -= __uint_as_float(h << 16);
+    x1 -= __uint_as_float(h & 0xffff0000u);
+    m = pack_bf16(x0, x1);
+    x0 -= __uint_as_float(m << 16);
+    x1 -= __uint_as_float(m & 0xffff0000u);
+    l = pack_bf16(x0, x1);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+decay_tc_kernel(const __grid_constant__ TcArgs ta) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(sm);
+    auto bar = [&](uint32_t b) { return sb + S_BAR + 8 * b; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S_BAR + 8 * B_COUNT);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S_BAR + 8 * B_COUNT + 4);
+    float* gamma = reinterpret_cast<float*>(sm + S_BAR + 8 * B_COUNT + 8);   // w_128, w_n of the last chunk: hi, lo each
+    float* pw = reinterpret_cast<float*>(sm + S_PW);
+    float* pr = reinterpret_cast<float*>(sm + S_PR);
+
+    const DecayArgs& a = ta.a;
+    const DecayScan& s = a.scan[blockIdx.y];
+    const Maps& maps = ta.maps[blockIdx.y];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int z = blockIdx.x & 1;
+    const int h = (blockIdx.x >> 1) % a.Hv;
+    const int i = (blockIdx.x >> 1) / a.Hv;
+    const bool rev = s.reverse;
+    long long t0, t1;
+    seq_range(a.cu, i, a.T, t0, t1);
+    const int nch = (int)((t1 - t0 + kC - 1) / kC);
+    const int tail = (int)(t1 - t0) - (nch - 1) * kC;   // valid tokens of the last chunk
+    const float g = fmaxf(a.log_decay[h], kMinLogDecay);
+
+    if (warp == 16) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tc_fence_before();
+    }
+    if (tid == 0) {
+        *abort_flag = 0;
+        for (uint32_t b = 0; b < B_COUNT; ++b) {
+            const uint32_t count = b == B_QKFREE || b == B_P ? 8
+                                   : b == B_VP || b == B_KVFREE || b == B_KVFREE + 1 || b == B_S || b == B_OFREE || b == B_OST ||
+                                           b == B_OST + 1
+                                       ? 4 : 1;
+            mbar_init(bar(b), count);
+        }
+        mbar_fence_init();
+    }
+    if (tid <= kC) {
+        const float w = expf(g * (float)tid);
+        pw[tid] = w;
+        if (tid < 32) pr[31 - tid] = w;
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);   // this warp's quarter of the lanes
+
+    unsigned* status = a.status;
+    auto wait = [&](uint32_t b, uint32_t parity) {
+        return mbar_wait_bounded(bar(b), parity & 1, abort_flag, status, kStatusTimeout, kWaitLimitNs);
+    };
+    auto arrive = [&](uint32_t b) {   // once for the warp, after all its lanes
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(b));
+    };
+    auto chunk_of = [&](int it) { return rev ? nch - 1 - it : it; };
+    auto valid_of = [&](int it) { return chunk_of(it) == nch - 1 ? tail : kC; };
+
+    if (warp == 17) {
+        // ------------------------------------------------------------ copies
+        if (lane == 0 && nch > 0) {
+            auto load_qk = [&](int it) {
+                const int st = it & 1, t = (int)t0 + chunk_of(it) * kC;
+                const uint32_t b = bar(B_FULLQK + st);
+                mbar_arrive_expect_tx(b, 4 * kPanel);
+                for (int p = 0; p < 2; ++p) {
+                    tma_load_3d(sb + S_Q + (2 * st + p) * kPanel, &maps.q, 64 * p, h / s.q_div, t, b);
+                    tma_load_3d(sb + S_K + (2 * st + p) * kPanel, &maps.k, 64 * p, h / s.k_div, t, b);
+                }
+            };
+            auto load_v = [&](int it) {
+                const int st = it & 1, t = (int)t0 + chunk_of(it) * kC;
+                const uint32_t b = bar(B_FULLV + st);
+                mbar_arrive_expect_tx(b, kPanel);
+                tma_load_3d(sb + S_V + st * kPanel, &maps.v, 64 * z, h / s.v_div, t, b);
+            };
+            int loaded_qk = 0, loaded_v = 0;
+            for (; loaded_qk < 2 && loaded_qk < nch; ++loaded_qk, ++loaded_v) {
+                load_qk(loaded_qk);
+                load_v(loaded_v);
+            }
+            for (int x = 0; x < 2; ++x) {   // the decay of a full and of the last chunk, in two floats
+                const double w = exp((double)g * (x ? tail : kC));
+                gamma[2 * x] = (float)w;
+                gamma[2 * x + 1] = (float)(w - (double)(float)w);
+            }
+            mbar_arrive(bar(B_GAMMA));
+            for (int it = 0; it < nch; ++it) {
+                const int st = it & 1;
+                if (!wait(B_FREE + st, it >> 1)) break;
+                if (loaded_qk < nch) load_qk(loaded_qk++);
+                if (!wait(B_OST + st, it >> 1)) break;
+                if (valid_of(it) == kC && !s.out_f32) {
+                    tma_store_3d(&maps.out, 64 * z, h, (int)t0 + chunk_of(it) * kC, sb + S_V + st * kPanel);
+                    bulk_commit();
+                    bulk_wait_read();
+                }
+                if (loaded_v < nch) load_v(loaded_v++);
+            }
+            bulk_wait_all();
+            if (*abort_flag) {   // a wait gave up: no copy may still be landing when the shared memory is released
+                for (int it = max(0, loaded_qk - 2); it < loaded_qk; ++it)
+                    mbar_wait_drain(bar(B_FULLQK + (it & 1)), (it >> 1) & 1, kWaitLimitNs);
+                for (int it = max(0, loaded_v - 2); it < loaded_v; ++it)
+                    mbar_wait_drain(bar(B_FULLV + (it & 1)), (it >> 1) & 1, kWaitLimitNs);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 16) {
+        // ------------------------------------------------------------ products
+        if (lane == 0 && nch > 0) {
+            const uint64_t dQ = smem_desc(sb + S_Q, 16, 1024), dK = smem_desc(sb + S_K, 16, 1024),
+                           dKt = smem_desc(sb + S_K, kPanel, 1024), dV = smem_desc(sb + S_V, 1024, 1024),
+                           dVP = smem_desc(sb + S_VP, 1024, 1024), dSB = smem_desc(sb + S_SB, 1024, 1024);
+            auto issue_qk = [&](int it) {
+                const uint32_t o = ((it & 1) * 2 * kPanel) >> 4;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint32_t x = o + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4);
+                    mma_bf16(tmem + T_QK, dQ + x, dK + x, idesc_bf16(128, 128, 0, 0), ks > 0);
+                }
+                mma_commit(bar(B_QK));
+            };
+            bool ok = wait(B_FULLQK, 0);
+            if (ok) {
+                tc_fence_after();
+                issue_qk(0);
+            }
+            for (int it = 0; ok && it < nch; ++it) {
+                const int st = it & 1;
+                // K^T V~: V's parts are there (and, in a last chunk, the rows past its end are zero)
+                ok = wait(B_VP, it) && (it < 2 || wait(B_KVFREE + st, (it >> 1) - 1));
+                if (!ok) break;
+                tc_fence_after();
+                {
+                    const uint64_t kt = dKt + ((st * 2 * kPanel) >> 4);
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_bf16(tmem + T_KV + 64 * st, kt + ((ks * 2048) >> 4), dVP + ((p * kPanel + ks * 2048) >> 4),
+                                     idesc_bf16(128, 64, 1, 1), p + ks > 0);
+                    mma_commit(bar(B_KV + st));
+                }
+                if (it + 1 < nch) {   // the next chunk's scores, ahead of this chunk's outputs
+                    ok = wait(B_FULLQK + ((it + 1) & 1), (it + 1) >> 1) && wait(B_QKFREE, it);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_qk(it + 1);
+                }
+                ok = wait(B_S, it) && (it < 1 || wait(B_OFREE, it - 1));
+                if (!ok) break;
+                tc_fence_after();
+                {
+                    const uint64_t q = dQ + ((st * 2 * kPanel) >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_bf16(tmem + T_QS, q + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4), dSB + ((ks * 2048) >> 4),
+                                 idesc_bf16(128, 64, 0, 1), ks > 0);
+                }
+                ok = wait(B_P, it);
+                if (!ok) break;
+                tc_fence_after();
+                {
+                    const uint64_t v = dV + ((st * kPanel) >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_bf16_ta(tmem + T_PV, tmem + T_P + 8 * ks, v + ((ks * 2048) >> 4), idesc_bf16(128, 64, 0, 1),
+                                    ks > 0);
+                }
+                mma_commit(bar(B_O));
+                mma_commit(bar(B_FREE + st));
+            }
+            if (!ok) {   // every product issued is complete before TMEM and shared memory are released
+                mma_commit(bar(B_DRAIN));
+                mbar_wait_drain(bar(B_DRAIN), 0, kWaitLimitNs);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ------------------------------------------------------------ P: rows 32 (warp % 4) .., columns 64 (warp / 4) ..
+        const int quarter = warp & 3, half = warp >> 2, r = 32 * quarter + lane;
+        const float f = s.so * s.su;
+        for (int it = 0; it < nch; ++it) {
+            const int n = valid_of(it);
+            if (!wait(B_QK, it)) break;
+            tc_fence_after();
+            uint32_t x[2][32];
+            tmem_ld32(tl + T_QK + 64 * half, x[0]);
+            tmem_ld32(tl + T_QK + 64 * half + 32, x[1]);
+            tmem_wait_ld();
+            tc_fence_before();
+            arrive(B_QKFREE);
+            uint32_t p[32];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int cb = 2 * half + b, j0 = 32 * cb;   // columns j0 .. j0 + 31
+                if (cb != quarter && (cb > quarter) != rev) {   // all masked
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) p[16 * b + e] = 0u;
+                } else if (cb == quarter || (rev && n < kC)) {   // masked element by element
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float y[2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int j = j0 + 2 * e + u, d = rev ? j - r : r - j;
+                            y[u] = d >= 0 && j < n ? f * pw[max(d, 0)] * __uint_as_float(x[b][2 * e + u]) : 0.f;
+                        }
+                        p[16 * b + e] = pack_bf16(y[0], y[1]);
+                    }
+                } else {   // w_|r - j| = w_|r - near| w_|near - j|, near the column closest to the diagonal
+                    const float fr = f * pw[rev ? j0 - r : r - (j0 + 31)];
+                    const float4* wj = reinterpret_cast<const float4*>(rev ? pw : pr);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 w = wj[e];
+                        p[16 * b + 2 * e] = pack_bf16(fr * w.x * __uint_as_float(x[b][4 * e]),
+                                                      fr * w.y * __uint_as_float(x[b][4 * e + 1]));
+                        p[16 * b + 2 * e + 1] = pack_bf16(fr * w.z * __uint_as_float(x[b][4 * e + 2]),
+                                                          fr * w.w * __uint_as_float(x[b][4 * e + 3]));
+                    }
+                }
+            }
+            if (it > 0 && !wait(B_O, it - 1)) break;   // the previous chunk's PV has read P
+            tc_fence_after();
+            tmem_st32(tl + T_P + 32 * half, p);
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(B_P);
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------------------ V's parts and the outputs: one row a thread
+        const int r = tid - 256;
+        auto split_v = [&](int it) {
+            const int st = it & 1, n = valid_of(it);
+            if (!wait(B_FULLV + st, it >> 1)) return false;
+            if (n < kC) {   // the rows past the sequence's end are zero wherever they are summed over
+                if (!wait(B_FULLQK + st, it >> 1)) return false;
+                if (r >= n) {
+                    for (int c = 0; c < 8; ++c) {
+                        *reinterpret_cast<uint4*>(sm + S_V + st * kPanel + swz(r, c)) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(sm + S_K + 2 * st * kPanel + swz(r, c)) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(sm + S_K + (2 * st + 1) * kPanel + swz(r, c)) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+            const float w = r < n ? s.su * pw[rev ? r + 1 : n - 1 - r] : 0.f;
+            if (it > 0 && !wait(B_KV + ((it - 1) & 1), (it - 1) >> 1)) return false;   // the parts are free
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const uint4 v = *reinterpret_cast<const uint4*>(sm + S_V + st * kPanel + swz(r, c));
+                const uint32_t y[4] = {v.x, v.y, v.z, v.w};
+                uint32_t o[kParts][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    split3(w * __uint_as_float(y[e] << 16), w * __uint_as_float(y[e] & 0xffff0000u), o[0][e], o[1][e], o[2][e]);
+#pragma unroll
+                for (int p = 0; p < kParts; ++p)
+                    *reinterpret_cast<uint4*>(sm + S_VP + p * kPanel + swz(r, c)) = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
+            }
+            fence_proxy_async_smem();
+            arrive(B_VP);
+            return true;
+        };
+        bool ok = nch == 0 || split_v(0);
+        for (int it = 0; ok && it < nch; ++it) {
+            if (it + 1 < nch && !split_v(it + 1)) break;
+            const int st = it & 1, n = valid_of(it);
+            if (!wait(B_O, it)) break;
+            tc_fence_after();
+            const float w = s.so * pw[rev ? max(n - 1 - r, 0) : r + 1];
+            const size_t row = (size_t)(t0 + (long long)chunk_of(it) * kC + r) * s.out_stride + (size_t)h * kD + kHalf * z;
+            const bool staged = n == kC && !s.out_f32;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint32_t qs[32], pv[32];
+                tmem_ld32(tl + T_QS + 32 * b, qs);
+                tmem_ld32(tl + T_PV + 32 * b, pv);
+                tmem_wait_ld();
+                if (b == 1) {
+                    tc_fence_before();
+                    arrive(B_OFREE);
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float o[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = fmaf(w, __uint_as_float(qs[8 * c + e]), __uint_as_float(pv[8 * c + e]));
+                    if (s.out_f32) {
+                        if (r < n) {
+                            float4* d = reinterpret_cast<float4*>(static_cast<float*>(s.out) + row + 32 * b + 8 * c);
+                            d[0] = make_float4(o[0], o[1], o[2], o[3]);
+                            d[1] = make_float4(o[4], o[5], o[6], o[7]);
+                        }
+                    } else {
+                        const uint4 y = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
+                                                   pack_bf16(o[6], o[7]));
+                        if (staged) *reinterpret_cast<uint4*>(sm + S_V + st * kPanel + swz(r, 4 * b + c)) = y;
+                        else if (r < n) *reinterpret_cast<uint4*>(static_cast<bf16*>(s.out) + row + 32 * b + 8 * c) = y;
+                    }
+                }
+            }
+            if (staged) fence_proxy_async_smem();
+            arrive(B_OST + st);
+        }
+    } else {
+        // ------------------------------------------------------------ the state: row R of dk, 64 columns a thread
+        const int R = tid - 384;
+        const size_t base = ((size_t)i * a.Hv + h) * kD * kD;
+        float S[64];
+        if (s.init && s.init_t) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e) S[e] = s.init[base + (size_t)(kHalf * z + e) * kD + R];
+        } else if (s.init) {
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(s.init + base + (size_t)R * kD + kHalf * z + e);
+                S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 64; ++e) S[e] = 0.f;
+        }
+        auto write_sb = [&] {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<uint4*>(sm + S_SB + swz(R, c)) =
+                    make_uint4(pack_bf16(S[8 * c], S[8 * c + 1]), pack_bf16(S[8 * c + 2], S[8 * c + 3]),
+                               pack_bf16(S[8 * c + 4], S[8 * c + 5]), pack_bf16(S[8 * c + 6], S[8 * c + 7]));
+            fence_proxy_async_smem();
+            arrive(B_S);
+        };
+        bool ok = true;
+        if (nch > 0) {
+            write_sb();
+            ok = wait(B_GAMMA, 0);
+        }
+        for (int it = 0; ok && it < nch; ++it) {
+            const int st = it & 1, x = valid_of(it) == kC ? 0 : 2;
+            const float ghi = gamma[x], glo = gamma[x + 1];
+            if (it + 1 == nch && !s.final) break;   // nobody needs the last state
+            if (!(ok = wait(B_KV + st, it >> 1))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint32_t d[32];
+                tmem_ld32(tl + T_KV + 64 * st + 32 * b, d);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    S[32 * b + e] = fmaf(ghi, S[32 * b + e], fmaf(glo, S[32 * b + e], __uint_as_float(d[e])));
+            }
+            tc_fence_before();
+            arrive(B_KVFREE + st);
+            if (it + 1 < nch) {
+                if (!(ok = wait(B_O, it))) break;   // QS of this chunk has read the copy
+                write_sb();
+            }
+        }
+        if (s.final && ok) {
+#pragma unroll
+            for (int e = 0; e < 64; e += 4)
+                *reinterpret_cast<float4*>(s.final + base + (size_t)R * kD + kHalf * z + e) =
+                    make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 16) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+// [tokens, heads, 128] tensor of `elem`-byte values, token rows `stride` elements apart; box of 128 tokens x
+// 1 head x 64 values, 128-byte swizzle.
+cudaError_t make_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const void* base, long long tokens,
+                     int heads, long long stride) {
+    const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 1, kC};
+    const cuuint32_t elem[3] = {1, 1, 1};
+    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, elem,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t set_attributes() {
+    constexpr int kMaxDevices = 64;
+    static std::mutex mu;
+    static bool done[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(decay_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e == cudaSuccess) done[dev] = true;
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_decay_scan_tc(const DecayArgs& a) {
+    const auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+    if (!encode) return cudaErrorNotSupported;
+    cudaError_t e = set_attributes();
+    if (e != cudaSuccess) return e;
+    TcArgs t;
+    t.a = a;
+    for (int i = 0; i < a.num_scans; ++i) {
+        const DecayScan& s = a.scan[i];
+        Maps& m = t.maps[i];
+        if ((e = make_map(encode, &m.q, s.q, a.tokens, a.Hv / s.q_div, s.q_stride)) != cudaSuccess) return e;
+        if ((e = make_map(encode, &m.k, s.k, a.tokens, a.Hv / s.k_div, s.k_stride)) != cudaSuccess) return e;
+        if ((e = make_map(encode, &m.v, s.v, a.tokens, a.Hv / s.v_div, s.v_stride)) != cudaSuccess) return e;
+        if (!s.out_f32 && (e = make_map(encode, &m.out, s.out, a.tokens, a.Hv, s.out_stride)) != cudaSuccess) return e;
+    }
+    const dim3 grid((unsigned)((long long)a.nseq * a.Hv * 2), (unsigned)a.num_scans);
+    decay_tc_kernel<<<grid, kThreads, kSmem, a.stream>>>(t);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn
