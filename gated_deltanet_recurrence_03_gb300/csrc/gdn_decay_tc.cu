@@ -40,15 +40,15 @@ constexpr int kParts = 3;     // bf16 parts of the scaled V
 // Shared memory (bytes from the 1024-aligned base).  Panels: 128 rows x 64 bf16, 128-byte swizzle.
 constexpr uint32_t kPanel = 16384;
 constexpr uint32_t S_Q = 0;                          // 2 stages x 2 panels
-constexpr uint32_t S_K = S_Q + 2 * 2 * kPanel;       // 2 stages x 2 panels
-constexpr uint32_t S_V = S_K + 2 * 2 * kPanel;       // 2 stages x 1 panel; then the chunk's outputs
+constexpr uint32_t S_K = S_Q + 2 * 2 * kPanel;       // 2 stages x 2 panels; then the chunk's outputs
+constexpr uint32_t S_V = S_K + 2 * 2 * kPanel;       // 2 stages x 1 panel
 constexpr uint32_t S_VP = S_V + 2 * kPanel;          // the three parts of the scaled V
 constexpr uint32_t S_SB = S_VP + kParts * kPanel;    // the state in bf16: 128 dk rows
 constexpr uint32_t S_BAR = S_SB + kPanel;
 constexpr uint32_t kBarBytes = 256;
 constexpr uint32_t S_PW = S_BAR + kBarBytes;         // w_0 .. w_128
-constexpr uint32_t S_PR = S_PW + 132 * 4;            // w_31 .. w_0
-constexpr uint32_t kSmem = S_PR + 32 * 4 + 1024;
+constexpr uint32_t S_PR = S_PW + 132 * 4;            // w_15 .. w_0
+constexpr uint32_t kSmem = S_PR + 16 * 4 + 1024;
 
 enum Bar : uint32_t {
     B_FULLQK = 0,   // 2: q and k tiles of a stage have landed
@@ -63,7 +63,7 @@ enum Bar : uint32_t {
     B_O = 13,       // QS and PV are complete
     B_OFREE = 14,   // QS and PV have been read
     B_FREE = 15,    // 2: every product of the chunk in a stage is complete
-    B_OST = 17,     // 2: the outputs are staged in (or past) a stage's v tile
+    B_OST = 17,     // 2: the outputs are staged in (or stored past) a stage's k tile
     B_GAMMA = 19,   // w_n in two floats
     B_DRAIN = 20,
     B_COUNT = 21
@@ -92,6 +92,11 @@ __device__ __forceinline__ void split3(float x0, float x1, uint32_t& h, uint32_t
     x0 -= __uint_as_float(m << 16);
     x1 -= __uint_as_float(m & 0xffff0000u);
     l = pack_bf16(x0, x1);
+}
+
+// The part of a wait after its first test, out of line: the five roles' loops share one instruction cache.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* status) {
+    return mbar_wait_bounded(bar, parity, abort, status, kStatusTimeout, kWaitLimitNs);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -138,7 +143,7 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
     if (tid <= kC) {
         const float w = expf(g * (float)tid);
         pw[tid] = w;
-        if (tid < 32) pr[31 - tid] = w;
+        if (tid < 16) pr[15 - tid] = w;
     }
     __syncthreads();
     tc_fence_after();
@@ -147,7 +152,7 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
 
     unsigned* status = a.status;
     auto wait = [&](uint32_t b, uint32_t parity) {
-        return mbar_wait_bounded(bar(b), parity & 1, abort_flag, status, kStatusTimeout, kWaitLimitNs);
+        return mbar_try_wait(bar(b), parity & 1) || wait_slow(bar(b), parity & 1, abort_flag, status);
     };
     auto arrive = [&](uint32_t b) {   // once for the warp, after all its lanes
         __syncwarp();
@@ -159,14 +164,17 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
     if (warp == 17) {
         // ------------------------------------------------------------ copies
         if (lane == 0 && nch > 0) {
-            auto load_qk = [&](int it) {
+            auto load_q = [&](int it) {   // arms the barrier for q and k
                 const int st = it & 1, t = (int)t0 + chunk_of(it) * kC;
                 const uint32_t b = bar(B_FULLQK + st);
                 mbar_arrive_expect_tx(b, 4 * kPanel);
-                for (int p = 0; p < 2; ++p) {
+                for (int p = 0; p < 2; ++p)
                     tma_load_3d(sb + S_Q + (2 * st + p) * kPanel, &maps.q, 64 * p, h / s.q_div, t, b);
-                    tma_load_3d(sb + S_K + (2 * st + p) * kPanel, &maps.k, 64 * p, h / s.k_div, t, b);
-                }
+            };
+            auto load_k = [&](int it) {
+                const int st = it & 1, t = (int)t0 + chunk_of(it) * kC;
+                for (int p = 0; p < 2; ++p)
+                    tma_load_3d(sb + S_K + (2 * st + p) * kPanel, &maps.k, 64 * p, h / s.k_div, t, bar(B_FULLQK + st));
             };
             auto load_v = [&](int it) {
                 const int st = it & 1, t = (int)t0 + chunk_of(it) * kC;
@@ -174,11 +182,12 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
                 mbar_arrive_expect_tx(b, kPanel);
                 tma_load_3d(sb + S_V + st * kPanel, &maps.v, 64 * z, h / s.v_div, t, b);
             };
-            int loaded_qk = 0, loaded_v = 0;
-            for (; loaded_qk < 2 && loaded_qk < nch; ++loaded_qk, ++loaded_v) {
-                load_qk(loaded_qk);
-                load_v(loaded_v);
+            for (int it = 0; it < 2 && it < nch; ++it) {
+                load_v(it);
+                load_q(it);
+                load_k(it);
             }
+            int loaded = min(2, nch);   // chunks whose copies have all been issued
             for (int x = 0; x < 2; ++x) {   // the decay of a full and of the last chunk, in two floats
                 const double w = exp((double)g * (x ? tail : kC));
                 gamma[2 * x] = (float)w;
@@ -188,93 +197,105 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
             for (int it = 0; it < nch; ++it) {
                 const int st = it & 1;
                 if (!wait(B_FREE + st, it >> 1)) break;
-                if (loaded_qk < nch) load_qk(loaded_qk++);
-                if (!wait(B_OST + st, it >> 1)) break;
-                if (valid_of(it) == kC && !s.out_f32) {
-                    tma_store_3d(&maps.out, 64 * z, h, (int)t0 + chunk_of(it) * kC, sb + S_V + st * kPanel);
+                // chunk it + 2 into this stage; its k after the outputs that are staged there.  From here on
+                // the loop goes through, so that a barrier that is armed gets all its bytes.
+                if (it + 2 < nch) {
+                    load_v(it + 2);
+                    load_q(it + 2);
+                }
+                const bool staged = wait(B_OST + st, it >> 1);
+                if (staged && valid_of(it) == kC && !s.out_f32) {
+                    tma_store_3d(&maps.out, 64 * z, h, (int)t0 + chunk_of(it) * kC, sb + S_K + 2 * st * kPanel);
                     bulk_commit();
                     bulk_wait_read();
                 }
-                if (loaded_v < nch) load_v(loaded_v++);
+                if (it + 2 < nch) {
+                    load_k(it + 2);
+                    ++loaded;
+                }
+                if (!staged) break;
             }
             bulk_wait_all();
             if (*abort_flag) {   // a wait gave up: no copy may still be landing when the shared memory is released
-                for (int it = max(0, loaded_qk - 2); it < loaded_qk; ++it)
+                for (int it = max(0, loaded - 2); it < loaded; ++it) {
                     mbar_wait_drain(bar(B_FULLQK + (it & 1)), (it >> 1) & 1, kWaitLimitNs);
-                for (int it = max(0, loaded_v - 2); it < loaded_v; ++it)
                     mbar_wait_drain(bar(B_FULLV + (it & 1)), (it >> 1) & 1, kWaitLimitNs);
+                }
             }
         }
         __syncwarp();
     } else if (warp == 16) {
         // ------------------------------------------------------------ products
-        if (lane == 0 && nch > 0) {
-            const uint64_t dQ = smem_desc(sb + S_Q, 16, 1024), dK = smem_desc(sb + S_K, 16, 1024),
-                           dKt = smem_desc(sb + S_K, kPanel, 1024), dV = smem_desc(sb + S_V, 1024, 1024),
-                           dVP = smem_desc(sb + S_VP, 1024, 1024), dSB = smem_desc(sb + S_SB, 1024, 1024);
-            auto issue_qk = [&](int it) {
-                const uint32_t o = ((it & 1) * 2 * kPanel) >> 4;
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint32_t x = o + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4);
-                    mma_bf16(tmem + T_QK, dQ + x, dK + x, idesc_bf16(128, 128, 0, 0), ks > 0);
-                }
-                mma_commit(bar(B_QK));
-            };
-            bool ok = wait(B_FULLQK, 0);
-            if (ok) {
-                tc_fence_after();
-                issue_qk(0);
-            }
-            for (int it = 0; ok && it < nch; ++it) {
-                const int st = it & 1;
+        // The whole warp runs the loop and one elected lane issues: always the same one, so that a commit
+        // covers every product before it.
+        const uint64_t dQ = smem_desc(sb + S_Q, 16, 1024), dK = smem_desc(sb + S_K, 16, 1024),
+                       dKt = smem_desc(sb + S_K, kPanel, 1024), dV = smem_desc(sb + S_V, 1024, 1024),
+                       dVP = smem_desc(sb + S_VP, 1024, 1024), dSB = smem_desc(sb + S_SB, 1024, 1024);
+        bool ok = true;
+        for (int it = nch > 0 ? -1 : 0; it < nch; ++it) {
+            const int st = it & 1;
+            if (it >= 0) {
                 // K^T V~: V's parts are there (and, in a last chunk, the rows past its end are zero)
                 ok = wait(B_VP, it) && (it < 2 || wait(B_KVFREE + st, (it >> 1) - 1));
-                if (!ok) break;
+                if (!__all_sync(~0u, ok)) break;
                 tc_fence_after();
-                {
-                    const uint64_t kt = dKt + ((st * 2 * kPanel) >> 4);
+                const uint64_t kt = dKt + ((st * 2 * kPanel) >> 4);
+                const uint64_t q = dQ + ((st * 2 * kPanel) >> 4), v = dV + ((st * kPanel) >> 4);
+                const uint32_t dkv = tmem + T_KV + 64 * st;
+                if (elect_one()) {
 #pragma unroll
                     for (int p = 0; p < kParts; ++p)
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            mma_bf16(tmem + T_KV + 64 * st, kt + ((ks * 2048) >> 4), dVP + ((p * kPanel + ks * 2048) >> 4),
+                            mma_bf16(dkv, kt + ((ks * 2048) >> 4), dVP + ((p * kPanel + ks * 2048) >> 4),
                                      idesc_bf16(128, 64, 1, 1), p + ks > 0);
                     mma_commit(bar(B_KV + st));
                 }
-                if (it + 1 < nch) {   // the next chunk's scores, ahead of this chunk's outputs
-                    ok = wait(B_FULLQK + ((it + 1) & 1), (it + 1) >> 1) && wait(B_QKFREE, it);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_qk(it + 1);
-                }
+                __syncwarp();
                 ok = wait(B_S, it) && (it < 1 || wait(B_OFREE, it - 1));
-                if (!ok) break;
+                if (!__all_sync(~0u, ok)) break;
                 tc_fence_after();
-                {
-                    const uint64_t q = dQ + ((st * 2 * kPanel) >> 4);
+                if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         mma_bf16(tmem + T_QS, q + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4), dSB + ((ks * 2048) >> 4),
                                  idesc_bf16(128, 64, 0, 1), ks > 0);
                 }
+                __syncwarp();
                 ok = wait(B_P, it);
-                if (!ok) break;
+                if (!__all_sync(~0u, ok)) break;
                 tc_fence_after();
-                {
-                    const uint64_t v = dV + ((st * kPanel) >> 4);
+                if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         mma_bf16_ta(tmem + T_PV, tmem + T_P + 8 * ks, v + ((ks * 2048) >> 4), idesc_bf16(128, 64, 0, 1),
                                     ks > 0);
+                    mma_commit(bar(B_O));
+                    mma_commit(bar(B_FREE + st));
                 }
-                mma_commit(bar(B_O));
-                mma_commit(bar(B_FREE + st));
+                __syncwarp();
             }
-            if (!ok) {   // every product issued is complete before TMEM and shared memory are released
-                mma_commit(bar(B_DRAIN));
-                mbar_wait_drain(bar(B_DRAIN), 0, kWaitLimitNs);
+            // the next chunk's scores: P is formed from them while the next KV and QS run
+            if (it + 1 < nch) {
+                ok = wait(B_FULLQK + ((it + 1) & 1), (it + 1) >> 1) && (it < 0 || wait(B_QKFREE, it));
+                if (!__all_sync(~0u, ok)) break;
+                tc_fence_after();
+                const uint32_t o = (((it + 1) & 1) * 2 * kPanel) >> 4;
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {
+                        const uint32_t x = o + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4);
+                        mma_bf16(tmem + T_QK, dQ + x, dK + x, idesc_bf16(128, 128, 0, 0), ks > 0);
+                    }
+                    mma_commit(bar(B_QK));
+                }
+                __syncwarp();
             }
+        }
+        if (*abort_flag) {   // every product issued is complete before TMEM and shared memory are released
+            if (elect_one()) mma_commit(bar(B_DRAIN));
+            __syncwarp();
+            mbar_wait_drain(bar(B_DRAIN), 0, kWaitLimitNs);
         }
         __syncwarp();
     } else if (warp < 8) {
@@ -285,46 +306,47 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
             const int n = valid_of(it);
             if (!wait(B_QK, it)) break;
             tc_fence_after();
-            uint32_t x[2][32];
-            tmem_ld32(tl + T_QK + 64 * half, x[0]);
-            tmem_ld32(tl + T_QK + 64 * half + 32, x[1]);
-            tmem_wait_ld();
-            tc_fence_before();
-            arrive(B_QKFREE);
-            uint32_t p[32];
+            // QK(it) was issued after PV(it - 1): that product has read P
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {   // 16 columns at a time
+                const int j0 = 64 * half + 16 * b;
+                uint32_t x[16], p[8];
+                tmem_ld16(tl + T_QK + j0, x);
+                tmem_wait_ld();
+                if (b == 3) {
+                    tc_fence_before();
+                    arrive(B_QKFREE);
+                }
+                // from the warp's nearest row, columns on the diagonal's masked side (> 0) and on its open one
+                const int r0 = 32 * quarter, masked = rev ? r0 - (j0 + 15) : j0 - (r0 + 31);
+                const int open = rev ? j0 - (r0 + 31) : r0 - (j0 + 15);
+                if (masked > 0) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int cb = 2 * half + b, j0 = 32 * cb;   // columns j0 .. j0 + 31
-                if (cb != quarter && (cb > quarter) != rev) {   // all masked
+                    for (int e = 0; e < 8; ++e) p[e] = 0u;
+                } else if (open < 0 || (rev && n < kC)) {   // masked element by element
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) p[16 * b + e] = 0u;
-                } else if (cb == quarter || (rev && n < kC)) {   // masked element by element
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
+                    for (int e = 0; e < 8; ++e) {
                         float y[2];
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             const int j = j0 + 2 * e + u, d = rev ? j - r : r - j;
-                            y[u] = d >= 0 && j < n ? f * pw[max(d, 0)] * __uint_as_float(x[b][2 * e + u]) : 0.f;
+                            y[u] = d >= 0 && j < n ? f * pw[max(d, 0)] * __uint_as_float(x[2 * e + u]) : 0.f;
                         }
-                        p[16 * b + e] = pack_bf16(y[0], y[1]);
+                        p[e] = pack_bf16(y[0], y[1]);
                     }
                 } else {   // w_|r - j| = w_|r - near| w_|near - j|, near the column closest to the diagonal
-                    const float fr = f * pw[rev ? j0 - r : r - (j0 + 31)];
+                    const float fr = f * pw[rev ? j0 - r : r - (j0 + 15)];
                     const float4* wj = reinterpret_cast<const float4*>(rev ? pw : pr);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < 4; ++e) {
                         const float4 w = wj[e];
-                        p[16 * b + 2 * e] = pack_bf16(fr * w.x * __uint_as_float(x[b][4 * e]),
-                                                      fr * w.y * __uint_as_float(x[b][4 * e + 1]));
-                        p[16 * b + 2 * e + 1] = pack_bf16(fr * w.z * __uint_as_float(x[b][4 * e + 2]),
-                                                          fr * w.w * __uint_as_float(x[b][4 * e + 3]));
+                        p[2 * e] = pack_bf16(fr * w.x * __uint_as_float(x[4 * e]), fr * w.y * __uint_as_float(x[4 * e + 1]));
+                        p[2 * e + 1] =
+                            pack_bf16(fr * w.z * __uint_as_float(x[4 * e + 2]), fr * w.w * __uint_as_float(x[4 * e + 3]));
                     }
                 }
+                tmem_st8(tl + T_P + j0 / 2, p);
             }
-            if (it > 0 && !wait(B_O, it - 1)) break;   // the previous chunk's PV has read P
-            tc_fence_after();
-            tmem_st32(tl + T_P + 32 * half, p);
             tmem_wait_st();
             tc_fence_before();
             arrive(B_P);
@@ -338,16 +360,16 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
             if (n < kC) {   // the rows past the sequence's end are zero wherever they are summed over
                 if (!wait(B_FULLQK + st, it >> 1)) return false;
                 if (r >= n) {
-                    for (int c = 0; c < 8; ++c) {
-                        *reinterpret_cast<uint4*>(sm + S_V + st * kPanel + swz(r, c)) = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(sm + S_K + 2 * st * kPanel + swz(r, c)) = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(sm + S_K + (2 * st + 1) * kPanel + swz(r, c)) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+                    for (int c = 0; c < 24; ++c) {   // v's panel and k's two
+                        const uint32_t panel = c < 8 ? S_V + st * kPanel : S_K + (2 * st + (c >> 3) - 1) * kPanel;
+                        *reinterpret_cast<uint4*>(sm + panel + swz(r, c & 7)) = make_uint4(0, 0, 0, 0);
                     }
                 }
             }
             const float w = r < n ? s.su * pw[rev ? r + 1 : n - 1 - r] : 0.f;
             if (it > 0 && !wait(B_KV + ((it - 1) & 1), (it - 1) >> 1)) return false;   // the parts are free
-#pragma unroll
+#pragma unroll 2
             for (int c = 0; c < 8; ++c) {
                 const uint4 v = *reinterpret_cast<const uint4*>(sm + S_V + st * kPanel + swz(r, c));
                 const uint32_t y[4] = {v.x, v.y, v.z, v.w};
@@ -363,41 +385,41 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
             arrive(B_VP);
             return true;
         };
-        bool ok = nch == 0 || split_v(0);
-        for (int it = 0; ok && it < nch; ++it) {
+        for (int it = -1; it < nch; ++it) {
             if (it + 1 < nch && !split_v(it + 1)) break;
+            if (it < 0) continue;
             const int st = it & 1, n = valid_of(it);
             if (!wait(B_O, it)) break;
             tc_fence_after();
             const float w = s.so * pw[rev ? max(n - 1 - r, 0) : r + 1];
             const size_t row = (size_t)(t0 + (long long)chunk_of(it) * kC + r) * s.out_stride + (size_t)h * kD + kHalf * z;
             const bool staged = n == kC && !s.out_f32;
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t qs[32], pv[32];
-                tmem_ld32(tl + T_QS + 32 * b, qs);
-                tmem_ld32(tl + T_PV + 32 * b, pv);
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                uint32_t qs[16], pv[16];
+                tmem_ld16(tl + T_QS + 16 * b, qs);
+                tmem_ld16(tl + T_PV + 16 * b, pv);
                 tmem_wait_ld();
-                if (b == 1) {
+                if (b == 3) {
                     tc_fence_before();
                     arrive(B_OFREE);
                 }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                     float o[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) o[e] = fmaf(w, __uint_as_float(qs[8 * c + e]), __uint_as_float(pv[8 * c + e]));
                     if (s.out_f32) {
                         if (r < n) {
-                            float4* d = reinterpret_cast<float4*>(static_cast<float*>(s.out) + row + 32 * b + 8 * c);
+                            float4* d = reinterpret_cast<float4*>(static_cast<float*>(s.out) + row + 16 * b + 8 * c);
                             d[0] = make_float4(o[0], o[1], o[2], o[3]);
                             d[1] = make_float4(o[4], o[5], o[6], o[7]);
                         }
                     } else {
                         const uint4 y = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
                                                    pack_bf16(o[6], o[7]));
-                        if (staged) *reinterpret_cast<uint4*>(sm + S_V + st * kPanel + swz(r, 4 * b + c)) = y;
-                        else if (r < n) *reinterpret_cast<uint4*>(static_cast<bf16*>(s.out) + row + 32 * b + 8 * c) = y;
+                        if (staged) *reinterpret_cast<uint4*>(sm + S_K + 2 * st * kPanel + swz(r, 2 * b + c)) = y;
+                        else if (r < n) *reinterpret_cast<uint4*>(static_cast<bf16*>(s.out) + row + 16 * b + 8 * c) = y;
                     }
                 }
             }
@@ -443,13 +465,13 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
             if (!(ok = wait(B_KV + st, it >> 1))) break;
             tc_fence_after();
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t d[32];
-                tmem_ld32(tl + T_KV + 64 * st + 32 * b, d);
+            for (int b = 0; b < 4; ++b) {
+                uint32_t d[16];
+                tmem_ld16(tl + T_KV + 64 * st + 16 * b, d);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    S[32 * b + e] = fmaf(ghi, S[32 * b + e], fmaf(glo, S[32 * b + e], __uint_as_float(d[e])));
+                for (int e = 0; e < 16; ++e)
+                    S[16 * b + e] = fmaf(ghi, S[16 * b + e], fmaf(glo, S[16 * b + e], __uint_as_float(d[e])));
             }
             tc_fence_before();
             arrive(B_KVFREE + st);
