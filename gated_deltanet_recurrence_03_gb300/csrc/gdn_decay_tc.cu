@@ -16,8 +16,8 @@
 // exactly, K is exact, so the states that leave the kernel have fp32 accuracy; P and the state's copy in QS are
 // rounded to bf16, each 2^-9 of terms whose sum is rounded to bf16 anyway.
 //
-// Warps: 0-7 form P; 8-11 scale and split V and write the outputs; 12-15 keep the state; 16 issues the MMAs,
-// 17 the copies.  Hand-overs are mbarriers; every wait is bounded.
+// Warps: 0-7 form P and write the outputs; 8-11 scale and split V; 12-15 keep the state; 16 issues the MMAs, 17
+// the copies.  Hand-overs are mbarriers; every wait is bounded.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -56,9 +56,10 @@ enum Bar : uint32_t {
     B_QK = 4,       // QK is complete
     B_QKFREE = 5,   // QK has been read
     B_P = 6,        // P is in TMEM
-    B_VP = 7,       // V's parts are in shared memory
-    B_KV = 8,       // 2: KV is complete
-    B_KVFREE = 10,  // 2: KV has been read
+    B_VP = 7,       // 2: the parts of V's rows 0-63, 64-127 are in shared memory
+    B_KVHALF = 9,   // the products of rows 0-63 are complete
+    B_KV = 10,      // KV is complete
+    B_KVFREE = 11,  // KV has been read
     B_S = 12,       // the state's bf16 copy is in shared memory
     B_O = 13,       // QS and PV are complete
     B_OFREE = 14,   // QS and PV have been read
@@ -69,11 +70,14 @@ enum Bar : uint32_t {
     B_COUNT = 21
 };
 
-// TMEM columns
-constexpr uint32_t T_QK = 0, T_P = 128, T_QS = 192, T_PV = 256, T_KV = 320;   // KV: 2 x 64
+// TMEM columns (all 512): KV holds the products with V's three parts side by side.
+constexpr uint32_t T_QK = 0, T_P = 128, T_QS = 192, T_PV = 256, T_KV = 320;
 constexpr uint32_t kTmemCols = 512;
 
-constexpr int kThreads = 18 * 32;
+// 20 warps, five groups of four.  Registers a thread: 96 at launch; the group of the issuing warps gives up 32 and
+// the state's takes them (64 hold its part of the state): 3 x 96 + 128 + 64 = 5 x 96.
+constexpr int kThreads = 20 * 32;
+constexpr int kRegsIssue = 64, kRegsState = 128;
 
 struct Maps {
     CUtensorMap q, k, v, out;
@@ -94,13 +98,24 @@ __device__ __forceinline__ void split3(float x0, float x1, uint32_t& h, uint32_t
     l = pack_bf16(x0, x1);
 }
 
-// The part of a wait after its first test, out of line: the five roles' loops share one instruction cache.
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* status) {
-    return mbar_wait_bounded(bar, parity, abort, status, kStatusTimeout, kWaitLimitNs);
+// mbar_wait_bounded in fewer instructions: the five roles' loops share one instruction cache.
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer();
+    while (!*abort) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (globaltimer() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            atomicOr(status, kStatusTimeout);
+        }
+    }
+    return false;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
-decay_tc_kernel(const __grid_constant__ TcArgs ta) {
+// One scan's CTA.  REV: a reverse scan; F32: the outputs are float.  (Template arguments, not branches, for the
+// instruction cache's sake.)
+template <bool REV, bool F32>
+__device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
@@ -118,7 +133,7 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
     const int z = blockIdx.x & 1;
     const int h = (blockIdx.x >> 1) % a.Hv;
     const int i = (blockIdx.x >> 1) / a.Hv;
-    const bool rev = s.reverse;
+    constexpr bool rev = REV;
     long long t0, t1;
     seq_range(a.cu, i, a.T, t0, t1);
     const int nch = (int)((t1 - t0 + kC - 1) / kC);
@@ -132,10 +147,9 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
     if (tid == 0) {
         *abort_flag = 0;
         for (uint32_t b = 0; b < B_COUNT; ++b) {
-            const uint32_t count = b == B_QKFREE || b == B_P ? 8
-                                   : b == B_VP || b == B_KVFREE || b == B_KVFREE + 1 || b == B_S || b == B_OFREE || b == B_OST ||
-                                           b == B_OST + 1
-                                       ? 4 : 1;
+            const uint32_t count = b == B_QKFREE || b == B_P || b == B_OFREE || b == B_OST || b == B_OST + 1 ? 8
+                                   : b == B_KVFREE || b == B_S ? 4
+                                   : b == B_VP || b == B_VP + 1 ? 2 : 1;
             mbar_init(bar(b), count);
         }
         mbar_fence_init();
@@ -152,7 +166,7 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
 
     unsigned* status = a.status;
     auto wait = [&](uint32_t b, uint32_t parity) {
-        return mbar_try_wait(bar(b), parity & 1) || wait_slow(bar(b), parity & 1, abort_flag, status);
+        return wait_or_abort(bar(b), parity & 1, abort_flag, status);
     };
     auto arrive = [&](uint32_t b) {   // once for the warp, after all its lanes
         __syncwarp();
@@ -161,33 +175,42 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
     auto chunk_of = [&](int it) { return rev ? nch - 1 - it : it; };
     auto valid_of = [&](int it) { return chunk_of(it) == nch - 1 ? tail : kC; };
 
-    if (warp == 17) {
+    if (warp >= 16) regs_dec<kRegsIssue>();
+    if (warp >= 18) {
+        // only there to make the group of four whole
+    } else if (warp == 17) {
         // ------------------------------------------------------------ copies
         if (lane == 0 && nch > 0) {
-            auto load_q = [&](int it) {   // arms the barrier for q and k
+            const int hq = h / s.q_div, hk = h / s.k_div, hv = h / s.v_div;
+            auto load_qv = [&](int it) {   // arms the barriers of the chunk's three tiles
                 const int st = it & 1, t = (int)t0 + chunk_of(it) * kC;
-                const uint32_t b = bar(B_FULLQK + st);
-                mbar_arrive_expect_tx(b, 4 * kPanel);
-                for (int p = 0; p < 2; ++p)
-                    tma_load_3d(sb + S_Q + (2 * st + p) * kPanel, &maps.q, 64 * p, h / s.q_div, t, b);
+                const uint32_t bv = bar(B_FULLV + st), bqk = bar(B_FULLQK + st);
+                mbar_arrive_expect_tx(bv, kPanel);
+                tma_load_3d(sb + S_V + st * kPanel, &maps.v, 64 * z, hv, t, bv);
+                mbar_arrive_expect_tx(bqk, 4 * kPanel);
+                tma_load_3d(sb + S_Q + 2 * st * kPanel, &maps.q, 0, hq, t, bqk);
+                tma_load_3d(sb + S_Q + (2 * st + 1) * kPanel, &maps.q, 64, hq, t, bqk);
             };
             auto load_k = [&](int it) {
                 const int st = it & 1, t = (int)t0 + chunk_of(it) * kC;
-                for (int p = 0; p < 2; ++p)
-                    tma_load_3d(sb + S_K + (2 * st + p) * kPanel, &maps.k, 64 * p, h / s.k_div, t, bar(B_FULLQK + st));
+                tma_load_3d(sb + S_K + 2 * st * kPanel, &maps.k, 0, hk, t, bar(B_FULLQK + st));
+                tma_load_3d(sb + S_K + (2 * st + 1) * kPanel, &maps.k, 64, hk, t, bar(B_FULLQK + st));
             };
-            auto load_v = [&](int it) {
-                const int st = it & 1, t = (int)t0 + chunk_of(it) * kC;
-                const uint32_t b = bar(B_FULLV + st);
-                mbar_arrive_expect_tx(b, kPanel);
-                tma_load_3d(sb + S_V + st * kPanel, &maps.v, 64 * z, h / s.v_div, t, b);
+            auto prefetch = [&](int it) {   // into L2: the loads wait for a stage to be free and then cannot wait for DRAM
+                if (it >= nch) return;
+                const int t = (int)t0 + chunk_of(it) * kC;
+                tma_prefetch_3d(&maps.v, 64 * z, hv, t);
+                tma_prefetch_3d(&maps.q, 64 * z, hq, t);   // the other half of q and k: the head's other CTA
+                tma_prefetch_3d(&maps.k, 64 * z, hk, t);
             };
-            for (int it = 0; it < 2 && it < nch; ++it) {
-                load_v(it);
-                load_q(it);
-                load_k(it);
+            int loaded = 0;
+            for (; loaded < 2 && loaded < nch; ++loaded) {
+                load_qv(loaded);
+                load_k(loaded);
             }
-            int loaded = min(2, nch);   // chunks whose copies have all been issued
+            prefetch(2);
+            prefetch(3);
+#pragma unroll 1
             for (int x = 0; x < 2; ++x) {   // the decay of a full and of the last chunk, in two floats
                 const double w = exp((double)g * (x ? tail : kC));
                 gamma[2 * x] = (float)w;
@@ -195,17 +218,20 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
             }
             mbar_arrive(bar(B_GAMMA));
             for (int it = 0; it < nch; ++it) {
-                const int st = it & 1;
+                const int st = it & 1, t = (int)t0 + chunk_of(it) * kC;
                 if (!wait(B_FREE + st, it >> 1)) break;
-                // chunk it + 2 into this stage; its k after the outputs that are staged there.  From here on
-                // the loop goes through, so that a barrier that is armed gets all its bytes.
-                if (it + 2 < nch) {
-                    load_v(it + 2);
-                    load_q(it + 2);
-                }
+                // chunk it + 2 into this stage, its k after the outputs that are staged there.  From here on the
+                // round goes through, so that a barrier that is armed gets all its bytes.
+                if (it + 2 < nch) load_qv(it + 2);
+                prefetch(it + 4);
                 const bool staged = wait(B_OST + st, it >> 1);
-                if (staged && valid_of(it) == kC && !s.out_f32) {
-                    tma_store_3d(&maps.out, 64 * z, h, (int)t0 + chunk_of(it) * kC, sb + S_K + 2 * st * kPanel);
+                if (staged && valid_of(it) == kC) {
+                    if (F32) {
+                        tma_store_3d(&maps.out, 64 * z, h, t, sb + S_K + 2 * st * kPanel);
+                        tma_store_3d(&maps.out, 64 * z + 32, h, t, sb + S_K + (2 * st + 1) * kPanel);
+                    } else {
+                        tma_store_3d(&maps.out, 64 * z, h, t, sb + S_K + 2 * st * kPanel);
+                    }
                     bulk_commit();
                     bulk_wait_read();
                 }
@@ -230,26 +256,35 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
         // covers every product before it.
         const uint64_t dQ = smem_desc(sb + S_Q, 16, 1024), dK = smem_desc(sb + S_K, 16, 1024),
                        dKt = smem_desc(sb + S_K, kPanel, 1024), dV = smem_desc(sb + S_V, 1024, 1024),
-                       dVP = smem_desc(sb + S_VP, 1024, 1024), dSB = smem_desc(sb + S_SB, 1024, 1024);
+                       dVP = smem_desc(sb + S_VP, kPanel, 1024), dSB = smem_desc(sb + S_SB, 1024, 1024);
         bool ok = true;
         for (int it = nch > 0 ? -1 : 0; it < nch; ++it) {
             const int st = it & 1;
             if (it >= 0) {
                 // K^T V~: V's parts are there (and, in a last chunk, the rows past its end are zero)
-                ok = wait(B_VP, it) && (it < 2 || wait(B_KVFREE + st, (it >> 1) - 1));
+                ok = wait(B_VP, it) && (it < 1 || wait(B_KVFREE, it - 1));
                 if (!__all_sync(~0u, ok)) break;
                 tc_fence_after();
                 const uint64_t kt = dKt + ((st * 2 * kPanel) >> 4);
                 const uint64_t q = dQ + ((st * 2 * kPanel) >> 4), v = dV + ((st * kPanel) >> 4);
-                const uint32_t dkv = tmem + T_KV + 64 * st;
+                // half the rows at a time, so that the first half's parts are replaced while the second runs
                 if (elect_one()) {
 #pragma unroll
-                    for (int p = 0; p < kParts; ++p)
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_bf16(tmem + T_KV, kt + ((ks * 2048) >> 4), dVP + ((ks * 2048) >> 4),
+                                 idesc_bf16(128, 64 * kParts, 1, 1), ks > 0);
+                    mma_commit(bar(B_KVHALF));
+                }
+                __syncwarp();
+                ok = wait(B_VP + 1, it);
+                if (!__all_sync(~0u, ok)) break;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            mma_bf16(dkv, kt + ((ks * 2048) >> 4), dVP + ((p * kPanel + ks * 2048) >> 4),
-                                     idesc_bf16(128, 64, 1, 1), p + ks > 0);
-                    mma_commit(bar(B_KV + st));
+                    for (int ks = 4; ks < 8; ++ks)
+                        mma_bf16(tmem + T_KV, kt + ((ks * 2048) >> 4), dVP + ((ks * 2048) >> 4),
+                                 idesc_bf16(128, 64 * kParts, 1, 1), 1);
+                    mma_commit(bar(B_KV));
                 }
                 __syncwarp();
                 ok = wait(B_S, it) && (it < 1 || wait(B_OFREE, it - 1));
@@ -299,14 +334,58 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
         }
         __syncwarp();
     } else if (warp < 8) {
-        // ------------------------------------------------------------ P: rows 32 (warp % 4) .., columns 64 (warp / 4) ..
+        // ------------------------------------------------------------ P and the outputs: rows 32 (warp % 4) ..,
+        // half warp / 4 of the columns.  A chunk's outputs come while the next chunk's scores are formed.
         const int quarter = warp & 3, half = warp >> 2, r = 32 * quarter + lane;
         const float f = s.so * s.su;
-        for (int it = 0; it < nch; ++it) {
-            const int n = valid_of(it);
-            if (!wait(B_QK, it)) break;
+        for (int it = -1; it < nch; ++it) {
+            if (it >= 0) {
+                const int st = it & 1, n = valid_of(it);
+                if (!wait(B_O, it)) break;
+                tc_fence_after();
+                const float w = s.so * pw[rev ? max(n - 1 - r, 0) : r + 1];
+                const size_t row = (size_t)(t0 + (long long)chunk_of(it) * kC + r) * s.out_stride + (size_t)h * kD + kHalf * z;
+#pragma unroll 1
+                for (int b = 2 * half; b < 2 * half + 2; ++b) {
+                    uint32_t qs[16], pv[16];
+                    tmem_ld16(tl + T_QS + 16 * b, qs);
+                    tmem_ld16(tl + T_PV + 16 * b, pv);
+                    tmem_wait_ld();
+                    if (b & 1) {
+                        tc_fence_before();
+                        arrive(B_OFREE);
+                    }
+                    float o[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = fmaf(w, __uint_as_float(qs[e]), __uint_as_float(pv[e]));
+                    if (F32) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const float4 y = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                            if (n == kC)
+                                *reinterpret_cast<float4*>(sm + S_K + (2 * st + half) * kPanel + swz(r, 4 * (b & 1) + c)) = y;
+                            else if (r < n)
+                                *reinterpret_cast<float4*>(static_cast<float*>(s.out) + row + 16 * b + 4 * c) = y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const uint4 y =
+                                make_uint4(pack_bf16(o[8 * c], o[8 * c + 1]), pack_bf16(o[8 * c + 2], o[8 * c + 3]),
+                                           pack_bf16(o[8 * c + 4], o[8 * c + 5]), pack_bf16(o[8 * c + 6], o[8 * c + 7]));
+                            if (n == kC) *reinterpret_cast<uint4*>(sm + S_K + 2 * st * kPanel + swz(r, 2 * b + c)) = y;
+                            else if (r < n) *reinterpret_cast<uint4*>(static_cast<bf16*>(s.out) + row + 16 * b + 8 * c) = y;
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                arrive(B_OST + st);
+            }
+            if (it + 1 >= nch) break;
+            const int n = valid_of(it + 1);
+            if (!wait(B_QK, it + 1)) break;
             tc_fence_after();
-            // QK(it) was issued after PV(it - 1): that product has read P
+            // the previous chunk's PV has read P: its outputs have been read above
 #pragma unroll 1
             for (int b = 0; b < 4; ++b) {   // 16 columns at a time
                 const int j0 = 64 * half + 16 * b;
@@ -352,13 +431,13 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
             arrive(B_P);
         }
     } else if (warp < 12) {
-        // ------------------------------------------------------------ V's parts and the outputs: one row a thread
-        const int r = tid - 256;
-        auto split_v = [&](int it) {
+        // ------------------------------------------------------------ V's parts: one row a thread
+        const int r = tid - 256, half = (warp >> 1) & 1;
+        for (int it = 0; it < nch; ++it) {
             const int st = it & 1, n = valid_of(it);
-            if (!wait(B_FULLV + st, it >> 1)) return false;
+            if (!wait(B_FULLV + st, it >> 1)) break;
             if (n < kC) {   // the rows past the sequence's end are zero wherever they are summed over
-                if (!wait(B_FULLQK + st, it >> 1)) return false;
+                if (!wait(B_FULLQK + st, it >> 1)) break;
                 if (r >= n) {
 #pragma unroll 1
                     for (int c = 0; c < 24; ++c) {   // v's panel and k's two
@@ -368,7 +447,8 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
                 }
             }
             const float w = r < n ? s.su * pw[rev ? r + 1 : n - 1 - r] : 0.f;
-            if (it > 0 && !wait(B_KV + ((it - 1) & 1), (it - 1) >> 1)) return false;   // the parts are free
+            // the products of the previous chunk that read these rows' parts are complete
+            if (it > 0 && !wait(half ? B_KV : B_KVHALF, it - 1)) break;
 #pragma unroll 2
             for (int c = 0; c < 8; ++c) {
                 const uint4 v = *reinterpret_cast<const uint4*>(sm + S_V + st * kPanel + swz(r, c));
@@ -382,52 +462,11 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
                     *reinterpret_cast<uint4*>(sm + S_VP + p * kPanel + swz(r, c)) = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
             }
             fence_proxy_async_smem();
-            arrive(B_VP);
-            return true;
-        };
-        for (int it = -1; it < nch; ++it) {
-            if (it + 1 < nch && !split_v(it + 1)) break;
-            if (it < 0) continue;
-            const int st = it & 1, n = valid_of(it);
-            if (!wait(B_O, it)) break;
-            tc_fence_after();
-            const float w = s.so * pw[rev ? max(n - 1 - r, 0) : r + 1];
-            const size_t row = (size_t)(t0 + (long long)chunk_of(it) * kC + r) * s.out_stride + (size_t)h * kD + kHalf * z;
-            const bool staged = n == kC && !s.out_f32;
-#pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-                uint32_t qs[16], pv[16];
-                tmem_ld16(tl + T_QS + 16 * b, qs);
-                tmem_ld16(tl + T_PV + 16 * b, pv);
-                tmem_wait_ld();
-                if (b == 3) {
-                    tc_fence_before();
-                    arrive(B_OFREE);
-                }
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float o[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = fmaf(w, __uint_as_float(qs[8 * c + e]), __uint_as_float(pv[8 * c + e]));
-                    if (s.out_f32) {
-                        if (r < n) {
-                            float4* d = reinterpret_cast<float4*>(static_cast<float*>(s.out) + row + 16 * b + 8 * c);
-                            d[0] = make_float4(o[0], o[1], o[2], o[3]);
-                            d[1] = make_float4(o[4], o[5], o[6], o[7]);
-                        }
-                    } else {
-                        const uint4 y = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
-                                                   pack_bf16(o[6], o[7]));
-                        if (staged) *reinterpret_cast<uint4*>(sm + S_K + 2 * st * kPanel + swz(r, 2 * b + c)) = y;
-                        else if (r < n) *reinterpret_cast<uint4*>(static_cast<bf16*>(s.out) + row + 16 * b + 8 * c) = y;
-                    }
-                }
-            }
-            if (staged) fence_proxy_async_smem();
-            arrive(B_OST + st);
+            arrive(B_VP + half);
         }
     } else {
         // ------------------------------------------------------------ the state: row R of dk, 64 columns a thread
+        regs_inc<kRegsState>();
         const int R = tid - 384;
         const size_t base = ((size_t)i * a.Hv + h) * kD * kD;
         float S[64];
@@ -459,24 +498,27 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
             ok = wait(B_GAMMA, 0);
         }
         for (int it = 0; ok && it < nch; ++it) {
-            const int st = it & 1, x = valid_of(it) == kC ? 0 : 2;
+            const int x = valid_of(it) == kC ? 0 : 2;
             const float ghi = gamma[x], glo = gamma[x + 1];
             if (it + 1 == nch && !s.final) break;   // nobody needs the last state
-            if (!(ok = wait(B_KV + st, it >> 1))) break;
+            if (!(ok = wait(B_KV, it))) break;
             tc_fence_after();
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                uint32_t d[16];
-                tmem_ld16(tl + T_KV + 64 * st + 16 * b, d);
+                uint32_t d[kParts][16];
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) tmem_ld16(tl + T_KV + 64 * p + 16 * b, d[p]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    S[16 * b + e] = fmaf(ghi, S[16 * b + e], fmaf(glo, S[16 * b + e], __uint_as_float(d[e])));
+                for (int e = 0; e < 16; ++e) {
+                    const float y = (__uint_as_float(d[2][e]) + __uint_as_float(d[1][e])) + __uint_as_float(d[0][e]);
+                    S[16 * b + e] = fmaf(ghi, S[16 * b + e], fmaf(glo, S[16 * b + e], y));
+                }
             }
             tc_fence_before();
-            arrive(B_KVFREE + st);
+            arrive(B_KVFREE);
             if (it + 1 < nch) {
-                if (!(ok = wait(B_O, it))) break;   // QS of this chunk has read the copy
+                if (!(ok = wait(B_O, it))) break;   // QS has read the copy of the state
                 write_sb();
             }
         }
@@ -495,16 +537,29 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
     }
 }
 
+__global__ void __launch_bounds__(kThreads, 1)
+decay_tc_kernel(const __grid_constant__ TcArgs ta) {
+    const DecayScan& s = ta.a.scan[blockIdx.y];
+    if (s.reverse) {
+        if (s.out_f32) decay_tc_body<true, true>(ta);
+        else decay_tc_body<true, false>(ta);
+    } else {
+        if (s.out_f32) decay_tc_body<false, true>(ta);
+        else decay_tc_body<false, false>(ta);
+    }
+}
+
 // ------------------------------------------------------------------ host side
-// [tokens, heads, 128] tensor of `elem`-byte values, token rows `stride` elements apart; box of 128 tokens x
-// 1 head x 64 values, 128-byte swizzle.
+// [tokens, heads, 128] bf16 (or float) tensor, token rows `stride` elements apart; box of 128 tokens x 1 head x
+// 128 bytes, 128-byte swizzle.
 cudaError_t make_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const void* base, long long tokens,
-                     int heads, long long stride) {
+                     int heads, long long stride, bool f32 = false) {
+    const unsigned bytes = f32 ? 4 : 2;
     const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)heads, (cuuint64_t)tokens};
-    const cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[3] = {64, 1, kC};
+    const cuuint64_t strides[2] = {(cuuint64_t)kD * bytes, (cuuint64_t)stride * bytes};
+    const cuuint32_t box[3] = {128 / bytes, 1, kC};
     const cuuint32_t elem[3] = {1, 1, 1};
-    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, elem,
+    const CUresult r = encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, elem,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -540,7 +595,7 @@ cudaError_t launch_decay_scan_tc(const DecayArgs& a) {
         if ((e = make_map(encode, &m.q, s.q, a.tokens, a.Hv / s.q_div, s.q_stride)) != cudaSuccess) return e;
         if ((e = make_map(encode, &m.k, s.k, a.tokens, a.Hv / s.k_div, s.k_stride)) != cudaSuccess) return e;
         if ((e = make_map(encode, &m.v, s.v, a.tokens, a.Hv / s.v_div, s.v_stride)) != cudaSuccess) return e;
-        if (!s.out_f32 && (e = make_map(encode, &m.out, s.out, a.tokens, a.Hv, s.out_stride)) != cudaSuccess) return e;
+        if ((e = make_map(encode, &m.out, s.out, a.tokens, a.Hv, s.out_stride, s.out_f32)) != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)((long long)a.nseq * a.Hv * 2), (unsigned)a.num_scans);
     decay_tc_kernel<<<grid, kThreads, kSmem, a.stream>>>(t);
