@@ -16,7 +16,7 @@
 // exactly, K is exact, so the states that leave the kernel have fp32 accuracy; P and the state's copy in QS are
 // rounded to bf16, each 2^-9 of terms whose sum is rounded to bf16 anyway.
 //
-// Warps: 0-7 form P and write the outputs; 8-11 scale and split V; 12-15 keep the state; 16 issues the MMAs, 17
+// Warps: 0-7 form P; 8-15 scale and split V and write the outputs; 16-19 keep the state; 20 issues the MMAs, 21
 // the copies.  Hand-overs are mbarriers; every wait is bounded.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -40,15 +40,14 @@ constexpr int kParts = 3;     // bf16 parts of the scaled V
 // Shared memory (bytes from the 1024-aligned base).  Panels: 128 rows x 64 bf16, 128-byte swizzle.
 constexpr uint32_t kPanel = 16384;
 constexpr uint32_t S_Q = 0;                          // 2 stages x 2 panels
-constexpr uint32_t S_K = S_Q + 2 * 2 * kPanel;       // 2 stages x 2 panels; then the chunk's outputs
+constexpr uint32_t S_K = S_Q + 2 * 2 * kPanel;       // 2 stages x 2 panels
 constexpr uint32_t S_V = S_K + 2 * 2 * kPanel;       // 2 stages x 1 panel
 constexpr uint32_t S_VP = S_V + 2 * kPanel;          // the three parts of the scaled V
-constexpr uint32_t S_SB = S_VP + kParts * kPanel;    // the state in bf16: 128 dk rows
+constexpr uint32_t S_SB = S_VP + kParts * kPanel;    // the state in bf16 (128 dk rows); between its uses, the outputs
 constexpr uint32_t S_BAR = S_SB + kPanel;
 constexpr uint32_t kBarBytes = 256;
 constexpr uint32_t S_PW = S_BAR + kBarBytes;         // w_0 .. w_128
-constexpr uint32_t S_PR = S_PW + 132 * 4;            // w_15 .. w_0
-constexpr uint32_t kSmem = S_PR + 16 * 4 + 1024;
+constexpr uint32_t kSmem = S_PW + 132 * 4 + 1024;
 
 enum Bar : uint32_t {
     B_FULLQK = 0,   // 2: q and k tiles of a stage have landed
@@ -64,46 +63,84 @@ enum Bar : uint32_t {
     B_O = 13,       // QS and PV are complete
     B_OFREE = 14,   // QS and PV have been read
     B_FREE = 15,    // 2: every product of the chunk in a stage is complete
-    B_OST = 17,     // 2: the outputs are staged in (or stored past) a stage's k tile
-    B_GAMMA = 19,   // w_n in two floats
-    B_DRAIN = 20,
-    B_COUNT = 21
+    B_SBFREE = 17,  // the outputs have left the place of the state's copy
+    B_GAMMA = 18,   // w_n in two floats
+    B_DRAIN = 19,
+    B_COUNT = 20
 };
 
 // TMEM columns (all 512): KV holds the products with V's three parts side by side.
 constexpr uint32_t T_QK = 0, T_P = 128, T_QS = 192, T_PV = 256, T_KV = 320;
 constexpr uint32_t kTmemCols = 512;
 
-// 20 warps, five groups of four.  Registers a thread: 96 at launch; the group of the issuing warps gives up 32 and
-// the state's takes them (64 hold its part of the state): 3 x 96 + 128 + 64 = 5 x 96.
-constexpr int kThreads = 20 * 32;
-constexpr int kRegsIssue = 64, kRegsState = 128;
+// 24 warps, six groups of four.  Registers a thread: 80 at launch; P's and V's groups give up 8 and the issuing
+// warps' 16, and the state's takes them (64 hold its part of the state): 4 x 72 + 128 + 64 = 6 x 80.
+constexpr int kThreads = 24 * 32;
+constexpr int kRegsWork = 72, kRegsIssue = 64, kRegsState = 128;
+constexpr int kWarpV = 8, kWarpState = 16, kWarpMma = 20, kWarpCopy = 21;
+constexpr float kStrong = -5.f;   // log decays below this are not factored over 16 columns
 
 struct Maps {
-    CUtensorMap q, k, v, out;
+    CUtensorMap q, k, v;
 };
 struct TcArgs {
     Maps maps[kMaxScans];
     DecayArgs a;
 };
 
-// x = h + m + l, three bf16 values whose sum is x to 2^-26 (each difference is exact in fp32).
-__device__ __forceinline__ void split3(float x0, float x1, uint32_t& h, uint32_t& m, uint32_t& l) {
-    h = pack_bf16(x0, x1);
-    x0 -= __uint_as_float(h << 16);
-    x1 -= __uint_as_float(h & 0xffff0000u);
-    m = pack_bf16(x0, x1);
-    x0 -= __uint_as_float(m << 16);
-    x1 -= __uint_as_float(m & 0xffff0000u);
-    l = pack_bf16(x0, x1);
+__device__ __forceinline__ void named_barrier_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// mbar_wait_bounded in fewer instructions: the five roles' loops share one instruction cache.
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t&>(d)) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t&>(d)) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(reinterpret_cast<uint64_t&>(d)) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 as_float2(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ uint32_t pack_bf16(float2 x) { return tc::pack_bf16(x.x, x.y); }
+// x = h + m + l, three bf16 values that hold it exactly: each is x, or what is left of it, cut to eight
+// significant bits, and the differences are exact in fp32.  h gets the pair's two high halves packed.
+__device__ __forceinline__ void split3(float2 x, uint32_t& h, uint32_t& m, uint32_t& l) {
+    constexpr uint32_t kCut = 0xffff0000u, kSign = 0x80000000u;
+    uint32_t a = __float_as_uint(x.x), b = __float_as_uint(x.y);
+    h = __byte_perm(a, b, 0x7632);
+    x = add2(x, make_float2(__uint_as_float((a & kCut) ^ kSign), __uint_as_float((b & kCut) ^ kSign)));
+    a = __float_as_uint(x.x), b = __float_as_uint(x.y);
+    m = __byte_perm(a, b, 0x7632);
+    x = add2(x, make_float2(__uint_as_float((a & kCut) ^ kSign), __uint_as_float((b & kCut) ^ kSign)));
+    l = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+
+// mbar_wait_bounded in fewer instructions, and with each test suspended for up to a millisecond: the roles' loops
+// share the schedulers and one instruction cache, and a polling warp takes both from the others.
+__device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* status) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (try_wait_long(bar, parity)) return true;
     const unsigned long long t0 = globaltimer();
     while (!*abort) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (try_wait_long(bar, parity)) return true;
         if (globaltimer() - t0 > kWaitLimitNs) {
             *abort = 1;
             atomicOr(status, kStatusTimeout);
@@ -124,7 +161,6 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S_BAR + 8 * B_COUNT + 4);
     float* gamma = reinterpret_cast<float*>(sm + S_BAR + 8 * B_COUNT + 8);   // w_128, w_n of the last chunk: hi, lo each
     float* pw = reinterpret_cast<float*>(sm + S_PW);
-    float* pr = reinterpret_cast<float*>(sm + S_PR);
 
     const DecayArgs& a = ta.a;
     const DecayScan& s = a.scan[blockIdx.y];
@@ -140,25 +176,20 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
     const int tail = (int)(t1 - t0) - (nch - 1) * kC;   // valid tokens of the last chunk
     const float g = fmaxf(a.log_decay[h], kMinLogDecay);
 
-    if (warp == 16) {
+    if (warp == kWarpMma) {
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tc_fence_before();
     }
     if (tid == 0) {
         *abort_flag = 0;
         for (uint32_t b = 0; b < B_COUNT; ++b) {
-            const uint32_t count = b == B_QKFREE || b == B_P || b == B_OFREE || b == B_OST || b == B_OST + 1 ? 8
-                                   : b == B_KVFREE || b == B_S ? 4
-                                   : b == B_VP || b == B_VP + 1 ? 2 : 1;
+            const uint32_t count = b == B_QKFREE || b == B_P || b == B_OFREE || b == B_SBFREE ? 8
+                                   : b == B_KVFREE || b == B_S || b == B_VP || b == B_VP + 1 ? 4 : 1;
             mbar_init(bar(b), count);
         }
         mbar_fence_init();
     }
-    if (tid <= kC) {
-        const float w = expf(g * (float)tid);
-        pw[tid] = w;
-        if (tid < 16) pr[15 - tid] = w;
-    }
+    if (tid <= kC) pw[tid] = expf(g * (float)tid);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
@@ -175,26 +206,23 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
     auto chunk_of = [&](int it) { return rev ? nch - 1 - it : it; };
     auto valid_of = [&](int it) { return chunk_of(it) == nch - 1 ? tail : kC; };
 
-    if (warp >= 16) regs_dec<kRegsIssue>();
-    if (warp >= 18) {
-        // only there to make the group of four whole
-    } else if (warp == 17) {
+    if (warp > kWarpCopy) {
+        regs_dec<kRegsIssue>();   // only there to make the group of four whole
+    } else if (warp == kWarpCopy) {
+        regs_dec<kRegsIssue>();
         // ------------------------------------------------------------ copies
         if (lane == 0 && nch > 0) {
             const int hq = h / s.q_div, hk = h / s.k_div, hv = h / s.v_div;
-            auto load_qv = [&](int it) {   // arms the barriers of the chunk's three tiles
+            auto load = [&](int it) {
                 const int st = it & 1, t = (int)t0 + chunk_of(it) * kC;
                 const uint32_t bv = bar(B_FULLV + st), bqk = bar(B_FULLQK + st);
                 mbar_arrive_expect_tx(bv, kPanel);
                 tma_load_3d(sb + S_V + st * kPanel, &maps.v, 64 * z, hv, t, bv);
                 mbar_arrive_expect_tx(bqk, 4 * kPanel);
                 tma_load_3d(sb + S_Q + 2 * st * kPanel, &maps.q, 0, hq, t, bqk);
+                tma_load_3d(sb + S_K + 2 * st * kPanel, &maps.k, 0, hk, t, bqk);
                 tma_load_3d(sb + S_Q + (2 * st + 1) * kPanel, &maps.q, 64, hq, t, bqk);
-            };
-            auto load_k = [&](int it) {
-                const int st = it & 1, t = (int)t0 + chunk_of(it) * kC;
-                tma_load_3d(sb + S_K + 2 * st * kPanel, &maps.k, 0, hk, t, bar(B_FULLQK + st));
-                tma_load_3d(sb + S_K + (2 * st + 1) * kPanel, &maps.k, 64, hk, t, bar(B_FULLQK + st));
+                tma_load_3d(sb + S_K + (2 * st + 1) * kPanel, &maps.k, 64, hk, t, bqk);
             };
             auto prefetch = [&](int it) {   // into L2: the loads wait for a stage to be free and then cannot wait for DRAM
                 if (it >= nch) return;
@@ -204,10 +232,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                 tma_prefetch_3d(&maps.k, 64 * z, hk, t);
             };
             int loaded = 0;
-            for (; loaded < 2 && loaded < nch; ++loaded) {
-                load_qv(loaded);
-                load_k(loaded);
-            }
+            for (; loaded < 2 && loaded < nch; ++loaded) load(loaded);
             prefetch(2);
             prefetch(3);
 #pragma unroll 1
@@ -217,31 +242,11 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                 gamma[2 * x + 1] = (float)(w - (double)(float)w);
             }
             mbar_arrive(bar(B_GAMMA));
-            for (int it = 0; it < nch; ++it) {
-                const int st = it & 1, t = (int)t0 + chunk_of(it) * kC;
-                if (!wait(B_FREE + st, it >> 1)) break;
-                // chunk it + 2 into this stage, its k after the outputs that are staged there.  From here on the
-                // round goes through, so that a barrier that is armed gets all its bytes.
-                if (it + 2 < nch) load_qv(it + 2);
-                prefetch(it + 4);
-                const bool staged = wait(B_OST + st, it >> 1);
-                if (staged && valid_of(it) == kC) {
-                    if (F32) {
-                        tma_store_3d(&maps.out, 64 * z, h, t, sb + S_K + 2 * st * kPanel);
-                        tma_store_3d(&maps.out, 64 * z + 32, h, t, sb + S_K + (2 * st + 1) * kPanel);
-                    } else {
-                        tma_store_3d(&maps.out, 64 * z, h, t, sb + S_K + 2 * st * kPanel);
-                    }
-                    bulk_commit();
-                    bulk_wait_read();
-                }
-                if (it + 2 < nch) {
-                    load_k(it + 2);
-                    ++loaded;
-                }
-                if (!staged) break;
+            for (; loaded < nch; ++loaded) {   // into the stage of the chunk two back
+                if (!wait(B_FREE + (loaded & 1), (loaded >> 1) - 1)) break;
+                load(loaded);
+                prefetch(loaded + 2);
             }
-            bulk_wait_all();
             if (*abort_flag) {   // a wait gave up: no copy may still be landing when the shared memory is released
                 for (int it = max(0, loaded - 2); it < loaded; ++it) {
                     mbar_wait_drain(bar(B_FULLQK + (it & 1)), (it >> 1) & 1, kWaitLimitNs);
@@ -250,7 +255,8 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
             }
         }
         __syncwarp();
-    } else if (warp == 16) {
+    } else if (warp == kWarpMma) {
+        regs_dec<kRegsIssue>();
         // ------------------------------------------------------------ products
         // The whole warp runs the loop and one elected lane issues: always the same one, so that a commit
         // covers every product before it.
@@ -266,7 +272,6 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                 if (!__all_sync(~0u, ok)) break;
                 tc_fence_after();
                 const uint64_t kt = dKt + ((st * 2 * kPanel) >> 4);
-                const uint64_t q = dQ + ((st * 2 * kPanel) >> 4), v = dV + ((st * kPanel) >> 4);
                 // half the rows at a time, so that the first half's parts are replaced while the second runs
                 if (elect_one()) {
 #pragma unroll
@@ -287,30 +292,8 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                     mma_commit(bar(B_KV));
                 }
                 __syncwarp();
-                ok = wait(B_S, it) && (it < 1 || wait(B_OFREE, it - 1));
-                if (!__all_sync(~0u, ok)) break;
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_bf16(tmem + T_QS, q + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4), dSB + ((ks * 2048) >> 4),
-                                 idesc_bf16(128, 64, 0, 1), ks > 0);
-                }
-                __syncwarp();
-                ok = wait(B_P, it);
-                if (!__all_sync(~0u, ok)) break;
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_bf16_ta(tmem + T_PV, tmem + T_P + 8 * ks, v + ((ks * 2048) >> 4), idesc_bf16(128, 64, 0, 1),
-                                    ks > 0);
-                    mma_commit(bar(B_O));
-                    mma_commit(bar(B_FREE + st));
-                }
-                __syncwarp();
             }
-            // the next chunk's scores: P is formed from them while the next KV and QS run
+            // the next chunk's scores: P is formed from them while this chunk's outputs and the next KV and QS run
             if (it + 1 < nch) {
                 ok = wait(B_FULLQK + ((it + 1) & 1), (it + 1) >> 1) && (it < 0 || wait(B_QKFREE, it));
                 if (!__all_sync(~0u, ok)) break;
@@ -326,6 +309,32 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                 }
                 __syncwarp();
             }
+            if (it >= 0) {
+                const uint64_t q = dQ + ((st * 2 * kPanel) >> 4);
+                ok = wait(B_S, it) && (it < 1 || wait(B_OFREE, it - 1));
+                if (!__all_sync(~0u, ok)) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_bf16(tmem + T_QS, q + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4), dSB + ((ks * 2048) >> 4),
+                                 idesc_bf16(128, 64, 0, 1), ks > 0);
+                }
+                __syncwarp();
+                ok = wait(B_P, it);
+                if (!__all_sync(~0u, ok)) break;
+                tc_fence_after();
+                const uint64_t v = dV + ((st * kPanel) >> 4);
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_bf16_ta(tmem + T_PV, tmem + T_P + 8 * ks, v + ((ks * 2048) >> 4), idesc_bf16(128, 64, 0, 1),
+                                    ks > 0);
+                    mma_commit(bar(B_O));
+                    mma_commit(bar(B_FREE + st));
+                }
+                __syncwarp();
+            }
         }
         if (*abort_flag) {   // every product issued is complete before TMEM and shared memory are released
             if (elect_one()) mma_commit(bar(B_DRAIN));
@@ -333,59 +342,19 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
             mbar_wait_drain(bar(B_DRAIN), 0, kWaitLimitNs);
         }
         __syncwarp();
-    } else if (warp < 8) {
-        // ------------------------------------------------------------ P and the outputs: rows 32 (warp % 4) ..,
-        // half warp / 4 of the columns.  A chunk's outputs come while the next chunk's scores are formed.
-        const int quarter = warp & 3, half = warp >> 2, r = 32 * quarter + lane;
-        const float f = s.so * s.su;
-        for (int it = -1; it < nch; ++it) {
-            if (it >= 0) {
-                const int st = it & 1, n = valid_of(it);
-                if (!wait(B_O, it)) break;
-                tc_fence_after();
-                const float w = s.so * pw[rev ? max(n - 1 - r, 0) : r + 1];
-                const size_t row = (size_t)(t0 + (long long)chunk_of(it) * kC + r) * s.out_stride + (size_t)h * kD + kHalf * z;
-#pragma unroll 1
-                for (int b = 2 * half; b < 2 * half + 2; ++b) {
-                    uint32_t qs[16], pv[16];
-                    tmem_ld16(tl + T_QS + 16 * b, qs);
-                    tmem_ld16(tl + T_PV + 16 * b, pv);
-                    tmem_wait_ld();
-                    if (b & 1) {
-                        tc_fence_before();
-                        arrive(B_OFREE);
-                    }
-                    float o[16];
+    } else if (warp < kWarpV) {
+        regs_dec<kRegsWork>();
+        // ------------------------------------------------------------ P: rows 32 (warp % 4) .., half warp / 4 of the columns
+        const int half = warp >> 2, r0 = 32 * (warp & 3), r = r0 + lane;
+        const float f = s.so * s.su, g2 = g * 1.44269504f;
+        float2 wj[8];   // 1 / w_0 .. 1 / w_15 (backwards in a reverse scan)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = fmaf(w, __uint_as_float(qs[e]), __uint_as_float(pv[e]));
-                    if (F32) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const float4 y = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-                            if (n == kC)
-                                *reinterpret_cast<float4*>(sm + S_K + (2 * st + half) * kPanel + swz(r, 4 * (b & 1) + c)) = y;
-                            else if (r < n)
-                                *reinterpret_cast<float4*>(static_cast<float*>(s.out) + row + 16 * b + 4 * c) = y;
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const uint4 y =
-                                make_uint4(pack_bf16(o[8 * c], o[8 * c + 1]), pack_bf16(o[8 * c + 2], o[8 * c + 3]),
-                                           pack_bf16(o[8 * c + 4], o[8 * c + 5]), pack_bf16(o[8 * c + 6], o[8 * c + 7]));
-                            if (n == kC) *reinterpret_cast<uint4*>(sm + S_K + 2 * st * kPanel + swz(r, 2 * b + c)) = y;
-                            else if (r < n) *reinterpret_cast<uint4*>(static_cast<bf16*>(s.out) + row + 16 * b + 8 * c) = y;
-                        }
-                    }
-                }
-                fence_proxy_async_smem();
-                arrive(B_OST + st);
-            }
-            if (it + 1 >= nch) break;
-            const int n = valid_of(it + 1);
-            if (!wait(B_QK, it + 1)) break;
+        for (int e = 0; e < 8; ++e)
+            wj[e] = make_float2(exp2f(-g2 * (float)(rev ? 15 - 2 * e : 2 * e)), exp2f(-g2 * (float)(rev ? 14 - 2 * e : 2 * e + 1)));
+        for (int it = 0; it < nch; ++it) {
+            const int n = valid_of(it);
+            if (!wait(B_QK, it)) break;
             tc_fence_after();
-            // the previous chunk's PV has read P: its outputs have been read above
 #pragma unroll 1
             for (int b = 0; b < 4; ++b) {   // 16 columns at a time
                 const int j0 = 64 * half + 16 * b;
@@ -396,33 +365,40 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                     tc_fence_before();
                     arrive(B_QKFREE);
                 }
-                // from the warp's nearest row, columns on the diagonal's masked side (> 0) and on its open one
-                const int r0 = 32 * quarter, masked = rev ? r0 - (j0 + 15) : j0 - (r0 + 31);
-                const int open = rev ? j0 - (r0 + 31) : r0 - (j0 + 15);
-                if (masked > 0) {
+                // how many of the 16 columns row r sees: the first ones (forward) or the last ones (reverse), of
+                // those before the sequence's end
+                const int seen = rev ? j0 + 16 - r : r - j0 + 1;
+                const int last = rev ? n - j0 : 16;
+                if (rev ? r0 > j0 + 15 : r0 + 31 < j0) {   // none, for the whole warp
 #pragma unroll
                     for (int e = 0; e < 8; ++e) p[e] = 0u;
-                } else if (open < 0 || (rev && n < kC)) {   // masked element by element
+                } else {
+                    if (g >= kStrong) {   // w_|r - j| = w_(seen - 1) / w_(distance of j from the block's far end)
+                        const float fr = f * exp2f(g2 * (float)max(seen - 1, 0));
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float y[2];
+                        for (int e = 0; e < 8; ++e)
+                            p[e] = pack_bf16(mul2(mul2(make_float2(fr, fr), wj[e]), as_float2(x[2 * e], x[2 * e + 1])));
+                    } else {              // strong decays, element by element
 #pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int j = j0 + 2 * e + u, d = rev ? j - r : r - j;
-                            y[u] = d >= 0 && j < n ? f * pw[max(d, 0)] * __uint_as_float(x[2 * e + u]) : 0.f;
+                        for (int e = 0; e < 8; ++e) {
+                            const int d0 = rev ? j0 + 2 * e - r : r - j0 - 2 * e, d1 = rev ? d0 + 1 : d0 - 1;
+                            p[e] = pack_bf16(make_float2(f * pw[max(d0, 0)] * __uint_as_float(x[2 * e]),
+                                                         f * pw[max(d1, 0)] * __uint_as_float(x[2 * e + 1])));
                         }
-                        p[e] = pack_bf16(y[0], y[1]);
                     }
-                } else {   // w_|r - j| = w_|r - near| w_|near - j|, near the column closest to the diagonal
-                    const float fr = f * pw[rev ? j0 - r : r - (j0 + 15)];
-                    const float4* wj = reinterpret_cast<const float4*>(rev ? pw : pr);
+                    // masked columns become zeros whatever they hold: on the diagonal, and past the end in reverse
+                    if (rev ? r0 + 31 > j0 || n < kC : r0 < j0 + 15) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float4 w = wj[e];
-                        p[2 * e] = pack_bf16(fr * w.x * __uint_as_float(x[4 * e]), fr * w.y * __uint_as_float(x[4 * e + 1]));
-                        p[2 * e + 1] =
-                            pack_bf16(fr * w.z * __uint_as_float(x[4 * e + 2]), fr * w.w * __uint_as_float(x[4 * e + 3]));
+                        for (int e = 0; e < 8; ++e) {
+                            const bool lo = rev ? 16 - 2 * e <= seen && 2 * e < last : 2 * e < seen;
+                            const bool hi = rev ? 15 - 2 * e <= seen && 2 * e + 1 < last : 2 * e + 1 < seen;
+                            p[e] &= (lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u);
+                        }
                     }
+                }
+                if (b == 0) {   // the previous chunk's PV has read P
+                    if (it > 0) wait(B_O, it - 1);
+                    tc_fence_after();
                 }
                 tmem_st8(tl + T_P + j0 / 2, p);
             }
@@ -430,65 +406,125 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
             tc_fence_before();
             arrive(B_P);
         }
-    } else if (warp < 12) {
-        // ------------------------------------------------------------ V's parts: one row a thread
-        const int r = tid - 256, half = (warp >> 1) & 1;
-        for (int it = 0; it < nch; ++it) {
+    } else if (warp < kWarpState) {
+        regs_dec<kRegsWork>();
+        // ------------------------------------------------------------ V's parts and the outputs: half a row a thread
+        const int r = 32 * (warp & 3) + lane, half = (warp >> 1) & 1, c0 = 4 * ((warp - kWarpV) >> 2);
+        auto split = [&](int it) {
             const int st = it & 1, n = valid_of(it);
-            if (!wait(B_FULLV + st, it >> 1)) break;
+            if (!wait(B_FULLV + st, it >> 1)) return false;
             if (n < kC) {   // the rows past the sequence's end are zero wherever they are summed over
-                if (!wait(B_FULLQK + st, it >> 1)) break;
+                if (!wait(B_FULLQK + st, it >> 1)) return false;
                 if (r >= n) {
 #pragma unroll 1
-                    for (int c = 0; c < 24; ++c) {   // v's panel and k's two
-                        const uint32_t panel = c < 8 ? S_V + st * kPanel : S_K + (2 * st + (c >> 3) - 1) * kPanel;
-                        *reinterpret_cast<uint4*>(sm + panel + swz(r, c & 7)) = make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < 12; ++c) {   // in v's panel and k's two
+                        const uint32_t panel = c < 4 ? S_V + st * kPanel : S_K + (2 * st + (c >> 2) - 1) * kPanel;
+                        *reinterpret_cast<uint4*>(sm + panel + swz(r, c0 + (c & 3))) = make_uint4(0, 0, 0, 0);
                     }
                 }
             }
             const float w = r < n ? s.su * pw[rev ? r + 1 : n - 1 - r] : 0.f;
+            uint4 v[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(sm + S_V + st * kPanel + swz(r, c0 + c));
             // the products of the previous chunk that read these rows' parts are complete
-            if (it > 0 && !wait(half ? B_KV : B_KVHALF, it - 1)) break;
-#pragma unroll 2
-            for (int c = 0; c < 8; ++c) {
-                const uint4 v = *reinterpret_cast<const uint4*>(sm + S_V + st * kPanel + swz(r, c));
-                const uint32_t y[4] = {v.x, v.y, v.z, v.w};
+            if (it > 0 && !wait(half ? B_KV : B_KVHALF, it - 1)) return false;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t y[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
                 uint32_t o[kParts][4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    split3(w * __uint_as_float(y[e] << 16), w * __uint_as_float(y[e] & 0xffff0000u), o[0][e], o[1][e], o[2][e]);
+                    split3(mul2(make_float2(w, w), make_float2(__uint_as_float(y[e] << 16), __uint_as_float(y[e] & 0xffff0000u))),
+                           o[0][e], o[1][e], o[2][e]);
 #pragma unroll
                 for (int p = 0; p < kParts; ++p)
-                    *reinterpret_cast<uint4*>(sm + S_VP + p * kPanel + swz(r, c)) = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
+                    *reinterpret_cast<uint4*>(sm + S_VP + p * kPanel + swz(r, c0 + c)) = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
             }
             fence_proxy_async_smem();
             arrive(B_VP + half);
+            return true;
+        };
+        // A chunk's outputs (rows of 128 bytes at a time) pass through the place of the state's copy, which QS has
+        // read: warps w and w + 4 hold the two halves of the same 32 rows, and each writes 16 whole rows.
+        constexpr int esize = F32 ? 4 : 2;
+        const int pair = 1 + (warp & 3), own = 32 * (warp & 3) + 4 * c0 + (lane >> 3), chunk = lane & 7;
+        uint8_t* const out = static_cast<uint8_t*>(s.out) + ((size_t)h * kD + kHalf * z) * esize +
+                             (F32 ? (chunk >> 2) * 128 + (chunk & 3) * 16 : chunk * 16);
+        const size_t pitch = (size_t)s.out_stride * esize;
+        for (int it = -1; it < nch; ++it) {
+            if (it + 1 < nch && !split(it + 1)) break;
+            if (it < 0) continue;
+            const int n = valid_of(it);
+            if (!wait(B_O, it)) break;
+            tc_fence_after();
+            const float w = s.so * pw[rev ? max(n - 1 - r, 0) : r + 1];
+            uint8_t* const first = out + (size_t)(t0 + (long long)chunk_of(it) * kC) * pitch;
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                uint32_t qs[16], pv[16];
+                tmem_ld16(tl + T_QS + 8 * c0 + 16 * b, qs);
+                tmem_ld16(tl + T_PV + 8 * c0 + 16 * b, pv);
+                tmem_wait_ld();
+                if (b) {
+                    tc_fence_before();
+                    arrive(B_OFREE);
+                }
+                float2 o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    o[e] = fma2(make_float2(w, w), as_float2(qs[2 * e], qs[2 * e + 1]), as_float2(pv[2 * e], pv[2 * e + 1]));
+                if (F32) {
+                    if (b) named_barrier_sync(pair, 64);   // the first 16 columns' rows have been read
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<float4*>(sm + S_SB + swz(r, c0 + c)) =
+                            make_float4(o[2 * c].x, o[2 * c].y, o[2 * c + 1].x, o[2 * c + 1].y);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        *reinterpret_cast<uint4*>(sm + S_SB + swz(r, c0 + 2 * b + c)) =
+                            make_uint4(pack_bf16(o[4 * c]), pack_bf16(o[4 * c + 1]), pack_bf16(o[4 * c + 2]), pack_bf16(o[4 * c + 3]));
+                }
+                if (F32 || b) {
+                    named_barrier_sync(pair, 64);
+#pragma unroll
+                    for (int x = 0; x < 16; x += 4)
+                        if (own + x < n)
+                            *reinterpret_cast<uint4*>(first + (size_t)(own + x) * pitch + (F32 ? 64 * b : 0)) =
+                                *reinterpret_cast<const uint4*>(sm + S_SB + swz(own + x, chunk));
+                }
+            }
+            arrive(B_SBFREE);
         }
     } else {
         // ------------------------------------------------------------ the state: row R of dk, 64 columns a thread
         regs_inc<kRegsState>();
-        const int R = tid - 384;
+        const int R = tid - 32 * kWarpState;
         const size_t base = ((size_t)i * a.Hv + h) * kD * kD;
-        float S[64];
+        float2 S[32];
         if (s.init && s.init_t) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e) S[e] = s.init[base + (size_t)(kHalf * z + e) * kD + R];
+            for (int e = 0; e < 32; ++e) {
+                const float* x = s.init + base + (size_t)(kHalf * z + 2 * e) * kD + R;
+                S[e] = make_float2(x[0], x[kD]);
+            }
         } else if (s.init) {
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(s.init + base + (size_t)R * kD + kHalf * z + e);
-                S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
+            for (int e = 0; e < 32; e += 2) {
+                const float4 x = *reinterpret_cast<const float4*>(s.init + base + (size_t)R * kD + kHalf * z + 2 * e);
+                S[e] = make_float2(x.x, x.y);
+                S[e + 1] = make_float2(x.z, x.w);
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < 64; ++e) S[e] = 0.f;
+            for (int e = 0; e < 32; ++e) S[e] = make_float2(0.f, 0.f);
         }
         auto write_sb = [&] {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
                 *reinterpret_cast<uint4*>(sm + S_SB + swz(R, c)) =
-                    make_uint4(pack_bf16(S[8 * c], S[8 * c + 1]), pack_bf16(S[8 * c + 2], S[8 * c + 3]),
-                               pack_bf16(S[8 * c + 4], S[8 * c + 5]), pack_bf16(S[8 * c + 6], S[8 * c + 7]));
+                    make_uint4(pack_bf16(S[4 * c]), pack_bf16(S[4 * c + 1]), pack_bf16(S[4 * c + 2]), pack_bf16(S[4 * c + 3]));
             fence_proxy_async_smem();
             arrive(B_S);
         };
@@ -499,7 +535,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
         }
         for (int it = 0; ok && it < nch; ++it) {
             const int x = valid_of(it) == kC ? 0 : 2;
-            const float ghi = gamma[x], glo = gamma[x + 1];
+            const float2 ghi = make_float2(gamma[x], gamma[x]), glo = make_float2(gamma[x + 1], gamma[x + 1]);
             if (it + 1 == nch && !s.final) break;   // nobody needs the last state
             if (!(ok = wait(B_KV, it))) break;
             tc_fence_after();
@@ -510,28 +546,30 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                 for (int p = 0; p < kParts; ++p) tmem_ld16(tl + T_KV + 64 * p + 16 * b, d[p]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float y = (__uint_as_float(d[2][e]) + __uint_as_float(d[1][e])) + __uint_as_float(d[0][e]);
-                    S[16 * b + e] = fmaf(ghi, S[16 * b + e], fmaf(glo, S[16 * b + e], y));
+                for (int e = 0; e < 8; ++e) {
+                    float2 y = add2(as_float2(d[2][2 * e], d[2][2 * e + 1]), as_float2(d[1][2 * e], d[1][2 * e + 1]));
+                    y = add2(y, as_float2(d[0][2 * e], d[0][2 * e + 1]));
+                    S[8 * b + e] = fma2(ghi, S[8 * b + e], fma2(glo, S[8 * b + e], y));
                 }
             }
             tc_fence_before();
             arrive(B_KVFREE);
             if (it + 1 < nch) {
-                if (!(ok = wait(B_O, it))) break;   // QS has read the copy of the state
+                // QS has read the copy of the state, and the outputs have passed through its place
+                if (!(ok = wait(B_SBFREE, it))) break;
                 write_sb();
             }
         }
         if (s.final && ok) {
 #pragma unroll
-            for (int e = 0; e < 64; e += 4)
-                *reinterpret_cast<float4*>(s.final + base + (size_t)R * kD + kHalf * z + e) =
-                    make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+            for (int e = 0; e < 32; e += 2)
+                *reinterpret_cast<float4*>(s.final + base + (size_t)R * kD + kHalf * z + 2 * e) =
+                    make_float4(S[e].x, S[e].y, S[e + 1].x, S[e + 1].y);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 16) {
+    if (warp == kWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
@@ -550,16 +588,15 @@ decay_tc_kernel(const __grid_constant__ TcArgs ta) {
 }
 
 // ------------------------------------------------------------------ host side
-// [tokens, heads, 128] bf16 (or float) tensor, token rows `stride` elements apart; box of 128 tokens x 1 head x
-// 128 bytes, 128-byte swizzle.
+// [tokens, heads, 128] bf16 tensor, token rows `stride` elements apart; box of 128 tokens x 1 head x 64 values,
+// 128-byte swizzle.
 cudaError_t make_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const void* base, long long tokens,
-                     int heads, long long stride, bool f32 = false) {
-    const unsigned bytes = f32 ? 4 : 2;
+                     int heads, long long stride) {
     const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)heads, (cuuint64_t)tokens};
-    const cuuint64_t strides[2] = {(cuuint64_t)kD * bytes, (cuuint64_t)stride * bytes};
-    const cuuint32_t box[3] = {128 / bytes, 1, kC};
+    const cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 1, kC};
     const cuuint32_t elem[3] = {1, 1, 1};
-    const CUresult r = encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, elem,
+    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, elem,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -595,7 +632,6 @@ cudaError_t launch_decay_scan_tc(const DecayArgs& a) {
         if ((e = make_map(encode, &m.q, s.q, a.tokens, a.Hv / s.q_div, s.q_stride)) != cudaSuccess) return e;
         if ((e = make_map(encode, &m.k, s.k, a.tokens, a.Hv / s.k_div, s.k_stride)) != cudaSuccess) return e;
         if ((e = make_map(encode, &m.v, s.v, a.tokens, a.Hv / s.v_div, s.v_stride)) != cudaSuccess) return e;
-        if ((e = make_map(encode, &m.out, s.out, a.tokens, a.Hv, s.out_stride, s.out_f32)) != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)((long long)a.nseq * a.Hv * 2), (unsigned)a.num_scans);
     decay_tc_kernel<<<grid, kThreads, kSmem, a.stream>>>(t);
