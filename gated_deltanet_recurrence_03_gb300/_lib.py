@@ -142,3 +142,14 @@ def default_opts(lib) -> GdnOpts:
     o = GdnOpts()
     lib.gdn_opts_init(ctypes.byref(o))
     return o
+
+
+_default_bytes = None
+
+
+def default_bytes(lib) -> bytes:
+    """default_opts as bytes (cached): options of a call are copied from it."""
+    global _default_bytes
+    if _default_bytes is None:
+        _default_bytes = bytes(default_opts(lib))
+    return _default_bytes

@@ -7,6 +7,7 @@ CUDA kernels; there is no other code path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional, Sequence
 
@@ -22,6 +23,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _need(name, t, dtype, device, shape):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.device != device:
@@ -37,6 +40,28 @@ def _need(name, t, dtype, device, shape):
 def _stream_handle(stream: Optional[torch.cuda.Stream], device) -> int:
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return int(s.cuda_stream)
+
+
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def _on(device):
+    """Context in which ``device`` is current; costs nothing where it already is."""
+    return _NO_SWITCH if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _call_opts(lib, dtype, scale, stream, device, events):
+    """Options of a call without flags: the library's defaults with the type, scale, stream and events."""
+    o = L.GdnOpts.from_buffer_copy(L.default_bytes(lib))
+    o.dtype = _DTYPES[dtype]
+    o.scale = scale
+    o.stream = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+    keep = None
+    if events:
+        keep = (ctypes.c_void_p * len(events))(*[int(e) for e in events])
+        o.events = ctypes.cast(keep, ctypes.POINTER(ctypes.c_void_p))
+        o.num_events = len(events)
+    return o, keep
 
 
 def _opts(lib, dtype, scale, chunk, normalize_qk, stream, device, events, raw_gates=None, Hv=None,
@@ -588,8 +613,8 @@ def gdn_decay_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
     lib = L.load()
     dev, dt, Hqk, Hv, dk, dv, strides = _decay_inputs(q, k, v, log_decay, 2)
     B, T = q.shape[:2]
-    with torch.cuda.device(dev):
-        o, keep = _opts(lib, dt, scale, 64, False, stream, dev, events)
+    with _on(dev):
+        o, keep = _call_opts(lib, dt, scale, stream, dev, events)
         nseq = _packed(o, cu_seqlens, B, dev)
         if S0 is not None:
             _need("S0", S0, torch.float32, dev, (nseq, Hv, dk, dv))
@@ -629,8 +654,8 @@ def gdn_decay_attn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_d
         out = torch.empty((N, Hv, dv), dtype=dt, device=dev)
     else:
         _need("out", out, dt, dev, (N, Hv, dv))
-    with torch.cuda.device(dev):
-        o, keep = _opts(lib, dt, scale, 64, False, stream, dev, events)
+    with _on(dev):
+        o, keep = _call_opts(lib, dt, scale, stream, dev, events)
         st = lib.gdn_decay_attn_step(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], _ptr(log_decay),
                                      _ptr(S), _ptr(slots), pool, _ptr(out), N, Hqk, Hv, dk, dv, ctypes.byref(o))
         del keep
@@ -658,8 +683,8 @@ def gdn_decay_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
         if g.shape != t.shape or g.dtype != dt or g.device != dev:
             raise ValueError(f"{name} must be {dt} of shape {tuple(t.shape)} on {dev}")
     gstrides = tuple(_token_rows(n, g, 2) for n, g in zip(("grad_q", "grad_k", "grad_v"), grads))
-    with torch.cuda.device(dev):
-        o, keep = _opts(lib, dt, scale, 64, False, stream, dev, events)
+    with _on(dev):
+        o, keep = _call_opts(lib, dt, scale, stream, dev, events)
         nseq = _packed(o, cu_seqlens, B, dev)
         for name, t in (("S0", S0), ("grad_S_final", grad_S_final)):
             if t is not None:
@@ -708,8 +733,8 @@ def gdn_block_norm_fwd(x: torch.Tensor, b: torch.Tensor, post_weight: torch.Tens
     r, n = (torch.empty_like(x), torch.empty_like(x)) if out is None else out
     _need("r", r, dt, dev, shape)
     _need("n", n, dt, dev, shape)
-    with torch.cuda.device(dev):
-        o, keep = _opts(lib, dt, 1.0, 64, False, stream, dev, events)
+    with _on(dev):
+        o, keep = _call_opts(lib, dt, 1.0, stream, dev, events)
         o.norm_eps = float(eps)
         st = lib.gdn_block_norm_fwd(_ptr(x), _ptr(b), _ptr(gate), cols, _ptr(res_scale), _ptr(post_weight),
                                     _ptr(pre_weight), _ptr(r), _ptr(n), rows, D, ctypes.byref(o))
@@ -733,8 +758,8 @@ def gdn_block_norm_bwd(x: torch.Tensor, b: torch.Tensor, post_weight: torch.Tens
     gg = None if gate is None else torch.empty_like(gate)
     sums = torch.empty((3 if res_scale is not None else 2, D), dtype=torch.float32, device=dev)
     gs = sums[2] if res_scale is not None else None
-    with torch.cuda.device(dev):
-        o, keep = _opts(lib, dt, 1.0, 64, False, stream, dev, events)
+    with _on(dev):
+        o, keep = _call_opts(lib, dt, 1.0, stream, dev, events)
         o.norm_eps = float(eps)
         ws = _scratch(o, int(lib.gdn_block_norm_bwd_workspace_size(rows, D, ctypes.byref(o))), None, dev)
         st = lib.gdn_block_norm_bwd(_ptr(x), _ptr(b), _ptr(gate), cols, _ptr(res_scale), _ptr(post_weight),

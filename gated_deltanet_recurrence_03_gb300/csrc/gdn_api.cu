@@ -864,7 +864,7 @@ gdn_status_t gdn_block_norm_fwd(const void* x, const void* b, const void* gate, 
     BlockNormArgs a{};
     a.x = x; a.b = b; a.gate = gate; a.gate_cols = gate_cols; a.res_scale = res_scale;
     a.post_w = post_weight; a.pre_w = pre_weight; a.eps = o.norm_eps; a.r = r; a.n = n;
-    a.rows = rows; a.D = D; a.dtype = o.dtype; a.stream = static_cast<cudaStream_t>(o.stream);
+    a.rows = rows; a.D = D; a.dtype = o.dtype; a.stream = static_cast<cudaStream_t>(o.stream); a.status = status;
     record(o, 0, a.stream);
     const cudaError_t e = launch_block_norm_fwd(a);
     if (e != cudaSuccess) return cuda_fail(e, "block norm launch");
@@ -904,7 +904,7 @@ gdn_status_t gdn_block_norm_bwd(const void* x, const void* b, const void* gate, 
     a.post_w = post_weight; a.pre_w = pre_weight; a.eps = o.norm_eps;
     a.gr = grad_r; a.gn = grad_n; a.gx = grad_x; a.gb = grad_b; a.ggate = grad_gate;
     a.g_post = grad_post; a.g_pre = grad_pre; a.g_scale = grad_res_scale; a.workspace = o.workspace;
-    a.rows = rows; a.D = D; a.dtype = o.dtype; a.stream = static_cast<cudaStream_t>(o.stream);
+    a.rows = rows; a.D = D; a.dtype = o.dtype; a.stream = static_cast<cudaStream_t>(o.stream); a.status = status;
     record(o, 0, a.stream);
     const cudaError_t e = launch_block_norm_bwd(a);
     if (e != cudaSuccess) return cuda_fail(e, "block norm backward launch");

@@ -249,8 +249,9 @@ struct BlockNormArgs {
     int D;
     int dtype;
     cudaStream_t stream;
+    unsigned* status;           // device status word (bounded waits)
 };
-constexpr int kBlockNormMaxD = 16384;
+constexpr int kBlockNormMaxD = 8192;
 cudaError_t launch_block_norm_fwd(const BlockNormArgs& a);
 size_t block_norm_bwd_workspace_bytes(long long rows, int D);
 cudaError_t launch_block_norm_bwd(const BlockNormArgs& a);

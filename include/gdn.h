@@ -405,7 +405,7 @@ gdn_status_t gdn_decay_attn_bwd(const void* q, long long q_stride, const void* k
  *   gate                     logits [rows, D] (gate_cols = D) or [rows] (gate_cols = 1) dtype, or NULL (no gate)
  *   res_scale                [D] float or NULL (1)
  *   post_weight, pre_weight  [D] float
- * Supported: D a multiple of 8 up to 16384, rows >= 0.  eps = opts->norm_eps; opts->flags must be 0.
+ * Supported: D a multiple of 8 up to 8192, rows >= 0.  eps = opts->norm_eps; opts->flags must be 0.
  */
 gdn_status_t gdn_block_norm_fwd(const void* x, const void* b, const void* gate, int gate_cols, const float* res_scale,
                                 const float* post_weight, const float* pre_weight, void* r, void* n, long long rows,

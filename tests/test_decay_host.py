@@ -97,7 +97,7 @@ def norm(lib, back=False, rows=4, D=64, cols=1, ptrs=None, **kw):
 
 @pytest.mark.parametrize("back", [False, True])
 @pytest.mark.parametrize("case,expect", [
-    (dict(rows=-1), BAD), (dict(rows=2 ** 31), BAD), (dict(D=0), BAD), (dict(D=60), BAD), (dict(D=16392), UNSUP),
+    (dict(rows=-1), BAD), (dict(rows=2 ** 31), BAD), (dict(D=0), BAD), (dict(D=60), BAD), (dict(D=8200), UNSUP),
     (dict(cols=2), BAD), (dict(dtype=3), BAD), (dict(flags=1), BAD), (dict(norm_eps=-1.0), BAD),
     *[(dict(ptrs=without(15, i)), BAD) for i in (0, 1, 4, 5, 6, 7)],
     *[(dict(ptrs=without(15, i, FAKE + 8)), BAD) for i in (0, 1, 3, 4, 5, 6, 7)],
@@ -125,5 +125,5 @@ def test_empty_calls_and_sizes(lib):
         assert size(1, 8, 1, 1, 48, 32, opts(lib)) == 0
     # shared query/key heads: an fp32 part of grad_q and grad_k for each value head
     assert lib.gdn_decay_attn_bwd_workspace_size(1, 100, 1, 2, 64, 64, opts(lib)) >= 2 * 100 * 2 * 64 * 4
-    assert lib.gdn_block_norm_bwd_workspace_size(10, 64, opts(lib)) >= 11 * 3 * 64 * 4
+    assert lib.gdn_block_norm_bwd_workspace_size(10, 64, opts(lib)) >= 2 * 64 * 4
     assert lib.gdn_block_norm_bwd_workspace_size(10, 60, opts(lib)) == 0
