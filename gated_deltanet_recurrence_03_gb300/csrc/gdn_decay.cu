@@ -105,10 +105,16 @@ cudaError_t launch_serial(const DecayArgs& a) {
 
 }  // namespace
 
-size_t decay_scan_workspace_bytes(int, int, int, int, int, long long, int) { return 0; }
+namespace {
+bool on_tensor_cores(int dtype, int dk, int dv) { return dtype == GDN_BF16 && dk == 128 && dv == 128; }
+}  // namespace
+
+size_t decay_scan_workspace_bytes(int dtype, int dk, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans) {
+    return on_tensor_cores(dtype, dk, dv) ? decay_scan_tc_workspace_bytes(Hv, nseq, tokens, packed, num_scans) : 0;
+}
 
 cudaError_t launch_decay_scan(const DecayArgs& a) {
-    if (a.dtype == GDN_BF16 && a.dk == 128 && a.dv == 128) return launch_decay_scan_tc(a);
+    if (on_tensor_cores(a.dtype, a.dk, a.dv)) return launch_decay_scan_tc(a);
     return a.dtype == GDN_BF16 ? launch_serial<__nv_bfloat16>(a) : launch_serial<float>(a);
 }
 

@@ -21,6 +21,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "gdn_internal.cuh"
@@ -86,7 +87,53 @@ struct Maps {
 struct TcArgs {
     Maps maps[kMaxScans];
     DecayArgs a;
+    // Segments: segment j of sequence i is slot floor(start_i / seg) + i + j (no prefix sum needed); `states` holds
+    // [scan][slot][Hv][dk][dv] floats, first a segment's own contribution to the state, then the state at its
+    // first visited end.  seg = 0: one CTA walks a whole sequence, and a slot is a sequence.
+    int seg, slots;
+    float* states;
 };
+
+// The tokens of a slot, and whether it is the first and the last one its sequence's scan visits; false for a slot
+// without a sequence's segment (an empty sequence has one segment of no tokens).
+struct Unit {
+    int seq;
+    long long t0, t1;
+    bool first, last;
+};
+__device__ __forceinline__ bool unit_of(const TcArgs& ta, int slot, bool rev, Unit& u) {
+    const DecayArgs& a = ta.a;
+    if (!ta.seg) {
+        u.seq = slot;
+        seq_range(a.cu, slot, a.T, u.t0, u.t1);
+        u.first = u.last = true;
+        return true;
+    }
+    auto base = [&](int i) {
+        long long s0, s1;
+        seq_range(a.cu, i, a.T, s0, s1);
+        return s0 / ta.seg + i;
+    };
+    int lo = 0, hi = a.nseq - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (base(mid) <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    long long s0, s1;
+    seq_range(a.cu, lo, a.T, s0, s1);
+    const long long j = slot - base(lo), n = max(1LL, (s1 - s0 + ta.seg - 1) / ta.seg);
+    if (j < 0 || j >= n) return false;
+    u.seq = lo;
+    u.t0 = s0 + j * ta.seg;
+    u.t1 = min(s1, u.t0 + ta.seg);
+    u.first = j == (rev ? n - 1 : 0);
+    u.last = j == (rev ? 0 : n - 1);
+    return true;
+}
+__device__ __forceinline__ float* unit_state(const TcArgs& ta, int scan, int slot, int h) {
+    return ta.states + (((size_t)scan * ta.slots + slot) * ta.a.Hv + h) * kD * kD;
+}
 
 __device__ __forceinline__ void named_barrier_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -149,9 +196,9 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
     return false;
 }
 
-// One scan's CTA.  REV: a reverse scan; F32: the outputs are float.  (Template arguments, not branches, for the
-// instruction cache's sake.)
-template <bool REV, bool F32>
+// One scan's CTA.  REV: a reverse scan; F32: the outputs are float; STATE: only a segment's contribution to the
+// state, from zeros, no outputs.  (Template arguments, not branches, for the instruction cache's sake.)
+template <bool REV, bool F32, bool STATE>
 __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -168,10 +215,12 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int z = blockIdx.x & 1;
     const int h = (blockIdx.x >> 1) % a.Hv;
-    const int i = (blockIdx.x >> 1) / a.Hv;
+    const int slot = (blockIdx.x >> 1) / a.Hv;
     constexpr bool rev = REV;
-    long long t0, t1;
-    seq_range(a.cu, i, a.T, t0, t1);
+    Unit unit;
+    if (!unit_of(ta, slot, rev, unit)) return;
+    if (STATE && unit.last) return;   // nothing comes after it
+    const long long t0 = unit.t0, t1 = unit.t1;
     const int nch = (int)((t1 - t0 + kC - 1) / kC);
     const int tail = (int)(t1 - t0) - (nch - 1) * kC;   // valid tokens of the last chunk
     const float g = fmaxf(a.log_decay[h], kMinLogDecay);
@@ -218,17 +267,17 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                 const uint32_t bv = bar(B_FULLV + st), bqk = bar(B_FULLQK + st);
                 mbar_arrive_expect_tx(bv, kPanel);
                 tma_load_3d(sb + S_V + st * kPanel, &maps.v, 64 * z, hv, t, bv);
-                mbar_arrive_expect_tx(bqk, 4 * kPanel);
-                tma_load_3d(sb + S_Q + 2 * st * kPanel, &maps.q, 0, hq, t, bqk);
+                mbar_arrive_expect_tx(bqk, (STATE ? 2 : 4) * kPanel);
+                if (!STATE) tma_load_3d(sb + S_Q + 2 * st * kPanel, &maps.q, 0, hq, t, bqk);
                 tma_load_3d(sb + S_K + 2 * st * kPanel, &maps.k, 0, hk, t, bqk);
-                tma_load_3d(sb + S_Q + (2 * st + 1) * kPanel, &maps.q, 64, hq, t, bqk);
+                if (!STATE) tma_load_3d(sb + S_Q + (2 * st + 1) * kPanel, &maps.q, 64, hq, t, bqk);
                 tma_load_3d(sb + S_K + (2 * st + 1) * kPanel, &maps.k, 64, hk, t, bqk);
             };
             auto prefetch = [&](int it) {   // into L2: the loads wait for a stage to be free and then cannot wait for DRAM
                 if (it >= nch) return;
                 const int t = (int)t0 + chunk_of(it) * kC;
                 tma_prefetch_3d(&maps.v, 64 * z, hv, t);
-                tma_prefetch_3d(&maps.q, 64 * z, hq, t);   // the other half of q and k: the head's other CTA
+                if (!STATE) tma_prefetch_3d(&maps.q, 64 * z, hq, t);   // the other half of q and k: the head's other CTA
                 tma_prefetch_3d(&maps.k, 64 * z, hk, t);
             };
             int loaded = 0;
@@ -290,8 +339,14 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                         mma_bf16(tmem + T_KV, kt + ((ks * 2048) >> 4), dVP + ((ks * 2048) >> 4),
                                  idesc_bf16(128, 64 * kParts, 1, 1), 1);
                     mma_commit(bar(B_KV));
+                    if (STATE) mma_commit(bar(B_FREE + st));
                 }
                 __syncwarp();
+            }
+            if (STATE) {   // the next chunk's k (with scores to form, its arrival is waited for below)
+                if (it + 1 < nch) ok = wait(B_FULLQK + ((it + 1) & 1), (it + 1) >> 1);
+                if (!__all_sync(~0u, ok)) break;
+                continue;
             }
             // the next chunk's scores: P is formed from them while this chunk's outputs and the next KV and QS run
             if (it + 1 < nch) {
@@ -336,6 +391,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                 __syncwarp();
             }
         }
+        if (nch > 0 && ok) wait(B_FREE + ((nch - 1) & 1), (nch - 1) >> 1);   // the last arrival of a commit
         if (*abort_flag) {   // every product issued is complete before TMEM and shared memory are released
             if (elect_one()) mma_commit(bar(B_DRAIN));
             __syncwarp();
@@ -351,7 +407,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             wj[e] = make_float2(exp2f(-g2 * (float)(rev ? 15 - 2 * e : 2 * e)), exp2f(-g2 * (float)(rev ? 14 - 2 * e : 2 * e + 1)));
-        for (int it = 0; it < nch; ++it) {
+        for (int it = 0; !STATE && it < nch; ++it) {
             const int n = valid_of(it);
             if (!wait(B_QK, it)) break;
             tc_fence_after();
@@ -454,7 +510,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
         const size_t pitch = (size_t)s.out_stride * esize;
         for (int it = -1; it < nch; ++it) {
             if (it + 1 < nch && !split(it + 1)) break;
-            if (it < 0) continue;
+            if (STATE || it < 0) continue;
             const int n = valid_of(it);
             if (!wait(B_O, it)) break;
             tc_fence_after();
@@ -501,18 +557,20 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
         // ------------------------------------------------------------ the state: row R of dk, 64 columns a thread
         regs_inc<kRegsState>();
         const int R = tid - 32 * kWarpState;
-        const size_t base = ((size_t)i * a.Hv + h) * kD * kD;
+        const size_t base = ((size_t)unit.seq * a.Hv + h) * kD * kD;
+        const float* const init = STATE ? nullptr : ta.seg ? unit_state(ta, blockIdx.y, slot, h) : s.init ? s.init + base : nullptr;
+        float* const final = STATE ? unit_state(ta, blockIdx.y, slot, h) : s.final && unit.last ? s.final + base : nullptr;
         float2 S[32];
-        if (s.init && s.init_t) {
+        if (init && s.init_t && !ta.seg) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-                const float* x = s.init + base + (size_t)(kHalf * z + 2 * e) * kD + R;
+                const float* x = init + (size_t)(kHalf * z + 2 * e) * kD + R;
                 S[e] = make_float2(x[0], x[kD]);
             }
-        } else if (s.init) {
+        } else if (init) {
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-                const float4 x = *reinterpret_cast<const float4*>(s.init + base + (size_t)R * kD + kHalf * z + 2 * e);
+                const float4 x = *reinterpret_cast<const float4*>(init + (size_t)R * kD + kHalf * z + 2 * e);
                 S[e] = make_float2(x.x, x.y);
                 S[e + 1] = make_float2(x.z, x.w);
             }
@@ -530,13 +588,13 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
         };
         bool ok = true;
         if (nch > 0) {
-            write_sb();
+            if (!STATE) write_sb();
             ok = wait(B_GAMMA, 0);
         }
         for (int it = 0; ok && it < nch; ++it) {
             const int x = valid_of(it) == kC ? 0 : 2;
             const float2 ghi = make_float2(gamma[x], gamma[x]), glo = make_float2(gamma[x + 1], gamma[x + 1]);
-            if (it + 1 == nch && !s.final) break;   // nobody needs the last state
+            if (it + 1 == nch && !final) break;   // nobody needs the last state
             if (!(ok = wait(B_KV, it))) break;
             tc_fence_after();
 #pragma unroll
@@ -554,16 +612,16 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
             }
             tc_fence_before();
             arrive(B_KVFREE);
-            if (it + 1 < nch) {
+            if (!STATE && it + 1 < nch) {
                 // QS has read the copy of the state, and the outputs have passed through its place
                 if (!(ok = wait(B_SBFREE, it))) break;
                 write_sb();
             }
         }
-        if (s.final && ok) {
+        if (final && ok) {
 #pragma unroll
             for (int e = 0; e < 32; e += 2)
-                *reinterpret_cast<float4*>(s.final + base + (size_t)R * kD + kHalf * z + 2 * e) =
+                *reinterpret_cast<float4*>(final + (size_t)R * kD + kHalf * z + 2 * e) =
                     make_float4(S[e].x, S[e].y, S[e + 1].x, S[e + 1].y);
         }
     }
@@ -579,11 +637,64 @@ __global__ void __launch_bounds__(kThreads, 1)
 decay_tc_kernel(const __grid_constant__ TcArgs ta) {
     const DecayScan& s = ta.a.scan[blockIdx.y];
     if (s.reverse) {
-        if (s.out_f32) decay_tc_body<true, true>(ta);
-        else decay_tc_body<true, false>(ta);
+        if (s.out_f32) decay_tc_body<true, true, false>(ta);
+        else decay_tc_body<true, false, false>(ta);
     } else {
-        if (s.out_f32) decay_tc_body<false, true>(ta);
-        else decay_tc_body<false, false>(ta);
+        if (s.out_f32) decay_tc_body<false, true, false>(ta);
+        else decay_tc_body<false, false, false>(ta);
+    }
+}
+
+// Segments, first: what each adds to the state.
+__global__ void __launch_bounds__(kThreads, 1)
+decay_tc_state_kernel(const __grid_constant__ TcArgs ta) {
+    if (ta.a.scan[blockIdx.y].reverse) decay_tc_body<true, false, true>(ta);
+    else decay_tc_body<false, false, true>(ta);
+}
+
+// Segments, second: the state at each one's first visited end, S <- a^length S + the segment's own part, walked in
+// the scan's order; one float4 of one (sequence, head)'s state a thread, the parts of eight segments loaded at once.
+constexpr int kJoinThreads = 256, kJoinAhead = 8;
+__global__ void __launch_bounds__(kJoinThreads) decay_tc_join_kernel(const __grid_constant__ TcArgs ta) {
+    const DecayArgs& a = ta.a;
+    const DecayScan& s = a.scan[blockIdx.y];
+    constexpr int blocks = kD * kD / 4 / kJoinThreads;   // of one state
+    const int part = blockIdx.x % blocks, h = (blockIdx.x / blocks) % a.Hv, i = blockIdx.x / blocks / a.Hv;
+    long long s0, s1;
+    seq_range(a.cu, i, a.T, s0, s1);
+    const int n = (int)max(1LL, (s1 - s0 + ta.seg - 1) / ta.seg), slot0 = (int)(s0 / ta.seg) + i;
+    __shared__ float w[4];   // the decay over a whole and over the last segment, in two floats each
+    if (threadIdx.x < 2) {
+        const double len = threadIdx.x ? (double)(s1 - s0 - (long long)(n - 1) * ta.seg) : (double)ta.seg;
+        const double x = exp((double)fmaxf(a.log_decay[h], kMinLogDecay) * len);
+        w[2 * threadIdx.x] = (float)x;
+        w[2 * threadIdx.x + 1] = (float)(x - (double)(float)x);
+    }
+    __syncthreads();
+    const int e = (part * kJoinThreads + threadIdx.x) * 4, row = e / kD, col = e % kD;
+    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s.init) {
+        const float* x = s.init + ((size_t)i * a.Hv + h) * kD * kD;
+        S = s.init_t ? make_float4(x[col * kD + row], x[(col + 1) * kD + row], x[(col + 2) * kD + row], x[(col + 3) * kD + row])
+                     : *reinterpret_cast<const float4*>(x + e);
+    }
+    for (int j0 = 0; j0 < n; j0 += kJoinAhead) {
+        float4 add[kJoinAhead];
+#pragma unroll
+        for (int x = 0; x < kJoinAhead; ++x) {
+            const int j = j0 + x, at = slot0 + (s.reverse ? n - 1 - j : j);
+            if (j + 1 < n) add[x] = *reinterpret_cast<const float4*>(unit_state(ta, blockIdx.y, at, h) + e);
+        }
+#pragma unroll
+        for (int x = 0; x < kJoinAhead; ++x) {
+            const int j = j0 + x, at = s.reverse ? n - 1 - j : j;
+            if (j >= n) break;
+            *reinterpret_cast<float4*>(unit_state(ta, blockIdx.y, slot0 + at, h) + e) = S;
+            const float hi = w[at == n - 1 ? 2 : 0], lo = w[at == n - 1 ? 3 : 1];
+            if (j + 1 < n)
+                S = make_float4(fmaf(hi, S.x, fmaf(lo, S.x, add[x].x)), fmaf(hi, S.y, fmaf(lo, S.y, add[x].y)),
+                                fmaf(hi, S.z, fmaf(lo, S.z, add[x].z)), fmaf(hi, S.w, fmaf(lo, S.w, add[x].w)));
+        }
     }
 }
 
@@ -613,11 +724,40 @@ cudaError_t set_attributes() {
     std::lock_guard<std::mutex> lock(mu);
     if (done[dev]) return cudaSuccess;
     e = cudaFuncSetAttribute(decay_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(decay_tc_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e == cudaSuccess) done[dev] = true;
     return e;
 }
 
+// Tokens of a segment, 0 for whole sequences.  One CTA fills an SM, so a call of few sequences and heads leaves most
+// of the card idle and is bound by its longest sequence; in n segments a sequence takes 1 / n of its chunks' time
+// plus that of the pass that forms the segments' parts of the state (under half of the main pass a chunk).  So
+// sequences are cut where at least two segments of each find an SM of their own; the lengths of packed sequences
+// are not known here, and their total is cut instead (a sequence shorter than that is one segment).  Segments
+// shorter than kMinSegment would be mostly start-up.
+constexpr int kSms = 152, kMinSegment = 1024;
+int segment_tokens(long long tokens, int nseq, bool packed, int ctas_per_slot) {
+    long long seg;
+    if (packed) {
+        if ((long long)ctas_per_slot * 2 > kSms) return 0;
+        seg = (tokens * ctas_per_slot + kSms - 1) / kSms;
+    } else {
+        const long long n = kSms / ((long long)nseq * ctas_per_slot);
+        if (n < 2) return 0;
+        seg = (tokens / nseq + n - 1) / n;
+    }
+    seg = std::max<long long>((seg + kC - 1) / kC * kC, kMinSegment);
+    return seg < (packed ? tokens : tokens / nseq) ? (int)seg : 0;
+}
+long long segment_slots(long long tokens, int nseq, int seg) { return seg ? tokens / seg + nseq : nseq; }
+
 }  // namespace
+
+size_t decay_scan_tc_workspace_bytes(int Hv, int nseq, long long tokens, bool packed, int num_scans) {
+    const int seg = segment_tokens(tokens, nseq, packed, 2 * Hv * num_scans);
+    return seg ? (size_t)segment_slots(tokens, nseq, seg) * Hv * num_scans * kD * kD * sizeof(float) : 0;
+}
 
 cudaError_t launch_decay_scan_tc(const DecayArgs& a) {
     const auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
@@ -633,7 +773,17 @@ cudaError_t launch_decay_scan_tc(const DecayArgs& a) {
         if ((e = make_map(encode, &m.k, s.k, a.tokens, a.Hv / s.k_div, s.k_stride)) != cudaSuccess) return e;
         if ((e = make_map(encode, &m.v, s.v, a.tokens, a.Hv / s.v_div, s.v_stride)) != cudaSuccess) return e;
     }
-    const dim3 grid((unsigned)((long long)a.nseq * a.Hv * 2), (unsigned)a.num_scans);
+    t.seg = segment_tokens(a.tokens, a.nseq, a.cu != nullptr, 2 * a.Hv * a.num_scans);
+    t.slots = (int)segment_slots(a.tokens, a.nseq, t.seg);
+    t.states = static_cast<float*>(a.workspace);
+    const dim3 grid((unsigned)((long long)t.slots * a.Hv * 2), (unsigned)a.num_scans);
+    if (t.seg) {
+        decay_tc_state_kernel<<<grid, kThreads, kSmem, a.stream>>>(t);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        const dim3 join((unsigned)((long long)a.nseq * a.Hv * (kD * kD / 4 / kJoinThreads)), (unsigned)a.num_scans);
+        decay_tc_join_kernel<<<join, kJoinThreads, 0, a.stream>>>(t);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
     decay_tc_kernel<<<grid, kThreads, kSmem, a.stream>>>(t);
     return cudaGetLastError();
 }
