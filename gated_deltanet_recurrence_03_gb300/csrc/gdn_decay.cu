@@ -105,17 +105,12 @@ cudaError_t launch_serial(const DecayArgs& a) {
 
 }  // namespace
 
-namespace {
-bool on_tensor_cores(int dtype, int dk, int dv) { return dtype == GDN_BF16 && dk == 128 && dv == 128; }
-}  // namespace
-
 size_t decay_scan_workspace_bytes(int dtype, int dk, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans) {
-    return on_tensor_cores(dtype, dk, dv) ? decay_scan_tc_workspace_bytes(Hv, nseq, tokens, packed, num_scans) : 0;
+    return dtype == GDN_BF16 ? decay_scan_tc_workspace_bytes(dk, dv, Hv, nseq, tokens, packed, num_scans) : 0;
 }
 
 cudaError_t launch_decay_scan(const DecayArgs& a) {
-    if (on_tensor_cores(a.dtype, a.dk, a.dv)) return launch_decay_scan_tc(a);
-    return a.dtype == GDN_BF16 ? launch_serial<__nv_bfloat16>(a) : launch_serial<float>(a);
+    return a.dtype == GDN_BF16 ? launch_decay_scan_tc(a) : launch_serial<float>(a);
 }
 
 cudaError_t launch_head_sum(const float* part, void* out, long long out_stride, long long tokens, int Hqk, int G, int d,

@@ -1,12 +1,12 @@
-// The decayed scan (gdn_internal.cuh, DecayScan) on the tcgen05 tensor cores: bf16, 128-wide heads.
+// The decayed scan (gdn_internal.cuh, DecayScan) on the tcgen05 tensor cores: bf16, head dims 32, 64 and 128.
 //
 // Inside a chunk of C = 128 tokens, n of them valid, with w_d = a^d and S the state at the chunk's first
 // visited end (its start; its end in a reverse scan), in token order r, j = 0 .. n - 1:
 //   forward   out_r = so (w_{r+1} q_r S + su sum_{j<=r} w_{r-j} (q_r.k_j) v_j),  S <- w_n S + su sum_j w_{n-1-j} k_j v_j^T
 //   reverse   out_r = so (w_{n-1-r} q_r S + su sum_{j>=r} w_{j-r} (q_r.k_j) v_j), S <- w_n S + su sum_j w_{j+1} k_j v_j^T
 //
-// One CTA walks one sequence (or one segment of it) of one value head for 64 of the 128 value columns, so
-// that a head keeps two SMs busy; the two read the same q and k tiles, the second time from L2.  Per chunk
+// One CTA walks one sequence (or one segment of it) of one value head for 64 of its value columns, so that a
+// 128-wide head keeps two SMs busy; the two read the same q and k tiles, the second time from L2.  Per chunk
 // four products (M = 128 each):
 //   QK [128 x 128] = Q K^T;   PV [128 x 64] = P V, P = the decayed, masked QK as the bf16 A operand in TMEM;
 //   QS [128 x 64] = Q S_bf16;   KV [dk x 64] = K^T V~, V~ = V scaled by su w and split into three bf16 parts.
@@ -34,7 +34,6 @@ using namespace tc;
 using bf16 = __nv_bfloat16;
 
 constexpr int kC = 128;       // tokens of a chunk
-constexpr int kD = 128;       // head dims
 constexpr int kHalf = 64;     // value columns of a CTA
 constexpr int kParts = 3;     // bf16 parts of the scaled V
 
@@ -132,7 +131,7 @@ __device__ __forceinline__ bool unit_of(const TcArgs& ta, int slot, bool rev, Un
     return true;
 }
 __device__ __forceinline__ float* unit_state(const TcArgs& ta, int scan, int slot, int h) {
-    return ta.states + (((size_t)scan * ta.slots + slot) * ta.a.Hv + h) * kD * kD;
+    return ta.states + (((size_t)scan * ta.slots + slot) * ta.a.Hv + h) * ta.a.dk * ta.a.dv;
 }
 
 __device__ __forceinline__ void named_barrier_sync(int id, int threads) {
@@ -213,9 +212,12 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
     const DecayScan& s = a.scan[blockIdx.y];
     const Maps& maps = ta.maps[blockIdx.y];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int z = blockIdx.x & 1;
-    const int h = (blockIdx.x >> 1) % a.Hv;
-    const int slot = (blockIdx.x >> 1) / a.Hv;
+    const int dk = a.dk, dv = a.dv;
+    const int zs = dv > kHalf ? 2 : 1, z = blockIdx.x % zs;   // 64-column parts of the values: this CTA's
+    const int h = blockIdx.x / zs % a.Hv;
+    const int slot = blockIdx.x / zs / a.Hv;
+    const int width = min(kHalf, dv - kHalf * z);             // 32 where dv = 32: the tile's other columns are zeros
+    const int steps = dk / 16, panels = dk > 64 ? 2 : 1;      // of q and k rows (32-wide ones lie in 64-wide panels)
     constexpr bool rev = REV;
     Unit unit;
     if (!unit_of(ta, slot, rev, unit)) return;
@@ -267,18 +269,22 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                 const uint32_t bv = bar(B_FULLV + st), bqk = bar(B_FULLQK + st);
                 mbar_arrive_expect_tx(bv, kPanel);
                 tma_load_3d(sb + S_V + st * kPanel, &maps.v, 64 * z, hv, t, bv);
-                mbar_arrive_expect_tx(bqk, (STATE ? 2 : 4) * kPanel);
-                if (!STATE) tma_load_3d(sb + S_Q + 2 * st * kPanel, &maps.q, 0, hq, t, bqk);
-                tma_load_3d(sb + S_K + 2 * st * kPanel, &maps.k, 0, hk, t, bqk);
-                if (!STATE) tma_load_3d(sb + S_Q + (2 * st + 1) * kPanel, &maps.q, 64, hq, t, bqk);
-                tma_load_3d(sb + S_K + (2 * st + 1) * kPanel, &maps.k, 64, hk, t, bqk);
+                mbar_arrive_expect_tx(bqk, (STATE ? 1 : 2) * panels * kPanel);
+#pragma unroll 1
+                for (int p = 0; p < panels; ++p) {
+                    if (!STATE) tma_load_3d(sb + S_Q + (2 * st + p) * kPanel, &maps.q, 64 * p, hq, t, bqk);
+                    tma_load_3d(sb + S_K + (2 * st + p) * kPanel, &maps.k, 64 * p, hk, t, bqk);
+                }
             };
             auto prefetch = [&](int it) {   // into L2: the loads wait for a stage to be free and then cannot wait for DRAM
                 if (it >= nch) return;
                 const int t = (int)t0 + chunk_of(it) * kC;
                 tma_prefetch_3d(&maps.v, 64 * z, hv, t);
-                if (!STATE) tma_prefetch_3d(&maps.q, 64 * z, hq, t);   // the other half of q and k: the head's other CTA
-                tma_prefetch_3d(&maps.k, 64 * z, hk, t);
+#pragma unroll 1
+                for (int p = z; p < panels; p += zs) {   // with two CTAs for a head each takes half of q and k
+                    if (!STATE) tma_prefetch_3d(&maps.q, 64 * p, hq, t);
+                    tma_prefetch_3d(&maps.k, 64 * p, hk, t);
+                }
             };
             int loaded = 0;
             for (; loaded < 2 && loaded < nch; ++loaded) load(loaded);
@@ -320,6 +326,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                 ok = wait(B_VP, it) && (it < 1 || wait(B_KVFREE, it - 1));
                 if (!__all_sync(~0u, ok)) break;
                 tc_fence_after();
+                // (rows past dk of the product come from whatever lies behind k's panel: nothing reads them)
                 const uint64_t kt = dKt + ((st * 2 * kPanel) >> 4);
                 // half the rows at a time, so that the first half's parts are replaced while the second runs
                 if (elect_one()) {
@@ -357,6 +364,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
+                        if (ks >= steps) break;
                         const uint32_t x = o + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4);
                         mma_bf16(tmem + T_QK, dQ + x, dK + x, idesc_bf16(128, 128, 0, 0), ks > 0);
                     }
@@ -371,9 +379,11 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
+                    for (int ks = 0; ks < 8; ++ks) {
+                        if (ks >= steps) break;
                         mma_bf16(tmem + T_QS, q + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4), dSB + ((ks * 2048) >> 4),
                                  idesc_bf16(128, 64, 0, 1), ks > 0);
+                    }
                 }
                 __syncwarp();
                 ok = wait(B_P, it);
@@ -505,7 +515,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
         // read: warps w and w + 4 hold the two halves of the same 32 rows, and each writes 16 whole rows.
         constexpr int esize = F32 ? 4 : 2;
         const int pair = 1 + (warp & 3), own = 32 * (warp & 3) + 4 * c0 + (lane >> 3), chunk = lane & 7;
-        uint8_t* const out = static_cast<uint8_t*>(s.out) + ((size_t)h * kD + kHalf * z) * esize +
+        uint8_t* const out = static_cast<uint8_t*>(s.out) + ((size_t)h * dv + kHalf * z) * esize +
                              (F32 ? (chunk >> 2) * 128 + (chunk & 3) * 16 : chunk * 16);
         const size_t pitch = (size_t)s.out_stride * esize;
         for (int it = -1; it < nch; ++it) {
@@ -546,7 +556,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                     named_barrier_sync(pair, 64);
 #pragma unroll
                     for (int x = 0; x < 16; x += 4)
-                        if (own + x < n)
+                        if (own + x < n && (F32 ? 32 * (chunk >> 2) + 16 * b + 4 * (chunk & 3) : 8 * chunk) < width)
                             *reinterpret_cast<uint4*>(first + (size_t)(own + x) * pitch + (F32 ? 64 * b : 0)) =
                                 *reinterpret_cast<const uint4*>(sm + S_SB + swz(own + x, chunk));
                 }
@@ -557,26 +567,30 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
         // ------------------------------------------------------------ the state: row R of dk, 64 columns a thread
         regs_inc<kRegsState>();
         const int R = tid - 32 * kWarpState;
-        const size_t base = ((size_t)unit.seq * a.Hv + h) * kD * kD;
+        const size_t base = ((size_t)unit.seq * a.Hv + h) * dk * dv;
         const float* const init = STATE ? nullptr : ta.seg ? unit_state(ta, blockIdx.y, slot, h) : s.init ? s.init + base : nullptr;
         float* const final = STATE ? unit_state(ta, blockIdx.y, slot, h) : s.final && unit.last ? s.final + base : nullptr;
+        // (rows past dk and columns past dv hold what the products leave there and go nowhere)
         float2 S[32];
-        if (init && s.init_t && !ta.seg) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const float* x = init + (size_t)(kHalf * z + 2 * e) * kD + R;
-                S[e] = make_float2(x[0], x[kD]);
+        for (int e = 0; e < 32; ++e) S[e] = make_float2(0.f, 0.f);
+        if (init && R < dk) {
+            if (s.init_t && !ta.seg) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    if (2 * e >= width) break;
+                    const float* x = init + (size_t)(kHalf * z + 2 * e) * dk + R;
+                    S[e] = make_float2(x[0], x[dk]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    if (2 * e >= width) break;
+                    const float4 x = *reinterpret_cast<const float4*>(init + (size_t)R * dv + kHalf * z + 2 * e);
+                    S[e] = make_float2(x.x, x.y);
+                    S[e + 1] = make_float2(x.z, x.w);
+                }
             }
-        } else if (init) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-                const float4 x = *reinterpret_cast<const float4*>(init + (size_t)R * kD + kHalf * z + 2 * e);
-                S[e] = make_float2(x.x, x.y);
-                S[e + 1] = make_float2(x.z, x.w);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) S[e] = make_float2(0.f, 0.f);
         }
         auto write_sb = [&] {
 #pragma unroll
@@ -618,11 +632,13 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                 write_sb();
             }
         }
-        if (final && ok) {
+        if (final && ok && R < dk) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 2)
-                *reinterpret_cast<float4*>(final + (size_t)R * kD + kHalf * z + 2 * e) =
+            for (int e = 0; e < 32; e += 2) {
+                if (2 * e >= width) break;
+                *reinterpret_cast<float4*>(final + (size_t)R * dv + kHalf * z + 2 * e) =
                     make_float4(S[e].x, S[e].y, S[e + 1].x, S[e + 1].y);
+            }
         }
     }
     tc_fence_before();
@@ -658,7 +674,7 @@ constexpr int kJoinThreads = 256, kJoinAhead = 8;
 __global__ void __launch_bounds__(kJoinThreads) decay_tc_join_kernel(const __grid_constant__ TcArgs ta) {
     const DecayArgs& a = ta.a;
     const DecayScan& s = a.scan[blockIdx.y];
-    constexpr int blocks = kD * kD / 4 / kJoinThreads;   // of one state
+    const int dk = a.dk, dv = a.dv, blocks = dk * dv / 4 / kJoinThreads;   // of one state (at least 32 x 32)
     const int part = blockIdx.x % blocks, h = (blockIdx.x / blocks) % a.Hv, i = blockIdx.x / blocks / a.Hv;
     long long s0, s1;
     seq_range(a.cu, i, a.T, s0, s1);
@@ -671,11 +687,11 @@ __global__ void __launch_bounds__(kJoinThreads) decay_tc_join_kernel(const __gri
         w[2 * threadIdx.x + 1] = (float)(x - (double)(float)x);
     }
     __syncthreads();
-    const int e = (part * kJoinThreads + threadIdx.x) * 4, row = e / kD, col = e % kD;
+    const int e = (part * kJoinThreads + threadIdx.x) * 4, row = e / dv, col = e % dv;
     float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
     if (s.init) {
-        const float* x = s.init + ((size_t)i * a.Hv + h) * kD * kD;
-        S = s.init_t ? make_float4(x[col * kD + row], x[(col + 1) * kD + row], x[(col + 2) * kD + row], x[(col + 3) * kD + row])
+        const float* x = s.init + ((size_t)i * a.Hv + h) * dk * dv;
+        S = s.init_t ? make_float4(x[col * dk + row], x[(col + 1) * dk + row], x[(col + 2) * dk + row], x[(col + 3) * dk + row])
                      : *reinterpret_cast<const float4*>(x + e);
     }
     for (int j0 = 0; j0 < n; j0 += kJoinAhead) {
@@ -699,12 +715,12 @@ __global__ void __launch_bounds__(kJoinThreads) decay_tc_join_kernel(const __gri
 }
 
 // ------------------------------------------------------------------ host side
-// [tokens, heads, 128] bf16 tensor, token rows `stride` elements apart; box of 128 tokens x 1 head x 64 values,
-// 128-byte swizzle.
+// [tokens, heads, d] bf16 tensor, token rows `stride` elements apart; box of 128 tokens x 1 head x 64 values (of a
+// head of 32 the other 32 are filled with zeros), 128-byte swizzle.
 cudaError_t make_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const void* base, long long tokens,
-                     int heads, long long stride) {
-    const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)heads, (cuuint64_t)tokens};
-    const cuuint64_t strides[2] = {(cuuint64_t)kD * 2, (cuuint64_t)stride * 2};
+                     int heads, int d, long long stride) {
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
     const cuuint32_t box[3] = {64, 1, kC};
     const cuuint32_t elem[3] = {1, 1, 1};
     const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, elem,
@@ -737,26 +753,27 @@ cudaError_t set_attributes() {
 // are not known here, and their total is cut instead (a sequence shorter than that is one segment).  Segments
 // shorter than kMinSegment would be mostly start-up.
 constexpr int kSms = 152, kMinSegment = 1024;
-int segment_tokens(long long tokens, int nseq, bool packed, int ctas_per_slot) {
+int segment_tokens(long long tokens, int nseq, bool packed, int ctas) {
     long long seg;
     if (packed) {
-        if ((long long)ctas_per_slot * 2 > kSms) return 0;
-        seg = (tokens * ctas_per_slot + kSms - 1) / kSms;
+        if (ctas * 2 > kSms) return 0;
+        seg = (tokens * ctas + kSms - 1) / kSms;
     } else {
-        const long long n = kSms / ((long long)nseq * ctas_per_slot);
+        const long long n = kSms / ((long long)nseq * ctas);
         if (n < 2) return 0;
         seg = (tokens / nseq + n - 1) / n;
     }
     seg = std::max<long long>((seg + kC - 1) / kC * kC, kMinSegment);
     return seg < (packed ? tokens : tokens / nseq) ? (int)seg : 0;
 }
+int ctas_per_slot(int dv, int Hv, int num_scans) { return (dv > kHalf ? 2 : 1) * Hv * num_scans; }
 long long segment_slots(long long tokens, int nseq, int seg) { return seg ? tokens / seg + nseq : nseq; }
 
 }  // namespace
 
-size_t decay_scan_tc_workspace_bytes(int Hv, int nseq, long long tokens, bool packed, int num_scans) {
-    const int seg = segment_tokens(tokens, nseq, packed, 2 * Hv * num_scans);
-    return seg ? (size_t)segment_slots(tokens, nseq, seg) * Hv * num_scans * kD * kD * sizeof(float) : 0;
+size_t decay_scan_tc_workspace_bytes(int dk, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans) {
+    const int seg = segment_tokens(tokens, nseq, packed, ctas_per_slot(dv, Hv, num_scans));
+    return seg ? (size_t)segment_slots(tokens, nseq, seg) * Hv * num_scans * dk * dv * sizeof(float) : 0;
 }
 
 cudaError_t launch_decay_scan_tc(const DecayArgs& a) {
@@ -769,18 +786,18 @@ cudaError_t launch_decay_scan_tc(const DecayArgs& a) {
     for (int i = 0; i < a.num_scans; ++i) {
         const DecayScan& s = a.scan[i];
         Maps& m = t.maps[i];
-        if ((e = make_map(encode, &m.q, s.q, a.tokens, a.Hv / s.q_div, s.q_stride)) != cudaSuccess) return e;
-        if ((e = make_map(encode, &m.k, s.k, a.tokens, a.Hv / s.k_div, s.k_stride)) != cudaSuccess) return e;
-        if ((e = make_map(encode, &m.v, s.v, a.tokens, a.Hv / s.v_div, s.v_stride)) != cudaSuccess) return e;
+        if ((e = make_map(encode, &m.q, s.q, a.tokens, a.Hv / s.q_div, a.dk, s.q_stride)) != cudaSuccess) return e;
+        if ((e = make_map(encode, &m.k, s.k, a.tokens, a.Hv / s.k_div, a.dk, s.k_stride)) != cudaSuccess) return e;
+        if ((e = make_map(encode, &m.v, s.v, a.tokens, a.Hv / s.v_div, a.dv, s.v_stride)) != cudaSuccess) return e;
     }
-    t.seg = segment_tokens(a.tokens, a.nseq, a.cu != nullptr, 2 * a.Hv * a.num_scans);
+    t.seg = segment_tokens(a.tokens, a.nseq, a.cu != nullptr, ctas_per_slot(a.dv, a.Hv, a.num_scans));
     t.slots = (int)segment_slots(a.tokens, a.nseq, t.seg);
     t.states = static_cast<float*>(a.workspace);
-    const dim3 grid((unsigned)((long long)t.slots * a.Hv * 2), (unsigned)a.num_scans);
+    const dim3 grid((unsigned)((long long)t.slots * ctas_per_slot(a.dv, a.Hv, 1)), (unsigned)a.num_scans);
     if (t.seg) {
         decay_tc_state_kernel<<<grid, kThreads, kSmem, a.stream>>>(t);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        const dim3 join((unsigned)((long long)a.nseq * a.Hv * (kD * kD / 4 / kJoinThreads)), (unsigned)a.num_scans);
+        const dim3 join((unsigned)((long long)a.nseq * a.Hv * (a.dk * a.dv / 4 / kJoinThreads)), (unsigned)a.num_scans);
         decay_tc_join_kernel<<<join, kJoinThreads, 0, a.stream>>>(t);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
