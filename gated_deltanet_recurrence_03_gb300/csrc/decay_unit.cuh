@@ -1,0 +1,64 @@
+// Units of work of the decayed scan's kernels: sequences, or segments of them.
+#pragma once
+
+#include "gdn_internal.cuh"
+
+namespace gdn {
+
+// Segments: segment j of sequence i is slot floor(start_i / seg) + i + j (no prefix sum needed); `states` holds
+// [scan][slot][Hv][dk][dv] floats, first a segment's own contribution to the state, then the state at its first
+// visited end.  seg = 0: one CTA walks a whole sequence, and a slot is a sequence.
+struct SegArgs {
+    DecayArgs a;
+    int seg, slots;
+    float* states;
+};
+
+// The tokens of a slot, and whether it is the first and the last one its sequence's scan visits; false for a slot
+// without a sequence's segment (an empty sequence has one segment of no tokens).
+struct Unit {
+    int seq;
+    long long t0, t1;
+    bool first, last;
+};
+__device__ __forceinline__ bool unit_of(const SegArgs& ta, int slot, bool rev, Unit& u) {
+    const DecayArgs& a = ta.a;
+    if (!ta.seg) {
+        u.seq = slot;
+        seq_range(a.cu, slot, a.T, u.t0, u.t1);
+        u.first = u.last = true;
+        return true;
+    }
+    auto base = [&](int i) {
+        long long s0, s1;
+        seq_range(a.cu, i, a.T, s0, s1);
+        return s0 / ta.seg + i;
+    };
+    int lo = 0, hi = a.nseq - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (base(mid) <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    long long s0, s1;
+    seq_range(a.cu, lo, a.T, s0, s1);
+    const long long j = slot - base(lo), n = max(1LL, (s1 - s0 + ta.seg - 1) / ta.seg);
+    if (j < 0 || j >= n) return false;
+    u.seq = lo;
+    u.t0 = s0 + j * ta.seg;
+    u.t1 = min(s1, u.t0 + ta.seg);
+    u.first = j == (rev ? n - 1 : 0);
+    u.last = j == (rev ? 0 : n - 1);
+    return true;
+}
+__device__ __forceinline__ float* unit_state(const SegArgs& ta, int scan, int slot, int h) {
+    return ta.states + (((size_t)scan * ta.slots + slot) * ta.a.Hv + h) * ta.a.dk * ta.a.dv;
+}
+
+// The scan's main kernel (state_only = false), or the pass before it that forms every segment's own contribution to
+// the state, on the tensor cores (bf16) and on the CUDA cores (fp32).
+cudaError_t launch_decay_tc(const SegArgs& s, bool state_only);
+cudaError_t launch_decay_f32(const SegArgs& s, bool state_only);
+constexpr int kDecayColumns = 64;   // value columns of a CTA of either
+
+}  // namespace gdn

@@ -1,73 +1,55 @@
-// Linear attention with a decay for each value head: the scan behind gdn_decay_attn_fwd and, three times,
-// behind gdn_decay_attn_bwd (gdn_internal.cuh, DecayScan).  The token-by-token form on CUDA cores: one CTA
-// owns one (sequence, value head) state, dk / 32 adjacent lanes own one of its columns (32 rows each, in
-// registers), and the tokens' q, k and v are staged through shared memory a few at a time.
-#include "gdn_internal.cuh"
+// Linear attention with a decay for each value head: the scan behind gdn_decay_attn_fwd and, three times, behind
+// gdn_decay_attn_bwd (gdn_internal.cuh, DecayScan): how long sequences are cut, and the passes over them.
+#include <algorithm>
+
+#include "decay_unit.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kTB = 16;   // tokens staged per round
-
-template <int DK, int DV, typename T>
-__global__ void __launch_bounds__(DV * (DK / 32))
-decay_serial_kernel(const __grid_constant__ DecayArgs a) {
-    constexpr int SPLIT = DK / 32, NT = DV * SPLIT;
-    __shared__ __align__(16) float sk[kTB][DK];
-    __shared__ __align__(16) float sq[kTB][DK];
-    __shared__ float sv[kTB][DV];
+// Between the two passes over segments: the state at each one's first visited end, S <- a^length S + the segment's own part, walked in
+// the scan's order; one float4 of one (sequence, head)'s state a thread, the parts of eight segments loaded at once.
+constexpr int kJoinThreads = 256, kJoinAhead = 8;
+__global__ void __launch_bounds__(kJoinThreads) decay_join_kernel(const __grid_constant__ SegArgs ta) {
+    const DecayArgs& a = ta.a;
     const DecayScan& s = a.scan[blockIdx.y];
-    const int h = blockIdx.x % a.Hv, i = blockIdx.x / a.Hv, tid = threadIdx.x;
-    const int j = tid / SPLIT, part = tid % SPLIT;   // column of S, rows part * 32 .. + 31
-    long long t0, t1;
-    seq_range(a.cu, i, a.T, t0, t1);
-    // the decay in two floats: a rounding error in it would compound over the head's whole memory
-    const double ad = exp((double)fmaxf(a.log_decay[h], kMinLogDecay));
-    const float al = (float)ad, al_lo = (float)(ad - (double)al);
-    const size_t sbase = ((size_t)i * a.Hv + h) * DK * DV;
-    float st[32];
-#pragma unroll
-    for (int r = 0; r < 32; ++r) {
-        const int row = part * 32 + r;
-        st[r] = s.init ? s.init[sbase + (s.init_t ? (size_t)j * DK + row : (size_t)row * DV + j)] : 0.f;
+    const int dk = a.dk, dv = a.dv, blocks = dk * dv / 4 / kJoinThreads;   // of one state (at least 32 x 32)
+    const int part = blockIdx.x % blocks, h = (blockIdx.x / blocks) % a.Hv, i = blockIdx.x / blocks / a.Hv;
+    long long s0, s1;
+    seq_range(a.cu, i, a.T, s0, s1);
+    const int n = (int)max(1LL, (s1 - s0 + ta.seg - 1) / ta.seg), slot0 = (int)(s0 / ta.seg) + i;
+    __shared__ float w[4];   // the decay over a whole and over the last segment, in two floats each
+    if (threadIdx.x < 2) {
+        const double len = threadIdx.x ? (double)(s1 - s0 - (long long)(n - 1) * ta.seg) : (double)ta.seg;
+        const double x = exp((double)fmaxf(a.log_decay[h], kMinLogDecay) * len);
+        w[2 * threadIdx.x] = (float)x;
+        w[2 * threadIdx.x + 1] = (float)(x - (double)(float)x);
     }
-    const T* q = static_cast<const T*>(s.q) + (size_t)(h / s.q_div) * DK;
-    const T* k = static_cast<const T*>(s.k) + (size_t)(h / s.k_div) * DK;
-    const T* v = static_cast<const T*>(s.v) + (size_t)(h / s.v_div) * DV;
-    for (long long done = 0; done < t1 - t0; done += kTB) {
-        const int nt = (int)min((long long)kTB, t1 - t0 - done);
-        const long long tb = s.reverse ? t1 - done - nt : t0 + done;
-        __syncthreads();   // the previous round has read the staging buffers
-        for (int e = tid; e < nt * DK; e += NT) {
-            const int tt = e / DK, c = e % DK;
-            sk[tt][c] = s.su * to_f32(k[(size_t)(tb + tt) * s.k_stride + c]);
-            sq[tt][c] = s.so * to_f32(q[(size_t)(tb + tt) * s.q_stride + c]);
-        }
-        for (int e = tid; e < nt * DV; e += NT) sv[e / DV][e % DV] = to_f32(v[(size_t)(tb + e / DV) * s.v_stride + e % DV]);
-        __syncthreads();
-        for (int x = 0; x < nt; ++x) {
-            const int tt = s.reverse ? nt - 1 - x : x;
-            const float vj = sv[tt][j];
-            float o = 0.f;
-#pragma unroll
-            for (int r = 0; r < 32; ++r) {
-                if (!s.reverse) st[r] = fmaf(al, st[r], al_lo * st[r]);
-                st[r] = fmaf(sk[tt][part * 32 + r], vj, st[r]);
-                o = fmaf(sq[tt][part * 32 + r], st[r], o);
-                if (s.reverse) st[r] = fmaf(al, st[r], al_lo * st[r]);
-            }
-#pragma unroll
-            for (int m = 1; m < SPLIT; m <<= 1) o += __shfl_xor_sync(0xffffffffu, o, m);
-            if (part == 0) {
-                const size_t at = (size_t)(tb + tt) * s.out_stride + (size_t)h * DV + j;
-                if (s.out_f32) static_cast<float*>(s.out)[at] = o;
-                else static_cast<T*>(s.out)[at] = from_f32<T>(o);
-            }
-        }
+    __syncthreads();
+    const int e = (part * kJoinThreads + threadIdx.x) * 4, row = e / dv, col = e % dv;
+    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s.init) {
+        const float* x = s.init + ((size_t)i * a.Hv + h) * dk * dv;
+        S = s.init_t ? make_float4(x[col * dk + row], x[(col + 1) * dk + row], x[(col + 2) * dk + row], x[(col + 3) * dk + row])
+                     : *reinterpret_cast<const float4*>(x + e);
     }
-    if (s.final) {
+    for (int j0 = 0; j0 < n; j0 += kJoinAhead) {
+        float4 add[kJoinAhead];
 #pragma unroll
-        for (int r = 0; r < 32; ++r) s.final[sbase + (size_t)(part * 32 + r) * DV + j] = st[r];
+        for (int x = 0; x < kJoinAhead; ++x) {
+            const int j = j0 + x, at = slot0 + (s.reverse ? n - 1 - j : j);
+            if (j + 1 < n) add[x] = *reinterpret_cast<const float4*>(unit_state(ta, blockIdx.y, at, h) + e);
+        }
+#pragma unroll
+        for (int x = 0; x < kJoinAhead; ++x) {
+            const int j = j0 + x, at = s.reverse ? n - 1 - j : j;
+            if (j >= n) break;
+            *reinterpret_cast<float4*>(unit_state(ta, blockIdx.y, slot0 + at, h) + e) = S;
+            const float hi = w[at == n - 1 ? 2 : 0], lo = w[at == n - 1 ? 3 : 1];
+            if (j + 1 < n)
+                S = make_float4(fmaf(hi, S.x, fmaf(lo, S.x, add[x].x)), fmaf(hi, S.y, fmaf(lo, S.y, add[x].y)),
+                                fmaf(hi, S.z, fmaf(lo, S.z, add[x].z)), fmaf(hi, S.w, fmaf(lo, S.w, add[x].w)));
+        }
     }
 }
 
@@ -88,29 +70,58 @@ __global__ void head_sum_kernel(const float* __restrict__ part, T* __restrict__ 
     o[0] = from_f32<T>(acc.x); o[1] = from_f32<T>(acc.y); o[2] = from_f32<T>(acc.z); o[3] = from_f32<T>(acc.w);
 }
 
-template <typename T>
-cudaError_t launch_serial(const DecayArgs& a) {
-    const dim3 grid((unsigned)((long long)a.nseq * a.Hv), (unsigned)a.num_scans);
-#define GDN_DECAY_CASE(DK_, DV_)                                                                  \
-    if (a.dk == DK_ && a.dv == DV_) {                                                             \
-        decay_serial_kernel<DK_, DV_, T><<<grid, DV_ * (DK_ / 32), 0, a.stream>>>(a);             \
-        return cudaGetLastError();                                                                \
+// Tokens of a segment, 0 for whole sequences.  One CTA walks one slot, so a call of few sequences and heads leaves most
+// of the card idle and is bound by its longest sequence; in n segments a sequence takes 1 / n of its chunks' time
+// plus that of the pass that forms the segments' parts of the state (under half of the main pass a chunk).  So
+// sequences are cut where at least two segments of each find an SM of their own; the lengths of packed sequences
+// are not known here, and their total is cut instead (a sequence shorter than that is one segment).  Segments
+// shorter than kMinSegment would be mostly start-up.
+constexpr int kSms = 152, kMinSegment = 1024;
+int segment_tokens(long long tokens, int nseq, bool packed, int ctas) {
+    long long seg;
+    if (packed) {
+        if (ctas * 2 > kSms) return 0;
+        seg = (tokens * ctas + kSms - 1) / kSms;
+    } else {
+        const long long n = kSms / ((long long)nseq * ctas);
+        if (n < 2) return 0;
+        seg = (tokens / nseq + n - 1) / n;
     }
-    GDN_DECAY_CASE(32, 32) GDN_DECAY_CASE(32, 64) GDN_DECAY_CASE(32, 128)
-    GDN_DECAY_CASE(64, 32) GDN_DECAY_CASE(64, 64) GDN_DECAY_CASE(64, 128)
-    GDN_DECAY_CASE(128, 32) GDN_DECAY_CASE(128, 64) GDN_DECAY_CASE(128, 128)
-#undef GDN_DECAY_CASE
-    return cudaErrorInvalidValue;
+    seg = std::max<long long>((seg + 127) / 128 * 128, kMinSegment);
+    return seg < (packed ? tokens : tokens / nseq) ? (int)seg : 0;
+}
+long long segment_slots(long long tokens, int nseq, int seg) { return seg ? tokens / seg + nseq : nseq; }
+
+
+// Segment tokens and slots of a call, and the bytes of its segments' states.
+SegArgs plan_of(int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans) {
+    SegArgs p{};
+    const int ctas = (dv > kDecayColumns ? dv / kDecayColumns : 1) * Hv * num_scans;   // of one slot
+    p.seg = segment_tokens(tokens, nseq, packed, ctas);
+    p.slots = (int)segment_slots(tokens, nseq, p.seg);
+    return p;
 }
 
 }  // namespace
 
-size_t decay_scan_workspace_bytes(int dtype, int dk, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans) {
-    return dtype == GDN_BF16 ? decay_scan_tc_workspace_bytes(dk, dv, Hv, nseq, tokens, packed, num_scans) : 0;
+size_t decay_scan_workspace_bytes(int dk, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans) {
+    const SegArgs p = plan_of(dv, Hv, nseq, tokens, packed, num_scans);
+    return p.seg ? (size_t)p.slots * Hv * num_scans * dk * dv * sizeof(float) : 0;
 }
 
 cudaError_t launch_decay_scan(const DecayArgs& a) {
-    return a.dtype == GDN_BF16 ? launch_decay_scan_tc(a) : launch_serial<float>(a);
+    SegArgs p = plan_of(a.dv, a.Hv, a.nseq, a.tokens, a.cu != nullptr, a.num_scans);
+    p.a = a;
+    p.states = static_cast<float*>(a.workspace);
+    const auto pass = a.dtype == GDN_BF16 ? launch_decay_tc : launch_decay_f32;
+    if (p.seg) {
+        cudaError_t e = pass(p, true);
+        if (e != cudaSuccess) return e;
+        const dim3 grid((unsigned)((long long)a.nseq * a.Hv * (a.dk * a.dv / 4 / kJoinThreads)), (unsigned)a.num_scans);
+        decay_join_kernel<<<grid, kJoinThreads, 0, a.stream>>>(p);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    return pass(p, false);
 }
 
 cudaError_t launch_head_sum(const float* part, void* out, long long out_stride, long long tokens, int Hqk, int G, int d,

@@ -21,10 +21,9 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <algorithm>
 #include <mutex>
 
-#include "gdn_internal.cuh"
+#include "decay_unit.cuh"
 #include "tc_ptx.cuh"
 
 namespace gdn {
@@ -34,7 +33,7 @@ using namespace tc;
 using bf16 = __nv_bfloat16;
 
 constexpr int kC = 128;       // tokens of a chunk
-constexpr int kHalf = 64;     // value columns of a CTA
+constexpr int kHalf = kDecayColumns;
 constexpr int kParts = 3;     // bf16 parts of the scaled V
 
 // Shared memory (bytes from the 1024-aligned base).  Panels: 128 rows x 64 bf16, 128-byte swizzle.
@@ -83,56 +82,10 @@ constexpr float kStrong = -5.f;   // log decays below this are not factored over
 struct Maps {
     CUtensorMap q, k, v;
 };
-struct TcArgs {
+struct TcArgs : SegArgs {
     Maps maps[kMaxScans];
-    DecayArgs a;
-    // Segments: segment j of sequence i is slot floor(start_i / seg) + i + j (no prefix sum needed); `states` holds
-    // [scan][slot][Hv][dk][dv] floats, first a segment's own contribution to the state, then the state at its
-    // first visited end.  seg = 0: one CTA walks a whole sequence, and a slot is a sequence.
-    int seg, slots;
-    float* states;
 };
 
-// The tokens of a slot, and whether it is the first and the last one its sequence's scan visits; false for a slot
-// without a sequence's segment (an empty sequence has one segment of no tokens).
-struct Unit {
-    int seq;
-    long long t0, t1;
-    bool first, last;
-};
-__device__ __forceinline__ bool unit_of(const TcArgs& ta, int slot, bool rev, Unit& u) {
-    const DecayArgs& a = ta.a;
-    if (!ta.seg) {
-        u.seq = slot;
-        seq_range(a.cu, slot, a.T, u.t0, u.t1);
-        u.first = u.last = true;
-        return true;
-    }
-    auto base = [&](int i) {
-        long long s0, s1;
-        seq_range(a.cu, i, a.T, s0, s1);
-        return s0 / ta.seg + i;
-    };
-    int lo = 0, hi = a.nseq - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (base(mid) <= slot) lo = mid;
-        else hi = mid - 1;
-    }
-    long long s0, s1;
-    seq_range(a.cu, lo, a.T, s0, s1);
-    const long long j = slot - base(lo), n = max(1LL, (s1 - s0 + ta.seg - 1) / ta.seg);
-    if (j < 0 || j >= n) return false;
-    u.seq = lo;
-    u.t0 = s0 + j * ta.seg;
-    u.t1 = min(s1, u.t0 + ta.seg);
-    u.first = j == (rev ? n - 1 : 0);
-    u.last = j == (rev ? 0 : n - 1);
-    return true;
-}
-__device__ __forceinline__ float* unit_state(const TcArgs& ta, int scan, int slot, int h) {
-    return ta.states + (((size_t)scan * ta.slots + slot) * ta.a.Hv + h) * ta.a.dk * ta.a.dv;
-}
 
 __device__ __forceinline__ void named_barrier_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -668,52 +621,6 @@ decay_tc_state_kernel(const __grid_constant__ TcArgs ta) {
     else decay_tc_body<false, false, true>(ta);
 }
 
-// Segments, second: the state at each one's first visited end, S <- a^length S + the segment's own part, walked in
-// the scan's order; one float4 of one (sequence, head)'s state a thread, the parts of eight segments loaded at once.
-constexpr int kJoinThreads = 256, kJoinAhead = 8;
-__global__ void __launch_bounds__(kJoinThreads) decay_tc_join_kernel(const __grid_constant__ TcArgs ta) {
-    const DecayArgs& a = ta.a;
-    const DecayScan& s = a.scan[blockIdx.y];
-    const int dk = a.dk, dv = a.dv, blocks = dk * dv / 4 / kJoinThreads;   // of one state (at least 32 x 32)
-    const int part = blockIdx.x % blocks, h = (blockIdx.x / blocks) % a.Hv, i = blockIdx.x / blocks / a.Hv;
-    long long s0, s1;
-    seq_range(a.cu, i, a.T, s0, s1);
-    const int n = (int)max(1LL, (s1 - s0 + ta.seg - 1) / ta.seg), slot0 = (int)(s0 / ta.seg) + i;
-    __shared__ float w[4];   // the decay over a whole and over the last segment, in two floats each
-    if (threadIdx.x < 2) {
-        const double len = threadIdx.x ? (double)(s1 - s0 - (long long)(n - 1) * ta.seg) : (double)ta.seg;
-        const double x = exp((double)fmaxf(a.log_decay[h], kMinLogDecay) * len);
-        w[2 * threadIdx.x] = (float)x;
-        w[2 * threadIdx.x + 1] = (float)(x - (double)(float)x);
-    }
-    __syncthreads();
-    const int e = (part * kJoinThreads + threadIdx.x) * 4, row = e / dv, col = e % dv;
-    float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (s.init) {
-        const float* x = s.init + ((size_t)i * a.Hv + h) * dk * dv;
-        S = s.init_t ? make_float4(x[col * dk + row], x[(col + 1) * dk + row], x[(col + 2) * dk + row], x[(col + 3) * dk + row])
-                     : *reinterpret_cast<const float4*>(x + e);
-    }
-    for (int j0 = 0; j0 < n; j0 += kJoinAhead) {
-        float4 add[kJoinAhead];
-#pragma unroll
-        for (int x = 0; x < kJoinAhead; ++x) {
-            const int j = j0 + x, at = slot0 + (s.reverse ? n - 1 - j : j);
-            if (j + 1 < n) add[x] = *reinterpret_cast<const float4*>(unit_state(ta, blockIdx.y, at, h) + e);
-        }
-#pragma unroll
-        for (int x = 0; x < kJoinAhead; ++x) {
-            const int j = j0 + x, at = s.reverse ? n - 1 - j : j;
-            if (j >= n) break;
-            *reinterpret_cast<float4*>(unit_state(ta, blockIdx.y, slot0 + at, h) + e) = S;
-            const float hi = w[at == n - 1 ? 2 : 0], lo = w[at == n - 1 ? 3 : 1];
-            if (j + 1 < n)
-                S = make_float4(fmaf(hi, S.x, fmaf(lo, S.x, add[x].x)), fmaf(hi, S.y, fmaf(lo, S.y, add[x].y)),
-                                fmaf(hi, S.z, fmaf(lo, S.z, add[x].z)), fmaf(hi, S.w, fmaf(lo, S.w, add[x].w)));
-        }
-    }
-}
-
 // ------------------------------------------------------------------ host side
 // [tokens, heads, d] bf16 tensor, token rows `stride` elements apart; box of 128 tokens x 1 head x 64 values (of a
 // head of 32 the other 32 are filled with zeros), 128-byte swizzle.
@@ -746,43 +653,16 @@ cudaError_t set_attributes() {
     return e;
 }
 
-// Tokens of a segment, 0 for whole sequences.  One CTA fills an SM, so a call of few sequences and heads leaves most
-// of the card idle and is bound by its longest sequence; in n segments a sequence takes 1 / n of its chunks' time
-// plus that of the pass that forms the segments' parts of the state (under half of the main pass a chunk).  So
-// sequences are cut where at least two segments of each find an SM of their own; the lengths of packed sequences
-// are not known here, and their total is cut instead (a sequence shorter than that is one segment).  Segments
-// shorter than kMinSegment would be mostly start-up.
-constexpr int kSms = 152, kMinSegment = 1024;
-int segment_tokens(long long tokens, int nseq, bool packed, int ctas) {
-    long long seg;
-    if (packed) {
-        if (ctas * 2 > kSms) return 0;
-        seg = (tokens * ctas + kSms - 1) / kSms;
-    } else {
-        const long long n = kSms / ((long long)nseq * ctas);
-        if (n < 2) return 0;
-        seg = (tokens / nseq + n - 1) / n;
-    }
-    seg = std::max<long long>((seg + kC - 1) / kC * kC, kMinSegment);
-    return seg < (packed ? tokens : tokens / nseq) ? (int)seg : 0;
-}
-int ctas_per_slot(int dv, int Hv, int num_scans) { return (dv > kHalf ? 2 : 1) * Hv * num_scans; }
-long long segment_slots(long long tokens, int nseq, int seg) { return seg ? tokens / seg + nseq : nseq; }
-
 }  // namespace
 
-size_t decay_scan_tc_workspace_bytes(int dk, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans) {
-    const int seg = segment_tokens(tokens, nseq, packed, ctas_per_slot(dv, Hv, num_scans));
-    return seg ? (size_t)segment_slots(tokens, nseq, seg) * Hv * num_scans * dk * dv * sizeof(float) : 0;
-}
-
-cudaError_t launch_decay_scan_tc(const DecayArgs& a) {
+cudaError_t launch_decay_tc(const SegArgs& seg, bool state_only) {
+    const DecayArgs& a = seg.a;
     const auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
     if (!encode) return cudaErrorNotSupported;
     cudaError_t e = set_attributes();
     if (e != cudaSuccess) return e;
     TcArgs t;
-    t.a = a;
+    static_cast<SegArgs&>(t) = seg;
     for (int i = 0; i < a.num_scans; ++i) {
         const DecayScan& s = a.scan[i];
         Maps& m = t.maps[i];
@@ -790,18 +670,9 @@ cudaError_t launch_decay_scan_tc(const DecayArgs& a) {
         if ((e = make_map(encode, &m.k, s.k, a.tokens, a.Hv / s.k_div, a.dk, s.k_stride)) != cudaSuccess) return e;
         if ((e = make_map(encode, &m.v, s.v, a.tokens, a.Hv / s.v_div, a.dv, s.v_stride)) != cudaSuccess) return e;
     }
-    t.seg = segment_tokens(a.tokens, a.nseq, a.cu != nullptr, ctas_per_slot(a.dv, a.Hv, a.num_scans));
-    t.slots = (int)segment_slots(a.tokens, a.nseq, t.seg);
-    t.states = static_cast<float*>(a.workspace);
-    const dim3 grid((unsigned)((long long)t.slots * ctas_per_slot(a.dv, a.Hv, 1)), (unsigned)a.num_scans);
-    if (t.seg) {
-        decay_tc_state_kernel<<<grid, kThreads, kSmem, a.stream>>>(t);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        const dim3 join((unsigned)((long long)a.nseq * a.Hv * (a.dk * a.dv / 4 / kJoinThreads)), (unsigned)a.num_scans);
-        decay_tc_join_kernel<<<join, kJoinThreads, 0, a.stream>>>(t);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    decay_tc_kernel<<<grid, kThreads, kSmem, a.stream>>>(t);
+    const dim3 grid((unsigned)((long long)t.slots * a.Hv * (a.dv > kHalf ? 2 : 1)), (unsigned)a.num_scans);
+    if (state_only) decay_tc_state_kernel<<<grid, kThreads, kSmem, a.stream>>>(t);
+    else decay_tc_kernel<<<grid, kThreads, kSmem, a.stream>>>(t);
     return cudaGetLastError();
 }
 

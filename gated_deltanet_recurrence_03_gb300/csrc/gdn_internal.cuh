@@ -198,11 +198,8 @@ struct DecayArgs {
 // differences of exponents into NaN.
 constexpr float kMinLogDecay = -100.f;
 // Device scratch of one launch_decay_scan call, and the launch.
-size_t decay_scan_workspace_bytes(int dtype, int dk, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans);
+size_t decay_scan_workspace_bytes(int dk, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans);
 cudaError_t launch_decay_scan(const DecayArgs& a);
-// The same on the tcgen05 tensor cores, for bf16.
-size_t decay_scan_tc_workspace_bytes(int dk, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans);
-cudaError_t launch_decay_scan_tc(const DecayArgs& a);
 // out[t][hk] = sum over the G value heads of query/key head hk of part[t][hk G + i] (fp32 [tokens][Hqk G][d]),
 // rounded once to the output type, rows out_stride elements apart.
 cudaError_t launch_head_sum(const float* part, void* out, long long out_stride, long long tokens, int Hqk, int G, int d,
