@@ -9,7 +9,7 @@
 // 128-wide head keeps two SMs busy; the two read the same q and k tiles, the second time from L2.  Per chunk
 // four products (M = 128 each):
 //   QK [128 x 128] = Q K^T;   PV [128 x 64] = P V, P = the decayed, masked QK as the bf16 A operand in TMEM;
-//   QS [128 x 64] = Q S_bf16;   KV [dk x 64] = K^T V~, V~ = V scaled by su w and split into three bf16 parts.
+//   QS [128 x 64] = Q S_bf16;   KV [dk x 64] = K^T V~, V~ = V scaled by su w, in three bf16 parts side by side.
 // The state is kept in registers in fp32 (64 columns of one row a thread), so the products of a chunk wait for
 // the state only in QS: KV goes to a fresh accumulator, and S <- w_n S + KV is one FMA per element (with w_n in
 // two floats: one rounding of it would compound over the head's memory).  V~'s three parts hold its fp32 value
@@ -34,7 +34,7 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kC = 128;       // tokens of a chunk
 constexpr int kHalf = kDecayColumns;
-constexpr int kParts = 3;     // bf16 parts of the scaled V
+constexpr int kMaxParts = 3;  // bf16 parts of the scaled V
 
 // Shared memory (bytes from the 1024-aligned base).  Panels: 128 rows x 64 bf16, 128-byte swizzle.
 constexpr uint32_t kPanel = 16384;
@@ -42,7 +42,8 @@ constexpr uint32_t S_Q = 0;                          // 2 stages x 2 panels
 constexpr uint32_t S_K = S_Q + 2 * 2 * kPanel;       // 2 stages x 2 panels
 constexpr uint32_t S_V = S_K + 2 * 2 * kPanel;       // 2 stages x 1 panel
 constexpr uint32_t S_VP = S_V + 2 * kPanel;          // the three parts of the scaled V
-constexpr uint32_t S_SB = S_VP + kParts * kPanel;    // the state in bf16 (128 dk rows); between its uses, the outputs
+constexpr uint32_t S_SB = S_VP + kMaxParts * kPanel; // the state in bf16 (128 dk rows); between its uses, the outputs
+constexpr uint32_t S_OUT = S_VP + 2 * kPanel;        // with two parts: the outputs on their way
 constexpr uint32_t S_BAR = S_SB + kPanel;
 constexpr uint32_t kBarBytes = 256;
 constexpr uint32_t S_PW = S_BAR + kBarBytes;         // w_0 .. w_128
@@ -68,7 +69,7 @@ enum Bar : uint32_t {
     B_COUNT = 20
 };
 
-// TMEM columns (all 512): KV holds the products with V's three parts side by side.
+// TMEM columns (all 512): KV holds the products with V's (up to three) parts side by side.
 constexpr uint32_t T_QK = 0, T_P = 128, T_QS = 192, T_PV = 256, T_KV = 320;
 constexpr uint32_t kTmemCols = 512;
 
@@ -109,19 +110,22 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 as_float2(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
 __device__ __forceinline__ uint32_t pack_bf16(float2 x) { return tc::pack_bf16(x.x, x.y); }
-// x = h + m + l, three bf16 values that hold it exactly: each is x, or what is left of it, cut to eight
-// significant bits, and the differences are exact in fp32.  h gets the pair's two high halves packed.
-__device__ __forceinline__ void split3(float2 x, uint32_t& h, uint32_t& m, uint32_t& l) {
+// x as a sum of bf16 values: each is x, or what is left of it, cut to eight significant bits (the differences are
+// exact in fp32), the last of two rounded.  Three hold x exactly, two to 2^-17.  A pair's two values are packed.
+template <int PARTS>
+__device__ __forceinline__ void split_bf16(float2 x, uint32_t (&part)[PARTS]) {
     constexpr uint32_t kCut = 0xffff0000u, kSign = 0x80000000u;
-    uint32_t a = __float_as_uint(x.x), b = __float_as_uint(x.y);
-    h = __byte_perm(a, b, 0x7632);
-    x = add2(x, make_float2(__uint_as_float((a & kCut) ^ kSign), __uint_as_float((b & kCut) ^ kSign)));
-    a = __float_as_uint(x.x), b = __float_as_uint(x.y);
-    m = __byte_perm(a, b, 0x7632);
-    x = add2(x, make_float2(__uint_as_float((a & kCut) ^ kSign), __uint_as_float((b & kCut) ^ kSign)));
-    l = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+        const uint32_t a = __float_as_uint(x.x), b = __float_as_uint(x.y);
+        if (PARTS == 2 && p == 1) {
+            part[p] = pack_bf16(x);
+        } else {
+            part[p] = __byte_perm(a, b, 0x7632);
+            if (p + 1 < PARTS) x = add2(x, as_float2((a & kCut) ^ kSign, (b & kCut) ^ kSign));
+        }
+    }
 }
-
 // mbar_wait_bounded in fewer instructions, and with each test suspended for up to a millisecond: the roles' loops
 // share the schedulers and one instruction cache, and a polling warp takes both from the others.
 __device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
@@ -148,9 +152,11 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
     return false;
 }
 
-// One scan's CTA.  REV: a reverse scan; F32: the outputs are float; STATE: only a segment's contribution to the
+// One scan's CTA.  REV: a reverse scan; F32: the outputs are float; PARTS: bf16 parts of the scaled V (three where
+// the last state is wanted, which then has fp32 accuracy; two where it only serves the outputs, whose own rounding
+// is 2^-9); STATE: only a segment's contribution to the
 // state, from zeros, no outputs.  (Template arguments, not branches, for the instruction cache's sake.)
-template <bool REV, bool F32, bool STATE>
+template <bool REV, bool F32, int PARTS, bool STATE>
 __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -286,7 +292,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         mma_bf16(tmem + T_KV, kt + ((ks * 2048) >> 4), dVP + ((ks * 2048) >> 4),
-                                 idesc_bf16(128, 64 * kParts, 1, 1), ks > 0);
+                                 idesc_bf16(128, 64 * PARTS, 1, 1), ks > 0);
                     mma_commit(bar(B_KVHALF));
                 }
                 __syncwarp();
@@ -297,7 +303,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
 #pragma unroll
                     for (int ks = 4; ks < 8; ++ks)
                         mma_bf16(tmem + T_KV, kt + ((ks * 2048) >> 4), dVP + ((ks * 2048) >> 4),
-                                 idesc_bf16(128, 64 * kParts, 1, 1), 1);
+                                 idesc_bf16(128, 64 * PARTS, 1, 1), 1);
                     mma_commit(bar(B_KV));
                     if (STATE) mma_commit(bar(B_FREE + st));
                 }
@@ -451,21 +457,22 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const uint32_t y[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-                uint32_t o[kParts][4];
+                uint32_t o[4][PARTS];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    split3(mul2(make_float2(w, w), make_float2(__uint_as_float(y[e] << 16), __uint_as_float(y[e] & 0xffff0000u))),
-                           o[0][e], o[1][e], o[2][e]);
+                    split_bf16<PARTS>(mul2(make_float2(w, w), as_float2(y[e] << 16, y[e] & 0xffff0000u)), o[e]);
 #pragma unroll
-                for (int p = 0; p < kParts; ++p)
-                    *reinterpret_cast<uint4*>(sm + S_VP + p * kPanel + swz(r, c0 + c)) = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
+                for (int p = 0; p < PARTS; ++p)
+                    *reinterpret_cast<uint4*>(sm + S_VP + p * kPanel + swz(r, c0 + c)) = make_uint4(o[0][p], o[1][p], o[2][p], o[3][p]);
             }
             fence_proxy_async_smem();
             arrive(B_VP + half);
             return true;
         };
-        // A chunk's outputs (rows of 128 bytes at a time) pass through the place of the state's copy, which QS has
-        // read: warps w and w + 4 hold the two halves of the same 32 rows, and each writes 16 whole rows.
+        // A chunk's outputs (rows of 128 bytes at a time) pass through the third part's place or, with three parts,
+        // that of the state's copy, which QS has read: warps w and w + 4 hold the two halves of the same 32 rows,
+        // and each writes 16 whole rows.
+        constexpr uint32_t kOut = PARTS == 2 ? S_OUT : S_SB;
         constexpr int esize = F32 ? 4 : 2;
         const int pair = 1 + (warp & 3), own = 32 * (warp & 3) + 4 * c0 + (lane >> 3), chunk = lane & 7;
         uint8_t* const out = static_cast<uint8_t*>(s.out) + ((size_t)h * dv + kHalf * z) * esize +
@@ -493,16 +500,16 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     o[e] = fma2(make_float2(w, w), as_float2(qs[2 * e], qs[2 * e + 1]), as_float2(pv[2 * e], pv[2 * e + 1]));
+                if (F32 || PARTS == 2 && !b) named_barrier_sync(pair, 64);   // the rows staged before have been read
                 if (F32) {
-                    if (b) named_barrier_sync(pair, 64);   // the first 16 columns' rows have been read
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        *reinterpret_cast<float4*>(sm + S_SB + swz(r, c0 + c)) =
+                        *reinterpret_cast<float4*>(sm + kOut + swz(r, c0 + c)) =
                             make_float4(o[2 * c].x, o[2 * c].y, o[2 * c + 1].x, o[2 * c + 1].y);
                 } else {
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
-                        *reinterpret_cast<uint4*>(sm + S_SB + swz(r, c0 + 2 * b + c)) =
+                        *reinterpret_cast<uint4*>(sm + kOut + swz(r, c0 + 2 * b + c)) =
                             make_uint4(pack_bf16(o[4 * c]), pack_bf16(o[4 * c + 1]), pack_bf16(o[4 * c + 2]), pack_bf16(o[4 * c + 3]));
                 }
                 if (F32 || b) {
@@ -511,10 +518,10 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                     for (int x = 0; x < 16; x += 4)
                         if (own + x < n && (F32 ? 32 * (chunk >> 2) + 16 * b + 4 * (chunk & 3) : 8 * chunk) < width)
                             *reinterpret_cast<uint4*>(first + (size_t)(own + x) * pitch + (F32 ? 64 * b : 0)) =
-                                *reinterpret_cast<const uint4*>(sm + S_SB + swz(own + x, chunk));
+                                *reinterpret_cast<const uint4*>(sm + kOut + swz(own + x, chunk));
                 }
             }
-            arrive(B_SBFREE);
+            if (PARTS == 3) arrive(B_SBFREE);
         }
     } else {
         // ------------------------------------------------------------ the state: row R of dk, 64 columns a thread
@@ -566,13 +573,14 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
             tc_fence_after();
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                uint32_t d[kParts][16];
+                uint32_t d[PARTS][16];
 #pragma unroll
-                for (int p = 0; p < kParts; ++p) tmem_ld16(tl + T_KV + 64 * p + 16 * b, d[p]);
+                for (int p = 0; p < PARTS; ++p) tmem_ld16(tl + T_KV + 64 * p + 16 * b, d[p]);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    float2 y = add2(as_float2(d[2][2 * e], d[2][2 * e + 1]), as_float2(d[1][2 * e], d[1][2 * e + 1]));
+                    float2 y = as_float2(d[1][2 * e], d[1][2 * e + 1]);
+                    if (PARTS == 3) y = add2(as_float2(d[PARTS - 1][2 * e], d[PARTS - 1][2 * e + 1]), y);
                     y = add2(y, as_float2(d[0][2 * e], d[0][2 * e + 1]));
                     S[8 * b + e] = fma2(ghi, S[8 * b + e], fma2(glo, S[8 * b + e], y));
                 }
@@ -580,8 +588,8 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
             tc_fence_before();
             arrive(B_KVFREE);
             if (!STATE && it + 1 < nch) {
-                // QS has read the copy of the state, and the outputs have passed through its place
-                if (!(ok = wait(B_SBFREE, it))) break;
+                // QS has read the copy of the state, and the outputs (with three parts) have passed through its place
+                if (!(ok = wait(PARTS == 3 ? B_SBFREE : B_O, it))) break;
                 write_sb();
             }
         }
@@ -605,20 +613,23 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
 __global__ void __launch_bounds__(kThreads, 1)
 decay_tc_kernel(const __grid_constant__ TcArgs ta) {
     const DecayScan& s = ta.a.scan[blockIdx.y];
-    if (s.reverse) {
-        if (s.out_f32) decay_tc_body<true, true, false>(ta);
-        else decay_tc_body<true, false, false>(ta);
+    if (s.out_f32) {   // a part of a sum over shared heads: no state is asked of such a scan
+        if (s.reverse) decay_tc_body<true, true, 2, false>(ta);
+        else decay_tc_body<false, true, 2, false>(ta);
+    } else if (s.final) {
+        if (s.reverse) decay_tc_body<true, false, 3, false>(ta);
+        else decay_tc_body<false, false, 3, false>(ta);
     } else {
-        if (s.out_f32) decay_tc_body<false, true, false>(ta);
-        else decay_tc_body<false, false, false>(ta);
+        if (s.reverse) decay_tc_body<true, false, 2, false>(ta);
+        else decay_tc_body<false, false, 2, false>(ta);
     }
 }
 
 // Segments, first: what each adds to the state.
 __global__ void __launch_bounds__(kThreads, 1)
 decay_tc_state_kernel(const __grid_constant__ TcArgs ta) {
-    if (ta.a.scan[blockIdx.y].reverse) decay_tc_body<true, false, true>(ta);
-    else decay_tc_body<false, false, true>(ta);
+    if (ta.a.scan[blockIdx.y].reverse) decay_tc_body<true, false, 3, true>(ta);
+    else decay_tc_body<false, false, 3, true>(ta);
 }
 
 // ------------------------------------------------------------------ host side
