@@ -539,17 +539,22 @@ def gdn_output_gate_bwd(o: torch.Tensor, z: torch.Tensor, norm_weight: torch.Ten
     return go, gz, gw
 
 
-def _token_rows(name, t, lead):
-    """Elements between consecutive token rows of t ([*lead, heads, features] with contiguous heads, token
-    rows evenly strided: a dense tensor or a slice of a packed projection)."""
-    d, H = t.shape[-1], t.shape[-2]
-    ok = t.stride(-1) == 1 and (H == 1 or t.stride(-2) == d)
-    row = t.stride(-3) if t.shape[-3] > 1 else (t.stride(0) if lead == 2 and t.shape[0] > 1 else H * d)
-    if ok and lead == 2 and t.shape[0] > 1:
-        ok = t.stride(0) == t.shape[1] * row
-    if t.numel() and not ok:
+def _token_rows(name, t, d, lead):
+    """Elements between consecutive token rows of t ([*lead, heads, d] with contiguous heads, token rows evenly
+    strided: a dense tensor or a slice of a packed projection)."""
+    shape, stride = t.shape, t.stride()
+    H = shape[lead]
+    if lead == 1:
+        row = stride[0] if shape[0] > 1 else H * d
+        even = True
+    else:
+        row = stride[1] if shape[1] > 1 else stride[0] if shape[0] > 1 else H * d
+        even = shape[0] <= 1 or stride[0] == shape[1] * row
+    if even and stride[lead + 1] == 1 and (H == 1 or stride[lead] == d):
+        return row
+    if t.numel():
         raise ValueError(f"{name} must have contiguous heads and evenly strided token rows")
-    return row if t.numel() else H * d
+    return H * d
 
 
 def _decay_inputs(q, k, v, log_decay, lead):
@@ -559,28 +564,30 @@ def _decay_inputs(q, k, v, log_decay, lead):
             raise TypeError(f"{name} must be a tensor")
         if t.dim() != lead + 2:
             raise ValueError(f"{name} must be {lead + 2}-D [{'B, T' if lead == 2 else 'N'}, H, d]")
-    dev, dt = q.device, q.dtype
+    dev, dt, qs, vs = q.device, q.dtype, q.shape, v.shape
     if dt not in _DTYPES:
         raise ValueError(f"unsupported dtype {dt}")
-    if k.shape != q.shape:
-        raise ValueError(f"k has shape {tuple(k.shape)}, expected {tuple(q.shape)}")
-    if v.shape[:lead] != q.shape[:lead]:
-        raise ValueError(f"v has shape {tuple(v.shape)}, expected leading {tuple(q.shape[:lead])}")
-    for name, t in (("k", k), ("v", v)):
-        if t.device != dev or t.dtype != dt:
-            raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {dt} on {dev}")
-    Hqk, dk = q.shape[-2:]
-    Hv, dv = v.shape[-2:]
+    if k.shape != qs:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected {tuple(qs)}")
+    if vs[0] != qs[0] or vs[lead - 1] != qs[lead - 1]:
+        raise ValueError(f"v has shape {tuple(vs)}, expected leading {tuple(qs[:lead])}")
+    if k.dtype is not dt or v.dtype is not dt or k.device != dev or v.device != dev:
+        raise ValueError(f"q, k, v must have one type and device: {dt} on {dev}, {k.dtype} on {k.device}, "
+                         f"{v.dtype} on {v.device}")
+    Hqk, dk = qs[lead], qs[lead + 1]
+    Hv, dv = vs[lead], vs[lead + 1]
     _need("log_decay", log_decay, torch.float32, dev, (Hv,))
-    return dev, dt, Hqk, Hv, dk, dv, tuple(_token_rows(n, t, lead) for n, t in (("q", q), ("k", k), ("v", v)))
+    return dev, dt, Hqk, Hv, dk, dv, (_token_rows("q", q, dk, lead), _token_rows("k", k, dk, lead),
+                                      _token_rows("v", v, dv, lead))
 
 
-def _scratch(o, need, workspace, dev):
-    """Point the options at a workspace of at least ``need`` bytes; returns the tensor to keep alive."""
+def _scratch(o, need, workspace, like):
+    """Point the options at a workspace of at least ``need`` bytes (a new one: fp32 on the device of ``like``, an
+    fp32 tensor); returns the tensor to keep alive."""
     if not need:
         return None
     if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = like.new_empty((need + 3) // 4)
     o.workspace = workspace.data_ptr()
     o.workspace_bytes = workspace.numel() * workspace.element_size()
     return workspace
@@ -619,15 +626,15 @@ def gdn_decay_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
         if S0 is not None:
             _need("S0", S0, torch.float32, dev, (nseq, Hv, dk, dv))
         if out is None:
-            out = torch.empty((B, T, Hv, dv), dtype=dt, device=dev)
+            out = v.new_empty(v.shape)
         else:
             _need("out", out, dt, dev, (B, T, Hv, dv))
         if S_final is not None:
             _need("S_final", S_final, torch.float32, dev, (nseq, Hv, dk, dv))
         elif output_final_state:
-            S_final = torch.empty((nseq, Hv, dk, dv), dtype=torch.float32, device=dev)
+            S_final = log_decay.new_empty((nseq, Hv, dk, dv))
         workspace = _scratch(o, int(lib.gdn_decay_attn_fwd_workspace_size(B, T, Hqk, Hv, dk, dv, ctypes.byref(o))),
-                             workspace, dev)
+                             workspace, log_decay)
         st = lib.gdn_decay_attn_fwd(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], _ptr(log_decay),
                                     _ptr(S0), _ptr(out), _ptr(S_final), B, T, Hqk, Hv, dk, dv, ctypes.byref(o))
         del keep
@@ -651,7 +658,7 @@ def gdn_decay_attn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_d
     if slots is not None:
         _need("slots", slots, torch.int32, dev, (N,))
     if out is None:
-        out = torch.empty((N, Hv, dv), dtype=dt, device=dev)
+        out = v.new_empty(v.shape)
     else:
         _need("out", out, dt, dev, (N, Hv, dv))
     with _on(dev):
@@ -678,20 +685,21 @@ def gdn_decay_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
     B, T = q.shape[:2]
     _need("grad_out", grad_out, dt, dev, (B, T, Hv, dv))
     if grads is None:
-        grads = tuple(torch.empty(t.shape, dtype=dt, device=dev) for t in (q, k, v))
-    for name, g, t in zip(("grad_q", "grad_k", "grad_v"), grads, (q, k, v)):
-        if g.shape != t.shape or g.dtype != dt or g.device != dev:
-            raise ValueError(f"{name} must be {dt} of shape {tuple(t.shape)} on {dev}")
-    gstrides = tuple(_token_rows(n, g, 2) for n, g in zip(("grad_q", "grad_k", "grad_v"), grads))
+        grads = (q.new_empty(q.shape), k.new_empty(k.shape), v.new_empty(v.shape))
+    else:
+        for name, g, t in zip(("grad_q", "grad_k", "grad_v"), grads, (q, k, v)):
+            if g.shape != t.shape or g.dtype != dt or g.device != dev:
+                raise ValueError(f"{name} must be {dt} of shape {tuple(t.shape)} on {dev}")
+    gstrides = tuple(_token_rows(n, g, g.shape[3], 2) for n, g in zip(("grad_q", "grad_k", "grad_v"), grads))
     with _on(dev):
         o, keep = _call_opts(lib, dt, scale, stream, dev, events)
         nseq = _packed(o, cu_seqlens, B, dev)
         for name, t in (("S0", S0), ("grad_S_final", grad_S_final)):
             if t is not None:
                 _need(name, t, torch.float32, dev, (nseq, Hv, dk, dv))
-        gS0 = torch.empty((nseq, Hv, dk, dv), dtype=torch.float32, device=dev) if want_grad_S0 else None
+        gS0 = log_decay.new_empty((nseq, Hv, dk, dv)) if want_grad_S0 else None
         workspace = _scratch(o, int(lib.gdn_decay_attn_bwd_workspace_size(B, T, Hqk, Hv, dk, dv, ctypes.byref(o))),
-                             workspace, dev)
+                             workspace, log_decay)
         st = lib.gdn_decay_attn_bwd(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], _ptr(log_decay),
                                     _ptr(S0), _ptr(grad_out), _ptr(grad_S_final), _ptr(grads[0]), gstrides[0],
                                     _ptr(grads[1]), gstrides[1], _ptr(grads[2]), gstrides[2], _ptr(gS0), B, T, Hqk, Hv,
@@ -730,9 +738,12 @@ def gdn_block_norm_fwd(x: torch.Tensor, b: torch.Tensor, post_weight: torch.Tens
     Returns (r, n)."""
     lib = L.load()
     dev, dt, shape, D, rows, cols = _block_norm_inputs(x, b, post_weight, pre_weight, gate, res_scale)
-    r, n = (torch.empty_like(x), torch.empty_like(x)) if out is None else out
-    _need("r", r, dt, dev, shape)
-    _need("n", n, dt, dev, shape)
+    if out is None:
+        r, n = torch.empty_like(x), torch.empty_like(x)
+    else:
+        r, n = out
+        _need("r", r, dt, dev, shape)
+        _need("n", n, dt, dev, shape)
     with _on(dev):
         o, keep = _call_opts(lib, dt, 1.0, stream, dev, events)
         o.norm_eps = float(eps)
@@ -756,15 +767,17 @@ def gdn_block_norm_bwd(x: torch.Tensor, b: torch.Tensor, post_weight: torch.Tens
     _need("grad_n", grad_n, dt, dev, shape)
     gx, gb = torch.empty_like(x), torch.empty_like(x)
     gg = None if gate is None else torch.empty_like(gate)
-    sums = torch.empty((3 if res_scale is not None else 2, D), dtype=torch.float32, device=dev)
-    gs = sums[2] if res_scale is not None else None
+    sums = post_weight.new_empty((2 if res_scale is None else 3, D))
+    at = sums.data_ptr()
     with _on(dev):
         o, keep = _call_opts(lib, dt, 1.0, stream, dev, events)
         o.norm_eps = float(eps)
-        ws = _scratch(o, int(lib.gdn_block_norm_bwd_workspace_size(rows, D, ctypes.byref(o))), None, dev)
+        ws = _scratch(o, int(lib.gdn_block_norm_bwd_workspace_size(rows, D, ctypes.byref(o))), None, post_weight)
         st = lib.gdn_block_norm_bwd(_ptr(x), _ptr(b), _ptr(gate), cols, _ptr(res_scale), _ptr(post_weight),
                                     _ptr(pre_weight), _ptr(grad_r), _ptr(grad_n), _ptr(gx), _ptr(gb), _ptr(gg),
-                                    _ptr(sums[0]), _ptr(sums[1]), _ptr(gs), rows, D, ctypes.byref(o))
+                                    at, at + 4 * D, None if res_scale is None else at + 8 * D, rows, D,
+                                    ctypes.byref(o))
         del keep, ws
         L.check(lib, st)
-    return gx, gb, sums[0], sums[1], gg, gs
+    gpost, gpre, *gs = sums.unbind(0)
+    return gx, gb, gpost, gpre, gg, gs[0] if gs else None

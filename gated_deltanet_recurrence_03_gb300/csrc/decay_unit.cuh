@@ -55,6 +55,37 @@ __device__ __forceinline__ float* unit_state(const SegArgs& ta, int scan, int sl
     return ta.states + (((size_t)scan * ta.slots + slot) * ta.a.Hv + h) * ta.a.dk * ta.a.dv;
 }
 
+// exp(g n) as hi + lo, to 2^-45 near 1 and 2^-31 at exp(-8): one rounding of a chunk's decay would compound over
+// the head's memory.  (Below exp(-12) a chunk forgets nearly all and one float does.)  From the series on y = g n / 2^s with
+// |y| <= 2^-10, then s squarings of 1 + e in two floats, (1 + e)^2 - 1 = 2 e + e^2.  (In fp64 the same takes ten
+// times as long on this chip.)
+__device__ __forceinline__ void decay_power(float g, float n, float& hi, float& lo) {
+    float xh = g * n, xl = fmaf(g, n, -xh);
+    if (xh < -12.f) {
+        hi = expf(xh);
+        lo = 0.f;
+        return;
+    }
+    int s = 0;
+    while (fabsf(xh) > 0.0009765625f) {   // exact halvings
+        xh *= 0.5f;
+        xl *= 0.5f;
+        ++s;
+    }
+    const float p = xh * xh * fmaf(xh, fmaf(xh, 0.041666668f, 0.16666667f), 0.5f);
+    float eh = xh + p, el = (p - (eh - xh)) + xl;
+    for (; s > 0; --s) {
+        const float sq = eh * eh, a = 2.f * eh, t = a + sq;
+        el = (sq - (t - a)) + (fmaf(eh, eh, -sq) + fmaf(2.f * eh, el, 2.f * el));
+        eh = t;
+    }
+    hi = 1.f + eh;
+    lo = (eh - (hi - 1.f)) + el;
+    const float t = hi + lo;
+    lo -= t - hi;
+    hi = t;
+}
+
 // The scan's main kernel (state_only = false), or the pass before it that forms every segment's own contribution to
 // the state, on the tensor cores (bf16) and on the CUDA cores (fp32).
 cudaError_t launch_decay_tc(const SegArgs& s, bool state_only);

@@ -662,15 +662,15 @@ bool decay_sequences(int B, int T, const gdn_opts_t& o, int* nseq, gdn_status_t*
 struct DecayBwdLayout {
     size_t dq, dk, scan, total;
 };
-DecayBwdLayout decay_bwd_layout(long long tokens, int Hqk, int Hv, int dk, int dv, int nseq,
+DecayBwdLayout decay_bwd_layout(int dtype, long long tokens, int Hqk, int Hv, int dk, int dv, int nseq,
                                 bool packed) {
     DecayBwdLayout l{};
     const size_t part = Hv > Hqk ? ((size_t)tokens * Hv * dk * 4 + 255) / 256 * 256 : 0;
     l.dk = part;
     l.scan = 2 * part;
-    const size_t scan = dk == dv ? decay_scan_workspace_bytes(dk, dv, Hv, nseq, tokens, packed, 3)
-                                 : std::max(decay_scan_workspace_bytes(dv, dk, Hv, nseq, tokens, packed, 2),
-                                            decay_scan_workspace_bytes(dk, dv, Hv, nseq, tokens, packed, 1));
+    const size_t scan = dk == dv ? decay_scan_workspace_bytes(dtype, dk, dv, Hv, nseq, tokens, packed, 3)
+                                 : std::max(decay_scan_workspace_bytes(dtype, dv, dk, Hv, nseq, tokens, packed, 2),
+                                            decay_scan_workspace_bytes(dtype, dk, dv, Hv, nseq, tokens, packed, 1));
     l.total = l.scan + scan;
     return l;
 }
@@ -683,7 +683,7 @@ size_t gdn_decay_attn_fwd_workspace_size(int B, int T, int Hqk, int Hv, int dk, 
     const gdn_opts_t o = resolve(opts);
     if (B <= 0 || T <= 0 || Hqk <= 0 || Hv <= 0 || Hv % Hqk || !dim_ok(dk) || !dim_ok(dv)) return 0;
     const int nseq = o.cu_seqlens ? o.num_seqs : B;
-    return nseq > 0 ? decay_scan_workspace_bytes(dk, dv, Hv, nseq, (long long)B * T, o.cu_seqlens != nullptr, 1) : 0;
+    return nseq > 0 ? decay_scan_workspace_bytes(o.dtype, dk, dv, Hv, nseq, (long long)B * T, o.cu_seqlens != nullptr, 1) : 0;
 }
 
 gdn_status_t gdn_decay_attn_fwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
@@ -700,7 +700,7 @@ gdn_status_t gdn_decay_attn_fwd(const void* q, long long q_stride, const void* k
         return fail(GDN_ERR_INVALID_ARG, "null input/output pointer");
     if ((st = need_aligned16({q, k, v, S0, out, S_final})) != GDN_OK) return st;
     if (nseq == 0) return GDN_OK;
-    const size_t need = have_tokens ? decay_scan_workspace_bytes(dk, dv, Hv, nseq, (long long)B * T, o.cu_seqlens != nullptr, 1) : 0;
+    const size_t need = have_tokens ? decay_scan_workspace_bytes(o.dtype, dk, dv, Hv, nseq, (long long)B * T, o.cu_seqlens != nullptr, 1) : 0;
     if ((st = need_workspace(o, need)) != GDN_OK) return st;
     unsigned* status = nullptr;
     if ((st = device_ready(&status)) != GDN_OK) return st;
@@ -758,7 +758,7 @@ size_t gdn_decay_attn_bwd_workspace_size(int B, int T, int Hqk, int Hv, int dk, 
     const gdn_opts_t o = resolve(opts);
     if (B <= 0 || T <= 0 || Hqk <= 0 || Hv <= 0 || Hv % Hqk || !dim_ok(dk) || !dim_ok(dv)) return 0;
     const int nseq = o.cu_seqlens ? o.num_seqs : B;
-    return nseq > 0 ? decay_bwd_layout((long long)B * T, Hqk, Hv, dk, dv, nseq, o.cu_seqlens != nullptr).total : 0;
+    return nseq > 0 ? decay_bwd_layout(o.dtype, (long long)B * T, Hqk, Hv, dk, dv, nseq, o.cu_seqlens != nullptr).total : 0;
 }
 
 gdn_status_t gdn_decay_attn_bwd(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
@@ -779,7 +779,7 @@ gdn_status_t gdn_decay_attn_bwd(const void* q, long long q_stride, const void* k
     if ((st = need_aligned16({q, k, v, S0, grad_out, grad_S_final, grad_q, grad_k, grad_v, grad_S0})) != GDN_OK) return st;
     if (nseq == 0) return GDN_OK;
     const long long tokens = (long long)B * T;
-    const DecayBwdLayout l = have_tokens ? decay_bwd_layout(tokens, Hqk, Hv, dk, dv, nseq, o.cu_seqlens != nullptr) : DecayBwdLayout{};
+    const DecayBwdLayout l = have_tokens ? decay_bwd_layout(o.dtype, tokens, Hqk, Hv, dk, dv, nseq, o.cu_seqlens != nullptr) : DecayBwdLayout{};
     if ((st = need_workspace(o, l.total)) != GDN_OK) return st;
     unsigned* status = nullptr;
     if ((st = device_ready(&status)) != GDN_OK) return st;

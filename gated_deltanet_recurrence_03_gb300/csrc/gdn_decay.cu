@@ -20,10 +20,8 @@ __global__ void __launch_bounds__(kJoinThreads) decay_join_kernel(const __grid_c
     const int n = (int)max(1LL, (s1 - s0 + ta.seg - 1) / ta.seg), slot0 = (int)(s0 / ta.seg) + i;
     __shared__ float w[4];   // the decay over a whole and over the last segment, in two floats each
     if (threadIdx.x < 2) {
-        const double len = threadIdx.x ? (double)(s1 - s0 - (long long)(n - 1) * ta.seg) : (double)ta.seg;
-        const double x = exp((double)fmaxf(a.log_decay[h], kMinLogDecay) * len);
-        w[2 * threadIdx.x] = (float)x;
-        w[2 * threadIdx.x + 1] = (float)(x - (double)(float)x);
+        const long long len = threadIdx.x ? s1 - s0 - (long long)(n - 1) * ta.seg : ta.seg;
+        decay_power(fmaxf(a.log_decay[h], kMinLogDecay), (float)len, w[2 * threadIdx.x], w[2 * threadIdx.x + 1]);
     }
     __syncthreads();
     const int e = (part * kJoinThreads + threadIdx.x) * 4, row = e / dv, col = e % dv;
@@ -75,9 +73,9 @@ __global__ void head_sum_kernel(const float* __restrict__ part, T* __restrict__ 
 // plus that of the pass that forms the segments' parts of the state (under half of the main pass a chunk).  So
 // sequences are cut where at least two segments of each find an SM of their own; the lengths of packed sequences
 // are not known here, and their total is cut instead (a sequence shorter than that is one segment).  Segments
-// shorter than kMinSegment would be mostly start-up.
-constexpr int kSms = 152, kMinSegment = 1024;
-int segment_tokens(long long tokens, int nseq, bool packed, int ctas) {
+// shorter than eight chunks of their kernel would be mostly start-up.
+constexpr int kSms = 152;
+int segment_tokens(long long tokens, int nseq, bool packed, int ctas, int min_segment) {
     long long seg;
     if (packed) {
         if (ctas * 2 > kSms) return 0;
@@ -87,30 +85,30 @@ int segment_tokens(long long tokens, int nseq, bool packed, int ctas) {
         if (n < 2) return 0;
         seg = (tokens / nseq + n - 1) / n;
     }
-    seg = std::max<long long>((seg + 127) / 128 * 128, kMinSegment);
+    seg = std::max<long long>((seg + 127) / 128 * 128, min_segment);
     return seg < (packed ? tokens : tokens / nseq) ? (int)seg : 0;
 }
 long long segment_slots(long long tokens, int nseq, int seg) { return seg ? tokens / seg + nseq : nseq; }
 
 
 // Segment tokens and slots of a call, and the bytes of its segments' states.
-SegArgs plan_of(int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans) {
+SegArgs plan_of(int dtype, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans) {
     SegArgs p{};
     const int ctas = (dv > kDecayColumns ? dv / kDecayColumns : 1) * Hv * num_scans;   // of one slot
-    p.seg = segment_tokens(tokens, nseq, packed, ctas);
+    p.seg = segment_tokens(tokens, nseq, packed, ctas, dtype == GDN_BF16 ? 1024 : 256);
     p.slots = (int)segment_slots(tokens, nseq, p.seg);
     return p;
 }
 
 }  // namespace
 
-size_t decay_scan_workspace_bytes(int dk, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans) {
-    const SegArgs p = plan_of(dv, Hv, nseq, tokens, packed, num_scans);
+size_t decay_scan_workspace_bytes(int dtype, int dk, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans) {
+    const SegArgs p = plan_of(dtype, dv, Hv, nseq, tokens, packed, num_scans);
     return p.seg ? (size_t)p.slots * Hv * num_scans * dk * dv * sizeof(float) : 0;
 }
 
 cudaError_t launch_decay_scan(const DecayArgs& a) {
-    SegArgs p = plan_of(a.dv, a.Hv, a.nseq, a.tokens, a.cu != nullptr, a.num_scans);
+    SegArgs p = plan_of(a.dtype, a.dv, a.Hv, a.nseq, a.tokens, a.cu != nullptr, a.num_scans);
     p.a = a;
     p.states = static_cast<float*>(a.workspace);
     const auto pass = a.dtype == GDN_BF16 ? launch_decay_tc : launch_decay_f32;

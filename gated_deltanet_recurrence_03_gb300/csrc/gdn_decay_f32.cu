@@ -15,6 +15,7 @@ namespace gdn {
 namespace {
 
 constexpr int kC = 32, kNT = 256;
+constexpr long long kFewCtas = 76;   // half of the 152 SMs
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     uint64_t d;
@@ -71,11 +72,7 @@ decay_f32_kernel(const __grid_constant__ SegArgs ta) {
     const int len = (int)(unit.t1 - unit.t0), nch = (len + kC - 1) / kC, tail = len - (nch - 1) * kC;
     const float g = fmaxf(a.log_decay[h], kMinLogDecay);
     if (tid <= kC) pw[tid] = expf(g * (float)tid);
-    if (tid < 2) {   // the decay of a full and of the last chunk, in two floats: one rounding would compound
-        const double w = exp((double)g * (tid ? tail : kC));
-        pw[34 + 2 * tid] = (float)w;
-        pw[35 + 2 * tid] = (float)(w - (double)(float)w);
-    }
+    if (tid < 2) decay_power(g, (float)(tid ? tail : kC), pw[34 + 2 * tid], pw[35 + 2 * tid]);   // of a full, of the last chunk
     const size_t base = ((size_t)unit.seq * a.Hv + h) * DK * a.dv;
     const float* const init = STATE ? nullptr : ta.seg ? unit_state(ta, blockIdx.y, slot, h) : s.init ? s.init + base : nullptr;
     float* const final = STATE ? unit_state(ta, blockIdx.y, slot, h) : s.final && unit.last ? s.final + base : nullptr;
@@ -275,7 +272,12 @@ cudaError_t launch_typed(const SegArgs& s, bool state_only) {
 }  // namespace
 
 cudaError_t launch_decay_f32(const SegArgs& s, bool state_only) {
-    const int dk = s.a.dk, dv = s.a.dv < kDecayColumns ? s.a.dv : kDecayColumns;
+    // 32 columns a CTA where 64 would leave half of the SMs without one: the scores are then formed twice, but by
+    // SMs that would idle.  (Taken up to twice as many CTAs as SMs it measured 67 us against 45 us on the packed
+    // backward of 1344 tokens, 8 heads of 64.)
+    const int dk = s.a.dk;
+    const long long ctas = (long long)s.slots * s.a.Hv * s.a.num_scans * ((s.a.dv + 63) / 64);
+    const int dv = s.a.dv < kDecayColumns || ctas < kFewCtas ? 32 : kDecayColumns;
 #define GDN_DECAY_CASE(DK_, DV_) \
     if (dk == DK_ && dv == DV_) return launch_typed<DK_, DV_>(s, state_only);
     GDN_DECAY_CASE(32, 32) GDN_DECAY_CASE(64, 32) GDN_DECAY_CASE(128, 32)

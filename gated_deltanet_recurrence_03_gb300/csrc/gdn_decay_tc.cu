@@ -250,11 +250,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
             prefetch(2);
             prefetch(3);
 #pragma unroll 1
-            for (int x = 0; x < 2; ++x) {   // the decay of a full and of the last chunk, in two floats
-                const double w = exp((double)g * (x ? tail : kC));
-                gamma[2 * x] = (float)w;
-                gamma[2 * x + 1] = (float)(w - (double)(float)w);
-            }
+            for (int x = 0; x < 2; ++x) decay_power(g, (float)(x ? tail : kC), gamma[2 * x], gamma[2 * x + 1]);   // of a full, of the last chunk
             mbar_arrive(bar(B_GAMMA));
             for (; loaded < nch; ++loaded) {   // into the stage of the chunk two back
                 if (!wait(B_FREE + (loaded & 1), (loaded >> 1) - 1)) break;

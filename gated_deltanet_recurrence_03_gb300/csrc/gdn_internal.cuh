@@ -198,7 +198,7 @@ struct DecayArgs {
 // differences of exponents into NaN.
 constexpr float kMinLogDecay = -100.f;
 // Device scratch of one launch_decay_scan call, and the launch.
-size_t decay_scan_workspace_bytes(int dk, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans);
+size_t decay_scan_workspace_bytes(int dtype, int dk, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans);
 cudaError_t launch_decay_scan(const DecayArgs& a);
 // out[t][hk] = sum over the G value heads of query/key head hk of part[t][hk G + i] (fp32 [tokens][Hqk G][d]),
 // rounded once to the output type, rows out_stride elements apart.
