@@ -70,18 +70,19 @@ __global__ void head_sum_kernel(const float* __restrict__ part, T* __restrict__ 
 
 // Tokens of a segment, 0 for whole sequences.  One CTA walks one slot, so a call of few sequences and heads leaves most
 // of the card idle and is bound by its longest sequence; in n segments a sequence takes 1 / n of its chunks' time
-// plus that of the pass that forms the segments' parts of the state (under half of the main pass a chunk).  So
-// sequences are cut where at least two segments of each find an SM of their own; the lengths of packed sequences
+// plus that of the pass that forms the segments' parts of the state (a third of the main pass).  So sequences are cut
+// where at least two segments of each find one of the card's `places` of their own; the lengths of packed sequences
 // are not known here, and their total is cut instead (a sequence shorter than that is one segment).  Segments
-// shorter than eight chunks of their kernel would be mostly start-up.
-constexpr int kSms = 152;
-int segment_tokens(long long tokens, int nseq, bool packed, int ctas, int min_segment) {
+// shorter than four chunks of their kernel would be mostly start-up.  Measured: 46,546 packed tokens (one sequence
+// of 40,961) of 6 heads of 128, bf16: 709 us whole, 185 us in 3712-token segments; 1212 tokens of 13 heads: 55 us
+// with 1024 tokens as the least, 46 us with 512.
+int segment_tokens(long long tokens, int nseq, bool packed, int ctas, int places, int min_segment) {
     long long seg;
     if (packed) {
-        if (ctas * 2 > kSms) return 0;
-        seg = (tokens * ctas + kSms - 1) / kSms;
+        if (ctas * 2 > places) return 0;
+        seg = (tokens * ctas + places - 1) / places;
     } else {
-        const long long n = kSms / ((long long)nseq * ctas);
+        const long long n = places / ((long long)nseq * ctas);
         if (n < 2) return 0;
         seg = (tokens / nseq + n - 1) / n;
     }
@@ -95,7 +96,9 @@ long long segment_slots(long long tokens, int nseq, int seg) { return seg ? toke
 SegArgs plan_of(int dtype, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans) {
     SegArgs p{};
     const int ctas = (dv > kDecayColumns ? dv / kDecayColumns : 1) * Hv * num_scans;   // of one slot
-    p.seg = segment_tokens(tokens, nseq, packed, ctas, dtype == GDN_BF16 ? 1024 : 256);
+    // the tensor-core kernel fills an SM and takes 128 tokens a chunk, the fp32 one shares an SM with another
+    p.seg = dtype == GDN_BF16 ? segment_tokens(tokens, nseq, packed, ctas, 152, 512)
+                              : segment_tokens(tokens, nseq, packed, ctas, 304, 128);
     p.slots = (int)segment_slots(tokens, nseq, p.seg);
     return p;
 }

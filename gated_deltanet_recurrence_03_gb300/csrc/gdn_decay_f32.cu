@@ -142,16 +142,16 @@ decay_f32_kernel(const __grid_constant__ SegArgs ta) {
         float2 O[L::OR][2];
         if (!STATE) {
             {   // P, two rows by two columns a thread
-                const int r0 = tid / 16 * 2, j0 = tid % 16 * 2;
+                const int r0 = tid / 16 * 2, j0 = tid % 16;   // columns j0 and j0 + 16: k rows on different banks
                 float2 acc[2][2] = {{all2(0.f), all2(0.f)}, {all2(0.f), all2(0.f)}};
-                if (rev ? j0 + 1 >= r0 : j0 <= r0 + 1) {
+                if (rev ? j0 + 16 >= r0 : j0 <= r0 + 1) {
 #pragma unroll 4
                     for (int c = 0; c < DK; c += 4) {
                         float4 x[2], y[2];
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             x[u] = *reinterpret_cast<const float4*>(Q + (r0 + u) * L::LK + c);
-                            y[u] = *reinterpret_cast<const float4*>(K + (j0 + u) * L::LK + c);
+                            y[u] = *reinterpret_cast<const float4*>(K + (j0 + 16 * u) * L::LK + c);
                         }
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
@@ -164,13 +164,12 @@ decay_f32_kernel(const __grid_constant__ SegArgs ta) {
                 }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    float y[2];
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
-                        const int d = rev ? j0 + v - r0 - u : r0 + u - j0 - v;
-                        y[v] = d >= 0 ? s.so * s.su * pw[max(d, 0)] * (acc[u][v].x + acc[u][v].y) : 0.f;
+                        const int d = rev ? j0 + 16 * v - r0 - u : r0 + u - j0 - 16 * v;
+                        P[(r0 + u) * L::LP + j0 + 16 * v] =
+                            d >= 0 ? s.so * s.su * pw[max(d, 0)] * (acc[u][v].x + acc[u][v].y) : 0.f;
                     }
-                    *reinterpret_cast<float2*>(P + (r0 + u) * L::LP + j0) = make_float2(y[0], y[1]);
                 }
             }
             if (rg < L::OT) {   // Q S, then its row factors
