@@ -43,6 +43,7 @@ constexpr uint32_t S_K = S_Q + 2 * 2 * kPanel;       // 2 stages x 2 panels
 constexpr uint32_t S_V = S_K + 2 * 2 * kPanel;       // 2 stages x 1 panel
 constexpr uint32_t S_VP = S_V + 2 * kPanel;          // the three parts of the scaled V
 constexpr uint32_t S_SB = S_VP + kMaxParts * kPanel; // the state in bf16 (128 dk rows); between its uses, the outputs
+constexpr uint32_t S_SLOW = S_V + kPanel;            // one chunk only: the state copy's second part
 constexpr uint32_t S_OUT = S_VP + 2 * kPanel;        // with two parts: the outputs on their way
 constexpr uint32_t S_BAR = S_SB + kPanel;
 constexpr uint32_t kBarBytes = 256;
@@ -152,12 +153,16 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
     return false;
 }
 
+__device__ __forceinline__ int slot_of(const DecayArgs& a) { return blockIdx.x / (a.dv > kHalf ? 2 : 1) / a.Hv; }
+
 // One scan's CTA.  REV: a reverse scan; F32: the outputs are float; PARTS: bf16 parts of the scaled V (three where
 // the last state is wanted, which then has fp32 accuracy; two where it only serves the outputs, whose own rounding
-// is 2^-9); STATE: only a segment's contribution to the
-// state, from zeros, no outputs.  (Template arguments, not branches, for the instruction cache's sake.)
-template <bool REV, bool F32, int PARTS, bool STATE>
-__device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
+// is 2^-9); STATE: only a segment's contribution to the state, from zeros, no outputs; FINE: one chunk or none, with P
+// and the state's copy in two bf16 parts each: an output of few tokens is a sum of few roundings, up to 1.7 times the
+// output type's own where one score rules it, and a lone chunk has the time (the same 15 us a call).  (Template
+// arguments, not branches, for the instruction cache's sake.)
+template <bool REV, bool F32, int PARTS, bool STATE, bool FINE>
+__device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(sm);
@@ -174,13 +179,10 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
     const int dk = a.dk, dv = a.dv;
     const int zs = dv > kHalf ? 2 : 1, z = blockIdx.x % zs;   // 64-column parts of the values: this CTA's
     const int h = blockIdx.x / zs % a.Hv;
-    const int slot = blockIdx.x / zs / a.Hv;
+    const int slot = slot_of(a);
     const int width = min(kHalf, dv - kHalf * z);             // 32 where dv = 32: the tile's other columns are zeros
     const int steps = dk / 16, panels = dk > 64 ? 2 : 1;      // of q and k rows (32-wide ones lie in 64-wide panels)
     constexpr bool rev = REV;
-    Unit unit;
-    if (!unit_of(ta, slot, rev, unit)) return;
-    if (STATE && unit.last) return;   // nothing comes after it
     const long long t0 = unit.t0, t1 = unit.t1;
     const int nch = (int)((t1 - t0 + kC - 1) / kC);
     const int tail = (int)(t1 - t0) - (nch - 1) * kC;   // valid tokens of the last chunk
@@ -339,6 +341,14 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                         mma_bf16(tmem + T_QS, q + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4), dSB + ((ks * 2048) >> 4),
                                  idesc_bf16(128, 64, 0, 1), ks > 0);
                     }
+                    if (FINE) {
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks) {
+                            if (ks >= steps) break;
+                            mma_bf16(tmem + T_QS, q + (((ks >> 2) * kPanel + (ks & 3) * 32) >> 4),
+                                     dSB + ((int)(S_SLOW - S_SB) / 16 + (ks * 2048) / 16), idesc_bf16(128, 64, 0, 1), 1);
+                        }
+                    }
                 }
                 __syncwarp();
                 ok = wait(B_P, it);
@@ -350,6 +360,12 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                     for (int ks = 0; ks < 8; ++ks)
                         mma_bf16_ta(tmem + T_PV, tmem + T_P + 8 * ks, v + ((ks * 2048) >> 4), idesc_bf16(128, 64, 0, 1),
                                     ks > 0);
+                    if (FINE) {
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_bf16_ta(tmem + T_PV, tmem + T_QK + 64 * (ks >> 2) + 8 * (ks & 3), v + ((ks * 2048) >> 4),
+                                        idesc_bf16(128, 64, 0, 1), 1);
+                    }
                     mma_commit(bar(B_O));
                     mma_commit(bar(B_FREE + st));
                 }
@@ -379,7 +395,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
 #pragma unroll 1
             for (int b = 0; b < 4; ++b) {   // 16 columns at a time
                 const int j0 = 64 * half + 16 * b;
-                uint32_t x[16], p[8];
+                uint32_t x[16], p[8], low[8];
                 tmem_ld16(tl + T_QK + j0, x);
                 tmem_wait_ld();
                 if (b == 3) {
@@ -392,19 +408,29 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                 const int last = rev ? n - j0 : 16;
                 if (rev ? r0 > j0 + 15 : r0 + 31 < j0) {   // none, for the whole warp
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) p[e] = 0u;
+                    for (int e = 0; e < 8; ++e) p[e] = low[e] = 0u;
                 } else {
+                    const auto put = [&](int e, float2 y) {
+                        if (FINE) {
+                            uint32_t part[2];
+                            split_bf16<2>(y, part);
+                            p[e] = part[0];
+                            low[e] = part[1];
+                        } else {
+                            p[e] = pack_bf16(y);
+                        }
+                    };
                     if (g >= kStrong) {   // w_|r - j| = w_(seen - 1) / w_(distance of j from the block's far end)
                         const float fr = f * exp2f(g2 * (float)max(seen - 1, 0));
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            p[e] = pack_bf16(mul2(mul2(make_float2(fr, fr), wj[e]), as_float2(x[2 * e], x[2 * e + 1])));
+                            put(e, mul2(mul2(make_float2(fr, fr), wj[e]), as_float2(x[2 * e], x[2 * e + 1])));
                     } else {              // strong decays, element by element
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const int d0 = rev ? j0 + 2 * e - r : r - j0 - 2 * e, d1 = rev ? d0 + 1 : d0 - 1;
-                            p[e] = pack_bf16(make_float2(f * pw[max(d0, 0)] * __uint_as_float(x[2 * e]),
-                                                         f * pw[max(d1, 0)] * __uint_as_float(x[2 * e + 1])));
+                            put(e, make_float2(f * pw[max(d0, 0)] * __uint_as_float(x[2 * e]),
+                                               f * pw[max(d1, 0)] * __uint_as_float(x[2 * e + 1])));
                         }
                     }
                     // masked columns become zeros whatever they hold: on the diagonal, and past the end in reverse
@@ -413,7 +439,9 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                         for (int e = 0; e < 8; ++e) {
                             const bool lo = rev ? 16 - 2 * e <= seen && 2 * e < last : 2 * e < seen;
                             const bool hi = rev ? 15 - 2 * e <= seen && 2 * e + 1 < last : 2 * e + 1 < seen;
-                            p[e] &= (lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u);
+                            const uint32_t keep = (lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u);
+                            p[e] &= keep;
+                            if (FINE) low[e] &= keep;
                         }
                     }
                 }
@@ -422,6 +450,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
                     tc_fence_after();
                 }
                 tmem_st8(tl + T_P + j0 / 2, p);
+                if (FINE) tmem_st8(tl + T_QK + 64 * half + 8 * b, low);   // scores that this warp has read
             }
             tmem_wait_st();
             tc_fence_before();
@@ -550,9 +579,19 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
         }
         auto write_sb = [&] {
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                *reinterpret_cast<uint4*>(sm + S_SB + swz(R, c)) =
-                    make_uint4(pack_bf16(S[4 * c]), pack_bf16(S[4 * c + 1]), pack_bf16(S[4 * c + 2]), pack_bf16(S[4 * c + 3]));
+            for (int c = 0; c < 8; ++c) {
+                if (FINE) {
+                    uint32_t y[4][2];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) split_bf16<2>(S[4 * c + e], y[e]);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+                        *reinterpret_cast<uint4*>(sm + (p ? S_SLOW : S_SB) + swz(R, c)) = make_uint4(y[0][p], y[1][p], y[2][p], y[3][p]);
+                } else {
+                    *reinterpret_cast<uint4*>(sm + S_SB + swz(R, c)) =
+                        make_uint4(pack_bf16(S[4 * c]), pack_bf16(S[4 * c + 1]), pack_bf16(S[4 * c + 2]), pack_bf16(S[4 * c + 3]));
+                }
+            }
             fence_proxy_async_smem();
             arrive(B_S);
         };
@@ -606,26 +645,44 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta) {
     }
 }
 
+// SHORT: units of one chunk, which take the finer form, may be among the call's.  A kernel of its own for calls
+// without them: the registers that the compiler gives to twelve forms in one cost the backward pass of two sequences
+// of 8192 tokens 566 us instead of 540.
+template <bool SHORT, bool REV, bool F32, int PARTS>
+__device__ __forceinline__ void decay_tc_scan(const TcArgs& ta, Unit unit) {
+    if (!SHORT && !unit_of(ta, slot_of(ta.a), REV, unit)) return;
+    if (SHORT && unit.t1 - unit.t0 <= kC) decay_tc_body<REV, F32, PARTS, false, true>(ta, unit);
+    else decay_tc_body<REV, F32, PARTS, false, false>(ta, unit);
+}
+
+template <bool SHORT>
 __global__ void __launch_bounds__(kThreads, 1)
 decay_tc_kernel(const __grid_constant__ TcArgs ta) {
     const DecayScan& s = ta.a.scan[blockIdx.y];
+    Unit unit;
+    if (SHORT && !unit_of(ta, slot_of(ta.a), s.reverse, unit)) return;
     if (s.out_f32) {   // a part of a sum over shared heads: no state is asked of such a scan
-        if (s.reverse) decay_tc_body<true, true, 2, false>(ta);
-        else decay_tc_body<false, true, 2, false>(ta);
+        if (s.reverse) decay_tc_scan<SHORT, true, true, 2>(ta, unit);
+        else decay_tc_scan<SHORT, false, true, 2>(ta, unit);
     } else if (s.final) {
-        if (s.reverse) decay_tc_body<true, false, 3, false>(ta);
-        else decay_tc_body<false, false, 3, false>(ta);
+        if (s.reverse) decay_tc_scan<SHORT, true, false, 3>(ta, unit);
+        else decay_tc_scan<SHORT, false, false, 3>(ta, unit);
     } else {
-        if (s.reverse) decay_tc_body<true, false, 2, false>(ta);
-        else decay_tc_body<false, false, 2, false>(ta);
+        if (s.reverse) decay_tc_scan<SHORT, true, false, 2>(ta, unit);
+        else decay_tc_scan<SHORT, false, false, 2>(ta, unit);
     }
 }
 
-// Segments, first: what each adds to the state.
+// Segments, first: what each adds to the state (the last one visited adds to none).
+template <bool REV>
+__device__ __forceinline__ void decay_tc_state(const TcArgs& ta) {
+    Unit unit;
+    if (unit_of(ta, slot_of(ta.a), REV, unit) && !unit.last) decay_tc_body<REV, false, 3, true, false>(ta, unit);
+}
 __global__ void __launch_bounds__(kThreads, 1)
 decay_tc_state_kernel(const __grid_constant__ TcArgs ta) {
-    if (ta.a.scan[blockIdx.y].reverse) decay_tc_body<true, false, 3, true>(ta);
-    else decay_tc_body<false, false, 3, true>(ta);
+    if (ta.a.scan[blockIdx.y].reverse) decay_tc_state<true>(ta);
+    else decay_tc_state<false>(ta);
 }
 
 // ------------------------------------------------------------------ host side
@@ -653,7 +710,9 @@ cudaError_t set_attributes() {
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (done[dev]) return cudaSuccess;
-    e = cudaFuncSetAttribute(decay_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    e = cudaFuncSetAttribute(decay_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(decay_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(decay_tc_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e == cudaSuccess) done[dev] = true;
@@ -679,7 +738,8 @@ cudaError_t launch_decay_tc(const SegArgs& seg, bool state_only) {
     }
     const dim3 grid((unsigned)((long long)t.slots * a.Hv * (a.dv > kHalf ? 2 : 1)), (unsigned)a.num_scans);
     if (state_only) decay_tc_state_kernel<<<grid, kThreads, kSmem, a.stream>>>(t);
-    else decay_tc_kernel<<<grid, kThreads, kSmem, a.stream>>>(t);
+    else if (a.cu || a.T <= kC) decay_tc_kernel<true><<<grid, kThreads, kSmem, a.stream>>>(t);
+    else decay_tc_kernel<false><<<grid, kThreads, kSmem, a.stream>>>(t);
     return cudaGetLastError();
 }
 
