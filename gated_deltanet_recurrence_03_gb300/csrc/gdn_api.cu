@@ -822,9 +822,8 @@ gdn_status_t gdn_decay_attn_bwd(const void* q, long long q_stride, const void* k
             e = launch_decay_scan(a);
         }
         if (e == cudaSuccess && G > 1)
-            e = launch_head_sum(static_cast<const float*>(dq), grad_q, gq_stride, tokens, Hqk, G, dk, o.dtype, stream);
-        if (e == cudaSuccess && G > 1)
-            e = launch_head_sum(static_cast<const float*>(dkk), grad_k, gk_stride, tokens, Hqk, G, dk, o.dtype, stream);
+            e = launch_head_sums(HeadSums{{static_cast<const float*>(dq), static_cast<const float*>(dkk)}, {grad_q, grad_k},
+                                          {gq_stride, gk_stride}, tokens, Hqk, G, dk}, o.dtype, stream);
     }
     if (e != cudaSuccess) return cuda_fail(e, "decayed attention backward launch");
     record(o, 1, stream);

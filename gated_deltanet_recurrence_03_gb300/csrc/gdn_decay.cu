@@ -51,21 +51,31 @@ __global__ void __launch_bounds__(kJoinThreads) decay_join_kernel(const __grid_c
     }
 }
 
+// A sum over shared heads reads G fp32 parts and writes one row, and is bound by HBM: a thread takes eight values of
+// one token and query/key head (two 16-byte loads of each part, read once and so streamed; one 16- or two 16-byte
+// stores), and both gradients' sums share a launch.
+constexpr int kSumThreads = 256;
 template <typename T>
-__global__ void head_sum_kernel(const float* __restrict__ part, T* __restrict__ out, long long out_stride,
-                                long long total, int Hqk, int G, int d) {
-    const long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x;   // 4 values each
-    if (e >= total) return;
-    const int v = d / 4;
-    const int c = (int)(e % v);
-    const long long th = e / v;   // token * Hqk + head
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < G; ++i) {
-        const float4 x = reinterpret_cast<const float4*>(part)[(th * G + i) * v + c];
-        acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+__global__ void __launch_bounds__(kSumThreads) head_sum_kernel(const __grid_constant__ HeadSums a) {
+    const int which = blockIdx.x & 1, hk = (blockIdx.x >> 1) % a.Hqk, lanes = a.d / 8;
+    const long long t = (long long)((blockIdx.x >> 1) / a.Hqk) * (kSumThreads / lanes) + threadIdx.x / lanes;
+    if (t >= a.tokens) return;
+    const int c = threadIdx.x % lanes * 8;
+    const float* part = a.part[which] + ((size_t)t * a.Hqk + hk) * a.G * a.d + c;
+    float x[8] = {};
+#pragma unroll 2
+    for (int i = 0; i < a.G; ++i) {
+        const float4 lo = __ldcs(reinterpret_cast<const float4*>(part + (size_t)i * a.d));
+        const float4 hi = __ldcs(reinterpret_cast<const float4*>(part + (size_t)i * a.d) + 1);
+        x[0] += lo.x; x[1] += lo.y; x[2] += lo.z; x[3] += lo.w;
+        x[4] += hi.x; x[5] += hi.y; x[6] += hi.z; x[7] += hi.w;
     }
-    T* o = out + (th / Hqk) * out_stride + (th % Hqk) * d + 4 * c;
-    o[0] = from_f32<T>(acc.x); o[1] = from_f32<T>(acc.y); o[2] = from_f32<T>(acc.z); o[3] = from_f32<T>(acc.w);
+    __align__(16) T y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = from_f32<T>(x[e]);
+    T* out = static_cast<T*>(a.out[which]) + (size_t)t * a.out_stride[which] + (size_t)hk * a.d + c;
+#pragma unroll
+    for (int e = 0; e < (int)sizeof(T) / 2; ++e) reinterpret_cast<uint4*>(out)[e] = reinterpret_cast<const uint4*>(y)[e];
 }
 
 // Tokens of a segment, 0 for whole sequences.  One CTA walks one slot, so a call of few sequences and heads leaves most
@@ -125,14 +135,11 @@ cudaError_t launch_decay_scan(const DecayArgs& a) {
     return pass(p, false);
 }
 
-cudaError_t launch_head_sum(const float* part, void* out, long long out_stride, long long tokens, int Hqk, int G, int d,
-                            int dtype, cudaStream_t stream) {
-    const long long total = tokens * Hqk * (d / 4);
-    const unsigned blocks = (unsigned)((total + 255) / 256);
-    if (dtype == GDN_BF16)
-        head_sum_kernel<<<blocks, 256, 0, stream>>>(part, static_cast<__nv_bfloat16*>(out), out_stride, total, Hqk, G, d);
-    else
-        head_sum_kernel<<<blocks, 256, 0, stream>>>(part, static_cast<float*>(out), out_stride, total, Hqk, G, d);
+cudaError_t launch_head_sums(const HeadSums& a, int dtype, cudaStream_t stream) {
+    const int per = kSumThreads / (a.d / 8);
+    const unsigned blocks = 2u * (unsigned)((a.tokens + per - 1) / per * a.Hqk);
+    if (dtype == GDN_BF16) head_sum_kernel<__nv_bfloat16><<<blocks, kSumThreads, 0, stream>>>(a);
+    else head_sum_kernel<float><<<blocks, kSumThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 

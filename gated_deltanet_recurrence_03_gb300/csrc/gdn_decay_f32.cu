@@ -1,6 +1,6 @@
-// The decayed scan (gdn_internal.cuh, DecayScan) for fp32 inputs, on the CUDA cores: the tensor cores would need
-// every operand in three parts, and the legacy tf32 path with its three products measured half the rate of packed
-// fp32 FMAs here.
+// The decayed scan (gdn_internal.cuh, DecayScan) for fp32 inputs, on the CUDA cores.  The tensor cores would need
+// every operand in three bf16 parts and six products of them, and mma.sync in tf32 three products, which at about six
+// SM cycles for each of 1024 FMAs is 18 cycles where packed fp32 FMAs (128 a cycle) take 8.
 //
 // The chunked form with C = 32 tokens (the quadratic part of a token's work grows with C and is below the two
 // dk x dv products of the state at these head dims).  With w_d = a^d, n valid tokens, S the state at the first
@@ -9,6 +9,12 @@
 // One CTA of 256 threads walks one unit of one value head for up to 64 value columns.  The state stays in
 // registers (rows x 4 columns a thread) and is copied to shared memory once a chunk for Q S; products are register
 // tiles of packed FMAs over float4 reads; the next chunk's rows are loaded while this one is computed.
+//
+// Bound by shared memory: each float4 that a product reads feeds 8 or 16 FMAs, and the L1 pipe is 83 % busy in the
+// main pass, the FMA pipe 21 %.  Measured, packed backward of 1344 tokens (the longest sequence 700), 8 heads of 64:
+// 4.6 ms as matrix products and a token loop in plain tensor operations, 287 us token by token in one CTA a head,
+// 121 us in chunks, 98 us in segments of 128 tokens, 66 us with those spread over two CTAs an SM (16 + 40 us in the
+// state and the main pass).
 #include "decay_unit.cuh"
 
 namespace gdn {
@@ -272,8 +278,8 @@ cudaError_t launch_typed(const SegArgs& s, bool state_only) {
 
 cudaError_t launch_decay_f32(const SegArgs& s, bool state_only) {
     // 32 columns a CTA where 64 would leave half of the SMs without one: the scores are then formed twice, but by
-    // SMs that would idle.  (Taken up to twice as many CTAs as SMs it measured 67 us against 45 us on the packed
-    // backward of 1344 tokens, 8 heads of 64.)
+    // SMs that would idle.  (Taken up to twice as many CTAs as SMs it measured 102.2 us against 101.3 us on the packed
+    // backward of 1344 tokens, 8 heads of 64, in coarser segments: no gain there.)
     const int dk = s.a.dk;
     const long long ctas = (long long)s.slots * s.a.Hv * s.a.num_scans * ((s.a.dv + 63) / 64);
     const int dv = s.a.dv < kDecayColumns || ctas < kFewCtas ? 32 : kDecayColumns;

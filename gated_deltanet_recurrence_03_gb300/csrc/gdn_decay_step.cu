@@ -6,6 +6,10 @@
 // One CTA owns CW adjacent columns of one (row n, value head) state: thread (row group, column lane) holds
 // its rows' four columns in registers, loads and stores are 128-bit and cover whole CW * 4 byte row pieces,
 // and the row sums go through shared memory once.
+//
+// Bound by HBM: 256 sequences of 32 heads of 128 x 128 (2 x 512 MiB of states) take 178.5 us = 6.05 TB/s, 0.90 of the
+// measured copy bandwidth.  Loads and stores stream past the caches (184 us without); limited to two or three CTAs an
+// SM it takes 275 or 197 us.
 #include "gdn_internal.cuh"
 
 namespace gdn {

@@ -201,9 +201,15 @@ constexpr float kMinLogDecay = -100.f;
 size_t decay_scan_workspace_bytes(int dtype, int dk, int dv, int Hv, int nseq, long long tokens, bool packed, int num_scans);
 cudaError_t launch_decay_scan(const DecayArgs& a);
 // out[t][hk] = sum over the G value heads of query/key head hk of part[t][hk G + i] (fp32 [tokens][Hqk G][d]),
-// rounded once to the output type, rows out_stride elements apart.
-cudaError_t launch_head_sum(const float* part, void* out, long long out_stride, long long tokens, int Hqk, int G, int d,
-                            int dtype, cudaStream_t stream);
+// rounded once to the output type, rows out_stride elements apart: two such sums of one shape.
+struct HeadSums {
+    const float* part[2];
+    void* out[2];
+    long long out_stride[2];
+    long long tokens;
+    int Hqk, G, d;
+};
+cudaError_t launch_head_sums(const HeadSums& a, int dtype, cudaStream_t stream);
 
 struct DecayStepArgs {
     const void* q;
