@@ -45,8 +45,14 @@ def _stream_handle(stream: Optional[torch.cuda.Stream], device) -> int:
 _NO_SWITCH = contextlib.nullcontext()
 
 
-def _on(device):
-    """Context in which ``device`` is current; costs nothing where it already is."""
+def _on(device, stream=None):
+    """Context in which ``device`` and, where given, ``stream`` are current; costs nothing where they already are.
+    What a call allocates in it belongs to the stream that its kernels run on, so that neither memory still in use
+    on another stream is written nor the call's own handed out before it is done."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        return torch.cuda.stream(stream)
     return _NO_SWITCH if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
@@ -620,7 +626,7 @@ def gdn_decay_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
     lib = L.load()
     dev, dt, Hqk, Hv, dk, dv, strides = _decay_inputs(q, k, v, log_decay, 2)
     B, T = q.shape[:2]
-    with _on(dev):
+    with _on(dev, stream):
         o, keep = _call_opts(lib, dt, scale, stream, dev, events)
         nseq = _packed(o, cu_seqlens, B, dev)
         if S0 is not None:
@@ -657,11 +663,11 @@ def gdn_decay_attn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_d
     _need("S", S, torch.float32, dev, (pool, Hv, dk, dv))
     if slots is not None:
         _need("slots", slots, torch.int32, dev, (N,))
-    if out is None:
-        out = v.new_empty(v.shape)
-    else:
-        _need("out", out, dt, dev, (N, Hv, dv))
-    with _on(dev):
+    with _on(dev, stream):
+        if out is None:
+            out = v.new_empty(v.shape)
+        else:
+            _need("out", out, dt, dev, (N, Hv, dv))
         o, keep = _call_opts(lib, dt, scale, stream, dev, events)
         st = lib.gdn_decay_attn_step(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], _ptr(log_decay),
                                      _ptr(S), _ptr(slots), pool, _ptr(out), N, Hqk, Hv, dk, dv, ctypes.byref(o))
@@ -684,14 +690,14 @@ def gdn_decay_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
     dev, dt, Hqk, Hv, dk, dv, strides = _decay_inputs(q, k, v, log_decay, 2)
     B, T = q.shape[:2]
     _need("grad_out", grad_out, dt, dev, (B, T, Hv, dv))
-    if grads is None:
-        grads = (q.new_empty(q.shape), k.new_empty(k.shape), v.new_empty(v.shape))
-    else:
-        for name, g, t in zip(("grad_q", "grad_k", "grad_v"), grads, (q, k, v)):
-            if g.shape != t.shape or g.dtype != dt or g.device != dev:
-                raise ValueError(f"{name} must be {dt} of shape {tuple(t.shape)} on {dev}")
-    gstrides = tuple(_token_rows(n, g, g.shape[3], 2) for n, g in zip(("grad_q", "grad_k", "grad_v"), grads))
-    with _on(dev):
+    with _on(dev, stream):
+        if grads is None:
+            grads = (q.new_empty(q.shape), k.new_empty(k.shape), v.new_empty(v.shape))
+        else:
+            for name, g, t in zip(("grad_q", "grad_k", "grad_v"), grads, (q, k, v)):
+                if g.shape != t.shape or g.dtype != dt or g.device != dev:
+                    raise ValueError(f"{name} must be {dt} of shape {tuple(t.shape)} on {dev}")
+        gstrides = tuple(_token_rows(n, g, g.shape[3], 2) for n, g in zip(("grad_q", "grad_k", "grad_v"), grads))
         o, keep = _call_opts(lib, dt, scale, stream, dev, events)
         nseq = _packed(o, cu_seqlens, B, dev)
         for name, t in (("S0", S0), ("grad_S_final", grad_S_final)):
@@ -738,13 +744,13 @@ def gdn_block_norm_fwd(x: torch.Tensor, b: torch.Tensor, post_weight: torch.Tens
     Returns (r, n)."""
     lib = L.load()
     dev, dt, shape, D, rows, cols = _block_norm_inputs(x, b, post_weight, pre_weight, gate, res_scale)
-    if out is None:
-        r, n = torch.empty_like(x), torch.empty_like(x)
-    else:
-        r, n = out
-        _need("r", r, dt, dev, shape)
-        _need("n", n, dt, dev, shape)
-    with _on(dev):
+    with _on(dev, stream):
+        if out is None:
+            r, n = torch.empty_like(x), torch.empty_like(x)
+        else:
+            r, n = out
+            _need("r", r, dt, dev, shape)
+            _need("n", n, dt, dev, shape)
         o, keep = _call_opts(lib, dt, 1.0, stream, dev, events)
         o.norm_eps = float(eps)
         st = lib.gdn_block_norm_fwd(_ptr(x), _ptr(b), _ptr(gate), cols, _ptr(res_scale), _ptr(post_weight),
@@ -765,11 +771,11 @@ def gdn_block_norm_bwd(x: torch.Tensor, b: torch.Tensor, post_weight: torch.Tens
     dev, dt, shape, D, rows, cols = _block_norm_inputs(x, b, post_weight, pre_weight, gate, res_scale)
     _need("grad_r", grad_r, dt, dev, shape)
     _need("grad_n", grad_n, dt, dev, shape)
-    gx, gb = torch.empty_like(x), torch.empty_like(x)
-    gg = None if gate is None else torch.empty_like(gate)
-    sums = post_weight.new_empty((2 if res_scale is None else 3, D))
-    at = sums.data_ptr()
-    with _on(dev):
+    with _on(dev, stream):
+        gx, gb = torch.empty_like(x), torch.empty_like(x)
+        gg = None if gate is None else torch.empty_like(gate)
+        sums = post_weight.new_empty((2 if res_scale is None else 3, D))
+        at = sums.data_ptr()
         o, keep = _call_opts(lib, dt, 1.0, stream, dev, events)
         o.norm_eps = float(eps)
         ws = _scratch(o, int(lib.gdn_block_norm_bwd_workspace_size(rows, D, ctypes.byref(o))), None, post_weight)

@@ -24,7 +24,8 @@
 // no heads are shared.  What brought it there from 318 us: the first tiles' prefetch to L2 (176 -> 154 us); the parts
 // of V side by side in one product of N = 192; QS ahead of P in the issue order; the outputs through shared memory in
 // whole rows (stored from the registers in 16-byte pieces: 20 % slower); two parts instead of three where no state
-// leaves (backward 603 -> 540 us); one streaming sum over shared heads for both gradients (537 -> 515 us); 64 / 72 / 128 registers for issue / work / state (56 / 72 / 136: 572 us).
+// leaves (backward 603 -> 540 us); one streaming sum over shared heads for both gradients (537 -> 515 us); 64 / 72 / 128 registers for
+// issue / work / state (56 / 72 / 136: 572 us).
 // 64 columns a CTA: a whole 128-wide head would not fit (state, V's parts and two stages of tiles) and would leave
 // half of the SMs idle here.
 //
