@@ -43,6 +43,7 @@ def _stream_handle(stream: Optional[torch.cuda.Stream], device) -> int:
 
 
 _NO_SWITCH = contextlib.nullcontext()
+_DENSE = torch.contiguous_format   # empty_like of a slice is dense (and 1 to 2 us cheaper than new_empty)
 
 
 def _on(device, stream=None):
@@ -632,13 +633,13 @@ def gdn_decay_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
         if S0 is not None:
             _need("S0", S0, torch.float32, dev, (nseq, Hv, dk, dv))
         if out is None:
-            out = v.new_empty(v.shape)
+            out = torch.empty_like(v, memory_format=_DENSE)
         else:
             _need("out", out, dt, dev, (B, T, Hv, dv))
         if S_final is not None:
             _need("S_final", S_final, torch.float32, dev, (nseq, Hv, dk, dv))
         elif output_final_state:
-            S_final = log_decay.new_empty((nseq, Hv, dk, dv))
+            S_final = log_decay.new_empty((nseq, Hv, dk, dv)) if S0 is None else torch.empty_like(S0)
         workspace = _scratch(o, int(lib.gdn_decay_attn_fwd_workspace_size(B, T, Hqk, Hv, dk, dv, ctypes.byref(o))),
                              workspace, log_decay)
         st = lib.gdn_decay_attn_fwd(_ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], _ptr(log_decay),
@@ -665,7 +666,7 @@ def gdn_decay_attn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_d
         _need("slots", slots, torch.int32, dev, (N,))
     with _on(dev, stream):
         if out is None:
-            out = v.new_empty(v.shape)
+            out = torch.empty_like(v, memory_format=_DENSE)
         else:
             _need("out", out, dt, dev, (N, Hv, dv))
         o, keep = _call_opts(lib, dt, scale, stream, dev, events)
@@ -692,7 +693,7 @@ def gdn_decay_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
     _need("grad_out", grad_out, dt, dev, (B, T, Hv, dv))
     with _on(dev, stream):
         if grads is None:
-            grads = (q.new_empty(q.shape), k.new_empty(k.shape), v.new_empty(v.shape))
+            grads = tuple(torch.empty_like(t, memory_format=_DENSE) for t in (q, k, v))
         else:
             for name, g, t in zip(("grad_q", "grad_k", "grad_v"), grads, (q, k, v)):
                 if g.shape != t.shape or g.dtype != dt or g.device != dev:

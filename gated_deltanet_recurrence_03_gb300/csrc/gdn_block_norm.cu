@@ -12,7 +12,7 @@
 // A row is read from HBM once: it passes through a ring in shared memory (bulk copies, up to four rows ahead of a group
 // of threads) and is held in registers between the two norms; one block an SM of up to 1024 threads walks the rows.
 // The forward pass is bound by HBM and its instructions alike, the backward pass by its instructions and shared-memory
-// reads (issue slots 71 and 67 % used).  Measured, 16,384 rows of 2048 bf16 values with a gate: forward 126 us, 0.80 of
+// reads (issue slots 71 and 67 % used).  Measured, 16,384 rows of 4096 bf16 values with a gate: forward 126 us, 0.80 of
 // the measured copy bandwidth (161 us with loads straight to registers; 130 us with the next row's in registers, whose
 // moves wait for the loads; 197 us with both sums of a row in one exchange); backward 253.5 us, 0.63 of it (from 627:
 // sums of the weights' gradients in registers 444, one pass over the row 374, packed arithmetic 333, one sum for the
