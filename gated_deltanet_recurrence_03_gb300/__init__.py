@@ -1,8 +1,9 @@
 """Gated DeltaNet state recurrence on GB300 (sm_103a).
 
 The compute runs in libgdn.so (hand-written CUDA: a tcgen05/TMA chunked prefill, a
-token-serial CUDA-core prefill and a one-pass decode step) behind the C ABI of
-``include/gdn.h``.  This package is the thin PyTorch binding of that ABI.
+token-serial CUDA-core prefill and a one-pass decode step; linear attention with a decay
+for each head and the norms around a block) behind the C ABI of ``include/gdn.h``.
+This package is the thin PyTorch binding of that ABI.
 """
 from ._lib import GdnError, GDN_BF16, GDN_F32, GDN_NORMALIZE_QK  # noqa: F401
 from .api import (backward_workspace_size, check_device_status, gdn_block_norm_bwd, gdn_block_norm_fwd,  # noqa: F401
