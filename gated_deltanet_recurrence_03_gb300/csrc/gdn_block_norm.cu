@@ -12,11 +12,11 @@
 // A row is read from HBM once: it passes through a ring in shared memory (bulk copies, up to four rows ahead of a group
 // of threads) and is held in registers between the two norms; one block an SM of up to 1024 threads walks the rows.
 // The forward pass is bound by HBM and its instructions alike, the backward pass by its instructions and shared-memory
-// reads (issue slots 71 and 67 % used).  Measured, 16,384 rows of 4096 bf16 values with a gate: forward 126 us, 0.80 of
-// the measured copy bandwidth (161 us with loads straight to registers; 130 us with the next row's in registers, whose
-// moves wait for the loads; 197 us with both sums of a row in one exchange); backward 253.5 us, 0.63 of it (from 627:
+// reads.  Measured, 16,384 rows of 4096 bf16 values with a gate: forward 118 us, 0.85 of the measured copy bandwidth
+// (161 us with loads straight to registers; 130 us with the next row's in registers, whose
+// moves wait for the loads; 197 us with both sums of a row in one exchange; 126 us with one vector a thread); backward 209 us, 0.77 of it (from 627:
 // sums of the weights' gradients in registers 444, one pass over the row 374, packed arithmetic 333, one sum for the
-// two weights 318, the ring 254).
+// two weights 318, the ring 254, two vectors a thread 209).
 #include <algorithm>
 #include <atomic>
 
@@ -453,7 +453,11 @@ __global__ void __launch_bounds__(1024) block_norm_sums_kernel(const float* __re
     }
 }
 
-// Vectors a thread holds (one up to D = 4096, then two), threads a row, row groups and ring stages a block, blocks.
+// Vectors a thread holds, threads a row, row groups and ring stages a block, blocks.  With two vectors a thread a row's
+// exchanges take half the threads and each has twice the work between them: 255 -> 209 us (backward, 16384 x 4096),
+// 234 -> 187 us (32768 x 2048), 129 -> 81 us (65536 x 264); four are no better (201, 194 us; forward 119 -> 130 us).
+// One vector where a row fits one warp, and where no SM has more than one row, whose latency then counts (4.2 against
+// 5.5 us forward, 37 x 2048).
 // A block fills an SM: up to 1024 threads and kSmemMax bytes, with as many groups as leave each at least two
 // stages; past one warp a row the groups are limited by the named barriers.
 struct Shape {
@@ -464,7 +468,7 @@ constexpr size_t kSmemMax = 227 * 1024;
 Shape shape_of(int D, long long rows, int row_bytes) {
     const int nv = D / kVec;
     Shape s;
-    s.v = nv <= 512 ? 1 : 2;
+    s.v = nv <= 32 || (nv <= 512 && rows <= 152) ? 1 : 2;
     s.tpr = ((nv + s.v - 1) / s.v + 31) / 32 * 32;
     s.groups = std::max(1, (s.v == 1 ? 1024 : 512) / s.tpr);
     if (s.tpr > 32) s.groups = std::min(s.groups, 8);
