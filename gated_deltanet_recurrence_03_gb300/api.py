@@ -775,16 +775,14 @@ def gdn_block_norm_bwd(x: torch.Tensor, b: torch.Tensor, post_weight: torch.Tens
     with _on(dev, stream):
         gx, gb = torch.empty_like(x), torch.empty_like(x)
         gg = None if gate is None else torch.empty_like(gate)
-        sums = post_weight.new_empty((2 if res_scale is None else 3, D))
-        at = sums.data_ptr()
+        gpost, gpre = torch.empty_like(post_weight), torch.empty_like(post_weight)
+        gs = None if res_scale is None else torch.empty_like(res_scale)
         o, keep = _call_opts(lib, dt, 1.0, stream, dev, events)
         o.norm_eps = float(eps)
         ws = _scratch(o, int(lib.gdn_block_norm_bwd_workspace_size(rows, D, ctypes.byref(o))), None, post_weight)
         st = lib.gdn_block_norm_bwd(_ptr(x), _ptr(b), _ptr(gate), cols, _ptr(res_scale), _ptr(post_weight),
                                     _ptr(pre_weight), _ptr(grad_r), _ptr(grad_n), _ptr(gx), _ptr(gb), _ptr(gg),
-                                    at, at + 4 * D, None if res_scale is None else at + 8 * D, rows, D,
-                                    ctypes.byref(o))
+                                    _ptr(gpost), _ptr(gpre), _ptr(gs), rows, D, ctypes.byref(o))
         del keep, ws
         L.check(lib, st)
-    gpost, gpre, *gs = sums.unbind(0)
-    return gx, gb, gpost, gpre, gg, gs[0] if gs else None
+    return gx, gb, gpost, gpre, gg, gs
