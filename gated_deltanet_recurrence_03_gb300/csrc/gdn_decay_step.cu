@@ -7,18 +7,26 @@
 // its rows' four columns in registers, loads and stores are 128-bit and cover whole CW * 4 byte row pieces,
 // and the row sums go through shared memory once.
 //
-// Bound by HBM: 256 sequences of 32 heads of 128 x 128 (2 x 512 MiB of states) take 178.5 us = 6.05 TB/s, 0.90 of the
-// measured copy bandwidth.  Loads and stores stream past the caches (184 us without); limited to two or three CTAs an
-// SM it takes 275 or 197 us.
+// Bound by HBM: 256 sequences of 32 heads of 128 x 128 (2 x 512 MiB of states) take 153.6 us = 7.0 TB/s, 1.05 of the
+// measured copy bandwidth.  What counts is that a CTA's loads are all in flight before its first store: with each row
+// stored as soon as it is loaded the compiler keeps few loads ahead, and it takes 176 us.  Streaming accesses make no
+// difference in this form.
 #include "gdn_internal.cuh"
 
 namespace gdn {
 namespace {
 
+// Rows of a state that a thread holds.
+__host__ __device__ constexpr int rows_of(int DK, int CW) { return DK / (256 / (CW / 4)); }
+
+// Two CTAs an SM where a thread holds 16 rows, so that all of them have registers; without the bound the compiler takes
+// fewer and loads in turns (160 against 153.6 us, 256 x 32 states of 128 x 128).  With fewer rows a thread the compiler's
+// own choice (0), of fewer registers and more CTAs, is better than a bound of 1 (58 against 67 us, 1024 x 32 states of
+// 32 x 32).
 template <int DK, int DV, int CW, typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, rows_of(DK, CW) >= 16 ? 2 : 0)
 decay_step_kernel(const __grid_constant__ DecayStepArgs a) {
-    constexpr int LX = CW / 4, RG = 256 / LX, RPT = DK / RG, SL = DV / CW;
+    constexpr int LX = CW / 4, RG = 256 / LX, RPT = rows_of(DK, CW), SL = DV / CW;
     static_assert(RPT >= 1 && DK % RG == 0 && DV % CW == 0, "tile");
     __shared__ __align__(16) float red[RG][CW + 4];
     __shared__ float skq;
@@ -45,12 +53,9 @@ decay_step_kernel(const __grid_constant__ DecayStepArgs a) {
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int r = 0; r < RPT; ++r) {
-        const float qr = to_f32(q[rg * RPT + r]), kr = to_f32(k[rg * RPT + r]);
+        const float qr = to_f32(q[rg * RPT + r]);
         acc.x = fmaf(st[r].x, qr, acc.x); acc.y = fmaf(st[r].y, qr, acc.y);
         acc.z = fmaf(st[r].z, qr, acc.z); acc.w = fmaf(st[r].w, qr, acc.w);
-        __stcs(reinterpret_cast<float4*>(S + (size_t)(rg * RPT + r) * DV),
-               make_float4(fmaf(kr, vj[0], al * st[r].x), fmaf(kr, vj[1], al * st[r].y), fmaf(kr, vj[2], al * st[r].z),
-                           fmaf(kr, vj[3], al * st[r].w)));
     }
     reinterpret_cast<float4*>(&red[rg][0])[lx] = acc;
     if (tid < 32) {
@@ -61,6 +66,14 @@ decay_step_kernel(const __grid_constant__ DecayStepArgs a) {
         if (tid == 0) skq = kq;
     }
     __syncthreads();
+    // the stores after the barrier: none can come between the loads
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+        const float kr = to_f32(k[rg * RPT + r]);
+        __stcs(reinterpret_cast<float4*>(S + (size_t)(rg * RPT + r) * DV),
+               make_float4(fmaf(kr, vj[0], al * st[r].x), fmaf(kr, vj[1], al * st[r].y), fmaf(kr, vj[2], al * st[r].z),
+                           fmaf(kr, vj[3], al * st[r].w)));
+    }
     if (tid < CW) {
         float s = 0.f;
 #pragma unroll 8
@@ -69,10 +82,9 @@ decay_step_kernel(const __grid_constant__ DecayStepArgs a) {
     }
 }
 
-// A CTA takes a whole state (row pieces of up to 512 bytes, all of a thread's loads in flight) where there are at
-// least four states for each of the 152 SMs; below that 32-column pieces, so that one sequence's 32 heads of 128
-// columns still reach 128 SMs.  Measured on 256 x 32 states of 128 x 128: 178 us whole (6.05 TB/s, 0.90 of the copy
-// rate), 184 us in pieces; capped at two CTAs a SM 275 us.
+// A CTA takes a whole state (row pieces of up to 512 bytes) where there are at least four states for each of the 152
+// SMs; below that 32-column pieces, so that one sequence's 32 heads of 128 columns still reach 128 SMs.  Measured on
+// 256 x 32 states of 128 x 128, with rows stored as they were loaded: 178 us whole, 184 us in pieces.
 constexpr long long kWideRows = 4 * 152;
 
 template <int DK, int DV, typename T>
