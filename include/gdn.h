@@ -385,6 +385,7 @@ gdn_status_t gdn_decay_attn_step(const void* q, long long q_stride, const void* 
  *                  elements apart (0 = dense), so the three can be slices of one packed tensor.  Sums over
  *                  the value heads that share a query/key head are fp32, rounded once
  *   grad_S0        [nseq, Hv, dk, dv] float or NULL (not written)
+ * No output may overlap an input or another output (the three scans run side by side).
  * Deterministic.  opts->workspace: 256-byte aligned, gdn_decay_attn_bwd_workspace_size bytes.
  */
 size_t gdn_decay_attn_bwd_workspace_size(int B, int T, int Hqk, int Hv, int dk, int dv, const gdn_opts_t* opts);
