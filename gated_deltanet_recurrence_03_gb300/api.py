@@ -548,7 +548,8 @@ def gdn_output_gate_bwd(o: torch.Tensor, z: torch.Tensor, norm_weight: torch.Ten
 
 def _token_rows(name, t, d, lead):
     """Elements between consecutive token rows of t ([*lead, heads, d] with contiguous heads, token rows evenly
-    strided: a dense tensor or a slice of a packed projection)."""
+    strided: a dense tensor or a slice of a packed projection).  Rows that share memory, a broadcast token's among them,
+    are refused: the library takes a row stride of 0 for dense rows."""
     shape, stride = t.shape, t.stride()
     H = shape[lead]
     if lead == 1:
@@ -557,10 +558,10 @@ def _token_rows(name, t, d, lead):
     else:
         row = stride[1] if shape[1] > 1 else stride[0] if shape[0] > 1 else H * d
         even = shape[0] <= 1 or stride[0] == shape[1] * row
-    if even and stride[lead + 1] == 1 and (H == 1 or stride[lead] == d):
+    if even and row >= H * d and stride[lead + 1] == 1 and (H == 1 or stride[lead] == d):
         return row
     if t.numel():
-        raise ValueError(f"{name} must have contiguous heads and evenly strided token rows")
+        raise ValueError(f"{name} must have contiguous heads and evenly strided token rows of their own memory")
     return H * d
 
 

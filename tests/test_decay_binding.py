@@ -1,0 +1,61 @@
+"""The decayed attention's Python entry points on the host: which layouts of token rows they take, and what they
+refuse before the library is called (CPU tensors, nothing is launched)."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pkg_lib = pytest.importorskip("gated_deltanet_recurrence_03_gb300._lib")
+from gated_deltanet_recurrence_03_gb300 import api   # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from gated_deltanet_recurrence_03_gb300 import build
+    build.build()
+
+
+def rows_of(t, lead):
+    return api._token_rows("x", t, t.shape[-1], lead)
+
+
+@pytest.mark.parametrize("t,lead,row", [
+    (torch.zeros(2, 5, 3, 8), 2, 24),                                    # dense
+    (torch.zeros(2, 5, 40)[..., 8:32].unflatten(-1, (3, 8)), 2, 40),     # a slice of a packed projection
+    (torch.zeros(2, 5, 40)[:, :1, :24].unflatten(-1, (3, 8)), 2, 200),   # one token of each sequence
+    (torch.zeros(1, 1, 1, 8).expand(1, 1, 1, 8), 2, 8),                  # one token row: any stride is right
+    (torch.zeros(7, 3, 8), 1, 24),
+    (torch.zeros(7, 4, 24)[:, 1].unflatten(-1, (3, 8)), 1, 96),
+    (torch.zeros(2, 0, 3, 8), 2, 24), (torch.zeros(0, 3, 8), 1, 24),     # no tokens
+], ids=lambda x: str(getattr(x, "shape", x)))
+def test_token_rows_taken(t, lead, row):
+    assert rows_of(t, lead) == row
+
+
+BROADCAST = [
+    (torch.zeros(1, 1, 3, 8).expand(1, 6, 3, 8), 2),         # one row for every token
+    (torch.zeros(1, 1, 3, 8).expand(4, 6, 3, 8), 2),
+    (torch.zeros(1, 1, 3, 8).expand(4, 1, 3, 8), 2),         # one token, one row for every sequence
+    (torch.zeros(1, 3, 8).expand(5, 3, 8), 1),
+    (torch.zeros(1, 6, 3, 8).expand(4, 6, 3, 8), 2),         # one sequence for all
+    (torch.zeros(200).as_strided((1, 6, 3, 8), (200, 8, 8, 1)), 2),   # rows that overlap
+]
+
+
+@pytest.mark.parametrize("t,lead", BROADCAST, ids=lambda x: str(getattr(x, "shape", x)))
+def test_rows_that_share_memory_are_refused(t, lead):
+    """A row stride of 0 means dense rows to the C entry points, which would read past a broadcast tensor."""
+    with pytest.raises(ValueError, match="token rows"):
+        rows_of(t, lead)
+
+
+def test_broadcast_inputs_are_refused_by_the_calls():
+    one, v, g = torch.zeros(1, 1, 2, 32), torch.zeros(1, 6, 2, 32), torch.zeros(2)
+    every = one.expand(1, 6, 2, 32)
+    dense = every.contiguous()
+    S = torch.zeros(6, 2, 32, 32)
+    for q, k, w in ((every, dense, v), (dense, every, v), (dense, dense, every)):
+        with pytest.raises(ValueError, match="token rows"):
+            api.gdn_decay_attn_fwd(q, k, w, g)
+        with pytest.raises(ValueError, match="token rows"):
+            api.gdn_decay_attn_bwd(q, k, w, g, None, v)
+        with pytest.raises(ValueError, match="token rows"):
+            api.gdn_decay_attn_step(q[0], k[0], w[0], g, S)
