@@ -55,32 +55,41 @@ __device__ __forceinline__ float* unit_state(const SegArgs& ta, int scan, int sl
     return ta.states + (((size_t)scan * ta.slots + slot) * ta.a.Hv + h) * ta.a.dk * ta.a.dv;
 }
 
-// exp(g n) as hi + lo, to 2^-45 near 1 and 2^-31 at exp(-8): one rounding of a chunk's decay would compound over
-// the head's memory.  (Below exp(-12) a chunk forgets nearly all and one float does.)  From the series on y = g n / 2^s with
-// |y| <= 2^-10, then s squarings of 1 + e in two floats, (1 + e)^2 - 1 = 2 e + e^2.  (In fp64 the same takes ten
-// times as long on this chip.)
-__device__ __forceinline__ void decay_power(float g, float n, float& hi, float& lo) {
+// a + b as its rounded value and the rest, whichever is larger.
+__host__ __device__ __forceinline__ float two_sum(float a, float b, float& rest) {
+    const float t = a + b, z = t - a;
+    rest = (a - (t - z)) + (b - z);
+    return t;
+}
+
+// exp(g n) as hi + lo: one rounding of a chunk's decay would compound over the head's memory.  For x = g n in [-12, 12]
+// the relative error is below 2^(s - 43) + 2^-44 exp(-x), s the halvings that bring |x| to 2^-10: 2^-43 up to there,
+// 2^-30 at x = -8.  From the series on y = x / 2^s, then s squarings of 1 + e in two floats, (1 + e)^2 - 1 = 2 e + e^2.
+// (In fp64 the same takes ten times as long on this chip.)  Below exp(-12) a chunk forgets nearly all and one float
+// does; infinities, NaN and overflowing growths end there too, as expf has them.
+__host__ __device__ __forceinline__ void decay_power(float g, float n, float& hi, float& lo) {
     float xh = g * n, xl = fmaf(g, n, -xh);
-    if (xh < -12.f) {
+    if (!(fabsf(xh) <= 12.f)) {
         hi = expf(xh);
+        if (hi > 0.f && hi <= 3e38f) hi = fmaf(hi, xl, hi);
         lo = 0.f;
         return;
     }
     int s = 0;
-    while (fabsf(xh) > 0.0009765625f) {   // exact halvings
+    while (fabsf(xh) > 0.0009765625f) {   // exact halvings, at most 14
         xh *= 0.5f;
         xl *= 0.5f;
         ++s;
     }
     const float p = xh * xh * fmaf(xh, fmaf(xh, 0.041666668f, 0.16666667f), 0.5f);
-    float eh = xh + p, el = (p - (eh - xh)) + xl;
+    float eh = xh + p, el = (p - (eh - xh)) + xl, rest;
     for (; s > 0; --s) {
-        const float sq = eh * eh, a = 2.f * eh, t = a + sq;
-        el = (sq - (t - a)) + (fmaf(eh, eh, -sq) + fmaf(2.f * eh, el, 2.f * el));
-        eh = t;
+        const float sq = eh * eh, low = fmaf(eh, eh, -sq) + fmaf(2.f * eh, el, 2.f * el);
+        eh = two_sum(2.f * eh, sq, rest);
+        el = rest + low;
     }
-    hi = 1.f + eh;
-    lo = (eh - (hi - 1.f)) + el;
+    hi = two_sum(1.f, eh, rest);
+    lo = rest + el;
     const float t = hi + lo;
     lo -= t - hi;
     hi = t;
