@@ -55,6 +55,12 @@ __device__ __forceinline__ float* unit_state(const SegArgs& ta, int scan, int sl
     return ta.states + (((size_t)scan * ta.slots + slot) * ta.a.Hv + h) * ta.a.dk * ta.a.dv;
 }
 
+// The decay's exponent that the kernels use: -100 below that (-inf among them); a NaN stays one and a value above 0 a
+// growth, as the formula has them.
+__host__ __device__ __forceinline__ float decay_exponent(float log_decay) {
+    return log_decay < kMinLogDecay ? kMinLogDecay : log_decay;
+}
+
 // a + b as its rounded value and the rest, whichever is larger.
 __host__ __device__ __forceinline__ float two_sum(float a, float b, float& rest) {
     const float t = a + b, z = t - a;

@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(kJoinThreads) decay_join_kernel(const __grid_c
     __shared__ float w[4];   // the decay over a whole and over the last segment, in two floats each
     if (threadIdx.x < 2) {
         const long long len = threadIdx.x ? s1 - s0 - (long long)(n - 1) * ta.seg : ta.seg;
-        decay_power(fmaxf(a.log_decay[h], kMinLogDecay), (float)len, w[2 * threadIdx.x], w[2 * threadIdx.x + 1]);
+        decay_power(decay_exponent(a.log_decay[h]), (float)len, w[2 * threadIdx.x], w[2 * threadIdx.x + 1]);
     }
     __syncthreads();
     const int e = (part * kJoinThreads + threadIdx.x) * 4, row = e / dv, col = e % dv;

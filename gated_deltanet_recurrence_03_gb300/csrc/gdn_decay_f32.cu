@@ -76,8 +76,8 @@ decay_f32_kernel(const __grid_constant__ SegArgs ta) {
     if (STATE && unit.last) return;
     const int tid = threadIdx.x, cg = tid % L::CG, rg = tid / L::CG;
     const int len = (int)(unit.t1 - unit.t0), nch = (len + kC - 1) / kC, tail = len - (nch - 1) * kC;
-    const float g = fmaxf(a.log_decay[h], kMinLogDecay);
-    if (tid <= kC) pw[tid] = expf(g * (float)tid);
+    const float g = decay_exponent(a.log_decay[h]);
+    if (tid <= kC) pw[tid] = tid ? expf(g * (float)tid) : 1.f;
     if (tid < 2) decay_power(g, (float)(tid ? tail : kC), pw[34 + 2 * tid], pw[35 + 2 * tid]);   // of a full, of the last chunk
     const size_t base = ((size_t)unit.seq * a.Hv + h) * DK * a.dv;
     const float* const init = STATE ? nullptr : ta.seg ? unit_state(ta, blockIdx.y, slot, h) : s.init ? s.init + base : nullptr;
@@ -174,7 +174,7 @@ decay_f32_kernel(const __grid_constant__ SegArgs ta) {
                     for (int v = 0; v < 2; ++v) {
                         const int d = rev ? j0 + 16 * v - r0 - u : r0 + u - j0 - 16 * v;
                         P[(r0 + u) * L::LP + j0 + 16 * v] =
-                            d >= 0 ? s.so * s.su * pw[max(d, 0)] * (acc[u][v].x + acc[u][v].y) : 0.f;
+                            d >= 0 && j0 + 16 * v < n ? s.so * s.su * pw[max(d, 0)] * (acc[u][v].x + acc[u][v].y) : 0.f;
                     }
                 }
             }

@@ -1,5 +1,5 @@
 // One token for each of N sequences through linear attention with a decay for each value head, in place on
-// the states: S <- a S + k v^T, out = scale S^T q, with a = exp(max(log_decay[h], -100)).  Expanded as
+// the states: S <- a S + k v^T, out = scale S^T q, with a = exp(max(log_decay[h], -100)), NaN for NaN.  Expanded as
 // out = scale (a S_old^T q + (k . q) v), so that the state is read once and written once and the sum over its
 // rows does not wait for the update.
 //
@@ -11,7 +11,7 @@
 // measured copy bandwidth.  What counts is that a CTA's loads are all in flight before its first store: with each row
 // stored as soon as it is loaded the compiler keeps few loads ahead, and it takes 176 us.  Streaming accesses make no
 // difference in this form.
-#include "gdn_internal.cuh"
+#include "decay_unit.cuh"
 
 namespace gdn {
 namespace {
@@ -46,7 +46,7 @@ decay_step_kernel(const __grid_constant__ DecayStepArgs a) {
     const T* q = static_cast<const T*>(a.q) + (size_t)n * a.q_stride + (size_t)hk * DK;
     const T* k = static_cast<const T*>(a.k) + (size_t)n * a.k_stride + (size_t)hk * DK;
     const T* v = static_cast<const T*>(a.v) + (size_t)n * a.v_stride + (size_t)h * DV + sl * CW;
-    const float al = expf(fmaxf(a.log_decay[h], kMinLogDecay));
+    const float al = expf(decay_exponent(a.log_decay[h]));
     float vj[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) vj[e] = to_f32(v[4 * lx + e]);

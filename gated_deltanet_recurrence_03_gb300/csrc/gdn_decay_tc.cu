@@ -92,7 +92,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kThreads = 24 * 32;
 constexpr int kRegsWork = 72, kRegsIssue = 64, kRegsState = 128;
 constexpr int kWarpV = 8, kWarpState = 16, kWarpMma = 20, kWarpCopy = 21;
-constexpr float kStrong = -5.f;   // log decays below this are not factored over 16 columns
+constexpr float kFactored = 5.f;  // log decays of a larger size (or NaN) are not factored over 16 columns
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -199,7 +199,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
     const long long t0 = unit.t0, t1 = unit.t1;
     const int nch = (int)((t1 - t0 + kC - 1) / kC);
     const int tail = (int)(t1 - t0) - (nch - 1) * kC;   // valid tokens of the last chunk
-    const float g = fmaxf(a.log_decay[h], kMinLogDecay);
+    const float g = decay_exponent(a.log_decay[h]);
 
     if (warp == kWarpMma) {
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -214,7 +214,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
         }
         mbar_fence_init();
     }
-    if (tid <= kC) pw[tid] = expf(g * (float)tid);
+    if (tid <= kC) pw[tid] = tid ? expf(g * (float)tid) : 1.f;
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
@@ -433,7 +433,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
                             p[e] = pack_bf16(y);
                         }
                     };
-                    if (g >= kStrong) {   // w_|r - j| = w_(seen - 1) / w_(distance of j from the block's far end)
+                    if (fabsf(g) <= kFactored) {   // w_|r - j| = w_(seen - 1) / w_(distance of j from the block's far end)
                         const float fr = f * exp2f(g2 * (float)max(seen - 1, 0));
 #pragma unroll
                         for (int e = 0; e < 8; ++e)

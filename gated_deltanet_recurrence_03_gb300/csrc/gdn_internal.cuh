@@ -159,7 +159,8 @@ size_t chunked_prefill_workspace_bytes(int B, int T, int Hv, int dk, int dv, int
 cudaError_t launch_chunked_prefill(const PrefillArgs& a);
 
 // ---------------------------------------------------------------- linear attention with a decay per head
-// One decayed scan over the tokens of every sequence, per value head h with a = exp(max(log_decay[h], -100)):
+// One decayed scan over the tokens of every sequence, per value head h with a = exp(max(log_decay[h], -100)) (NaN for a
+// NaN):
 //     forward:  S <- a S + su k_t v_t^T,   out_t = so S^T q_t           (t ascending, S starts at `init`)
 //     reverse:  S <- S + su k_t v_t^T,     out_t = so S^T q_t,  S <- a S   (t descending)
 // `final` gets the last S.  The operator's forward is one such scan; its three gradients are the scans

@@ -341,7 +341,8 @@ gdn_status_t gdn_output_gate_bwd(const void* o, const void* z, const float* norm
  *   q, k        [B, T, Hqk, dk] dtype, token rows q_stride / k_stride elements apart (0 = dense: Hqk dk)
  *   v           [B, T, Hv, dv] dtype, rows v_stride apart (0 = Hv dv).  Slices of one packed q | k | v
  *               projection can be passed directly; strides are multiples of 16 bytes
- *   log_decay   [Hv] float, <= 0 (values below -100, -inf among them, act as -100: exp(-100) leaves nothing)
+ *   log_decay   [Hv] float, <= 0 for a decay (values below -100, -inf among them, act as -100: exp(-100) leaves
+ *               nothing; above 0 the state grows by the same formula, and a NaN makes its head's results NaN)
  *   S0          [nseq, Hv, dk, dv] float or NULL (zero states); nseq = B, or num_seqs when packed
  *   out         [B, T, Hv, dv] dtype, dense; must not overlap any input
  *   S_final     [nseq, Hv, dk, dv] float or NULL (not written); may equal S0 (in-place update)

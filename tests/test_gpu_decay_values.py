@@ -1,5 +1,6 @@
-"""GPU: decays that are not ordinary ones: growths, infinities, values whose powers overflow.  They stay in their head,
-and a call with them ends."""
+"""GPU: decays that are not ordinary ones: growths, infinities, values whose powers overflow, NaN.  They stay in their
+head, a call with them ends, and what the formula makes NaN is NaN."""
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -60,3 +61,25 @@ def test_growths_follow_the_formula(shape):
     for name, want in (("out", out), ("grad_q", gq), ("grad_k", gk), ("grad_v", gv), ("S_final", S), ("grad_S0", gS)):
         for h in range(2):
             close(head(name, want, h), head(name, got[name], h), STATE_TOL if "S" in name else TOL[dtype], (name, h))
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_a_nan_decay_shows(shape):
+    """Everything that a NaN decay multiplies is NaN, in its head only; the gradients of a sequence's last token see no
+    decay and are finite, and sequences without tokens keep their states."""
+    dtype, lens, packed, d = shape
+    x = make(dtype, lens, packed, 3, 3, d, d, seed=22)
+    g = torch.tensor([-0.1, -0.3, -0.01]).cuda()
+    clean = calls(x, g)
+    g[1] = float("nan")
+    got = calls(x, g)
+    a = [f64(x[n]) for n in "qkv"] + [f64(g)]
+    out, S = od.forward(*a, f64(x["S0"]), 0.1, x["cu"])
+    gq, gk, gv, gS = od.backward(*a, f64(x["do"]), f64(x["S0"]), f64(x["dS"]), 0.1, x["cu"])
+    want = {"out": out, "S_final": S, "grad_q": gq, "grad_k": gk, "grad_v": gv, "grad_S0": gS}
+    n = len(lens)
+    want["step"], want["pool"] = od.step(*(f64(x[m][0, :n]) for m in "qkv"), f64(g), f64(x["S0"]), scale=0.1)
+    for name, w in want.items():
+        for h in (0, 2):
+            assert torch.equal(head(name, got[name], h), head(name, clean[name], h)), (name, h)
+        assert np.array_equal(np.isnan(head(name, w, 1)), np.isnan(f64(head(name, got[name], 1)))), name
