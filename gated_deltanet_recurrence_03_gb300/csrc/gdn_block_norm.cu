@@ -20,8 +20,8 @@
 #include <algorithm>
 #include <atomic>
 
+#include "bulk_ring.cuh"
 #include "gdn_internal.cuh"
-#include "tc_ptx.cuh"
 
 namespace gdn {
 namespace {
@@ -123,34 +123,8 @@ __device__ __forceinline__ V8 gate8(const V8& u) {
     return s;
 }
 
-// The rows a group will need, in shared memory ahead of their use: `stages` rows of N tensors, each row's pieces
-// copied by one thread with bulk copies that complete on the stage's mbarrier.
-template <typename T, int N>
-struct Ring {
-    const void* src[N];
-    uint8_t* base;
-    uint32_t bar;
-    int D, stages;
-    volatile int* abort;
-    unsigned* status;
-    __device__ __forceinline__ void issue(int k, long long row) const {
-        const uint32_t bytes = (uint32_t)D * sizeof(T), b = bar + 8 * (k % stages);
-        uint32_t to = tc::smem_u32(base) + (k % stages) * N * bytes;
-        tc::mbar_arrive_expect_tx(b, N * bytes);
-#pragma unroll
-        for (int t = 0; t < N; ++t) tc::bulk_g2s(to + t * bytes, static_cast<const T*>(src[t]) + (size_t)row * D, bytes, b);
-    }
-    __device__ __forceinline__ void wait(int k) const {   // a wait that gives up sets the status; the rows are then wrong
-        tc::mbar_wait_bounded(bar + 8 * (k % stages), (uint32_t)(k / stages) & 1, abort, status, kStatusTimeout, kWaitLimitNs);
-    }
-    __device__ __forceinline__ const T* at(int k, int t) const {
-        return reinterpret_cast<const T*>(base) + (size_t)((k % stages) * N + t) * D;
-    }
-};
-
 // Shared memory of a block: the groups' reduction buffers (two of 64 floats each), mbarriers, the columns'
 // constants m = w_post c and w_pre, and the groups' rings.
-constexpr int kMaxStages = 4;
 struct Smem {
     float *red, *m, *wq;
     uint64_t* bars;
@@ -161,18 +135,18 @@ __device__ __forceinline__ Smem carve(uint8_t* p, int groups, int D) {
     Smem s;
     s.red = reinterpret_cast<float*>(p);
     s.bars = reinterpret_cast<uint64_t*>(s.red + groups * 128);
-    s.abort = reinterpret_cast<int*>(s.bars + groups * kMaxStages);
+    s.abort = reinterpret_cast<int*>(s.bars + groups * kRingWords);
     s.m = reinterpret_cast<float*>(s.abort + 4);
     s.wq = s.m + D;
     s.rings = reinterpret_cast<uint8_t*>(s.wq + D);
     return s;
 }
 size_t smem_bytes(int groups, int D, int row_bytes, int stages) {
-    return (size_t)groups * 128 * 4 + groups * kMaxStages * 8 + 16 + (size_t)2 * D * 4 + (size_t)groups * stages * row_bytes;
+    return (size_t)groups * 128 * 4 + groups * kRingWords * 8 + 16 + (size_t)2 * D * 4 + (size_t)groups * stages * row_bytes;
 }
 __device__ __forceinline__ void set_up(const Smem& s, const BlockNormArgs& a, int groups) {
     for (int i = threadIdx.x; i < groups * 128; i += blockDim.x) s.red[i] = 0.f;
-    for (int i = threadIdx.x; i < groups * kMaxStages; i += blockDim.x) tc::mbar_init(tc::smem_u32(s.bars + i), 1);
+    if ((int)threadIdx.x < groups) ring_init(s.bars + threadIdx.x * kRingWords);
     if (threadIdx.x == 0) *s.abort = 0;
     tc::mbar_fence_init();
     for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
@@ -194,23 +168,25 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormArgs a, int tpr, int stag
     float* const red = sm.red + g.id * 128;
     const float invD = 1.f / (float)a.D;
     const bool one = !GATE && a.gate;
-    Ring<T, N> ring;
+    BulkRing<T, N> ring;
     ring.src[0] = a.b;
     ring.src[1] = a.x;
     if constexpr (GATE) ring.src[2] = a.gate;
     ring.base = sm.rings + (size_t)g.id * stages * N * a.D * sizeof(T);
-    ring.bar = tc::smem_u32(sm.bars + g.id * kMaxStages);
+    ring.bars = sm.bars + g.id * kRingWords;
     ring.D = a.D;
     ring.stages = stages;
     ring.abort = sm.abort;
     ring.status = a.status;
+    ring.status_flag = kStatusTimeout;
+    ring.limit_ns = kWaitLimitNs;
     const long long step = (long long)gridDim.x * groups, first = (long long)blockIdx.x * groups + g.id;
     if (g.tid == 0)
         for (int k = 0; k < stages && first + k * step < a.rows; ++k) ring.issue(k, first + k * step);
     int k = 0;
     for (long long row = first; row < a.rows; row += step, ++k) {
         const float logit = one ? to_f32(static_cast<const T*>(a.gate)[row]) : 0.f;
-        ring.wait(k);
+        const bool go = ring.wait(k);
         const T *pb = ring.at(k, 0), *px = ring.at(k, 1), *pu = GATE ? ring.at(k, N - 1) : nullptr;
         float2 q = make_float2(0.f, 0.f);
 #pragma unroll
@@ -225,7 +201,7 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormArgs a, int tpr, int stag
         float sum[1] = {q.x + q.y};
         group_sum(sum, red, g);
         // past this every thread of the group has finished the previous row: its stage is free
-        if (g.tid == 0 && k > 0 && stages > 1 && row + (stages - 1) * step < a.rows)
+        if (g.tid == 0 && go && k > 0 && stages > 1 && row + (stages - 1) * step < a.rows)
             ring.issue(k + stages - 1, row + (stages - 1) * step);
         const float ib = rsqrtf(fmaf(sum[0], invD, a.eps)) * (one ? sigmoid_f(logit) : 1.f);
         V8 r[V];
@@ -265,9 +241,10 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormArgs a, int tpr, int stag
         }
         if (stages == 1 && row + step < a.rows) {
             group_sync(g);
-            if (g.tid == 0) ring.issue(k + 1, row + step);
+            if (g.tid == 0 && go) ring.issue(k + 1, row + step);
         }
     }
+    if (g.tid == 0) ring.drain();
 }
 
 // Backward.  With m = w_post c everything but the weights' sums needs only m and w_pre: e = dx s m (= dy w_post),
@@ -286,18 +263,20 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, float* __restrict
     float* const red = sm.red + g.id * 128;
     const float invD = 1.f / (float)a.D;
     const bool one = !GATE && a.gate;
-    Ring<T, N> ring;
+    BulkRing<T, N> ring;
     ring.src[0] = a.b;
     ring.src[1] = a.x;
     ring.src[2] = a.gn;
     ring.src[3] = a.gr;
     if constexpr (GATE) ring.src[4] = a.gate;
     ring.base = sm.rings + (size_t)g.id * stages * N * a.D * sizeof(T);
-    ring.bar = tc::smem_u32(sm.bars + g.id * kMaxStages);
+    ring.bars = sm.bars + g.id * kRingWords;
     ring.D = a.D;
     ring.stages = stages;
     ring.abort = sm.abort;
     ring.status = a.status;
+    ring.status_flag = kStatusTimeout;
+    ring.limit_ns = kWaitLimitNs;
     const long long step = (long long)gridDim.x * groups, first = (long long)blockIdx.x * groups + g.id;
     if (g.tid == 0)
         for (int k = 0; k < stages && first + k * step < a.rows; ++k) ring.issue(k, first + k * step);
@@ -309,7 +288,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, float* __restrict
     int k = 0;
     for (long long row = first; row < a.rows; row += step, ++k) {
         const float logit = one ? to_f32(static_cast<const T*>(a.gate)[row]) : 0.f;
-        ring.wait(k);
+        const bool go = ring.wait(k);
         const T *pb = ring.at(k, 0), *px = ring.at(k, 1), *pn = ring.at(k, 2), *pr = ring.at(k, 3),
                 *pu = GATE ? ring.at(k, N - 1) : nullptr;
         float2 q = make_float2(0.f, 0.f);
@@ -325,7 +304,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, float* __restrict
         float s1[1] = {q.x + q.y};
         group_sum(s1, red, g);
         // past this every thread of the group has finished the previous row: its stage is free
-        if (g.tid == 0 && k > 0 && stages > 1 && row + (stages - 1) * step < a.rows)
+        if (g.tid == 0 && go && k > 0 && stages > 1 && row + (stages - 1) * step < a.rows)
             ring.issue(k + stages - 1, row + (stages - 1) * step);
         const float ib = rsqrtf(fmaf(s1[0], invD, a.eps));
         const float gate1 = one ? sigmoid_f(logit) : 1.f;
@@ -399,9 +378,10 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, float* __restrict
         if (one && g.tid == 0) static_cast<T*>(a.ggate)[row] = from_f32<T>(s3[0] * (1.f - gate1));
         if (stages == 1 && row + step < a.rows) {
             group_sync(g);
-            if (g.tid == 0) ring.issue(k + 1, row + step);
+            if (g.tid == 0 && go) ring.issue(k + 1, row + step);
         }
     }
+    if (g.tid == 0) ring.drain();
     if (!part) return;
     float* p = part + (size_t)blockIdx.x * 2 * a.D;
     float* const sums = sm.m;   // [2 D]: the constants are done with
@@ -474,7 +454,7 @@ Shape shape_of(int D, long long rows, int row_bytes) {
     if (s.tpr > 32) s.groups = std::min(s.groups, 8);
     s.groups = (int)std::min<long long>(s.groups, std::max(1LL, (rows + 151) / 152));   // few rows: every SM has some
     while (s.groups > 1 && smem_bytes(s.groups, D, row_bytes, 2) > kSmemMax) --s.groups;
-    s.stages = kMaxStages;
+    s.stages = kRingMaxStages;
     while (s.stages > 1 && smem_bytes(s.groups, D, row_bytes, s.stages) > kSmemMax) --s.stages;
     s.blocks = (int)std::min<long long>(152, (rows + s.groups - 1) / s.groups);
     s.smem = smem_bytes(s.groups, D, row_bytes, s.stages);
