@@ -166,6 +166,21 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
     return false;
 }
 
+// The same by a whole warp: one answer for all lanes, which must not part where one of them gives up.  (A vote
+// after a wait of each lane's own makes the compiler spill: 160 us instead of 140 for 2 x 8192 tokens.)
+__device__ __forceinline__ bool warp_wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort, unsigned* status) {
+    if (__all_sync(~0u, try_wait_long(bar, parity))) return true;
+    const unsigned long long t0 = globaltimer();
+    while (true) {
+        if (__any_sync(~0u, *abort)) return false;
+        if (__all_sync(~0u, try_wait_long(bar, parity))) return true;
+        if (globaltimer() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            atomicOr(status, kStatusTimeout);
+        }
+    }
+}
+
 __device__ __forceinline__ int slot_of(const DecayArgs& a) { return blockIdx.x / (a.dv > kHalf ? 2 : 1) / a.Hv; }
 
 // One scan's CTA.  REV: a reverse scan; F32: the outputs are float; PARTS: bf16 parts of the scaled V (three where
@@ -221,9 +236,10 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);   // this warp's quarter of the lanes
 
     unsigned* status = a.status;
-    auto wait = [&](uint32_t b, uint32_t parity) {
+    auto wait_one = [&](uint32_t b, uint32_t parity) {
         return wait_or_abort(bar(b), parity & 1, abort_flag, status);
     };
+    auto wait = [&](uint32_t b, uint32_t parity) { return warp_wait_or_abort(bar(b), parity & 1, abort_flag, status); };
     auto arrive = [&](uint32_t b) {   // once for the warp, after all its lanes
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(b));
@@ -268,15 +284,14 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
             for (int x = 0; x < 2; ++x) decay_power(g, (float)(x ? tail : kC), gamma[2 * x], gamma[2 * x + 1]);   // of a full, of the last chunk
             mbar_arrive(bar(B_GAMMA));
             for (; loaded < nch; ++loaded) {   // into the stage of the chunk two back
-                if (!wait(B_FREE + (loaded & 1), (loaded >> 1) - 1)) break;
+                if (!wait_one(B_FREE + (loaded & 1), (loaded >> 1) - 1)) break;
                 load(loaded);
                 prefetch(loaded + 2);
             }
-            if (*abort_flag) {   // a wait gave up: no copy may still be landing when the shared memory is released
-                for (int it = max(0, loaded - 2); it < loaded; ++it) {
-                    mbar_wait_drain(bar(B_FULLQK + (it & 1)), (it >> 1) & 1, kWaitLimitNs);
-                    mbar_wait_drain(bar(B_FULLV + (it & 1)), (it >> 1) & 1, kWaitLimitNs);
-                }
+            // whichever wait gives up, now or later: no copy may still be landing when the shared memory is released
+            for (int it = max(0, loaded - 2); it < loaded; ++it) {
+                mbar_wait_drain(bar(B_FULLQK + (it & 1)), (it >> 1) & 1, kWaitLimitNs);
+                mbar_wait_drain(bar(B_FULLV + (it & 1)), (it >> 1) & 1, kWaitLimitNs);
             }
         }
         __syncwarp();
@@ -294,7 +309,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
             if (it >= 0) {
                 // K^T V~: V's parts are there (and, in a last chunk, the rows past its end are zero)
                 ok = wait(B_VP, it) && (it < 1 || wait(B_KVFREE, it - 1));
-                if (!__all_sync(~0u, ok)) break;
+                if (!ok) break;
                 tc_fence_after();
                 // (rows past dk of the product come from whatever lies behind k's panel: nothing reads them)
                 const uint64_t kt = dKt + ((st * 2 * kPanel) >> 4);
@@ -308,7 +323,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
                 }
                 __syncwarp();
                 ok = wait(B_VP + 1, it);
-                if (!__all_sync(~0u, ok)) break;
+                if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -322,13 +337,13 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
             }
             if (STATE) {   // the next chunk's k (with scores to form, its arrival is waited for below)
                 if (it + 1 < nch) ok = wait(B_FULLQK + ((it + 1) & 1), (it + 1) >> 1);
-                if (!__all_sync(~0u, ok)) break;
+                if (!ok) break;
                 continue;
             }
             // the next chunk's scores: P is formed from them while this chunk's outputs and the next KV and QS run
             if (it + 1 < nch) {
                 ok = wait(B_FULLQK + ((it + 1) & 1), (it + 1) >> 1) && (it < 0 || wait(B_QKFREE, it));
-                if (!__all_sync(~0u, ok)) break;
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t o = (((it + 1) & 1) * 2 * kPanel) >> 4;
                 if (elect_one()) {
@@ -345,7 +360,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
             if (it >= 0) {
                 const uint64_t q = dQ + ((st * 2 * kPanel) >> 4);
                 ok = wait(B_S, it) && (it < 1 || wait(B_OFREE, it - 1));
-                if (!__all_sync(~0u, ok)) break;
+                if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -365,7 +380,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
                 }
                 __syncwarp();
                 ok = wait(B_P, it);
-                if (!__all_sync(~0u, ok)) break;
+                if (!ok) break;
                 tc_fence_after();
                 const uint64_t v = dV + ((st * kPanel) >> 4);
                 if (elect_one()) {
@@ -516,11 +531,11 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
         uint8_t* const out = static_cast<uint8_t*>(s.out) + ((size_t)h * dv + kHalf * z) * esize +
                              (F32 ? (chunk >> 2) * 128 + (chunk & 3) * 16 : chunk * 16);
         const size_t pitch = (size_t)s.out_stride * esize;
-        for (int it = -1; it < nch; ++it) {
-            if (it + 1 < nch && !split(it + 1)) break;
-            if (STATE || it < 0) continue;
+        // A wait that gives up leaves its warp going on with whatever is there, until the pair decides at a barrier: a warp
+        // that stopped alone would leave its partner waiting there for ever.
+        auto write_outputs = [&](int it) {
             const int n = valid_of(it);
-            if (!wait(B_O, it)) break;
+            wait(B_O, it);
             tc_fence_after();
             const float w = s.so * pw[rev ? max(n - 1 - r, 0) : r + 1];
             uint8_t* const first = out + (size_t)(t0 + (long long)chunk_of(it) * kC) * pitch;
@@ -538,7 +553,12 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     o[e] = fma2(make_float2(w, w), as_float2(qs[2 * e], qs[2 * e + 1]), as_float2(pv[2 * e], pv[2 * e + 1]));
-                if (F32 || PARTS == 2 && !b) named_barrier_sync(pair, 64);   // the rows staged before have been read
+                // (the rows staged before have been read)
+                if (PARTS == 2 && !b) {
+                    if (!named_barrier_all(pair, 64, !*abort_flag)) return false;
+                } else if (F32) {
+                    named_barrier_sync(pair, 64);
+                }
                 if (F32) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
@@ -551,7 +571,11 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
                             make_uint4(pack_bf16(o[4 * c]), pack_bf16(o[4 * c + 1]), pack_bf16(o[4 * c + 2]), pack_bf16(o[4 * c + 3]));
                 }
                 if (F32 || b) {
-                    named_barrier_sync(pair, 64);
+                    if (PARTS == 3) {
+                        if (!named_barrier_all(pair, 64, !*abort_flag)) return false;
+                    } else {
+                        named_barrier_sync(pair, 64);
+                    }
 #pragma unroll
                     for (int x = 0; x < 16; x += 4)
                         if (own + x < n && (F32 ? 32 * (chunk >> 2) + 16 * b + 4 * (chunk & 3) : 8 * chunk) < width)
@@ -560,6 +584,11 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
                 }
             }
             if (PARTS == 3) arrive(B_SBFREE);
+            return true;
+        };
+        for (int it = -1; it < nch; ++it) {
+            if (it + 1 < nch && !split(it + 1) && STATE) break;
+            if (!STATE && it >= 0 && !write_outputs(it)) break;
         }
     } else {
         // ------------------------------------------------------------ the state: row R of dk, 64 columns a thread

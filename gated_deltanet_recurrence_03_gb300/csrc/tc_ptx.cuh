@@ -86,6 +86,21 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     }
 }
 
+// Named barrier of `threads` threads (whole warps), and whether ok held in all of them: a decision that each has made for
+// itself, after a wait that may have run out, made theirs in common.
+__device__ __forceinline__ bool named_barrier_all(int id, int threads, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "bar.red.and.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(id), "r"(threads), "r"((uint32_t)ok)
+        : "memory");
+    return all != 0;
+}
+
 // Give up registers down to N a thread, or take some up to N: all four warps of an aligned group of four execute
 // one of them, and the shares add up to at most what the block was launched with.
 template <int N>

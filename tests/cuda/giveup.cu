@@ -61,7 +61,38 @@ ring_kernel(const float* src, float* dst, int rows, int stages, int drop, unsign
     }
 }
 
+// Two warps that hand rows to each other through a named barrier, as the decayed scan's output warps do: each waits for
+// an arrival of its own in every round, and the pair decides at the barrier.  Warp 1's arrival of round `drop` never
+// comes.  result = {rounds that warp 0 finished, rounds that warp 1 finished}.
+__global__ void __launch_bounds__(64, 1)
+pair_kernel(int rounds, int drop, unsigned long long limit_ns, unsigned* status, int* result) {
+    __shared__ __align__(8) uint64_t bars[2];
+    __shared__ int abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < 2; ++i) gdn::tc::mbar_init(gdn::tc::smem_u32(bars + i), 1);
+        gdn::tc::mbar_fence_init();
+    }
+    __syncthreads();
+    int done = 0;
+    for (int it = 0; it < rounds; ++it) {
+        const uint32_t bar = gdn::tc::smem_u32(bars + warp);
+        if (lane == 0 && (warp == 0 || it != drop)) gdn::tc::mbar_arrive(bar);
+        bool ok = __all_sync(~0u, gdn::tc::mbar_wait_bounded(bar, it & 1, &abort_flag, status, 1u, limit_ns));
+        ok = gdn::tc::named_barrier_all(1, 64, ok);
+        if (!ok) break;
+        ++done;
+    }
+    if (lane == 0) result[warp] = done;
+}
+
 }  // namespace
+
+extern "C" int giveup_pair(int rounds, int drop, unsigned long long limit_ns, unsigned* status, int* result) {
+    pair_kernel<<<1, 64>>>(rounds, drop, limit_ns, status, result);
+    return cudaGetLastError() == cudaSuccess ? 0 : 3;
+}
 
 extern "C" int giveup_ring(const float* src, float* dst, int rows, int stages, int drop, unsigned long long limit_ns,
                            unsigned* status, int* result) {

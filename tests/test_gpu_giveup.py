@@ -29,6 +29,7 @@ def lib():
         subprocess.check_call([b._nvcc(), *b.NVCC_FLAGS, "-shared", "-o", LIB, SRC])
     L = ctypes.CDLL(LIB)
     L.giveup_ring.argtypes = [ctypes.c_void_p] * 2 + [ctypes.c_int] * 3 + [ctypes.c_ulonglong] + [ctypes.c_void_p] * 2
+    L.giveup_pair.argtypes = [ctypes.c_int] * 2 + [ctypes.c_ulonglong] + [ctypes.c_void_p] * 2
     return L
 
 
@@ -53,3 +54,14 @@ def test_a_ring_whose_copy_never_lands_asks_for_no_more(lib, stages, drop):
     # stages - 2 ahead (the first ones: all stages)
     asked = max(drop + 1, stages) if drop == 0 or stages == 1 else drop + stages - 1
     assert result.tolist() == [min(rows, asked), 1]
+
+
+@pytest.mark.parametrize("drop", [-1, 0, 1, 4])
+def test_a_pair_of_warps_gives_up_together(lib, drop):
+    status, result = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    t0 = time.time()
+    assert lib.giveup_pair(5, drop, LIMIT, status.data_ptr(), result.data_ptr()) == 0
+    torch.cuda.synchronize()
+    assert time.time() - t0 < 5.0
+    assert int(status) == (drop >= 0) and result.tolist() == [5 if drop < 0 else drop] * 2
