@@ -594,6 +594,8 @@ def _scratch(o, need, workspace, like):
     fp32 tensor); returns the tensor to keep alive."""
     if not need:
         return None
+    if workspace is not None and (workspace.device != like.device or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = like.new_empty((need + 3) // 4)
     o.workspace = workspace.data_ptr()

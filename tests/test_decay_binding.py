@@ -59,3 +59,17 @@ def test_broadcast_inputs_are_refused_by_the_calls():
             api.gdn_decay_attn_bwd(q, k, w, g, None, v)
         with pytest.raises(ValueError, match="token rows"):
             api.gdn_decay_attn_step(q[0], k[0], w[0], g, S)
+
+
+def test_workspaces_taken_and_refused():
+    like = torch.zeros(2)
+    o = pkg_lib.GdnOpts()
+    given = torch.empty(300, dtype=torch.uint8)
+    assert api._scratch(o, 256, given, like) is given and o.workspace == given.data_ptr() and o.workspace_bytes == 300
+    assert api._scratch(o, 0, given, like) is None
+    new = api._scratch(o, 1001, given, like)   # too small: a new one
+    assert new is not given and new.device == like.device and o.workspace_bytes >= 1001 and o.workspace == new.data_ptr()
+    for bad in (torch.empty(300, dtype=torch.uint8, device="meta"),           # of another device
+                torch.empty(1, dtype=torch.uint8).expand(300), given[::2]):   # more elements than memory, or not its own
+        with pytest.raises(ValueError, match="workspace"):
+            api._scratch(o, 100, bad, like)
