@@ -645,7 +645,7 @@ gdn_status_t need_workspace(const gdn_opts_t& o, size_t need) {
 }
 
 // Sequences and packing of a call over whole sequences; false (with *st set) on an argument error.
-bool decay_sequences(int B, int T, const gdn_opts_t& o, int* nseq, gdn_status_t* st) {
+bool decay_sequences(int B, int T, int Hv, const gdn_opts_t& o, int* nseq, gdn_status_t* st) {
     *st = GDN_OK;
     if (B < 0 || T < 0) *st = fail(GDN_ERR_INVALID_ARG, "B=%d T=%d must be >= 0", B, T);
     else if (o.cu_seqlens && (B != 1 || o.num_seqs < 1))
@@ -654,6 +654,8 @@ bool decay_sequences(int B, int T, const gdn_opts_t& o, int* nseq, gdn_status_t*
         *st = fail(GDN_ERR_INVALID_ARG, "cu_seqlens must be 4-byte aligned");
     else if ((long long)B * T > INT32_MAX) *st = fail(GDN_ERR_INVALID_ARG, "more than 2^31 - 1 tokens");
     *nseq = o.cu_seqlens ? o.num_seqs : B;
+    if (*st == GDN_OK && (long long)*nseq * Hv > INT32_MAX / 16)   // up to 16 blocks each in one grid
+        *st = fail(GDN_ERR_INVALID_ARG, "%d sequences of %d heads are too many", *nseq, Hv);
     return *st == GDN_OK;
 }
 
@@ -693,7 +695,7 @@ gdn_status_t gdn_decay_attn_fwd(const void* q, long long q_stride, const void* k
     const gdn_opts_t o = resolve(opts);
     gdn_status_t st;
     int nseq;
-    if (!decay_sequences(B, T, o, &nseq, &st)) return st;
+    if (!decay_sequences(B, T, Hv, o, &nseq, &st)) return st;
     if ((st = decay_common(Hqk, Hv, dk, dv, o, log_decay, &q_stride, &k_stride, &v_stride)) != GDN_OK) return st;
     const bool have_tokens = (long long)B * T > 0;
     if (have_tokens && (!q || !k || !v || !log_decay || !out))
@@ -770,7 +772,7 @@ gdn_status_t gdn_decay_attn_bwd(const void* q, long long q_stride, const void* k
     const gdn_opts_t o = resolve(opts);
     gdn_status_t st;
     int nseq;
-    if (!decay_sequences(B, T, o, &nseq, &st)) return st;
+    if (!decay_sequences(B, T, Hv, o, &nseq, &st)) return st;
     if ((st = decay_common(Hqk, Hv, dk, dv, o, log_decay, &q_stride, &k_stride, &v_stride)) != GDN_OK) return st;
     if ((st = decay_common(Hqk, Hv, dk, dv, o, log_decay, &gq_stride, &gk_stride, &gv_stride)) != GDN_OK) return st;
     const bool have_tokens = (long long)B * T > 0;

@@ -73,3 +73,17 @@ def test_workspaces_taken_and_refused():
                 torch.empty(1, dtype=torch.uint8).expand(300), given[::2]):   # more elements than memory, or not its own
         with pytest.raises(ValueError, match="workspace"):
             api._scratch(o, 100, bad, like)
+
+
+def test_more_blocks_than_a_grid_holds_are_refused():
+    """2^26 + 1 empty or short sequences of 64 heads: the grid's blocks would pass 32 bits and only a few would run."""
+    import ctypes
+    lib, fake = pkg_lib.load(), 0x10000
+    o = pkg_lib.default_opts(lib)
+    o.cu_seqlens, o.num_seqs = fake, 2 ** 26 + 1
+    dims = (1, 8, 64, 64, 128, 128, ctypes.byref(o))
+    assert lib.gdn_decay_attn_fwd(fake, 0, fake, 0, fake, 0, fake, None, fake, None, *dims) == pkg_lib.GDN_ERR_INVALID_ARG
+    assert b"sequences" in lib.gdn_last_error()
+    assert lib.gdn_decay_attn_bwd(fake, 0, fake, 0, fake, 0, fake, None, fake, None, fake, 0, fake, 0, fake, 0, None,
+                                  *dims) == pkg_lib.GDN_ERR_INVALID_ARG
+    assert b"sequences" in lib.gdn_last_error()
