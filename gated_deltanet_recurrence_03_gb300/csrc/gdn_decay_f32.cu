@@ -205,8 +205,11 @@ decay_f32_kernel(const __grid_constant__ SegArgs ta) {
             }
             __syncthreads();
             if (rg < L::OT) {
-#pragma unroll 2
-                for (int j = 0; j < kC; j += 4) {
+                // P V over the columns that the rows see: a value of V that is not finite would make NaN of a masked
+                // zero.  A warp's rows lie in one block of four columns, whose masked values act as zeros.
+                static_assert(L::OR * (32 / L::CG) <= 4, "rows of a warp");
+                const int diag = rg * L::OR / 4 * 4;
+                const auto add = [&](int j, bool masked) {
                     float x[L::OR][4];
 #pragma unroll
                     for (int r = 0; r < L::OR; ++r) load_vec(P + (rg * L::OR + r) * L::LP + j, x[r]);
@@ -215,11 +218,16 @@ decay_f32_kernel(const __grid_constant__ SegArgs ta) {
                         const float4 y = *reinterpret_cast<const float4*>(V + (j + u) * L::LV + 4 * cg);
 #pragma unroll
                         for (int r = 0; r < L::OR; ++r) {
+                            const int row = rg * L::OR + r;
+                            if (masked && (rev ? j + u < row : j + u > row)) continue;
                             O[r][0] = fma2(all2(x[r][u]), make_float2(y.x, y.y), O[r][0]);
                             O[r][1] = fma2(all2(x[r][u]), make_float2(y.z, y.w), O[r][1]);
                         }
                     }
-                }
+                };
+#pragma unroll 2
+                for (int j = rev ? diag + 4 : 0; j < (rev ? kC : diag); j += 4) add(j, false);
+                add(diag, true);
 #pragma unroll
                 for (int r = 0; r < L::OR; ++r) {
                     const int row = rg * L::OR + r;

@@ -30,10 +30,11 @@
 // half of the SMs idle here.
 //
 // Warps: 0-7 form P; 8-15 scale and split V and write the outputs; 16-19 keep the state; 20 issues the MMAs, 21
-// the copies.  Hand-overs are mbarriers; every wait is bounded.
+// the copies; 22 and 23 see to values of V that are not finite.  Hand-overs are mbarriers; every wait on one is bounded.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <climits>
 #include <mutex>
 
 #include "decay_unit.cuh"
@@ -61,7 +62,9 @@ constexpr uint32_t S_OUT = S_VP + 2 * kPanel;        // with two parts: the outp
 constexpr uint32_t S_BAR = S_SB + kPanel;
 constexpr uint32_t kBarBytes = 256;
 constexpr uint32_t S_PW = S_BAR + kBarBytes;         // w_0 .. w_128
-constexpr uint32_t kSmem = S_PW + 132 * 4 + 1024;
+constexpr uint32_t S_ODD = S_PW + 132 * 4;           // 64 columns of V: the first token with a value that is not finite
+constexpr uint32_t kSmem = S_ODD + 64 * 4 + 1024;
+static_assert(kSmem <= 227 * 1024, "shared memory");
 
 enum Bar : uint32_t {
     B_FULLQK = 0,   // 2: q and k tiles of a stage have landed
@@ -91,6 +94,7 @@ constexpr uint32_t kTmemCols = 512;
 // warps' 16, and the state's takes them (64 hold its part of the state): 4 x 72 + 128 + 64 = 6 x 80.
 constexpr int kThreads = 24 * 32;
 constexpr int kRegsWork = 72, kRegsIssue = 64, kRegsState = 128;
+constexpr int kBarOutputs = 5;   // named barriers: 1-4 the pairs of output warps
 constexpr int kWarpV = 8, kWarpState = 16, kWarpMma = 20, kWarpCopy = 21;
 constexpr float kFactored = 5.f;  // log decays of a larger size (or NaN) are not factored over 16 columns
 
@@ -199,6 +203,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S_BAR + 8 * B_COUNT + 4);
     float* gamma = reinterpret_cast<float*>(sm + S_BAR + 8 * B_COUNT + 8);   // w_128, w_n of the last chunk: hi, lo each
     float* pw = reinterpret_cast<float*>(sm + S_PW);
+    int* odd = reinterpret_cast<int*>(sm + S_ODD);
 
     const DecayArgs& a = ta.a;
     const DecayScan& s = a.scan[blockIdx.y];
@@ -229,6 +234,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
         }
         mbar_fence_init();
     }
+    if (tid < 64) odd[tid] = INT_MAX;
     if (tid <= kC) pw[tid] = tid ? expf(g * (float)tid) : 1.f;
     __syncthreads();
     tc_fence_after();
@@ -248,7 +254,22 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
     auto valid_of = [&](int it) { return chunk_of(it) == nch - 1 ? tail : kC; };
 
     if (warp > kWarpCopy) {
-        regs_dec<kRegsIssue>();   // only there to make the group of four whole
+        regs_dec<kRegsIssue>();   // there to make the group of four whole, and for columns of V that are not finite
+        // (in the output warps the same code takes 2 to 5 % of the gradients' time, wherever it stands)
+        if (!STATE) {
+            named_barrier_sync(kBarOutputs, 320);   // every output is written
+            const int c = tid & 63, from = odd[c];
+            if (from != INT_MAX && c < width) {
+                const int it = from / kC, n = valid_of(it);
+#pragma unroll 1
+                for (int v = from % kC; v < n; ++v) {
+                    const size_t e = (size_t)(t0 + (long long)chunk_of(it) * kC + (rev ? n - 1 - v : v)) * s.out_stride +
+                                     (size_t)h * dv + kHalf * z + c;
+                    if (F32) static_cast<uint32_t*>(s.out)[e] = 0x7fffffffu;   // NaN
+                    else static_cast<uint16_t*>(s.out)[e] = 0x7fffu;
+                }
+            }
+        }
     } else if (warp == kWarpCopy) {
         regs_dec<kRegsIssue>();
         // ------------------------------------------------------------ copies
@@ -507,16 +528,31 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
             for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(sm + S_V + st * kPanel + swz(r, c0 + c));
             // the products of the previous chunk that read these rows' parts are complete
             if (it > 0 && !wait(half ? B_KV : B_KVHALF, it - 1)) return false;
+            float2 zero = make_float2(0.f, 0.f);   // NaN after a value that is not finite
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const uint32_t y[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
                 uint32_t o[4][PARTS];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    split_bf16<PARTS>(mul2(make_float2(w, w), as_float2(y[e] << 16, y[e] & 0xffff0000u)), o[e]);
+                for (int e = 0; e < 4; ++e) {
+                    const float2 x = as_float2(y[e] << 16, y[e] & 0xffff0000u);
+                    split_bf16<PARTS>(mul2(make_float2(w, w), x), o[e]);
+                    if (!STATE) zero = fma2(x, make_float2(0.f, 0.f), zero);
+                }
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p)
                     *reinterpret_cast<uint4*>(sm + S_VP + p * kPanel + swz(r, c0 + c)) = make_uint4(o[0][p], o[1][p], o[2][p], o[3][p]);
+            }
+            if (!STATE && !(zero.x + zero.y == 0.f)) {
+                // It would make NaN of a masked zero of P.  So it leaves V's panel, and a warp apart makes its column's outputs
+                // of the chunk NaN from its token on; later chunks see it through the state.
+#pragma unroll 1
+                for (int c = 8 * c0; c < 8 * c0 + 32; ++c) {
+                    uint16_t* x = reinterpret_cast<uint16_t*>(sm + S_V + st * kPanel + swz(r, c >> 3)) + (c & 7);
+                    if ((*x & 0x7f80) != 0x7f80) continue;
+                    *x = 0;
+                    atomicMin(odd + c, it * kC + (rev ? n - 1 - r : r));
+                }
             }
             fence_proxy_async_smem();
             arrive(B_VP + half);
@@ -590,6 +626,7 @@ __device__ __forceinline__ void decay_tc_body(const TcArgs& ta, const Unit& unit
             if (it + 1 < nch && !split(it + 1) && STATE) break;
             if (!STATE && it >= 0 && !write_outputs(it)) break;
         }
+        if (!STATE) named_barrier_sync(kBarOutputs, 320);
     } else {
         // ------------------------------------------------------------ the state: row R of dk, 64 columns a thread
         regs_inc<kRegsState>();

@@ -348,7 +348,8 @@ gdn_status_t gdn_output_gate_bwd(const void* o, const void* z, const float* norm
  *   S_final     [nseq, Hv, dk, dv] float or NULL (not written); may equal S0 (in-place update)
  * Supported: dk, dv in {32, 64, 128}; Hv a multiple of Hqk; B, T >= 0, sequences of no tokens included
  * (their S_final is S0, or zeros), nseq Hv < 2^27, B T < 2^31.  States, sums and decays are fp32.  A value (a NaN, say) in one
- * sequence's tokens never reaches another sequence's results.  opts->workspace: 256-byte aligned, of
+ * sequence's tokens never reaches another sequence's results, nor results of its own that the formula does not
+ * give it to (earlier tokens' outputs).  opts->workspace: 256-byte aligned, of
  * gdn_decay_attn_fwd_workspace_size bytes (GDN_ERR_WORKSPACE if that is not 0 and it is missing or too
  * small).  opts->flags must be 0; dtype, scale, cu_seqlens, num_seqs, stream and events[0] / [1] (around
  * the kernels) are used.  Errors otherwise as for gdn_chunk_fwd.

@@ -1,5 +1,6 @@
 """GPU: decays that are not ordinary ones: growths, infinities, values whose powers overflow, NaN.  They stay in their
-head, a call with them ends, and what the formula makes NaN is NaN."""
+head, a call with them ends, and what the formula makes NaN is NaN.  Inputs that are not finite reach what the formula
+gives them to, and nothing else."""
 import numpy as np
 import pytest
 
@@ -83,3 +84,37 @@ def test_a_nan_decay_shows(shape):
         for h in (0, 2):
             assert torch.equal(head(name, got[name], h), head(name, clean[name], h)), (name, h)
         assert np.array_equal(np.isnan(head(name, w, 1)), np.isnan(f64(head(name, got[name], 1)))), name
+
+
+PLACES = ("first", "inside", "last")
+
+
+@pytest.mark.parametrize("shape", [("bf16", [300], False, 128), ("bf16", [77, 0, 140], True, 64),
+                                   ("bf16", [1300], False, 32), ("f32", [70, 1, 33], True, 64),
+                                   ("f32", [200], False, 128)], ids=str)
+@pytest.mark.parametrize("which", ["q", "k", "v", "do"])
+@pytest.mark.parametrize("value", [float("nan"), -float("inf")], ids=["nan", "inf"])
+def test_a_value_that_is_not_finite_reaches_only_what_the_formula_gives_it(shape, which, value):
+    """One bad element: results are finite where the formula's are (earlier tokens' outputs, say) and equal there to the
+    clean ones; where the formula has NaN they are NaN, and where it has infinities not finite."""
+    dtype, lens, packed, d = shape
+    x = make(dtype, lens, packed, 1, 2, d, d, seed=23)
+    g = torch.tensor([-0.05, -0.3]).cuda()
+    clean = calls(x, g)
+    total = sum(lens)
+    for place in PLACES:
+        t = {"first": 0, "inside": min(lens[0] - 2, 45), "last": total - 1}[place]
+        y = dict(x)
+        y[which] = x[which].clone()
+        y[which][0, t, -1, 5] = value
+        got = calls(y, g)
+        a = [f64(y[n]) for n in "qkv"] + [f64(g)]
+        with np.errstate(invalid="ignore"):
+            out, S = od.forward(*a, f64(x["S0"]), 0.1, x["cu"])
+            gq, gk, gv, gS = od.backward(*a, f64(y["do"]), f64(x["S0"]), f64(x["dS"]), 0.1, x["cu"])
+        for name, want in (("out", out), ("S_final", S), ("grad_q", gq), ("grad_k", gk), ("grad_v", gv), ("grad_S0", gS)):
+            have, fine = f64(got[name]), np.isfinite(want)
+            assert np.array_equal(np.isfinite(have), fine), (place, name)
+            assert np.array_equal(have[fine], f64(clean[name])[fine]), (place, name)
+            if np.isnan(value):
+                assert np.array_equal(np.isnan(have), np.isnan(want)), (place, name)
