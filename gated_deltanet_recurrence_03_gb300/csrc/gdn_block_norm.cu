@@ -12,11 +12,11 @@
 // A row is read from HBM once: it passes through a ring in shared memory (bulk copies, up to four rows ahead of a group
 // of threads) and is held in registers between the two norms; one block an SM of up to 1024 threads walks the rows.
 // The forward pass is bound by HBM and its instructions alike, the backward pass by its instructions and shared-memory
-// reads.  Measured, 16,384 rows of 4096 bf16 values with a gate: forward 118 us, 0.85 of the measured copy bandwidth
+// reads.  Measured, 16,384 rows of 4096 bf16 values with a gate: forward 119 us, 0.84 of the measured copy bandwidth
 // (161 us with loads straight to registers; 130 us with the next row's in registers, whose moves wait for the loads;
-// 197 us with both sums of a row in one exchange; 126 us with one vector a thread); backward 209 us, 0.77 of it (from
+// 197 us with both sums of a row in one exchange; 126 us with one vector a thread); backward 207 us, 0.77 of it (from
 // 627: sums of the weights' gradients in registers 444, one pass over the row 374, packed arithmetic 333, one sum for
-// the two weights 318, the ring 254, two vectors a thread 209).
+// the two weights 318, the ring 254, two vectors a thread 207).
 #include <algorithm>
 #include <atomic>
 

@@ -84,7 +84,8 @@ __global__ void __launch_bounds__(kSumThreads) head_sum_kernel(const __grid_cons
 // where at least two segments of each find one of the card's `places` of their own; the lengths of packed sequences
 // are not known here, and their total is cut instead (a sequence shorter than that is one segment).  Segments
 // shorter than four chunks of their kernel would be mostly start-up.  Measured: 46,546 packed tokens (one sequence
-// of 40,961) of 6 heads of 128, bf16: 709 us whole, 185 us in 3712-token segments; 1212 tokens of 13 heads: 55 us
+// of 40,961) of 6 heads of 128, bf16: 709 us whole, 182 us in 3712-token segments (each sequence's last segment is a part
+// of one, so these are 17 units x 12 CTAs, a second wave on 152 SMs that is a third full); 1212 tokens of 13 heads: 55 us
 // with 1024 tokens as the least, 46 us with 512.
 int segment_tokens(long long tokens, int nseq, bool packed, int ctas, int places, int min_segment) {
     long long seg;

@@ -1,6 +1,7 @@
 // The decayed scan (gdn_internal.cuh, DecayScan) for fp32 inputs, on the CUDA cores.  The tensor cores would need
 // every operand in three bf16 parts and six products of them, and mma.sync in tf32 three products, which at about six
-// SM cycles for each of 1024 FMAs is 18 cycles where packed fp32 FMAs (128 a cycle) take 8.
+// SM cycles for each of 1024 FMAs is 18 cycles where packed fp32 FMAs (128 a cycle) take 8 at their rate.  What this
+// kernel reaches is a fifth of that rate (below): split products might be ahead of it, and are not built.
 //
 // The chunked form with C = 32 tokens (the quadratic part of a token's work grows with C and is below the two
 // dk x dv products of the state at these head dims).  With w_d = a^d, n valid tokens, S the state at the first
@@ -10,11 +11,12 @@
 // registers (rows x 4 columns a thread) and is copied to shared memory once a chunk for Q S; products are register
 // tiles of packed FMAs over float4 reads; the next chunk's rows are loaded while this one is computed.
 //
-// Bound by shared memory: each float4 that a product reads feeds 8 or 16 FMAs, and the L1 pipe is 83 % busy in the
+// Bound by shared memory: each float4 that a product reads feeds 8 or 16 FMAs, and the L1 pipe is 81 % busy in the
 // main pass, the FMA pipe 21 %.  Measured, packed backward of 1344 tokens (the longest sequence 700), 8 heads of 64:
 // 4.6 ms as matrix products and a token loop in plain tensor operations, 287 us token by token in one CTA a head,
-// 121 us in chunks, 98 us in segments of 128 tokens, 66 us with those spread over two CTAs an SM (16 + 40 us in the
-// state and the main pass).
+// 121 us in chunks, 98 us in segments of 128 tokens, 66 us with those spread over two CTAs an SM, 63.5 us with
+// P V over the columns that a row sees (16 + 38.5 us in the state and the main pass).  2 x 2048 tokens of 32 heads of 128:
+// 541 us.
 #include "decay_unit.cuh"
 
 namespace gdn {

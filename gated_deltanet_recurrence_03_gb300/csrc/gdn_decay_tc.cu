@@ -19,8 +19,8 @@
 // Bound by the chunk's chain of hand-overs and by shared memory, not by the tensor pipe: a chunk moves about 400 KB
 // through shared memory (tiles in, V's parts written and read, P's and the state's operands, outputs), 3100 cycles at
 // 128 bytes a cycle, and takes about 4000; the tensor pipe is 40 % active, HBM at 32 % of its peak.  Measured (bf16,
-// 2 x 8192 tokens, 32 value heads and 16 query/key heads of 128): forward 146 us with the final state (2.8 TB/s of the
-// bytes that it must move), 139 us without; backward 515 us, of it 425 us in this kernel's three scans, 408 us where
+// 2 x 8192 tokens, 32 value heads and 16 query/key heads of 128): forward 144 us with the final state (2.9 TB/s of the
+// bytes that it must move), 135 us without; backward 519 us, of it 423 us in this kernel's three scans, 398 us where
 // no heads are shared.  What brought it there from 318 us: the first tiles' prefetch to L2 (176 -> 154 us); the parts
 // of V side by side in one product of N = 192; QS ahead of P in the issue order; the outputs through shared memory in
 // whole rows (stored from the registers in 16-byte pieces: 20 % slower); two parts instead of three where no state

@@ -347,7 +347,10 @@ gdn_status_t gdn_output_gate_bwd(const void* o, const void* z, const float* norm
  *   out         [B, T, Hv, dv] dtype, dense; must not overlap any input
  *   S_final     [nseq, Hv, dk, dv] float or NULL (not written); may equal S0 (in-place update)
  * Supported: dk, dv in {32, 64, 128}; Hv a multiple of Hqk; B, T >= 0, sequences of no tokens included
- * (their S_final is S0, or zeros), nseq Hv < 2^27, B T < 2^31.  States, sums and decays are fp32.  A value (a NaN, say) in one
+ * (their S_final is S0, or zeros), nseq Hv < 2^27, B T < 2^31.  States, sums and decays are fp32.  With
+ * bf16 inputs the outputs of sequences of more than 128 tokens hold, beside their own rounding, that of
+ * the decayed scores and of the state's copy that q reads to bf16 (0.0023 to 0.0024 of the whole in all,
+ * against 0.0017 for the outputs' own); shorter sequences do not, and S_final never does.  A value (a NaN, say) in one
  * sequence's tokens never reaches another sequence's results, nor results of its own that the formula does not
  * give it to (earlier tokens' outputs).  opts->workspace: 256-byte aligned, of
  * gdn_decay_attn_fwd_workspace_size bytes (GDN_ERR_WORKSPACE if that is not 0 and it is missing or too
