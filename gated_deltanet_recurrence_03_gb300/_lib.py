@@ -24,7 +24,9 @@ EXPORTED = ("gdn_opts_init", "gdn_chunk_fwd", "gdn_chunk_fwd_workspace_size", "g
             "gdn_output_gate_bwd_workspace_size", "gdn_causal_conv1d_bwd", "gdn_causal_conv1d_bwd_workspace_size",
             "gdn_decay_attn_fwd", "gdn_decay_attn_fwd_workspace_size", "gdn_decay_attn_step", "gdn_decay_attn_bwd",
             "gdn_decay_attn_bwd_workspace_size", "gdn_block_norm_fwd", "gdn_block_norm_bwd",
-            "gdn_block_norm_bwd_workspace_size")
+            "gdn_block_norm_bwd_workspace_size", "gdn_selective_scan_fwd", "gdn_selective_scan_fwd_workspace_size",
+            "gdn_selective_scan_step", "gdn_selective_scan_bwd", "gdn_selective_scan_bwd_workspace_size",
+            "gdn_layer_norm_fwd", "gdn_layer_norm_bwd", "gdn_layer_norm_bwd_workspace_size")
 
 
 class GdnOpts(ctypes.Structure):
@@ -119,6 +121,22 @@ def load(path: str = LIB_PATH):
     lib.gdn_block_norm_bwd.restype = i
     lib.gdn_block_norm_bwd_workspace_size.argtypes = [ll, i, opts_p]
     lib.gdn_block_norm_bwd_workspace_size.restype = ctypes.c_size_t
+    scan_in = [vp, ll, vp, ll, vp, vp, ll, vp, ll, vp, vp, vp, ll]   # u, delta, A_log, B, C, skip, dt_bias, z
+    lib.gdn_selective_scan_fwd.argtypes = scan_in + [vp] * 3 + [i] * 5 + [opts_p]
+    lib.gdn_selective_scan_fwd.restype = i
+    lib.gdn_selective_scan_step.argtypes = scan_in + [vp, vp, i, vp] + [i] * 4 + [opts_p]
+    lib.gdn_selective_scan_step.restype = i
+    lib.gdn_selective_scan_bwd.argtypes = (scan_in + [vp] * 7 + [ll, vp, ll, vp, vp, vp, ll, vp] + [i] * 5 + [opts_p])
+    lib.gdn_selective_scan_bwd.restype = i
+    for size in (lib.gdn_selective_scan_fwd_workspace_size, lib.gdn_selective_scan_bwd_workspace_size):
+        size.argtypes = [i] * 5 + [opts_p]
+        size.restype = ctypes.c_size_t
+    lib.gdn_layer_norm_fwd.argtypes = [vp] * 6 + [ll, i, opts_p]
+    lib.gdn_layer_norm_fwd.restype = i
+    lib.gdn_layer_norm_bwd.argtypes = [vp] * 8 + [ll, i, opts_p]
+    lib.gdn_layer_norm_bwd.restype = i
+    lib.gdn_layer_norm_bwd_workspace_size.argtypes = [ll, i, opts_p]
+    lib.gdn_layer_norm_bwd_workspace_size.restype = ctypes.c_size_t
     lib.gdn_check_device_status.argtypes = [vp]
     lib.gdn_check_device_status.restype = i
     lib.gdn_status_string.argtypes = [i]

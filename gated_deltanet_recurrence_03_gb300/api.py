@@ -789,3 +789,244 @@ def gdn_block_norm_bwd(x: torch.Tensor, b: torch.Tensor, post_weight: torch.Tens
         del keep, ws
         L.check(lib, st)
     return gx, gb, gpost, gpre, gg, gs
+
+
+def _row_stride(name, t, lead, width):
+    """Elements between consecutive token rows of t ([*lead, ...], the dimensions behind ``lead`` contiguous and
+    ``width`` values in all): a dense tensor or a slice of a packed projection."""
+    shape, stride = t.shape, t.stride()
+    if lead == 1:
+        row, even = (stride[0] if shape[0] > 1 else width), True
+    else:
+        row = stride[1] if shape[1] > 1 else stride[0] if shape[0] > 1 else width
+        even = shape[0] <= 1 or stride[0] == shape[1] * row
+    inner = 1
+    for n, s in zip(reversed(shape[lead:]), reversed(stride[lead:])):
+        even = even and (n == 1 or s == inner)
+        inner *= n
+    if even and row >= width:
+        return row
+    if t.numel():
+        raise ValueError(f"{name} must have contiguous rows, evenly strided and of their own memory")
+    return width
+
+
+def _token_tensor(name, t, dt, dev, shape, lead):
+    """Checks t and returns its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype is not dt or t.device != dev or t.shape != shape:
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dt} {tuple(shape)} on {dev}")
+    width = 1
+    for n in shape[lead:]:
+        width *= n
+    return _row_stride(name, t, lead, width)
+
+
+def _scan_inputs(u, delta, A_log, B, C, skip, dt_bias, z, lead):
+    """Sizes of the selective scan's inputs, and the arguments that its entry points begin with."""
+    if not isinstance(u, torch.Tensor) or not isinstance(B, torch.Tensor) or not isinstance(A_log, torch.Tensor):
+        raise TypeError("u, A_log and B must be tensors")
+    dims = "B, T" if lead == 2 else "N"
+    if u.dim() != lead + 1:
+        raise ValueError(f"u must be {lead + 1}-D [{dims}, D]")
+    if B.dim() != lead + 2:
+        raise ValueError(f"B must be {lead + 2}-D [{dims}, G, N]")
+    if A_log.dim() != 2:
+        raise ValueError("A_log must be 2-D [D, N]")
+    dev, dt, us = u.device, u.dtype, u.shape
+    if dt not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
+    D, G, N = us[lead], B.shape[lead], A_log.shape[1]
+    bs = us[:lead] + (G, N)
+    _need("A_log", A_log, torch.float32, dev, (D, N))
+    for name, t in (("skip", skip), ("dt_bias", dt_bias)):
+        if t is not None:
+            _need(name, t, torch.float32, dev, (D,))
+    rows = [_token_tensor(name, t, dt, dev, shape, lead)
+            for name, t, shape in (("u", u, us), ("delta", delta, us), ("B", B, bs), ("C", C, bs))]
+    z_row = 0 if z is None else _token_tensor("z", z, dt, dev, us, lead)
+    return dev, dt, D, G, N, (_ptr(u), rows[0], _ptr(delta), rows[1], _ptr(A_log), _ptr(B), rows[2], _ptr(C), rows[3],
+                              _ptr(skip), _ptr(dt_bias), _ptr(z), z_row)
+
+
+def gdn_selective_scan_fwd(u: torch.Tensor, delta: torch.Tensor, A_log: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                           h0: Optional[torch.Tensor] = None, *, skip: Optional[torch.Tensor] = None,
+                           dt_bias: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                           cu_seqlens: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                           h_final: Optional[torch.Tensor] = None, output_final_state: bool = True,
+                           workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                           events: Optional[Sequence[int]] = None):
+    """The selective state space scan over whole sequences: dt = softplus(delta + dt_bias), h <- exp(-dt exp(A_log)) h +
+    dt u B, y = (sum_n C h + skip u) silu(z).  u, delta and z (or None: no gate) [B, T, D], B and C [B, T, G, N] (bf16 or
+    fp32; slices of packed projections are taken as they are); A_log fp32 [D, N] with N of 8, 16, 32 or 64; skip and
+    dt_bias fp32 [D] or None (0); h0 [nseq, D, N] fp32 or None.  Channel d reads B and C of group d // (D // G).  With
+    ``cu_seqlens`` (int32 device tensor of nseq+1 offsets) the batch must be 1.  Returns (y [B, T, D], h_final or None)."""
+    lib = L.load()
+    dev, dt, D, G, N, args = _scan_inputs(u, delta, A_log, B, C, skip, dt_bias, z, 2)
+    nB, T = u.shape[:2]
+    with _on(dev, stream):
+        o, keep = _call_opts(lib, dt, 1.0, stream, dev, events)
+        nseq = _packed(o, cu_seqlens, nB, dev)
+        if h0 is not None:
+            _need("h0", h0, torch.float32, dev, (nseq, D, N))
+        if out is None:
+            out = torch.empty_like(u, memory_format=_DENSE)
+        else:
+            _need("out", out, dt, dev, (nB, T, D))
+        if h_final is not None:
+            _need("h_final", h_final, torch.float32, dev, (nseq, D, N))
+        elif output_final_state:
+            h_final = A_log.new_empty((nseq, D, N)) if h0 is None else torch.empty_like(h0)
+        workspace = _scratch(o, int(lib.gdn_selective_scan_fwd_workspace_size(nB, T, D, G, N, ctypes.byref(o))), workspace,
+                             A_log)
+        st = lib.gdn_selective_scan_fwd(*args, _ptr(h0), _ptr(out), _ptr(h_final), nB, T, D, G, N, ctypes.byref(o))
+        del keep
+        L.check(lib, st)
+    return out, h_final
+
+
+def gdn_selective_scan_step(u: torch.Tensor, delta: torch.Tensor, A_log: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                            h: torch.Tensor, *, skip: Optional[torch.Tensor] = None,
+                            dt_bias: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                            slots: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                            stream: Optional[torch.cuda.Stream] = None,
+                            events: Optional[Sequence[int]] = None) -> torch.Tensor:
+    """One token for each of N rows through gdn_selective_scan_fwd's recurrence.  u, delta, z [N, D]; B, C [N, G, states];
+    h [pool, D, states] fp32, updated in place.  ``slots`` (int32 [N]) names each row's state in the pool (None: row n,
+    state n); a row whose slot is outside the pool (-1, say) is idle and gets zeros.  Returns y [N, D]."""
+    lib = L.load()
+    dev, dt, D, G, N, args = _scan_inputs(u, delta, A_log, B, C, skip, dt_bias, z, 1)
+    rows = u.shape[0]
+    pool = h.shape[0] if slots is not None and h.dim() == 3 else rows
+    _need("h", h, torch.float32, dev, (pool, D, N))
+    if slots is not None:
+        _need("slots", slots, torch.int32, dev, (rows,))
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty_like(u, memory_format=_DENSE)
+        else:
+            _need("out", out, dt, dev, (rows, D))
+        o, keep = _call_opts(lib, dt, 1.0, stream, dev, events)
+        st = lib.gdn_selective_scan_step(*args, _ptr(h), _ptr(slots), pool, _ptr(out), rows, D, G, N, ctypes.byref(o))
+        del keep
+        L.check(lib, st)
+    return out
+
+
+def gdn_selective_scan_bwd(u: torch.Tensor, delta: torch.Tensor, A_log: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                           h0: Optional[torch.Tensor], grad_y: torch.Tensor, grad_h_final: Optional[torch.Tensor] = None,
+                           *, skip: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
+                           z: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                           want_grad_h0: bool = True, grads: Optional[Sequence[torch.Tensor]] = None,
+                           workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                           events: Optional[Sequence[int]] = None):
+    """Gradients of a loss on (y, h_final) of gdn_selective_scan_fwd.  Inputs as there; grad_y like y (dense);
+    grad_h_final fp32 like h_final or None.  ``grads`` = (grad_B, grad_C, grad_z) receives those three where given
+    (slices of packed gradients, say; grad_z None without z).  Returns (grad_u, grad_delta in u's type, grad_A_log fp32,
+    grad_B, grad_C in u's type, grad_skip, grad_dt_bias fp32 or None where the input is None, grad_z in u's type or None,
+    grad_h0 fp32 or None)."""
+    lib = L.load()
+    dev, dt, D, G, N, args = _scan_inputs(u, delta, A_log, B, C, skip, dt_bias, z, 2)
+    nB, T = u.shape[:2]
+    _need("grad_y", grad_y, dt, dev, (nB, T, D))
+    with _on(dev, stream):
+        if grads is None:
+            grads = (torch.empty_like(B, memory_format=_DENSE), torch.empty_like(C, memory_format=_DENSE),
+                     None if z is None else torch.empty_like(z, memory_format=_DENSE))
+        gB, gC, gz = grads
+        if (gz is None) != (z is None):
+            raise ValueError("grad_z goes with z")
+        gb_stride = _token_tensor("grad_B", gB, dt, dev, B.shape, 2)
+        gc_stride = _token_tensor("grad_C", gC, dt, dev, B.shape, 2)
+        gz_stride = 0 if gz is None else _token_tensor("grad_z", gz, dt, dev, u.shape, 2)
+        o, keep = _call_opts(lib, dt, 1.0, stream, dev, events)
+        nseq = _packed(o, cu_seqlens, nB, dev)
+        for name, t in (("h0", h0), ("grad_h_final", grad_h_final)):
+            if t is not None:
+                _need(name, t, torch.float32, dev, (nseq, D, N))
+        gu, gd = torch.empty_like(u, memory_format=_DENSE), torch.empty_like(u, memory_format=_DENSE)
+        gA = torch.empty_like(A_log)
+        gs = None if skip is None else torch.empty_like(skip)
+        gbias = None if dt_bias is None else torch.empty_like(dt_bias)
+        gh0 = A_log.new_empty((nseq, D, N)) if want_grad_h0 else None
+        workspace = _scratch(o, int(lib.gdn_selective_scan_bwd_workspace_size(nB, T, D, G, N, ctypes.byref(o))), workspace,
+                             A_log)
+        st = lib.gdn_selective_scan_bwd(*args, _ptr(h0), _ptr(grad_y), _ptr(grad_h_final), _ptr(gu), _ptr(gd), _ptr(gA),
+                                        _ptr(gB), gb_stride, _ptr(gC), gc_stride, _ptr(gs), _ptr(gbias), _ptr(gz),
+                                        gz_stride, _ptr(gh0), nB, T, D, G, N, ctypes.byref(o))
+        del keep
+        L.check(lib, st)
+    return gu, gd, gA, gB, gC, gs, gbias, gz, gh0
+
+
+def _layer_norm_inputs(x, weight, residual):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a tensor")
+    dev, dt = x.device, x.dtype
+    if dt not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    shape, D = x.shape, x.shape[-1]
+    _need("x", x, dt, dev, shape)
+    _need("weight", weight, torch.float32, dev, (D,))
+    if residual is not None:
+        _need("residual", residual, dt, dev, shape)
+    return dev, dt, shape, D, (x.numel() // D if D else 0)
+
+
+def gdn_layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
+                       residual: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                       out: Optional[Sequence[torch.Tensor]] = None, stream: Optional[torch.cuda.Stream] = None,
+                       events: Optional[Sequence[int]] = None):
+    """Layer norm with the residual add in front of it: r = x + residual (x where there is none), n = (r - mean(r)) /
+    sqrt(var(r) + eps) weight + bias.  x and residual [..., D] (bf16 or fp32, contiguous); weight and bias (None: 0) fp32
+    [D].  ``out`` = (n, r) receives the results where given (r None without a residual; each may be x or residual).
+    Returns (n, r), r None without a residual."""
+    lib = L.load()
+    dev, dt, shape, D, rows = _layer_norm_inputs(x, weight, residual)
+    if bias is not None:
+        _need("bias", bias, torch.float32, dev, (D,))
+    with _on(dev, stream):
+        if out is None:
+            n, r = torch.empty_like(x), None if residual is None else torch.empty_like(x)
+        else:
+            n, r = out
+            _need("n", n, dt, dev, shape)
+            if (r is None) != (residual is None):
+                raise ValueError("r goes with residual")
+            if r is not None:
+                _need("r", r, dt, dev, shape)
+        o, keep = _call_opts(lib, dt, 1.0, stream, dev, events)
+        o.norm_eps = float(eps)
+        st = lib.gdn_layer_norm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(n), _ptr(r), rows, D,
+                                    ctypes.byref(o))
+        del keep
+        L.check(lib, st)
+    return n, r
+
+
+def gdn_layer_norm_bwd(x: torch.Tensor, weight: torch.Tensor, grad_n: torch.Tensor, *,
+                       residual: Optional[torch.Tensor] = None, grad_r: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                       want_grad_bias: bool = True, stream: Optional[torch.cuda.Stream] = None,
+                       events: Optional[Sequence[int]] = None):
+    """Gradients through gdn_layer_norm_fwd, from its inputs, grad_n and, for a residual stream that goes on, grad_r (like
+    x).  Returns (grad_x in x's type, the gradient of x and of residual; grad_weight fp32 [D]; grad_bias fp32 [D] or
+    None)."""
+    lib = L.load()
+    dev, dt, shape, D, rows = _layer_norm_inputs(x, weight, residual)
+    _need("grad_n", grad_n, dt, dev, shape)
+    if grad_r is not None:
+        _need("grad_r", grad_r, dt, dev, shape)
+    with _on(dev, stream):
+        gx, gw = torch.empty_like(x), torch.empty_like(weight)
+        gb = torch.empty_like(weight) if want_grad_bias else None
+        o, keep = _call_opts(lib, dt, 1.0, stream, dev, events)
+        o.norm_eps = float(eps)
+        ws = _scratch(o, int(lib.gdn_layer_norm_bwd_workspace_size(rows, D, ctypes.byref(o))), None, weight)
+        st = lib.gdn_layer_norm_bwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(grad_n), _ptr(grad_r), _ptr(gx), _ptr(gw),
+                                    _ptr(gb), rows, D, ctypes.byref(o))
+        del keep, ws
+        L.check(lib, st)
+    return gx, gw, gb

@@ -914,6 +914,289 @@ gdn_status_t gdn_block_norm_bwd(const void* x, const void* b, const void* gate, 
     return GDN_OK;
 }
 
+// ---------------------------------------------------------------- selective scan
+}  // extern "C"
+
+namespace {
+
+constexpr long long kMaxBlocks = INT32_MAX;
+
+bool scan_dims_ok(int D, int G, int N) {
+    return D > 0 && G > 0 && D % (8LL * G) == 0 && (N == 8 || N == 16 || N == 32 || N == 64);
+}
+
+// A row stride of 0 is the dense one; rows hold their values and stay 16-byte aligned.
+gdn_status_t check_stride(const char* name, long long* stride, long long width, int dtype) {
+    if (*stride == 0) *stride = width;
+    const int per16 = dtype == GDN_BF16 ? 8 : 4;
+    if (*stride < width || *stride % per16 != 0 || *stride > INT32_MAX)
+        return fail(GDN_ERR_INVALID_ARG, "%s stride %lld must be >= %lld, a multiple of %d and below 2^31", name, *stride,
+                    width, per16);
+    return GDN_OK;
+}
+
+// Checks shared by the selective scan's entry points.
+gdn_status_t scan_common(int D, int G, int N, const gdn_opts_t& o, long long* u_stride, long long* delta_stride,
+                         long long* b_stride, long long* c_stride, long long* z_stride) {
+    if (o.dtype != GDN_F32 && o.dtype != GDN_BF16) return fail(GDN_ERR_INVALID_ARG, "unknown dtype %d", o.dtype);
+    if (o.flags) return fail(GDN_ERR_INVALID_ARG, "flags 0x%x: the selective scan takes none", o.flags);
+    if (o.num_events < 0 || (o.num_events > 0 && !o.events)) return fail(GDN_ERR_INVALID_ARG, "bad event list");
+    if (D <= 0 || G <= 0 || D % (8LL * G) != 0)
+        return fail(GDN_ERR_INVALID_ARG, "D=%d must be a positive multiple of 8 G (G=%d)", D, G);
+    if (N != 8 && N != 16 && N != 32 && N != 64) return fail(GDN_ERR_UNSUPPORTED, "N=%d not in {8,16,32,64}", N);
+    if ((long long)D * N > INT32_MAX / 4) return fail(GDN_ERR_INVALID_ARG, "D=%d N=%d: a state is too large", D, N);
+    gdn_status_t st = check_stride("u", u_stride, D, o.dtype);
+    if (st == GDN_OK) st = check_stride("delta", delta_stride, D, o.dtype);
+    if (st == GDN_OK) st = check_stride("B", b_stride, (long long)G * N, o.dtype);
+    if (st == GDN_OK) st = check_stride("C", c_stride, (long long)G * N, o.dtype);
+    if (st == GDN_OK) st = check_stride("z", z_stride, D, o.dtype);
+    return st;
+}
+
+// Sequences of a call over whole sequences; blocks of the scan's largest grid must stay below 2^31.
+gdn_status_t scan_sequences(int B, int T, int D, int G, int N, const gdn_opts_t& o, int* nseq) {
+    if (B < 0 || T < 0) return fail(GDN_ERR_INVALID_ARG, "B=%d T=%d must be >= 0", B, T);
+    if (o.cu_seqlens && (B != 1 || o.num_seqs < 1))
+        return fail(GDN_ERR_INVALID_ARG, "cu_seqlens needs B == 1 and num_seqs >= 1 (B=%d num_seqs=%d)", B, o.num_seqs);
+    if (o.cu_seqlens && !aligned_to(o.cu_seqlens, 4)) return fail(GDN_ERR_INVALID_ARG, "cu_seqlens must be 4-byte aligned");
+    const long long tokens = (long long)B * T;
+    if (tokens > INT32_MAX) return fail(GDN_ERR_INVALID_ARG, "more than 2^31 - 1 tokens");
+    *nseq = o.cu_seqlens ? o.num_seqs : B;
+    // tiles of at least 8 channels of a group and vectors of four states, for each sequence and segment
+    const long long slots = *nseq + tokens / kScanSegment, tiles = std::max((long long)D / 8, (long long)D * N / 512 + 1);
+    if (slots > kMaxBlocks / tiles) return fail(GDN_ERR_INVALID_ARG, "%lld tokens in %d sequences of %d channels are too many", tokens, *nseq, D);
+    if (tokens * ((long long)G * N / 2) / 256 >= kMaxBlocks) return fail(GDN_ERR_INVALID_ARG, "%lld tokens of %d groups are too many", tokens, G);
+    return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_selective_scan_fwd_workspace_size(int B, int T, int D, int G, int N, const gdn_opts_t* opts) {
+    const gdn_opts_t o = resolve(opts);
+    const int nseq = o.cu_seqlens ? o.num_seqs : B;
+    if (B <= 0 || T <= 0 || nseq <= 0 || !scan_dims_ok(D, G, N)) return 0;
+    return scan_fwd_layout((long long)B * T, D, N, nseq, o.cu_seqlens != nullptr).total;
+}
+
+gdn_status_t gdn_selective_scan_fwd(const void* u, long long u_stride, const void* delta, long long delta_stride,
+                                    const float* A_log, const void* Bm, long long b_stride, const void* Cm,
+                                    long long c_stride, const float* skip, const float* dt_bias, const void* z,
+                                    long long z_stride, const float* h0, void* y, float* h_final, int B, int T, int D,
+                                    int G, int N, const gdn_opts_t* opts) {
+    t_last_error[0] = 0;
+    const gdn_opts_t o = resolve(opts);
+    gdn_status_t st = scan_common(D, G, N, o, &u_stride, &delta_stride, &b_stride, &c_stride, &z_stride);
+    if (st != GDN_OK) return st;
+    int nseq = 0;
+    if ((st = scan_sequences(B, T, D, G, N, o, &nseq)) != GDN_OK) return st;
+    const long long tokens = (long long)B * T;
+    if (tokens > 0 && (!u || !delta || !A_log || !Bm || !Cm || !y)) return fail(GDN_ERR_INVALID_ARG, "null input/output pointer");
+    if ((st = need_aligned16({u, delta, A_log, Bm, Cm, skip, dt_bias, z, h0, y, h_final})) != GDN_OK) return st;
+    if (nseq == 0) return GDN_OK;
+    const ScanFwdLayout l = tokens > 0 ? scan_fwd_layout(tokens, D, N, nseq, o.cu_seqlens != nullptr) : ScanFwdLayout{};
+    if ((st = need_workspace(o, l.total)) != GDN_OK) return st;
+    unsigned* status = nullptr;
+    if ((st = device_ready(&status)) != GDN_OK) return st;
+    cudaStream_t stream = static_cast<cudaStream_t>(o.stream);
+    record(o, 0, stream);
+    cudaError_t e = cudaSuccess;
+    if (tokens == 0) {   // no tokens: the final states are the initial ones
+        const size_t bytes = (size_t)nseq * D * N * sizeof(float);
+        if (h_final && h_final != h0)
+            e = h0 ? cudaMemcpyAsync(h_final, h0, bytes, cudaMemcpyDeviceToDevice, stream)
+                   : cudaMemsetAsync(h_final, 0, bytes, stream);
+    } else {
+        ScanArgs a{};
+        a.u = u; a.delta = delta; a.z = z; a.B = Bm; a.C = Cm;
+        a.u_stride = u_stride; a.delta_stride = delta_stride; a.z_stride = z_stride;
+        a.b_stride = b_stride; a.c_stride = c_stride;
+        a.A_log = A_log; a.skip = skip; a.dt_bias = dt_bias; a.h0 = h0; a.y = y; a.h_final = h_final;
+        a.T = T; a.D = D; a.G = G; a.N = N; a.dtype = o.dtype;
+        a.cu = o.cu_seqlens; a.nseq = nseq; a.tokens = (int)tokens;
+        a.seg = l.seg; a.slots = (int)l.slots;
+        uint8_t* ws = static_cast<uint8_t*>(o.workspace);
+        a.states = reinterpret_cast<float*>(ws);
+        a.sum_dt = reinterpret_cast<float*>(ws + l.sum_dt);
+        a.stream = stream;
+        e = launch_scan_fwd(a);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "selective scan launch");
+    record(o, 1, stream);
+    return GDN_OK;
+}
+
+gdn_status_t gdn_selective_scan_step(const void* u, long long u_stride, const void* delta, long long delta_stride,
+                                     const float* A_log, const void* Bm, long long b_stride, const void* Cm,
+                                     long long c_stride, const float* skip, const float* dt_bias, const void* z,
+                                     long long z_stride, float* h, const int32_t* slots, int num_slots, void* y,
+                                     int rows, int D, int G, int N, const gdn_opts_t* opts) {
+    t_last_error[0] = 0;
+    const gdn_opts_t o = resolve(opts);
+    if (rows < 0 || num_slots < 0) return fail(GDN_ERR_INVALID_ARG, "rows=%d num_slots=%d must be >= 0", rows, num_slots);
+    gdn_status_t st = scan_common(D, G, N, o, &u_stride, &delta_stride, &b_stride, &c_stride, &z_stride);
+    if (st != GDN_OK) return st;
+    if (!slots && num_slots < rows) return fail(GDN_ERR_INVALID_ARG, "%d states for %d rows without slots", num_slots, rows);
+    if (rows == 0) return GDN_OK;
+    if (!u || !delta || !A_log || !Bm || !Cm || (!h && num_slots > 0) || !y) return fail(GDN_ERR_INVALID_ARG, "null pointer");
+    if ((long long)rows * ((long long)D * N / 512 + 1) > kMaxBlocks)
+        return fail(GDN_ERR_INVALID_ARG, "rows=%d of %d channels are too many", rows, D);
+    if ((st = need_aligned16({u, delta, A_log, Bm, Cm, skip, dt_bias, z, h, y})) != GDN_OK) return st;
+    if (slots && !aligned_to(slots, 4)) return fail(GDN_ERR_INVALID_ARG, "slots is not 4-byte aligned");
+    unsigned* status = nullptr;
+    if ((st = device_ready(&status)) != GDN_OK) return st;
+    ScanStepArgs a{u, delta, z, Bm, Cm, u_stride, delta_stride, z_stride, b_stride, c_stride, A_log, skip, dt_bias, h, slots,
+                   num_slots, y, rows, D, G, N, o.dtype, static_cast<cudaStream_t>(o.stream)};
+    record(o, 0, a.stream);
+    const cudaError_t e = launch_scan_step(a);
+    if (e != cudaSuccess) return cuda_fail(e, "selective scan step launch");
+    record(o, 1, a.stream);
+    return GDN_OK;
+}
+
+size_t gdn_selective_scan_bwd_workspace_size(int B, int T, int D, int G, int N, const gdn_opts_t* opts) {
+    const gdn_opts_t o = resolve(opts);
+    const int nseq = o.cu_seqlens ? o.num_seqs : B;
+    if (B <= 0 || T <= 0 || nseq <= 0 || !scan_dims_ok(D, G, N)) return 0;
+    return scan_bwd_layout((long long)B * T, D, G, N, nseq, o.cu_seqlens != nullptr).total;
+}
+
+gdn_status_t gdn_selective_scan_bwd(const void* u, long long u_stride, const void* delta, long long delta_stride,
+                                    const float* A_log, const void* Bm, long long b_stride, const void* Cm,
+                                    long long c_stride, const float* skip, const float* dt_bias, const void* z,
+                                    long long z_stride, const float* h0, const void* grad_y, const float* grad_h_final,
+                                    void* grad_u, void* grad_delta, float* grad_A_log, void* grad_B, long long gb_stride,
+                                    void* grad_C, long long gc_stride, float* grad_skip, float* grad_dt_bias,
+                                    void* grad_z, long long gz_stride, float* grad_h0, int B, int T, int D, int G, int N,
+                                    const gdn_opts_t* opts) {
+    t_last_error[0] = 0;
+    const gdn_opts_t o = resolve(opts);
+    gdn_status_t st = scan_common(D, G, N, o, &u_stride, &delta_stride, &b_stride, &c_stride, &z_stride);
+    if (st == GDN_OK) st = check_stride("grad_B", &gb_stride, (long long)G * N, o.dtype);
+    if (st == GDN_OK) st = check_stride("grad_C", &gc_stride, (long long)G * N, o.dtype);
+    if (st == GDN_OK) st = check_stride("grad_z", &gz_stride, D, o.dtype);
+    if (st != GDN_OK) return st;
+    int nseq = 0;
+    if ((st = scan_sequences(B, T, D, G, N, o, &nseq)) != GDN_OK) return st;
+    const long long tokens = (long long)B * T;
+    if (tokens > 0 && (!u || !delta || !A_log || !Bm || !Cm || !grad_y || !grad_u || !grad_delta || !grad_B || !grad_C))
+        return fail(GDN_ERR_INVALID_ARG, "null input/output pointer");
+    if (tokens > 0 && z && !grad_z) return fail(GDN_ERR_INVALID_ARG, "z needs grad_z");
+    if ((st = need_aligned16({u, delta, A_log, Bm, Cm, skip, dt_bias, z, h0, grad_y, grad_h_final, grad_u, grad_delta,
+                              grad_A_log, grad_B, grad_C, grad_skip, grad_dt_bias, grad_z, grad_h0})) != GDN_OK)
+        return st;
+    const ScanBwdLayout l = tokens > 0 ? scan_bwd_layout(tokens, D, G, N, nseq, o.cu_seqlens != nullptr) : ScanBwdLayout{};
+    if ((st = need_workspace(o, l.total)) != GDN_OK) return st;
+    if (nseq == 0 && !grad_A_log && !grad_skip && !grad_dt_bias) return GDN_OK;
+    unsigned* status = nullptr;
+    if ((st = device_ready(&status)) != GDN_OK) return st;
+    cudaStream_t stream = static_cast<cudaStream_t>(o.stream);
+    record(o, 0, stream);
+    cudaError_t e = cudaSuccess;
+    if (tokens == 0) {   // no tokens: the initial states' gradient is the final ones', the weights' are zeros
+        const size_t bytes = (size_t)nseq * D * N * sizeof(float);
+        if (grad_h0 && bytes && grad_h0 != grad_h_final)
+            e = grad_h_final ? cudaMemcpyAsync(grad_h0, grad_h_final, bytes, cudaMemcpyDeviceToDevice, stream)
+                             : cudaMemsetAsync(grad_h0, 0, bytes, stream);
+        if (e == cudaSuccess && grad_A_log) e = cudaMemsetAsync(grad_A_log, 0, (size_t)D * N * sizeof(float), stream);
+        if (e == cudaSuccess && grad_skip) e = cudaMemsetAsync(grad_skip, 0, (size_t)D * sizeof(float), stream);
+        if (e == cudaSuccess && grad_dt_bias) e = cudaMemsetAsync(grad_dt_bias, 0, (size_t)D * sizeof(float), stream);
+    } else {
+        ScanArgs a{};
+        a.u = u; a.delta = delta; a.z = z; a.B = Bm; a.C = Cm;
+        a.u_stride = u_stride; a.delta_stride = delta_stride; a.z_stride = z_stride;
+        a.b_stride = b_stride; a.c_stride = c_stride;
+        a.A_log = A_log; a.skip = skip; a.dt_bias = dt_bias; a.h0 = h0;
+        a.T = T; a.D = D; a.G = G; a.N = N; a.dtype = o.dtype;
+        a.cu = o.cu_seqlens; a.nseq = nseq; a.tokens = (int)tokens;
+        a.seg = l.seg; a.slots = (int)l.slots;
+        uint8_t* ws = static_cast<uint8_t*>(o.workspace);
+        a.states = reinterpret_cast<float*>(ws);
+        a.adjoints = reinterpret_cast<float*>(ws + l.adjoints);
+        a.sum_dt = reinterpret_cast<float*>(ws + l.sum_dt);
+        a.part_A = reinterpret_cast<float*>(ws + l.part_A);
+        a.part_s = reinterpret_cast<float*>(ws + l.part_s);
+        a.part_bc = reinterpret_cast<float*>(ws + l.part_bc);
+        a.gy = grad_y; a.gh = grad_h_final; a.gu = grad_u; a.gdelta = grad_delta;
+        a.gB = grad_B; a.gC = grad_C; a.gz = grad_z;
+        a.gb_stride = gb_stride; a.gc_stride = gc_stride; a.gz_stride = gz_stride;
+        a.gA = grad_A_log; a.gskip = grad_skip; a.gbias = grad_dt_bias; a.gh0 = grad_h0;
+        a.stream = stream;
+        e = launch_scan_bwd(a);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "selective scan backward launch");
+    record(o, 1, stream);
+    return GDN_OK;
+}
+
+// ---------------------------------------------------------------- layer norm
+static gdn_status_t layer_norm_common(const gdn_opts_t& o, long long rows, int D, const float* weight) {
+    if (rows < 0 || rows > INT32_MAX) return fail(GDN_ERR_INVALID_ARG, "rows=%lld not in 0..2^31 - 1", rows);
+    if (o.dtype != GDN_F32 && o.dtype != GDN_BF16) return fail(GDN_ERR_INVALID_ARG, "unknown dtype %d", o.dtype);
+    if (o.flags) return fail(GDN_ERR_INVALID_ARG, "flags 0x%x: the layer norm takes none", o.flags);
+    if (!(o.norm_eps >= 0.f)) return fail(GDN_ERR_INVALID_ARG, "norm_eps must be >= 0");
+    if (o.num_events < 0 || (o.num_events > 0 && !o.events)) return fail(GDN_ERR_INVALID_ARG, "bad event list");
+    if (D <= 0 || D % 8 != 0) return fail(GDN_ERR_INVALID_ARG, "D=%d must be a positive multiple of 8", D);
+    if (D > kBlockNormMaxD) return fail(GDN_ERR_UNSUPPORTED, "D=%d is above %d", D, kBlockNormMaxD);
+    if (!weight) return fail(GDN_ERR_INVALID_ARG, "null weight");
+    return GDN_OK;
+}
+
+gdn_status_t gdn_layer_norm_fwd(const void* x, const void* b, const float* weight, const float* bias, void* n, void* r,
+                                long long rows, int D, const gdn_opts_t* opts) {
+    t_last_error[0] = 0;
+    const gdn_opts_t o = resolve(opts);
+    gdn_status_t st = layer_norm_common(o, rows, D, weight);
+    if (st != GDN_OK) return st;
+    if (rows > 0 && (!x || !n)) return fail(GDN_ERR_INVALID_ARG, "null x or n");
+    if (rows > 0 && !b != !r) return fail(GDN_ERR_INVALID_ARG, "b and r go together");
+    if (rows > 0 && r && r == n) return fail(GDN_ERR_INVALID_ARG, "r and n are the same");
+    if ((st = need_aligned16({x, b, weight, bias, n, r})) != GDN_OK) return st;
+    if (rows == 0) return GDN_OK;
+    unsigned* status = nullptr;
+    if ((st = device_ready(&status)) != GDN_OK) return st;
+    LayerNormArgs a{};
+    a.x = x; a.b = b; a.w = weight; a.bias = bias; a.eps = o.norm_eps; a.n = n; a.r = r;
+    a.rows = rows; a.D = D; a.dtype = o.dtype; a.stream = static_cast<cudaStream_t>(o.stream); a.status = status;
+    record(o, 0, a.stream);
+    const cudaError_t e = launch_layer_norm_fwd(a);
+    if (e != cudaSuccess) return cuda_fail(e, "layer norm launch");
+    record(o, 1, a.stream);
+    return GDN_OK;
+}
+
+size_t gdn_layer_norm_bwd_workspace_size(long long rows, int D, const gdn_opts_t* opts) {
+    (void)opts;
+    if (rows < 0 || D <= 0 || D % 8 || D > kBlockNormMaxD) return 0;
+    return layer_norm_bwd_workspace_bytes(rows, D);
+}
+
+gdn_status_t gdn_layer_norm_bwd(const void* x, const void* b, const float* weight, const void* grad_n, const void* grad_r,
+                                void* grad_x, float* grad_weight, float* grad_bias, long long rows, int D,
+                                const gdn_opts_t* opts) {
+    t_last_error[0] = 0;
+    const gdn_opts_t o = resolve(opts);
+    gdn_status_t st = layer_norm_common(o, rows, D, weight);
+    if (st != GDN_OK) return st;
+    if (rows > 0 && (!x || !grad_n || !grad_x)) return fail(GDN_ERR_INVALID_ARG, "null x, grad_n or grad_x");
+    if ((st = need_aligned16({x, b, weight, grad_n, grad_r, grad_x, grad_weight, grad_bias})) != GDN_OK) return st;
+    const bool sums = grad_weight || grad_bias;
+    if (rows == 0 && !sums) return GDN_OK;
+    if (sums && (st = need_workspace(o, layer_norm_bwd_workspace_bytes(rows, D))) != GDN_OK) return st;
+    unsigned* status = nullptr;
+    if ((st = device_ready(&status)) != GDN_OK) return st;
+    LayerNormArgs a{};
+    a.x = x; a.b = b; a.w = weight; a.eps = o.norm_eps; a.gn = grad_n; a.gr = grad_r; a.gx = grad_x;
+    a.gw = grad_weight; a.gbias = grad_bias; a.workspace = o.workspace;
+    a.rows = rows; a.D = D; a.dtype = o.dtype; a.stream = static_cast<cudaStream_t>(o.stream); a.status = status;
+    record(o, 0, a.stream);
+    const cudaError_t e = launch_layer_norm_bwd(a);
+    if (e != cudaSuccess) return cuda_fail(e, "layer norm backward launch");
+    record(o, 1, a.stream);
+    return GDN_OK;
+}
+
 gdn_status_t gdn_check_device_status(void* stream) {
     t_last_error[0] = 0;
     unsigned* status = nullptr;

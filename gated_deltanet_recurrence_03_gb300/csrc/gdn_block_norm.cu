@@ -18,102 +18,12 @@
 // 627: sums of the weights' gradients in registers 444, one pass over the row 374, packed arithmetic 333, one sum for
 // the two weights 318, the ring 254, two vectors a thread 207).
 #include <algorithm>
-#include <atomic>
 
-#include "bulk_ring.cuh"
-#include "gdn_internal.cuh"
+#include "norm_rows.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kVec = 8;   // values of one vector of a thread
-
-// Eight values as four pairs; the arithmetic is two fp32 operations an instruction.
-struct V8 {
-    float2 v[4];
-};
-__device__ __forceinline__ uint64_t u64(float2 a) { return *reinterpret_cast<uint64_t*>(&a); }
-__device__ __forceinline__ float2 f2(uint64_t a) { return *reinterpret_cast<float2*>(&a); }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(u64(a)), "l"(u64(b)));
-    return f2(d);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(u64(a)), "l"(u64(b)));
-    return f2(d);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(u64(a)), "l"(u64(b)), "l"(u64(c)));
-    return f2(d);
-}
-__device__ __forceinline__ float2 all2(float x) { return make_float2(x, x); }
-
-// Eight values of either type at p (shared or global memory) as fp32, and back.
-__device__ __forceinline__ V8 load8(const float* p) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    return {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
-}
-__device__ __forceinline__ V8 load8(const __nv_bfloat16* p) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    V8 x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x.v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-    return x;
-}
-__device__ __forceinline__ void store8(float* p, const V8& x) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const V8& x) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x.v[i].x, x.v[i].y);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// A block holds `groups` row groups of `tpr` threads (a multiple of 32), each with a row of its own.
-struct Group {
-    int tpr, id, tid;   // threads of a row; this thread's group and place in it
-};
-__device__ __forceinline__ void group_sync(const Group& g) {
-    if (g.tpr == 32) __syncwarp();
-    else if (g.tpr == (int)blockDim.x) __syncthreads();
-    else asm volatile("bar.sync %0, %1;" ::"r"(g.id + 1), "r"(g.tpr) : "memory");
-}
-// Sums of N values over a row group's threads, in a fixed order; every thread gets them.  `buf` holds 32 N floats
-// of the group, zero past its warps, and may be written again after the group's next synchronisation.
-template <int N>
-__device__ __forceinline__ void group_sum(float (&x)[N], float* buf, const Group& g) {
-    const int lane = g.tid & 31, warp = g.tid >> 5, nw = g.tpr >> 5;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
-    if (nw == 1) {
-        __syncwarp();
-        return;
-    }
-    if (lane == 0)
-#pragma unroll
-        for (int i = 0; i < N; ++i) buf[i * 32 + warp] = x[i];
-    group_sync(g);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {   // every thread adds the warps' sums: no second round of shuffles
-        float4 t = *reinterpret_cast<const float4*>(buf + i * 32);
-        for (int w = 4; w < nw; w += 4) {
-            const float4 u = *reinterpret_cast<const float4*>(buf + i * 32 + w);
-            t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
-        }
-        x[i] = (t.x + t.y) + (t.z + t.w);
-    }
-}
 // Logits below -87 act as -87 (1e-38): past 2^126 the fast division is not defined.  A NaN stays one.
 __device__ __forceinline__ float sigmoid_f(float u) { return __fdividef(1.f, 1.f + __expf(u < -87.f ? 87.f : -u)); }
 __device__ __forceinline__ V8 gate8(const V8& u) {
@@ -123,28 +33,7 @@ __device__ __forceinline__ V8 gate8(const V8& u) {
     return s;
 }
 
-// Shared memory of a block: the groups' reduction buffers (two of 64 floats each), mbarriers, the columns'
-// constants m = w_post c and w_pre, and the groups' rings.
-struct Smem {
-    float *red, *m, *wq;
-    uint64_t* bars;
-    int* abort;
-    uint8_t* rings;
-};
-__device__ __forceinline__ Smem carve(uint8_t* p, int groups, int D) {
-    Smem s;
-    s.red = reinterpret_cast<float*>(p);
-    s.bars = reinterpret_cast<uint64_t*>(s.red + groups * 128);
-    s.abort = reinterpret_cast<int*>(s.bars + groups * kRingWords);
-    s.m = reinterpret_cast<float*>(s.abort + 4);
-    s.wq = s.m + D;
-    s.rings = reinterpret_cast<uint8_t*>(s.wq + D);
-    return s;
-}
-size_t smem_bytes(int groups, int D, int row_bytes, int stages) {
-    return (size_t)groups * 128 * 4 + groups * kRingWords * 8 + 16 + (size_t)2 * D * 4 + (size_t)groups * stages * row_bytes;
-}
-__device__ __forceinline__ void set_up(const Smem& s, const BlockNormArgs& a, int groups) {
+__device__ __forceinline__ void set_up(const RowSmem& s, const BlockNormArgs& a, int groups) {
     for (int i = threadIdx.x; i < groups * 128; i += blockDim.x) s.red[i] = 0.f;
     if ((int)threadIdx.x < groups) ring_init(s.bars + threadIdx.x * kRingWords);
     if (threadIdx.x == 0) *s.abort = 0;
@@ -163,7 +52,7 @@ block_norm_fwd_kernel(const __grid_constant__ BlockNormArgs a, int tpr, int stag
     extern __shared__ __align__(128) uint8_t smem[];
     const Group g{tpr, (int)threadIdx.x / tpr, (int)threadIdx.x % tpr};
     const int nv = a.D / kVec, groups = blockDim.x / tpr;
-    const Smem sm = carve(smem, groups, a.D);
+    const RowSmem sm = carve(smem, groups, a.D);
     set_up(sm, a, groups);
     float* const red = sm.red + g.id * 128;
     const float invD = 1.f / (float)a.D;
@@ -258,7 +147,7 @@ block_norm_bwd_kernel(const __grid_constant__ BlockNormArgs a, float* __restrict
     extern __shared__ __align__(128) uint8_t smem[];
     const Group g{tpr, (int)threadIdx.x / tpr, (int)threadIdx.x % tpr};
     const int nv = a.D / kVec, groups = blockDim.x / tpr;
-    const Smem sm = carve(smem, groups, a.D);
+    const RowSmem sm = carve(smem, groups, a.D);
     set_up(sm, a, groups);
     float* const red = sm.red + g.id * 128;
     const float invD = 1.f / (float)a.D;
@@ -433,67 +322,26 @@ __global__ void __launch_bounds__(1024) block_norm_sums_kernel(const float* __re
     }
 }
 
-// Vectors a thread holds, threads a row, row groups and ring stages a block, blocks.  With two vectors a thread a row's
-// exchanges take half the threads and each has twice the work between them: 255 -> 209 us (backward, 16384 x 4096),
-// 234 -> 187 us (32768 x 2048), 129 -> 81 us (65536 x 264); four are no better (201, 194 us; forward 119 -> 130 us).
-// One vector where a row fits one warp, and where no SM has more than one row, whose latency then counts (4.2 against
-// 5.5 us forward, 37 x 2048).
-// A block fills an SM: up to 1024 threads and kSmemMax bytes, with as many groups as leave each at least two
-// stages; past one warp a row the groups are limited by the named barriers.
-struct Shape {
-    int v, tpr, groups, stages, blocks;
-    size_t smem;
-};
-constexpr size_t kSmemMax = 227 * 1024;
-Shape shape_of(int D, long long rows, int row_bytes) {
-    const int nv = D / kVec;
-    Shape s;
-    s.v = nv <= 32 || (nv <= 512 && rows <= 152) ? 1 : 2;
-    s.tpr = ((nv + s.v - 1) / s.v + 31) / 32 * 32;
-    s.groups = std::max(1, (s.v == 1 ? 1024 : 512) / s.tpr);
-    if (s.tpr > 32) s.groups = std::min(s.groups, 8);
-    s.groups = (int)std::min<long long>(s.groups, std::max(1LL, (rows + 151) / 152));   // few rows: every SM has some
-    while (s.groups > 1 && smem_bytes(s.groups, D, row_bytes, 2) > kSmemMax) --s.groups;
-    s.stages = kRingMaxStages;
-    while (s.stages > 1 && smem_bytes(s.groups, D, row_bytes, s.stages) > kSmemMax) --s.stages;
-    s.blocks = (int)std::min<long long>(152, (rows + s.groups - 1) / s.groups);
-    s.smem = smem_bytes(s.groups, D, row_bytes, s.stages);
-    return s;
-}
-Shape fwd_shape(const BlockNormArgs& a) {
+RowShape fwd_shape(const BlockNormArgs& a) {
     const bool full = a.gate && a.gate_cols > 1;
-    return shape_of(a.D, a.rows, (full ? 3 : 2) * a.D * (a.dtype == GDN_BF16 ? 2 : 4));
+    return row_shape(a.D, a.rows, (full ? 3 : 2) * a.D * (a.dtype == GDN_BF16 ? 2 : 4));
 }
 // The backward's blocks do not depend on the type or the gate, so that the scratch is a function of rows and D: the
 // row bytes only change how many groups share a block, and blocks is at most one for each SM.
-Shape bwd_shape(const BlockNormArgs& a) {
+RowShape bwd_shape(const BlockNormArgs& a) {
     const bool full = a.gate && a.gate_cols > 1;
-    return shape_of(a.D, a.rows, (full ? 5 : 4) * a.D * (a.dtype == GDN_BF16 ? 2 : 4));
+    return row_shape(a.D, a.rows, (full ? 5 : 4) * a.D * (a.dtype == GDN_BF16 ? 2 : 4));
 }
 
-// The shared-memory limit of a kernel belongs to a device: raised once on each.
-template <auto KERNEL>
-cudaError_t allow_smem() {
-    constexpr int kMaxDevices = 64;
-    static std::atomic<bool> done[kMaxDevices];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
-    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
-    return e;
-}
 template <int V, typename T, bool GATE>
-cudaError_t fwd_one(const BlockNormArgs& a, const Shape& s) {
+cudaError_t fwd_one(const BlockNormArgs& a, const RowShape& s) {
     const cudaError_t e = allow_smem<block_norm_fwd_kernel<V, T, GATE>>();
     if (e != cudaSuccess) return e;
     block_norm_fwd_kernel<V, T, GATE><<<s.blocks, s.tpr * s.groups, s.smem, a.stream>>>(a, s.tpr, s.stages);
     return cudaGetLastError();
 }
 template <int V, typename T, bool GATE>
-cudaError_t bwd_one(const BlockNormArgs& a, const Shape& s, float* part) {
+cudaError_t bwd_one(const BlockNormArgs& a, const RowShape& s, float* part) {
     const cudaError_t e = allow_smem<block_norm_bwd_kernel<V, T, GATE>>();
     if (e != cudaSuccess) return e;
     block_norm_bwd_kernel<V, T, GATE><<<s.blocks, s.tpr * s.groups, s.smem, a.stream>>>(a, part, s.tpr, s.stages);
@@ -501,13 +349,13 @@ cudaError_t bwd_one(const BlockNormArgs& a, const Shape& s, float* part) {
 }
 template <typename T>
 cudaError_t fwd_typed(const BlockNormArgs& a) {
-    const Shape s = fwd_shape(a);
+    const RowShape s = fwd_shape(a);
     const bool full = a.gate && a.gate_cols > 1;
     if (s.v == 1) return full ? fwd_one<1, T, true>(a, s) : fwd_one<1, T, false>(a, s);
     return full ? fwd_one<2, T, true>(a, s) : fwd_one<2, T, false>(a, s);
 }
 template <typename T>
-cudaError_t bwd_typed(const BlockNormArgs& a, const Shape& s, float* part) {
+cudaError_t bwd_typed(const BlockNormArgs& a, const RowShape& s, float* part) {
     const bool full = a.gate && a.gate_cols > 1;
     if (s.v == 1) return full ? bwd_one<1, T, true>(a, s, part) : bwd_one<1, T, false>(a, s, part);
     return full ? bwd_one<2, T, true>(a, s, part) : bwd_one<2, T, false>(a, s, part);
@@ -524,7 +372,7 @@ size_t block_norm_bwd_workspace_bytes(long long rows, int D) {
 }
 
 cudaError_t launch_block_norm_bwd(const BlockNormArgs& a) {
-    const Shape s = bwd_shape(a);
+    const RowShape s = bwd_shape(a);
     float* part = (a.g_post || a.g_pre || a.g_scale) ? static_cast<float*>(a.workspace) : nullptr;
     if (s.blocks) {
         const cudaError_t e = a.dtype == GDN_BF16 ? bwd_typed<__nv_bfloat16>(a, s, part) : bwd_typed<float>(a, s, part);

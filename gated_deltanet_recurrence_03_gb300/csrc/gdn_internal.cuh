@@ -261,6 +261,112 @@ cudaError_t launch_block_norm_fwd(const BlockNormArgs& a);
 size_t block_norm_bwd_workspace_bytes(long long rows, int D);
 cudaError_t launch_block_norm_bwd(const BlockNormArgs& a);
 
+// ---------------------------------------------------------------- selective scan
+struct ScanArgs {
+    const void* u;              // [tokens][D] each, rows *_stride elements apart
+    const void* delta;
+    const void* z;              // or nullptr
+    const void* B;              // [tokens][G][N]
+    const void* C;
+    long long u_stride, delta_stride, z_stride, b_stride, c_stride;
+    const float* A_log;         // [D][N]
+    const float* skip;          // [D] or nullptr (0)
+    const float* dt_bias;       // [D] or nullptr (0)
+    const float* h0;            // [nseq][D][N] or nullptr (zeros)
+    void* y;                    // [tokens][D]
+    float* h_final;             // [nseq][D][N] or nullptr (not wanted)
+    int T, D, G, N;
+    int dtype;
+    const int32_t* cu;
+    int nseq;
+    int tokens;                 // all tokens of the call
+    // segments of `seg` tokens, `slots` of them (token_units.cuh; seg = 0: sequences), their states [slots][D][N],
+    // adjoints (gradients only) and sums of dt [slots][D]
+    int seg, slots;
+    float* states;
+    float* adjoints;
+    float* sum_dt;
+    // gradients
+    const void* gy;             // [tokens][D]
+    const float* gh;            // [nseq][D][N] or nullptr (zeros)
+    void* gu;                   // [tokens][D]
+    void* gdelta;
+    void* gB;                   // [tokens][G][N]
+    void* gC;
+    void* gz;
+    long long gb_stride, gc_stride, gz_stride;
+    float* gA;                  // [D][N], [D], [D], [nseq][D][N], each or nullptr (not wanted)
+    float* gskip;
+    float* gbias;
+    float* gh0;
+    float* part_A;              // [slots][D][N]: sums over a segment's tokens
+    float* part_s;              // [slots][2][D]
+    float* part_bc;             // [channel tile][tokens][2 N]: sums over a tile's channels
+    cudaStream_t stream;
+};
+constexpr int kScanSegment = 128;   // tokens of a segment of the gradients
+struct ScanFwdLayout {
+    int seg;
+    long long slots;
+    size_t sum_dt, total;       // byte offsets (the states come first)
+};
+ScanFwdLayout scan_fwd_layout(long long tokens, int D, int N, int nseq, bool packed);
+cudaError_t launch_scan_fwd(const ScanArgs& a);
+struct ScanBwdLayout {
+    int seg;
+    long long slots;
+    size_t adjoints, sum_dt, part_A, part_s, part_bc, total;
+};
+ScanBwdLayout scan_bwd_layout(long long tokens, int D, int G, int N, int nseq, bool packed);
+cudaError_t launch_scan_bwd(const ScanArgs& a);
+// The state before each segment and the adjoint behind it.
+cudaError_t launch_scan_states(const ScanArgs& a);
+cudaError_t launch_scan_join(const ScanArgs& a, bool adjoints);
+struct ScanStepArgs {
+    const void* u;              // [rows][D] each
+    const void* delta;
+    const void* z;
+    const void* B;              // [rows][G][N]
+    const void* C;
+    long long u_stride, delta_stride, z_stride, b_stride, c_stride;
+    const float* A_log;
+    const float* skip;
+    const float* dt_bias;
+    float* h;                   // [num_slots][D][N]
+    const int32_t* slots;       // [rows], or nullptr (row n uses state n)
+    int num_slots;
+    void* y;                    // [rows][D]
+    int rows, D, G, N;
+    int dtype;
+    cudaStream_t stream;
+};
+cudaError_t launch_scan_step(const ScanStepArgs& a);
+
+// ---------------------------------------------------------------- layer norm
+struct LayerNormArgs {
+    const void* x;              // [rows][D]
+    const void* b;              // [rows][D] added to x, or nullptr
+    const float* w;             // [D]
+    const float* bias;          // [D] or nullptr (0)
+    float eps;
+    void* n;                    // forward outputs
+    void* r;                    // x + b, or nullptr
+    const void* gn;             // backward inputs
+    const void* gr;             // or nullptr (no gradient at r)
+    void* gx;                   // backward outputs
+    float* gw;                  // [D] or nullptr (not wanted)
+    float* gbias;
+    void* workspace;
+    long long rows;
+    int D;
+    int dtype;
+    cudaStream_t stream;
+    unsigned* status;           // device status word (bounded waits)
+};
+cudaError_t launch_layer_norm_fwd(const LayerNormArgs& a);
+size_t layer_norm_bwd_workspace_bytes(long long rows, int D);
+cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a);
+
 // The CUDA driver's cuTensorMapEncodeTiled (looked up once), or nullptr when the CUDA driver lacks it.
 void* tensor_map_encoder();
 

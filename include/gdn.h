@@ -433,6 +433,103 @@ gdn_status_t gdn_block_norm_bwd(const void* x, const void* b, const void* gate, 
                                 const void* grad_n, void* grad_x, void* grad_b, void* grad_gate, float* grad_post,
                                 float* grad_pre, float* grad_res_scale, long long rows, int D, const gdn_opts_t* opts);
 
+/*
+ * gdn_selective_scan_fwd -- the selective state space scan: a recurrence with a diagonal state for each channel whose
+ * decay and write strength come from the token (the gated-linear rung of the update-rule table, learn-llm page "linear
+ * attention", with a state of N values a channel).  Per sequence, channel d of group g(d) = floor(d / (D / G)) and state n:
+ *     dt_t = softplus(delta_t + dt_bias),   A = -exp(A_log),   h_t = exp(dt_t A) h_{t-1} + dt_t u_t B_t
+ *     y_t  = (sum_n C_t h_t + skip u_t) silu(z_t)
+ *   u, delta, z  [B, T, D] dtype, token rows u_stride / delta_stride / z_stride elements apart (0 = dense: D); z may be
+ *                NULL (no gate).  u is what gdn_causal_conv1d_fwd writes
+ *   Bm, Cm       [B, T, G, N] dtype, rows b_stride / c_stride apart (0 = G N).  Slices of one packed projection can be
+ *                passed directly; strides are multiples of 16 bytes
+ *   A_log        [D, N] float;  skip, dt_bias [D] float, each may be NULL (0)
+ *   h0           [nseq, D, N] float or NULL (zero states); nseq = B, or num_seqs when packed
+ *   y            [B, T, D] dtype, dense; must not overlap any input
+ *   h_final      [nseq, D, N] float or NULL (not written); may equal h0 (in-place update)
+ * Supported: N in {8, 16, 32, 64}; D a multiple of 8 G; B, T >= 0, sequences of no tokens included (their h_final is h0,
+ * or zeros), B T < 2^31.  dt, decays, states and sums are fp32.  Token rows of no sequence (behind the last one's end)
+ * are not written.  A value that is not finite reaches only the results that the formula gives it to (its channel's
+ * later tokens, or, from B and C, its group's).  opts->workspace: 256-byte aligned, of
+ * gdn_selective_scan_fwd_workspace_size bytes (GDN_ERR_WORKSPACE if that is not 0 and it is missing or too small).
+ * opts->flags must be 0; dtype, cu_seqlens, num_seqs, stream and events[0] / [1] (around the kernels) are used; scale is
+ * not.  All pointers are 16-byte aligned.  Errors otherwise as for gdn_chunk_fwd.
+ */
+size_t gdn_selective_scan_fwd_workspace_size(int B, int T, int D, int G, int N, const gdn_opts_t* opts);
+gdn_status_t gdn_selective_scan_fwd(const void* u, long long u_stride, const void* delta, long long delta_stride,
+                                    const float* A_log, const void* Bm, long long b_stride, const void* Cm,
+                                    long long c_stride, const float* skip, const float* dt_bias, const void* z,
+                                    long long z_stride, const float* h0, void* y, float* h_final, int B, int T, int D,
+                                    int G, int N, const gdn_opts_t* opts);
+
+/*
+ * gdn_selective_scan_step -- one token for each of `rows` rows through the same recurrence, the states updated in place:
+ * u, delta, z [rows, D], Bm, Cm [rows, G, N] dtype (row strides as above), y [rows, D] dtype, dense.
+ *   h       [num_slots, D, N] float: a pool of states
+ *   slots   [rows] int32 DEVICE or NULL: row n uses state slots[n] (NULL: state n, num_slots >= rows).  A row whose slot
+ *           is outside 0 .. num_slots - 1 (-1, say) is idle: its y row is zeros, no state is touched.  Two rows must not
+ *           name the same state.
+ * Each state is read once and written once.  opts->flags must be 0; cu_seqlens and workspace are ignored.
+ */
+gdn_status_t gdn_selective_scan_step(const void* u, long long u_stride, const void* delta, long long delta_stride,
+                                     const float* A_log, const void* Bm, long long b_stride, const void* Cm,
+                                     long long c_stride, const float* skip, const float* dt_bias, const void* z,
+                                     long long z_stride, float* h, const int32_t* slots, int num_slots, void* y,
+                                     int rows, int D, int G, int N, const gdn_opts_t* opts);
+
+/*
+ * gdn_selective_scan_bwd -- gradients of a loss on (y, h_final) of gdn_selective_scan_fwd, from its inputs, grad_y =
+ * dL/dy and grad_h_final = dL/dh_final.  With p = grad_y silu(z) and lam = dL/dh walked backwards from grad_h_final,
+ *     lam_t = C_t p_t + a_{t+1} lam_{t+1};   dC = sum_d p h;   dB = sum_d lam dt u;   q = sum_n lam B;
+ *     w = lam a h_{t-1};   du = dt q + skip p;   ddelta = (u q + sum_n A w) sigmoid(delta + dt_bias);
+ *     dA_log = A sum_t dt w;   dskip = sum_t p u;   ddt_bias = sum_t ddelta;   dz = grad_y (sum_n C h + skip u) silu'(z);
+ *     dh0 = a_1 lam_1
+ *   inputs, strides, B, T, D, G, N   as gdn_selective_scan_fwd
+ *   grad_y         [B, T, D] dtype, dense;  grad_h_final [nseq, D, N] float or NULL (no loss on the final states)
+ *   grad_u, grad_delta   [B, T, D] dtype, dense
+ *   grad_B, grad_C       [B, T, G, N] dtype, rows gb_stride / gc_stride elements apart (0 = dense), and grad_z (required
+ *                  with z) [B, T, D] dtype, rows gz_stride apart: they can be slices of packed gradients
+ *   grad_A_log [D, N], grad_skip [D], grad_dt_bias [D], grad_h0 [nseq, D, N] float, each may be NULL (not computed)
+ * Sums are fp32 and rounded once.  No output may overlap an input or another output.  Deterministic.
+ * opts->workspace: 256-byte aligned, gdn_selective_scan_bwd_workspace_size bytes.
+ */
+size_t gdn_selective_scan_bwd_workspace_size(int B, int T, int D, int G, int N, const gdn_opts_t* opts);
+gdn_status_t gdn_selective_scan_bwd(const void* u, long long u_stride, const void* delta, long long delta_stride,
+                                    const float* A_log, const void* Bm, long long b_stride, const void* Cm,
+                                    long long c_stride, const float* skip, const float* dt_bias, const void* z,
+                                    long long z_stride, const float* h0, const void* grad_y, const float* grad_h_final,
+                                    void* grad_u, void* grad_delta, float* grad_A_log, void* grad_B, long long gb_stride,
+                                    void* grad_C, long long gc_stride, float* grad_skip, float* grad_dt_bias,
+                                    void* grad_z, long long gz_stride, float* grad_h0, int B, int T, int D, int G, int N,
+                                    const gdn_opts_t* opts);
+
+/*
+ * gdn_layer_norm_fwd -- layer norm with the residual add in front of it, in one pass over the rows: per row of D values
+ *     r = x + b,   n = (r - mean(r)) / sqrt(mean((r - mean(r))^2) + eps) * weight + bias
+ * (n from r before its rounding).
+ *   x, n      [rows, D] dtype, 16-byte aligned; n may equal x or b (in place)
+ *   b, r      [rows, D] dtype, both or neither (NULL: r = x); r may equal x or b, but not n
+ *   weight    [D] float;  bias [D] float or NULL (0)
+ * Supported: D a multiple of 8 up to 8192, rows >= 0.  eps = opts->norm_eps; opts->flags must be 0.
+ */
+gdn_status_t gdn_layer_norm_fwd(const void* x, const void* b, const float* weight, const float* bias, void* n, void* r,
+                                long long rows, int D, const gdn_opts_t* opts);
+
+/*
+ * gdn_layer_norm_bwd -- gradients through gdn_layer_norm_fwd given grad_n = dL/dn and, for a residual stream that goes
+ * on, grad_r = dL/dr, from the forward's inputs (r is formed again, so nothing of the forward has to be kept).
+ *   grad_r                     [rows, D] dtype or NULL (no loss on r)
+ *   grad_x                     [rows, D] dtype, 16-byte aligned: the gradient of x, and of b
+ *   grad_weight, grad_bias     [D] float, each may be NULL (not computed): sums over the rows in a fixed order through
+ *                              opts->workspace (256-byte aligned, gdn_layer_norm_bwd_workspace_size bytes; needed if one
+ *                              of them is wanted)
+ * grad_x overlaps no input.  Deterministic.  Errors and options as for gdn_layer_norm_fwd.
+ */
+size_t gdn_layer_norm_bwd_workspace_size(long long rows, int D, const gdn_opts_t* opts);
+gdn_status_t gdn_layer_norm_bwd(const void* x, const void* b, const float* weight, const void* grad_n, const void* grad_r,
+                                void* grad_x, float* grad_weight, float* grad_bias, long long rows, int D,
+                                const gdn_opts_t* opts);
+
 /* Synchronise `stream` (cudaStream_t, NULL = legacy), then read and clear the device status word
  * that kernels set when a bounded wait runs out.  GDN_OK if clear, GDN_ERR_TIMEOUT if set,
  * GDN_ERR_CUDA if the synchronisation itself failed. */
