@@ -13,198 +13,274 @@ namespace {
 
 template <int N>
 struct Shape {
-    static constexpr int L = N / 4, CH = kScanThreads / L, K = N <= 16 ? 16 : 32;
-    static constexpr int kRow = CH + (32 / L > 4 ? 32 / L : 4);   // floats of a row of sums: no bank conflicts
-    static constexpr int kVecs = (K * CH / 4 + kScanThreads - 1) / kScanThreads;   // 4-channel vectors a thread
-    static constexpr int kBC = (2 * K * N / 4 + kScanThreads - 1) / kScanThreads;  // 4-state vectors of B and C a thread
+    static constexpr int L = N / 4, CH = kScanThreads / L;
 };
 
-// The raw values of a thread's share of a tile.
-template <int N, typename T, int IN>
-struct Tile {
-    Raw4<T> x[IN][Shape<N>::kVecs];
-    Raw4<T> bc[Shape<N>::kBC];
+// Per-thread shares of a tile of K tokens by CH channels among M threads: 4-channel vectors, and 4-state vectors of B and C.
+template <int N, int K, int M>
+struct Share {
+    static constexpr int kVecs = (K * Shape<N>::CH / 4 + M - 1) / M, kBC = (2 * K * N / 4 + M - 1) / M;
+};
+struct Rows {
+    const void* p;
+    long long stride;
 };
 
-template <int N, typename T, int IN>
-__device__ __forceinline__ void load_tile(Tile<N, T, IN>& t, const T* const (&src)[IN], const long long (&stride)[IN],
-                                          const T* B, long long b_stride, const T* C, long long c_stride, long long t0,
-                                          int tokens, int channels) {
-    using S = Shape<N>;
-    const int tid = threadIdx.x;
+// Vectors of the tile's tensors as loaded; zeros past the end and where there is none.
+template <int K, int CH, int M, typename T, int V>
+__device__ __forceinline__ void load_rows(Raw4<T> (&x)[V], Rows src, int d0, long long t0, int tokens, int channels, int tid) {
 #pragma unroll
-    for (int v = 0; v < S::kVecs; ++v) {
-        const int i = tid + v * kScanThreads, k = i / (S::CH / 4), c = i % (S::CH / 4) * 4;
-        const bool ok = k < tokens && c < channels;
-#pragma unroll
-        for (int x = 0; x < IN; ++x)
-            t.x[x][v] = ok && src[x] ? load4(src[x] + (t0 + k) * stride[x] + c) : Raw4<T>::zero();
-    }
-#pragma unroll
-    for (int v = 0; v < S::kBC; ++v) {
-        const int i = tid + v * kScanThreads, which = i / (S::K * N / 4), k = i / (N / 4) % S::K, n = i % (N / 4) * 4;
-        const T* p = which == 0 ? B : C;
-        t.bc[v] = which < 2 && k < tokens && p ? load4(p + (t0 + k) * (which == 0 ? b_stride : c_stride) + n) : Raw4<T>::zero();
+    for (int v = 0; v < V; ++v) {
+        const int i = tid + v * M, k = i / (CH / 4), c = i % (CH / 4) * 4;
+        x[v] = k < tokens && c < channels && src.p ? load4(static_cast<const T*>(src.p) + (t0 + k) * src.stride + d0 + c)
+                                                   : Raw4<T>::zero();
     }
 }
+// B, then C (C.p may be nullptr), of group g.
+template <int K, int N, int M, typename T, int V>
+__device__ __forceinline__ void load_bc(Raw4<T> (&x)[V], Rows B, Rows C, int g, long long t0, int tokens, int tid) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int i = tid + v * M, which = i / (K * N / 4), k = i / (N / 4) % K, n = i % (N / 4) * 4;
+        const Rows r = which == 0 ? B : C;
+        x[v] = which < 2 && k < tokens && r.p ? load4(static_cast<const T*>(r.p) + (t0 + k) * r.stride + (size_t)g * N + n)
+                                              : Raw4<T>::zero();
+    }
+}
+template <int K, int CH, int M, typename T, int V>
+__device__ __forceinline__ void form_dt(float2 (&to)[K][CH], const Raw4<T> (&u)[V], const Raw4<T> (&delta)[V], float4 bias,
+                                        int tokens, int channels, int tid) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int i = tid + v * M, k = i / (CH / 4), c = i % (CH / 4) * 4;
+        if (k >= K) break;
+        const float4 x = u[v].f();
+        float4 d = softplus4(add4(delta[v].f(), bias));
+        if (k >= tokens || c >= channels) d = make_float4(0.f, 0.f, 0.f, 0.f);   // past the end: the state stays as it is
+        float4* p = reinterpret_cast<float4*>(&to[k][c]);
+        p[0] = make_float4(d.x, d.x * x.x, d.y, d.y * x.y);
+        p[1] = make_float4(d.z, d.z * x.z, d.w, d.w * x.w);
+    }
+}
+template <int K, int N, int M, typename T, int V>
+__device__ __forceinline__ void form_bc(float (&to)[2][K][N], const Raw4<T> (&x)[V], int tid) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int i = tid + v * M, which = i / (K * N / 4), k = i / (N / 4) % K, n = i % (N / 4) * 4;
+        if (which < 2) *reinterpret_cast<float4*>(&to[which][k][n]) = x[v].f();
+    }
+}
+__device__ __forceinline__ float4 column_values(const float* p, const ChannelTile& tile, int c) {
+    return p && c < tile.n ? *reinterpret_cast<const float4*>(p + tile.d0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
 
-// The outputs, or (STATE) each segment's own contribution to the state, from zero, and its sum of dt.  ADJ: also the
-// contribution of its outputs to the adjoint of the state before it, sum_t (a_first .. a_t) C_t p_t, p = dy silu(z).
-template <int N, typename T, bool STATE, bool ADJ>
-__global__ void __launch_bounds__(kScanThreads) scan_kernel(const __grid_constant__ ScanArgs a) {
-    using S = Shape<N>;
-    constexpr int L = S::L, CH = S::CH, K = S::K;
-    constexpr int IN = STATE && !ADJ ? 2 : ADJ ? 4 : 3;
+// Each segment's own contribution to the state, from zero, and its sum of dt.  ADJ: also the contribution of its outputs
+// to the adjoint of the state before it, sum_t (a_first .. a_t) C_t p_t with p = dy silu(z).
+template <int N, typename T, bool ADJ>
+__global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_constant__ ScanArgs a) {
+    constexpr int L = Shape<N>::L, CH = Shape<N>::CH, K = N <= 16 ? 16 : 32, M = kScanThreads;
+    using S = Share<N, K, M>;
     __shared__ __align__(16) float2 s_dt[K][CH];
     __shared__ __align__(16) float s_p[ADJ ? K : 1][CH];
     __shared__ __align__(16) float s_bc[2][K][N];
-    __shared__ __align__(16) float s_y[STATE ? 1 : K][S::kRow];
     const int tiles = a.G * ((a.D / a.G + CH - 1) / CH), slot = blockIdx.x / tiles;
     const ChannelTile tile = channel_tile(a.D, a.G, CH, blockIdx.x % tiles);
     Unit u;
     if (!unit_at(a.cu, a.T, a.nseq, a.seg, slot, false, u)) return;
-    if (STATE && (ADJ ? u.first && u.last : u.last)) return;   // nothing reads it
-    const int tid = threadIdx.x, lane = tid & 31, cl = tid / L, n4 = tid % L * 4;
-    const int c4 = tid % (CH / 4) * 4;   // the thread's channels in the elementwise work
+    if (ADJ ? u.first && u.last : u.last) return;   // nothing reads it
+    const int tid = threadIdx.x, cl = tid / L, n4 = tid % L * 4, c4 = tid % (CH / 4) * 4;
     const bool own = cl < tile.n;
     const size_t at = (size_t)(tile.d0 + cl) * N + n4, DN = (size_t)a.D * N;
-
     float2 A2[2], h[2], lam[2], E[2];
-    h[0] = h[1] = lam[0] = lam[1] = all2(0.f);
+    h[0] = h[1] = lam[0] = lam[1] = A2[0] = A2[1] = all2(0.f);
     E[0] = E[1] = all2(1.f);
-    A2[0] = A2[1] = all2(0.f);
     float sum_dt = 0.f;
     if (own) {
         const float4 l = *reinterpret_cast<const float4*>(a.A_log + at);
         A2[0] = make_float2(rate2(l.x), rate2(l.y));
         A2[1] = make_float2(rate2(l.z), rate2(l.w));
-        if (!STATE) {
-            const float* from = a.seg ? a.states + (size_t)slot * DN : a.h0 ? a.h0 + (size_t)u.seq * DN : nullptr;
-            if (from) {
-                const float4 f = *reinterpret_cast<const float4*>(from + at);
-                h[0] = make_float2(f.x, f.y);
-                h[1] = make_float2(f.z, f.w);
-            }
+    }
+    const float4 bias = column_values(a.dt_bias, tile, c4);
+    const Rows B{a.B, a.b_stride}, C{ADJ ? a.C : nullptr, a.c_stride};
+    Raw4<T> ru[S::kVecs], rd[S::kVecs], rz[ADJ ? S::kVecs : 1], rg[ADJ ? S::kVecs : 1], rbc[S::kBC];
+    auto load = [&](long long t0) {
+        const int tokens = (int)min((long long)K, u.t1 - t0);
+        load_rows<K, CH, M>(ru, Rows{a.u, a.u_stride}, tile.d0, t0, tokens, tile.n, tid);
+        load_rows<K, CH, M>(rd, Rows{a.delta, a.delta_stride}, tile.d0, t0, tokens, tile.n, tid);
+        if constexpr (ADJ) {
+            load_rows<K, CH, M>(rz, Rows{a.z, a.z_stride}, tile.d0, t0, tokens, tile.n, tid);
+            load_rows<K, CH, M>(rg, Rows{a.gy, a.D}, tile.d0, t0, tokens, tile.n, tid);
         }
-    }
-    float4 bias = make_float4(0.f, 0.f, 0.f, 0.f), skip = bias;
-    if (c4 < tile.n) {
-        if (a.dt_bias) bias = *reinterpret_cast<const float4*>(a.dt_bias + tile.d0 + c4);
-        if (!STATE && a.skip) skip = *reinterpret_cast<const float4*>(a.skip + tile.d0 + c4);
-    }
-    auto head = [&](const void* p) { return p ? static_cast<const T*>(p) + tile.d0 : nullptr; };
-    const T* src[IN];
-    long long stride[IN];
-    src[0] = head(a.u); stride[0] = a.u_stride;
-    src[1] = head(a.delta); stride[1] = a.delta_stride;
-    if constexpr (IN > 2) { src[2] = head(a.z); stride[2] = a.z_stride; }
-    if constexpr (IN > 3) { src[3] = head(a.gy); stride[3] = a.D; }
-    const T* B = static_cast<const T*>(a.B) + (size_t)tile.g * N;
-    const T* C = STATE && !ADJ ? nullptr : static_cast<const T*>(a.C) + (size_t)tile.g * N;
-
-    Tile<N, T, IN> raw;
-    load_tile<N, T, IN>(raw, src, stride, B, a.b_stride, C, a.c_stride, u.t0, (int)min((long long)K, u.t1 - u.t0), tile.n);
+        load_bc<K, N, M>(rbc, B, C, tile.g, t0, tokens, tid);
+    };
+    load(u.t0);
     for (long long t0 = u.t0; t0 < u.t1; t0 += K) {
         const int tokens = (int)min((long long)K, u.t1 - t0);
-        Raw4<T> cu[S::kVecs], cz[S::kVecs];
-#pragma unroll
-        for (int v = 0; v < S::kVecs; ++v) {
-            const int i = tid + v * kScanThreads, k = i / (CH / 4);
-            if (k >= K) break;
-            float4 x = raw.x[0][v].f(), d = raw.x[1][v].f();
-            const bool ok = k < tokens && c4 < tile.n;   // a token past the end leaves the state as it is: dt = 0
-            d.x = ok ? softplus_f(d.x + bias.x) : 0.f;
-            d.y = ok ? softplus_f(d.y + bias.y) : 0.f;
-            d.z = ok ? softplus_f(d.z + bias.z) : 0.f;
-            d.w = ok ? softplus_f(d.w + bias.w) : 0.f;
-            float4* to = reinterpret_cast<float4*>(&s_dt[k][c4]);
-            to[0] = make_float4(d.x, d.x * x.x, d.y, d.y * x.y);
-            to[1] = make_float4(d.z, d.z * x.z, d.w, d.w * x.w);
-            cu[v] = raw.x[0][v];
-            if constexpr (!STATE) cz[v] = raw.x[2][v];
-            if constexpr (ADJ) {
-                float4 p = raw.x[3][v].f();
-                if (a.z) {
-                    const float4 z = raw.x[2][v].f();
-                    p.x *= z.x * logistic_f(z.x);
-                    p.y *= z.y * logistic_f(z.y);
-                    p.z *= z.z * logistic_f(z.z);
-                    p.w *= z.w * logistic_f(z.w);
-                }
-                *reinterpret_cast<float4*>(&s_p[k][c4]) = p;
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < S::kBC; ++v) {
-            const int i = tid + v * kScanThreads, which = i / (K * N / 4), k = i / (N / 4) % K, n = i % (N / 4) * 4;
-            if (which < 2) *reinterpret_cast<float4*>(&s_bc[which][k][n]) = raw.bc[v].f();
-        }
-        __syncthreads();
-        if (t0 + K < u.t1)
-            load_tile<N, T, IN>(raw, src, stride, B, a.b_stride, C, a.c_stride, t0 + K, (int)min((long long)K, u.t1 - t0 - K),
-                                tile.n);
-#pragma unroll 1
-        for (int k0 = 0; k0 < K; k0 += L) {
-            float part[L];
-#pragma unroll
-            for (int e = 0; e < L; ++e) {
-                const int k = k0 + e;
-                const float2 dd = s_dt[k][cl];
-                const float4 b = *reinterpret_cast<const float4*>(&s_bc[0][k][n4]);
-                float2 ar[2], w[2] = {make_float2(b.x, b.y), make_float2(b.z, b.w)};
-                float2 c[2];
-                if constexpr (!STATE || ADJ) {
-                    const float4 x = *reinterpret_cast<const float4*>(&s_bc[1][k][n4]);
-                    c[0] = make_float2(x.x, x.y);
-                    c[1] = make_float2(x.z, x.w);
-                }
-                float2 y = all2(0.f);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    ar[i] = mul2(A2[i], all2(dd.x));
-                    ar[i] = make_float2(ex2(ar[i].x), ex2(ar[i].y));
-                    h[i] = fma2(ar[i], h[i], mul2(w[i], all2(dd.y)));
-                    if constexpr (!STATE) y = i == 0 ? mul2(h[i], c[i]) : fma2(h[i], c[i], y);
-                    if constexpr (ADJ) {
-                        E[i] = mul2(E[i], ar[i]);
-                        lam[i] = fma2(E[i], mul2(c[i], all2(s_p[k][cl])), lam[i]);
-                    }
-                }
-                if constexpr (STATE) sum_dt += dd.x;
-                part[e] = y.x + y.y;
-            }
-            if constexpr (!STATE) s_y[k0 + lane % L][cl] = transpose_sum<L>(part, lane);
-        }
-        __syncthreads();
-        if constexpr (!STATE) {
+        form_dt<K, CH, M>(s_dt, ru, rd, bias, tokens, tile.n, tid);
+        form_bc<K, N, M>(s_bc, rbc, tid);
+        if constexpr (ADJ) {
 #pragma unroll
             for (int v = 0; v < S::kVecs; ++v) {
-                const int i = tid + v * kScanThreads, k = i / (CH / 4);
-                if (k >= tokens || c4 >= tile.n) continue;
-                float4 y = *reinterpret_cast<const float4*>(&s_y[k][c4]);
-                const float4 x = cu[v].f();
-                y = make_float4(fmaf(skip.x, x.x, y.x), fmaf(skip.y, x.y, y.y), fmaf(skip.z, x.z, y.z), fmaf(skip.w, x.w, y.w));
-                if (a.z) {
-                    const float4 z = cz[v].f();
-                    y.x *= z.x * logistic_f(z.x);
-                    y.y *= z.y * logistic_f(z.y);
-                    y.z *= z.z * logistic_f(z.z);
-                    y.w *= z.w * logistic_f(z.w);
-                }
-                store4(static_cast<T*>(a.y) + (t0 + k) * a.D + tile.d0 + c4, y);
+                const int i = tid + v * M, k = i / (CH / 4);
+                if (k >= K) break;
+                *reinterpret_cast<float4*>(&s_p[k][c4]) = a.z ? gated4(rg[v].f(), rz[v].f()) : rg[v].f();
             }
         }
+        __syncthreads();
+        if (t0 + K < u.t1) load(t0 + K);
+#pragma unroll 4
+        for (int k = 0; k < K; ++k) {
+            const float2 dd = s_dt[k][cl];
+            const float4 b = *reinterpret_cast<const float4*>(&s_bc[0][k][n4]);
+            const float2 w[2] = {make_float2(b.x, b.y), make_float2(b.z, b.w)};
+            float2 c[2];
+            if constexpr (ADJ) {
+                const float4 x = *reinterpret_cast<const float4*>(&s_bc[1][k][n4]);
+                const float p = s_p[k][cl];
+                c[0] = mul2(make_float2(x.x, x.y), all2(p));
+                c[1] = mul2(make_float2(x.z, x.w), all2(p));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 e = decay(A2[i], dd.x);
+                h[i] = fma2(e, h[i], mul2(w[i], all2(dd.y)));
+                if constexpr (ADJ) {
+                    E[i] = mul2(E[i], e);
+                    lam[i] = fma2(E[i], c[i], lam[i]);
+                }
+            }
+            sum_dt += dd.x;
+        }
+        __syncthreads();
     }
     if (!own) return;
-    const float4 hf = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
-    if constexpr (STATE) {
-        *reinterpret_cast<float4*>(a.states + (size_t)slot * DN + at) = hf;
-        if constexpr (ADJ)
-            *reinterpret_cast<float4*>(a.adjoints + (size_t)slot * DN + at) = make_float4(lam[0].x, lam[0].y, lam[1].x, lam[1].y);
-        if (n4 == 0) a.sum_dt[(size_t)slot * a.D + tile.d0 + cl] = sum_dt;
-    } else if (a.h_final && u.last) {
-        *reinterpret_cast<float4*>(a.h_final + (size_t)u.seq * DN + at) = hf;
+    *reinterpret_cast<float4*>(a.states + (size_t)slot * DN + at) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+    if constexpr (ADJ)
+        *reinterpret_cast<float4*>(a.adjoints + (size_t)slot * DN + at) = make_float4(lam[0].x, lam[0].y, lam[1].x, lam[1].y);
+    if (n4 == 0) a.sum_dt[(size_t)slot * a.D + tile.d0 + cl] = sum_dt;
+}
+
+// The outputs.  Four warps walk the states; two others form the next tile's dt, dt u, B and C in shared memory and finish
+// the last one's outputs meanwhile (one barrier a tile), so that a sequence's walk waits for neither.
+constexpr int kHelpers = 64;
+template <int N, typename T>
+__global__ void __launch_bounds__(kScanThreads + kHelpers) scan_main_kernel(const __grid_constant__ ScanArgs a) {
+    constexpr int L = Shape<N>::L, CH = Shape<N>::CH, K = N == 16 || N == 32 ? 32 : 16, M = kHelpers;
+    constexpr int kRow = CH + (32 / L > 4 ? 32 / L : 4);   // floats of a row of sums: no bank conflicts
+    using S = Share<N, K, M>;
+    __shared__ __align__(16) float2 s_dt[2][K][CH];
+    __shared__ __align__(16) float s_bc[2][2][K][N];
+    __shared__ __align__(16) float s_y[2][K][kRow];
+    const int tiles = a.G * ((a.D / a.G + CH - 1) / CH), slot = blockIdx.x / tiles;
+    const ChannelTile tile = channel_tile(a.D, a.G, CH, blockIdx.x % tiles);
+    Unit u;
+    if (!unit_at(a.cu, a.T, a.nseq, a.seg, slot, false, u)) return;
+    const int n = (int)((u.t1 - u.t0 + K - 1) / K);
+    const size_t DN = (size_t)a.D * N;
+    if (threadIdx.x >= kScanThreads) {
+        const int tid = threadIdx.x - kScanThreads, c4 = tid % (CH / 4) * 4;
+        const float4 bias = column_values(a.dt_bias, tile, c4), skip = column_values(a.skip, tile, c4);
+        const Rows B{a.B, a.b_stride}, C{a.C, a.c_stride};
+        Raw4<T> ru[S::kVecs], rd[S::kVecs], rz[S::kVecs], rbc[S::kBC];   // the next tile's
+        Raw4<T> cu[S::kVecs], cz[S::kVecs], pu[S::kVecs], pz[S::kVecs];  // of the tile that is walked, of the last one
+        auto tokens_of = [&](int i) { return (int)min((long long)K, u.t1 - u.t0 - (long long)i * K); };
+        auto load = [&](int i) {
+            const long long t0 = u.t0 + (long long)i * K;
+            const int tokens = tokens_of(i);
+            load_rows<K, CH, M>(ru, Rows{a.u, a.u_stride}, tile.d0, t0, tokens, tile.n, tid);
+            load_rows<K, CH, M>(rd, Rows{a.delta, a.delta_stride}, tile.d0, t0, tokens, tile.n, tid);
+            load_rows<K, CH, M>(rz, Rows{a.z, a.z_stride}, tile.d0, t0, tokens, tile.n, tid);
+            load_bc<K, N, M>(rbc, B, C, tile.g, t0, tokens, tid);
+        };
+        auto form = [&](int i) {
+            form_dt<K, CH, M>(s_dt[i & 1], ru, rd, bias, tokens_of(i), tile.n, tid);
+            form_bc<K, N, M>(s_bc[i & 1], rbc, tid);
+        };
+        auto finish = [&](int i, const Raw4<T> (&fu)[S::kVecs], const Raw4<T> (&fz)[S::kVecs]) {
+            const long long t0 = u.t0 + (long long)i * K;
+            const int tokens = tokens_of(i);
+#pragma unroll
+            for (int v = 0; v < S::kVecs; ++v) {
+                const int e = tid + v * M, k = e / (CH / 4);
+                if (k >= tokens || c4 >= tile.n) continue;
+                float4 y = *reinterpret_cast<const float4*>(&s_y[i & 1][k][c4]);
+                const float4 x = fu[v].f();
+                const float2 ya = fma2(make_float2(skip.x, skip.y), make_float2(x.x, x.y), make_float2(y.x, y.y));
+                const float2 yb = fma2(make_float2(skip.z, skip.w), make_float2(x.z, x.w), make_float2(y.z, y.w));
+                y = make_float4(ya.x, ya.y, yb.x, yb.y);
+                if (a.z) y = gated4(y, fz[v].f());
+                store4(static_cast<T*>(a.y) + (t0 + k) * a.D + tile.d0 + c4, y);
+            }
+        };
+        auto keep = [&]() {
+#pragma unroll
+            for (int v = 0; v < S::kVecs; ++v) {
+                pu[v] = cu[v];
+                pz[v] = cz[v];
+                cu[v] = ru[v];
+                cz[v] = rz[v];
+            }
+        };
+        if (n > 0) {
+            load(0);
+            form(0);
+            keep();
+            if (n > 1) load(1);
+        }
+        __syncthreads();
+        for (int i = 0; i < n; ++i) {
+            if (i + 1 < n) form(i + 1);
+            keep();   // pu, pz: tile i
+            if (i + 2 < n) load(i + 2);
+            __syncthreads();
+            finish(i, pu, pz);
+        }
+        return;
     }
+    const int tid = threadIdx.x, lane = tid & 31, cl = tid / L, n4 = tid % L * 4;
+    const bool own = cl < tile.n;
+    const size_t at = (size_t)(tile.d0 + cl) * N + n4;
+    float2 A2[2], h[2];
+    h[0] = h[1] = A2[0] = A2[1] = all2(0.f);
+    if (own) {
+        const float4 l = *reinterpret_cast<const float4*>(a.A_log + at);
+        A2[0] = make_float2(rate2(l.x), rate2(l.y));
+        A2[1] = make_float2(rate2(l.z), rate2(l.w));
+        const float* from = a.seg ? a.states + (size_t)slot * DN : a.h0 ? a.h0 + (size_t)u.seq * DN : nullptr;
+        if (from) {
+            const float4 f = *reinterpret_cast<const float4*>(from + at);
+            h[0] = make_float2(f.x, f.y);
+            h[1] = make_float2(f.z, f.w);
+        }
+    }
+    __syncthreads();
+    for (int i = 0; i < n; ++i) {
+        const float2(*dt)[CH] = s_dt[i & 1];
+        const float(*bc)[K][N] = s_bc[i & 1];
+        constexpr int U = L < 8 ? 8 : L;   // tokens between whose results the instructions can be moved
+#pragma unroll 1
+        for (int k0 = 0; k0 < K; k0 += U) {
+#pragma unroll
+            for (int j = 0; j < U; j += L) {
+                float part[L];
+#pragma unroll
+                for (int e = 0; e < L; ++e) {
+                    const int k = k0 + j + e;
+                    const float2 dd = dt[k][cl];
+                    const float4 b = *reinterpret_cast<const float4*>(&bc[0][k][n4]);
+                    const float4 c = *reinterpret_cast<const float4*>(&bc[1][k][n4]);
+                    h[0] = fma2(decay(A2[0], dd.x), h[0], mul2(make_float2(b.x, b.y), all2(dd.y)));
+                    h[1] = fma2(decay(A2[1], dd.x), h[1], mul2(make_float2(b.z, b.w), all2(dd.y)));
+                    const float2 y = fma2(h[1], make_float2(c.z, c.w), mul2(h[0], make_float2(c.x, c.y)));
+                    part[e] = y.x + y.y;
+                }
+                s_y[i & 1][k0 + j + lane % L][cl] = transpose_sum<L>(part, lane);
+            }
+        }
+        __syncthreads();
+    }
+    if (own && a.h_final && u.last)
+        *reinterpret_cast<float4*>(a.h_final + (size_t)u.seq * DN + at) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
 }
 
 // The segments' contributions, in place: states to the state before each segment, adjoints (blockIdx.y 1) to the
@@ -242,8 +318,8 @@ __global__ void __launch_bounds__(kScanThreads) scan_join_kernel(const __grid_co
             const size_t slot = base + (adj ? n - 1 - j0 - w : j0 + w);
             *reinterpret_cast<float4*>(s + slot * DN) = h;
             if (j0 + w < n - 1)
-                h = make_float4(fmaf(ex2(A[0] * dt[w]), h.x, x[w].x), fmaf(ex2(A[1] * dt[w]), h.y, x[w].y),
-                                fmaf(ex2(A[2] * dt[w]), h.z, x[w].z), fmaf(ex2(A[3] * dt[w]), h.w, x[w].w));
+                h = make_float4(fmaf(decay(A[0], dt[w]), h.x, x[w].x), fmaf(decay(A[1], dt[w]), h.y, x[w].y),
+                                fmaf(decay(A[2], dt[w]), h.z, x[w].z), fmaf(decay(A[3], dt[w]), h.w, x[w].w));
         }
     }
 }
@@ -270,10 +346,10 @@ __global__ void __launch_bounds__(kScanThreads) scan_step_kernel(const __grid_co
         const float4 c = load4(static_cast<const T*>(a.C) + (size_t)row * a.c_stride + (size_t)g * N + n4).f();
         u = to_f32(static_cast<const T*>(a.u)[(size_t)row * a.u_stride + d]);
         const float raw = to_f32(static_cast<const T*>(a.delta)[(size_t)row * a.delta_stride + d]);
-        const float dt = softplus_f(raw + (a.dt_bias ? a.dt_bias[d] : 0.f)), w = dt * u;
+        const float dt = softplus2(all2(raw + (a.dt_bias ? a.dt_bias[d] : 0.f))).x, w = dt * u;
         const float4 x = make_float4(
-            fmaf(ex2(dt * rate2(l.x)), h.x, w * b.x), fmaf(ex2(dt * rate2(l.y)), h.y, w * b.y),
-            fmaf(ex2(dt * rate2(l.z)), h.z, w * b.z), fmaf(ex2(dt * rate2(l.w)), h.w, w * b.w));
+            fmaf(decay(rate2(l.x), dt), h.x, w * b.x), fmaf(decay(rate2(l.y), dt), h.y, w * b.y),
+            fmaf(decay(rate2(l.z), dt), h.z, w * b.z), fmaf(decay(rate2(l.w), dt), h.w, w * b.w));
         *hp = x;
         s = fmaf(x.x, c.x, x.y * c.y) + fmaf(x.z, c.z, x.w * c.w);
     }
@@ -297,16 +373,16 @@ template <int N, typename T>
 cudaError_t fwd_typed(const ScanArgs& a) {
     const unsigned blocks = (unsigned)((long long)a.slots * tiles_of<N>(a));
     if (a.seg) {
-        scan_kernel<N, T, true, false><<<blocks, kScanThreads, 0, a.stream>>>(a);
+        scan_state_kernel<N, T, false><<<blocks, kScanThreads, 0, a.stream>>>(a);
         const cudaError_t e = launch_scan_join(a, false);
         if (e != cudaSuccess) return e;
     }
-    scan_kernel<N, T, false, false><<<blocks, kScanThreads, 0, a.stream>>>(a);
+    scan_main_kernel<N, T><<<blocks, kScanThreads + kHelpers, 0, a.stream>>>(a);
     return cudaGetLastError();
 }
 template <int N, typename T>
 cudaError_t adj_typed(const ScanArgs& a) {
-    scan_kernel<N, T, true, true><<<(unsigned)((long long)a.slots * tiles_of<N>(a)), kScanThreads, 0, a.stream>>>(a);
+    scan_state_kernel<N, T, true><<<(unsigned)((long long)a.slots * tiles_of<N>(a)), kScanThreads, 0, a.stream>>>(a);
     return cudaGetLastError();
 }
 template <int N, typename T>

@@ -85,22 +85,17 @@ __device__ __forceinline__ void form_tile(const Tile<N, T>& t, Smem<N>& sm, cons
         if (k >= S::K) break;
         const float4 x = t.u[v].f(), d = t.d[v].f();
         const bool ok = k < tokens && c < channels;
-        float dt[4] = {d.x + bias.x, d.y + bias.y, d.z + bias.z, d.w + bias.w}, p[4] = {0.f, 0.f, 0.f, 0.f};
+        const float4 sp = softplus4(add4(d, bias));
+        float dt[4] = {sp.x, sp.y, sp.z, sp.w}, p[4] = {0.f, 0.f, 0.f, 0.f};
         const float uu[4] = {x.x, x.y, x.z, x.w};
         if (FULL) {
-            const float4 g = t.gy[v].f();
+            float4 g = t.gy[v].f();
+            if (a.z) g = gated4(g, t.z[v].f());
             p[0] = g.x; p[1] = g.y; p[2] = g.z; p[3] = g.w;
-            if (a.z) {
-                const float4 z = t.z[v].f();
-                p[0] *= z.x * logistic_f(z.x);
-                p[1] *= z.y * logistic_f(z.y);
-                p[2] *= z.z * logistic_f(z.z);
-                p[3] *= z.w * logistic_f(z.w);
-            }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            dt[e] = ok ? softplus_f(dt[e]) : 0.f;   // dt = 0: a token past the end changes nothing
+            dt[e] = ok ? dt[e] : 0.f;   // dt = 0: a token past the end changes nothing
             sm.tok[k][c + e] = make_float4(dt[e], dt[e] * uu[e], p[e], 0.f);
         }
     }
@@ -215,8 +210,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_bwd_kernel(const __grid_
                 const float2 dd = *reinterpret_cast<const float2*>(&sm.tok[k][ch[s]]);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float2 e = mul2(A2[s][i], all2(dd.x));
-                    h[s][i] = fma2(make_float2(ex2(e.x), ex2(e.y)), h[s][i], mul2(B[i], all2(dd.y)));
+                    h[s][i] = fma2(decay(A2[s][i], dd.x), h[s][i], mul2(B[i], all2(dd.y)));
                 }
             }
         }
@@ -247,8 +241,7 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_bwd_kernel(const __grid_
                 const float2 dd = *reinterpret_cast<const float2*>(&sm.tok[k][ch[s]]);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float2 e = mul2(A2[s][i], all2(dd.x));
-                    aa[k][s][i] = make_float2(ex2(e.x), ex2(e.y));
+                    aa[k][s][i] = decay(A2[s][i], dd.x);
                     P[k][s][i] = mul2(aa[k][s][i], h[s][i]);
                     h[s][i] = fma2(B[i], all2(dd.y), P[k][s][i]);
                 }

@@ -42,14 +42,63 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// A token's decay 2^(A dt).  ex2.approx is 0.5 to 2e-8 low on average for exponents between -1/2 and 0, which compounds over
+// a channel's memory (77 tokens: 1.6e-6 of the state, of which 0.6e-6 is rounding); this much more in the exponent leaves
+// an average within 0.9e-8 there, and 2^0 is 1 with it too.
+constexpr float kDecayShift = 2e-8f;
+__device__ __forceinline__ float decay(float A2, float dt) { return ex2(fmaf(A2, dt, kDecayShift)); }
+__device__ __forceinline__ float2 decay(float2 A2, float dt) { return ex2(fma2(A2, all2(dt), all2(kDecayShift))); }
 // A = -exp(A_log) in powers of two, finite: a token past a sequence's end has dt = 0 and must leave the state as it is.
 __device__ __forceinline__ float rate2(float A_log) {
     const float A = -kLog2e * expf(A_log);
     return A < -3e38f ? -3e38f : A;
 }
-// dt = softplus(x), as the raw gates have it.
-__device__ __forceinline__ float softplus_f(float x) { return fmaxf(x, 0.f) + log1pf(__expf(-fabsf(x))); }
-__device__ __forceinline__ float logistic_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// dt = softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) with the exponent's rounding put back, log1p(e) as e times a
+// polynomial (a least-maximum fit of log1p(e) / e on [0, 1], 5e-9 off; with its roundings 1.6e-7).
+__device__ __forceinline__ float2 softplus2(float2 x) {
+    const float2 n = make_float2(fmaxf(-fabsf(x.x), -150.f), fmaxf(-fabsf(x.y), -150.f));   // finite: exp(-150) is 0
+    const float2 t = mul2(n, all2(kLog2e));
+    const float2 rest = fma2(n, all2(kLog2e), make_float2(-t.x, -t.y));
+    float2 e = ex2(t);
+    e = fma2(e, mul2(rest, all2(kLn2)), e);
+    float2 p = all2(-0.0032440212f);
+    p = fma2(p, e, all2(0.019851444f));
+    p = fma2(p, e, all2(-0.056959499f));
+    p = fma2(p, e, all2(0.10603651f));
+    p = fma2(p, e, all2(-0.1530559f));
+    p = fma2(p, e, all2(0.19675939f));
+    p = fma2(p, e, all2(-0.24954134f));
+    p = fma2(p, e, all2(0.33329964f));
+    p = fma2(p, e, all2(-0.49999902f));
+    p = fma2(p, e, all2(1.f));
+    // not fmaxf, which drops a NaN
+    return fma2(p, e, make_float2(x.x < 0.f ? 0.f : x.x, x.y < 0.f ? 0.f : x.y));
+}
+__device__ __forceinline__ float4 softplus4(float4 x) {
+    const float2 a = softplus2(make_float2(x.x, x.y)), b = softplus2(make_float2(x.z, x.w));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ float logistic_f(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
+__device__ __forceinline__ float2 logistic2(float2 x) {
+    const float2 e = add2(ex2(mul2(x, all2(-kLog2e))), all2(1.f));
+    return make_float2(rcp(e.x), rcp(e.y));
+}
+// y silu(z)
+__device__ __forceinline__ float4 gated4(float4 y, float4 z) {
+    const float2 za = make_float2(z.x, z.y), zb = make_float2(z.z, z.w);
+    const float2 a = mul2(make_float2(y.x, y.y), mul2(za, logistic2(za))), b = mul2(make_float2(y.z, y.w), mul2(zb, logistic2(zb)));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+    const float2 x = add2(make_float2(a.x, a.y), make_float2(b.x, b.y)), y = add2(make_float2(a.z, a.w), make_float2(b.z, b.w));
+    return make_float4(x.x, x.y, y.x, y.y);
+}
 
 // A tile of adjacent channels of one group: `width` tiles a group, the last one with fewer channels.
 struct ChannelTile {
