@@ -2,19 +2,37 @@
 // and A = -exp(A_log),
 //     h_t = exp(dt_t A) h_{t-1} + dt_t u_t B_t,      y_t = (sum_n C_t h_t + skip u_t) silu(z_t).
 //
-// A warp holds 32 / L channels, L = N / 4 lanes a channel with four states each.  Per tile of K tokens a block forms dt
-// and dt u of its channels and B, C in fp32 in shared memory, walks the tile, and applies skip and gate to the sums.
+// Per tile of K tokens a block forms dt and dt u of its channels and B, C in fp32 in shared memory, walks the tile with the
+// states in registers, and applies skip and gate to the sums.
 #include <algorithm>
 
+#include "norm_rows.cuh"
 #include "scan_common.cuh"
 
 namespace gdn {
 namespace {
 
+// A lane holds two channels of four states each; the L lanes of a channel pair are 32 / L lanes apart (adjacent lanes then
+// read the same B and C, half the shared-memory cycles of L adjacent lanes with L addresses).
 template <int N>
 struct Shape {
-    static constexpr int L = N / 4, CH = kScanThreads / L;
+    static constexpr int L = N / 4, CH = 2 * kScanThreads / L, kPairs = 32 / L;
 };
+struct Lane {
+    int n4, pair, swap;   // first state, channel pair in the warp, whether the pair's channels are held in the other order
+    int ch[2];            // channels in the tile
+};
+template <int N>
+__device__ __forceinline__ Lane lane_of(int tid) {
+    constexpr int P = Shape<N>::kPairs;
+    Lane l;
+    l.pair = tid % P;
+    l.n4 = tid % 32 / P * 4;
+    l.swap = tid / P & 1;
+    l.ch[0] = tid / 32 * 2 * P + 2 * l.pair + l.swap;
+    l.ch[1] = l.ch[0] ^ 1;
+    return l;
+}
 
 // Per-thread shares of a tile of K tokens by CH channels among M threads: 4-channel vectors, and 4-state vectors of B and C.
 template <int N, int K, int M>
@@ -26,15 +44,23 @@ struct Rows {
     long long stride;
 };
 
-// Vectors of the tile's tensors as loaded; zeros past the end and where there is none.
-template <int K, int CH, int M, typename T, int V>
-__device__ __forceinline__ void load_rows(Raw4<T> (&x)[V], Rows src, int d0, long long t0, int tokens, int channels, int tid) {
+// Vectors of the tile's tensors as loaded, from the thread's first one on; zeros past the end and where there is none.
+template <typename T>
+struct Walk {
+    const T* p;       // the thread's first vector of the tile, or nullptr
+    int step;         // elements between its vectors
+};
+template <int CH, int M, typename T>
+__device__ __forceinline__ Walk<T> walk_of(Rows src, int d0, long long t0, int channels, int tid) {
+    const int k = tid / (CH / 4), c = tid % (CH / 4) * 4;
+    const T* p = static_cast<const T*>(src.p);
+    return {p && c < channels ? p + (t0 + k) * src.stride + d0 + c : nullptr, (int)src.stride * (M / (CH / 4))};
+}
+template <int CH, int M, typename T, int V>
+__device__ __forceinline__ void load_rows(Raw4<T> (&x)[V], const Walk<T>& w, int tokens, int tid) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int i = tid + v * M, k = i / (CH / 4), c = i % (CH / 4) * 4;
-        x[v] = k < tokens && c < channels && src.p ? load4(static_cast<const T*>(src.p) + (t0 + k) * src.stride + d0 + c)
-                                                   : Raw4<T>::zero();
-    }
+    for (int v = 0; v < V; ++v)
+        x[v] = w.p && tid / (CH / 4) + v * (M / (CH / 4)) < tokens ? load4(w.p + (size_t)v * w.step) : Raw4<T>::zero();
 }
 // B, then C (C.p may be nullptr), of group g.
 template <int K, int N, int M, typename T, int V>
@@ -74,11 +100,32 @@ __device__ __forceinline__ float4 column_values(const float* p, const ChannelTil
     return p && c < tile.n ? *reinterpret_cast<const float4*>(p + tile.d0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
+__device__ __forceinline__ void load_pairs(float2 (&x)[2], const float* p) {
+    const float4 f = *reinterpret_cast<const float4*>(p);
+    x[0] = make_float2(f.x, f.y);
+    x[1] = make_float2(f.z, f.w);
+}
+__device__ __forceinline__ void store_pairs(float* p, const float2 (&x)[2]) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+}
+template <int N>
+__device__ __forceinline__ void load_rates(float2 (&A2)[2][2], const ScanArgs& a, const ChannelTile& tile, const Lane& l) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        A2[s][0] = A2[s][1] = all2(0.f);
+        if (l.ch[s] < tile.n) {
+            load_pairs(A2[s], a.A_log + (size_t)(tile.d0 + l.ch[s]) * N + l.n4);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) A2[s][i] = make_float2(rate2(A2[s][i].x), rate2(A2[s][i].y));
+        }
+    }
+}
+
 // Each segment's own contribution to the state, from zero, and its sum of dt.  ADJ: also the contribution of its outputs
 // to the adjoint of the state before it, sum_t (a_first .. a_t) C_t p_t with p = dy silu(z).
 template <int N, typename T, bool ADJ>
 __global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_constant__ ScanArgs a) {
-    constexpr int L = Shape<N>::L, CH = Shape<N>::CH, K = N <= 16 ? 16 : 32, M = kScanThreads;
+    constexpr int CH = Shape<N>::CH, K = 16, M = kScanThreads;
     using S = Share<N, K, M>;
     __shared__ __align__(16) float2 s_dt[K][CH];
     __shared__ __align__(16) float s_p[ADJ ? K : 1][CH];
@@ -88,28 +135,32 @@ __global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_c
     Unit u;
     if (!unit_at(a.cu, a.T, a.nseq, a.seg, slot, false, u)) return;
     if (ADJ ? u.first && u.last : u.last) return;   // nothing reads it
-    const int tid = threadIdx.x, cl = tid / L, n4 = tid % L * 4, c4 = tid % (CH / 4) * 4;
-    const bool own = cl < tile.n;
-    const size_t at = (size_t)(tile.d0 + cl) * N + n4, DN = (size_t)a.D * N;
-    float2 A2[2], h[2], lam[2], E[2];
-    h[0] = h[1] = lam[0] = lam[1] = A2[0] = A2[1] = all2(0.f);
-    E[0] = E[1] = all2(1.f);
-    float sum_dt = 0.f;
-    if (own) {
-        const float4 l = *reinterpret_cast<const float4*>(a.A_log + at);
-        A2[0] = make_float2(rate2(l.x), rate2(l.y));
-        A2[1] = make_float2(rate2(l.z), rate2(l.w));
-    }
+    const int tid = threadIdx.x, c4 = tid % (CH / 4) * 4;
+    const Lane l = lane_of<N>(tid);
+    const size_t DN = (size_t)a.D * N;
+    float2 A2[2][2], h[2][2], lam[2][2], E[2][2];
+    float sum_dt[2] = {0.f, 0.f};
+    load_rates<N>(A2, a, tile, l);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            h[s][i] = lam[s][i] = all2(0.f);
+            E[s][i] = all2(1.f);
+        }
     const float4 bias = column_values(a.dt_bias, tile, c4);
     const Rows B{a.B, a.b_stride}, C{ADJ ? a.C : nullptr, a.c_stride};
     Raw4<T> ru[S::kVecs], rd[S::kVecs], rz[ADJ ? S::kVecs : 1], rg[ADJ ? S::kVecs : 1], rbc[S::kBC];
     auto load = [&](long long t0) {
         const int tokens = (int)min((long long)K, u.t1 - t0);
-        load_rows<K, CH, M>(ru, Rows{a.u, a.u_stride}, tile.d0, t0, tokens, tile.n, tid);
-        load_rows<K, CH, M>(rd, Rows{a.delta, a.delta_stride}, tile.d0, t0, tokens, tile.n, tid);
+        auto get = [&](auto& x, const void* p, long long stride) {
+            load_rows<CH, M>(x, walk_of<CH, M, T>(Rows{p, stride}, tile.d0, t0, tile.n, tid), tokens, tid);
+        };
+        get(ru, a.u, a.u_stride);
+        get(rd, a.delta, a.delta_stride);
         if constexpr (ADJ) {
-            load_rows<K, CH, M>(rz, Rows{a.z, a.z_stride}, tile.d0, t0, tokens, tile.n, tid);
-            load_rows<K, CH, M>(rg, Rows{a.gy, a.D}, tile.d0, t0, tokens, tile.n, tid);
+            get(rz, a.z, a.z_stride);
+            get(rg, a.gy, a.D);
         }
         load_bc<K, N, M>(rbc, B, C, tile.g, t0, tokens, tid);
     };
@@ -130,47 +181,53 @@ __global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_c
         if (t0 + K < u.t1) load(t0 + K);
 #pragma unroll 4
         for (int k = 0; k < K; ++k) {
-            const float2 dd = s_dt[k][cl];
-            const float4 b = *reinterpret_cast<const float4*>(&s_bc[0][k][n4]);
-            const float2 w[2] = {make_float2(b.x, b.y), make_float2(b.z, b.w)};
-            float2 c[2];
-            if constexpr (ADJ) {
-                const float4 x = *reinterpret_cast<const float4*>(&s_bc[1][k][n4]);
-                const float p = s_p[k][cl];
-                c[0] = mul2(make_float2(x.x, x.y), all2(p));
-                c[1] = mul2(make_float2(x.z, x.w), all2(p));
-            }
+            float2 B2[2], C2[2];
+            load_pairs(B2, &s_bc[0][k][l.n4]);
+            if constexpr (ADJ) load_pairs(C2, &s_bc[1][k][l.n4]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float2 e = decay(A2[i], dd.x);
-                h[i] = fma2(e, h[i], mul2(w[i], all2(dd.y)));
-                if constexpr (ADJ) {
-                    E[i] = mul2(E[i], e);
-                    lam[i] = fma2(E[i], c[i], lam[i]);
+            for (int s = 0; s < 2; ++s) {
+                const float2 dd = s_dt[k][l.ch[s]];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 e = decay(A2[s][i], dd.x);
+                    h[s][i] = fma2(e, h[s][i], mul2(B2[i], all2(dd.y)));
+                    if constexpr (ADJ) {
+                        E[s][i] = mul2(E[s][i], e);
+                        lam[s][i] = fma2(E[s][i], mul2(C2[i], all2(s_p[k][l.ch[s]])), lam[s][i]);
+                    }
                 }
+                sum_dt[s] += dd.x;
             }
-            sum_dt += dd.x;
         }
         __syncthreads();
     }
-    if (!own) return;
-    *reinterpret_cast<float4*>(a.states + (size_t)slot * DN + at) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
-    if constexpr (ADJ)
-        *reinterpret_cast<float4*>(a.adjoints + (size_t)slot * DN + at) = make_float4(lam[0].x, lam[0].y, lam[1].x, lam[1].y);
-    if (n4 == 0) a.sum_dt[(size_t)slot * a.D + tile.d0 + cl] = sum_dt;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        if (l.ch[s] >= tile.n) continue;
+        const size_t d = tile.d0 + l.ch[s];
+        store_pairs(a.states + (size_t)slot * DN + d * N + l.n4, h[s]);
+        if constexpr (ADJ) store_pairs(a.adjoints + (size_t)slot * DN + d * N + l.n4, lam[s]);
+        if (l.n4 == 0) a.sum_dt[(size_t)slot * a.D + d] = sum_dt[s];
+    }
 }
 
-// The outputs.  Four warps walk the states; two others form the next tile's dt, dt u, B and C in shared memory and finish
+// The outputs.  Four warps walk the states; eight others form the next tile's dt, dt u, B and C in shared memory and finish
 // the last one's outputs meanwhile (one barrier a tile), so that a sequence's walk waits for neither.
-constexpr int kHelpers = 64;
+constexpr int kHelpers = 256;
+template <int N>
+struct MainSmem {
+    static constexpr int K = N == 8 ? 16 : 32, CH = Shape<N>::CH;
+    static constexpr int kRow = CH + (N == 8 ? 0 : 256 / N);   // floats of a row of sums: no bank conflicts
+    float2 dt[2][K][CH];
+    float bc[2][2][K][N];
+    float y[2][K][kRow];
+};
 template <int N, typename T>
-__global__ void __launch_bounds__(kScanThreads + kHelpers) scan_main_kernel(const __grid_constant__ ScanArgs a) {
-    constexpr int L = Shape<N>::L, CH = Shape<N>::CH, K = N == 16 || N == 32 ? 32 : 16, M = kHelpers;
-    constexpr int kRow = CH + (32 / L > 4 ? 32 / L : 4);   // floats of a row of sums: no bank conflicts
+__global__ void __launch_bounds__(kScanThreads + kHelpers, 1) scan_main_kernel(const __grid_constant__ ScanArgs a) {
+    constexpr int L = Shape<N>::L, CH = Shape<N>::CH, P = Shape<N>::kPairs, K = MainSmem<N>::K, M = kHelpers;
     using S = Share<N, K, M>;
-    __shared__ __align__(16) float2 s_dt[2][K][CH];
-    __shared__ __align__(16) float s_bc[2][2][K][N];
-    __shared__ __align__(16) float s_y[2][K][kRow];
+    extern __shared__ __align__(16) uint8_t smem[];
+    MainSmem<N>& sm = *reinterpret_cast<MainSmem<N>*>(smem);
     const int tiles = a.G * ((a.D / a.G + CH - 1) / CH), slot = blockIdx.x / tiles;
     const ChannelTile tile = channel_tile(a.D, a.G, CH, blockIdx.x % tiles);
     Unit u;
@@ -184,33 +241,40 @@ __global__ void __launch_bounds__(kScanThreads + kHelpers) scan_main_kernel(cons
         Raw4<T> ru[S::kVecs], rd[S::kVecs], rz[S::kVecs], rbc[S::kBC];   // the next tile's
         Raw4<T> cu[S::kVecs], cz[S::kVecs], pu[S::kVecs], pz[S::kVecs];  // of the tile that is walked, of the last one
         auto tokens_of = [&](int i) { return (int)min((long long)K, u.t1 - u.t0 - (long long)i * K); };
-        auto load = [&](int i) {
-            const long long t0 = u.t0 + (long long)i * K;
+        Walk<T> wu = walk_of<CH, M, T>(Rows{a.u, a.u_stride}, tile.d0, u.t0, tile.n, tid);
+        Walk<T> wd = walk_of<CH, M, T>(Rows{a.delta, a.delta_stride}, tile.d0, u.t0, tile.n, tid);
+        Walk<T> wz = walk_of<CH, M, T>(Rows{a.z, a.z_stride}, tile.d0, u.t0, tile.n, tid);
+        T* out = static_cast<T*>(a.y) + (u.t0 + tid / (CH / 4)) * a.D + tile.d0 + c4;
+        auto load = [&](int i) {   // the tiles in order
             const int tokens = tokens_of(i);
-            load_rows<K, CH, M>(ru, Rows{a.u, a.u_stride}, tile.d0, t0, tokens, tile.n, tid);
-            load_rows<K, CH, M>(rd, Rows{a.delta, a.delta_stride}, tile.d0, t0, tokens, tile.n, tid);
-            load_rows<K, CH, M>(rz, Rows{a.z, a.z_stride}, tile.d0, t0, tokens, tile.n, tid);
-            load_bc<K, N, M>(rbc, B, C, tile.g, t0, tokens, tid);
+            load_rows<CH, M>(ru, wu, tokens, tid);
+            load_rows<CH, M>(rd, wd, tokens, tid);
+            load_rows<CH, M>(rz, wz, tokens, tid);
+            load_bc<K, N, M>(rbc, B, C, tile.g, u.t0 + (long long)i * K, tokens, tid);
+            auto next = [](Walk<T>& w, long long stride) { if (w.p) w.p += K * stride; };
+            next(wu, a.u_stride);
+            next(wd, a.delta_stride);
+            next(wz, a.z_stride);
         };
         auto form = [&](int i) {
-            form_dt<K, CH, M>(s_dt[i & 1], ru, rd, bias, tokens_of(i), tile.n, tid);
-            form_bc<K, N, M>(s_bc[i & 1], rbc, tid);
+            form_dt<K, CH, M>(sm.dt[i & 1], ru, rd, bias, tokens_of(i), tile.n, tid);
+            form_bc<K, N, M>(sm.bc[i & 1], rbc, tid);
         };
         auto finish = [&](int i, const Raw4<T> (&fu)[S::kVecs], const Raw4<T> (&fz)[S::kVecs]) {
-            const long long t0 = u.t0 + (long long)i * K;
-            const int tokens = tokens_of(i);
+            const int tokens = c4 < tile.n ? tokens_of(i) : 0;
 #pragma unroll
             for (int v = 0; v < S::kVecs; ++v) {
-                const int e = tid + v * M, k = e / (CH / 4);
-                if (k >= tokens || c4 >= tile.n) continue;
-                float4 y = *reinterpret_cast<const float4*>(&s_y[i & 1][k][c4]);
+                const int k = tid / (CH / 4) + v * (M / (CH / 4));
+                if (k >= tokens) break;
+                float4 y = *reinterpret_cast<const float4*>(&sm.y[i & 1][k][c4]);
                 const float4 x = fu[v].f();
                 const float2 ya = fma2(make_float2(skip.x, skip.y), make_float2(x.x, x.y), make_float2(y.x, y.y));
                 const float2 yb = fma2(make_float2(skip.z, skip.w), make_float2(x.z, x.w), make_float2(y.z, y.w));
                 y = make_float4(ya.x, ya.y, yb.x, yb.y);
                 if (a.z) y = gated4(y, fz[v].f());
-                store4(static_cast<T*>(a.y) + (t0 + k) * a.D + tile.d0 + c4, y);
+                store4(out + (size_t)v * (M / (CH / 4)) * a.D, y);
             }
+            out += (size_t)K * a.D;
         };
         auto keep = [&]() {
 #pragma unroll
@@ -237,50 +301,59 @@ __global__ void __launch_bounds__(kScanThreads + kHelpers) scan_main_kernel(cons
         }
         return;
     }
-    const int tid = threadIdx.x, lane = tid & 31, cl = tid / L, n4 = tid % L * 4;
-    const bool own = cl < tile.n;
-    const size_t at = (size_t)(tile.d0 + cl) * N + n4;
-    float2 A2[2], h[2];
-    h[0] = h[1] = A2[0] = A2[1] = all2(0.f);
-    if (own) {
-        const float4 l = *reinterpret_cast<const float4*>(a.A_log + at);
-        A2[0] = make_float2(rate2(l.x), rate2(l.y));
-        A2[1] = make_float2(rate2(l.z), rate2(l.w));
-        const float* from = a.seg ? a.states + (size_t)slot * DN : a.h0 ? a.h0 + (size_t)u.seq * DN : nullptr;
-        if (from) {
-            const float4 f = *reinterpret_cast<const float4*>(from + at);
-            h[0] = make_float2(f.x, f.y);
-            h[1] = make_float2(f.z, f.w);
-        }
+    const Lane l = lane_of<N>(threadIdx.x);
+    float2 A2[2][2], h[2][2];
+    load_rates<N>(A2, a, tile, l);
+    const float* from = a.seg ? a.states + (size_t)slot * DN : a.h0 ? a.h0 + (size_t)u.seq * DN : nullptr;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        h[s][0] = h[s][1] = all2(0.f);
+        if (from && l.ch[s] < tile.n) load_pairs(h[s], from + (size_t)(tile.d0 + l.ch[s]) * N + l.n4);
     }
     __syncthreads();
+    constexpr int TT = L / 2;              // tokens whose sums over the lanes are finished together
+    constexpr int U = 16;                  // tokens between which instructions can be moved: no store before a load
     for (int i = 0; i < n; ++i) {
-        const float2(*dt)[CH] = s_dt[i & 1];
-        const float(*bc)[K][N] = s_bc[i & 1];
-        constexpr int U = L < 8 ? 8 : L;   // tokens between whose results the instructions can be moved
+        const float2(*dt)[CH] = sm.dt[i & 1];
+        const float(*bc)[K][N] = sm.bc[i & 1];
 #pragma unroll 1
         for (int k0 = 0; k0 < K; k0 += U) {
+            float out[U / TT];
 #pragma unroll
-            for (int j = 0; j < U; j += L) {
-                float part[L];
+            for (int j = 0; j < U; j += TT) {
+                float sum[TT];
 #pragma unroll
-                for (int e = 0; e < L; ++e) {
+                for (int e = 0; e < TT; ++e) {
                     const int k = k0 + j + e;
-                    const float2 dd = dt[k][cl];
-                    const float4 b = *reinterpret_cast<const float4*>(&bc[0][k][n4]);
-                    const float4 c = *reinterpret_cast<const float4*>(&bc[1][k][n4]);
-                    h[0] = fma2(decay(A2[0], dd.x), h[0], mul2(make_float2(b.x, b.y), all2(dd.y)));
-                    h[1] = fma2(decay(A2[1], dd.x), h[1], mul2(make_float2(b.z, b.w), all2(dd.y)));
-                    const float2 y = fma2(h[1], make_float2(c.z, c.w), mul2(h[0], make_float2(c.x, c.y)));
-                    part[e] = y.x + y.y;
+                    float2 B2[2], C2[2];
+                    load_pairs(B2, &bc[0][k][l.n4]);
+                    load_pairs(C2, &bc[1][k][l.n4]);
+                    float part[2];
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const float2 dd = dt[k][l.ch[s]];
+                        float2 y;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            h[s][x] = fma2(decay(A2[s][x], dd.x), h[s][x], mul2(B2[x], all2(dd.y)));
+                            y = x == 0 ? mul2(h[s][x], C2[x]) : fma2(h[s][x], C2[x], y);
+                        }
+                        part[s] = y.x + y.y;
+                    }
+                    // the next lane of the pair holds the channels in the other order: each gets its first one's sum
+                    sum[e] = part[0] + __shfl_xor_sync(0xffffffffu, part[1], P);
                 }
-                s_y[i & 1][k0 + j + lane % L][cl] = transpose_sum<L>(part, lane);
+                out[j / TT] = transpose_sum<TT, 2 * P>(sum, threadIdx.x);
             }
+#pragma unroll
+            for (int j = 0; j < U; j += TT) sm.y[i & 1][k0 + j + threadIdx.x / (2 * P) % TT][l.ch[0]] = out[j / TT];
         }
         __syncthreads();
     }
-    if (own && a.h_final && u.last)
-        *reinterpret_cast<float4*>(a.h_final + (size_t)u.seq * DN + at) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+    if (a.h_final && u.last)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            if (l.ch[s] < tile.n) store_pairs(a.h_final + (size_t)u.seq * DN + (size_t)(tile.d0 + l.ch[s]) * N + l.n4, h[s]);
 }
 
 // The segments' contributions, in place: states to the state before each segment, adjoints (blockIdx.y 1) to the
@@ -377,7 +450,9 @@ cudaError_t fwd_typed(const ScanArgs& a) {
         const cudaError_t e = launch_scan_join(a, false);
         if (e != cudaSuccess) return e;
     }
-    scan_main_kernel<N, T><<<blocks, kScanThreads + kHelpers, 0, a.stream>>>(a);
+    const cudaError_t e = allow_smem<scan_main_kernel<N, T>>();
+    if (e != cudaSuccess) return e;
+    scan_main_kernel<N, T><<<blocks, kScanThreads + kHelpers, sizeof(MainSmem<N>), a.stream>>>(a);
     return cudaGetLastError();
 }
 template <int N, typename T>
@@ -413,10 +488,10 @@ cudaError_t step_n(const ScanStepArgs& a) { GDN_SCAN_N(step_typed, a) }
 // A sequence is walked by one block a channel tile where the tiles of all sequences fill the GPU, else in segments,
 // whose states are formed first.
 int scan_fwd_segment(long long tokens, int D, int N, int nseq, bool packed) {
-    const long long warps = (long long)D * N / 128 * (packed ? 1 : nseq);   // at work at once, in the worst case
-    if (warps >= 608) return 0;
+    const long long warps = (long long)D * N / 256 * (packed ? 1 : nseq);   // at work at once, in the worst case
+    if (warps >= 500) return 0;
     const long long want = 4 * 608;   // warps
-    const long long per = tokens * std::max(1LL, (long long)D * N / 128) / want;
+    const long long per = tokens * std::max(1LL, (long long)D * N / 256) / want;
     const long long seg = std::max(256LL, (per + 63) / 64 * 64);
     return tokens / (packed ? 1 : nseq) <= seg ? 0 : (int)std::min<long long>(seg, 1 << 20);
 }

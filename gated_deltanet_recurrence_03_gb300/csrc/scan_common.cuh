@@ -59,6 +59,12 @@ __device__ __forceinline__ float rate2(float A_log) {
     const float A = -kLog2e * expf(A_log);
     return A < -3e38f ? -3e38f : A;
 }
+// The larger one, or NaN (fmaxf drops it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
 // dt = softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) with the exponent's rounding put back, log1p(e) as e times a
 // polynomial (a least-maximum fit of log1p(e) / e on [0, 1], 5e-9 off; with its roundings 1.6e-7).
 __device__ __forceinline__ float2 softplus2(float2 x) {
@@ -77,8 +83,7 @@ __device__ __forceinline__ float2 softplus2(float2 x) {
     p = fma2(p, e, all2(0.33329964f));
     p = fma2(p, e, all2(-0.49999902f));
     p = fma2(p, e, all2(1.f));
-    // not fmaxf, which drops a NaN
-    return fma2(p, e, make_float2(x.x < 0.f ? 0.f : x.x, x.y < 0.f ? 0.f : x.y));
+    return fma2(p, e, make_float2(max_nan(x.x, 0.f), max_nan(x.y, 0.f)));
 }
 __device__ __forceinline__ float4 softplus4(float4 x) {
     const float2 a = softplus2(make_float2(x.x, x.y)), b = softplus2(make_float2(x.z, x.w));
