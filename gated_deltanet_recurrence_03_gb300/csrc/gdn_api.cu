@@ -1115,6 +1115,8 @@ gdn_status_t gdn_selective_scan_bwd(const void* u, long long u_stride, const voi
         a.states = reinterpret_cast<float*>(ws);
         a.adjoints = reinterpret_cast<float*>(ws + l.adjoints);
         a.sum_dt = reinterpret_cast<float*>(ws + l.sum_dt);
+        a.mids = reinterpret_cast<float*>(ws + l.mids);
+        a.mid_dt = reinterpret_cast<float*>(ws + l.mid_dt);
         a.part_A = reinterpret_cast<float*>(ws + l.part_A);
         a.part_s = reinterpret_cast<float*>(ws + l.part_s);
         a.part_bc = reinterpret_cast<float*>(ws + l.part_bc);

@@ -286,6 +286,8 @@ struct ScanArgs {
     float* states;
     float* adjoints;
     float* sum_dt;
+    float* mids;                // gradients: a segment's contribution to the state in its middle, and its sum of dt to there
+    float* mid_dt;
     // gradients
     const void* gy;             // [tokens][D]
     const float* gh;            // [nseq][D][N] or nullptr (zeros)
@@ -315,12 +317,11 @@ cudaError_t launch_scan_fwd(const ScanArgs& a);
 struct ScanBwdLayout {
     int seg;
     long long slots;
-    size_t adjoints, sum_dt, part_A, part_s, part_bc, total;
+    size_t adjoints, mids, sum_dt, mid_dt, part_A, part_s, part_bc, total;
 };
 ScanBwdLayout scan_bwd_layout(long long tokens, int D, int G, int N, int nseq, bool packed);
 cudaError_t launch_scan_bwd(const ScanArgs& a);
-// The state before each segment and the adjoint behind it.
-cudaError_t launch_scan_states(const ScanArgs& a);
+// The segments' contributions (states, adjoints where asked for) in place: the state before each, the adjoint behind it.
 cudaError_t launch_scan_join(const ScanArgs& a, bool adjoints);
 struct ScanStepArgs {
     const void* u;              // [rows][D] each

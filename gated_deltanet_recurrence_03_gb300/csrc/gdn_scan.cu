@@ -121,36 +121,31 @@ __device__ __forceinline__ void load_rates(float2 (&A2)[2][2], const ScanArgs& a
     }
 }
 
-// Each segment's own contribution to the state, from zero, and its sum of dt.  ADJ: also the contribution of its outputs
-// to the adjoint of the state before it, sum_t (a_first .. a_t) C_t p_t with p = dy silu(z).
-template <int N, typename T, bool ADJ>
+// Each segment's own contribution to the state, from zero, and its sum of dt.
+template <int N, typename T>
 __global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_constant__ ScanArgs a) {
     constexpr int CH = Shape<N>::CH, K = 16, M = kScanThreads;
     using S = Share<N, K, M>;
     __shared__ __align__(16) float2 s_dt[K][CH];
-    __shared__ __align__(16) float s_p[ADJ ? K : 1][CH];
     __shared__ __align__(16) float s_bc[2][K][N];
     const int tiles = a.G * ((a.D / a.G + CH - 1) / CH), slot = blockIdx.x / tiles;
     const ChannelTile tile = channel_tile(a.D, a.G, CH, blockIdx.x % tiles);
     Unit u;
     if (!unit_at(a.cu, a.T, a.nseq, a.seg, slot, false, u)) return;
-    if (ADJ ? u.first && u.last : u.last) return;   // nothing reads it
+    if (u.last) return;   // nothing reads it
     const int tid = threadIdx.x, c4 = tid % (CH / 4) * 4;
     const Lane l = lane_of<N>(tid);
     const size_t DN = (size_t)a.D * N;
-    float2 A2[2][2], h[2][2], lam[2][2], E[2][2];
+    float2 A2[2][2], h[2][2];
     float sum_dt[2] = {0.f, 0.f};
     load_rates<N>(A2, a, tile, l);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            h[s][i] = lam[s][i] = all2(0.f);
-            E[s][i] = all2(1.f);
-        }
+        for (int i = 0; i < 2; ++i) h[s][i] = all2(0.f);
     const float4 bias = column_values(a.dt_bias, tile, c4);
-    const Rows B{a.B, a.b_stride}, C{ADJ ? a.C : nullptr, a.c_stride};
-    Raw4<T> ru[S::kVecs], rd[S::kVecs], rz[ADJ ? S::kVecs : 1], rg[ADJ ? S::kVecs : 1], rbc[S::kBC];
+    const Rows B{a.B, a.b_stride}, C{nullptr, 0};
+    Raw4<T> ru[S::kVecs], rd[S::kVecs], rbc[S::kBC];
     auto load = [&](long long t0) {
         const int tokens = (int)min((long long)K, u.t1 - t0);
         auto get = [&](auto& x, const void* p, long long stride) {
@@ -158,10 +153,6 @@ __global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_c
         };
         get(ru, a.u, a.u_stride);
         get(rd, a.delta, a.delta_stride);
-        if constexpr (ADJ) {
-            get(rz, a.z, a.z_stride);
-            get(rg, a.gy, a.D);
-        }
         load_bc<K, N, M>(rbc, B, C, tile.g, t0, tokens, tid);
     };
     load(u.t0);
@@ -169,21 +160,12 @@ __global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_c
         const int tokens = (int)min((long long)K, u.t1 - t0);
         form_dt<K, CH, M>(s_dt, ru, rd, bias, tokens, tile.n, tid);
         form_bc<K, N, M>(s_bc, rbc, tid);
-        if constexpr (ADJ) {
-#pragma unroll
-            for (int v = 0; v < S::kVecs; ++v) {
-                const int i = tid + v * M, k = i / (CH / 4);
-                if (k >= K) break;
-                *reinterpret_cast<float4*>(&s_p[k][c4]) = a.z ? gated4(rg[v].f(), rz[v].f()) : rg[v].f();
-            }
-        }
         __syncthreads();
         if (t0 + K < u.t1) load(t0 + K);
 #pragma unroll 4
         for (int k = 0; k < K; ++k) {
-            float2 B2[2], C2[2];
+            float2 B2[2];
             load_pairs(B2, &s_bc[0][k][l.n4]);
-            if constexpr (ADJ) load_pairs(C2, &s_bc[1][k][l.n4]);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const float2 dd = s_dt[k][l.ch[s]];
@@ -191,10 +173,6 @@ __global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_c
                 for (int i = 0; i < 2; ++i) {
                     const float2 e = decay(A2[s][i], dd.x);
                     h[s][i] = fma2(e, h[s][i], mul2(B2[i], all2(dd.y)));
-                    if constexpr (ADJ) {
-                        E[s][i] = mul2(E[s][i], e);
-                        lam[s][i] = fma2(E[s][i], mul2(C2[i], all2(s_p[k][l.ch[s]])), lam[s][i]);
-                    }
                 }
                 sum_dt[s] += dd.x;
             }
@@ -206,7 +184,6 @@ __global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_c
         if (l.ch[s] >= tile.n) continue;
         const size_t d = tile.d0 + l.ch[s];
         store_pairs(a.states + (size_t)slot * DN + d * N + l.n4, h[s]);
-        if constexpr (ADJ) store_pairs(a.adjoints + (size_t)slot * DN + d * N + l.n4, lam[s]);
         if (l.n4 == 0) a.sum_dt[(size_t)slot * a.D + d] = sum_dt[s];
     }
 }
@@ -446,18 +423,13 @@ template <int N, typename T>
 cudaError_t fwd_typed(const ScanArgs& a) {
     const unsigned blocks = (unsigned)((long long)a.slots * tiles_of<N>(a));
     if (a.seg) {
-        scan_state_kernel<N, T, false><<<blocks, kScanThreads, 0, a.stream>>>(a);
+        scan_state_kernel<N, T><<<blocks, kScanThreads, 0, a.stream>>>(a);
         const cudaError_t e = launch_scan_join(a, false);
         if (e != cudaSuccess) return e;
     }
     const cudaError_t e = allow_smem<scan_main_kernel<N, T>>();
     if (e != cudaSuccess) return e;
     scan_main_kernel<N, T><<<blocks, kScanThreads + kHelpers, sizeof(MainSmem<N>), a.stream>>>(a);
-    return cudaGetLastError();
-}
-template <int N, typename T>
-cudaError_t adj_typed(const ScanArgs& a) {
-    scan_state_kernel<N, T, true><<<(unsigned)((long long)a.slots * tiles_of<N>(a)), kScanThreads, 0, a.stream>>>(a);
     return cudaGetLastError();
 }
 template <int N, typename T>
@@ -477,8 +449,6 @@ cudaError_t step_typed(const ScanStepArgs& a) {
     return cudaErrorInvalidValue;
 template <typename T>
 cudaError_t fwd_n(const ScanArgs& a) { GDN_SCAN_N(fwd_typed, a) }
-template <typename T>
-cudaError_t adj_n(const ScanArgs& a) { GDN_SCAN_N(adj_typed, a) }
 template <typename T>
 cudaError_t step_n(const ScanStepArgs& a) { GDN_SCAN_N(step_typed, a) }
 #undef GDN_SCAN_N
@@ -513,10 +483,6 @@ cudaError_t launch_scan_join(const ScanArgs& a, bool adjoints) {
 }
 cudaError_t launch_scan_fwd(const ScanArgs& a) {
     return a.dtype == GDN_BF16 ? fwd_n<__nv_bfloat16>(a) : fwd_n<float>(a);
-}
-cudaError_t launch_scan_states(const ScanArgs& a) {
-    const cudaError_t e = a.dtype == GDN_BF16 ? adj_n<__nv_bfloat16>(a) : adj_n<float>(a);
-    return e == cudaSuccess ? launch_scan_join(a, true) : e;
 }
 cudaError_t launch_scan_step(const ScanStepArgs& a) {
     return a.dtype == GDN_BF16 ? step_n<__nv_bfloat16>(a) : step_n<float>(a);

@@ -2,365 +2,572 @@
 //     lam_t = C_t p_t + a_{t+1} lam_{t+1},   dC = sum_d p h,   dB = sum_d lam dt u,   q = sum_n lam B,
 //     w = lam a h_{t-1},   r = sum_n A w,   dA = sum_t dt w,   du = dt q + skip p,   d(dt) = u q + r,
 //     d(delta) = d(dt) sigmoid(delta + bias),   dz = dy (sum_n C h + skip u) silu'(z)
-// (a h_{t-1} is kept rather than h_{t-1}, so that w needs no division and h = a h_{t-1} + dt u B).
+// (w from a lam, which is the next lam).
 //
-// Every segment of kSegment tokens is a block's work on its own, with the state before it and the adjoint behind it
-// formed first (launch_scan_states).  A block walks its segment forwards, keeping the state every K tokens in shared
-// memory, then the chunks of K tokens backwards: each is walked forwards again with a and a h_{t-1} in registers, then
-// backwards.  Sums over a group's channels (dB, dC) leave as one partial sum a tile, sums over tokens (dA_log, dskip,
-// dbias) as one a segment; the last kernels add them in order.
+// Every segment of kScanSegment tokens is a block's work on its own, with the state before it and the adjoint behind it
+// formed first (scan_ends_kernel and launch_scan_join).  A block walks half a segment forwards, keeping the state every K
+// tokens in shared memory, then the chunks of K tokens backwards: each is walked forwards again with its states in
+// registers, then backwards; then the other half.  Sums over a group's channels (dB, dC) leave as one partial sum a tile,
+// sums over tokens (dA_log, dskip, dbias) as one a segment; the last kernels add them in order.
 #include <algorithm>
 
 #include "norm_rows.cuh"
 #include "scan_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kChunk = 8;   // tokens whose a and a h_{t-1} a thread holds
+constexpr int kChunk = 8;                       // tokens whose states a thread holds
+constexpr int kHalf = kScanSegment / 2;
 
-// A lane has two channels of four states each: L lanes a channel pair.
+// A lane has two channels of SN states each; the L lanes of a channel pair are P lanes apart.
 template <int N>
 struct Shape {
-    static constexpr int L = N / 4, CH = 2 * kScanThreads / L, K = kChunk;
+    static constexpr int SN = 4, L = N / SN, P = 32 / L, CH = 2 * P * (kScanThreads / 32), K = kChunk;
     static constexpr int kRow = CH + 8;
-    static constexpr int kVecs = (K * CH / 4 + kScanThreads - 1) / kScanThreads;
-    static constexpr int kBC = (2 * K * N / 4 + kScanThreads - 1) / kScanThreads;
-    static constexpr int kSlots = 32 / L;   // channel pairs of a warp
+    static constexpr int Q = SN / 2, V = SN / 4;   // pairs and vectors of a lane's states of a channel
 };
-
+struct Lane {
+    int n0, pair, swap, turn;   // first state, channel pair in the warp, whether the pair's channels and (turn) the two
+                                // vectors of states are held in the other order: what a lane sends in the first exchange of
+                                // a sum is then in the same registers everywhere
+    int ch[2];                  // channels in the tile
+};
 template <int N>
-struct Smem {
-    float4 tok[kChunk][Shape<N>::CH];             // dt, dt u, p
-    float bc[2][4][kChunk][N];                    // B, C, the states of each four in the order of a lane: entry r is r ^ perm
-    float sums[3][kChunk][Shape<N>::kRow];        // y, q, r
-    float red[kScanThreads / 32][kChunk][2 * N];  // dB, dC of each warp
-    float4 state[kScanSegment / kChunk][2][kScanThreads];
+__device__ __forceinline__ Lane lane_of(int tid) {
+    using S = Shape<N>;
+    Lane l;
+    const int nl = tid % 32 / S::P;
+    l.pair = tid % S::P;
+    l.n0 = nl * S::SN;
+    l.swap = nl & 1;
+    l.turn = S::SN == 8 ? l.pair / (S::P / 2) : 0;
+    l.ch[0] = tid / 32 * 2 * S::P + 2 * l.pair + l.swap;
+    l.ch[1] = l.ch[0] ^ 1;
+    return l;
+}
+// A lane's SN states at p (of its channel, or of B, C).
+template <int N>
+__device__ __forceinline__ void load_states(float2 (&x)[Shape<N>::Q], const float* p, const Lane& l) {
+#pragma unroll
+    for (int v = 0; v < Shape<N>::V; ++v) {
+        const float4 f = *reinterpret_cast<const float4*>(p + l.n0 + 4 * (v ^ l.turn));
+        x[2 * v] = make_float2(f.x, f.y);
+        x[2 * v + 1] = make_float2(f.z, f.w);
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_states(float* p, const float2 (&x)[Shape<N>::Q], const Lane& l) {
+#pragma unroll
+    for (int v = 0; v < Shape<N>::V; ++v)
+        *reinterpret_cast<float4*>(p + l.n0 + 4 * (v ^ l.turn)) =
+            make_float4(x[2 * v].x, x[2 * v].y, x[2 * v + 1].x, x[2 * v + 1].y);
+}
+template <int N>
+__device__ __forceinline__ void load_rates(float2 (&A2)[2][Shape<N>::Q], const ScanArgs& a, const ChannelTile& tile, const Lane& l) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const bool own = l.ch[s] < tile.n;
+        if (own) load_states<N>(A2[s], a.A_log + (size_t)(tile.d0 + l.ch[s]) * N, l);
+#pragma unroll
+        for (int i = 0; i < Shape<N>::Q; ++i) A2[s][i] = own ? make_float2(rate2(A2[s][i].x), rate2(A2[s][i].y)) : all2(0.f);
+    }
+}
+
+// A thread's vectors of four channels: column c4, rows k0, k0 + kStep, ...
+template <int N>
+struct Own {
+    static constexpr int kCols = Shape<N>::CH / 4, kStep = kScanThreads / kCols;
+    int c4, k0;
+    __device__ __forceinline__ explicit Own(int tid) : c4(tid % kCols * 4), k0(tid / kCols) {}
 };
 
+__device__ __forceinline__ float4 columns(const float* p, const ChannelTile& tile, int c) {
+    return p && c < tile.n ? *reinterpret_cast<const float4*>(p + tile.d0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// ---------------------------------------------------------------- the segments' ends
+// Each segment's contribution to the state behind it, from zero, and to the adjoint before it, sum_t (a_first .. a_t) C_t
+// p_t; its sum of dt, and the same of its first half for the state in its middle.
 template <int N, typename T>
-struct Tile {
-    Raw4<T> u[Shape<N>::kVecs], d[Shape<N>::kVecs], z[Shape<N>::kVecs], gy[Shape<N>::kVecs];
-    Raw4<T> bc[Shape<N>::kBC];
+__global__ void __launch_bounds__(kScanThreads) scan_ends_kernel(const __grid_constant__ ScanArgs a) {
+    using S = Shape<N>;
+    using O = Own<N>;
+    constexpr int CH = S::CH, K = 16, VEC = (K * CH / 4 + kScanThreads - 1) / kScanThreads, BC = (2 * K * N / 4 + kScanThreads - 1) / kScanThreads;
+    static_assert(kHalf % K == 0, "halves are whole tiles");
+    __shared__ __align__(16) float2 s_dt[K][CH];
+    __shared__ __align__(16) float s_p[K][CH];
+    __shared__ __align__(16) float s_bc[2][K][N];
+    const int tiles = a.G * ((a.D / a.G + CH - 1) / CH), slot = blockIdx.x / tiles;
+    const ChannelTile tile = channel_tile(a.D, a.G, CH, blockIdx.x % tiles);
+    Unit u;
+    if (!unit_at(a.cu, a.T, a.nseq, a.seg, slot, false, u)) return;
+    if (u.first && u.last && u.t1 - u.t0 <= kHalf) return;   // nothing reads it
+    const int tid = threadIdx.x, len = (int)(u.t1 - u.t0);
+    const Lane l = lane_of<N>(tid);
+    const O own(tid);
+    const size_t DN = (size_t)a.D * N;
+    float2 A2[2][S::Q], h[2][S::Q], lam[2][S::Q], E[2][S::Q];
+    float sum_dt[2] = {0.f, 0.f};
+    load_rates<N>(A2, a, tile, l);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < S::Q; ++i) {
+            h[s][i] = lam[s][i] = all2(0.f);
+            E[s][i] = all2(1.f);
+        }
+    const float4 bias = columns(a.dt_bias, tile, own.c4);
+    const bool some = own.c4 < tile.n;
+    // the thread's first vector of the next tile, and elements between its rows
+    auto first = [&](const void* p, long long stride) {
+        return static_cast<const T*>(p) + (u.t0 + own.k0) * stride + tile.d0 + own.c4;
+    };
+    const T *pu = first(a.u, a.u_stride), *pd = first(a.delta, a.delta_stride), *pg = first(a.gy, a.D),
+            *pz = a.z ? first(a.z, a.z_stride) : nullptr;
+    Raw4<T> ru[VEC], rd[VEC], rz[VEC], rg[VEC], rbc[BC];
+    auto load = [&](int t) {   // the tiles in order
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const bool ok = some && t + own.k0 + v * O::kStep < len && own.k0 + v * O::kStep < K;
+            const long long row = v * O::kStep;
+            ru[v] = ok ? load4(pu + row * a.u_stride) : Raw4<T>::zero();
+            rd[v] = ok ? load4(pd + row * a.delta_stride) : Raw4<T>::zero();
+            rg[v] = ok ? load4(pg + row * a.D) : Raw4<T>::zero();
+            if (pz) rz[v] = ok ? load4(pz + row * a.z_stride) : Raw4<T>::zero();
+        }
+        pu += K * a.u_stride;
+        pd += K * a.delta_stride;
+        pg += (long long)K * a.D;
+        if (pz) pz += K * a.z_stride;
+#pragma unroll
+        for (int v = 0; v < BC; ++v) {
+            const int i = tid + v * kScanThreads, which = i / (K * N / 4), k = i / (N / 4) % K, n = i % (N / 4) * 4;
+            const T* p = static_cast<const T*>(which == 0 ? a.B : a.C) + (size_t)tile.g * N + n;
+            rbc[v] = which < 2 && t + k < len ? load4(p + (u.t0 + t + k) * (which == 0 ? a.b_stride : a.c_stride)) : Raw4<T>::zero();
+        }
+    };
+    load(0);
+    for (int t = 0; t < len; t += K) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const int k = own.k0 + v * O::kStep;
+            if (k >= K) break;
+            const float4 x = ru[v].f();
+            float4 d = softplus4(add4(rd[v].f(), bias));
+            if (!some || t + k >= len) d = make_float4(0.f, 0.f, 0.f, 0.f);   // past the end: nothing changes
+            float4* p = reinterpret_cast<float4*>(&s_dt[k][own.c4]);
+            p[0] = make_float4(d.x, d.x * x.x, d.y, d.y * x.y);
+            p[1] = make_float4(d.z, d.z * x.z, d.w, d.w * x.w);
+            *reinterpret_cast<float4*>(&s_p[k][own.c4]) = pz ? gated4(rg[v].f(), rz[v].f()) : rg[v].f();
+        }
+#pragma unroll
+        for (int v = 0; v < BC; ++v) {
+            const int i = tid + v * kScanThreads, which = i / (K * N / 4), k = i / (N / 4) % K, n = i % (N / 4) * 4;
+            if (which < 2) *reinterpret_cast<float4*>(&s_bc[which][k][n]) = rbc[v].f();
+        }
+        __syncthreads();
+        if (t + K < len) load(t + K);
+        if (t == kHalf)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (l.ch[s] >= tile.n) continue;
+                const size_t d = tile.d0 + l.ch[s];
+                store_states<N>(a.mids + (size_t)slot * DN + d * N, h[s], l);
+                if (l.n0 == 0) a.mid_dt[(size_t)slot * a.D + d] = sum_dt[s];
+            }
+#pragma unroll 4
+        for (int k = 0; k < K; ++k) {
+            float2 B[S::Q], C[S::Q];
+            load_states<N>(B, s_bc[0][k], l);
+            load_states<N>(C, s_bc[1][k], l);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const float2 dd = s_dt[k][l.ch[s]];
+                const float p = s_p[k][l.ch[s]];
+#pragma unroll
+                for (int i = 0; i < S::Q; ++i) {
+                    const float2 e = decay(A2[s][i], dd.x);
+                    h[s][i] = fma2(e, h[s][i], mul2(B[i], all2(dd.y)));
+                    E[s][i] = mul2(E[s][i], e);
+                    lam[s][i] = fma2(E[s][i], mul2(C[i], all2(p)), lam[s][i]);
+                }
+                sum_dt[s] += dd.x;
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        if (l.ch[s] >= tile.n) continue;
+        const size_t d = tile.d0 + l.ch[s];
+        store_states<N>(a.states + (size_t)slot * DN + d * N, h[s], l);
+        store_states<N>(a.adjoints + (size_t)slot * DN + d * N, lam[s], l);
+        if (l.n0 == 0) a.sum_dt[(size_t)slot * a.D + d] = sum_dt[s];
+    }
+}
+
+// ---------------------------------------------------------------- the gradients
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool ok, float) {   // four values; zeros without
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool ok, __nv_bfloat16) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(ok ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_done() {
+    asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
+}
+
+// A stage holds the raw values of a chunk: K tokens of u, delta, z, dy, B and C, or (walking forwards) 2 K tokens of u,
+// delta and B.  A thread reads back only what it copied itself.
+template <int N, typename T>
+struct Smem {
+    using S = Shape<N>;
+    float2 dt[2 * kChunk][S::CH];                     // dt, dt u; backwards the second half holds p
+    float bc[2][kChunk][N];                           // B, C, or B of 2 K tokens
+    float sums[3][kChunk][S::kRow];                   // y, q, r
+    float red[kScanThreads / 32][kChunk][2 * N];      // dB, dC of each warp
+    float4 state[kHalf / kChunk][2 * S::V][kScanThreads];
+    T rows[2][4 * kChunk][S::CH];
+    T bc_rows[2][2 * kChunk][N];
 };
-
-// FULL: all of a chunk; else what the states need.
-template <int N, typename T, bool FULL>
-__device__ __forceinline__ void load_tile(Tile<N, T>& t, const ScanArgs& a, const ChannelTile& tile, long long t0, int tokens) {
-    using S = Shape<N>;
-    const int tid = threadIdx.x;
-#pragma unroll
-    for (int v = 0; v < S::kVecs; ++v) {
-        const int i = tid + v * kScanThreads, k = i / (S::CH / 4), c = i % (S::CH / 4) * 4;
-        const bool ok = k < tokens && c < tile.n;
-        const size_t row = t0 + k, d = tile.d0 + c;
-        auto get = [&](const void* p, long long stride) {
-            return ok && p ? load4(static_cast<const T*>(p) + row * stride + d) : Raw4<T>::zero();
-        };
-        t.u[v] = get(a.u, a.u_stride);
-        t.d[v] = get(a.delta, a.delta_stride);
-        if (FULL) {
-            t.z[v] = get(a.z, a.z_stride);
-            t.gy[v] = get(a.gy, a.D);
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < S::kBC; ++v) {
-        const int i = tid + v * kScanThreads, which = i / (S::K * N / 4), k = i / (N / 4) % S::K, n = i % (N / 4) * 4;
-        const bool ok = which < (FULL ? 2 : 1) && k < tokens;
-        const T* p = static_cast<const T*>(which == 0 ? a.B : a.C) + (size_t)tile.g * N + n;
-        t.bc[v] = ok ? load4(p + (t0 + k) * (which == 0 ? a.b_stride : a.c_stride)) : Raw4<T>::zero();
-    }
-}
-
-// A tile's values in fp32 in shared memory.
-template <int N, typename T, bool FULL>
-__device__ __forceinline__ void form_tile(const Tile<N, T>& t, Smem<N>& sm, const ScanArgs& a, int channels, int tokens,
-                                          float4 bias) {
-    using S = Shape<N>;
-    const int tid = threadIdx.x;
-#pragma unroll
-    for (int v = 0; v < S::kVecs; ++v) {
-        const int i = tid + v * kScanThreads, k = i / (S::CH / 4), c = i % (S::CH / 4) * 4;
-        if (k >= S::K) break;
-        const float4 x = t.u[v].f(), d = t.d[v].f();
-        const bool ok = k < tokens && c < channels;
-        const float4 sp = softplus4(add4(d, bias));
-        float dt[4] = {sp.x, sp.y, sp.z, sp.w}, p[4] = {0.f, 0.f, 0.f, 0.f};
-        const float uu[4] = {x.x, x.y, x.z, x.w};
-        if (FULL) {
-            float4 g = t.gy[v].f();
-            if (a.z) g = gated4(g, t.z[v].f());
-            p[0] = g.x; p[1] = g.y; p[2] = g.z; p[3] = g.w;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            dt[e] = ok ? dt[e] : 0.f;   // dt = 0: a token past the end changes nothing
-            sm.tok[k][c + e] = make_float4(dt[e], dt[e] * uu[e], p[e], 0.f);
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < S::kBC; ++v) {
-        const int i = tid + v * kScanThreads, which = i / (S::K * N / 4), k = i / (N / 4) % S::K, n = i % (N / 4) * 4;
-        if (which >= 2) continue;
-        const float4 b = t.bc[v].f();
-        *reinterpret_cast<float4*>(&sm.bc[which][0][k][n]) = b;
-        *reinterpret_cast<float4*>(&sm.bc[which][1][k][n]) = make_float4(b.y, b.x, b.w, b.z);
-        *reinterpret_cast<float4*>(&sm.bc[which][2][k][n]) = make_float4(b.z, b.w, b.x, b.y);
-        *reinterpret_cast<float4*>(&sm.bc[which][3][k][n]) = make_float4(b.w, b.z, b.y, b.x);
-    }
-}
-
-// Entry r of a lane's four states is state r ^ perm.
-__device__ __forceinline__ float4 permuted(float4 x, int perm) {
-    if (perm & 1) x = make_float4(x.y, x.x, x.w, x.z);
-    if (perm & 2) x = make_float4(x.z, x.w, x.x, x.y);
-    return x;
-}
-
-// Four values a lane, entry r belonging to state r ^ perm: their sums over the warp's channel pairs, so that a lane ends
-// with entry 0 (and, with two channel pairs a warp, 1).  The lanes that are exchanged with hold the other entries first,
-// so no value has to be selected.
-template <int N>
-__device__ __forceinline__ void channel_sum(float (&v)[4]) {
-    constexpr int L = N / 4, kSlots = 32 / L;
-    v[0] += __shfl_xor_sync(0xffffffffu, v[2], L);
-    v[1] += __shfl_xor_sync(0xffffffffu, v[3], L);
-    if (kSlots >= 4) v[0] += __shfl_xor_sync(0xffffffffu, v[1], 2 * L);
-#pragma unroll
-    for (int o = 4 * L; o < 32; o *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-}
 
 template <int N, typename T>
 __global__ void __launch_bounds__(kScanThreads, 2) scan_bwd_kernel(const __grid_constant__ ScanArgs a) {
     using S = Shape<N>;
-    constexpr int L = S::L, CH = S::CH, K = S::K, TT = L / 2;   // TT: tokens whose sums over states are finished together
+    using O = Own<N>;
+    constexpr int L = S::L, P = S::P, CH = S::CH, K = S::K, Q = S::Q, V = S::V;
+    constexpr int TT = L < 4 ? 1 : 2;   // tokens whose sums over the lanes are finished together
+    constexpr int VEC = (K * CH / 4 + kScanThreads - 1) / kScanThreads, BC = (2 * K * N / 4 + kScanThreads - 1) / kScanThreads;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    Smem<N>& sm = *reinterpret_cast<Smem<N>*>(smem_raw);
+    Smem<N, T>& sm = *reinterpret_cast<Smem<N, T>*>(smem_raw);
+    float(*const s_p)[CH] = reinterpret_cast<float(*)[CH]>(sm.dt[K]);
+    float(*const s_b2)[N] = sm.bc[0];
     const int tiles = a.G * ((a.D / a.G + CH - 1) / CH), slot = blockIdx.x / tiles, tile_id = blockIdx.x % tiles;
     const ChannelTile tile = channel_tile(a.D, a.G, CH, tile_id);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n4 = lane % L * 4, pair = lane / L, swap = lane & 1;
-    const int perm = ((pair & 1) ? 2 : 0) | ((S::kSlots >= 4 && (pair & 2)) ? 1 : 0);
-    const int c4 = tid % (CH / 4) * 4;
-    // the lane's channels: the lanes of a pair hold them in the other order, as the states' entries
-    int ch[2];
-    ch[0] = warp * 2 * S::kSlots + pair * 2 + swap;
-    ch[1] = ch[0] ^ 1;
+    const Lane l = lane_of<N>(tid);
+    const O own(tid);
+    const bool some = own.c4 < tile.n;
     const size_t DN = (size_t)a.D * N;
-    size_t at[2];
-    bool own[2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        own[s] = ch[s] < tile.n;
-        at[s] = (size_t)(tile.d0 + ch[s]) * N + n4;
-    }
-    float* const part_A = a.part_A + (size_t)slot * DN;
-    float* const part_s = a.part_s + (size_t)slot * 2 * a.D + tile.d0;
     Unit u;
     if (!unit_at(a.cu, a.T, a.nseq, a.seg, slot, false, u)) u.t0 = u.t1 = 0, u.first = false;
-    const long long len = u.t1 - u.t0;
-    const int chunks = (int)((len + K - 1) / K);
-
-    float2 A2[2][2], h[2][2], lam[2][2], gA[2][2];
-    auto take = [&](const float* p, int s, float2 (&x)[2]) {
-        const float4 f = p && own[s] ? permuted(*reinterpret_cast<const float4*>(p + at[s]), perm) : make_float4(0.f, 0.f, 0.f, 0.f);
-        x[0] = make_float2(f.x, f.y);
-        x[1] = make_float2(f.z, f.w);
+    const int len = (int)(u.t1 - u.t0);
+    float* const part_A = a.part_A + (size_t)slot * DN;
+    float* const part_s = a.part_s + (size_t)slot * 2 * a.D + tile.d0;
+    auto channel = [&](int s) { return (size_t)(tile.d0 + l.ch[s]); };
+    auto take = [&](const float* p, int s, float2 (&x)[Q]) {   // zeros where there is none
+#pragma unroll
+        for (int i = 0; i < Q; ++i) x[i] = all2(0.f);
+        if (p && l.ch[s] < tile.n) load_states<N>(x, p + channel(s) * N, l);
     };
+    auto put = [&](float* p, int s, const float2 (&x)[Q]) {
+        if (l.ch[s] < tile.n) store_states<N>(p + channel(s) * N, x, l);
+    };
+
+    float2 A2[2][Q], lam[2][Q], gA[2][Q];
+    load_rates<N>(A2, a, tile, l);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        take(a.A_log, s, A2[s]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            A2[s][i] = own[s] ? make_float2(rate2(A2[s][i].x), rate2(A2[s][i].y)) : all2(0.f);
-            gA[s][i] = all2(0.f);
+        for (int i = 0; i < Q; ++i) gA[s][i] = all2(0.f);
+        take(len == 0 ? nullptr : a.seg ? a.adjoints + (size_t)slot * DN : a.gh ? a.gh + (size_t)u.seq * DN : nullptr, s, lam[s]);
+    }
+    const float4 bias = columns(a.dt_bias, tile, own.c4), skip = columns(a.skip, tile, own.c4);
+    float4 g_skip = make_float4(0.f, 0.f, 0.f, 0.f), g_bias = g_skip;
+
+    // asks for rows r .. r + rows - 1 of the segment into a stage; row k of tensor x goes to rows[x K + k]
+    auto ask_rows = [&](int st, int x, const void* p, long long stride, int t, int rows) {
+        const T* from = static_cast<const T*>(p) + (u.t0 + t + own.k0) * stride + tile.d0 + own.c4;
+        for (int k = own.k0; k < rows; k += O::kStep, from += O::kStep * stride) {
+            const bool ok = some && t + k < len;
+            copy_async(tc::smem_u32(&sm.rows[st][x * K + k][own.c4]), ok ? from : static_cast<const T*>(p), ok, T{});
         }
-        const bool some = len > 0;   // not an empty slot, whose sequence is none
-        take(!some ? nullptr : a.seg ? a.states + (size_t)slot * DN : a.h0 ? a.h0 + (size_t)u.seq * DN : nullptr, s, h[s]);
-        take(!some ? nullptr : a.seg ? a.adjoints + (size_t)slot * DN : a.gh ? a.gh + (size_t)u.seq * DN : nullptr, s, lam[s]);
-    }
-    float4 bias = make_float4(0.f, 0.f, 0.f, 0.f), skip = bias, g_skip = bias, g_bias = bias;
-    if (c4 < tile.n) {
-        if (a.dt_bias) bias = *reinterpret_cast<const float4*>(a.dt_bias + tile.d0 + c4);
-        if (a.skip) skip = *reinterpret_cast<const float4*>(a.skip + tile.d0 + c4);
-    }
-    auto put = [&](float* p, int s, const float2 (&x)[2]) {
-        if (own[s]) *reinterpret_cast<float4*>(p + at[s]) = permuted(make_float4(x[0].x, x[0].y, x[1].x, x[1].y), perm);
+    };
+    auto ask_bc = [&](int st, int t, bool both) {
+#pragma unroll
+        for (int v = 0; v < BC; ++v) {
+            const int i = tid + v * kScanThreads, k = i / (N / 4), n = i % (N / 4) * 4;
+            if (k >= 2 * K) break;
+            const bool c = both && k >= K;
+            const int tk = t + (c ? k - K : k);
+            const T* p = static_cast<const T*>(c ? a.C : a.B) + (size_t)tile.g * N + n;
+            const bool ok = tk < len;
+            copy_async(tc::smem_u32(&sm.bc_rows[st][k][n]), ok ? p + (u.t0 + tk) * (c ? a.c_stride : a.b_stride) : p, ok, T{});
+        }
+    };
+    auto form_bc = [&](int st) {
+#pragma unroll
+        for (int v = 0; v < BC; ++v) {
+            const int i = tid + v * kScanThreads, k = i / (N / 4), n = i % (N / 4) * 4;
+            if (k >= 2 * K) break;
+            *reinterpret_cast<float4*>(&s_b2[k][n]) = load4(&sm.bc_rows[st][k][n]).f();
+        }
+    };
+    auto form_dt = [&](int k, float4 x, float4 delta, bool ok) {
+        float4 d = softplus4(add4(delta, bias));
+        if (!ok) d = make_float4(0.f, 0.f, 0.f, 0.f);   // past the end: nothing changes
+        float4* p = reinterpret_cast<float4*>(&sm.dt[k][own.c4]);
+        p[0] = make_float4(d.x, d.x * x.x, d.y, d.y * x.y);
+        p[1] = make_float4(d.z, d.z * x.z, d.w, d.w * x.w);
+    };
+    auto ask_walk = [&](int st, int t) {
+        ask_rows(st, 0, a.u, a.u_stride, t, 2 * K);
+        ask_rows(st, 2, a.delta, a.delta_stride, t, 2 * K);
+        ask_bc(st, t, false);
+    };
+    auto ask_chunk = [&](int st, int t) {
+        ask_rows(st, 0, a.u, a.u_stride, t, K);
+        ask_rows(st, 1, a.delta, a.delta_stride, t, K);
+        if (a.z) ask_rows(st, 2, a.z, a.z_stride, t, K);
+        ask_rows(st, 3, a.gy, a.D, t, K);
+        ask_bc(st, t, true);
     };
 
-    // forwards: the state before each chunk
-    Tile<N, T> raw;
-    auto tokens_of = [&](int c) { return (int)min((long long)K, len - (long long)c * K); };
-    if (chunks > 1) load_tile<N, T, false>(raw, a, tile, u.t0, K);
-    for (int c = 0; c < chunks; ++c) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) sm.state[c][s][tid] = make_float4(h[s][0].x, h[s][0].y, h[s][1].x, h[s][1].y);
-        if (c + 1 == chunks) break;
-        __syncthreads();
-        form_tile<N, T, false>(raw, sm, a, tile.n, K, bias);
-        __syncthreads();
-        if (c + 2 < chunks) load_tile<N, T, false>(raw, a, tile, u.t0 + (c + 1) * K, K);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const float4 b = *reinterpret_cast<const float4*>(&sm.bc[0][perm][k][n4]);
-            const float2 B[2] = {make_float2(b.x, b.y), make_float2(b.z, b.w)};
+    for (int half = len > kHalf ? 1 : 0; half >= 0 && len > 0; --half) {
+        const int h0 = half * kHalf, n = min(len - h0, kHalf), chunks = (n + K - 1) / K;
+        // forwards: the state before each chunk
+        {
+            float2 h[2][Q];
+            if (chunks > 1) ask_walk(0, h0);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const float2 dd = *reinterpret_cast<const float2*>(&sm.tok[k][ch[s]]);
+                take(a.seg ? a.states + (size_t)slot * DN : a.h0 ? a.h0 + (size_t)u.seq * DN : nullptr, s, h[s]);
+                if (half) {
+                    float2 m[Q];
+                    take(a.mids + (size_t)slot * DN, s, m);
+                    const float dt = l.ch[s] < tile.n ? a.mid_dt[(size_t)slot * a.D + channel(s)] : 0.f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    h[s][i] = fma2(decay(A2[s][i], dd.x), h[s][i], mul2(B[i], all2(dd.y)));
+                    for (int i = 0; i < Q; ++i) h[s][i] = fma2(decay(A2[s][i], dt), h[s][i], m[i]);
                 }
             }
-        }
-    }
-
-    if (chunks > 0) load_tile<N, T, true>(raw, a, tile, u.t0 + (long long)(chunks - 1) * K, tokens_of(chunks - 1));
-    for (int c = chunks - 1; c >= 0; --c) {
-        const long long t0 = u.t0 + (long long)c * K;
-        const int tokens = tokens_of(c);
-        __syncthreads();
-        form_tile<N, T, true>(raw, sm, a, tile.n, tokens, bias);
-        const Tile<N, T> cur = raw;
-        __syncthreads();
-        if (c > 0) load_tile<N, T, true>(raw, a, tile, t0 - K, K);
-        float2 aa[K][2][2], P[K][2][2];   // a and a h_{t-1}
+            auto keep = [&](int c) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const float4 f = sm.state[c][s][tid];
-            h[s][0] = make_float2(f.x, f.y);
-            h[s][1] = make_float2(f.z, f.w);
-        }
+                for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const float4 b = *reinterpret_cast<const float4*>(&sm.bc[0][perm][k][n4]);
-            const float2 B[2] = {make_float2(b.x, b.y), make_float2(b.z, b.w)};
+                    for (int v = 0; v < V; ++v)
+                        sm.state[c][s * V + v][tid] = make_float4(h[s][2 * v].x, h[s][2 * v].y, h[s][2 * v + 1].x, h[s][2 * v + 1].y);
+            };
+            for (int c = 0; c < chunks; c += 2) {
+                const int st = c / 2 & 1;
+                keep(c);
+                if (c + 1 == chunks) break;
+                copies_done();
+                __syncthreads();   // the last tile has been walked
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const float2 dd = *reinterpret_cast<const float2*>(&sm.tok[k][ch[s]]);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    aa[k][s][i] = decay(A2[s][i], dd.x);
-                    P[k][s][i] = mul2(aa[k][s][i], h[s][i]);
-                    h[s][i] = fma2(B[i], all2(dd.y), P[k][s][i]);
+                for (int v = 0; v < 2 * VEC; ++v) {
+                    const int k = own.k0 + v * O::kStep;
+                    if (k >= 2 * K) break;
+                    form_dt(k, load4(&sm.rows[st][k][own.c4]).f(), load4(&sm.rows[st][2 * K + k][own.c4]).f(),
+                            some && c * K + k < n);
                 }
+                form_bc(st);
+                __syncthreads();
+                if (c + 3 < chunks) ask_walk(st ^ 1, h0 + (c + 2) * K);
+                const int two = c + 2 < chunks ? 2 : 1;   // the last chunk's own steps come again backwards
+                for (int x = 0; x < two; ++x) {
+                    if (x) keep(c + 1);
+#pragma unroll
+                    for (int k0 = 0; k0 < K; ++k0) {
+                        const int k = x * K + k0;
+                        float2 B[Q];
+                        load_states<N>(B, s_b2[k], l);
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            const float2 dd = sm.dt[k][l.ch[s]];
+#pragma unroll
+                            for (int i = 0; i < Q; ++i) h[s][i] = fma2(decay(A2[s][i], dd.x), h[s][i], mul2(B[i], all2(dd.y)));
+                        }
+                    }
+                }
+                if (two == 1) keep(c + 1);
             }
         }
+        __syncthreads();
+        ask_chunk(0, h0 + (chunks - 1) * K);
+        for (int c = chunks - 1; c >= 0; --c) {
+            const int t = h0 + c * K, tokens = min(K, len - t), st = (chunks - 1 - c) & 1;
+            copies_done();
 #pragma unroll
-        for (int kk = K - TT; kk >= 0; kk -= TT) {
+            for (int v = 0; v < VEC; ++v) {
+                const int k = own.k0 + v * O::kStep;
+                if (k >= K) break;
+                form_dt(k, load4(&sm.rows[st][k][own.c4]).f(), load4(&sm.rows[st][K + k][own.c4]).f(), some && k < tokens);
+                const float4 g = load4(&sm.rows[st][3 * K + k][own.c4]).f();
+                *reinterpret_cast<float4*>(&s_p[k][own.c4]) = a.z ? gated4(g, load4(&sm.rows[st][2 * K + k][own.c4]).f()) : g;
+            }
+            form_bc(st);
+            __syncthreads();
+            if (c > 0) ask_chunk(st ^ 1, t - K);
+            float2 hs[K][2][Q], before[2][Q];
+            auto start = [&](float2 (&x)[2][Q]) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float4 f = sm.state[c][s * V + v][tid];
+                        x[s][2 * v] = make_float2(f.x, f.y);
+                        x[s][2 * v + 1] = make_float2(f.z, f.w);
+                    }
+            };
+            start(before);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float2 B[Q];
+                load_states<N>(B, sm.bc[0][k], l);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const float2 dd = sm.dt[k][l.ch[s]];
+#pragma unroll
+                    for (int i = 0; i < Q; ++i)
+                        hs[k][s][i] = fma2(decay(A2[s][i], dd.x), k ? hs[k ? k - 1 : 0][s][i] : before[s][i], mul2(B[i], all2(dd.y)));
+                }
+            }
+            start(before);   // read again rather than held
             float sum[3][TT];   // y, q, r of the lane's first channel
 #pragma unroll
-            for (int e = TT - 1; e >= 0; --e) {
-                const int k = kk + e;
-                const float4 b = *reinterpret_cast<const float4*>(&sm.bc[0][perm][k][n4]);
-                const float4 cc = *reinterpret_cast<const float4*>(&sm.bc[1][perm][k][n4]);
-                const float2 B[2] = {make_float2(b.x, b.y), make_float2(b.z, b.w)};
-                const float2 C[2] = {make_float2(cc.x, cc.y), make_float2(cc.z, cc.w)};
-                float2 gB[2], gC[2];
+            for (int k = K - 1; k >= 0; --k) {
+                float2 B[Q], C[Q], gB[Q], gC[Q];
+                load_states<N>(B, sm.bc[0][k], l);
+                load_states<N>(C, sm.bc[1][k], l);
                 float part[3][2];
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    const float4 dd = sm.tok[k][ch[s]];   // dt, dt u, p
+                    const float2 dd = sm.dt[k][l.ch[s]];
+                    const float p = s_p[k][l.ch[s]];
                     float2 y, q, r;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        lam[s][i] = fma2(C[i], all2(dd.z), lam[s][i]);
-                        const float2 hh = fma2(B[i], all2(dd.y), P[k][s][i]), w = mul2(lam[s][i], P[k][s][i]);
-                        gC[i] = s == 0 ? mul2(hh, all2(dd.z)) : fma2(hh, all2(dd.z), gC[i]);
+                    for (int i = 0; i < Q; ++i) {
+                        const float2 hh = hs[k][s][i], prev = k ? hs[k ? k - 1 : 0][s][i] : before[s][i];
+                        lam[s][i] = fma2(C[i], all2(p), lam[s][i]);
+                        gC[i] = s == 0 ? mul2(hh, all2(p)) : fma2(hh, all2(p), gC[i]);
                         gB[i] = s == 0 ? mul2(lam[s][i], all2(dd.y)) : fma2(lam[s][i], all2(dd.y), gB[i]);
                         y = i == 0 ? mul2(hh, C[i]) : fma2(hh, C[i], y);
                         q = i == 0 ? mul2(lam[s][i], B[i]) : fma2(lam[s][i], B[i], q);
+                        lam[s][i] = mul2(lam[s][i], decay(A2[s][i], dd.x));
+                        const float2 w = mul2(lam[s][i], prev);
                         r = i == 0 ? mul2(w, A2[s][i]) : fma2(w, A2[s][i], r);
                         gA[s][i] = fma2(w, all2(dd.x), gA[s][i]);
-                        lam[s][i] = mul2(lam[s][i], aa[k][s][i]);
                     }
                     part[0][s] = y.x + y.y;
                     part[1][s] = q.x + q.y;
                     part[2][s] = r.x + r.y;
                 }
+                // the next lane of the pair holds the channels in the other order: each gets its first one's sums
 #pragma unroll
-                for (int x = 0; x < 3; ++x) sum[x][e] = part[x][0] + __shfl_xor_sync(0xffffffffu, part[x][1], 1);
-                float vB[4] = {gB[0].x, gB[0].y, gB[1].x, gB[1].y}, vC[4] = {gC[0].x, gC[0].y, gC[1].x, gC[1].y};
-                channel_sum<N>(vB);
-                channel_sum<N>(vC);
-                float* to = &sm.red[warp][k][n4 + perm];
-                if (S::kSlots >= 4) {
-                    if (pair == (perm & 1 ? 2 : 0) + (perm & 2 ? 1 : 0)) {   // one of the lanes that have the sums
-                        to[0] = vB[0];
-                        to[N] = vC[0];
+                for (int x = 0; x < 3; ++x) sum[x][k % TT] = part[x][0] + __shfl_xor_sync(0xffffffffu, part[x][1], P);
+                if (k % TT == 0)
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) {
+                        float s = transpose_sum<TT, 2 * P>(sum[x], lane);
+#pragma unroll
+                        for (int o = 2 * P * TT; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+                        sm.sums[x][k + lane / (2 * P) % TT][l.ch[0]] = s;
                     }
-                } else {
-                    to[0] = vB[0];
-                    to[N] = vC[0];
-                    sm.red[warp][k][n4 + (perm ^ 1)] = vB[1];
-                    sm.red[warp][k][n4 + (perm ^ 1) + N] = vC[1];
+                // sums over the pairs of the warp: the turned lanes' other vectors first, then values 2 j (dB) and 2 j + 1
+                // (dC) of four states
+                constexpr int P2 = S::SN == 8 ? P / 2 : P, R = 8 / (P2 < 8 ? P2 : 8);
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 b = gB[j / 2], g = gC[j / 2];
+                    v[2 * j] = j & 1 ? b.y : b.x;
+                    v[2 * j + 1] = j & 1 ? g.y : g.x;
+                    if (S::SN == 8) {
+                        const float2 b2 = gB[(Q - 2) + j / 2], g2 = gC[(Q - 2) + j / 2];
+                        v[2 * j] += __shfl_xor_sync(0xffffffffu, j & 1 ? b2.y : b2.x, P / 2);
+                        v[2 * j + 1] += __shfl_xor_sync(0xffffffffu, j & 1 ? g2.y : g2.x, P / 2);
+                    }
+                }
+#pragma unroll
+                for (int w = 8, x = 1; x < P2 && w > 1; w /= 2, x *= 2) {
+                    const bool up = lane & x;
+#pragma unroll
+                    for (int i = 0; i < w / 2; ++i) {
+                        const float mine = up ? v[2 * i + 1] : v[2 * i], theirs = up ? v[2 * i] : v[2 * i + 1];
+                        v[i] = mine + __shfl_xor_sync(0xffffffffu, theirs, x);
+                    }
+                }
+#pragma unroll
+                for (int x = 8; x < P2; x *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], x);
+                if (P2 <= 8 || l.pair < 8) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const int i = r * (8 / R) + l.pair % (8 / R);
+                        sm.red[warp][k][(i & 1) * N + l.n0 + 4 * l.turn + i / 2] = v[r];
+                    }
                 }
             }
+            __syncthreads();
+            if (some)
 #pragma unroll
-            for (int x = 0; x < 3; ++x) sm.sums[x][kk + (lane >> 1) % TT][ch[0]] = transpose_sum<TT, 2>(sum[x], lane);
+                for (int v = 0; v < VEC; ++v) {
+                    const int k = own.k0 + v * O::kStep;
+                    if (k >= tokens) break;
+                    const long long row = u.t0 + t + k;
+                    const size_t d = tile.d0 + own.c4;
+                    auto raw = [&](int x) { return load4(&sm.rows[st][x * K + k][own.c4]).f(); };
+                    auto f4 = [&](const float* p) { return *reinterpret_cast<const float4*>(p); };
+                    const float4 x4 = raw(0), d4 = add4(raw(1), bias), g4 = raw(3), p4 = f4(&s_p[k][own.c4]);
+                    const float4 y4 = f4(&sm.sums[0][k][own.c4]), q4 = f4(&sm.sums[1][k][own.c4]), r4 = f4(&sm.sums[2][k][own.c4]);
+                    const float4 ta = f4(&sm.dt[k][own.c4].x), tb = f4(&sm.dt[k][own.c4 + 2].x);
+                    float4 gu4, gd4, gs4, gz4 = make_float4(0.f, 0.f, 0.f, 0.f), z4 = gz4;
+                    if (a.z) z4 = raw(2);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        auto pick = [&](float4 f) { return e == 0 ? make_float2(f.x, f.y) : make_float2(f.z, f.w); };
+                        const float2 x = pick(x4), g = pick(g4), p = pick(p4), q = pick(q4), sk = pick(skip);
+                        const float2 dt = e == 0 ? make_float2(ta.x, ta.z) : make_float2(tb.x, tb.z);
+                        const float2 gu = fma2(dt, q, mul2(sk, p));
+                        const float2 gd = mul2(fma2(x, q, mul2(pick(r4), all2(kLn2))), logistic2(pick(d4)));
+                        const float2 gs = mul2(p, x);
+                        float2 gz = all2(0.f);
+                        if (a.z) {
+                            const float2 z = pick(z4), sg = logistic2(z), full = fma2(sk, x, pick(y4));
+                            // silu'(z) = s (1 + z (1 - s))
+                            gz = mul2(mul2(g, full), mul2(sg, fma2(z, fma2(sg, all2(-1.f), all2(1.f)), all2(1.f))));
+                        }
+                        if (e == 0) {
+                            gu4.x = gu.x; gu4.y = gu.y; gd4.x = gd.x; gd4.y = gd.y; gz4.x = gz.x; gz4.y = gz.y; gs4.x = gs.x; gs4.y = gs.y;
+                        } else {
+                            gu4.z = gu.x; gu4.w = gu.y; gd4.z = gd.x; gd4.w = gd.y; gz4.z = gz.x; gz4.w = gz.y; gs4.z = gs.x; gs4.w = gs.y;
+                        }
+                    }
+                    store4(static_cast<T*>(a.gu) + row * a.D + d, gu4);
+                    store4(static_cast<T*>(a.gdelta) + row * a.D + d, gd4);
+                    if (a.z) store4(static_cast<T*>(a.gz) + row * a.gz_stride + d, gz4);
+                    g_skip = add4(g_skip, gs4);
+                    g_bias = add4(g_bias, gd4);
+                }
+            for (int i = tid; i < tokens * N / 2; i += kScanThreads) {
+                const int k = i / (N / 2), n = i % (N / 2) * 4;
+                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kScanThreads / 32; ++w) s = add4(s, *reinterpret_cast<const float4*>(&sm.red[w][k][n]));
+                *reinterpret_cast<float4*>(a.part_bc + ((size_t)tile_id * a.tokens + u.t0 + t + k) * 2 * N + n) = s;
+            }
         }
         __syncthreads();
-#pragma unroll
-        for (int v = 0; v < S::kVecs; ++v) {
-            const int i = tid + v * kScanThreads, k = i / (CH / 4);
-            if (k >= tokens || c4 >= tile.n) continue;
-            const size_t row = t0 + k, d = tile.d0 + c4;
-            const float4 x4 = cur.u[v].f(), d4 = cur.d[v].f(), g4 = cur.gy[v].f(), z4 = cur.z[v].f();
-            const float uu[4] = {x4.x, x4.y, x4.z, x4.w}, raw_d[4] = {d4.x + bias.x, d4.y + bias.y, d4.z + bias.z, d4.w + bias.w};
-            const float gg[4] = {g4.x, g4.y, g4.z, g4.w}, zz[4] = {z4.x, z4.y, z4.z, z4.w};
-            const float sk[4] = {skip.x, skip.y, skip.z, skip.w};
-            float gu[4], gd[4], gz[4], gs[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float4 tk = sm.tok[k][c4 + e];
-                const float y = sm.sums[0][k][c4 + e], q = sm.sums[1][k][c4 + e], r = sm.sums[2][k][c4 + e] * kLn2;
-                gu[e] = fmaf(tk.x, q, sk[e] * tk.z);
-                gd[e] = fmaf(uu[e], q, r) * logistic_f(raw_d[e]);
-                gs[e] = tk.z * uu[e];
-                const float sg = logistic_f(zz[e]);
-                gz[e] = gg[e] * fmaf(sk[e], uu[e], y) * sg * fmaf(zz[e], 1.f - sg, 1.f);
-            }
-            store4(static_cast<T*>(a.gu) + row * a.D + d, make_float4(gu[0], gu[1], gu[2], gu[3]));
-            store4(static_cast<T*>(a.gdelta) + row * a.D + d, make_float4(gd[0], gd[1], gd[2], gd[3]));
-            if (a.z) store4(static_cast<T*>(a.gz) + row * a.gz_stride + d, make_float4(gz[0], gz[1], gz[2], gz[3]));
-            g_skip.x += gs[0]; g_skip.y += gs[1]; g_skip.z += gs[2]; g_skip.w += gs[3];
-            g_bias.x += gd[0]; g_bias.y += gd[1]; g_bias.z += gd[2]; g_bias.w += gd[3];
-        }
-        for (int i = tid; i < tokens * 2 * N; i += kScanThreads) {
-            const int k = i / (2 * N), n = i % (2 * N);
-            float s = 0.f;
-#pragma unroll
-            for (int w = 0; w < kScanThreads / 32; ++w) s += sm.red[w][k][n];
-            a.part_bc[((size_t)tile_id * a.tokens + t0 + k) * 2 * N + n] = s;
-        }
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         put(part_A, s, gA[s]);
-        if (a.gh0 && u.first && len > 0) put(a.gh0 + (size_t)u.seq * DN, s, lam[s]);
+        if (!a.gh0 || !u.first) continue;
+        // an empty sequence's initial state is its final one
+        if (len == 0) take(a.gh ? a.gh + (size_t)u.seq * DN : nullptr, s, lam[s]);
+        put(a.gh0 + (size_t)u.seq * DN, s, lam[s]);
     }
-    // an empty sequence's initial state is its final one
-    if (a.gh0 && u.first && len == 0)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            float2 x[2];
-            take(a.gh ? a.gh + (size_t)u.seq * DN : nullptr, s, x);
-            put(a.gh0 + (size_t)u.seq * DN, s, x);
-        }
     // the threads with the same channels, in order
-    __syncthreads();
     float4* const fold = reinterpret_cast<float4*>(smem_raw);
+    __syncthreads();
     fold[2 * tid] = g_skip;
     fold[2 * tid + 1] = g_bias;
     __syncthreads();
-    for (int i = tid; i < 2 * (CH / 4); i += kScanThreads) {
+    for (int i = tid; i < 2 * O::kCols; i += kScanThreads) {
         const int c = i >> 1;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int x = c; x < kScanThreads; x += CH / 4) {
-            const float4 y = fold[2 * x + (i & 1)];
-            s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
-        }
+        for (int x = c; x < kScanThreads; x += O::kCols) s = add4(s, fold[2 * x + (i & 1)]);
         if (c * 4 < tile.n) *reinterpret_cast<float4*>(part_s + (i & 1) * a.D + c * 4) = s;
     }
 }
@@ -381,41 +588,38 @@ __global__ void __launch_bounds__(256) scan_bc_sums_kernel(const __grid_constant
     const float* p = a.part_bc + ((size_t)g * tiles_per_group * a.tokens + t) * 2 * a.N + n;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int x = 0; x < tiles_per_group; ++x) {
-        const float4 y = *reinterpret_cast<const float4*>(p + (size_t)x * a.tokens * 2 * a.N);
-        s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
-    }
+    for (int x = 0; x < tiles_per_group; ++x) s = add4(s, *reinterpret_cast<const float4*>(p + (size_t)x * a.tokens * 2 * a.N));
     const bool is_c = n >= a.N;
     T* to = static_cast<T*>(is_c ? a.gC : a.gB) + t * (is_c ? a.gc_stride : a.gb_stride);
     store4(to + (size_t)g * a.N + (is_c ? n - a.N : n), s);
 }
 
-// dA_log = sum over the segments of A dA, dskip, dbias: 32 columns a block of the slots' rows of D N + 2 D sums.
-__global__ void __launch_bounds__(1024) scan_weight_sums_kernel(const __grid_constant__ ScanArgs a) {
-    __shared__ float red[32][33];
-    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
-    const size_t DN = (size_t)a.D * a.N, c = (size_t)blockIdx.x * 32 + lane;
+// dA_log = A sum dA, dskip, dbias over the segments: vectors of four columns of the slots' rows of D N + 2 D sums, eight
+// threads a vector.
+constexpr int kSumCols = 32, kSumRows = 8;
+__global__ void __launch_bounds__(kSumCols * kSumRows) scan_weight_sums_kernel(const __grid_constant__ ScanArgs a) {
+    __shared__ float4 red[kSumRows][kSumCols];
+    const int x = threadIdx.x % kSumCols, y = threadIdx.x / kSumCols;
+    const size_t DN = (size_t)a.D * a.N, c = ((size_t)blockIdx.x * kSumCols + x) * 4;
     const bool rate = c < DN, any = c < DN + 2 * a.D;
     const float* p = rate ? a.part_A + c : a.part_s + (c - DN);
     const size_t row = rate ? DN : 2 * (size_t)a.D;
-    float s = 0.f;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (any)
-        for (int r = grp; r < a.slots; r += 32) s += p[r * row];
-    red[grp][lane] = s;
+#pragma unroll 4
+        for (int r = y; r < a.slots; r += kSumRows) s = add4(s, *reinterpret_cast<const float4*>(p + r * row));
+    red[y][x] = s;
     __syncthreads();
+    if (y != 0 || !any) return;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        if (grp < o) red[grp][lane] += red[grp + o][lane];
-        __syncthreads();
-    }
-    if (grp != 0 || !any) return;
-    s = red[0][lane];
+    for (int r = 1; r < kSumRows; ++r) s = add4(s, red[r][x]);
     if (rate) {
-        if (a.gA) a.gA[c] = -expf(a.A_log[c]) * s;
-    } else if (c < DN + a.D) {
-        if (a.gskip) a.gskip[c - DN] = s;
-    } else if (a.gbias) {
-        a.gbias[c - DN - a.D] = s;
+        if (!a.gA) return;
+        const float4 l = *reinterpret_cast<const float4*>(a.A_log + c);
+        *reinterpret_cast<float4*>(a.gA + c) = make_float4(-expf(l.x) * s.x, -expf(l.y) * s.y, -expf(l.z) * s.z, -expf(l.w) * s.w);
+    } else {
+        float* to = c < DN + a.D ? a.gskip : a.gbias;
+        if (to) *reinterpret_cast<float4*>(to + (c < DN + a.D ? c - DN : c - DN - a.D)) = s;
     }
 }
 
@@ -425,13 +629,18 @@ cudaError_t bwd_typed(const ScanArgs& a) {
     cudaError_t e = allow_smem<scan_bwd_kernel<N, T>>();
     if (e != cudaSuccess) return e;
     const int per_group = (a.D / a.G + S::CH - 1) / S::CH;
-    scan_bwd_kernel<N, T><<<(unsigned)((long long)a.slots * a.G * per_group), kScanThreads, sizeof(Smem<N>), a.stream>>>(a);
+    const unsigned blocks = (unsigned)((long long)a.slots * a.G * per_group);
+    if (a.seg) {
+        scan_ends_kernel<N, T><<<blocks, kScanThreads, 0, a.stream>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_scan_join(a, true)) != cudaSuccess) return e;
+    }
+    scan_bwd_kernel<N, T><<<blocks, kScanThreads, sizeof(Smem<N, T>), a.stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long long vecs = (long long)a.tokens * a.G * N / 2;
     scan_bc_sums_kernel<T><<<(unsigned)((vecs + 255) / 256), 256, 0, a.stream>>>(a, per_group);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const size_t cols = (size_t)a.D * N + 2 * a.D;
-    scan_weight_sums_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, a.stream>>>(a);
+    scan_weight_sums_kernel<<<(unsigned)((cols / 4 + kSumCols - 1) / kSumCols), kSumCols * kSumRows, 0, a.stream>>>(a);
     return cudaGetLastError();
 }
 template <typename T>
@@ -449,14 +658,17 @@ cudaError_t bwd_n(const ScanArgs& a) {
 
 ScanBwdLayout scan_bwd_layout(long long tokens, int D, int G, int N, int nseq, bool packed) {
     ScanBwdLayout l{};
-    // one segment a sequence: nothing to join
-    l.seg = !packed && tokens / nseq <= kScanSegment ? 0 : kScanSegment;
+    // half a segment a sequence at most: nothing to join
+    l.seg = !packed && tokens / nseq <= kHalf ? 0 : kScanSegment;
     l.slots = l.seg ? tokens / kScanSegment + nseq : nseq;
     const size_t states = ((size_t)l.slots * D * N * 4 + 255) / 256 * 256, rows = ((size_t)l.slots * D * 4 + 255) / 256 * 256;
-    const int ch = 2 * kScanThreads / (N / 4), tiles = G * ((D / G + ch - 1) / ch);
+    const int ch = N == 8 ? Shape<8>::CH : N == 16 ? Shape<16>::CH : N == 32 ? Shape<32>::CH : Shape<64>::CH;
+    const int tiles = G * ((D / G + ch - 1) / ch);
     l.adjoints = l.seg ? states : 0;   // the states come first
-    l.sum_dt = 2 * l.adjoints;
-    l.part_A = l.sum_dt + (l.seg ? rows : 0);
+    l.mids = 2 * l.adjoints;
+    l.sum_dt = 3 * l.adjoints;
+    l.mid_dt = l.sum_dt + (l.seg ? rows : 0);
+    l.part_A = l.mid_dt + (l.seg ? rows : 0);
     l.part_s = l.part_A + states;
     l.part_bc = l.part_s + 2 * rows;
     l.total = l.part_bc + (size_t)tiles * tokens * 2 * N * 4;
@@ -464,10 +676,6 @@ ScanBwdLayout scan_bwd_layout(long long tokens, int D, int G, int N, int nseq, b
 }
 
 cudaError_t launch_scan_bwd(const ScanArgs& a) {
-    if (a.seg) {
-        const cudaError_t e = launch_scan_states(a);
-        if (e != cudaSuccess) return e;
-    }
     return a.dtype == GDN_BF16 ? bwd_n<__nv_bfloat16>(a) : bwd_n<float>(a);
 }
 
