@@ -963,7 +963,7 @@ gdn_status_t scan_sequences(int B, int T, int D, int G, int N, const gdn_opts_t&
     if (tokens > INT32_MAX) return fail(GDN_ERR_INVALID_ARG, "more than 2^31 - 1 tokens");
     *nseq = o.cu_seqlens ? o.num_seqs : B;
     // tiles of at least 8 channels of a group and vectors of four states, for each sequence and segment
-    const long long slots = *nseq + tokens / kScanSegment, tiles = std::max((long long)D / 8, (long long)D * N / 512 + 1);
+    const long long slots = *nseq + tokens / kScanMinSegment, tiles = std::max((long long)D / 8, (long long)D * N / 512 + 1);
     if (slots > kMaxBlocks / tiles) return fail(GDN_ERR_INVALID_ARG, "%lld tokens in %d sequences of %d channels are too many", tokens, *nseq, D);
     if (tokens * ((long long)G * N / 2) / 256 >= kMaxBlocks) return fail(GDN_ERR_INVALID_ARG, "%lld tokens of %d groups are too many", tokens, G);
     return GDN_OK;
@@ -1059,7 +1059,7 @@ size_t gdn_selective_scan_bwd_workspace_size(int B, int T, int D, int G, int N, 
     const gdn_opts_t o = resolve(opts);
     const int nseq = o.cu_seqlens ? o.num_seqs : B;
     if (B <= 0 || T <= 0 || nseq <= 0 || !scan_dims_ok(D, G, N)) return 0;
-    return scan_bwd_layout((long long)B * T, D, G, N, nseq, o.cu_seqlens != nullptr).total;
+    return scan_bwd_layout((long long)B * T, D, G, N, nseq).total;
 }
 
 gdn_status_t gdn_selective_scan_bwd(const void* u, long long u_stride, const void* delta, long long delta_stride,
@@ -1086,7 +1086,7 @@ gdn_status_t gdn_selective_scan_bwd(const void* u, long long u_stride, const voi
     if ((st = need_aligned16({u, delta, A_log, Bm, Cm, skip, dt_bias, z, h0, grad_y, grad_h_final, grad_u, grad_delta,
                               grad_A_log, grad_B, grad_C, grad_skip, grad_dt_bias, grad_z, grad_h0})) != GDN_OK)
         return st;
-    const ScanBwdLayout l = tokens > 0 ? scan_bwd_layout(tokens, D, G, N, nseq, o.cu_seqlens != nullptr) : ScanBwdLayout{};
+    const ScanBwdLayout l = tokens > 0 ? scan_bwd_layout(tokens, D, G, N, nseq) : ScanBwdLayout{};
     if ((st = need_workspace(o, l.total)) != GDN_OK) return st;
     if (nseq == 0 && !grad_A_log && !grad_skip && !grad_dt_bias) return GDN_OK;
     unsigned* status = nullptr;
@@ -1115,8 +1115,8 @@ gdn_status_t gdn_selective_scan_bwd(const void* u, long long u_stride, const voi
         a.states = reinterpret_cast<float*>(ws);
         a.adjoints = reinterpret_cast<float*>(ws + l.adjoints);
         a.sum_dt = reinterpret_cast<float*>(ws + l.sum_dt);
-        a.mids = reinterpret_cast<float*>(ws + l.mids);
-        a.mid_dt = reinterpret_cast<float*>(ws + l.mid_dt);
+        a.chunks = reinterpret_cast<float*>(ws + l.chunks);
+        a.chunk_dt = reinterpret_cast<float*>(ws + l.chunk_dt);
         a.part_A = reinterpret_cast<float*>(ws + l.part_A);
         a.part_s = reinterpret_cast<float*>(ws + l.part_s);
         a.part_bc = reinterpret_cast<float*>(ws + l.part_bc);

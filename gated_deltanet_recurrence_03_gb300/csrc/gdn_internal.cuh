@@ -286,8 +286,8 @@ struct ScanArgs {
     float* states;
     float* adjoints;
     float* sum_dt;
-    float* mids;                // gradients: a segment's contribution to the state in its middle, and its sum of dt to there
-    float* mid_dt;
+    float* chunks;              // gradients: a segment's contributions to the states before its chunks, [slots][seg / kScanChunk][D][N],
+    float* chunk_dt;            // and its sums of dt to there, [slots][seg / kScanChunk][D]
     // gradients
     const void* gy;             // [tokens][D]
     const float* gh;            // [nseq][D][N] or nullptr (zeros)
@@ -306,7 +306,8 @@ struct ScanArgs {
     float* part_bc;             // [channel tile][tokens][2 N]: sums over a tile's channels
     cudaStream_t stream;
 };
-constexpr int kScanSegment = 128;   // tokens of a segment of the gradients
+constexpr int kScanChunk = 8;         // tokens that the gradients walk at a time
+constexpr int kScanMinSegment = 64;   // tokens of their segments: a multiple of this
 struct ScanFwdLayout {
     int seg;
     long long slots;
@@ -317,9 +318,9 @@ cudaError_t launch_scan_fwd(const ScanArgs& a);
 struct ScanBwdLayout {
     int seg;
     long long slots;
-    size_t adjoints, mids, sum_dt, mid_dt, part_A, part_s, part_bc, total;
+    size_t adjoints, sum_dt, chunks, chunk_dt, part_A, part_s, part_bc, total;
 };
-ScanBwdLayout scan_bwd_layout(long long tokens, int D, int G, int N, int nseq, bool packed);
+ScanBwdLayout scan_bwd_layout(long long tokens, int D, int G, int N, int nseq);
 cudaError_t launch_scan_bwd(const ScanArgs& a);
 // The segments' contributions (states, adjoints where asked for) in place: the state before each, the adjoint behind it.
 cudaError_t launch_scan_join(const ScanArgs& a, bool adjoints);

@@ -4,11 +4,12 @@
 //     d(delta) = d(dt) sigmoid(delta + bias),   dz = dy (sum_n C h + skip u) silu'(z)
 // (w from a lam, which is the next lam).
 //
-// Every segment of kScanSegment tokens is a block's work on its own, with the state before it and the adjoint behind it
-// formed first (scan_ends_kernel and launch_scan_join).  A block walks half a segment forwards, keeping the state every K
-// tokens in shared memory, then the chunks of K tokens backwards: each is walked forwards again with its states in
-// registers, then backwards; then the other half.  Sums over a group's channels (dB, dC) leave as one partial sum a tile,
-// sums over tokens (dA_log, dskip, dbias) as one a segment; the last kernels add them in order.
+// Every segment of tokens is a block's work on its own.  A first kernel walks it forwards from zero and leaves the state
+// every K tokens, and what the segment adds to the state behind it and to the adjoint before it; launch_scan_join makes
+// those the state before each segment and the adjoint behind it.  Then a block takes its segment's chunks of K tokens from
+// the last to the first: each is walked forwards with its states in registers, then backwards.  Sums over a group's channels
+// (dB, dC) leave as one partial sum a tile, sums over tokens (dA_log, dskip, dbias) as one a segment; the last kernels add
+// them in order.
 #include <algorithm>
 
 #include "norm_rows.cuh"
@@ -18,60 +19,45 @@
 namespace gdn {
 namespace {
 
-constexpr int kChunk = 8;                       // tokens whose states a thread holds
-constexpr int kHalf = kScanSegment / 2;
+constexpr int kChunk = kScanChunk;   // tokens whose states a thread holds
 
-// A lane has two channels of SN states each; the L lanes of a channel pair are P lanes apart.
+// A lane has two channels of four states each; the L lanes of a channel pair are P lanes apart, so that adjacent lanes read
+// the same B and C.
 template <int N>
 struct Shape {
-    static constexpr int SN = 4, L = N / SN, P = 32 / L, CH = 2 * P * (kScanThreads / 32), K = kChunk;
+    static constexpr int L = N / 4, P = 32 / L, CH = 2 * P * (kScanThreads / 32), K = kChunk;
     static constexpr int kRow = CH + 8;
-    static constexpr int Q = SN / 2, V = SN / 4;   // pairs and vectors of a lane's states of a channel
 };
 struct Lane {
-    int n0, pair, swap, turn;   // first state, channel pair in the warp, whether the pair's channels and (turn) the two
-                                // vectors of states are held in the other order: what a lane sends in the first exchange of
-                                // a sum is then in the same registers everywhere
-    int ch[2];                  // channels in the tile
+    int n0, pair;   // first state, channel pair in the warp
+    int ch[2];      // channels in the tile; every other of a pair's lanes holds them in the other order
 };
 template <int N>
 __device__ __forceinline__ Lane lane_of(int tid) {
-    using S = Shape<N>;
+    constexpr int P = Shape<N>::P;
     Lane l;
-    const int nl = tid % 32 / S::P;
-    l.pair = tid % S::P;
-    l.n0 = nl * S::SN;
-    l.swap = nl & 1;
-    l.turn = S::SN == 8 ? l.pair / (S::P / 2) : 0;
-    l.ch[0] = tid / 32 * 2 * S::P + 2 * l.pair + l.swap;
+    l.pair = tid % P;
+    l.n0 = tid % 32 / P * 4;
+    l.ch[0] = tid / 32 * 2 * P + 2 * l.pair + (tid / P & 1);
     l.ch[1] = l.ch[0] ^ 1;
     return l;
 }
-// A lane's SN states at p (of its channel, or of B, C).
-template <int N>
-__device__ __forceinline__ void load_states(float2 (&x)[Shape<N>::Q], const float* p, const Lane& l) {
-#pragma unroll
-    for (int v = 0; v < Shape<N>::V; ++v) {
-        const float4 f = *reinterpret_cast<const float4*>(p + l.n0 + 4 * (v ^ l.turn));
-        x[2 * v] = make_float2(f.x, f.y);
-        x[2 * v + 1] = make_float2(f.z, f.w);
-    }
+__device__ __forceinline__ void load_states(float2 (&x)[2], const float* p) {
+    const float4 f = *reinterpret_cast<const float4*>(p);
+    x[0] = make_float2(f.x, f.y);
+    x[1] = make_float2(f.z, f.w);
+}
+__device__ __forceinline__ void store_states(float* p, const float2 (&x)[2]) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
 }
 template <int N>
-__device__ __forceinline__ void store_states(float* p, const float2 (&x)[Shape<N>::Q], const Lane& l) {
-#pragma unroll
-    for (int v = 0; v < Shape<N>::V; ++v)
-        *reinterpret_cast<float4*>(p + l.n0 + 4 * (v ^ l.turn)) =
-            make_float4(x[2 * v].x, x[2 * v].y, x[2 * v + 1].x, x[2 * v + 1].y);
-}
-template <int N>
-__device__ __forceinline__ void load_rates(float2 (&A2)[2][Shape<N>::Q], const ScanArgs& a, const ChannelTile& tile, const Lane& l) {
+__device__ __forceinline__ void load_rates(float2 (&A2)[2][2], const ScanArgs& a, const ChannelTile& tile, const Lane& l) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         const bool own = l.ch[s] < tile.n;
-        if (own) load_states<N>(A2[s], a.A_log + (size_t)(tile.d0 + l.ch[s]) * N, l);
+        if (own) load_states(A2[s], a.A_log + (size_t)(tile.d0 + l.ch[s]) * N + l.n0);
 #pragma unroll
-        for (int i = 0; i < Shape<N>::Q; ++i) A2[s][i] = own ? make_float2(rate2(A2[s][i].x), rate2(A2[s][i].y)) : all2(0.f);
+        for (int i = 0; i < 2; ++i) A2[s][i] = own ? make_float2(rate2(A2[s][i].x), rate2(A2[s][i].y)) : all2(0.f);
     }
 }
 
@@ -86,16 +72,25 @@ struct Own {
 __device__ __forceinline__ float4 columns(const float* p, const ChannelTile& tile, int c) {
     return p && c < tile.n ? *reinterpret_cast<const float4*>(p + tile.d0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
+// dt and dt u of four channels; dt = 0 past the end, where nothing changes.
+__device__ __forceinline__ void form_dt(float2* to, float4 u, float4 delta, float4 bias, bool ok) {
+    float4 d = softplus4(add4(delta, bias));
+    if (!ok) d = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4* p = reinterpret_cast<float4*>(to);
+    p[0] = make_float4(d.x, d.x * u.x, d.y, d.y * u.y);
+    p[1] = make_float4(d.z, d.z * u.z, d.w, d.w * u.w);
+}
 
 // ---------------------------------------------------------------- the segments' ends
 // Each segment's contribution to the state behind it, from zero, and to the adjoint before it, sum_t (a_first .. a_t) C_t
-// p_t; its sum of dt, and the same of its first half for the state in its middle.
+// p_t; its sum of dt; and the state and the sum before each chunk but the first.
 template <int N, typename T>
 __global__ void __launch_bounds__(kScanThreads) scan_ends_kernel(const __grid_constant__ ScanArgs a) {
     using S = Shape<N>;
     using O = Own<N>;
-    constexpr int CH = S::CH, K = 16, VEC = (K * CH / 4 + kScanThreads - 1) / kScanThreads, BC = (2 * K * N / 4 + kScanThreads - 1) / kScanThreads;
-    static_assert(kHalf % K == 0, "halves are whole tiles");
+    constexpr int CH = S::CH, K = 16, VEC = (K * CH / 4 + kScanThreads - 1) / kScanThreads,
+                  BC = (2 * K * N / 4 + kScanThreads - 1) / kScanThreads;
+    static_assert(K % kChunk == 0, "tiles are whole chunks");
     __shared__ __align__(16) float2 s_dt[K][CH];
     __shared__ __align__(16) float s_p[K][CH];
     __shared__ __align__(16) float s_bc[2][K][N];
@@ -103,24 +98,23 @@ __global__ void __launch_bounds__(kScanThreads) scan_ends_kernel(const __grid_co
     const ChannelTile tile = channel_tile(a.D, a.G, CH, blockIdx.x % tiles);
     Unit u;
     if (!unit_at(a.cu, a.T, a.nseq, a.seg, slot, false, u)) return;
-    if (u.first && u.last && u.t1 - u.t0 <= kHalf) return;   // nothing reads it
     const int tid = threadIdx.x, len = (int)(u.t1 - u.t0);
     const Lane l = lane_of<N>(tid);
     const O own(tid);
     const size_t DN = (size_t)a.D * N;
-    float2 A2[2][S::Q], h[2][S::Q], lam[2][S::Q], E[2][S::Q];
+    float2 A2[2][2], h[2][2], lam[2][2], E[2][2];
     float sum_dt[2] = {0.f, 0.f};
     load_rates<N>(A2, a, tile, l);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int i = 0; i < S::Q; ++i) {
+        for (int i = 0; i < 2; ++i) {
             h[s][i] = lam[s][i] = all2(0.f);
             E[s][i] = all2(1.f);
         }
     const float4 bias = columns(a.dt_bias, tile, own.c4);
     const bool some = own.c4 < tile.n;
-    // the thread's first vector of the next tile, and elements between its rows
+    // the thread's first vector of the next tile
     auto first = [&](const void* p, long long stride) {
         return static_cast<const T*>(p) + (u.t0 + own.k0) * stride + tile.d0 + own.c4;
     };
@@ -130,7 +124,8 @@ __global__ void __launch_bounds__(kScanThreads) scan_ends_kernel(const __grid_co
     auto load = [&](int t) {   // the tiles in order
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-            const bool ok = some && t + own.k0 + v * O::kStep < len && own.k0 + v * O::kStep < K;
+            const int k = own.k0 + v * O::kStep;
+            const bool ok = some && t + k < len && k < K;
             const long long row = v * O::kStep;
             ru[v] = ok ? load4(pu + row * a.u_stride) : Raw4<T>::zero();
             rd[v] = ok ? load4(pd + row * a.delta_stride) : Raw4<T>::zero();
@@ -148,18 +143,13 @@ __global__ void __launch_bounds__(kScanThreads) scan_ends_kernel(const __grid_co
             rbc[v] = which < 2 && t + k < len ? load4(p + (u.t0 + t + k) * (which == 0 ? a.b_stride : a.c_stride)) : Raw4<T>::zero();
         }
     };
-    load(0);
+    if (len > 0) load(0);
     for (int t = 0; t < len; t += K) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             const int k = own.k0 + v * O::kStep;
             if (k >= K) break;
-            const float4 x = ru[v].f();
-            float4 d = softplus4(add4(rd[v].f(), bias));
-            if (!some || t + k >= len) d = make_float4(0.f, 0.f, 0.f, 0.f);   // past the end: nothing changes
-            float4* p = reinterpret_cast<float4*>(&s_dt[k][own.c4]);
-            p[0] = make_float4(d.x, d.x * x.x, d.y, d.y * x.y);
-            p[1] = make_float4(d.z, d.z * x.z, d.w, d.w * x.w);
+            form_dt(&s_dt[k][own.c4], ru[v].f(), rd[v].f(), bias, some && t + k < len);
             *reinterpret_cast<float4*>(&s_p[k][own.c4]) = pz ? gated4(rg[v].f(), rz[v].f()) : rg[v].f();
         }
 #pragma unroll
@@ -169,31 +159,34 @@ __global__ void __launch_bounds__(kScanThreads) scan_ends_kernel(const __grid_co
         }
         __syncthreads();
         if (t + K < len) load(t + K);
-        if (t == kHalf)
+#pragma unroll 1
+        for (int k0 = 0; k0 < K; k0 += kChunk) {
+            if (t + k0 > 0 && t + k0 < len)
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (l.ch[s] >= tile.n) continue;
-                const size_t d = tile.d0 + l.ch[s];
-                store_states<N>(a.mids + (size_t)slot * DN + d * N, h[s], l);
-                if (l.n0 == 0) a.mid_dt[(size_t)slot * a.D + d] = sum_dt[s];
-            }
-#pragma unroll 4
-        for (int k = 0; k < K; ++k) {
-            float2 B[S::Q], C[S::Q];
-            load_states<N>(B, s_bc[0][k], l);
-            load_states<N>(C, s_bc[1][k], l);
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const float2 dd = s_dt[k][l.ch[s]];
-                const float p = s_p[k][l.ch[s]];
-#pragma unroll
-                for (int i = 0; i < S::Q; ++i) {
-                    const float2 e = decay(A2[s][i], dd.x);
-                    h[s][i] = fma2(e, h[s][i], mul2(B[i], all2(dd.y)));
-                    E[s][i] = mul2(E[s][i], e);
-                    lam[s][i] = fma2(E[s][i], mul2(C[i], all2(p)), lam[s][i]);
+                for (int s = 0; s < 2; ++s) {
+                    if (l.ch[s] >= tile.n) continue;
+                    const size_t row = (size_t)slot * (a.seg / kChunk) + (t + k0) / kChunk, d = tile.d0 + l.ch[s];
+                    store_states(a.chunks + row * DN + d * N + l.n0, h[s]);
+                    if (l.n0 == 0) a.chunk_dt[row * a.D + d] = sum_dt[s];
                 }
-                sum_dt[s] += dd.x;
+#pragma unroll
+            for (int k = k0; k < k0 + kChunk; ++k) {
+                float2 B[2], C[2];
+                load_states(B, &s_bc[0][k][l.n0]);
+                load_states(C, &s_bc[1][k][l.n0]);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const float2 dd = s_dt[k][l.ch[s]];
+                    const float p = s_p[k][l.ch[s]];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 e = decay(A2[s][i], dd.x);
+                        h[s][i] = fma2(e, h[s][i], mul2(B[i], all2(dd.y)));
+                        E[s][i] = mul2(E[s][i], e);
+                        lam[s][i] = fma2(E[s][i], mul2(C[i], all2(p)), lam[s][i]);
+                    }
+                    sum_dt[s] += dd.x;
+                }
             }
         }
         __syncthreads();
@@ -202,14 +195,15 @@ __global__ void __launch_bounds__(kScanThreads) scan_ends_kernel(const __grid_co
     for (int s = 0; s < 2; ++s) {
         if (l.ch[s] >= tile.n) continue;
         const size_t d = tile.d0 + l.ch[s];
-        store_states<N>(a.states + (size_t)slot * DN + d * N, h[s], l);
-        store_states<N>(a.adjoints + (size_t)slot * DN + d * N, lam[s], l);
+        store_states(a.states + (size_t)slot * DN + d * N + l.n0, h[s]);
+        store_states(a.adjoints + (size_t)slot * DN + d * N + l.n0, lam[s]);
         if (l.n0 == 0) a.sum_dt[(size_t)slot * a.D + d] = sum_dt[s];
     }
 }
 
 // ---------------------------------------------------------------- the gradients
-__device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool ok, float) {   // four values; zeros without
+// Four values; zeros where there is none.
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool ok, float) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool ok, __nv_bfloat16) {
@@ -219,31 +213,31 @@ __device__ __forceinline__ void copies_done() {
     asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
 }
 
-// A stage holds the raw values of a chunk: K tokens of u, delta, z, dy, B and C, or (walking forwards) 2 K tokens of u,
-// delta and B.  A thread reads back only what it copied itself.
+// A stage holds a chunk as it is in memory: K tokens of u, delta, z, dy, B and C, and the state before it.  A thread reads
+// back only what it copied itself.
 template <int N, typename T>
 struct Smem {
     using S = Shape<N>;
-    float2 dt[2 * kChunk][S::CH];                     // dt, dt u; backwards the second half holds p
-    float bc[2][kChunk][N];                           // B, C, or B of 2 K tokens
+    float2 dt[kChunk][S::CH];                         // dt, dt u
+    float p[kChunk][S::CH];
+    float bc[2][kChunk][N];
     float sums[3][kChunk][S::kRow];                   // y, q, r
     float red[kScanThreads / 32][kChunk][2 * N];      // dB, dC of each warp
-    float4 state[kHalf / kChunk][2 * S::V][kScanThreads];
+    float4 first[2][kScanThreads];                    // the state before the segment
+    float4 state[2][2][kScanThreads];
     T rows[2][4 * kChunk][S::CH];
     T bc_rows[2][2 * kChunk][N];
 };
 
 template <int N, typename T>
-__global__ void __launch_bounds__(kScanThreads, 2) scan_bwd_kernel(const __grid_constant__ ScanArgs a) {
+__global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_constant__ ScanArgs a) {
     using S = Shape<N>;
     using O = Own<N>;
-    constexpr int L = S::L, P = S::P, CH = S::CH, K = S::K, Q = S::Q, V = S::V;
+    constexpr int L = S::L, P = S::P, CH = S::CH, K = S::K;
     constexpr int TT = L < 4 ? 1 : 2;   // tokens whose sums over the lanes are finished together
     constexpr int VEC = (K * CH / 4 + kScanThreads - 1) / kScanThreads, BC = (2 * K * N / 4 + kScanThreads - 1) / kScanThreads;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     Smem<N, T>& sm = *reinterpret_cast<Smem<N, T>*>(smem_raw);
-    float(*const s_p)[CH] = reinterpret_cast<float(*)[CH]>(sm.dt[K]);
-    float(*const s_b2)[N] = sm.bc[0];
     const int tiles = a.G * ((a.D / a.G + CH - 1) / CH), slot = blockIdx.x / tiles, tile_id = blockIdx.x % tiles;
     const ChannelTile tile = channel_tile(a.D, a.G, CH, tile_id);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -253,302 +247,220 @@ __global__ void __launch_bounds__(kScanThreads, 2) scan_bwd_kernel(const __grid_
     const size_t DN = (size_t)a.D * N;
     Unit u;
     if (!unit_at(a.cu, a.T, a.nseq, a.seg, slot, false, u)) u.t0 = u.t1 = 0, u.first = false;
-    const int len = (int)(u.t1 - u.t0);
+    const int len = (int)(u.t1 - u.t0), chunks = (len + K - 1) / K;
     float* const part_A = a.part_A + (size_t)slot * DN;
     float* const part_s = a.part_s + (size_t)slot * 2 * a.D + tile.d0;
     auto channel = [&](int s) { return (size_t)(tile.d0 + l.ch[s]); };
-    auto take = [&](const float* p, int s, float2 (&x)[Q]) {   // zeros where there is none
-#pragma unroll
-        for (int i = 0; i < Q; ++i) x[i] = all2(0.f);
-        if (p && l.ch[s] < tile.n) load_states<N>(x, p + channel(s) * N, l);
+    auto take = [&](const float* p, int s, float2 (&x)[2]) {   // zeros where there is none
+        x[0] = x[1] = all2(0.f);
+        if (p && l.ch[s] < tile.n) load_states(x, p + channel(s) * N + l.n0);
     };
-    auto put = [&](float* p, int s, const float2 (&x)[Q]) {
-        if (l.ch[s] < tile.n) store_states<N>(p + channel(s) * N, x, l);
+    auto put = [&](float* p, int s, const float2 (&x)[2]) {
+        if (l.ch[s] < tile.n) store_states(p + channel(s) * N + l.n0, x);
     };
 
-    float2 A2[2][Q], lam[2][Q], gA[2][Q];
+    float2 A2[2][2], lam[2][2], gA[2][2];
     load_rates<N>(A2, a, tile, l);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-#pragma unroll
-        for (int i = 0; i < Q; ++i) gA[s][i] = all2(0.f);
-        take(len == 0 ? nullptr : a.seg ? a.adjoints + (size_t)slot * DN : a.gh ? a.gh + (size_t)u.seq * DN : nullptr, s, lam[s]);
+        gA[s][0] = gA[s][1] = all2(0.f);
+        float2 x[2];
+        take(len ? a.states + (size_t)slot * DN : nullptr, s, x);
+        store_states(&sm.first[s][tid].x, x);
+        take(len ? a.adjoints + (size_t)slot * DN : nullptr, s, lam[s]);
     }
     const float4 bias = columns(a.dt_bias, tile, own.c4), skip = columns(a.skip, tile, own.c4);
     float4 g_skip = make_float4(0.f, 0.f, 0.f, 0.f), g_bias = g_skip;
 
-    // asks for rows r .. r + rows - 1 of the segment into a stage; row k of tensor x goes to rows[x K + k]
-    auto ask_rows = [&](int st, int x, const void* p, long long stride, int t, int rows) {
-        const T* from = static_cast<const T*>(p) + (u.t0 + t + own.k0) * stride + tile.d0 + own.c4;
-        for (int k = own.k0; k < rows; k += O::kStep, from += O::kStep * stride) {
+    // asks for the chunk at token t of the segment
+    auto ask_rows = [&](int st, int x, const void* p, long long stride, int t) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const int k = own.k0 + v * O::kStep;
+            if (k >= K) break;
             const bool ok = some && t + k < len;
-            copy_async(tc::smem_u32(&sm.rows[st][x * K + k][own.c4]), ok ? from : static_cast<const T*>(p), ok, T{});
+            const T* from = static_cast<const T*>(p) + (ok ? (u.t0 + t + k) * stride + tile.d0 + own.c4 : 0);
+            copy_async(tc::smem_u32(&sm.rows[st][x * K + k][own.c4]), from, ok, T{});
         }
     };
-    auto ask_bc = [&](int st, int t, bool both) {
+    auto ask = [&](int st, int t) {
+        ask_rows(st, 0, a.u, a.u_stride, t);
+        ask_rows(st, 1, a.delta, a.delta_stride, t);
+        if (a.z) ask_rows(st, 2, a.z, a.z_stride, t);
+        ask_rows(st, 3, a.gy, a.D, t);
 #pragma unroll
         for (int v = 0; v < BC; ++v) {
             const int i = tid + v * kScanThreads, k = i / (N / 4), n = i % (N / 4) * 4;
             if (k >= 2 * K) break;
-            const bool c = both && k >= K;
-            const int tk = t + (c ? k - K : k);
-            const T* p = static_cast<const T*>(c ? a.C : a.B) + (size_t)tile.g * N + n;
-            const bool ok = tk < len;
-            copy_async(tc::smem_u32(&sm.bc_rows[st][k][n]), ok ? p + (u.t0 + tk) * (c ? a.c_stride : a.b_stride) : p, ok, T{});
+            const bool c = k >= K, ok = t + k % K < len;
+            const T* from = static_cast<const T*>(c ? a.C : a.B) +
+                            (ok ? (u.t0 + t + k % K) * (c ? a.c_stride : a.b_stride) + (size_t)tile.g * N + n : 0);
+            copy_async(tc::smem_u32(&sm.bc_rows[st][k][n]), from, ok, T{});
         }
-    };
-    auto form_bc = [&](int st) {
+        const float* state = a.chunks + ((size_t)slot * (a.seg / K) + t / K) * DN;
 #pragma unroll
-        for (int v = 0; v < BC; ++v) {
-            const int i = tid + v * kScanThreads, k = i / (N / 4), n = i % (N / 4) * 4;
-            if (k >= 2 * K) break;
-            *reinterpret_cast<float4*>(&s_b2[k][n]) = load4(&sm.bc_rows[st][k][n]).f();
+        for (int s = 0; s < 2; ++s) {   // nothing before the first chunk
+            const bool ok = t > 0 && l.ch[s] < tile.n;
+            copy_async(tc::smem_u32(&sm.state[st][s][tid]), ok ? state + channel(s) * N + l.n0 : a.A_log, ok, 0.f);
         }
-    };
-    auto form_dt = [&](int k, float4 x, float4 delta, bool ok) {
-        float4 d = softplus4(add4(delta, bias));
-        if (!ok) d = make_float4(0.f, 0.f, 0.f, 0.f);   // past the end: nothing changes
-        float4* p = reinterpret_cast<float4*>(&sm.dt[k][own.c4]);
-        p[0] = make_float4(d.x, d.x * x.x, d.y, d.y * x.y);
-        p[1] = make_float4(d.z, d.z * x.z, d.w, d.w * x.w);
-    };
-    auto ask_walk = [&](int st, int t) {
-        ask_rows(st, 0, a.u, a.u_stride, t, 2 * K);
-        ask_rows(st, 2, a.delta, a.delta_stride, t, 2 * K);
-        ask_bc(st, t, false);
-    };
-    auto ask_chunk = [&](int st, int t) {
-        ask_rows(st, 0, a.u, a.u_stride, t, K);
-        ask_rows(st, 1, a.delta, a.delta_stride, t, K);
-        if (a.z) ask_rows(st, 2, a.z, a.z_stride, t, K);
-        ask_rows(st, 3, a.gy, a.D, t, K);
-        ask_bc(st, t, true);
     };
 
-    for (int half = len > kHalf ? 1 : 0; half >= 0 && len > 0; --half) {
-        const int h0 = half * kHalf, n = min(len - h0, kHalf), chunks = (n + K - 1) / K;
-        // forwards: the state before each chunk
-        {
-            float2 h[2][Q];
-            if (chunks > 1) ask_walk(0, h0);
+    if (chunks > 0) ask(0, (chunks - 1) * K);
+    for (int c = chunks - 1; c >= 0; --c) {
+        const int t = c * K, tokens = min(K, len - t), st = (chunks - 1 - c) & 1;
+        float cum[2] = {0.f, 0.f};   // dt up to the chunk
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                take(a.seg ? a.states + (size_t)slot * DN : a.h0 ? a.h0 + (size_t)u.seq * DN : nullptr, s, h[s]);
-                if (half) {
-                    float2 m[Q];
-                    take(a.mids + (size_t)slot * DN, s, m);
-                    const float dt = l.ch[s] < tile.n ? a.mid_dt[(size_t)slot * a.D + channel(s)] : 0.f;
+        for (int s = 0; s < 2; ++s)
+            if (c > 0 && l.ch[s] < tile.n) cum[s] = a.chunk_dt[((size_t)slot * (a.seg / K) + c) * a.D + channel(s)];
+        copies_done();
 #pragma unroll
-                    for (int i = 0; i < Q; ++i) h[s][i] = fma2(decay(A2[s][i], dt), h[s][i], m[i]);
-                }
-            }
-            auto keep = [&](int c) {
+        for (int v = 0; v < VEC; ++v) {
+            const int k = own.k0 + v * O::kStep;
+            if (k >= K) break;
+            const float4 g = load4(&sm.rows[st][3 * K + k][own.c4]).f();
+            form_dt(&sm.dt[k][own.c4], load4(&sm.rows[st][k][own.c4]).f(), load4(&sm.rows[st][K + k][own.c4]).f(), bias,
+                    some && k < tokens);
+            *reinterpret_cast<float4*>(&sm.p[k][own.c4]) = a.z ? gated4(g, load4(&sm.rows[st][2 * K + k][own.c4]).f()) : g;
+        }
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
+        for (int v = 0; v < BC; ++v) {
+            const int i = tid + v * kScanThreads, k = i / (N / 4), n = i % (N / 4) * 4;
+            if (k >= 2 * K) break;
+            *reinterpret_cast<float4*>(&sm.bc[0][k][n]) = load4(&sm.bc_rows[st][k][n]).f();
+        }
+        float2 hs[K][2][2], before[2][2];
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        sm.state[c][s * V + v][tid] = make_float4(h[s][2 * v].x, h[s][2 * v].y, h[s][2 * v + 1].x, h[s][2 * v + 1].y);
-            };
-            for (int c = 0; c < chunks; c += 2) {
-                const int st = c / 2 & 1;
-                keep(c);
-                if (c + 1 == chunks) break;
-                copies_done();
-                __syncthreads();   // the last tile has been walked
+        for (int s = 0; s < 2; ++s) {
+            float2 f[2], x[2];
+            load_states(f, &sm.first[s][tid].x);
+            load_states(x, &sm.state[st][s][tid].x);
 #pragma unroll
-                for (int v = 0; v < 2 * VEC; ++v) {
-                    const int k = own.k0 + v * O::kStep;
-                    if (k >= 2 * K) break;
-                    form_dt(k, load4(&sm.rows[st][k][own.c4]).f(), load4(&sm.rows[st][2 * K + k][own.c4]).f(),
-                            some && c * K + k < n);
-                }
-                form_bc(st);
-                __syncthreads();
-                if (c + 3 < chunks) ask_walk(st ^ 1, h0 + (c + 2) * K);
-                const int two = c + 2 < chunks ? 2 : 1;   // the last chunk's own steps come again backwards
-                for (int x = 0; x < two; ++x) {
-                    if (x) keep(c + 1);
-#pragma unroll
-                    for (int k0 = 0; k0 < K; ++k0) {
-                        const int k = x * K + k0;
-                        float2 B[Q];
-                        load_states<N>(B, s_b2[k], l);
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            const float2 dd = sm.dt[k][l.ch[s]];
-#pragma unroll
-                            for (int i = 0; i < Q; ++i) h[s][i] = fma2(decay(A2[s][i], dd.x), h[s][i], mul2(B[i], all2(dd.y)));
-                        }
-                    }
-                }
-                if (two == 1) keep(c + 1);
-            }
+            for (int i = 0; i < 2; ++i) before[s][i] = fma2(decay(A2[s][i], cum[s]), f[i], x[i]);
         }
         __syncthreads();
-        ask_chunk(0, h0 + (chunks - 1) * K);
-        for (int c = chunks - 1; c >= 0; --c) {
-            const int t = h0 + c * K, tokens = min(K, len - t), st = (chunks - 1 - c) & 1;
-            copies_done();
+        if (c > 0) ask(st ^ 1, t - K);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float2 B[2];
+            load_states(B, &sm.bc[0][k][l.n0]);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const float2 dd = sm.dt[k][l.ch[s]];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    hs[k][s][i] = fma2(decay(A2[s][i], dd.x), k ? hs[k ? k - 1 : 0][s][i] : before[s][i], mul2(B[i], all2(dd.y)));
+            }
+        }
+        // the decays are formed again: held from here, they would take as many registers as the states
+        asm volatile("" ::: "memory");
+        float sum[3][TT];   // y, q, r of the lane's first channel
+#pragma unroll
+        for (int k = K - 1; k >= 0; --k) {
+            float2 B[2], C[2], gB[2], gC[2];
+            load_states(B, &sm.bc[0][k][l.n0]);
+            load_states(C, &sm.bc[1][k][l.n0]);
+            float part[3][2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const float2 dd = sm.dt[k][l.ch[s]];
+                const float p = sm.p[k][l.ch[s]];
+                float2 y, q, r;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 hh = hs[k][s][i], prev = k ? hs[k ? k - 1 : 0][s][i] : before[s][i];
+                    lam[s][i] = fma2(C[i], all2(p), lam[s][i]);
+                    gC[i] = s == 0 ? mul2(hh, all2(p)) : fma2(hh, all2(p), gC[i]);
+                    gB[i] = s == 0 ? mul2(lam[s][i], all2(dd.y)) : fma2(lam[s][i], all2(dd.y), gB[i]);
+                    y = i == 0 ? mul2(hh, C[i]) : fma2(hh, C[i], y);
+                    q = i == 0 ? mul2(lam[s][i], B[i]) : fma2(lam[s][i], B[i], q);
+                    lam[s][i] = mul2(lam[s][i], decay(A2[s][i], dd.x));
+                    const float2 w = mul2(lam[s][i], prev);
+                    r = i == 0 ? mul2(w, A2[s][i]) : fma2(w, A2[s][i], r);
+                    gA[s][i] = fma2(w, all2(dd.x), gA[s][i]);
+                }
+                part[0][s] = y.x + y.y;
+                part[1][s] = q.x + q.y;
+                part[2][s] = r.x + r.y;
+            }
+            // the next lane of the pair holds the channels in the other order: each gets its first one's sums
+#pragma unroll
+            for (int x = 0; x < 3; ++x) sum[x][k % TT] = part[x][0] + __shfl_xor_sync(0xffffffffu, part[x][1], P);
+            if (k % TT == 0)
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    float s = transpose_sum<TT, 2 * P>(sum[x], lane);
+#pragma unroll
+                    for (int o = 2 * P * TT; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+                    sm.sums[x][k + lane / (2 * P) % TT][l.ch[0]] = s;
+                }
+            // sums over the pairs of the warp, values 2 j (dB) and 2 j + 1 (dC) of four states
+            constexpr int R = 8 / (P < 8 ? P : 8);
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 b = gB[j / 2], g = gC[j / 2];
+                v[2 * j] = j & 1 ? b.y : b.x;
+                v[2 * j + 1] = j & 1 ? g.y : g.x;
+            }
+#pragma unroll
+            for (int w = 8, x = 1; x < P && w > 1; w /= 2, x *= 2) {
+                const bool up = lane & x;
+#pragma unroll
+                for (int i = 0; i < w / 2; ++i) {
+                    const float mine = up ? v[2 * i + 1] : v[2 * i], theirs = up ? v[2 * i] : v[2 * i + 1];
+                    v[i] = mine + __shfl_xor_sync(0xffffffffu, theirs, x);
+                }
+            }
+#pragma unroll
+            for (int x = 8; x < P; x *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], x);
+            if (P <= 8 || l.pair < 8)
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int i = r * (8 / R) + l.pair % (8 / R);
+                    sm.red[warp][k][(i & 1) * N + l.n0 + i / 2] = v[r];
+                }
+        }
+        __syncthreads();
+        if (some)
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 const int k = own.k0 + v * O::kStep;
-                if (k >= K) break;
-                form_dt(k, load4(&sm.rows[st][k][own.c4]).f(), load4(&sm.rows[st][K + k][own.c4]).f(), some && k < tokens);
-                const float4 g = load4(&sm.rows[st][3 * K + k][own.c4]).f();
-                *reinterpret_cast<float4*>(&s_p[k][own.c4]) = a.z ? gated4(g, load4(&sm.rows[st][2 * K + k][own.c4]).f()) : g;
+                if (k >= tokens) break;
+                const long long row = u.t0 + t + k;
+                const size_t d = tile.d0 + own.c4;
+                auto raw = [&](int x) { return load4(&sm.rows[st][x * K + k][own.c4]).f(); };
+                auto f4 = [&](const float* p) { return *reinterpret_cast<const float4*>(p); };
+                const float4 x4 = raw(0), d4 = add4(raw(1), bias), g4 = raw(3), p4 = f4(&sm.p[k][own.c4]);
+                const float4 y4 = f4(&sm.sums[0][k][own.c4]), q4 = f4(&sm.sums[1][k][own.c4]), r4 = f4(&sm.sums[2][k][own.c4]);
+                const float4 ta = f4(&sm.dt[k][own.c4].x), tb = f4(&sm.dt[k][own.c4 + 2].x);
+                float2 gu[2], gd[2], gs[2], gz[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    auto pick = [&](float4 f) { return e == 0 ? make_float2(f.x, f.y) : make_float2(f.z, f.w); };
+                    const float2 x = pick(x4), p = pick(p4), q = pick(q4), sk = pick(skip);
+                    const float2 dt = e == 0 ? make_float2(ta.x, ta.z) : make_float2(tb.x, tb.z);
+                    gu[e] = fma2(dt, q, mul2(sk, p));
+                    gd[e] = mul2(fma2(x, q, mul2(pick(r4), all2(kLn2))), logistic2(pick(d4)));
+                    gs[e] = mul2(p, x);
+                    if (a.z) {   // silu'(z) = s (1 + z (1 - s))
+                        const float2 z = pick(raw(2)), sg = logistic2(z), full = fma2(sk, x, pick(y4));
+                        gz[e] = mul2(mul2(pick(g4), full), mul2(sg, fma2(z, fma2(sg, all2(-1.f), all2(1.f)), all2(1.f))));
+                    }
+                }
+                auto join = [](const float2 (&x)[2]) { return make_float4(x[0].x, x[0].y, x[1].x, x[1].y); };
+                store4(static_cast<T*>(a.gu) + row * a.D + d, join(gu));
+                store4(static_cast<T*>(a.gdelta) + row * a.D + d, join(gd));
+                if (a.z) store4(static_cast<T*>(a.gz) + row * a.gz_stride + d, join(gz));
+                g_skip = add4(g_skip, join(gs));
+                g_bias = add4(g_bias, join(gd));
             }
-            form_bc(st);
-            __syncthreads();
-            if (c > 0) ask_chunk(st ^ 1, t - K);
-            float2 hs[K][2][Q], before[2][Q];
-            auto start = [&](float2 (&x)[2][Q]) {
+        for (int i = tid; i < tokens * N / 2; i += kScanThreads) {
+            const int k = i / (N / 2), n = i % (N / 2) * 4;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const float4 f = sm.state[c][s * V + v][tid];
-                        x[s][2 * v] = make_float2(f.x, f.y);
-                        x[s][2 * v + 1] = make_float2(f.z, f.w);
-                    }
-            };
-            start(before);
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                float2 B[Q];
-                load_states<N>(B, sm.bc[0][k], l);
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const float2 dd = sm.dt[k][l.ch[s]];
-#pragma unroll
-                    for (int i = 0; i < Q; ++i)
-                        hs[k][s][i] = fma2(decay(A2[s][i], dd.x), k ? hs[k ? k - 1 : 0][s][i] : before[s][i], mul2(B[i], all2(dd.y)));
-                }
-            }
-            start(before);   // read again rather than held
-            float sum[3][TT];   // y, q, r of the lane's first channel
-#pragma unroll
-            for (int k = K - 1; k >= 0; --k) {
-                float2 B[Q], C[Q], gB[Q], gC[Q];
-                load_states<N>(B, sm.bc[0][k], l);
-                load_states<N>(C, sm.bc[1][k], l);
-                float part[3][2];
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const float2 dd = sm.dt[k][l.ch[s]];
-                    const float p = s_p[k][l.ch[s]];
-                    float2 y, q, r;
-#pragma unroll
-                    for (int i = 0; i < Q; ++i) {
-                        const float2 hh = hs[k][s][i], prev = k ? hs[k ? k - 1 : 0][s][i] : before[s][i];
-                        lam[s][i] = fma2(C[i], all2(p), lam[s][i]);
-                        gC[i] = s == 0 ? mul2(hh, all2(p)) : fma2(hh, all2(p), gC[i]);
-                        gB[i] = s == 0 ? mul2(lam[s][i], all2(dd.y)) : fma2(lam[s][i], all2(dd.y), gB[i]);
-                        y = i == 0 ? mul2(hh, C[i]) : fma2(hh, C[i], y);
-                        q = i == 0 ? mul2(lam[s][i], B[i]) : fma2(lam[s][i], B[i], q);
-                        lam[s][i] = mul2(lam[s][i], decay(A2[s][i], dd.x));
-                        const float2 w = mul2(lam[s][i], prev);
-                        r = i == 0 ? mul2(w, A2[s][i]) : fma2(w, A2[s][i], r);
-                        gA[s][i] = fma2(w, all2(dd.x), gA[s][i]);
-                    }
-                    part[0][s] = y.x + y.y;
-                    part[1][s] = q.x + q.y;
-                    part[2][s] = r.x + r.y;
-                }
-                // the next lane of the pair holds the channels in the other order: each gets its first one's sums
-#pragma unroll
-                for (int x = 0; x < 3; ++x) sum[x][k % TT] = part[x][0] + __shfl_xor_sync(0xffffffffu, part[x][1], P);
-                if (k % TT == 0)
-#pragma unroll
-                    for (int x = 0; x < 3; ++x) {
-                        float s = transpose_sum<TT, 2 * P>(sum[x], lane);
-#pragma unroll
-                        for (int o = 2 * P * TT; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-                        sm.sums[x][k + lane / (2 * P) % TT][l.ch[0]] = s;
-                    }
-                // sums over the pairs of the warp: the turned lanes' other vectors first, then values 2 j (dB) and 2 j + 1
-                // (dC) of four states
-                constexpr int P2 = S::SN == 8 ? P / 2 : P, R = 8 / (P2 < 8 ? P2 : 8);
-                float v[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 b = gB[j / 2], g = gC[j / 2];
-                    v[2 * j] = j & 1 ? b.y : b.x;
-                    v[2 * j + 1] = j & 1 ? g.y : g.x;
-                    if (S::SN == 8) {
-                        const float2 b2 = gB[(Q - 2) + j / 2], g2 = gC[(Q - 2) + j / 2];
-                        v[2 * j] += __shfl_xor_sync(0xffffffffu, j & 1 ? b2.y : b2.x, P / 2);
-                        v[2 * j + 1] += __shfl_xor_sync(0xffffffffu, j & 1 ? g2.y : g2.x, P / 2);
-                    }
-                }
-#pragma unroll
-                for (int w = 8, x = 1; x < P2 && w > 1; w /= 2, x *= 2) {
-                    const bool up = lane & x;
-#pragma unroll
-                    for (int i = 0; i < w / 2; ++i) {
-                        const float mine = up ? v[2 * i + 1] : v[2 * i], theirs = up ? v[2 * i] : v[2 * i + 1];
-                        v[i] = mine + __shfl_xor_sync(0xffffffffu, theirs, x);
-                    }
-                }
-#pragma unroll
-                for (int x = 8; x < P2; x *= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], x);
-                if (P2 <= 8 || l.pair < 8) {
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const int i = r * (8 / R) + l.pair % (8 / R);
-                        sm.red[warp][k][(i & 1) * N + l.n0 + 4 * l.turn + i / 2] = v[r];
-                    }
-                }
-            }
-            __syncthreads();
-            if (some)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const int k = own.k0 + v * O::kStep;
-                    if (k >= tokens) break;
-                    const long long row = u.t0 + t + k;
-                    const size_t d = tile.d0 + own.c4;
-                    auto raw = [&](int x) { return load4(&sm.rows[st][x * K + k][own.c4]).f(); };
-                    auto f4 = [&](const float* p) { return *reinterpret_cast<const float4*>(p); };
-                    const float4 x4 = raw(0), d4 = add4(raw(1), bias), g4 = raw(3), p4 = f4(&s_p[k][own.c4]);
-                    const float4 y4 = f4(&sm.sums[0][k][own.c4]), q4 = f4(&sm.sums[1][k][own.c4]), r4 = f4(&sm.sums[2][k][own.c4]);
-                    const float4 ta = f4(&sm.dt[k][own.c4].x), tb = f4(&sm.dt[k][own.c4 + 2].x);
-                    float4 gu4, gd4, gs4, gz4 = make_float4(0.f, 0.f, 0.f, 0.f), z4 = gz4;
-                    if (a.z) z4 = raw(2);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        auto pick = [&](float4 f) { return e == 0 ? make_float2(f.x, f.y) : make_float2(f.z, f.w); };
-                        const float2 x = pick(x4), g = pick(g4), p = pick(p4), q = pick(q4), sk = pick(skip);
-                        const float2 dt = e == 0 ? make_float2(ta.x, ta.z) : make_float2(tb.x, tb.z);
-                        const float2 gu = fma2(dt, q, mul2(sk, p));
-                        const float2 gd = mul2(fma2(x, q, mul2(pick(r4), all2(kLn2))), logistic2(pick(d4)));
-                        const float2 gs = mul2(p, x);
-                        float2 gz = all2(0.f);
-                        if (a.z) {
-                            const float2 z = pick(z4), sg = logistic2(z), full = fma2(sk, x, pick(y4));
-                            // silu'(z) = s (1 + z (1 - s))
-                            gz = mul2(mul2(g, full), mul2(sg, fma2(z, fma2(sg, all2(-1.f), all2(1.f)), all2(1.f))));
-                        }
-                        if (e == 0) {
-                            gu4.x = gu.x; gu4.y = gu.y; gd4.x = gd.x; gd4.y = gd.y; gz4.x = gz.x; gz4.y = gz.y; gs4.x = gs.x; gs4.y = gs.y;
-                        } else {
-                            gu4.z = gu.x; gu4.w = gu.y; gd4.z = gd.x; gd4.w = gd.y; gz4.z = gz.x; gz4.w = gz.y; gs4.z = gs.x; gs4.w = gs.y;
-                        }
-                    }
-                    store4(static_cast<T*>(a.gu) + row * a.D + d, gu4);
-                    store4(static_cast<T*>(a.gdelta) + row * a.D + d, gd4);
-                    if (a.z) store4(static_cast<T*>(a.gz) + row * a.gz_stride + d, gz4);
-                    g_skip = add4(g_skip, gs4);
-                    g_bias = add4(g_bias, gd4);
-                }
-            for (int i = tid; i < tokens * N / 2; i += kScanThreads) {
-                const int k = i / (N / 2), n = i % (N / 2) * 4;
-                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < kScanThreads / 32; ++w) s = add4(s, *reinterpret_cast<const float4*>(&sm.red[w][k][n]));
-                *reinterpret_cast<float4*>(a.part_bc + ((size_t)tile_id * a.tokens + u.t0 + t + k) * 2 * N + n) = s;
-            }
+            for (int w = 0; w < kScanThreads / 32; ++w) s = add4(s, *reinterpret_cast<const float4*>(&sm.red[w][k][n]));
+            *reinterpret_cast<float4*>(a.part_bc + ((size_t)tile_id * a.tokens + u.t0 + t + k) * 2 * N + n) = s;
         }
-        __syncthreads();
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -630,10 +542,8 @@ cudaError_t bwd_typed(const ScanArgs& a) {
     if (e != cudaSuccess) return e;
     const int per_group = (a.D / a.G + S::CH - 1) / S::CH;
     const unsigned blocks = (unsigned)((long long)a.slots * a.G * per_group);
-    if (a.seg) {
-        scan_ends_kernel<N, T><<<blocks, kScanThreads, 0, a.stream>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_scan_join(a, true)) != cudaSuccess) return e;
-    }
+    scan_ends_kernel<N, T><<<blocks, kScanThreads, 0, a.stream>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_scan_join(a, true)) != cudaSuccess) return e;
     scan_bwd_kernel<N, T><<<blocks, kScanThreads, sizeof(Smem<N, T>), a.stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long long vecs = (long long)a.tokens * a.G * N / 2;
@@ -656,22 +566,30 @@ cudaError_t bwd_n(const ScanArgs& a) {
 
 }  // namespace
 
-ScanBwdLayout scan_bwd_layout(long long tokens, int D, int G, int N, int nseq, bool packed) {
+ScanBwdLayout scan_bwd_layout(long long tokens, int D, int G, int N, int nseq) {
     ScanBwdLayout l{};
-    // half a segment a sequence at most: nothing to join
-    l.seg = !packed && tokens / nseq <= kHalf ? 0 : kScanSegment;
-    l.slots = l.seg ? tokens / kScanSegment + nseq : nseq;
-    const size_t states = ((size_t)l.slots * D * N * 4 + 255) / 256 * 256, rows = ((size_t)l.slots * D * 4 + 255) / 256 * 256;
-    const int ch = N == 8 ? Shape<8>::CH : N == 16 ? Shape<16>::CH : N == 32 ? Shape<32>::CH : Shape<64>::CH;
-    const int tiles = G * ((D / G + ch - 1) / ch);
-    l.adjoints = l.seg ? states : 0;   // the states come first
-    l.mids = 2 * l.adjoints;
-    l.sum_dt = 3 * l.adjoints;
-    l.mid_dt = l.sum_dt + (l.seg ? rows : 0);
-    l.part_A = l.mid_dt + (l.seg ? rows : 0);
-    l.part_s = l.part_A + states;
-    l.part_bc = l.part_s + 2 * rows;
-    l.total = l.part_bc + (size_t)tiles * tokens * 2 * N * 4;
+    const int ch = 2 * kScanThreads / (N / 4);
+    const long long tiles = (long long)G * ((D / G + ch - 1) / ch);
+    // some 4000 blocks, nine for each place on an SM
+    const long long seg = (tokens * tiles / 4000 + kScanMinSegment - 1) / kScanMinSegment * kScanMinSegment;
+    l.seg = (int)std::min(512LL, std::max((long long)kScanMinSegment, seg));
+    l.slots = tokens / l.seg + nseq;
+    size_t at = 0;
+    auto place = [&](size_t floats) {
+        const size_t p = at;
+        at += (floats * 4 + 255) / 256 * 256;
+        return p;
+    };
+    const size_t DN = (size_t)D * N, slots = (size_t)l.slots;
+    place(slots * DN);   // the states
+    l.adjoints = place(slots * DN);
+    l.sum_dt = place(slots * D);
+    l.chunks = place(slots * (l.seg / kChunk) * DN);
+    l.chunk_dt = place(slots * (l.seg / kChunk) * D);
+    l.part_A = place(slots * DN);
+    l.part_s = place(slots * 2 * D);
+    l.part_bc = place((size_t)tiles * tokens * 2 * N);
+    l.total = at;
     return l;
 }
 
