@@ -192,19 +192,20 @@ __global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_c
 // the last one's outputs meanwhile (one barrier a tile), so that a sequence's walk waits for neither.
 constexpr int kHelpers = 256;
 template <int N>
-struct MainSmem {
+struct MainShape {
     static constexpr int K = N == 8 ? 16 : 32, CH = Shape<N>::CH;
     static constexpr int kRow = CH + (N == 8 ? 0 : 256 / N);   // floats of a row of sums: no bank conflicts
-    float2 dt[2][K][CH];
-    float bc[2][2][K][N];
-    float y[2][K][kRow];
+    static constexpr size_t kSums = sizeof(float) * 2 * K * kRow;
 };
 template <int N, typename T>
 __global__ void __launch_bounds__(kScanThreads + kHelpers, 1) scan_main_kernel(const __grid_constant__ ScanArgs a) {
-    constexpr int L = Shape<N>::L, CH = Shape<N>::CH, P = Shape<N>::kPairs, K = MainSmem<N>::K, M = kHelpers;
+    constexpr int L = Shape<N>::L, CH = Shape<N>::CH, P = Shape<N>::kPairs, K = MainShape<N>::K, M = kHelpers, kRow = MainShape<N>::kRow;
     using S = Share<N, K, M>;
+    // arrays of their own, so that what is stored to the sums does not hold back the next tokens' loads
+    __shared__ __align__(16) float2 s_dt[2][K][CH];
+    __shared__ __align__(16) float s_bc[2][2][K][N];
     extern __shared__ __align__(16) uint8_t smem[];
-    MainSmem<N>& sm = *reinterpret_cast<MainSmem<N>*>(smem);
+    float(*const s_y)[K][kRow] = reinterpret_cast<float(*)[K][kRow]>(smem);
     const int tiles = a.G * ((a.D / a.G + CH - 1) / CH), slot = blockIdx.x / tiles;
     const ChannelTile tile = channel_tile(a.D, a.G, CH, blockIdx.x % tiles);
     Unit u;
@@ -234,8 +235,8 @@ __global__ void __launch_bounds__(kScanThreads + kHelpers, 1) scan_main_kernel(c
             next(wz, a.z_stride);
         };
         auto form = [&](int i) {
-            form_dt<K, CH, M>(sm.dt[i & 1], ru, rd, bias, tokens_of(i), tile.n, tid);
-            form_bc<K, N, M>(sm.bc[i & 1], rbc, tid);
+            form_dt<K, CH, M>(s_dt[i & 1], ru, rd, bias, tokens_of(i), tile.n, tid);
+            form_bc<K, N, M>(s_bc[i & 1], rbc, tid);
         };
         auto finish = [&](int i, const Raw4<T> (&fu)[S::kVecs], const Raw4<T> (&fz)[S::kVecs]) {
             const int tokens = c4 < tile.n ? tokens_of(i) : 0;
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(kScanThreads + kHelpers, 1) scan_main_kernel(c
             for (int v = 0; v < S::kVecs; ++v) {
                 const int k = tid / (CH / 4) + v * (M / (CH / 4));
                 if (k >= tokens) break;
-                float4 y = *reinterpret_cast<const float4*>(&sm.y[i & 1][k][c4]);
+                float4 y = *reinterpret_cast<const float4*>(&s_y[i & 1][k][c4]);
                 const float4 x = fu[v].f();
                 const float2 ya = fma2(make_float2(skip.x, skip.y), make_float2(x.x, x.y), make_float2(y.x, y.y));
                 const float2 yb = fma2(make_float2(skip.z, skip.w), make_float2(x.z, x.w), make_float2(y.z, y.w));
@@ -291,8 +292,8 @@ __global__ void __launch_bounds__(kScanThreads + kHelpers, 1) scan_main_kernel(c
     constexpr int TT = L / 2;              // tokens whose sums over the lanes are finished together
     constexpr int U = 16;                  // tokens between which instructions can be moved: no store before a load
     for (int i = 0; i < n; ++i) {
-        const float2(*dt)[CH] = sm.dt[i & 1];
-        const float(*bc)[K][N] = sm.bc[i & 1];
+        const float2(*dt)[CH] = s_dt[i & 1];
+        const float(*bc)[K][N] = s_bc[i & 1];
 #pragma unroll 1
         for (int k0 = 0; k0 < K; k0 += U) {
             float out[U / TT];
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kScanThreads + kHelpers, 1) scan_main_kernel(c
                 out[j / TT] = transpose_sum<TT, 2 * P>(sum, threadIdx.x);
             }
 #pragma unroll
-            for (int j = 0; j < U; j += TT) sm.y[i & 1][k0 + j + threadIdx.x / (2 * P) % TT][l.ch[0]] = out[j / TT];
+            for (int j = 0; j < U; j += TT) s_y[i & 1][k0 + j + threadIdx.x / (2 * P) % TT][l.ch[0]] = out[j / TT];
         }
         __syncthreads();
     }
@@ -427,9 +428,9 @@ cudaError_t fwd_typed(const ScanArgs& a) {
         const cudaError_t e = launch_scan_join(a, false);
         if (e != cudaSuccess) return e;
     }
-    const cudaError_t e = allow_smem<scan_main_kernel<N, T>>();
+    const cudaError_t e = allow_smem<scan_main_kernel<N, T>>(MainShape<N>::kSums);
     if (e != cudaSuccess) return e;
-    scan_main_kernel<N, T><<<blocks, kScanThreads + kHelpers, sizeof(MainSmem<N>), a.stream>>>(a);
+    scan_main_kernel<N, T><<<blocks, kScanThreads + kHelpers, MainShape<N>::kSums, a.stream>>>(a);
     return cudaGetLastError();
 }
 template <int N, typename T>

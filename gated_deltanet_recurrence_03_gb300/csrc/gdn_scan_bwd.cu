@@ -85,7 +85,7 @@ __device__ __forceinline__ void form_dt(float2* to, float4 u, float4 delta, floa
 // Each segment's contribution to the state behind it, from zero, and to the adjoint before it, sum_t (a_first .. a_t) C_t
 // p_t; its sum of dt; and the state and the sum before each chunk but the first.
 template <int N, typename T>
-__global__ void __launch_bounds__(kScanThreads) scan_ends_kernel(const __grid_constant__ ScanArgs a) {
+__global__ void __launch_bounds__(kScanThreads, 4) scan_ends_kernel(const __grid_constant__ ScanArgs a) {
     using S = Shape<N>;
     using O = Own<N>;
     constexpr int CH = S::CH, K = 16, VEC = (K * CH / 4 + kScanThreads - 1) / kScanThreads,
@@ -216,14 +216,9 @@ __device__ __forceinline__ void copies_done() {
 // A stage holds a chunk as it is in memory: K tokens of u, delta, z, dy, B and C, and the state before it.  A thread reads
 // back only what it copied itself.
 template <int N, typename T>
-struct Smem {
+struct Stages {
     using S = Shape<N>;
-    float2 dt[kChunk][S::CH];                         // dt, dt u
-    float p[kChunk][S::CH];
-    float bc[2][kChunk][N];
-    float sums[3][kChunk][S::kRow];                   // y, q, r
-    float red[kScanThreads / 32][kChunk][2 * N];      // dB, dC of each warp
-    float4 first[2][kScanThreads];                    // the state before the segment
+    float4 first[2][kScanThreads];   // the state before the segment
     float4 state[2][2][kScanThreads];
     T rows[2][4 * kChunk][S::CH];
     T bc_rows[2][2 * kChunk][N];
@@ -237,7 +232,13 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
     constexpr int TT = L < 4 ? 1 : 2;   // tokens whose sums over the lanes are finished together
     constexpr int VEC = (K * CH / 4 + kScanThreads - 1) / kScanThreads, BC = (2 * K * N / 4 + kScanThreads - 1) / kScanThreads;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    Smem<N, T>& sm = *reinterpret_cast<Smem<N, T>*>(smem_raw);
+    Stages<N, T>& sm = *reinterpret_cast<Stages<N, T>*>(smem_raw);
+    // arrays of their own, so that what is stored to one does not hold back the next token's loads from another
+    __shared__ __align__(16) float2 s_dt[K][CH];                              // dt, dt u
+    __shared__ __align__(16) float s_p[K][CH];
+    __shared__ __align__(16) float s_bc[2][K][N];
+    __shared__ __align__(16) float s_sums[3][K][S::kRow];                     // y, q, r
+    __shared__ __align__(16) float s_red[kScanThreads / 32][K][2 * N];        // dB, dC of each warp
     const int tiles = a.G * ((a.D / a.G + CH - 1) / CH), slot = blockIdx.x / tiles, tile_id = blockIdx.x % tiles;
     const ChannelTile tile = channel_tile(a.D, a.G, CH, tile_id);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -318,15 +319,15 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
             const int k = own.k0 + v * O::kStep;
             if (k >= K) break;
             const float4 g = load4(&sm.rows[st][3 * K + k][own.c4]).f();
-            form_dt(&sm.dt[k][own.c4], load4(&sm.rows[st][k][own.c4]).f(), load4(&sm.rows[st][K + k][own.c4]).f(), bias,
+            form_dt(&s_dt[k][own.c4], load4(&sm.rows[st][k][own.c4]).f(), load4(&sm.rows[st][K + k][own.c4]).f(), bias,
                     some && k < tokens);
-            *reinterpret_cast<float4*>(&sm.p[k][own.c4]) = a.z ? gated4(g, load4(&sm.rows[st][2 * K + k][own.c4]).f()) : g;
+            *reinterpret_cast<float4*>(&s_p[k][own.c4]) = a.z ? gated4(g, load4(&sm.rows[st][2 * K + k][own.c4]).f()) : g;
         }
 #pragma unroll
         for (int v = 0; v < BC; ++v) {
             const int i = tid + v * kScanThreads, k = i / (N / 4), n = i % (N / 4) * 4;
             if (k >= 2 * K) break;
-            *reinterpret_cast<float4*>(&sm.bc[0][k][n]) = load4(&sm.bc_rows[st][k][n]).f();
+            *reinterpret_cast<float4*>(&s_bc[0][k][n]) = load4(&sm.bc_rows[st][k][n]).f();
         }
         float2 hs[K][2][2], before[2][2];
 #pragma unroll
@@ -342,10 +343,10 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             float2 B[2];
-            load_states(B, &sm.bc[0][k][l.n0]);
+            load_states(B, &s_bc[0][k][l.n0]);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const float2 dd = sm.dt[k][l.ch[s]];
+                const float2 dd = s_dt[k][l.ch[s]];
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     hs[k][s][i] = fma2(decay(A2[s][i], dd.x), k ? hs[k ? k - 1 : 0][s][i] : before[s][i], mul2(B[i], all2(dd.y)));
@@ -357,13 +358,13 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
 #pragma unroll
         for (int k = K - 1; k >= 0; --k) {
             float2 B[2], C[2], gB[2], gC[2];
-            load_states(B, &sm.bc[0][k][l.n0]);
-            load_states(C, &sm.bc[1][k][l.n0]);
+            load_states(B, &s_bc[0][k][l.n0]);
+            load_states(C, &s_bc[1][k][l.n0]);
             float part[3][2];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const float2 dd = sm.dt[k][l.ch[s]];
-                const float p = sm.p[k][l.ch[s]];
+                const float2 dd = s_dt[k][l.ch[s]];
+                const float p = s_p[k][l.ch[s]];
                 float2 y, q, r;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
                     float s = transpose_sum<TT, 2 * P>(sum[x], lane);
 #pragma unroll
                     for (int o = 2 * P * TT; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-                    sm.sums[x][k + lane / (2 * P) % TT][l.ch[0]] = s;
+                    s_sums[x][k + lane / (2 * P) % TT][l.ch[0]] = s;
                 }
             // sums over the pairs of the warp, values 2 j (dB) and 2 j + 1 (dC) of four states
             constexpr int R = 8 / (P < 8 ? P : 8);
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const int i = r * (8 / R) + l.pair % (8 / R);
-                    sm.red[warp][k][(i & 1) * N + l.n0 + i / 2] = v[r];
+                    s_red[warp][k][(i & 1) * N + l.n0 + i / 2] = v[r];
                 }
         }
         __syncthreads();
@@ -430,9 +431,9 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
                 const size_t d = tile.d0 + own.c4;
                 auto raw = [&](int x) { return load4(&sm.rows[st][x * K + k][own.c4]).f(); };
                 auto f4 = [&](const float* p) { return *reinterpret_cast<const float4*>(p); };
-                const float4 x4 = raw(0), d4 = add4(raw(1), bias), g4 = raw(3), p4 = f4(&sm.p[k][own.c4]);
-                const float4 y4 = f4(&sm.sums[0][k][own.c4]), q4 = f4(&sm.sums[1][k][own.c4]), r4 = f4(&sm.sums[2][k][own.c4]);
-                const float4 ta = f4(&sm.dt[k][own.c4].x), tb = f4(&sm.dt[k][own.c4 + 2].x);
+                const float4 x4 = raw(0), d4 = add4(raw(1), bias), g4 = raw(3), p4 = f4(&s_p[k][own.c4]);
+                const float4 y4 = f4(&s_sums[0][k][own.c4]), q4 = f4(&s_sums[1][k][own.c4]), r4 = f4(&s_sums[2][k][own.c4]);
+                const float4 ta = f4(&s_dt[k][own.c4].x), tb = f4(&s_dt[k][own.c4 + 2].x);
                 float2 gu[2], gd[2], gs[2], gz[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
             const int k = i / (N / 2), n = i % (N / 2) * 4;
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kScanThreads / 32; ++w) s = add4(s, *reinterpret_cast<const float4*>(&sm.red[w][k][n]));
+            for (int w = 0; w < kScanThreads / 32; ++w) s = add4(s, *reinterpret_cast<const float4*>(&s_red[w][k][n]));
             *reinterpret_cast<float4*>(a.part_bc + ((size_t)tile_id * a.tokens + u.t0 + t + k) * 2 * N + n) = s;
         }
     }
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
         put(a.gh0 + (size_t)u.seq * DN, s, lam[s]);
     }
     // the threads with the same channels, in order
-    float4* const fold = reinterpret_cast<float4*>(smem_raw);
+    float4* const fold = &sm.state[0][0][0];
     __syncthreads();
     fold[2 * tid] = g_skip;
     fold[2 * tid + 1] = g_bias;
@@ -538,13 +539,13 @@ __global__ void __launch_bounds__(kSumCols * kSumRows) scan_weight_sums_kernel(c
 template <int N, typename T>
 cudaError_t bwd_typed(const ScanArgs& a) {
     using S = Shape<N>;
-    cudaError_t e = allow_smem<scan_bwd_kernel<N, T>>();
+    cudaError_t e = allow_smem<scan_bwd_kernel<N, T>>(sizeof(Stages<N, T>));
     if (e != cudaSuccess) return e;
     const int per_group = (a.D / a.G + S::CH - 1) / S::CH;
     const unsigned blocks = (unsigned)((long long)a.slots * a.G * per_group);
     scan_ends_kernel<N, T><<<blocks, kScanThreads, 0, a.stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_scan_join(a, true)) != cudaSuccess) return e;
-    scan_bwd_kernel<N, T><<<blocks, kScanThreads, sizeof(Smem<N, T>), a.stream>>>(a);
+    scan_bwd_kernel<N, T><<<blocks, kScanThreads, sizeof(Stages<N, T>), a.stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const long long vecs = (long long)a.tokens * a.G * N / 2;
     scan_bc_sums_kernel<T><<<(unsigned)((vecs + 255) / 256), 256, 0, a.stream>>>(a, per_group);

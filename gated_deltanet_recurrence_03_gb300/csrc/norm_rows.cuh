@@ -106,7 +106,7 @@ constexpr size_t kSmemMax = 227 * 1024;
 
 // The shared-memory limit of a kernel belongs to a device: raised once on each.
 template <auto KERNEL>
-cudaError_t allow_smem() {
+cudaError_t allow_smem(size_t bytes = kSmemMax) {
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> done[kMaxDevices];
     int dev = 0;
@@ -114,7 +114,7 @@ cudaError_t allow_smem() {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
     return e;
 }
