@@ -188,18 +188,21 @@ __global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_c
     }
 }
 
-// The outputs.  Four warps walk the states; eight others form the next tile's dt, dt u, B and C in shared memory and finish
-// the last one's outputs meanwhile (one barrier a tile), so that a sequence's walk waits for neither.
-constexpr int kHelpers = 256;
+// The outputs.  Four warps walk the states; others form the next tile's dt, dt u, B and C in shared memory and finish the
+// last one's outputs meanwhile (one barrier a tile), so that the walk waits for neither.  Where whole sequences are walked
+// (SEG false) few blocks are there and the walk itself is what takes the time: registers for a whole tile's instructions in
+// any order, eight warps of helpers.  Segments fill the GPU: two blocks an SM with bf16 (fp32 vectors would not fit the
+// registers), four warps of helpers.
+__host__ __device__ constexpr int helpers(bool seg) { return seg ? 128 : 256; }
 template <int N>
 struct MainShape {
     static constexpr int K = N == 8 ? 16 : 32, CH = Shape<N>::CH;
     static constexpr int kRow = CH + (N == 8 ? 0 : 256 / N);   // floats of a row of sums: no bank conflicts
     static constexpr size_t kSums = sizeof(float) * 2 * K * kRow;
 };
-template <int N, typename T>
-__global__ void __launch_bounds__(kScanThreads + kHelpers, 1) scan_main_kernel(const __grid_constant__ ScanArgs a) {
-    constexpr int L = Shape<N>::L, CH = Shape<N>::CH, P = Shape<N>::kPairs, K = MainShape<N>::K, M = kHelpers, kRow = MainShape<N>::kRow;
+template <int N, typename T, bool SEG>
+__global__ void __launch_bounds__(kScanThreads + helpers(SEG), SEG && sizeof(T) == 2 ? 2 : 1) scan_main_kernel(const __grid_constant__ ScanArgs a) {
+    constexpr int L = Shape<N>::L, CH = Shape<N>::CH, P = Shape<N>::kPairs, K = MainShape<N>::K, M = helpers(SEG), kRow = MainShape<N>::kRow;
     using S = Share<N, K, M>;
     // arrays of their own, so that what is stored to the sums does not hold back the next tokens' loads
     __shared__ __align__(16) float2 s_dt[2][K][CH];
@@ -282,7 +285,7 @@ __global__ void __launch_bounds__(kScanThreads + kHelpers, 1) scan_main_kernel(c
     const Lane l = lane_of<N>(threadIdx.x);
     float2 A2[2][2], h[2][2];
     load_rates<N>(A2, a, tile, l);
-    const float* from = a.seg ? a.states + (size_t)slot * DN : a.h0 ? a.h0 + (size_t)u.seq * DN : nullptr;
+    const float* from = SEG ? a.states + (size_t)slot * DN : a.h0 ? a.h0 + (size_t)u.seq * DN : nullptr;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         h[s][0] = h[s][1] = all2(0.f);
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(kScanThreads + kHelpers, 1) scan_main_kernel(c
     }
     __syncthreads();
     constexpr int TT = L / 2;              // tokens whose sums over the lanes are finished together
-    constexpr int U = 16;                  // tokens between which instructions can be moved: no store before a load
+    constexpr int U = SEG ? 8 : K;                   // tokens between which instructions can be moved: no store before a load
     for (int i = 0; i < n; ++i) {
         const float2(*dt)[CH] = s_dt[i & 1];
         const float(*bc)[K][N] = s_bc[i & 1];
@@ -416,22 +419,25 @@ __global__ void __launch_bounds__(kScanThreads) scan_step_kernel(const __grid_co
 }
 
 template <int N>
-int tiles_of(const ScanArgs& a) {
-    return a.G * ((a.D / a.G + Shape<N>::CH - 1) / Shape<N>::CH);
+unsigned blocks_of(const ScanArgs& a) {
+    return (unsigned)((long long)a.slots * a.G * ((a.D / a.G + Shape<N>::CH - 1) / Shape<N>::CH));
+}
+template <int N, typename T, bool SEG>
+cudaError_t main_typed(const ScanArgs& a) {
+    constexpr size_t smem = MainShape<N>::kSums;
+    const cudaError_t e = allow_smem<scan_main_kernel<N, T, SEG>>(smem);
+    if (e != cudaSuccess) return e;
+    scan_main_kernel<N, T, SEG><<<blocks_of<N>(a), kScanThreads + helpers(SEG), smem, a.stream>>>(a);
+    return cudaGetLastError();
 }
 
 template <int N, typename T>
 cudaError_t fwd_typed(const ScanArgs& a) {
-    const unsigned blocks = (unsigned)((long long)a.slots * tiles_of<N>(a));
-    if (a.seg) {
-        scan_state_kernel<N, T><<<blocks, kScanThreads, 0, a.stream>>>(a);
-        const cudaError_t e = launch_scan_join(a, false);
-        if (e != cudaSuccess) return e;
-    }
-    const cudaError_t e = allow_smem<scan_main_kernel<N, T>>(MainShape<N>::kSums);
-    if (e != cudaSuccess) return e;
-    scan_main_kernel<N, T><<<blocks, kScanThreads + kHelpers, MainShape<N>::kSums, a.stream>>>(a);
-    return cudaGetLastError();
+    if (!a.seg) return main_typed<N, T, false>(a);
+    scan_state_kernel<N, T><<<blocks_of<N>(a), kScanThreads, 0, a.stream>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_scan_join(a, false);
+    return e == cudaSuccess ? main_typed<N, T, true>(a) : e;
 }
 template <int N, typename T>
 cudaError_t step_typed(const ScanStepArgs& a) {
@@ -461,7 +467,7 @@ cudaError_t step_n(const ScanStepArgs& a) { GDN_SCAN_N(step_typed, a) }
 int scan_fwd_segment(long long tokens, int D, int N, int nseq, bool packed) {
     const long long warps = (long long)D * N / 256 * (packed ? 1 : nseq);   // at work at once, in the worst case
     if (warps >= 500) return 0;
-    const long long want = 4 * 608;   // warps
+    const long long want = 8 * 608;   // warps
     const long long per = tokens * std::max(1LL, (long long)D * N / 256) / want;
     const long long seg = std::max(256LL, (per + 63) / 64 * 64);
     return tokens / (packed ? 1 : nseq) <= seg ? 0 : (int)std::min<long long>(seg, 1 << 20);
