@@ -12,6 +12,10 @@
 namespace gdn {
 namespace {
 
+// Threads of a block with two vectors a thread, as many as the registers allow: with more row groups at work on an SM the
+// exchanges of one hide behind the others.
+constexpr int kFwdThreads = 1024, kBwdThreads = 512;
+
 __device__ __forceinline__ void set_up(const RowSmem& s, const float* w, const float* bias, int D, int groups) {
     for (int i = threadIdx.x; i < groups * 128; i += blockDim.x) s.red[i] = 0.f;
     if ((int)threadIdx.x < groups) ring_init(s.bars + threadIdx.x * kRingWords);
@@ -39,7 +43,7 @@ __device__ __forceinline__ void set_up_ring(BulkRing<T, N>& ring, const RowSmem&
 }
 
 template <int V, typename T, bool ADD>
-__global__ void __launch_bounds__(V == 1 ? 1024 : 512, 1)
+__global__ void __launch_bounds__(V == 1 ? 1024 : kFwdThreads, 1)
 layer_norm_fwd_kernel(const __grid_constant__ LayerNormArgs a, int tpr, int stages) {
     constexpr int N = ADD ? 2 : 1;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -112,7 +116,7 @@ layer_norm_fwd_kernel(const __grid_constant__ LayerNormArgs a, int tpr, int stag
 // The sums over the rows stay in registers; a block's groups are added in order in shared memory, part [gridDim.x][2 D]
 // gets the blocks' sums (dw, then dbias), and layer_norm_sums_kernel adds those in order.
 template <int V, typename T, bool ADD, bool RES>
-__global__ void __launch_bounds__(V == 1 ? 1024 : 512, 1)
+__global__ void __launch_bounds__(V == 1 ? 1024 : kBwdThreads, 1)
 layer_norm_bwd_kernel(const __grid_constant__ LayerNormArgs a, float* __restrict__ part, int tpr, int stages) {
     constexpr int N = 2 + ADD + RES, DN = 1 + ADD;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -280,7 +284,7 @@ cudaError_t bwd_v(const LayerNormArgs& a, const RowShape& s, float* part) {
 }
 template <typename T>
 cudaError_t fwd_typed(const LayerNormArgs& a) {
-    const RowShape s = row_shape(a.D, a.rows, (a.b ? 2 : 1) * a.D * value_bytes(a));
+    const RowShape s = row_shape(a.D, a.rows, (a.b ? 2 : 1) * a.D * value_bytes(a), kFwdThreads);
     return s.v == 1 ? fwd_v<1, T>(a, s) : fwd_v<2, T>(a, s);
 }
 template <typename T>
@@ -300,7 +304,7 @@ size_t layer_norm_bwd_workspace_bytes(long long rows, int D) {
 }
 
 cudaError_t launch_layer_norm_bwd(const LayerNormArgs& a) {
-    const RowShape s = row_shape(a.D, a.rows, (2 + (a.b != nullptr) + (a.gr != nullptr)) * a.D * value_bytes(a));
+    const RowShape s = row_shape(a.D, a.rows, (2 + (a.b != nullptr) + (a.gr != nullptr)) * a.D * value_bytes(a), kBwdThreads);
     float* part = a.gw || a.gbias ? static_cast<float*>(a.workspace) : nullptr;
     if (s.blocks) {
         const cudaError_t e = a.dtype == GDN_BF16 ? bwd_typed<__nv_bfloat16>(a, s, part) : bwd_typed<float>(a, s, part);

@@ -378,44 +378,70 @@ __global__ void __launch_bounds__(kScanThreads) scan_join_kernel(const __grid_co
     }
 }
 
-// One token for each of N rows, in place on the states: L lanes a channel, four states each.
+// One token for each of the rows, in place on the states: L lanes a channel, four states each.  A block has a tile of
+// channels and every `splits`-th row; what a row needs is asked for while the one before it is worked on.
+template <typename T>
+struct StepRow {
+    float4 h;
+    Raw4<T> b, c;
+    T u, delta, z;
+    float* at;   // the lane's states, or nullptr
+};
 template <int N, typename T>
-__global__ void __launch_bounds__(kScanThreads) scan_step_kernel(const __grid_constant__ ScanStepArgs a) {
+__global__ void __launch_bounds__(kScanThreads, 8) scan_step_kernel(const __grid_constant__ ScanStepArgs a, int splits) {
     constexpr int L = N / 4, CH = kScanThreads / L;
-    const int tiles = (a.D + CH - 1) / CH, row = blockIdx.x / tiles, d = blockIdx.x % tiles * CH + threadIdx.x / L;
-    const int n4 = threadIdx.x % L * 4;
+    const int tiles = (a.D + CH - 1) / CH, split = blockIdx.x / tiles;
+    const int d = blockIdx.x % tiles * CH + threadIdx.x / L, n4 = threadIdx.x % L * 4;
     const bool own = d < a.D;   // D is a multiple of 8, a warp's channels may not be
-    const int slot = a.slots ? a.slots[row] : row;
-    T* const y = static_cast<T*>(a.y) + (size_t)row * a.D + d;
-    if (slot < 0 || slot >= a.num_slots) {   // a row without a request
-        if (own && n4 == 0) *y = from_f32<T>(0.f);
-        return;
-    }
-    float s = 0.f, u = 0.f;
+    auto slot_of = [&](int row) {   // -1: no such row, or one without a request
+        const int slot = row < a.rows ? a.slots ? a.slots[row] : row : -1;
+        return slot < a.num_slots ? slot : -1;
+    };
+    const size_t g = own ? d / (a.D / a.G) : 0;
+    auto load = [&](int row, int slot) {
+        StepRow<T> x;
+        x.at = own && slot >= 0 ? a.h + ((size_t)slot * a.D + d) * N + n4 : nullptr;
+        if (x.at) {
+            x.h = __ldcs(reinterpret_cast<const float4*>(x.at));
+            x.b = load4(static_cast<const T*>(a.B) + row * a.b_stride + g * N + n4);
+            x.c = load4(static_cast<const T*>(a.C) + row * a.c_stride + g * N + n4);
+            x.u = static_cast<const T*>(a.u)[row * a.u_stride + d];
+            x.delta = static_cast<const T*>(a.delta)[row * a.delta_stride + d];
+            if (a.z) x.z = static_cast<const T*>(a.z)[row * a.z_stride + d];
+        }
+        return x;
+    };
+    StepRow<T> next = load(split, slot_of(split));
+    int slot = slot_of(split + splits);
+    float A[4] = {0.f, 0.f, 0.f, 0.f};
+    const float bias = own && a.dt_bias ? a.dt_bias[d] : 0.f, skip = own && a.skip ? a.skip[d] : 0.f;
     if (own) {
-        float4* const hp = reinterpret_cast<float4*>(a.h + ((size_t)slot * a.D + d) * N + n4);
-        const float4 h = *hp, l = *reinterpret_cast<const float4*>(a.A_log + (size_t)d * N + n4);
-        const int g = d / (a.D / a.G);
-        const float4 b = load4(static_cast<const T*>(a.B) + (size_t)row * a.b_stride + (size_t)g * N + n4).f();
-        const float4 c = load4(static_cast<const T*>(a.C) + (size_t)row * a.c_stride + (size_t)g * N + n4).f();
-        u = to_f32(static_cast<const T*>(a.u)[(size_t)row * a.u_stride + d]);
-        const float raw = to_f32(static_cast<const T*>(a.delta)[(size_t)row * a.delta_stride + d]);
-        const float dt = softplus2(all2(raw + (a.dt_bias ? a.dt_bias[d] : 0.f))).x, w = dt * u;
-        const float4 x = make_float4(
-            fmaf(decay(rate2(l.x), dt), h.x, w * b.x), fmaf(decay(rate2(l.y), dt), h.y, w * b.y),
-            fmaf(decay(rate2(l.z), dt), h.z, w * b.z), fmaf(decay(rate2(l.w), dt), h.w, w * b.w));
-        *hp = x;
-        s = fmaf(x.x, c.x, x.y * c.y) + fmaf(x.z, c.z, x.w * c.w);
+        const float4 l = *reinterpret_cast<const float4*>(a.A_log + (size_t)d * N + n4);
+        A[0] = rate2(l.x); A[1] = rate2(l.y); A[2] = rate2(l.z); A[3] = rate2(l.w);
     }
+    for (int row = split; row < a.rows; row += splits) {
+        const StepRow<T> x = next;
+        next = load(row + splits, slot);
+        slot = slot_of(row + 2 * splits);
+        float s = 0.f;
+        if (x.at) {
+            const float4 b = x.b.f(), c = x.c.f();
+            const float u = to_f32(x.u), dt = softplus2(all2(to_f32(x.delta) + bias)).x, w = dt * u;
+            const float4 h = make_float4(fmaf(decay(A[0], dt), x.h.x, w * b.x), fmaf(decay(A[1], dt), x.h.y, w * b.y),
+                                         fmaf(decay(A[2], dt), x.h.z, w * b.z), fmaf(decay(A[3], dt), x.h.w, w * b.w));
+            __stcs(reinterpret_cast<float4*>(x.at), h);
+            s = fmaf(h.x, c.x, h.y * c.y) + fmaf(h.z, c.z, h.w * c.w);
+            if (n4 == 0) s = fmaf(skip, u, s);
+        }
 #pragma unroll
-    for (int o = L / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (!own || n4) return;
-    if (a.skip) s = fmaf(a.skip[d], u, s);
-    if (a.z) {
-        const float z = to_f32(static_cast<const T*>(a.z)[(size_t)row * a.z_stride + d]);
-        s *= z * logistic_f(z);
+        for (int o = L / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (!own || n4) continue;
+        if (a.z && x.at) {
+            const float z = to_f32(x.z);
+            s *= z * logistic_f(z);
+        }
+        static_cast<T*>(a.y)[(size_t)row * a.D + d] = from_f32<T>(s);
     }
-    *y = from_f32<T>(s);
 }
 
 template <int N>
@@ -439,10 +465,13 @@ cudaError_t fwd_typed(const ScanArgs& a) {
     if (e == cudaSuccess) e = launch_scan_join(a, false);
     return e == cudaSuccess ? main_typed<N, T, true>(a) : e;
 }
+// Rows are split over eight blocks for each of the 152 SMs (what fits), each block with a few of them where there are more.
 template <int N, typename T>
 cudaError_t step_typed(const ScanStepArgs& a) {
     constexpr int CH = kScanThreads / (N / 4);
-    scan_step_kernel<N, T><<<(unsigned)((long long)a.rows * ((a.D + CH - 1) / CH)), kScanThreads, 0, a.stream>>>(a);
+    const long long tiles = (a.D + CH - 1) / CH;
+    const int splits = (int)std::min<long long>(a.rows, std::max(1LL, 8 * 152 / tiles));
+    scan_step_kernel<N, T><<<(unsigned)(tiles * splits), kScanThreads, 0, a.stream>>>(a, splits);
     return cudaGetLastError();
 }
 

@@ -130,12 +130,12 @@ struct RowShape {
     int v, tpr, groups, stages, blocks;
     size_t smem;
 };
-inline RowShape row_shape(int D, long long rows, int row_bytes) {
+inline RowShape row_shape(int D, long long rows, int row_bytes, int threads2 = 512) {   // threads2: with two vectors a thread
     const int nv = D / kVec;
     RowShape s;
     s.v = nv <= 32 || (nv <= 512 && rows <= 152) ? 1 : 2;
     s.tpr = ((nv + s.v - 1) / s.v + 31) / 32 * 32;
-    s.groups = std::max(1, (s.v == 1 ? 1024 : 512) / s.tpr);
+    s.groups = std::max(1, (s.v == 1 ? 1024 : threads2) / s.tpr);
     if (s.tpr > 32) s.groups = std::min(s.groups, 8);
     s.groups = (int)std::min<long long>(s.groups, std::max(1LL, (rows + 151) / 152));   // few rows: every SM has some
     while (s.groups > 1 && smem_bytes(s.groups, D, row_bytes, 2) > kSmemMax) --s.groups;
