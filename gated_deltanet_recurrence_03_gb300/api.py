@@ -792,62 +792,63 @@ def gdn_block_norm_bwd(x: torch.Tensor, b: torch.Tensor, post_weight: torch.Tens
 
 
 def _row_stride(name, t, lead, width):
-    """Elements between consecutive token rows of t ([*lead, ...], the dimensions behind ``lead`` contiguous and
-    ``width`` values in all): a dense tensor or a slice of a packed projection."""
+    """Elements between consecutive token rows of t ([*lead, values] or [*lead, groups, values], contiguous behind
+    ``lead``, ``width`` values in all): a dense tensor or a slice of a packed projection."""
     shape, stride = t.shape, t.stride()
-    if lead == 1:
-        row, even = (stride[0] if shape[0] > 1 else width), True
-    else:
-        row = stride[1] if shape[1] > 1 else stride[0] if shape[0] > 1 else width
-        even = shape[0] <= 1 or stride[0] == shape[1] * row
-    inner = 1
-    for n, s in zip(reversed(shape[lead:]), reversed(stride[lead:])):
-        even = even and (n == 1 or s == inner)
-        inner *= n
-    if even and row >= width:
+    row = stride[lead - 1] if shape[lead - 1] > 1 else stride[0] if lead == 2 and shape[0] > 1 else width
+    even = lead == 1 or shape[0] <= 1 or stride[0] == shape[1] * row
+    inner = stride[-1] == 1 or shape[-1] == 1
+    if len(shape) > lead + 1:
+        inner = inner and (shape[lead] == 1 or stride[lead] == shape[lead + 1])
+    if even and inner and row >= width:
         return row
     if t.numel():
         raise ValueError(f"{name} must have contiguous rows, evenly strided and of their own memory")
     return width
 
 
-def _token_tensor(name, t, dt, dev, shape, lead):
+def _token_tensor(name, t, dt, dev, shape, lead, width):
     """Checks t and returns its row stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if t.dtype is not dt or t.device != dev or t.shape != shape:
+    if t.dtype is not dt or t.shape != shape or t.device != dev:
         raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}, expected {dt} {tuple(shape)} on {dev}")
-    width = 1
-    for n in shape[lead:]:
-        width *= n
-    return _row_stride(name, t, lead, width)
+    return width if t.is_contiguous() else _row_stride(name, t, lead, width)
 
 
 def _scan_inputs(u, delta, A_log, B, C, skip, dt_bias, z, lead):
     """Sizes of the selective scan's inputs, and the arguments that its entry points begin with."""
     if not isinstance(u, torch.Tensor) or not isinstance(B, torch.Tensor) or not isinstance(A_log, torch.Tensor):
         raise TypeError("u, A_log and B must be tensors")
-    dims = "B, T" if lead == 2 else "N"
-    if u.dim() != lead + 1:
-        raise ValueError(f"u must be {lead + 1}-D [{dims}, D]")
-    if B.dim() != lead + 2:
-        raise ValueError(f"B must be {lead + 2}-D [{dims}, G, N]")
-    if A_log.dim() != 2:
-        raise ValueError("A_log must be 2-D [D, N]")
-    dev, dt, us = u.device, u.dtype, u.shape
+    us, bs, As = u.shape, B.shape, A_log.shape
+    if len(us) != lead + 1 or len(bs) != lead + 2 or len(As) != 2:
+        dims = "B, T" if lead == 2 else "N"
+        raise ValueError(f"u must be [{dims}, D], B and C [{dims}, G, N], A_log [D, N]; they are {tuple(us)}, {tuple(bs)}, "
+                         f"{tuple(As)}")
+    dev, dt = u.device, u.dtype
     if dt not in _DTYPES:
         raise ValueError(f"unsupported dtype {dt}")
-    D, G, N = us[lead], B.shape[lead], A_log.shape[1]
-    bs = us[:lead] + (G, N)
+    D, G, N = us[lead], bs[lead], As[1]
+    if bs[:lead] != us[:lead] or bs[lead + 1] != N:
+        raise ValueError(f"B has shape {tuple(bs)}, expected {tuple(us[:lead]) + (G, N)}")
     _need("A_log", A_log, torch.float32, dev, (D, N))
-    for name, t in (("skip", skip), ("dt_bias", dt_bias)):
-        if t is not None:
-            _need(name, t, torch.float32, dev, (D,))
-    rows = [_token_tensor(name, t, dt, dev, shape, lead)
-            for name, t, shape in (("u", u, us), ("delta", delta, us), ("B", B, bs), ("C", C, bs))]
-    z_row = 0 if z is None else _token_tensor("z", z, dt, dev, us, lead)
-    return dev, dt, D, G, N, (_ptr(u), rows[0], _ptr(delta), rows[1], _ptr(A_log), _ptr(B), rows[2], _ptr(C), rows[3],
-                              _ptr(skip), _ptr(dt_bias), _ptr(z), z_row)
+    if skip is not None:
+        _need("skip", skip, torch.float32, dev, (D,))
+    if dt_bias is not None:
+        _need("dt_bias", dt_bias, torch.float32, dev, (D,))
+    GN = G * N
+    return dev, dt, D, G, N, (
+        u.data_ptr(), _token_tensor("u", u, dt, dev, us, lead, D),
+        _pointer("delta", delta), _token_tensor("delta", delta, dt, dev, us, lead, D), A_log.data_ptr(),
+        B.data_ptr(), _token_tensor("B", B, dt, dev, bs, lead, GN),
+        _pointer("C", C), _token_tensor("C", C, dt, dev, bs, lead, GN), _ptr(skip), _ptr(dt_bias),
+        None if z is None else _pointer("z", z), 0 if z is None else _token_tensor("z", z, dt, dev, us, lead, D))
+
+
+def _pointer(name, t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    return t.data_ptr()
 
 
 def gdn_selective_scan_fwd(u: torch.Tensor, delta: torch.Tensor, A_log: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
@@ -937,9 +938,9 @@ def gdn_selective_scan_bwd(u: torch.Tensor, delta: torch.Tensor, A_log: torch.Te
         gB, gC, gz = grads
         if (gz is None) != (z is None):
             raise ValueError("grad_z goes with z")
-        gb_stride = _token_tensor("grad_B", gB, dt, dev, B.shape, 2)
-        gc_stride = _token_tensor("grad_C", gC, dt, dev, B.shape, 2)
-        gz_stride = 0 if gz is None else _token_tensor("grad_z", gz, dt, dev, u.shape, 2)
+        gb_stride = _token_tensor("grad_B", gB, dt, dev, B.shape, 2, G * N)
+        gc_stride = _token_tensor("grad_C", gC, dt, dev, B.shape, 2, G * N)
+        gz_stride = 0 if gz is None else _token_tensor("grad_z", gz, dt, dev, u.shape, 2, D)
         o, keep = _call_opts(lib, dt, 1.0, stream, dev, events)
         nseq = _packed(o, cu_seqlens, nB, dev)
         for name, t in (("h0", h0), ("grad_h_final", grad_h_final)):

@@ -135,15 +135,17 @@ layer_norm_bwd_kernel(const __grid_constant__ LayerNormArgs a, float* __restrict
     const long long step = (long long)gridDim.x * groups, first = (long long)blockIdx.x * groups + g.id;
     if (g.tid == 0)
         for (int k = 0; k < stages && first + k * step < a.rows; ++k) ring.issue(k, first + k * step);
-    V8 gw[V], gb[V];
+    V8 gw[V], gb[V], w[V];   // the thread's columns are the same in every row
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i) {
+        if (g.tid + i * tpr < nv) w[i] = load8(sm.m + (g.tid + i * tpr) * kVec);
 #pragma unroll
         for (int e = 0; e < 4; ++e) gw[i].v[e] = gb[i].v[e] = make_float2(0.f, 0.f);
+    }
     int k = 0;
     for (long long row = first; row < a.rows; row += step, ++k) {
         const bool go = ring.wait(k);
-        V8 r[V];
+        V8 r[V], dn[V];
         float2 q = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -171,12 +173,12 @@ layer_norm_bwd_kernel(const __grid_constant__ LayerNormArgs a, float* __restrict
         for (int i = 0; i < V; ++i) {
             const int c = g.tid + i * tpr;
             if (c < nv) {
-                const V8 dn = load8(ring.at(k, DN) + c * kVec), w = load8(sm.m + c * kVec);
+                dn[i] = load8(ring.at(k, DN) + c * kVec);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     r[i].v[e] = add2(r[i].v[e], m);
                     q = fma2(r[i].v[e], r[i].v[e], q);
-                    const float2 h = mul2(dn.v[e], w.v[e]);
+                    const float2 h = mul2(dn[i].v[e], w[i].v[e]);
                     qh = add2(qh, h);
                     qr = fma2(h, r[i].v[e], qr);
                 }
@@ -191,15 +193,14 @@ layer_norm_bwd_kernel(const __grid_constant__ LayerNormArgs a, float* __restrict
         for (int i = 0; i < V; ++i) {
             const int c = g.tid + i * tpr;
             if (c < nv) {
-                const V8 dn = load8(ring.at(k, DN) + c * kVec), w = load8(sm.m + c * kVec);
                 V8 dx;
                 if constexpr (RES) dx = load8(ring.at(k, DN + 1) + c * kVec);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 rh = mul2(r[i].v[e], all2(inv));
-                    gw[i].v[e] = fma2(dn.v[e], rh, gw[i].v[e]);
-                    gb[i].v[e] = add2(dn.v[e], gb[i].v[e]);
-                    const float2 t = fma2(rh, mr, fma2(dn.v[e], w.v[e], mh));
+                    gw[i].v[e] = fma2(dn[i].v[e], rh, gw[i].v[e]);
+                    gb[i].v[e] = add2(dn[i].v[e], gb[i].v[e]);
+                    const float2 t = fma2(rh, mr, fma2(dn[i].v[e], w[i].v[e], mh));
                     dx.v[e] = RES ? fma2(all2(inv), t, dx.v[e]) : mul2(all2(inv), t);
                 }
                 store8(static_cast<T*>(a.gx) + base + c * kVec, dx);
