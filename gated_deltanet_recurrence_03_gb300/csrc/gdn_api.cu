@@ -925,12 +925,14 @@ bool scan_dims_ok(int D, int G, int N) {
     return D > 0 && G > 0 && D % (8LL * G) == 0 && (N == 8 || N == 16 || N == 32 || N == 64);
 }
 
-// A row stride of 0 is the dense one; rows hold their values and stay 16-byte aligned.
+// A row stride of 0 is the dense one; rows hold their values and stay 16-byte aligned, and what a kernel steps over at once
+// (up to 64 rows) stays within 32 bits.
+constexpr long long kMaxScanStride = 1 << 24;
 gdn_status_t check_stride(const char* name, long long* stride, long long width, int dtype) {
     if (*stride == 0) *stride = width;
     const int per16 = dtype == GDN_BF16 ? 8 : 4;
-    if (*stride < width || *stride % per16 != 0 || *stride > INT32_MAX)
-        return fail(GDN_ERR_INVALID_ARG, "%s stride %lld must be >= %lld, a multiple of %d and below 2^31", name, *stride,
+    if (*stride < width || *stride % per16 != 0 || *stride > kMaxScanStride)
+        return fail(GDN_ERR_INVALID_ARG, "%s stride %lld must be >= %lld, a multiple of %d and at most 2^24", name, *stride,
                     width, per16);
     return GDN_OK;
 }
@@ -1040,7 +1042,7 @@ gdn_status_t gdn_selective_scan_step(const void* u, long long u_stride, const vo
     if (!slots && num_slots < rows) return fail(GDN_ERR_INVALID_ARG, "%d states for %d rows without slots", num_slots, rows);
     if (rows == 0) return GDN_OK;
     if (!u || !delta || !A_log || !Bm || !Cm || (!h && num_slots > 0) || !y) return fail(GDN_ERR_INVALID_ARG, "null pointer");
-    if ((long long)rows * ((long long)D * N / 512 + 1) > kMaxBlocks)
+    if ((long long)rows * ((long long)D * N / 512 + 1) > kMaxBlocks / 2)
         return fail(GDN_ERR_INVALID_ARG, "rows=%d of %d channels are too many", rows, D);
     if ((st = need_aligned16({u, delta, A_log, Bm, Cm, skip, dt_bias, z, h, y})) != GDN_OK) return st;
     if (slots && !aligned_to(slots, 4)) return fail(GDN_ERR_INVALID_ARG, "slots is not 4-byte aligned");

@@ -307,7 +307,7 @@ struct ScanArgs {
     cudaStream_t stream;
 };
 constexpr int kScanChunk = 8;         // tokens that the gradients walk at a time
-constexpr int kScanMinSegment = 64;   // tokens of their segments: a multiple of this
+constexpr int kScanMinSegment = 32;   // tokens of their segments: a multiple of this
 struct ScanFwdLayout {
     int seg;
     long long slots;

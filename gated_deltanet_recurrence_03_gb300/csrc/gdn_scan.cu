@@ -48,7 +48,7 @@ struct Rows {
 template <typename T>
 struct Walk {
     const T* p;       // the thread's first vector of the tile, or nullptr
-    int step;         // elements between its vectors
+    int step;         // elements between its vectors (a row stride is at most 2^24)
 };
 template <int CH, int M, typename T>
 __device__ __forceinline__ Walk<T> walk_of(Rows src, int d0, long long t0, int channels, int tid) {

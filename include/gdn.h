@@ -442,7 +442,7 @@ gdn_status_t gdn_block_norm_bwd(const void* x, const void* b, const void* gate, 
  *   u, delta, z  [B, T, D] dtype, token rows u_stride / delta_stride / z_stride elements apart (0 = dense: D); z may be
  *                NULL (no gate).  u is what gdn_causal_conv1d_fwd writes
  *   Bm, Cm       [B, T, G, N] dtype, rows b_stride / c_stride apart (0 = G N).  Slices of one packed projection can be
- *                passed directly; strides are multiples of 16 bytes
+ *                passed directly; strides are multiples of 16 bytes and at most 2^24 elements
  *   A_log        [D, N] float;  skip, dt_bias [D] float, each may be NULL (0)
  *   h0           [nseq, D, N] float or NULL (zero states); nseq = B, or num_seqs when packed
  *   y            [B, T, D] dtype, dense; must not overlap any input
