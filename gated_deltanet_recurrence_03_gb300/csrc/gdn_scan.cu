@@ -378,20 +378,22 @@ __global__ void __launch_bounds__(kScanThreads) scan_join_kernel(const __grid_co
     }
 }
 
-// One token for each of the rows, in place on the states: L lanes a channel, four states each.  A block has a tile of
-// channels and every `splits`-th row; what a row needs is asked for while the one before it is worked on.
+// One token for each of the rows, in place on the states: eight states a lane, so that the functions of dt and of the gate,
+// which the L lanes of a channel all form, weigh little.  A block has a tile of channels and every `splits`-th row; what a
+// row needs is asked for while the one before it is worked on.
 template <typename T>
 struct StepRow {
-    float4 h;
-    Raw4<T> b, c;
+    float4 h[2];
+    Raw4<T> b[2], c[2];
     T u, delta, z;
     float* at;   // the lane's states, or nullptr
 };
+constexpr int kStepStates = 8, kStepBlocks = 6;   // states a lane, blocks an SM
 template <int N, typename T>
-__global__ void __launch_bounds__(kScanThreads, 8) scan_step_kernel(const __grid_constant__ ScanStepArgs a, int splits) {
-    constexpr int L = N / 4, CH = kScanThreads / L;
+__global__ void __launch_bounds__(kScanThreads, kStepBlocks) scan_step_kernel(const __grid_constant__ ScanStepArgs a, int splits) {
+    constexpr int L = N / kStepStates, CH = kScanThreads / L;
     const int tiles = (a.D + CH - 1) / CH, split = blockIdx.x / tiles;
-    const int d = blockIdx.x % tiles * CH + threadIdx.x / L, n4 = threadIdx.x % L * 4;
+    const int d = blockIdx.x % tiles * CH + threadIdx.x / L, n0 = threadIdx.x % L * kStepStates;
     const bool own = d < a.D;   // D is a multiple of 8, a warp's channels may not be
     auto slot_of = [&](int row) {   // -1: no such row, or one without a request
         const int slot = row < a.rows ? a.slots ? a.slots[row] : row : -1;
@@ -400,11 +402,16 @@ __global__ void __launch_bounds__(kScanThreads, 8) scan_step_kernel(const __grid
     const size_t g = own ? d / (a.D / a.G) : 0;
     auto load = [&](int row, int slot) {
         StepRow<T> x;
-        x.at = own && slot >= 0 ? a.h + ((size_t)slot * a.D + d) * N + n4 : nullptr;
+        x.at = own && slot >= 0 ? a.h + ((size_t)slot * a.D + d) * N + n0 : nullptr;
         if (x.at) {
-            x.h = __ldcs(reinterpret_cast<const float4*>(x.at));
-            x.b = load4(static_cast<const T*>(a.B) + row * a.b_stride + g * N + n4);
-            x.c = load4(static_cast<const T*>(a.C) + row * a.c_stride + g * N + n4);
+            const T* b = static_cast<const T*>(a.B) + row * a.b_stride + g * N + n0;
+            const T* c = static_cast<const T*>(a.C) + row * a.c_stride + g * N + n0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                x.h[i] = __ldcs(reinterpret_cast<const float4*>(x.at) + i);
+                x.b[i] = load4(b + 4 * i);
+                x.c[i] = load4(c + 4 * i);
+            }
             x.u = static_cast<const T*>(a.u)[row * a.u_stride + d];
             x.delta = static_cast<const T*>(a.delta)[row * a.delta_stride + d];
             if (a.z) x.z = static_cast<const T*>(a.z)[row * a.z_stride + d];
@@ -413,11 +420,15 @@ __global__ void __launch_bounds__(kScanThreads, 8) scan_step_kernel(const __grid
     };
     StepRow<T> next = load(split, slot_of(split));
     int slot = slot_of(split + splits);
-    float A[4] = {0.f, 0.f, 0.f, 0.f};
+    float2 A[4];
     const float bias = own && a.dt_bias ? a.dt_bias[d] : 0.f, skip = own && a.skip ? a.skip[d] : 0.f;
-    if (own) {
-        const float4 l = *reinterpret_cast<const float4*>(a.A_log + (size_t)d * N + n4);
-        A[0] = rate2(l.x); A[1] = rate2(l.y); A[2] = rate2(l.z); A[3] = rate2(l.w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        A[i] = all2(0.f);
+        if (own) {
+            const float2 l = *reinterpret_cast<const float2*>(a.A_log + (size_t)d * N + n0 + 2 * i);
+            A[i] = make_float2(rate2(l.x), rate2(l.y));
+        }
     }
     for (int row = split; row < a.rows; row += splits) {
         const StepRow<T> x = next;
@@ -425,17 +436,22 @@ __global__ void __launch_bounds__(kScanThreads, 8) scan_step_kernel(const __grid
         slot = slot_of(row + 2 * splits);
         float s = 0.f;
         if (x.at) {
-            const float4 b = x.b.f(), c = x.c.f();
             const float u = to_f32(x.u), dt = softplus2(all2(to_f32(x.delta) + bias)).x, w = dt * u;
-            const float4 h = make_float4(fmaf(decay(A[0], dt), x.h.x, w * b.x), fmaf(decay(A[1], dt), x.h.y, w * b.y),
-                                         fmaf(decay(A[2], dt), x.h.z, w * b.z), fmaf(decay(A[3], dt), x.h.w, w * b.w));
-            __stcs(reinterpret_cast<float4*>(x.at), h);
-            s = fmaf(h.x, c.x, h.y * c.y) + fmaf(h.z, c.z, h.w * c.w);
-            if (n4 == 0) s = fmaf(skip, u, s);
+            float2 y = all2(0.f);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float4 b = x.b[i].f(), c = x.c[i].f();
+                const float2 p = fma2(decay(A[2 * i], dt), make_float2(x.h[i].x, x.h[i].y), mul2(make_float2(b.x, b.y), all2(w)));
+                const float2 q = fma2(decay(A[2 * i + 1], dt), make_float2(x.h[i].z, x.h[i].w), mul2(make_float2(b.z, b.w), all2(w)));
+                __stcs(reinterpret_cast<float4*>(x.at) + i, make_float4(p.x, p.y, q.x, q.y));
+                y = fma2(p, make_float2(c.x, c.y), fma2(q, make_float2(c.z, c.w), y));
+            }
+            s = y.x + y.y;
+            if (n0 == 0) s = fmaf(skip, u, s);
         }
 #pragma unroll
         for (int o = L / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (!own || n4) continue;
+        if (!own || n0) continue;
         if (a.z && x.at) {
             const float z = to_f32(x.z);
             s *= z * logistic_f(z);
@@ -465,12 +481,12 @@ cudaError_t fwd_typed(const ScanArgs& a) {
     if (e == cudaSuccess) e = launch_scan_join(a, false);
     return e == cudaSuccess ? main_typed<N, T, true>(a) : e;
 }
-// Rows are split over eight blocks for each of the 152 SMs (what fits), each block with a few of them where there are more.
+// Rows are split over the blocks that fit the 152 SMs, each with a few of them where there are more.
 template <int N, typename T>
 cudaError_t step_typed(const ScanStepArgs& a) {
-    constexpr int CH = kScanThreads / (N / 4);
+    constexpr int CH = kScanThreads / (N / kStepStates);
     const long long tiles = (a.D + CH - 1) / CH;
-    const int splits = (int)std::min<long long>(a.rows, std::max(1LL, 8 * 152 / tiles));
+    const int splits = (int)std::min<long long>(a.rows, std::max(1LL, kStepBlocks * 152 / tiles));
     scan_step_kernel<N, T><<<(unsigned)(tiles * splits), kScanThreads, 0, a.stream>>>(a, splits);
     return cudaGetLastError();
 }
