@@ -3,9 +3,11 @@
 //     n = rh w + bias,
 // and its gradients for dr, dn (inv = 1 / sqrt(v + eps)):
 //     h = dn w,  dx = db = dr + inv (h - mean(h) - rh mean(h rh)),  dw = sum dn rh,  dbias = sum dn (over the rows).
-// n is formed from r before its rounding, and the gradients from r formed again from x and b.  The variance is the mean
-// of squares around the mean, whose sum is taken first: a row far from zero loses nothing.
+// n is formed from r before its rounding, and the gradients from r formed again from x and b.
 //
+// A row far from zero loses nothing.  Forward, every warp takes the mean m_w of its n_w values first and sums around that,
+// and the warps' sums, exchanged once, join exactly: m = sum n_w m_w / D, sum (r - m)^2 = sum [M_w + n_w (m_w - m)^2].
+// Backward the row's mean is exchanged before the other three sums.
 // Rows pass through the ring of the block norm (norm_rows.cuh) and are held in registers between the sums.
 #include "norm_rows.cuh"
 
@@ -14,7 +16,7 @@ namespace {
 
 // Threads of a block with two vectors a thread, as many as the registers allow: with more row groups at work on an SM the
 // exchanges of one hide behind the others.
-constexpr int kFwdThreads = 1024, kBwdThreads = 512;
+constexpr int kFwdThreads = 768, kBwdThreads = 512;
 
 __device__ __forceinline__ void set_up(const RowSmem& s, const float* w, const float* bias, int D, int groups) {
     for (int i = threadIdx.x; i < groups * 128; i += blockDim.x) s.red[i] = 0.f;
@@ -26,6 +28,22 @@ __device__ __forceinline__ void set_up(const RowSmem& s, const float* w, const f
         s.wq[c] = bias ? bias[c] : 0.f;
     }
     __syncthreads();
+}
+
+constexpr int kWarps = 16;   // of a row group at most
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+// What the warps of a row group hold: `count` [kWarps] (n_w, zero past the group's warps), shared by the block.
+__device__ __forceinline__ float set_up_counts(float* count, const Group& g, int nv, int V) {
+    int n = 0;
+    for (int i = 0; i < V; ++i) n += min(max(nv - i * g.tpr - (g.tid & ~31), 0), 32) * kVec;
+    if (g.id == 0 && (g.tid & 31) == 0) count[g.tid >> 5] = (float)n;
+    if (g.id == 0 && g.tid < kWarps && g.tid >= g.tpr >> 5) count[g.tid] = 0.f;
+    __syncthreads();
+    return (float)n;
 }
 
 // The group's ring: x, [b], then the backward's dn, [dr].
@@ -53,6 +71,9 @@ layer_norm_fwd_kernel(const __grid_constant__ LayerNormArgs a, int tpr, int stag
     set_up(sm, a.w, a.bias, a.D, groups);
     float* const red = sm.red + g.id * 128;
     const float invD = 1.f / (float)a.D;
+    float* const count = sm.red + 64;   // of group 0: the exchanges take 64 floats of a group's 128
+    const float n_w = set_up_counts(count, g, nv, V), inv_w = n_w > 0.f ? 1.f / n_w : 0.f;
+    const int nw = tpr >> 5;
     BulkRing<T, N> ring;
     ring.src[0] = a.x;
     if constexpr (ADD) ring.src[1] = a.b;
@@ -81,23 +102,42 @@ layer_norm_fwd_kernel(const __grid_constant__ LayerNormArgs a, int tpr, int stag
                 for (int e = 0; e < 4; ++e) q = add2(q, r[i].v[e]);
             }
         }
-        float sum[1] = {q.x + q.y};
-        group_sum(sum, red, g);
-        // past this every thread of the group has read this row: its stage is free
-        if (g.tid == 0 && go && row + stages * step < a.rows) ring.issue(k + stages, row + stages * step);
-        const float2 m = all2(-sum[0] * invD);
+        float mean = warp_sum(q.x + q.y) * inv_w;
         q = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < V; ++i)
             if (g.tid + i * tpr < nv)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    r[i].v[e] = add2(r[i].v[e], m);
-                    q = fma2(r[i].v[e], r[i].v[e], q);
+                    const float2 d = add2(r[i].v[e], all2(-mean));
+                    q = fma2(d, d, q);
                 }
-        sum[0] = q.x + q.y;
-        group_sum(sum, red + 64, g);
-        const float inv = rsqrtf(fmaf(sum[0], invD, a.eps));
+        float m2 = warp_sum(q.x + q.y);
+        if (nw > 1) {
+            float* const buf = red + (k & 1) * 2 * kWarps;   // m_w, M_w; the other one may still be read
+            if ((g.tid & 31) == 0) {
+                buf[g.tid >> 5] = mean;
+                buf[kWarps + (g.tid >> 5)] = m2;
+            }
+            group_sync(g);
+            mean = m2 = 0.f;
+            for (int w = 0; w < nw; w += 4) {
+                const float4 n = *reinterpret_cast<const float4*>(count + w), m = *reinterpret_cast<const float4*>(buf + w);
+                mean += fmaf(n.x, m.x, n.y * m.y) + fmaf(n.z, m.z, n.w * m.w);
+            }
+            mean *= invD;
+            for (int w = 0; w < nw; w += 4) {
+                const float4 n = *reinterpret_cast<const float4*>(count + w), m = *reinterpret_cast<const float4*>(buf + w);
+                const float4 q4 = *reinterpret_cast<const float4*>(buf + kWarps + w);
+                const float dx = m.x - mean, dy = m.y - mean, dz = m.z - mean, dw = m.w - mean;
+                m2 += (fmaf(n.x * dx, dx, q4.x) + fmaf(n.y * dy, dy, q4.y)) + (fmaf(n.z * dz, dz, q4.z) + fmaf(n.w * dw, dw, q4.w));
+            }
+        } else {
+            __syncwarp();
+        }
+        // past this every thread of the group has read this row: its stage is free
+        if (g.tid == 0 && go && row + stages * step < a.rows) ring.issue(k + stages, row + stages * step);
+        const float inv = rsqrtf(fmaf(m2, invD, a.eps));
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = g.tid + i * tpr;
@@ -105,7 +145,8 @@ layer_norm_fwd_kernel(const __grid_constant__ LayerNormArgs a, int tpr, int stag
                 const V8 w = load8(sm.m + c * kVec);
                 V8 y = load8(sm.wq + c * kVec);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y.v[e] = fma2(mul2(r[i].v[e], all2(inv)), w.v[e], y.v[e]);
+                for (int e = 0; e < 4; ++e)
+                    y.v[e] = fma2(mul2(add2(r[i].v[e], all2(-mean)), all2(inv)), w.v[e], y.v[e]);
                 store8(static_cast<T*>(a.n) + base + c * kVec, y);
             }
         }
