@@ -306,13 +306,15 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
         }
     };
 
-    if (chunks > 0) ask(0, (chunks - 1) * K);
-    for (int c = chunks - 1; c >= 0; --c) {
-        const int t = c * K, tokens = min(K, len - t), st = (chunks - 1 - c) & 1;
-        float cum[2] = {0.f, 0.f};   // dt up to the chunk
+    float cum[2] = {0.f, 0.f};   // dt up to the chunk
+    auto ask_cum = [&](int c) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (c > 0 && l.ch[s] < tile.n) cum[s] = a.chunk_dt[((size_t)slot * (a.seg / K) + c) * a.D + channel(s)];
+            cum[s] = c > 0 && l.ch[s] < tile.n ? a.chunk_dt[((size_t)slot * (a.seg / K) + c) * a.D + channel(s)] : 0.f;
+    };
+    if (chunks > 0) ask(0, (chunks - 1) * K), ask_cum(chunks - 1);
+    for (int c = chunks - 1; c >= 0; --c) {
+        const int t = c * K, tokens = min(K, len - t), st = (chunks - 1 - c) & 1;
         copies_done();
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
@@ -339,7 +341,7 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
             for (int i = 0; i < 2; ++i) before[s][i] = fma2(decay(A2[s][i], cum[s]), f[i], x[i]);
         }
         __syncthreads();
-        if (c > 0) ask(st ^ 1, t - K);
+        if (c > 0) ask(st ^ 1, t - K), ask_cum(c - 1);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             float2 B[2];
