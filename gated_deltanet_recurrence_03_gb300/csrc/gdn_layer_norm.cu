@@ -9,13 +9,18 @@
 // and the warps' sums, exchanged once, join exactly: m = sum n_w m_w / D, sum (r - m)^2 = sum [M_w + n_w (m_w - m)^2].
 // Backward the row's mean is exchanged before the other three sums.
 // Rows pass through the ring of the block norm (norm_rows.cuh) and are held in registers between the sums.
+//
+// 16,384 rows of 4096 bf16 values with the residual: forward 94.6 us, 0.84 of the measured copy bandwidth (two exchanges a
+// row 101.3, and two row groups an SM 104.5 us); gradients 132.7 us, 0.74 of it, HBM 58 %, issue slots 45 % of their rates:
+// each row's two exchanges with only two row groups of 128 registers a thread on an SM.  One exchange of four sums: 144 us
+// (more instructions); three groups, registers spilled: the same as two.
 #include "norm_rows.cuh"
 
 namespace gdn {
 namespace {
 
-// Threads of a block with two vectors a thread, as many as the registers allow: with more row groups at work on an SM the
-// exchanges of one hide behind the others.
+// Threads of a block with two vectors a thread: with more row groups at work on an SM the exchanges of one hide behind the
+// others (16384 x 4096 forward: 512 threads 98.9, 768 94.6, 1024 102.8 us, where registers spill; gradients 512).
 constexpr int kFwdThreads = 768, kBwdThreads = 512;
 
 __device__ __forceinline__ void set_up(const RowSmem& s, const float* w, const float* bias, int D, int groups) {

@@ -3,7 +3,13 @@
 //     h_t = exp(dt_t A) h_{t-1} + dt_t u_t B_t,      y_t = (sum_n C_t h_t + skip u_t) silu(z_t).
 //
 // Per tile of K tokens a block forms dt and dt u of its channels and B, C in fp32 in shared memory, walks the tile with the
-// states in registers, and applies skip and gate to the sums.
+// states in registers, and applies skip and gate to the sums.  A state and token costs one exponential, 2 fp32 pairs of
+// operations and its share of the tile's reads; those, not HBM, bound the prompt: 2 x 8192 tokens of 4096 channels of 16
+// states, bf16, 357 us, where HBM would take 79 and the exponentials alone (32 a clock and SM, measured) 115 us.  What is
+// left: 512 warps of two channels a lane are all there are, one for each scheduler of 128 SMs, and a warp of its own runs
+// at 45 % of what its pipes take (74 cycles a token against 33 instructions); the helpers' instructions come on top.  From
+// 798 us: dt by a packed polynomial and helpers apart from the walk 516, two channels a lane 409, registers for 16 tokens
+// 373, for 32 tokens 357.  One channel a lane, twice the warps: 391 us, shared-memory reads.
 #include <algorithm>
 
 #include "norm_rows.cuh"
@@ -12,32 +18,10 @@
 namespace gdn {
 namespace {
 
-// A lane holds two channels of four states each; the L lanes of a channel pair are 32 / L lanes apart (adjacent lanes then
-// read the same B and C, half the shared-memory cycles of L adjacent lanes with L addresses).
-template <int N>
-struct Shape {
-    static constexpr int L = N / 4, CH = 2 * kScanThreads / L, kPairs = 32 / L;
-};
-struct Lane {
-    int n4, pair, swap;   // first state, channel pair in the warp, whether the pair's channels are held in the other order
-    int ch[2];            // channels in the tile
-};
-template <int N>
-__device__ __forceinline__ Lane lane_of(int tid) {
-    constexpr int P = Shape<N>::kPairs;
-    Lane l;
-    l.pair = tid % P;
-    l.n4 = tid % 32 / P * 4;
-    l.swap = tid / P & 1;
-    l.ch[0] = tid / 32 * 2 * P + 2 * l.pair + l.swap;
-    l.ch[1] = l.ch[0] ^ 1;
-    return l;
-}
-
 // Per-thread shares of a tile of K tokens by CH channels among M threads: 4-channel vectors, and 4-state vectors of B and C.
 template <int N, int K, int M>
 struct Share {
-    static constexpr int kVecs = (K * Shape<N>::CH / 4 + M - 1) / M, kBC = (2 * K * N / 4 + M - 1) / M;
+    static constexpr int kVecs = (K * ScanShape<N>::CH / 4 + M - 1) / M, kBC = (2 * K * N / 4 + M - 1) / M;
 };
 struct Rows {
     const void* p;
@@ -74,18 +58,13 @@ __device__ __forceinline__ void load_bc(Raw4<T> (&x)[V], Rows B, Rows C, int g, 
     }
 }
 template <int K, int CH, int M, typename T, int V>
-__device__ __forceinline__ void form_dt(float2 (&to)[K][CH], const Raw4<T> (&u)[V], const Raw4<T> (&delta)[V], float4 bias,
-                                        int tokens, int channels, int tid) {
+__device__ __forceinline__ void form_tile_dt(float2 (&to)[K][CH], const Raw4<T> (&u)[V], const Raw4<T> (&delta)[V], float4 bias,
+                                             int tokens, int channels, int tid) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int i = tid + v * M, k = i / (CH / 4), c = i % (CH / 4) * 4;
         if (k >= K) break;
-        const float4 x = u[v].f();
-        float4 d = softplus4(add4(delta[v].f(), bias));
-        if (k >= tokens || c >= channels) d = make_float4(0.f, 0.f, 0.f, 0.f);   // past the end: the state stays as it is
-        float4* p = reinterpret_cast<float4*>(&to[k][c]);
-        p[0] = make_float4(d.x, d.x * x.x, d.y, d.y * x.y);
-        p[1] = make_float4(d.z, d.z * x.z, d.w, d.w * x.w);
+        form_dt(&to[k][c], u[v].f(), delta[v].f(), bias, k < tokens && c < channels);
     }
 }
 template <int K, int N, int M, typename T, int V>
@@ -96,35 +75,11 @@ __device__ __forceinline__ void form_bc(float (&to)[2][K][N], const Raw4<T> (&x)
         if (which < 2) *reinterpret_cast<float4*>(&to[which][k][n]) = x[v].f();
     }
 }
-__device__ __forceinline__ float4 column_values(const float* p, const ChannelTile& tile, int c) {
-    return p && c < tile.n ? *reinterpret_cast<const float4*>(p + tile.d0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-}
-
-__device__ __forceinline__ void load_pairs(float2 (&x)[2], const float* p) {
-    const float4 f = *reinterpret_cast<const float4*>(p);
-    x[0] = make_float2(f.x, f.y);
-    x[1] = make_float2(f.z, f.w);
-}
-__device__ __forceinline__ void store_pairs(float* p, const float2 (&x)[2]) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
-}
-template <int N>
-__device__ __forceinline__ void load_rates(float2 (&A2)[2][2], const ScanArgs& a, const ChannelTile& tile, const Lane& l) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        A2[s][0] = A2[s][1] = all2(0.f);
-        if (l.ch[s] < tile.n) {
-            load_pairs(A2[s], a.A_log + (size_t)(tile.d0 + l.ch[s]) * N + l.n4);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) A2[s][i] = make_float2(rate2(A2[s][i].x), rate2(A2[s][i].y));
-        }
-    }
-}
-
-// Each segment's own contribution to the state, from zero, and its sum of dt.
+// Each segment's own contribution to the state, from zero, and its sum of dt.  Issue slots 64 %, special functions 55 %, the
+// fp32 pipe 58 % of their rates: 159 us for 46,547 packed tokens of 1024 channels (199 us in half as many segments).
 template <int N, typename T>
 __global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_constant__ ScanArgs a) {
-    constexpr int CH = Shape<N>::CH, K = 16, M = kScanThreads;
+    constexpr int CH = ScanShape<N>::CH, K = 16, M = kScanThreads;
     using S = Share<N, K, M>;
     __shared__ __align__(16) float2 s_dt[K][CH];
     __shared__ __align__(16) float s_bc[2][K][N];
@@ -134,16 +89,16 @@ __global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_c
     if (!unit_at(a.cu, a.T, a.nseq, a.seg, slot, false, u)) return;
     if (u.last) return;   // nothing reads it
     const int tid = threadIdx.x, c4 = tid % (CH / 4) * 4;
-    const Lane l = lane_of<N>(tid);
+    const ScanLane l = scan_lane<N>(tid);
     const size_t DN = (size_t)a.D * N;
     float2 A2[2][2], h[2][2];
     float sum_dt[2] = {0.f, 0.f};
-    load_rates<N>(A2, a, tile, l);
+    load_rates<N>(A2, a.A_log, tile, l);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int i = 0; i < 2; ++i) h[s][i] = all2(0.f);
-    const float4 bias = column_values(a.dt_bias, tile, c4);
+    const float4 bias = columns(a.dt_bias, tile, c4);
     const Rows B{a.B, a.b_stride}, C{nullptr, 0};
     Raw4<T> ru[S::kVecs], rd[S::kVecs], rbc[S::kBC];
     auto load = [&](long long t0) {
@@ -158,14 +113,14 @@ __global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_c
     load(u.t0);
     for (long long t0 = u.t0; t0 < u.t1; t0 += K) {
         const int tokens = (int)min((long long)K, u.t1 - t0);
-        form_dt<K, CH, M>(s_dt, ru, rd, bias, tokens, tile.n, tid);
+        form_tile_dt<K, CH, M>(s_dt, ru, rd, bias, tokens, tile.n, tid);
         form_bc<K, N, M>(s_bc, rbc, tid);
         __syncthreads();
         if (t0 + K < u.t1) load(t0 + K);
 #pragma unroll 4
         for (int k = 0; k < K; ++k) {
             float2 B2[2];
-            load_pairs(B2, &s_bc[0][k][l.n4]);
+            load_states(B2, &s_bc[0][k][l.n0]);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const float2 dd = s_dt[k][l.ch[s]];
@@ -183,26 +138,27 @@ __global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_c
     for (int s = 0; s < 2; ++s) {
         if (l.ch[s] >= tile.n) continue;
         const size_t d = tile.d0 + l.ch[s];
-        store_pairs(a.states + (size_t)slot * DN + d * N + l.n4, h[s]);
-        if (l.n4 == 0) a.sum_dt[(size_t)slot * a.D + d] = sum_dt[s];
+        store_states(a.states + (size_t)slot * DN + d * N + l.n0, h[s]);
+        if (l.n0 == 0) a.sum_dt[(size_t)slot * a.D + d] = sum_dt[s];
     }
 }
 
 // The outputs.  Four warps walk the states; others form the next tile's dt, dt u, B and C in shared memory and finish the
 // last one's outputs meanwhile (one barrier a tile), so that the walk waits for neither.  Where whole sequences are walked
 // (SEG false) few blocks are there and the walk itself is what takes the time: registers for a whole tile's instructions in
-// any order, eight warps of helpers.  Segments fill the GPU: two blocks an SM with bf16 (fp32 vectors would not fit the
-// registers), four warps of helpers.
+// any order, eight warps of helpers (four: 102 against 98 us for 2 x 2048 tokens).  Segments fill the GPU: two blocks an SM
+// with bf16 (fp32 vectors would not fit the registers), four warps of helpers (46,547 packed tokens, all three launches: 394
+// us; one block of twelve warps an SM 428; three blocks 429, registers spilled).
 __host__ __device__ constexpr int helpers(bool seg) { return seg ? 128 : 256; }
 template <int N>
 struct MainShape {
-    static constexpr int K = N == 8 ? 16 : 32, CH = Shape<N>::CH;
+    static constexpr int K = N == 8 ? 16 : 32, CH = ScanShape<N>::CH;
     static constexpr int kRow = CH + (N == 8 ? 0 : 256 / N);   // floats of a row of sums: no bank conflicts
     static constexpr size_t kSums = sizeof(float) * 2 * K * kRow;
 };
 template <int N, typename T, bool SEG>
 __global__ void __launch_bounds__(kScanThreads + helpers(SEG), SEG && sizeof(T) == 2 ? 2 : 1) scan_main_kernel(const __grid_constant__ ScanArgs a) {
-    constexpr int L = Shape<N>::L, CH = Shape<N>::CH, P = Shape<N>::kPairs, K = MainShape<N>::K, M = helpers(SEG), kRow = MainShape<N>::kRow;
+    constexpr int L = ScanShape<N>::L, CH = ScanShape<N>::CH, P = ScanShape<N>::P, K = MainShape<N>::K, M = helpers(SEG), kRow = MainShape<N>::kRow;
     using S = Share<N, K, M>;
     // arrays of their own, so that what is stored to the sums does not hold back the next tokens' loads
     __shared__ __align__(16) float2 s_dt[2][K][CH];
@@ -217,7 +173,7 @@ __global__ void __launch_bounds__(kScanThreads + helpers(SEG), SEG && sizeof(T) 
     const size_t DN = (size_t)a.D * N;
     if (threadIdx.x >= kScanThreads) {
         const int tid = threadIdx.x - kScanThreads, c4 = tid % (CH / 4) * 4;
-        const float4 bias = column_values(a.dt_bias, tile, c4), skip = column_values(a.skip, tile, c4);
+        const float4 bias = columns(a.dt_bias, tile, c4), skip = columns(a.skip, tile, c4);
         const Rows B{a.B, a.b_stride}, C{a.C, a.c_stride};
         Raw4<T> ru[S::kVecs], rd[S::kVecs], rz[S::kVecs], rbc[S::kBC];   // the next tile's
         Raw4<T> cu[S::kVecs], cz[S::kVecs], pu[S::kVecs], pz[S::kVecs];  // of the tile that is walked, of the last one
@@ -238,7 +194,7 @@ __global__ void __launch_bounds__(kScanThreads + helpers(SEG), SEG && sizeof(T) 
             next(wz, a.z_stride);
         };
         auto form = [&](int i) {
-            form_dt<K, CH, M>(s_dt[i & 1], ru, rd, bias, tokens_of(i), tile.n, tid);
+            form_tile_dt<K, CH, M>(s_dt[i & 1], ru, rd, bias, tokens_of(i), tile.n, tid);
             form_bc<K, N, M>(s_bc[i & 1], rbc, tid);
         };
         auto finish = [&](int i, const Raw4<T> (&fu)[S::kVecs], const Raw4<T> (&fz)[S::kVecs]) {
@@ -282,14 +238,14 @@ __global__ void __launch_bounds__(kScanThreads + helpers(SEG), SEG && sizeof(T) 
         }
         return;
     }
-    const Lane l = lane_of<N>(threadIdx.x);
+    const ScanLane l = scan_lane<N>(threadIdx.x);
     float2 A2[2][2], h[2][2];
-    load_rates<N>(A2, a, tile, l);
+    load_rates<N>(A2, a.A_log, tile, l);
     const float* from = SEG ? a.states + (size_t)slot * DN : a.h0 ? a.h0 + (size_t)u.seq * DN : nullptr;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         h[s][0] = h[s][1] = all2(0.f);
-        if (from && l.ch[s] < tile.n) load_pairs(h[s], from + (size_t)(tile.d0 + l.ch[s]) * N + l.n4);
+        if (from && l.ch[s] < tile.n) load_states(h[s], from + (size_t)(tile.d0 + l.ch[s]) * N + l.n0);
     }
     __syncthreads();
     constexpr int TT = L / 2;              // tokens whose sums over the lanes are finished together
@@ -307,8 +263,8 @@ __global__ void __launch_bounds__(kScanThreads + helpers(SEG), SEG && sizeof(T) 
                 for (int e = 0; e < TT; ++e) {
                     const int k = k0 + j + e;
                     float2 B2[2], C2[2];
-                    load_pairs(B2, &bc[0][k][l.n4]);
-                    load_pairs(C2, &bc[1][k][l.n4]);
+                    load_states(B2, &bc[0][k][l.n0]);
+                    load_states(C2, &bc[1][k][l.n0]);
                     float part[2];
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
@@ -334,7 +290,7 @@ __global__ void __launch_bounds__(kScanThreads + helpers(SEG), SEG && sizeof(T) 
     if (a.h_final && u.last)
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            if (l.ch[s] < tile.n) store_pairs(a.h_final + (size_t)u.seq * DN + (size_t)(tile.d0 + l.ch[s]) * N + l.n4, h[s]);
+            if (l.ch[s] < tile.n) store_states(a.h_final + (size_t)u.seq * DN + (size_t)(tile.d0 + l.ch[s]) * N + l.n0, h[s]);
 }
 
 // The segments' contributions, in place: states to the state before each segment, adjoints (blockIdx.y 1) to the
@@ -380,7 +336,9 @@ __global__ void __launch_bounds__(kScanThreads) scan_join_kernel(const __grid_co
 
 // One token for each of the rows, in place on the states: eight states a lane, so that the functions of dt and of the gate,
 // which the L lanes of a channel all form, weigh little.  A block has a tile of channels and every `splits`-th row; what a
-// row needs is asked for while the one before it is worked on.
+// row needs is asked for while the one before it is worked on.  256 rows of 4096 channels of 16 states, bf16: 26.9 us a
+// call, 5.3 TB/s, 0.78 of the copy bandwidth (four states a lane 34.8 us, held by its instructions; without rows ahead
+// 36 - 43 us; two or more rows ahead spill: 41 us and more).
 template <typename T>
 struct StepRow {
     float4 h[2];
@@ -462,7 +420,7 @@ __global__ void __launch_bounds__(kScanThreads, kStepBlocks) scan_step_kernel(co
 
 template <int N>
 unsigned blocks_of(const ScanArgs& a) {
-    return (unsigned)((long long)a.slots * a.G * ((a.D / a.G + Shape<N>::CH - 1) / Shape<N>::CH));
+    return (unsigned)((long long)a.slots * a.G * ((a.D / a.G + ScanShape<N>::CH - 1) / ScanShape<N>::CH));
 }
 template <int N, typename T, bool SEG>
 cudaError_t main_typed(const ScanArgs& a) {
@@ -507,8 +465,11 @@ cudaError_t step_n(const ScanStepArgs& a) { GDN_SCAN_N(step_typed, a) }
 
 }  // namespace
 
-// A sequence is walked by one block a channel tile where the tiles of all sequences fill the GPU, else in segments,
-// whose states are formed first.
+// A sequence is walked by one block a channel tile where the tiles' warps are about as many as the GPU's schedulers (608),
+// else in segments, whose states are formed first: 60 % more work, but on all of them.  With 512 warps the whole walk takes
+// 357 us (2 x 8192 tokens of 4096 channels), segments about 540.  Packed sequences are taken as one long one, as lengths are
+// on the device.  At least 256 tokens a segment; about 8 x 608 warps of work in all (4 x: 452, 12 x: 430, 16 x: 457 against
+// 428 us for 46,547 packed tokens of 1024 channels).
 int scan_fwd_segment(long long tokens, int D, int N, int nseq, bool packed) {
     const long long warps = (long long)D * N / 256 * (packed ? 1 : nseq);   // at work at once, in the worst case
     if (warps >= 500) return 0;

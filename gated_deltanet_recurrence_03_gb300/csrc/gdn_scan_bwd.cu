@@ -10,6 +10,15 @@
 // the last to the first: each is walked forwards with its states in registers, then backwards.  Sums over a group's channels
 // (dB, dC) leave as one partial sum a tile, sums over tokens (dA_log, dskip, dbias) as one a segment; the last kernels add
 // them in order.
+//
+// 2 x 8192 tokens of 4096 channels of 16 states, bf16: 1636 us (first walk 425, join 29, chunks 1143, sums 31).  Bound by
+// instructions and shared memory together: a warp's token of two channels and four states a lane is about 200 instructions,
+// 12 of them exchanges; issue slots 58 %, shared-memory pipe 61 %, fp32 pipe 43 %, at 168 registers (three blocks an SM;
+// two 5 % slower, four spill and are 3 % slower).  HBM would take 139 us, three exponentials a state and token 345 us.
+// From 2857 us: raw rows by asynchronous copies, no bank conflicts, h kept rather than a h 1877; no state walked twice for
+// the chunks' starts 1687; four blocks an SM in the first walk 1656; a chunk's sum of dt asked for ahead 1636.  Not kept:
+// eight states a lane with 6-token chunks (602 against 519 us for 2 x 2048 tokens: spills), a's held from one walk for the
+// other (spills), segments in the chunks' kernel from states kept in shared memory (520 us).
 #include <algorithm>
 
 #include "norm_rows.cuh"
@@ -21,72 +30,20 @@ namespace {
 
 constexpr int kChunk = kScanChunk;   // tokens whose states a thread holds
 
-// A lane has two channels of four states each; the L lanes of a channel pair are P lanes apart, so that adjacent lanes read
-// the same B and C.
-template <int N>
-struct Shape {
-    static constexpr int L = N / 4, P = 32 / L, CH = 2 * P * (kScanThreads / 32), K = kChunk;
-    static constexpr int kRow = CH + 8;
-};
-struct Lane {
-    int n0, pair;   // first state, channel pair in the warp
-    int ch[2];      // channels in the tile; every other of a pair's lanes holds them in the other order
-};
-template <int N>
-__device__ __forceinline__ Lane lane_of(int tid) {
-    constexpr int P = Shape<N>::P;
-    Lane l;
-    l.pair = tid % P;
-    l.n0 = tid % 32 / P * 4;
-    l.ch[0] = tid / 32 * 2 * P + 2 * l.pair + (tid / P & 1);
-    l.ch[1] = l.ch[0] ^ 1;
-    return l;
-}
-__device__ __forceinline__ void load_states(float2 (&x)[2], const float* p) {
-    const float4 f = *reinterpret_cast<const float4*>(p);
-    x[0] = make_float2(f.x, f.y);
-    x[1] = make_float2(f.z, f.w);
-}
-__device__ __forceinline__ void store_states(float* p, const float2 (&x)[2]) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
-}
-template <int N>
-__device__ __forceinline__ void load_rates(float2 (&A2)[2][2], const ScanArgs& a, const ChannelTile& tile, const Lane& l) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const bool own = l.ch[s] < tile.n;
-        if (own) load_states(A2[s], a.A_log + (size_t)(tile.d0 + l.ch[s]) * N + l.n0);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) A2[s][i] = own ? make_float2(rate2(A2[s][i].x), rate2(A2[s][i].y)) : all2(0.f);
-    }
-}
-
 // A thread's vectors of four channels: column c4, rows k0, k0 + kStep, ...
 template <int N>
 struct Own {
-    static constexpr int kCols = Shape<N>::CH / 4, kStep = kScanThreads / kCols;
+    static constexpr int kCols = ScanShape<N>::CH / 4, kStep = kScanThreads / kCols;
     int c4, k0;
     __device__ __forceinline__ explicit Own(int tid) : c4(tid % kCols * 4), k0(tid / kCols) {}
 };
-
-__device__ __forceinline__ float4 columns(const float* p, const ChannelTile& tile, int c) {
-    return p && c < tile.n ? *reinterpret_cast<const float4*>(p + tile.d0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-}
-// dt and dt u of four channels; dt = 0 past the end, where nothing changes.
-__device__ __forceinline__ void form_dt(float2* to, float4 u, float4 delta, float4 bias, bool ok) {
-    float4 d = softplus4(add4(delta, bias));
-    if (!ok) d = make_float4(0.f, 0.f, 0.f, 0.f);
-    float4* p = reinterpret_cast<float4*>(to);
-    p[0] = make_float4(d.x, d.x * u.x, d.y, d.y * u.y);
-    p[1] = make_float4(d.z, d.z * u.z, d.w, d.w * u.w);
-}
 
 // ---------------------------------------------------------------- the segments' ends
 // Each segment's contribution to the state behind it, from zero, and to the adjoint before it, sum_t (a_first .. a_t) C_t
 // p_t; its sum of dt; and the state and the sum before each chunk but the first.
 template <int N, typename T>
 __global__ void __launch_bounds__(kScanThreads, 4) scan_ends_kernel(const __grid_constant__ ScanArgs a) {
-    using S = Shape<N>;
+    using S = ScanShape<N>;
     using O = Own<N>;
     constexpr int CH = S::CH, K = 16, VEC = (K * CH / 4 + kScanThreads - 1) / kScanThreads,
                   BC = (2 * K * N / 4 + kScanThreads - 1) / kScanThreads;
@@ -99,12 +56,12 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_ends_kernel(const __grid
     Unit u;
     if (!unit_at(a.cu, a.T, a.nseq, a.seg, slot, false, u)) return;
     const int tid = threadIdx.x, len = (int)(u.t1 - u.t0);
-    const Lane l = lane_of<N>(tid);
+    const ScanLane l = scan_lane<N>(tid);
     const O own(tid);
     const size_t DN = (size_t)a.D * N;
     float2 A2[2][2], h[2][2], lam[2][2], E[2][2];
     float sum_dt[2] = {0.f, 0.f};
-    load_rates<N>(A2, a, tile, l);
+    load_rates<N>(A2, a.A_log, tile, l);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -217,7 +174,7 @@ __device__ __forceinline__ void copies_done() {
 // back only what it copied itself.
 template <int N, typename T>
 struct Stages {
-    using S = Shape<N>;
+    using S = ScanShape<N>;
     float4 first[2][kScanThreads];   // the state before the segment
     float4 state[2][2][kScanThreads];
     T rows[2][4 * kChunk][S::CH];
@@ -226,9 +183,9 @@ struct Stages {
 
 template <int N, typename T>
 __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_constant__ ScanArgs a) {
-    using S = Shape<N>;
+    using S = ScanShape<N>;
     using O = Own<N>;
-    constexpr int L = S::L, P = S::P, CH = S::CH, K = S::K;
+    constexpr int L = S::L, P = S::P, CH = S::CH, K = kChunk, kRow = CH + 8;
     constexpr int TT = L < 4 ? 1 : 2;   // tokens whose sums over the lanes are finished together
     constexpr int VEC = (K * CH / 4 + kScanThreads - 1) / kScanThreads, BC = (2 * K * N / 4 + kScanThreads - 1) / kScanThreads;
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -237,12 +194,12 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
     __shared__ __align__(16) float2 s_dt[K][CH];                              // dt, dt u
     __shared__ __align__(16) float s_p[K][CH];
     __shared__ __align__(16) float s_bc[2][K][N];
-    __shared__ __align__(16) float s_sums[3][K][S::kRow];                     // y, q, r
+    __shared__ __align__(16) float s_sums[3][K][kRow];                     // y, q, r
     __shared__ __align__(16) float s_red[kScanThreads / 32][K][2 * N];        // dB, dC of each warp
     const int tiles = a.G * ((a.D / a.G + CH - 1) / CH), slot = blockIdx.x / tiles, tile_id = blockIdx.x % tiles;
     const ChannelTile tile = channel_tile(a.D, a.G, CH, tile_id);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Lane l = lane_of<N>(tid);
+    const ScanLane l = scan_lane<N>(tid);
     const O own(tid);
     const bool some = own.c4 < tile.n;
     const size_t DN = (size_t)a.D * N;
@@ -261,7 +218,7 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
     };
 
     float2 A2[2][2], lam[2][2], gA[2][2];
-    load_rates<N>(A2, a, tile, l);
+    load_rates<N>(A2, a.A_log, tile, l);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         gA[s][0] = gA[s][1] = all2(0.f);
@@ -540,7 +497,7 @@ __global__ void __launch_bounds__(kSumCols * kSumRows) scan_weight_sums_kernel(c
 
 template <int N, typename T>
 cudaError_t bwd_typed(const ScanArgs& a) {
-    using S = Shape<N>;
+    using S = ScanShape<N>;
     cudaError_t e = allow_smem<scan_bwd_kernel<N, T>>(sizeof(Stages<N, T>));
     if (e != cudaSuccess) return e;
     const int per_group = (a.D / a.G + S::CH - 1) / S::CH;

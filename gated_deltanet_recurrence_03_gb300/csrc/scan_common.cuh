@@ -119,6 +119,59 @@ __device__ __forceinline__ ChannelTile channel_tile(int D, int G, int per_tile, 
     return c;
 }
 
+// A lane holds two channels of four states each; the L lanes of a channel pair are P = 32 / L lanes apart: adjacent lanes then
+// read the same B and C, 2.1 cycles of shared memory a 16-byte read instead of 3.9 with L adjacent lanes on L addresses.
+template <int N>
+struct ScanShape {
+    static constexpr int L = N / 4, P = 32 / L, CH = 2 * P * (kScanThreads / 32);   // CH: channels of a tile
+};
+struct ScanLane {
+    int n0, pair;   // first state, channel pair in the warp
+    int ch[2];      // channels in the tile; every other of a pair's lanes holds them in the other order, so that one exchange
+                    // leaves each with its first channel's sum
+};
+template <int N>
+__device__ __forceinline__ ScanLane scan_lane(int tid) {
+    constexpr int P = ScanShape<N>::P;
+    ScanLane l;
+    l.pair = tid % P;
+    l.n0 = tid % 32 / P * 4;
+    l.ch[0] = tid / 32 * 2 * P + 2 * l.pair + (tid / P & 1);
+    l.ch[1] = l.ch[0] ^ 1;
+    return l;
+}
+__device__ __forceinline__ void load_states(float2 (&x)[2], const float* p) {
+    const float4 f = *reinterpret_cast<const float4*>(p);
+    x[0] = make_float2(f.x, f.y);
+    x[1] = make_float2(f.z, f.w);
+}
+__device__ __forceinline__ void store_states(float* p, const float2 (&x)[2]) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+}
+// A lane's rates, zeros past the tile.
+template <int N>
+__device__ __forceinline__ void load_rates(float2 (&A2)[2][2], const float* A_log, const ChannelTile& tile, const ScanLane& l) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const bool own = l.ch[s] < tile.n;
+        if (own) load_states(A2[s], A_log + (size_t)(tile.d0 + l.ch[s]) * N + l.n0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) A2[s][i] = own ? make_float2(rate2(A2[s][i].x), rate2(A2[s][i].y)) : all2(0.f);
+    }
+}
+// Four adjacent columns of a [D] tensor from the tile's column c on; zeros past the tile or without one.
+__device__ __forceinline__ float4 columns(const float* p, const ChannelTile& tile, int c) {
+    return p && c < tile.n ? *reinterpret_cast<const float4*>(p + tile.d0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+// dt and dt u of four channels; dt = 0 past the end, where nothing changes.
+__device__ __forceinline__ void form_dt(float2* to, float4 u, float4 delta, float4 bias, bool ok) {
+    float4 d = softplus4(add4(delta, bias));
+    if (!ok) d = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4* p = reinterpret_cast<float4*>(to);
+    p[0] = make_float4(d.x, d.x * u.x, d.y, d.y * u.y);
+    p[1] = make_float4(d.z, d.z * u.z, d.w, d.w * u.w);
+}
+
 // W values of a lane, summed over the W lanes that differ in lane / BIT % W: lane gets the sum of value lane / BIT % W.
 template <int W, int BIT = 1>
 __device__ __forceinline__ float transpose_sum(float (&v)[W], int lane) {
