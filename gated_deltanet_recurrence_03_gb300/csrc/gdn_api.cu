@@ -967,7 +967,7 @@ gdn_status_t scan_sequences(int B, int T, int D, int G, int N, const gdn_opts_t&
     // tiles of at least 8 channels of a group and vectors of four states, for each sequence and segment
     const long long slots = *nseq + tokens / kScanMinSegment, tiles = std::max((long long)D / 8, (long long)D * N / 512 + 1);
     if (slots > kMaxBlocks / tiles) return fail(GDN_ERR_INVALID_ARG, "%lld tokens in %d sequences of %d channels are too many", tokens, *nseq, D);
-    if (tokens * ((long long)G * N / 2) / 256 >= kMaxBlocks) return fail(GDN_ERR_INVALID_ARG, "%lld tokens of %d groups are too many", tokens, G);
+    if (tokens * ((long long)G * N / 2) / 256 >= kMaxBlocks / 2) return fail(GDN_ERR_INVALID_ARG, "%lld tokens of %d groups are too many", tokens, G);
     return GDN_OK;
 }
 

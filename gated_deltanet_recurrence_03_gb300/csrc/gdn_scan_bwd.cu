@@ -444,11 +444,14 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
     }
 }
 
-// dB and dC of a token, over the tiles of each group.
+// The partial sums, added in order.  Blocks below bc_blocks: dB and dC of a token over the tiles of each group, a vector of
+// four a thread.  The others: dA_log = A sum dA, dskip and dbias over the segments, vectors of four columns of the slots'
+// rows of D N + 2 D sums, eight threads a vector.
+constexpr int kSumCols = 32, kSumRows = 8;
 template <typename T>
-__global__ void __launch_bounds__(256) scan_bc_sums_kernel(const __grid_constant__ ScanArgs a, int tiles_per_group) {
-    const int per = a.G * a.N / 2;   // vectors of four: dB and dC of the groups
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, t = i / per;
+__device__ __forceinline__ void bc_sums(const ScanArgs& a, int tiles_per_group) {
+    const int per = a.G * a.N / 2;   // vectors of a token
+    const long long i = (long long)blockIdx.x * (kSumCols * kSumRows) + threadIdx.x, t = i / per;
     if (t >= a.tokens) return;
     if (a.cu) {   // a token of no sequence has no partial sums
         long long s0, s1, e0, e1;
@@ -465,14 +468,16 @@ __global__ void __launch_bounds__(256) scan_bc_sums_kernel(const __grid_constant
     T* to = static_cast<T*>(is_c ? a.gC : a.gB) + t * (is_c ? a.gc_stride : a.gb_stride);
     store4(to + (size_t)g * a.N + (is_c ? n - a.N : n), s);
 }
-
-// dA_log = A sum dA, dskip, dbias over the segments: vectors of four columns of the slots' rows of D N + 2 D sums, eight
-// threads a vector.
-constexpr int kSumCols = 32, kSumRows = 8;
-__global__ void __launch_bounds__(kSumCols * kSumRows) scan_weight_sums_kernel(const __grid_constant__ ScanArgs a) {
+template <typename T>
+__global__ void __launch_bounds__(kSumCols * kSumRows) scan_sums_kernel(const __grid_constant__ ScanArgs a, int tiles_per_group,
+                                                                       unsigned bc_blocks) {
+    if (blockIdx.x < bc_blocks) {
+        bc_sums<T>(a, tiles_per_group);
+        return;
+    }
     __shared__ float4 red[kSumRows][kSumCols];
     const int x = threadIdx.x % kSumCols, y = threadIdx.x / kSumCols;
-    const size_t DN = (size_t)a.D * a.N, c = ((size_t)blockIdx.x * kSumCols + x) * 4;
+    const size_t DN = (size_t)a.D * a.N, c = ((size_t)(blockIdx.x - bc_blocks) * kSumCols + x) * 4;
     const bool rate = c < DN, any = c < DN + 2 * a.D;
     const float* p = rate ? a.part_A + c : a.part_s + (c - DN);
     const size_t row = rate ? DN : 2 * (size_t)a.D;
@@ -506,11 +511,10 @@ cudaError_t bwd_typed(const ScanArgs& a) {
     if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_scan_join(a, true)) != cudaSuccess) return e;
     scan_bwd_kernel<N, T><<<blocks, kScanThreads, sizeof(Stages<N, T>), a.stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const long long vecs = (long long)a.tokens * a.G * N / 2;
-    scan_bc_sums_kernel<T><<<(unsigned)((vecs + 255) / 256), 256, 0, a.stream>>>(a, per_group);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const size_t cols = (size_t)a.D * N + 2 * a.D;
-    scan_weight_sums_kernel<<<(unsigned)((cols / 4 + kSumCols - 1) / kSumCols), kSumCols * kSumRows, 0, a.stream>>>(a);
+    constexpr int kThreads = kSumCols * kSumRows;
+    const long long bc = ((long long)a.tokens * a.G * N / 2 + kThreads - 1) / kThreads;
+    const long long cols = ((long long)a.D * N + 2 * a.D) / 4;
+    scan_sums_kernel<T><<<(unsigned)(bc + (cols + kSumCols - 1) / kSumCols), kThreads, 0, a.stream>>>(a, per_group, (unsigned)bc);
     return cudaGetLastError();
 }
 template <typename T>
