@@ -1,7 +1,7 @@
 // Units of work of the decayed scan's kernels: sequences, or segments of them.
 #pragma once
 
-#include "token_units.cuh"
+#include "gdn_internal.cuh"
 
 namespace gdn {
 
@@ -14,8 +14,42 @@ struct SegArgs {
     float* states;
 };
 
+// The tokens of a slot, and whether it is the first and the last one its sequence's scan visits; false for a slot
+// without a sequence's segment (an empty sequence has one segment of no tokens).
+struct Unit {
+    int seq;
+    long long t0, t1;
+    bool first, last;
+};
 __device__ __forceinline__ bool unit_of(const SegArgs& ta, int slot, bool rev, Unit& u) {
-    return unit_at(ta.a.cu, ta.a.T, ta.a.nseq, ta.seg, slot, rev, u);
+    const DecayArgs& a = ta.a;
+    if (!ta.seg) {
+        u.seq = slot;
+        seq_range(a.cu, slot, a.T, u.t0, u.t1);
+        u.first = u.last = true;
+        return true;
+    }
+    auto base = [&](int i) {
+        long long s0, s1;
+        seq_range(a.cu, i, a.T, s0, s1);
+        return s0 / ta.seg + i;
+    };
+    int lo = 0, hi = a.nseq - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (base(mid) <= slot) lo = mid;
+        else hi = mid - 1;
+    }
+    long long s0, s1;
+    seq_range(a.cu, lo, a.T, s0, s1);
+    const long long j = slot - base(lo), n = max(1LL, (s1 - s0 + ta.seg - 1) / ta.seg);
+    if (j < 0 || j >= n) return false;
+    u.seq = lo;
+    u.t0 = s0 + j * ta.seg;
+    u.t1 = min(s1, u.t0 + ta.seg);
+    u.first = j == (rev ? n - 1 : 0);
+    u.last = j == (rev ? 0 : n - 1);
+    return true;
 }
 __device__ __forceinline__ float* unit_state(const SegArgs& ta, int scan, int slot, int h) {
     return ta.states + (((size_t)scan * ta.slots + slot) * ta.a.Hv + h) * ta.a.dk * ta.a.dv;

@@ -280,7 +280,7 @@ struct ScanArgs {
     const int32_t* cu;
     int nseq;
     int tokens;                 // all tokens of the call
-    // segments of `seg` tokens, `slots` of them (token_units.cuh; seg = 0: sequences), their states [slots][D][N],
+    // segments of `seg` tokens, `slots` of them (scan_common.cuh; seg = 0: sequences), their states [slots][D][N],
     // adjoints (gradients only) and sums of dt [slots][D]
     int seg, slots;
     float* states;

@@ -85,8 +85,8 @@ __global__ void __launch_bounds__(kScanThreads) scan_state_kernel(const __grid_c
     __shared__ __align__(16) float s_bc[2][K][N];
     const int tiles = a.G * ((a.D / a.G + CH - 1) / CH), slot = blockIdx.x / tiles;
     const ChannelTile tile = channel_tile(a.D, a.G, CH, blockIdx.x % tiles);
-    Unit u;
-    if (!unit_at(a.cu, a.T, a.nseq, a.seg, slot, false, u)) return;
+    ScanUnit u;
+    if (!scan_unit_at(a.cu, a.T, a.nseq, a.seg, slot, u)) return;
     if (u.last) return;   // nothing reads it
     const int tid = threadIdx.x, c4 = tid % (CH / 4) * 4;
     const ScanLane l = scan_lane<N>(tid);
@@ -167,8 +167,8 @@ __global__ void __launch_bounds__(kScanThreads + helpers(SEG), SEG && sizeof(T) 
     float(*const s_y)[K][kRow] = reinterpret_cast<float(*)[K][kRow]>(smem);
     const int tiles = a.G * ((a.D / a.G + CH - 1) / CH), slot = blockIdx.x / tiles;
     const ChannelTile tile = channel_tile(a.D, a.G, CH, blockIdx.x % tiles);
-    Unit u;
-    if (!unit_at(a.cu, a.T, a.nseq, a.seg, slot, false, u)) return;
+    ScanUnit u;
+    if (!scan_unit_at(a.cu, a.T, a.nseq, a.seg, slot, u)) return;
     const int n = (int)((u.t1 - u.t0 + K - 1) / K);
     const size_t DN = (size_t)a.D * N;
     if (threadIdx.x >= kScanThreads) {

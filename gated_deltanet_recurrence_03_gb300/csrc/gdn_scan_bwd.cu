@@ -8,15 +8,15 @@
 // every K tokens, and what the segment adds to the state behind it and to the adjoint before it; launch_scan_join makes
 // those the state before each segment and the adjoint behind it.  Then a block takes its segment's chunks of K tokens from
 // the last to the first: each is walked forwards with its states in registers, then backwards.  Sums over a group's channels
-// (dB, dC) leave as one partial sum a tile, sums over tokens (dA_log, dskip, dbias) as one a segment; the last kernels add
+// (dB, dC) leave as one partial sum a tile, sums over tokens (dA_log, dskip, dbias) as one a segment; the last kernel adds
 // them in order.
 //
-// 2 x 8192 tokens of 4096 channels of 16 states, bf16: 1636 us (first walk 425, join 29, chunks 1143, sums 31).  Bound by
+// 2 x 8192 tokens of 4096 channels of 16 states, bf16: 1632 us (first walk 425, join 29, chunks 1143, sums 25).  Bound by
 // instructions and shared memory together: a warp's token of two channels and four states a lane is about 200 instructions,
 // 12 of them exchanges; issue slots 58 %, shared-memory pipe 61 %, fp32 pipe 43 %, at 168 registers (three blocks an SM;
 // two 5 % slower, four spill and are 3 % slower).  HBM would take 139 us, three exponentials a state and token 345 us.
 // From 2857 us: raw rows by asynchronous copies, no bank conflicts, h kept rather than a h 1877; no state walked twice for
-// the chunks' starts 1687; four blocks an SM in the first walk 1656; a chunk's sum of dt asked for ahead 1636.  Not kept:
+// the chunks' starts 1687; four blocks an SM in the first walk 1656; a chunk's sum of dt asked for ahead 1636; one launch of sums 1632.  Not kept:
 // eight states a lane with 6-token chunks (602 against 519 us for 2 x 2048 tokens: spills), a's held from one walk for the
 // other (spills), segments in the chunks' kernel from states kept in shared memory (520 us).
 #include <algorithm>
@@ -53,8 +53,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_ends_kernel(const __grid
     __shared__ __align__(16) float s_bc[2][K][N];
     const int tiles = a.G * ((a.D / a.G + CH - 1) / CH), slot = blockIdx.x / tiles;
     const ChannelTile tile = channel_tile(a.D, a.G, CH, blockIdx.x % tiles);
-    Unit u;
-    if (!unit_at(a.cu, a.T, a.nseq, a.seg, slot, false, u)) return;
+    ScanUnit u;
+    if (!scan_unit_at(a.cu, a.T, a.nseq, a.seg, slot, u)) return;
     const int tid = threadIdx.x, len = (int)(u.t1 - u.t0);
     const ScanLane l = scan_lane<N>(tid);
     const O own(tid);
@@ -203,8 +203,8 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
     const O own(tid);
     const bool some = own.c4 < tile.n;
     const size_t DN = (size_t)a.D * N;
-    Unit u;
-    if (!unit_at(a.cu, a.T, a.nseq, a.seg, slot, false, u)) u.t0 = u.t1 = 0, u.first = false;
+    ScanUnit u;
+    if (!scan_unit_at(a.cu, a.T, a.nseq, a.seg, slot, u)) u.t0 = u.t1 = 0, u.first = false;
     const int len = (int)(u.t1 - u.t0), chunks = (len + K - 1) / K;
     float* const part_A = a.part_A + (size_t)slot * DN;
     float* const part_s = a.part_s + (size_t)slot * 2 * a.D + tile.d0;
