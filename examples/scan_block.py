@@ -32,6 +32,7 @@ class Layer:
         self.w_in, self.w_x, self.w_dt = weight(WIDTH, 2 * D), weight(D, RANK + 2 * N), weight(RANK, D, std=0.1)
         self.w_o = weight(D, WIDTH)
         self.taps = weight(D, K, std=0.5, dtype=f32)
+        self.conv_bias = weight(D, std=0.1, dtype=f32)
         self.A_log = torch.log(torch.arange(1.0, N + 1)).expand(D, N).contiguous().to(device)
         self.skip = weight(D, std=0.1, mean=1.0, dtype=f32)
         step = torch.exp(torch.empty(D).uniform_(-6.9, -2.3, generator=gen))   # dt of 0.001 to 0.1 at first
@@ -52,7 +53,7 @@ class Layer:
         taps_in, h = cache
         n, r = gdn.gdn_layer_norm_fwd(x, self.norm, self.norm_bias, residual=b)
         xz = n @ self.w_in
-        u, taps_out = gdn.gdn_causal_conv1d_fwd(xz[..., :D], self.taps, taps_in)
+        u, taps_out = gdn.gdn_causal_conv1d_fwd(xz[..., :D], self.taps, taps_in, bias=self.conv_bias)
         p, delta, B, C = self.split(u)
         y, h = gdn.gdn_selective_scan_fwd(u, delta, self.A_log, B, C, h, skip=self.skip, dt_bias=self.dt_bias, z=xz[..., D:])
         self.saved = (x, b, n, xz, u, p, delta, y)
@@ -63,7 +64,7 @@ class Layer:
         taps, h = cache
         n, r = gdn.gdn_layer_norm_fwd(x, self.norm, self.norm_bias, residual=b)
         xz = n @ self.w_in
-        u = gdn.gdn_causal_conv1d_step(xz[..., :D], self.taps, taps)
+        u = gdn.gdn_causal_conv1d_step(xz[..., :D], self.taps, taps, bias=self.conv_bias)
         _, delta, B, C = self.split(u)
         y = gdn.gdn_selective_scan_step(u, delta, self.A_log, B, C, h, skip=self.skip, dt_bias=self.dt_bias, z=xz[..., D:])
         return y @ self.w_o, r
@@ -84,7 +85,8 @@ class Layer:
         gp[..., :RANK] = gdelta @ self.w_dt.T
         g["w_x"] = rows(u).T @ rows(gp)
         gu = gu + gp @ self.w_x.T
-        gx, g["taps"], _ = gdn.gdn_causal_conv1d_bwd(xz[..., :D], self.taps, gu, want_grad_cache_in=False)
+        gx, g["taps"], _, g["conv_bias"] = gdn.gdn_causal_conv1d_bwd(xz[..., :D], self.taps, gu, bias=self.conv_bias,
+                                                                     want_grad_cache_in=False)
         gxz[..., :D] = gx
         g["w_in"] = rows(n).T @ rows(gxz)
         g["x"], g["norm"], g["norm_bias"] = gdn.gdn_layer_norm_bwd(x, self.norm, gxz @ self.w_in.T, residual=b, grad_r=grad_r)

@@ -49,6 +49,8 @@ class GdnOpts(ctypes.Structure):
         ("norm_eps", ctypes.c_float),
         ("grad_A_log", ctypes.c_void_p),
         ("grad_dt_bias", ctypes.c_void_p),
+        ("conv_bias", ctypes.c_void_p),
+        ("grad_conv_bias", ctypes.c_void_p),
     ]
 
 

@@ -221,14 +221,22 @@ def version() -> int:
     return int(L.load().gdn_version())
 
 
+def _conv_bias(o, bias, C, dev):
+    if bias is not None:
+        _need("bias", bias, torch.float32, dev, (C,))
+        o.conv_bias = bias.data_ptr()
+
+
 def gdn_causal_conv1d_fwd(x: torch.Tensor, w: torch.Tensor, cache_in: Optional[torch.Tensor] = None, *,
-                          cu_seqlens: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                          bias: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                          out: Optional[torch.Tensor] = None,
                           cache_out: Optional[torch.Tensor] = None, return_cache: bool = True, stream: Optional[torch.cuda.Stream] = None,
                           events: Optional[Sequence[int]] = None):
     """Depthwise causal convolution + SiLU.  x [B, T, C] (bf16 or fp32; may be a channel slice of a
     wider tensor: rows must be evenly strided with the channels contiguous); w [C, K] fp32;
     cache_in [nseq, K-1, C] or None.  ``cache_out`` (or a new tensor when ``return_cache``) receives each
-    sequence's last K-1 inputs.  Returns (y [B, T, C], cache_out [nseq, K-1, C] or None)."""
+    sequence's last K-1 inputs.  ``bias`` (fp32 [C] or None) is added before the SiLU.  Returns (y [B, T, C],
+    cache_out [nseq, K-1, C] or None)."""
     lib = L.load()
     if x.dim() != 3 or x.stride(2) != 1 or x.stride(0) != x.shape[1] * x.stride(1):
         raise ValueError("x must be [B, T, C] with contiguous channels and evenly strided token rows")
@@ -256,6 +264,7 @@ def gdn_causal_conv1d_fwd(x: torch.Tensor, w: torch.Tensor, cache_in: Optional[t
         if cu_seqlens is not None:
             o.cu_seqlens = cu_seqlens.data_ptr()
             o.num_seqs = nseq
+        _conv_bias(o, bias, C, dev)
         st = lib.gdn_causal_conv1d_fwd(_ptr(x), x.stride(1), _ptr(w), _ptr(cache_in), _ptr(out), _ptr(cache_out),
                                        B, T, C, K, ctypes.byref(o))
         del keep
@@ -264,12 +273,13 @@ def gdn_causal_conv1d_fwd(x: torch.Tensor, w: torch.Tensor, cache_in: Optional[t
 
 
 def gdn_causal_conv1d_bwd(x: torch.Tensor, w: torch.Tensor, grad_y: torch.Tensor, cache_in: Optional[torch.Tensor] = None,
-                          *, grad_cache_out: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
-                          want_grad_w: bool = True, want_grad_cache_in: bool = True,
-                          stream: Optional[torch.cuda.Stream] = None, events: Optional[Sequence[int]] = None):
-    """Gradients through gdn_causal_conv1d_fwd: x, w, cache_in as there; grad_y [B, T, C] like x (dense);
+                          *, bias: Optional[torch.Tensor] = None, grad_cache_out: Optional[torch.Tensor] = None,
+                          cu_seqlens: Optional[torch.Tensor] = None, want_grad_w: bool = True,
+                          want_grad_cache_in: bool = True, stream: Optional[torch.cuda.Stream] = None,
+                          events: Optional[Sequence[int]] = None):
+    """Gradients through gdn_causal_conv1d_fwd: x, w, cache_in, bias as there; grad_y [B, T, C] like x (dense);
     grad_cache_out [nseq, K-1, C] like x or None.  Returns fp32 (grad_x [B, T, C], grad_w [C, K] or None,
-    grad_cache_in [nseq, K-1, C] or None)."""
+    grad_cache_in [nseq, K-1, C] or None), and with a bias a fourth one, grad_bias [C]."""
     lib = L.load()
     if x.dim() != 3 or x.stride(2) != 1 or x.stride(0) != x.shape[1] * x.stride(1):
         raise ValueError("x must be [B, T, C] with contiguous channels and evenly strided token rows")
@@ -297,8 +307,13 @@ def gdn_causal_conv1d_bwd(x: torch.Tensor, w: torch.Tensor, grad_y: torch.Tensor
         if cu_seqlens is not None:
             o.cu_seqlens = cu_seqlens.data_ptr()
             o.num_seqs = nseq
+        _conv_bias(o, bias, C, dev)
+        gb = None
+        if bias is not None:
+            gb = (torch.empty if nseq > 0 else torch.zeros)((C,), **f32)   # no sequences: nothing is launched
+            o.grad_conv_bias = gb.data_ptr()
         ws = None
-        if want_grad_w:
+        if want_grad_w or gb is not None:
             need = int(lib.gdn_causal_conv1d_bwd_workspace_size(B, T, C, K, ctypes.byref(o)))
             ws = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
             o.workspace, o.workspace_bytes = ws.data_ptr(), ws.numel()
@@ -307,14 +322,15 @@ def gdn_causal_conv1d_bwd(x: torch.Tensor, w: torch.Tensor, grad_y: torch.Tensor
                                        ctypes.byref(o))
         del keep
         L.check(lib, st)
-    return gx, gw, gc
+    return (gx, gw, gc) if bias is None else (gx, gw, gc, gb)
 
 
 def gdn_causal_conv1d_step(x: torch.Tensor, w: torch.Tensor, cache: torch.Tensor, *,
-                           out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None,
+                           bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                           stream: Optional[torch.cuda.Stream] = None,
                            events: Optional[Sequence[int]] = None) -> torch.Tensor:
     """One decode token per sequence: x [N, C] (channels contiguous, rows evenly strided), w [C, K] fp32,
-    cache [N, K-1, C] updated in place.  Returns y [N, C]."""
+    cache [N, K-1, C] updated in place; bias fp32 [C] or None.  Returns y [N, C]."""
     lib = L.load()
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be [N, C] with contiguous channels")
@@ -328,6 +344,7 @@ def gdn_causal_conv1d_step(x: torch.Tensor, w: torch.Tensor, cache: torch.Tensor
     _need("out", out, dt, dev, (N, C))
     with torch.cuda.device(dev):
         o, keep = _opts(lib, dt, 1.0, 64, False, stream, dev, events)
+        _conv_bias(o, bias, C, dev)
         st = lib.gdn_causal_conv1d_step(_ptr(x), x.stride(0), _ptr(w), _ptr(cache), _ptr(out), N, C, K,
                                         ctypes.byref(o))
         del keep
@@ -336,8 +353,9 @@ def gdn_causal_conv1d_step(x: torch.Tensor, w: torch.Tensor, cache: torch.Tensor
 
 
 def gdn_causal_conv1d_fwd_qkv(x: torch.Tensor, w: torch.Tensor, widths: Sequence[int],
-                              cache_in: Optional[torch.Tensor] = None, *, cu_seqlens: Optional[torch.Tensor] = None,
-                              out: Optional[Sequence[torch.Tensor]] = None, cache_out: Optional[torch.Tensor] = None,
+                              cache_in: Optional[torch.Tensor] = None, *, bias: Optional[torch.Tensor] = None,
+                              cu_seqlens: Optional[torch.Tensor] = None, out: Optional[Sequence[torch.Tensor]] = None,
+                              cache_out: Optional[torch.Tensor] = None,
                               return_cache: bool = True, stream: Optional[torch.cuda.Stream] = None,
                               events: Optional[Sequence[int]] = None):
     """The convolution of gdn_causal_conv1d_fwd over the packed q | k | v projection x [B, T, Cq + Ck + Cv]
@@ -374,6 +392,7 @@ def gdn_causal_conv1d_fwd_qkv(x: torch.Tensor, w: torch.Tensor, widths: Sequence
         if cu_seqlens is not None:
             o.cu_seqlens = cu_seqlens.data_ptr()
             o.num_seqs = nseq
+        _conv_bias(o, bias, C, dev)
         st = lib.gdn_causal_conv1d_fwd_qkv(_ptr(x), x.stride(1), _ptr(w), _ptr(cache_in), _ptr(out[0]), _ptr(out[1]),
                                            _ptr(out[2]), _ptr(cache_out), B, T, Cq, Ck, Cv, K, ctypes.byref(o))
         del keep
@@ -382,7 +401,7 @@ def gdn_causal_conv1d_fwd_qkv(x: torch.Tensor, w: torch.Tensor, widths: Sequence
 
 
 def gdn_causal_conv1d_step_qkv(x: torch.Tensor, w: torch.Tensor, cache: torch.Tensor, widths: Sequence[int], *,
-                               out: Optional[Sequence[torch.Tensor]] = None,
+                               bias: Optional[torch.Tensor] = None, out: Optional[Sequence[torch.Tensor]] = None,
                                stream: Optional[torch.cuda.Stream] = None,
                                events: Optional[Sequence[int]] = None):
     """One decode token per sequence through the convolution of the packed q | k | v projection
@@ -405,6 +424,7 @@ def gdn_causal_conv1d_step_qkv(x: torch.Tensor, w: torch.Tensor, cache: torch.Te
         _need(name, y, dt, dev, (N, c))
     with torch.cuda.device(dev):
         o, keep = _opts(lib, dt, 1.0, 64, False, stream, dev, events)
+        _conv_bias(o, bias, C, dev)
         st = lib.gdn_causal_conv1d_step_qkv(_ptr(x), x.stride(0), _ptr(w), _ptr(cache), _ptr(out[0]), _ptr(out[1]),
                                             _ptr(out[2]), N, Cq, Ck, Cv, K, ctypes.byref(o))
         del keep

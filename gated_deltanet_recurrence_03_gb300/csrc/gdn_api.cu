@@ -298,6 +298,7 @@ static gdn_status_t conv_common(const void* x, long long* x_stride, const float*
         return fail(GDN_ERR_INVALID_ARG, "x_stride=%lld must be >= C and a multiple of %d", *x_stride, per16);
     if (!x || !w) return fail(GDN_ERR_INVALID_ARG, "null x or w");
     if (!aligned16(x) || !aligned_to(w, 4)) return fail(GDN_ERR_INVALID_ARG, "x must be 16-byte aligned, w 4-byte aligned");
+    if (!aligned_to(o.conv_bias, 4)) return fail(GDN_ERR_INVALID_ARG, "conv_bias must be 4-byte aligned");
     return GDN_OK;
 }
 
@@ -330,7 +331,7 @@ gdn_status_t conv_fwd_impl(const void* x, long long x_stride, const float* w, co
     if (st != GDN_OK) return st;
     ConvArgs a{};
     a.x = x; a.x_stride = x_stride; a.w = w; a.cache_in = cache_in; a.y = y; a.cache_out = cache_out;
-    a.y_k = y_k; a.y_v = y_v; a.c1 = c1; a.c2 = c2;
+    a.y_k = y_k; a.y_v = y_v; a.c1 = c1; a.c2 = c2; a.bias = o.conv_bias;
     a.B = B; a.T = T; a.C = C; a.K = K; a.dtype = o.dtype; a.cu_seqlens = o.cu_seqlens; a.num_seqs = nseq;
     a.packed = packed; a.stream = static_cast<cudaStream_t>(o.stream); a.status = status;
     record(o, 0, a.stream);
@@ -357,7 +358,7 @@ gdn_status_t conv_step_impl(const void* x, long long x_stride, const float* w, v
     if (st != GDN_OK) return st;
     ConvArgs a{};
     a.x = x; a.x_stride = x_stride; a.w = w; a.y = y; a.cache_out = cache;
-    a.y_k = y_k; a.y_v = y_v; a.c1 = c1; a.c2 = c2;
+    a.y_k = y_k; a.y_v = y_v; a.c1 = c1; a.c2 = c2; a.bias = o.conv_bias;
     a.B = N; a.C = C; a.K = K; a.dtype = o.dtype; a.stream = static_cast<cudaStream_t>(o.stream);
     record(o, 0, a.stream);
     const cudaError_t e = launch_conv_step(a);
@@ -414,7 +415,7 @@ size_t gdn_causal_conv1d_bwd_workspace_size(int B, int T, int C, int K, const gd
     const bool packed = o.cu_seqlens != nullptr;
     const int nseq = packed ? o.num_seqs : B;
     if (nseq <= 0) return 0;
-    return conv_bwd_workspace_bytes(B, T, C, K, nseq, packed);
+    return conv_bwd_workspace_bytes(B, T, C, K, nseq, packed, o.grad_conv_bias != nullptr);
 }
 
 gdn_status_t gdn_causal_conv1d_bwd(const void* x, long long x_stride, const float* w, const void* cache_in,
@@ -437,8 +438,11 @@ gdn_status_t gdn_causal_conv1d_bwd(const void* x, long long x_stride, const floa
         if (p && !aligned16(p)) return fail(GDN_ERR_INVALID_ARG, "pointer %p is not 16-byte aligned", p);
     if (grad_w && !aligned_to(grad_w, 4)) return fail(GDN_ERR_INVALID_ARG, "grad_w must be 4-byte aligned");
     if (packed && !aligned_to(o.cu_seqlens, 4)) return fail(GDN_ERR_INVALID_ARG, "cu_seqlens must be 4-byte aligned");
-    const size_t need = conv_bwd_workspace_bytes(B, T, C, K, nseq, packed);
-    if (grad_w && (!o.workspace || o.workspace_bytes < need))
+    if (o.grad_conv_bias && !o.conv_bias) return fail(GDN_ERR_INVALID_ARG, "grad_conv_bias without a conv_bias");
+    if (!aligned_to(o.grad_conv_bias, 4)) return fail(GDN_ERR_INVALID_ARG, "grad_conv_bias must be 4-byte aligned");
+    const bool sums = grad_w || o.grad_conv_bias;
+    const size_t need = conv_bwd_workspace_bytes(B, T, C, K, nseq, packed, o.grad_conv_bias != nullptr);
+    if (sums && (!o.workspace || o.workspace_bytes < need))
         return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                     o.workspace ? o.workspace_bytes : (size_t)0);
     if (o.workspace && (reinterpret_cast<uintptr_t>(o.workspace) & 255u) != 0)
@@ -447,12 +451,12 @@ gdn_status_t gdn_causal_conv1d_bwd(const void* x, long long x_stride, const floa
     st = device_ready(&status);
     if (st != GDN_OK) return st;
     ConvArgs a{};
-    a.x = x; a.x_stride = x_stride; a.w = w; a.cache_in = cache_in;
+    a.x = x; a.x_stride = x_stride; a.w = w; a.cache_in = cache_in; a.bias = o.conv_bias;
     a.B = B; a.T = T; a.C = C; a.K = K; a.dtype = o.dtype; a.cu_seqlens = o.cu_seqlens; a.num_seqs = nseq;
     a.packed = packed; a.stream = static_cast<cudaStream_t>(o.stream); a.status = status;
     record(o, 0, a.stream);
-    const cudaError_t e = launch_conv_bwd(a, grad_y, grad_cache_out, grad_x, grad_w, grad_cache_in,
-                                          grad_w ? o.workspace : nullptr);
+    const cudaError_t e = launch_conv_bwd(a, grad_y, grad_cache_out, grad_x, grad_w, o.grad_conv_bias, grad_cache_in,
+                                          sums ? o.workspace : nullptr);
     record(o, 1, a.stream);
     if (e != cudaSuccess) return cuda_fail(e, "conv backward launch");
     return GDN_OK;

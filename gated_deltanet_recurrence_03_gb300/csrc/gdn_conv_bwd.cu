@@ -2,14 +2,14 @@
 // "qwen/deltanet.py": conv1d(groups = channels, kernel K, padding K - 1) cut to the first T outputs,
 // then SiLU; the decode cache of the learn-llm "linear attention" page holds the last K - 1 inputs).
 // With xp the inputs of a sequence padded on the left by its K - 1 cached inputs and
-//     u_t = sum_{j<K} w[c, j] xp[t + j],   y_t = silu(u_t),   du_t = dy_t silu'(u_t),
+//     u_t = sum_{j<K} w[c, j] xp[t + j] (+ bias[c]),   y_t = silu(u_t),   du_t = dy_t silu'(u_t),
 // the gradients are
 //     dxp[p] = sum_j w[c, j] du_{p - j}     (the input at p feeds the outputs p - j, j < K)
-//     dw[c, j] = sum_t du_t xp[t + j]
+//     dw[c, j] = sum_t du_t xp[t + j],   dbias[c] = sum_t du_t
 // and the outgoing cache (the last K - 1 rows of xp) passes its gradient straight to those rows.
 // Each 64-token slot of a sequence (chunk c of sequence i in slot floor(start_i / 64) + i + c) is
 // handled with its K - 1 tokens of halo on each side, so slots are independent; the slots' shares of dw
-// are added by column_sum_kernel in a fixed order.
+// are added by column_sum_kernel in a fixed order, the bias's behind the taps' in the same launch.
 #include <algorithm>
 
 #include "gdn_internal.cuh"
@@ -68,9 +68,10 @@ __device__ __forceinline__ float2 ld2<float>(const float* p) {
     return *reinterpret_cast<const float2*>(p);
 }
 
-template <typename T, int K>
+template <bool BIAS, typename T, int K>
 __global__ void __launch_bounds__(kThreads)
-conv_bwd_tile_kernel(const T* __restrict__ x, long long xs, const float* __restrict__ w, const T* __restrict__ cache_in,
+conv_bwd_tile_kernel(const T* __restrict__ x, long long xs, const float* __restrict__ w, const float* __restrict__ bias,
+                     bool want_dbias, const T* __restrict__ cache_in,
                      const T* __restrict__ dy, const T* __restrict__ dco, float* __restrict__ dx,
                      float* __restrict__ dcache, float* __restrict__ partial, const int32_t* __restrict__ cu, int nseq,
                      int T_len, int C) {
@@ -89,12 +90,17 @@ conv_bwd_tile_kernel(const T* __restrict__ x, long long xs, const float* __restr
     const int cb0 = (int)(blockIdx.x % nblk) * CB;
     const int pr = tid % P, grp = tid / P, c = cb0 + 2 * pr;
     const bool cok = c < C;
-    float* part = partial ? partial + ((size_t)slot * C + c) * K : nullptr;
+    // a slot's sums: [C][K] of the taps, then, where it is wanted, [C] of the bias
+    const bool with_db = BIAS && want_dbias;
+    const size_t slot0 = (size_t)slot * (with_db ? K + 1 : K) * C;
+    float* part = partial ? partial + slot0 + (size_t)c * K : nullptr;
+    float* part_b = partial && with_db ? partial + slot0 + (size_t)C * K + c : nullptr;
     int seq, n;
     long long t0;
     if (!conv_slot(cu, nseq, T_len, slot, seq, t0, n)) {   // an unused slot adds nothing
         if (part && cok)
             for (int i = 0; i < 2 * K; ++i) part[i] = 0.f;
+        if (part_b && cok) part_b[0] = part_b[1] = 0.f;
         return;
     }
     long long s0, s1;
@@ -133,7 +139,8 @@ conv_bwd_tile_kernel(const T* __restrict__ x, long long xs, const float* __restr
         const int r = rb + k * RPP;
         if (r < RX + RD) *reinterpret_cast<uint4*>((r < RX ? sx + r * CB : sdy + (r - RX) * CB) + q * V16N) = v[k];
     }
-    float wv[2][K], acc[2][K];
+    float wv[2][K], acc[2][K], acc_b[2] = {0.f, 0.f};
+    const float bv[2] = {BIAS && cok ? bias[c] : 0.f, BIAS && cok ? bias[c + 1] : 0.f};
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -161,7 +168,7 @@ conv_bwd_tile_kernel(const T* __restrict__ x, long long xs, const float* __restr
             float2 d = make_float2(0.f, 0.f);
             if (r < nd) {
                 const float2 g = ld2<T>(sdy + r * CB + 2 * pr);
-                float u0 = 0.f, u1 = 0.f;
+                float u0 = bv[0], u1 = bv[1];
 #pragma unroll
                 for (int j = 0; j < K; ++j) {
                     u0 = fmaf(wv[0][j], xw[j].x, u0);
@@ -176,6 +183,10 @@ conv_bwd_tile_kernel(const T* __restrict__ x, long long xs, const float* __restr
                     for (int j = 0; j < K; ++j) {
                         acc[0][j] = fmaf(d.x, xw[j].x, acc[0][j]);
                         acc[1][j] = fmaf(d.y, xw[j].y, acc[1][j]);
+                    }
+                    if constexpr (BIAS) {
+                        acc_b[0] += d.x;
+                        acc_b[1] += d.y;
                     }
                 }
             }
@@ -222,21 +233,31 @@ conv_bwd_tile_kernel(const T* __restrict__ x, long long xs, const float* __restr
             *reinterpret_cast<float2*>(dst) = gx;
         }
     }
-    // 4. the token groups' tap sums, added in group order
+    // 4. the token groups' sums of the taps (and the bias), added in group order
     __syncthreads();
-    float* red = reinterpret_cast<float*>(smem);   // [NG][P][2K] over the staged rows
+    constexpr int S = 2 * K + (BIAS ? 2 : 0);      // sums of a thread's channel pair
+    float* red = reinterpret_cast<float*>(smem);   // [NG][P][S] over the staged rows
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int j = 0; j < K; ++j) red[(grp * P + pr) * 2 * K + e * K + j] = acc[e][j];
+        for (int j = 0; j < K; ++j) red[(grp * P + pr) * S + e * K + j] = acc[e][j];
+        if constexpr (BIAS) red[(grp * P + pr) * S + 2 * K + e] = acc_b[e];
+    }
     __syncthreads();
     if (part && grp == 0 && cok) {
 #pragma unroll
         for (int i = 0; i < 2 * K; ++i) {
             float t = 0.f;
-            for (int g = 0; g < NG; ++g) t += red[(g * P + pr) * 2 * K + i];
+            for (int g = 0; g < NG; ++g) t += red[(g * P + pr) * S + i];
             part[i] = t;   // channel c + i / K, tap i % K: [c][K] then [c + 1][K]
         }
+        if (part_b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float t = 0.f;
+                for (int g = 0; g < NG; ++g) t += red[(g * P + pr) * S + 2 * K + e];
+                part_b[e] = t;
+            }
     }
 }
 
@@ -266,59 +287,66 @@ long long conv_slots(const ConvArgs& a) {
     return (ttot + kSlot - 1) / kSlot + a.num_seqs;
 }
 
-template <typename T, int K>
-cudaError_t launch_k(const ConvArgs& a, const void* dy, const void* dco, float* dx, float* dw, float* dcache,
-                     float* partial) {
+template <bool BIAS, typename T, int K>
+cudaError_t launch_one(const ConvArgs& a, const void* dy, const void* dco, float* dx, float* dw, float* dbias, float* dcache,
+                       void* workspace) {
+    float* partial = dw || dbias ? static_cast<float*>(workspace) : nullptr;
     const long long slots = conv_slots(a);
     const int T_len = a.T;
     const int32_t* cu = a.packed ? a.cu_seqlens : nullptr;
     constexpr size_t smem = tile_smem_bytes<T, K>();
     const long long blocks = slots * ((a.C + kTileRowBytes / (int)sizeof(T) - 1) / (kTileRowBytes / (int)sizeof(T)));
     if (blocks > 0) {
-        cudaError_t e = cudaFuncSetAttribute(conv_bwd_tile_kernel<T, K>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(conv_bwd_tile_kernel<BIAS, T, K>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem);
         if (e != cudaSuccess) return e;
-        conv_bwd_tile_kernel<T, K><<<(unsigned)blocks, kThreads, smem, a.stream>>>(
-            static_cast<const T*>(a.x), a.x_stride, a.w, static_cast<const T*>(a.cache_in), static_cast<const T*>(dy),
-            static_cast<const T*>(dco), dx, dcache, partial, cu, a.num_seqs, T_len, a.C);
+        conv_bwd_tile_kernel<BIAS, T, K><<<(unsigned)blocks, kThreads, smem, a.stream>>>(
+            static_cast<const T*>(a.x), a.x_stride, a.w, a.bias, dbias != nullptr, static_cast<const T*>(a.cache_in),
+            static_cast<const T*>(dy), static_cast<const T*>(dco), dx, dcache, partial, cu, a.num_seqs, T_len, a.C);
     }
     if (K > 1 && dcache) {
         const long long n = (long long)(K - 1) * a.C * a.num_seqs;
         conv_bwd_empty_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, a.stream>>>(static_cast<const T*>(dco), dcache, cu,
                                                                                    a.num_seqs, T_len, a.C, K);
     }
-    if (dw) {
-        const int CK = a.C * K;
-        column_sum_kernel<<<(CK + 31) / 32, kColSumThreads, 0, a.stream>>>(partial, slots, CK, dw);
+    if (partial) {
+        const int CK = a.C * K, cols = dbias ? CK + a.C : CK;
+        column_sum_kernel<<<(cols + 31) / 32, kColSumThreads, 0, a.stream>>>(partial, slots, cols, dw, CK, dbias);
     }
     return cudaGetLastError();
 }
 
+template <typename T, int K>
+cudaError_t launch_k(const ConvArgs& a, const void* dy, const void* dco, float* dx, float* dw, float* dbias, float* dcache,
+                     void* workspace) {
+    return a.bias ? launch_one<true, T, K>(a, dy, dco, dx, dw, dbias, dcache, workspace)
+                  : launch_one<false, T, K>(a, dy, dco, dx, dw, nullptr, dcache, workspace);
+}
+
 template <typename T>
-cudaError_t launch_t(const ConvArgs& a, const void* dy, const void* dco, float* dx, float* dw, float* dcache,
-                     float* partial) {
+cudaError_t launch_t(const ConvArgs& a, const void* dy, const void* dco, float* dx, float* dw, float* dbias, float* dcache,
+                     void* workspace) {
     switch (a.K) {
-        case 1: return launch_k<T, 1>(a, dy, dco, dx, dw, dcache, partial);
-        case 2: return launch_k<T, 2>(a, dy, dco, dx, dw, dcache, partial);
-        case 3: return launch_k<T, 3>(a, dy, dco, dx, dw, dcache, partial);
-        case 4: return launch_k<T, 4>(a, dy, dco, dx, dw, dcache, partial);
+        case 1: return launch_k<T, 1>(a, dy, dco, dx, dw, dbias, dcache, workspace);
+        case 2: return launch_k<T, 2>(a, dy, dco, dx, dw, dbias, dcache, workspace);
+        case 3: return launch_k<T, 3>(a, dy, dco, dx, dw, dbias, dcache, workspace);
+        case 4: return launch_k<T, 4>(a, dy, dco, dx, dw, dbias, dcache, workspace);
     }
     return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t conv_bwd_workspace_bytes(int B, int T, int C, int K, int nseq, bool packed) {
+size_t conv_bwd_workspace_bytes(int B, int T, int C, int K, int nseq, bool packed, bool with_bias) {
     const long long ttot = packed ? (long long)T : (long long)B * T;
     const long long slots = (ttot + kSlot - 1) / kSlot + nseq;
-    return (size_t)slots * C * K * sizeof(float);
+    return (size_t)slots * C * (K + (with_bias ? 1 : 0)) * sizeof(float);
 }
 
-cudaError_t launch_conv_bwd(const ConvArgs& a, const void* dy, const void* dco, float* dx, float* dw, float* dcache,
-                            void* workspace) {
-    float* partial = static_cast<float*>(workspace);
-    return a.dtype == GDN_BF16 ? launch_t<__nv_bfloat16>(a, dy, dco, dx, dw, dcache, partial)
-                               : launch_t<float>(a, dy, dco, dx, dw, dcache, partial);
+cudaError_t launch_conv_bwd(const ConvArgs& a, const void* dy, const void* dco, float* dx, float* dw, float* dbias,
+                            float* dcache, void* workspace) {
+    return a.dtype == GDN_BF16 ? launch_t<__nv_bfloat16>(a, dy, dco, dx, dw, dbias, dcache, workspace)
+                               : launch_t<float>(a, dy, dco, dx, dw, dbias, dcache, workspace);
 }
 
 }  // namespace gdn

@@ -258,7 +258,8 @@ cudaError_t launch_output_gate_to(const void* in, void* out, const void* z, cons
 }
 
 __global__ void __launch_bounds__(kColSumThreads)
-column_sum_kernel(const float* __restrict__ in, long long rows, int cols, float* __restrict__ out) {
+column_sum_kernel(const float* __restrict__ in, long long rows, int cols, float* __restrict__ out, int split,
+                  float* __restrict__ out2) {
     __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float t = 0.f;
@@ -272,7 +273,10 @@ column_sum_kernel(const float* __restrict__ in, long long rows, int cols, float*
         if (grp < w) red[grp][lane] += red[grp + w][lane];
         __syncthreads();
     }
-    if (grp == 0 && c < cols) out[c] = red[0][lane];
+    if (grp == 0 && c < cols) {
+        float* const dst = c < split ? out : out2;
+        if (dst) dst[c < split ? c : c - split] = red[0][lane];
+    }
 }
 
 size_t output_gate_bwd_workspace_bytes(long long rows, int dv) {

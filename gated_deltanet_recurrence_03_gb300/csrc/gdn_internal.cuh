@@ -82,6 +82,7 @@ struct ConvArgs {
     void* y_k;
     void* y_v;
     int c1, c2;
+    const float* bias;          // [C] or nullptr
 };
 
 // Launchers (return the launch error, cudaSuccess if enqueued).
@@ -375,12 +376,12 @@ void* tensor_map_encoder();
 cudaError_t launch_conv_fwd(const ConvArgs& a);
 cudaError_t launch_conv_step(const ConvArgs& a);
 // Backward of the conv + SiLU: dx [B*T, C] and dcache [nseq, K-1, C] fp32 (dcache may be NULL), dw [C, K]
-// fp32 summed over 64-token slots in a fixed order through `workspace` (conv_bwd_workspace_bytes; may be
-// NULL when dw is NULL).  dy is dense [B*T, C], dco (the outgoing cache's gradient) [nseq, K-1, C] or NULL,
+// and dbias [C] (each may be NULL) fp32 summed over 64-token slots in a fixed order through `workspace`
+// (conv_bwd_workspace_bytes; may be NULL when both are NULL).  dy is dense [B*T, C], dco (the outgoing cache's gradient) [nseq, K-1, C] or NULL,
 // both in a.dtype.
-size_t conv_bwd_workspace_bytes(int B, int T, int C, int K, int nseq, bool packed);
-cudaError_t launch_conv_bwd(const ConvArgs& a, const void* dy, const void* dco, float* dx, float* dw, float* dcache,
-                            void* workspace);
+size_t conv_bwd_workspace_bytes(int B, int T, int C, int K, int nseq, bool packed, bool with_bias);
+cudaError_t launch_conv_bwd(const ConvArgs& a, const void* dy, const void* dco, float* dx, float* dw, float* dbias,
+                            float* dcache, void* workspace);
 cudaError_t launch_decode(const DecodeArgs& a);
 cudaError_t launch_recurrent_prefill(const PrefillArgs& a);
 // out <- RMSNorm(out) * norm_weight * silu(z) over each of `rows` rows of dv values, in place.
@@ -403,9 +404,11 @@ cudaError_t launch_tc_prefill(const PrefillArgs& a, void** events, int num_event
 
 // out[c] = sum over r < rows of in[r * cols + c], for c < cols, in a fixed order (deterministic): each block
 // takes 32 columns; its 32 x 32 threads sum every 32nd row (warp-coalesced) and a shared-memory tree adds
-// the 32 partial sums.  Launch: grid ceil(cols / 32), block kColSumThreads.
+// the 32 partial sums.  Columns from `split` on go to out2[c - split]; a NULL destination is left out.
+// Launch: grid ceil(cols / 32), block kColSumThreads.
 constexpr int kColSumThreads = 1024;
-__global__ void column_sum_kernel(const float* __restrict__ in, long long rows, int cols, float* __restrict__ out);
+__global__ void column_sum_kernel(const float* __restrict__ in, long long rows, int cols, float* __restrict__ out,
+                                  int split = 0x7fffffff, float* __restrict__ out2 = nullptr);
 
 // Set the calling thread's gdn_last_error() message.
 void set_error_message(const char* msg);

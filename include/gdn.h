@@ -97,6 +97,8 @@ typedef struct gdn_opts {
     float norm_eps;             /* GDN_OUTPUT_GATE epsilon; default 1e-6 */
     float* grad_A_log;          /* gdn_recurrent_bwd with GDN_RAW_GATES: [Hv] dL/dA_log out, DEVICE; NULL = not computed */
     float* grad_dt_bias;        /* gdn_recurrent_bwd with GDN_RAW_GATES: [Hv] dL/ddt_bias out, DEVICE; NULL = not computed */
+    const float* conv_bias;     /* gdn_causal_conv1d_*: [C] added before the SiLU, DEVICE; NULL = none */
+    float* grad_conv_bias;      /* gdn_causal_conv1d_bwd: [C] dL/dconv_bias out, DEVICE; NULL = not computed */
 } gdn_opts_t;
 
 /* Fill *opts with the defaults listed above. */
@@ -201,6 +203,8 @@ gdn_status_t gdn_chunk_fwd_noalloc(const void* q, const void* k, const void* v, 
  *   cache_out  [nseq, K-1, C] dtype or NULL: the last K-1 inputs of each sequence (what a decode step
  *              needs next; for sequences shorter than K-1 the older entries come from cache_in)
  * nseq = B, or num_seqs with opts->cu_seqlens (B == 1, packed sequences, state reset at each start).
+ * opts->conv_bias ([C] float, 4-byte aligned) is added before the SiLU where it is not NULL, as the conv in front of a
+ * selective scan has it: in every call of the convolution here and below.
  * Supported: C a multiple of 8, 1 <= K <= 4.  opts->dtype, cu_seqlens, num_seqs, stream are used.
  */
 gdn_status_t gdn_causal_conv1d_fwd(const void* x, long long x_stride, const float* w, const void* cache_in,
@@ -253,6 +257,8 @@ gdn_status_t gdn_causal_conv1d_step_qkv(const void* x, long long x_stride, const
  *                    through opts->workspace (256-byte aligned, gdn_causal_conv1d_bwd_workspace_size
  *                    bytes; GDN_ERR_WORKSPACE if missing)
  *   grad_cache_in    [nseq, K-1, C] float or NULL (not written), 16-byte aligned
+ * opts->grad_conv_bias, where not NULL, receives [C] floats, the sum of du_t over all tokens, in the same fixed order (the
+ * workspace is then needed for it too, and gdn_causal_conv1d_bwd_workspace_size counts it); it needs opts->conv_bias.
  * Deterministic.  Asynchronous on opts->stream; events[0] / [1] around the kernels.
  */
 size_t gdn_causal_conv1d_bwd_workspace_size(int B, int T, int C, int K, const gdn_opts_t* opts);

@@ -11,8 +11,8 @@ import numpy as np
 from .gates import silu
 
 
-def causal_conv1d(x, w, cache_in=None, cu_seqlens=None):
-    """x [B, T, C]; w [C, K]; cache_in [nseq, K-1, C] or None.  Returns (y [B, T, C], cache_out [nseq, K-1, C])."""
+def causal_conv1d(x, w, cache_in=None, cu_seqlens=None, bias=None):
+    """x [B, T, C]; w [C, K]; cache_in [nseq, K-1, C] or None; bias [C] or None, added before the SiLU.  Returns (y [B, T, C], cache_out [nseq, K-1, C])."""
     x = np.asarray(x, dtype=np.float64)
     w = np.asarray(w, dtype=np.float64)
     B, T, C = x.shape
@@ -22,6 +22,7 @@ def causal_conv1d(x, w, cache_in=None, cu_seqlens=None):
     else:
         cu = np.asarray(cu_seqlens, dtype=np.int64)
         spans = [(0, int(cu[i]), int(cu[i + 1])) for i in range(len(cu) - 1)]
+    b0 = 0.0 if bias is None else np.asarray(bias, dtype=np.float64)
     y = np.zeros_like(x)
     cache_out = np.zeros((len(spans), K - 1, C))
     for i, (b, t0, t1) in enumerate(spans):
@@ -29,17 +30,18 @@ def causal_conv1d(x, w, cache_in=None, cu_seqlens=None):
         xp = np.concatenate([past, x[b, t0:t1]], axis=0)          # [K-1 + n, C]
         for t in range(t1 - t0):
             window = xp[t:t + K]                                  # oldest first; last row = token t
-            y[b, t0 + t] = silu(np.sum(w.T * window, axis=0))
+            y[b, t0 + t] = silu(np.sum(w.T * window, axis=0) + b0)
         cache_out[i] = xp[xp.shape[0] - (K - 1):] if K > 1 else np.zeros((0, C))
     return y, cache_out
 
 
-def causal_conv1d_backward(x, w, dy, cache_in=None, cu_seqlens=None, dcache_out=None):
+def causal_conv1d_backward(x, w, dy, cache_in=None, cu_seqlens=None, dcache_out=None, bias=None):
     """Gradients through causal_conv1d given dy = dL/dy [B, T, C] (and dcache_out = dL/dcache_out
     [nseq, K-1, C] or None): with xp the cache-padded inputs of a sequence and u_t = sum_j w[:, j] xp[t + j]
     the pre-activation of token t, du_t = dy_t silu'(u_t), dxp[t + j] += w[:, j] du_t and
     dw[:, j] += du_t xp[t + j]; the cache_out rows are copies of the last K - 1 rows of xp.
-    Returns (dx [B, T, C], dw [C, K], dcache_in [nseq, K-1, C]) in fp64."""
+    Returns (dx [B, T, C], dw [C, K], dcache_in [nseq, K-1, C]) in fp64, and with a bias [C] (then a term of u_t) a
+    fourth, dbias [C] = the sum of du_t."""
     from .gates import silu_grad
     x = np.asarray(x, dtype=np.float64)
     w = np.asarray(w, dtype=np.float64)
@@ -52,7 +54,8 @@ def causal_conv1d_backward(x, w, dy, cache_in=None, cu_seqlens=None, dcache_out=
         cu = np.asarray(cu_seqlens, dtype=np.int64)
         spans = [(0, int(cu[i]), int(cu[i + 1])) for i in range(len(cu) - 1)]
     dx = np.zeros_like(x)
-    dw = np.zeros((C, K))
+    b0 = 0.0 if bias is None else np.asarray(bias, dtype=np.float64)
+    dw, db = np.zeros((C, K)), np.zeros(C)
     dcache = np.zeros((len(spans), K - 1, C))
     for i, (b, t0, t1) in enumerate(spans):
         past = np.zeros((K - 1, C)) if cache_in is None else np.asarray(cache_in[i], dtype=np.float64)
@@ -60,11 +63,12 @@ def causal_conv1d_backward(x, w, dy, cache_in=None, cu_seqlens=None, dcache_out=
         dxp = np.zeros_like(xp)
         for t in range(t1 - t0):
             window = xp[t:t + K]
-            du = dy[b, t0 + t] * silu_grad(np.sum(w.T * window, axis=0))
+            du = dy[b, t0 + t] * silu_grad(np.sum(w.T * window, axis=0) + b0)
             dxp[t:t + K] += w.T * du
             dw += (window * du).T
+            db += du
         if dcache_out is not None and K > 1:
             dxp[xp.shape[0] - (K - 1):] += np.asarray(dcache_out[i], dtype=np.float64)
         dx[b, t0:t1] = dxp[K - 1:]
         dcache[i] = dxp[:K - 1]
-    return dx, dw, dcache
+    return (dx, dw, dcache) if bias is None else (dx, dw, dcache, db)

@@ -32,7 +32,7 @@ def plain_layer(ex, layer, x, b):
     """The layer's prompt from empty caches in fp64, elementary torch operations: what autograd differentiates."""
     import torch.nn.functional as F
     L = {k: getattr(layer, k).double().requires_grad_(True)
-         for k in ("norm", "norm_bias", "w_in", "w_x", "w_dt", "w_o", "taps", "A_log", "skip", "dt_bias")}
+         for k in ("norm", "norm_bias", "w_in", "w_x", "w_dt", "w_o", "taps", "conv_bias", "A_log", "skip", "dt_bias")}
     L["x"] = x.requires_grad_(True)
     T = x.shape[1]
     r = x + b
@@ -40,7 +40,7 @@ def plain_layer(ex, layer, x, b):
     n = d / torch.sqrt(d.square().mean(-1, keepdim=True) + 1e-5) * L["norm"] + L["norm_bias"]
     u, z = (n @ L["w_in"]).split(ex.D, -1)
     u = F.pad(u, (0, 0, ex.K - 1, 0))
-    u = F.silu(sum(u[:, i:i + T] * L["taps"][:, i] for i in range(ex.K)))
+    u = F.silu(sum(u[:, i:i + T] * L["taps"][:, i] for i in range(ex.K)) + L["conv_bias"])
     low, B, C = (u @ L["w_x"]).split([ex.RANK, ex.N, ex.N], -1)
     dt = F.softplus(low @ L["w_dt"] + L["dt_bias"])
     h, ys = 0.0, []
