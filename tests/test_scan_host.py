@@ -164,3 +164,16 @@ def test_binding_refuses_wrong_tensors():
         api.gdn_selective_scan_fwd(every, u, A, B, B)
     with pytest.raises(ValueError):
         api.gdn_selective_scan_step(u[0], u[0], A, B[0], B[0], torch.zeros(3, 16, 8))   # three states for four rows
+
+
+@pytest.mark.parametrize("i", range(5))
+def test_strides_up_to_two_to_the_24(lib, i):
+    """What a kernel steps over at once stays within 32 bits: a longer stride is refused, the longest one is not."""
+    at = lambda v: tuple(v if j == i else 0 for j in range(5))   # noqa: E731
+    for what in ("fwd", "step", "bwd"):
+        assert scan(lib, what, strides=at(2 ** 24 + 8)) == ARG
+        # past the strides' check: refused for what comes behind it
+        assert scan(lib, what, strides=at(2 ** 24), ptrs={"A_log": FAKE + 4}) == ARG and b"stride" not in lib.gdn_last_error()
+    if i >= 2:
+        g = tuple(2 ** 24 + 8 if j == i - 2 else 0 for j in range(3))
+        assert scan(lib, "bwd", g=g) == ARG and b"stride" in lib.gdn_last_error()
