@@ -333,10 +333,14 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
                     gB[i] = s == 0 ? mul2(lam[s][i], all2(dd.y)) : fma2(lam[s][i], all2(dd.y), gB[i]);
                     y = i == 0 ? mul2(hh, C[i]) : fma2(hh, C[i], y);
                     q = i == 0 ? mul2(lam[s][i], B[i]) : fma2(lam[s][i], B[i], q);
-                    lam[s][i] = mul2(lam[s][i], decay(A2[s][i], dd.x));
-                    const float2 w = mul2(lam[s][i], prev);
+                    const float2 down = mul2(lam[s][i], decay(A2[s][i], dd.x)), w = mul2(down, prev);
                     r = i == 0 ? mul2(w, A2[s][i]) : fma2(w, A2[s][i], r);
-                    gA[s][i] = fma2(w, all2(dd.x), gA[s][i]);
+                    // behind the end too, dt = 0 leaves both as they are, but for 0 times an infinite state and a rate that
+                    // is no number
+                    if (k < tokens) {
+                        lam[s][i] = down;
+                        gA[s][i] = fma2(w, all2(dd.x), gA[s][i]);
+                    }
                 }
                 part[0][s] = y.x + y.y;
                 part[1][s] = q.x + q.y;
