@@ -497,7 +497,11 @@ __global__ void __launch_bounds__(kSumCols * kSumRows) scan_sums_kernel(const __
     if (rate) {
         if (!a.gA) return;
         const float4 l = *reinterpret_cast<const float4*>(a.A_log + c);
-        *reinterpret_cast<float4*>(a.gA + c) = make_float4(-expf(l.x) * s.x, -expf(l.y) * s.y, -expf(l.z) * s.z, -expf(l.w) * s.w);
+        auto rate = [](float A_log) {   // finite, as in the walk: no state is left there, and the sum it takes is 0
+            const float A = -expf(A_log);
+            return A < -3e38f ? -3e38f : A;
+        };
+        *reinterpret_cast<float4*>(a.gA + c) = make_float4(rate(l.x) * s.x, rate(l.y) * s.y, rate(l.z) * s.z, rate(l.w) * s.w);
     } else {
         float* to = c < DN + a.D ? a.gskip : a.gbias;
         if (to) *reinterpret_cast<float4*>(to + (c < DN + a.D ? c - DN : c - DN - a.D)) = s;
