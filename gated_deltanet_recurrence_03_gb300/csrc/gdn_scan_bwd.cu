@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_ends_kernel(const __grid
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     if (l.ch[s] >= tile.n) continue;
-                    const size_t row = (size_t)slot * (a.seg / kChunk) + (t + k0) / kChunk, d = tile.d0 + l.ch[s];
+                    const size_t row = scan_chunk_row(u) + (t + k0) / kChunk, d = tile.d0 + l.ch[s];
                     store_states(a.chunks + row * DN + d * N + l.n0, h[s]);
                     if (l.n0 == 0) a.chunk_dt[row * a.D + d] = sum_dt[s];
                 }
@@ -204,8 +204,9 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
     const bool some = own.c4 < tile.n;
     const size_t DN = (size_t)a.D * N;
     ScanUnit u;
-    if (!scan_unit_at(a.cu, a.T, a.nseq, a.seg, slot, u)) u.t0 = u.t1 = 0, u.first = false;
+    if (!scan_unit_at(a.cu, a.T, a.nseq, a.seg, slot, u)) u.t0 = u.t1 = u.seq = 0, u.first = false;
     const int len = (int)(u.t1 - u.t0), chunks = (len + K - 1) / K;
+    const size_t chunk_row = scan_chunk_row(u);
     float* const part_A = a.part_A + (size_t)slot * DN;
     float* const part_s = a.part_s + (size_t)slot * 2 * a.D + tile.d0;
     auto channel = [&](int s) { return (size_t)(tile.d0 + l.ch[s]); };
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
                             (ok ? (u.t0 + t + k % K) * (c ? a.c_stride : a.b_stride) + (size_t)tile.g * N + n : 0);
             copy_async(tc::smem_u32(&sm.bc_rows[st][k][n]), from, ok, T{});
         }
-        const float* state = a.chunks + ((size_t)slot * (a.seg / K) + t / K) * DN;
+        const float* state = a.chunks + (chunk_row + t / K) * DN;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {   // nothing before the first chunk
             const bool ok = t > 0 && l.ch[s] < tile.n;
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
     auto ask_cum = [&](int c) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-            cum[s] = c > 0 && l.ch[s] < tile.n ? a.chunk_dt[((size_t)slot * (a.seg / K) + c) * a.D + channel(s)] : 0.f;
+            cum[s] = c > 0 && l.ch[s] < tile.n ? a.chunk_dt[(chunk_row + c) * a.D + channel(s)] : 0.f;
     };
     if (chunks > 0) ask(0, (chunks - 1) * K), ask_cum(chunks - 1);
     for (int c = chunks - 1; c >= 0; --c) {
@@ -556,8 +557,9 @@ ScanBwdLayout scan_bwd_layout(long long tokens, int D, int G, int N, int nseq) {
     place(slots * DN);   // the states
     l.adjoints = place(slots * DN);
     l.sum_dt = place(slots * D);
-    l.chunks = place(slots * (l.seg / kChunk) * DN);
-    l.chunk_dt = place(slots * (l.seg / kChunk) * D);
+    const size_t rows = (size_t)(tokens / kChunk + nseq);
+    l.chunks = place(rows * DN);
+    l.chunk_dt = place(rows * D);
     l.part_A = place(slots * DN);
     l.part_s = place(slots * 2 * D);
     l.part_bc = place((size_t)tiles * tokens * 2 * N);

@@ -48,6 +48,12 @@ __device__ __forceinline__ bool scan_unit_at(const int32_t* cu, int T, int nseq,
     return true;
 }
 
+// The row of a segment's first chunk among the chunks of kScanChunk tokens of all sequences; its others follow.  Segments are
+// whole chunks but for a sequence's last, so that chunk c of sequence i is row floor(start_i / kScanChunk) + i + c, and all are
+// below floor(tokens / kScanChunk) + nseq.
+static_assert(kScanMinSegment % kScanChunk == 0, "segments are whole chunks");
+__device__ __forceinline__ size_t scan_chunk_row(const ScanUnit& u) { return (size_t)(u.t0 / kScanChunk + u.seq); }
+
 // Four adjacent values of a token's row as loaded, and as fp32.
 template <typename T>
 struct Raw4;
