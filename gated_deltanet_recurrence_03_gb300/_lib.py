@@ -10,6 +10,8 @@ import os
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
 
+VERSION = 400   # GDN_VERSION of the header that these declarations follow
+
 GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA, GDN_ERR_TIMEOUT, GDN_ERR_WORKSPACE = range(6)
 GDN_F32, GDN_BF16 = 0, 1
 GDN_NORMALIZE_QK = 0x1
@@ -72,6 +74,11 @@ def load(path: str = LIB_PATH):
         raise ImportError(f"libgdn.so is not built ({path}); run __graft_entry__.build() "
                           "or python -m gated_deltanet_recurrence_03_gb300.build")
     lib = ctypes.CDLL(path)
+    lib.gdn_version.argtypes = []
+    lib.gdn_version.restype = ctypes.c_int
+    if lib.gdn_version() // 100 != VERSION // 100:   # another layout of GdnOpts
+        raise ImportError(f"{path} is version {lib.gdn_version()}, these declarations are of {VERSION}; run "
+                          "__graft_entry__.build() or python -m gated_deltanet_recurrence_03_gb300.build")
     vp, i, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
     opts_p = ctypes.POINTER(GdnOpts)
     lib.gdn_opts_init.argtypes = [opts_p]
@@ -145,8 +152,6 @@ def load(path: str = LIB_PATH):
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_last_error.argtypes = []
     lib.gdn_last_error.restype = ctypes.c_char_p
-    lib.gdn_version.argtypes = []
-    lib.gdn_version.restype = i
     if path == LIB_PATH:
         _lib = lib
     return lib

@@ -3,6 +3,7 @@
 // enqueued.
 #include <algorithm>
 #include <cstdarg>
+#include <cstddef>
 #include <cstdio>
 #include <cstring>
 #include <initializer_list>
@@ -10,9 +11,9 @@
 
 #include "gdn_internal.cuh"
 
-#define GDN_VERSION_MAJOR 0
-#define GDN_VERSION_MINOR 3
-#define GDN_VERSION_PATCH 0
+// A change of the struct's layout raises the minor version.
+static_assert(GDN_VERSION / 100 == 4 && sizeof(gdn_opts_t) == 144 && offsetof(gdn_opts_t, grad_conv_bias) == 136,
+              "gdn_opts_t of version 0.4");
 
 namespace gdn {
 namespace {
@@ -126,7 +127,7 @@ void gdn_opts_init(gdn_opts_t* o) {
     o->norm_eps = 1e-6f;
 }
 
-int gdn_version(void) { return GDN_VERSION_MAJOR * 10000 + GDN_VERSION_MINOR * 100 + GDN_VERSION_PATCH; }
+int gdn_version(void) { return GDN_VERSION; }
 
 const char* gdn_last_error(void) { return t_last_error; }
 

@@ -32,6 +32,9 @@
  *   clamped to [0, T]).
  * - Thread safety: calls on different streams may run concurrently; a workspace
  *   must not be shared by calls that overlap on the device.
+ * - The layout of gdn_opts_t belongs to GDN_VERSION_MAJOR.GDN_VERSION_MINOR: the library reads (and gdn_opts_init writes) the
+ *   whole struct, so a program calls only a library of the minor version that it was compiled for, which
+ *   gdn_version() / 100 == GDN_VERSION / 100 tells.
  */
 #ifndef GDN_H_
 #define GDN_H_
@@ -42,6 +45,12 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/* 0.4: gdn_opts_t has conv_bias and grad_conv_bias. */
+#define GDN_VERSION_MAJOR 0
+#define GDN_VERSION_MINOR 4
+#define GDN_VERSION_PATCH 0
+#define GDN_VERSION (GDN_VERSION_MAJOR * 10000 + GDN_VERSION_MINOR * 100 + GDN_VERSION_PATCH)
 
 typedef enum gdn_status {
     GDN_OK = 0,
@@ -550,7 +559,7 @@ const char* gdn_status_string(gdn_status_t status);
 /* Message of the last failure on the calling thread ("" if none). */
 const char* gdn_last_error(void);
 
-/* Library version: major * 10000 + minor * 100 + patch. */
+/* GDN_VERSION of the header that the library was built with: major * 10000 + minor * 100 + patch. */
 int gdn_version(void);
 
 #ifdef __cplusplus
