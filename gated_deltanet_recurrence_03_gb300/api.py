@@ -252,14 +252,14 @@ def gdn_causal_conv1d_fwd(x: torch.Tensor, w: torch.Tensor, cache_in: Optional[t
         _need("cu_seqlens", cu_seqlens, torch.int32, dev, (nseq + 1,))
     if cache_in is not None:
         _need("cache_in", cache_in, dt, dev, (nseq, K - 1, C))
-    if out is None:
-        out = torch.empty((B, T, C), dtype=dt, device=dev)
-    _need("out", out, dt, dev, (B, T, C))
-    if cache_out is None and return_cache:
-        cache_out = torch.empty((nseq, K - 1, C), dtype=dt, device=dev)
-    if cache_out is not None:
-        _need("cache_out", cache_out, dt, dev, (nseq, K - 1, C))
-    with torch.cuda.device(dev):
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((B, T, C), dtype=dt, device=dev)
+        _need("out", out, dt, dev, (B, T, C))
+        if cache_out is None and return_cache:
+            cache_out = torch.empty((nseq, K - 1, C), dtype=dt, device=dev)
+        if cache_out is not None:
+            _need("cache_out", cache_out, dt, dev, (nseq, K - 1, C))
         o, keep = _opts(lib, dt, 1.0, 64, False, stream, dev, events)
         if cu_seqlens is not None:
             o.cu_seqlens = cu_seqlens.data_ptr()
@@ -299,10 +299,10 @@ def gdn_causal_conv1d_bwd(x: torch.Tensor, w: torch.Tensor, grad_y: torch.Tensor
     if grad_cache_out is not None:
         _need("grad_cache_out", grad_cache_out, dt, dev, (nseq, K - 1, C))
     f32 = dict(dtype=torch.float32, device=dev)
-    gx = torch.empty((B, T, C), **f32)
-    gw = torch.empty((C, K), **f32) if want_grad_w else None
-    gc = torch.empty((nseq, K - 1, C), **f32) if want_grad_cache_in and K > 1 else None
-    with torch.cuda.device(dev):
+    with _on(dev, stream):
+        gx = torch.empty((B, T, C), **f32)
+        gw = torch.empty((C, K), **f32) if want_grad_w else None
+        gc = torch.empty((nseq, K - 1, C), **f32) if want_grad_cache_in and K > 1 else None
         o, keep = _opts(lib, dt, 1.0, 64, False, stream, dev, events)
         if cu_seqlens is not None:
             o.cu_seqlens = cu_seqlens.data_ptr()
@@ -339,10 +339,10 @@ def gdn_causal_conv1d_step(x: torch.Tensor, w: torch.Tensor, cache: torch.Tensor
     K = int(w.shape[1])
     _need("w", w, torch.float32, dev, (C, K))
     _need("cache", cache, dt, dev, (N, K - 1, C))
-    if out is None:
-        out = torch.empty((N, C), dtype=dt, device=dev)
-    _need("out", out, dt, dev, (N, C))
-    with torch.cuda.device(dev):
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((N, C), dtype=dt, device=dev)
+        _need("out", out, dt, dev, (N, C))
         o, keep = _opts(lib, dt, 1.0, 64, False, stream, dev, events)
         _conv_bias(o, bias, C, dev)
         st = lib.gdn_causal_conv1d_step(_ptr(x), x.stride(0), _ptr(w), _ptr(cache), _ptr(out), N, C, K,
@@ -379,15 +379,15 @@ def gdn_causal_conv1d_fwd_qkv(x: torch.Tensor, w: torch.Tensor, widths: Sequence
         _need("cu_seqlens", cu_seqlens, torch.int32, dev, (nseq + 1,))
     if cache_in is not None:
         _need("cache_in", cache_in, dt, dev, (nseq, K - 1, C))
-    if out is None:
-        out = tuple(torch.empty((B, T, c), dtype=dt, device=dev) for c in (Cq, Ck, Cv))
-    for name, y, c in zip(("y_q", "y_k", "y_v"), out, (Cq, Ck, Cv)):
-        _need(name, y, dt, dev, (B, T, c))
-    if cache_out is None and return_cache:
-        cache_out = torch.empty((nseq, K - 1, C), dtype=dt, device=dev)
-    if cache_out is not None:
-        _need("cache_out", cache_out, dt, dev, (nseq, K - 1, C))
-    with torch.cuda.device(dev):
+    with _on(dev, stream):
+        if out is None:
+            out = tuple(torch.empty((B, T, c), dtype=dt, device=dev) for c in (Cq, Ck, Cv))
+        for name, y, c in zip(("y_q", "y_k", "y_v"), out, (Cq, Ck, Cv)):
+            _need(name, y, dt, dev, (B, T, c))
+        if cache_out is None and return_cache:
+            cache_out = torch.empty((nseq, K - 1, C), dtype=dt, device=dev)
+        if cache_out is not None:
+            _need("cache_out", cache_out, dt, dev, (nseq, K - 1, C))
         o, keep = _opts(lib, dt, 1.0, 64, False, stream, dev, events)
         if cu_seqlens is not None:
             o.cu_seqlens = cu_seqlens.data_ptr()
@@ -418,11 +418,11 @@ def gdn_causal_conv1d_step_qkv(x: torch.Tensor, w: torch.Tensor, cache: torch.Te
     K = int(w.shape[1])
     _need("w", w, torch.float32, dev, (C, K))
     _need("cache", cache, dt, dev, (N, K - 1, C))
-    if out is None:
-        out = tuple(torch.empty((N, c), dtype=dt, device=dev) for c in (Cq, Ck, Cv))
-    for name, y, c in zip(("y_q", "y_k", "y_v"), out, (Cq, Ck, Cv)):
-        _need(name, y, dt, dev, (N, c))
-    with torch.cuda.device(dev):
+    with _on(dev, stream):
+        if out is None:
+            out = tuple(torch.empty((N, c), dtype=dt, device=dev) for c in (Cq, Ck, Cv))
+        for name, y, c in zip(("y_q", "y_k", "y_v"), out, (Cq, Ck, Cv)):
+            _need(name, y, dt, dev, (N, c))
         o, keep = _opts(lib, dt, 1.0, 64, False, stream, dev, events)
         _conv_bias(o, bias, C, dev)
         st = lib.gdn_causal_conv1d_step_qkv(_ptr(x), x.stride(0), _ptr(w), _ptr(cache), _ptr(out[0]), _ptr(out[1]),
