@@ -984,7 +984,7 @@ size_t gdn_selective_scan_fwd_workspace_size(int B, int T, int D, int G, int N, 
     const gdn_opts_t o = resolve(opts);
     const int nseq = o.cu_seqlens ? o.num_seqs : B;
     if (B <= 0 || T <= 0 || nseq <= 0 || !scan_dims_ok(D, G, N)) return 0;
-    return scan_fwd_layout((long long)B * T, D, N, nseq, o.cu_seqlens != nullptr).total;
+    return scan_fwd_layout((long long)B * T, D, G, N, nseq, o.cu_seqlens != nullptr, o.dtype).total;
 }
 
 gdn_status_t gdn_selective_scan_fwd(const void* u, long long u_stride, const void* delta, long long delta_stride,
@@ -1002,7 +1002,7 @@ gdn_status_t gdn_selective_scan_fwd(const void* u, long long u_stride, const voi
     if (tokens > 0 && (!u || !delta || !A_log || !Bm || !Cm || !y)) return fail(GDN_ERR_INVALID_ARG, "null input/output pointer");
     if ((st = need_aligned16({u, delta, A_log, Bm, Cm, skip, dt_bias, z, h0, y, h_final})) != GDN_OK) return st;
     if (nseq == 0) return GDN_OK;
-    const ScanFwdLayout l = tokens > 0 ? scan_fwd_layout(tokens, D, N, nseq, o.cu_seqlens != nullptr) : ScanFwdLayout{};
+    const ScanFwdLayout l = tokens > 0 ? scan_fwd_layout(tokens, D, G, N, nseq, o.cu_seqlens != nullptr, o.dtype) : ScanFwdLayout{};
     if ((st = need_workspace(o, l.total)) != GDN_OK) return st;
     unsigned* status = nullptr;
     if ((st = device_ready(&status)) != GDN_OK) return st;

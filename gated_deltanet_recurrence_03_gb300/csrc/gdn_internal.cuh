@@ -314,7 +314,7 @@ struct ScanFwdLayout {
     long long slots;
     size_t sum_dt, total;       // byte offsets (the states come first)
 };
-ScanFwdLayout scan_fwd_layout(long long tokens, int D, int N, int nseq, bool packed);
+ScanFwdLayout scan_fwd_layout(long long tokens, int D, int G, int N, int nseq, bool packed, int dtype);
 cudaError_t launch_scan_fwd(const ScanArgs& a);
 struct ScanBwdLayout {
     int seg;

@@ -465,22 +465,35 @@ cudaError_t step_n(const ScanStepArgs& a) { GDN_SCAN_N(step_typed, a) }
 
 }  // namespace
 
-// A sequence is walked by one block a channel tile where the tiles' warps are about as many as the GPU's schedulers (608),
-// else in segments, whose states are formed first: 60 % more work, but on all of them.  With 512 warps the whole walk takes
-// 357 us (2 x 8192 tokens of 4096 channels), segments about 540.  Packed sequences are taken as one long one, as lengths are
-// on the device.  At least 256 tokens a segment; about 8 x 608 warps of work in all (4 x: 452, 12 x: 430, 16 x: 457 against
+// Whole walks, a block a sequence and channel tile, or segments, whose states are formed first: 60 % more work, but on all SMs.
+// A wave of whole walks (152 blocks of four walking warps, one an SM) takes the time of its tokens however few blocks it has,
+// segments the time of all tokens x warps and some 18 us more.  The two meet where a wave's place is `wave` warps' segments and
+// the 18 us are 150,000 tokens x warps of them.  Measured, whole / segments in us a call, by warps (batch x channels x states /
+// 256), 16 states a channel, bf16:
+//     8192 tokens: 256 359 / 277, 320 359 / 347, 352 359 / 359, 384 358 / 387, 448 358 / 473, 512 359 / 527, 608 358 / 569, in
+//     two waves 640 709 / 631, 704 709 / 689, 768 709 / 773, in three 1280 1061 / 1197;  32768: 320 1411 / 1234, 384 1411 / 1519;
+//     2048: 128 96 / 55, 224 96 / 76, 288 96 / 94, 384 95 / 121;  1024: 128 51 / 39, 224 51 / 55
+// fp32, one block of segments an SM in place of two:
+//     8192 tokens: 256 375 / 335, 288 373 / 373, 384 373 / 467, 512 373 / 629, 640 740 / 758;  2048: 224 99 / 90, 288 99 / 113
+// and with 8 states a channel, shorter tiles, 8192 tokens: bf16 320 509 / 461, 368 512 / 509, 448 511 / 632, fp32 288 544 / 510,
+// 320 546 / 568.  Near the border the choice costs 5 % at most.
+// Packed sequences are taken as one long one, the worst case of their lengths, which are on the device: several share a wave.
+// A segment has at least 256 tokens, and there are about 8 x 608 warps of work in all (4 x: 452, 12 x: 430, 16 x: 457 against
 // 428 us for 46,547 packed tokens of 1024 channels).
-int scan_fwd_segment(long long tokens, int D, int N, int nseq, bool packed) {
-    const long long warps = (long long)D * N / 256 * (packed ? 1 : nseq);   // at work at once, in the worst case
-    if (warps >= 500) return 0;
+static int scan_fwd_segment(long long tokens, int D, int G, int N, int nseq, bool packed, int dtype) {
+    const long long T = packed ? tokens : tokens / nseq;
+    const int ch = 2 * kScanThreads / (N / 4);
+    const long long blocks = (long long)G * ((D / G + ch - 1) / ch) * (packed ? 1 : nseq);
+    const long long waves = packed ? 1 : (blocks + 151) / 152, wave = (dtype == GDN_BF16 ? 360 : 310) + (N == 8 ? 30 : 0);
+    if (waves * T * wave <= 4 * blocks * T + 150000) return 0;
     const long long want = 8 * 608;   // warps
     const long long per = tokens * std::max(1LL, (long long)D * N / 256) / want;
     const long long seg = std::max(256LL, (per + 63) / 64 * 64);
-    return tokens / (packed ? 1 : nseq) <= seg ? 0 : (int)std::min<long long>(seg, 1 << 20);
+    return T <= seg ? 0 : (int)std::min<long long>(seg, 1 << 20);
 }
-ScanFwdLayout scan_fwd_layout(long long tokens, int D, int N, int nseq, bool packed) {
+ScanFwdLayout scan_fwd_layout(long long tokens, int D, int G, int N, int nseq, bool packed, int dtype) {
     ScanFwdLayout l{};
-    l.seg = scan_fwd_segment(tokens, D, N, nseq, packed);
+    l.seg = scan_fwd_segment(tokens, D, G, N, nseq, packed, dtype);
     l.slots = l.seg ? tokens / l.seg + nseq : nseq;
     if (l.seg) {
         l.sum_dt = ((size_t)l.slots * D * N * 4 + 255) / 256 * 256;
