@@ -882,7 +882,8 @@ def gdn_selective_scan_fwd(u: torch.Tensor, delta: torch.Tensor, A_log: torch.Te
     dt u B, y = (sum_n C h + skip u) silu(z).  u, delta and z (or None: no gate) [B, T, D], B and C [B, T, G, N] (bf16 or
     fp32; slices of packed projections are taken as they are); A_log fp32 [D, N] with N of 8, 16, 32 or 64; skip and
     dt_bias fp32 [D] or None (0); h0 [nseq, D, N] fp32 or None.  Channel d reads B and C of group d // (D // G).  With
-    ``cu_seqlens`` (int32 device tensor of nseq+1 offsets) the batch must be 1.  Returns (y [B, T, D], h_final or None)."""
+    ``cu_seqlens`` (int32 device tensor of nseq+1 offsets) the batch must be 1.  ``out`` overlaps no input; ``h_final`` may be
+    ``h0``.  Returns (y [B, T, D], h_final or None)."""
     lib = L.load()
     dev, dt, D, G, N, args = _scan_inputs(u, delta, A_log, B, C, skip, dt_bias, z, 2)
     nB, T = u.shape[:2]
@@ -915,7 +916,8 @@ def gdn_selective_scan_step(u: torch.Tensor, delta: torch.Tensor, A_log: torch.T
                             events: Optional[Sequence[int]] = None) -> torch.Tensor:
     """One token for each of N rows through gdn_selective_scan_fwd's recurrence.  u, delta, z [N, D]; B, C [N, G, states];
     h [pool, D, states] fp32, updated in place.  ``slots`` (int32 [N]) names each row's state in the pool (None: row n,
-    state n); a row whose slot is outside the pool (-1, say) is idle and gets zeros.  Returns y [N, D]."""
+    state n); a row whose slot is outside the pool (-1, say) is idle and gets zeros; ``out``
+    overlaps no input.  Returns y [N, D]."""
     lib = L.load()
     dev, dt, D, G, N, args = _scan_inputs(u, delta, A_log, B, C, skip, dt_bias, z, 1)
     rows = u.shape[0]
@@ -944,9 +946,10 @@ def gdn_selective_scan_bwd(u: torch.Tensor, delta: torch.Tensor, A_log: torch.Te
                            events: Optional[Sequence[int]] = None):
     """Gradients of a loss on (y, h_final) of gdn_selective_scan_fwd.  Inputs as there; grad_y like y (dense);
     grad_h_final fp32 like h_final or None.  ``grads`` = (grad_B, grad_C, grad_z) receives those three where given
-    (slices of packed gradients, say; grad_z None without z).  Returns (grad_u, grad_delta in u's type, grad_A_log fp32,
-    grad_B, grad_C in u's type, grad_skip, grad_dt_bias fp32 or None where the input is None, grad_z in u's type or None,
-    grad_h0 fp32 or None)."""
+    (slices of packed gradients, say; grad_z None without z; none overlaps an input or another one).  The scratch, about
+    D (N / 2 + N^2 / 128) bytes a token and 16 D N a sequence, is allocated where ``workspace`` is not large enough for it.
+    Returns (grad_u, grad_delta in u's type, grad_A_log fp32, grad_B, grad_C in u's type, grad_skip, grad_dt_bias fp32 or
+    None where the input is None, grad_z in u's type or None, grad_h0 fp32 or None)."""
     lib = L.load()
     dev, dt, D, G, N, args = _scan_inputs(u, delta, A_log, B, C, skip, dt_bias, z, 2)
     nB, T = u.shape[:2]

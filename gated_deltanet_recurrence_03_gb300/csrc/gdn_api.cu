@@ -971,8 +971,10 @@ gdn_status_t scan_sequences(int B, int T, int D, int G, int N, const gdn_opts_t&
     *nseq = o.cu_seqlens ? o.num_seqs : B;
     // tiles of at least 8 channels of a group and vectors of four states, for each sequence and segment
     const long long slots = *nseq + tokens / kScanMinSegment, tiles = std::max((long long)D / 8, (long long)D * N / 512 + 1);
-    if (slots > kMaxBlocks / tiles) return fail(GDN_ERR_INVALID_ARG, "%lld tokens in %d sequences of %d channels are too many", tokens, *nseq, D);
-    if (tokens * ((long long)G * N / 2) / 256 >= kMaxBlocks / 2) return fail(GDN_ERR_INVALID_ARG, "%lld tokens of %d groups are too many", tokens, G);
+    if (slots > kMaxBlocks / tiles)
+        return fail(GDN_ERR_INVALID_ARG, "%lld tokens in %d sequences of %d channels are too many", tokens, *nseq, D);
+    if (tokens * ((long long)G * N / 2) / 256 >= kMaxBlocks / 2)
+        return fail(GDN_ERR_INVALID_ARG, "%lld tokens of %d groups are too many", tokens, G);
     return GDN_OK;
 }
 
@@ -999,10 +1001,12 @@ gdn_status_t gdn_selective_scan_fwd(const void* u, long long u_stride, const voi
     int nseq = 0;
     if ((st = scan_sequences(B, T, D, G, N, o, &nseq)) != GDN_OK) return st;
     const long long tokens = (long long)B * T;
-    if (tokens > 0 && (!u || !delta || !A_log || !Bm || !Cm || !y)) return fail(GDN_ERR_INVALID_ARG, "null input/output pointer");
+    if (tokens > 0 && (!u || !delta || !A_log || !Bm || !Cm || !y))
+        return fail(GDN_ERR_INVALID_ARG, "null input/output pointer");
     if ((st = need_aligned16({u, delta, A_log, Bm, Cm, skip, dt_bias, z, h0, y, h_final})) != GDN_OK) return st;
     if (nseq == 0) return GDN_OK;
-    const ScanFwdLayout l = tokens > 0 ? scan_fwd_layout(tokens, D, G, N, nseq, o.cu_seqlens != nullptr, o.dtype) : ScanFwdLayout{};
+    ScanFwdLayout l{};
+    if (tokens > 0) l = scan_fwd_layout(tokens, D, G, N, nseq, o.cu_seqlens != nullptr, o.dtype);
     if ((st = need_workspace(o, l.total)) != GDN_OK) return st;
     unsigned* status = nullptr;
     if ((st = device_ready(&status)) != GDN_OK) return st;

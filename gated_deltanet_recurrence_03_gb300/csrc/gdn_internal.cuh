@@ -287,8 +287,8 @@ struct ScanArgs {
     float* states;
     float* adjoints;
     float* sum_dt;
-    float* chunks;              // gradients: a segment's contributions to the states before its chunks, [rows][D][N] (scan_chunk_row),
-    float* chunk_dt;            // and its sums of dt to there, [rows][D]
+    float* chunks;              // gradients: a segment's contributions to the states before its chunks, [rows][D][N]
+    float* chunk_dt;            // and its sums of dt to there, [rows][D] (scan_chunk_row)
     // gradients
     const void* gy;             // [tokens][D]
     const float* gh;            // [nseq][D][N] or nullptr (zeros)

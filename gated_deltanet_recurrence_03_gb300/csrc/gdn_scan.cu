@@ -157,8 +157,10 @@ struct MainShape {
     static constexpr size_t kSums = sizeof(float) * 2 * K * kRow;
 };
 template <int N, typename T, bool SEG>
-__global__ void __launch_bounds__(kScanThreads + helpers(SEG), SEG && sizeof(T) == 2 ? 2 : 1) scan_main_kernel(const __grid_constant__ ScanArgs a) {
-    constexpr int L = ScanShape<N>::L, CH = ScanShape<N>::CH, P = ScanShape<N>::P, K = MainShape<N>::K, M = helpers(SEG), kRow = MainShape<N>::kRow;
+__global__ void __launch_bounds__(kScanThreads + helpers(SEG), SEG && sizeof(T) == 2 ? 2 : 1)
+scan_main_kernel(const __grid_constant__ ScanArgs a) {
+    constexpr int L = ScanShape<N>::L, CH = ScanShape<N>::CH, P = ScanShape<N>::P;
+    constexpr int K = MainShape<N>::K, M = helpers(SEG), kRow = MainShape<N>::kRow;
     using S = Share<N, K, M>;
     // arrays of their own, so that what is stored to the sums does not hold back the next tokens' loads
     __shared__ __align__(16) float2 s_dt[2][K][CH];
@@ -348,7 +350,8 @@ struct StepRow {
 };
 constexpr int kStepStates = 8, kStepBlocks = 6;   // states a lane, blocks an SM
 template <int N, typename T>
-__global__ void __launch_bounds__(kScanThreads, kStepBlocks) scan_step_kernel(const __grid_constant__ ScanStepArgs a, int splits) {
+__global__ void __launch_bounds__(kScanThreads, kStepBlocks)
+scan_step_kernel(const __grid_constant__ ScanStepArgs a, int splits) {
     constexpr int L = N / kStepStates, CH = kScanThreads / L;
     const int tiles = (a.D + CH - 1) / CH, split = blockIdx.x / tiles;
     const int d = blockIdx.x % tiles * CH + threadIdx.x / L, n0 = threadIdx.x % L * kStepStates;
@@ -399,8 +402,10 @@ __global__ void __launch_bounds__(kScanThreads, kStepBlocks) scan_step_kernel(co
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float4 b = x.b[i].f(), c = x.c[i].f();
-                const float2 p = fma2(decay(A[2 * i], dt), make_float2(x.h[i].x, x.h[i].y), mul2(make_float2(b.x, b.y), all2(w)));
-                const float2 q = fma2(decay(A[2 * i + 1], dt), make_float2(x.h[i].z, x.h[i].w), mul2(make_float2(b.z, b.w), all2(w)));
+                const float2 p = fma2(decay(A[2 * i], dt), make_float2(x.h[i].x, x.h[i].y),
+                                      mul2(make_float2(b.x, b.y), all2(w)));
+                const float2 q = fma2(decay(A[2 * i + 1], dt), make_float2(x.h[i].z, x.h[i].w),
+                                      mul2(make_float2(b.z, b.w), all2(w)));
                 __stcs(reinterpret_cast<float4*>(x.at) + i, make_float4(p.x, p.y, q.x, q.y));
                 y = fma2(p, make_float2(c.x, c.y), fma2(q, make_float2(c.z, c.w), y));
             }
@@ -465,21 +470,23 @@ cudaError_t step_n(const ScanStepArgs& a) { GDN_SCAN_N(step_typed, a) }
 
 }  // namespace
 
-// Whole walks, a block a sequence and channel tile, or segments, whose states are formed first: 60 % more work, but on all SMs.
-// A wave of whole walks (152 blocks of four walking warps, one an SM) takes the time of its tokens however few blocks it has,
-// segments the time of all tokens x warps and some 18 us more.  The two meet where a wave's place is `wave` warps' segments and
-// the 18 us are 150,000 tokens x warps of them.  Measured, whole / segments in us a call, by warps (batch x channels x states /
-// 256), 16 states a channel, bf16:
-//     8192 tokens: 256 359 / 277, 320 359 / 347, 352 359 / 359, 384 358 / 387, 448 358 / 473, 512 359 / 527, 608 358 / 569, in
-//     two waves 640 709 / 631, 704 709 / 689, 768 709 / 773, in three 1280 1061 / 1197;  32768: 320 1411 / 1234, 384 1411 / 1519;
-//     2048: 128 96 / 55, 224 96 / 76, 288 96 / 94, 384 95 / 121;  1024: 128 51 / 39, 224 51 / 55
-// fp32, one block of segments an SM in place of two:
-//     8192 tokens: 256 375 / 335, 288 373 / 373, 384 373 / 467, 512 373 / 629, 640 740 / 758;  2048: 224 99 / 90, 288 99 / 113
-// and with 8 states a channel, shorter tiles, 8192 tokens: bf16 320 509 / 461, 368 512 / 509, 448 511 / 632, fp32 288 544 / 510,
-// 320 546 / 568.  Near the border the choice costs 5 % at most.
-// Packed sequences are taken as one long one, the worst case of their lengths, which are on the device: several share a wave.
-// A segment has at least 256 tokens, and there are about 8 x 608 warps of work in all (4 x: 452, 12 x: 430, 16 x: 457 against
-// 428 us for 46,547 packed tokens of 1024 channels).
+// Whole walks, a block a sequence and channel tile, or segments, whose states are formed first: 60 % more work, on all SMs.
+// A wave of whole walks (152 blocks of four walking warps, one an SM) takes the time of its tokens however few its blocks,
+// segments that of all tokens x warps and some 18 us more.  The two meet where a wave costs as much as segments of `wave`
+// warps, the 18 us being 150,000 tokens x warps of them.  Measured, whole / segments in us a call, by warps (batch x channels
+// x states / 256), 16 states a channel, bf16:
+//   8192 tokens: 256 359 / 277, 320 359 / 347, 352 359 / 359, 384 358 / 387, 448 358 / 473, 512 359 / 527, 608 358 / 569,
+//     in two waves 640 709 / 631, 704 709 / 689, 768 709 / 773, in three 1280 1061 / 1197;
+//   32768: 320 1411 / 1234, 384 1411 / 1519;  2048: 128 96 / 55, 224 96 / 76, 288 96 / 94, 384 95 / 121;
+//   1024: 128 51 / 39, 224 51 / 55;
+// fp32, whose segments' vectors leave registers for one block an SM in place of two:
+//   8192 tokens: 256 375 / 335, 288 373 / 373, 384 373 / 467, 512 373 / 629, 640 740 / 758;
+//   2048: 224 99 / 90, 288 99 / 113;
+// 8 states a channel, shorter tiles, 8192 tokens:
+//   bf16 320 509 / 461, 368 512 / 509, 448 511 / 632;  fp32 288 544 / 510, 320 546 / 568.
+// Near the border the choice costs 5 % at most.  Packed sequences are taken as one long one, the worst case of their lengths,
+// which are on the device: several share a wave.  A segment has at least 256 tokens, and there are about 8 x 608 warps of
+// work in all (4 x: 452, 12 x: 430, 16 x: 457 against 428 us for 46,547 packed tokens of 1024 channels).
 static int scan_fwd_segment(long long tokens, int D, int G, int N, int nseq, bool packed, int dtype) {
     const long long T = packed ? tokens : tokens / nseq;
     const int ch = 2 * kScanThreads / (N / 4);

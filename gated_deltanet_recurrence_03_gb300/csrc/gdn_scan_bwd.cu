@@ -11,14 +11,18 @@
 // (dB, dC) leave as one partial sum a tile, sums over tokens (dA_log, dskip, dbias) as one a segment; the last kernel adds
 // them in order.
 //
-// 2 x 8192 tokens of 4096 channels of 16 states, bf16: 1632 us (first walk 425, join 29, chunks 1143, sums 25).  Bound by
-// instructions and shared memory together: a warp's token of two channels and four states a lane is about 200 instructions,
-// 12 of them exchanges; issue slots 58 %, shared-memory pipe 61 %, fp32 pipe 43 %, at 168 registers (three blocks an SM;
-// two 5 % slower, four spill and are 3 % slower).  HBM would take 139 us, three exponentials a state and token 345 us.
+// 2 x 8192 tokens of 4096 channels of 16 states, bf16: 1605 us (first walk 428, join 29, chunks 1113, sums 26).  Bound by
+// instructions and shared memory together: a warp's token of two channels and four states a lane is about 220 instructions,
+// 12 of them exchanges; issue slots 64 %, shared-memory pipe 61 %, fp32 pipe 45 %, at 166 registers (three blocks an SM;
+// two 5 % slower, four spill and are 3 % slower).  HBM would take 139 us for each tensor once, some 380 us for the 2.6 GB
+// that this method moves (u, delta, z and dy twice, the states before the chunks and the partial sums of B and C written and
+// read), three exponentials a state and token 345 us.
 // From 2857 us: raw rows by asynchronous copies, no bank conflicts, h kept rather than a h 1877; no state walked twice for
-// the chunks' starts 1687; four blocks an SM in the first walk 1656; a chunk's sum of dt asked for ahead 1636; one launch of sums 1632.  Not kept:
-// eight states a lane with 6-token chunks (602 against 519 us for 2 x 2048 tokens: spills), a's held from one walk for the
-// other (spills), segments in the chunks' kernel from states kept in shared memory (520 us).
+// the chunks' starts 1687; four blocks an SM in the first walk 1656; a chunk's sum of dt asked for ahead 1636; one launch of
+// sums 1632; lam and dA under a condition in a sequence's last chunk, which leaves no register to spill, 1597 - 1605.  Not
+// kept: eight states a lane with 6-token chunks (602 against 519 us for 2 x 2048 tokens: spills), a's held from one walk for
+// the other (spills), segments in the chunks' kernel from states kept in shared memory (520 us), the chunks' rows found anew
+// from the segment at every chunk (1634 us: spills).
 #include <algorithm>
 
 #include "norm_rows.cuh"
@@ -97,7 +101,8 @@ __global__ void __launch_bounds__(kScanThreads, 4) scan_ends_kernel(const __grid
         for (int v = 0; v < BC; ++v) {
             const int i = tid + v * kScanThreads, which = i / (K * N / 4), k = i / (N / 4) % K, n = i % (N / 4) * 4;
             const T* p = static_cast<const T*>(which == 0 ? a.B : a.C) + (size_t)tile.g * N + n;
-            rbc[v] = which < 2 && t + k < len ? load4(p + (u.t0 + t + k) * (which == 0 ? a.b_stride : a.c_stride)) : Raw4<T>::zero();
+            const long long stride = which == 0 ? a.b_stride : a.c_stride;
+            rbc[v] = which < 2 && t + k < len ? load4(p + (u.t0 + t + k) * stride) : Raw4<T>::zero();
         }
     };
     if (len > 0) load(0);
@@ -309,7 +314,8 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_bwd_kernel(const __grid_
                 const float2 dd = s_dt[k][l.ch[s]];
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    hs[k][s][i] = fma2(decay(A2[s][i], dd.x), k ? hs[k ? k - 1 : 0][s][i] : before[s][i], mul2(B[i], all2(dd.y)));
+                    hs[k][s][i] = fma2(decay(A2[s][i], dd.x), k ? hs[k ? k - 1 : 0][s][i] : before[s][i],
+                                       mul2(B[i], all2(dd.y)));
             }
         }
         // the decays are formed again: held from here, they would take as many registers as the states
@@ -523,7 +529,8 @@ cudaError_t bwd_typed(const ScanArgs& a) {
     constexpr int kThreads = kSumCols * kSumRows;
     const long long bc = ((long long)a.tokens * a.G * N / 2 + kThreads - 1) / kThreads;
     const long long cols = ((long long)a.D * N + 2 * a.D) / 4;
-    scan_sums_kernel<T><<<(unsigned)(bc + (cols + kSumCols - 1) / kSumCols), kThreads, 0, a.stream>>>(a, per_group, (unsigned)bc);
+    const unsigned blocks_of_sums = (unsigned)(bc + (cols + kSumCols - 1) / kSumCols);
+    scan_sums_kernel<T><<<blocks_of_sums, kThreads, 0, a.stream>>>(a, per_group, (unsigned)bc);
     return cudaGetLastError();
 }
 template <typename T>

@@ -48,9 +48,9 @@ __device__ __forceinline__ bool scan_unit_at(const int32_t* cu, int T, int nseq,
     return true;
 }
 
-// The row of a segment's first chunk among the chunks of kScanChunk tokens of all sequences; its others follow.  Segments are
-// whole chunks but for a sequence's last, so that chunk c of sequence i is row floor(start_i / kScanChunk) + i + c, and all are
-// below floor(tokens / kScanChunk) + nseq.
+// The row of a segment's first chunk among the chunks of kScanChunk tokens of all sequences; its others follow.  Segments
+// are whole chunks but for a sequence's last, so that chunk c of sequence i is row floor(start_i / kScanChunk) + i + c, and
+// all are below floor(tokens / kScanChunk) + nseq.
 static_assert(kScanMinSegment % kScanChunk == 0, "segments are whole chunks");
 __device__ __forceinline__ size_t scan_chunk_row(const ScanUnit& u) { return (size_t)(u.t0 / kScanChunk + u.seq); }
 
@@ -111,7 +111,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return y;
 }
 // dt = softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) with the exponent's rounding put back, log1p(e) as e times a
-// polynomial (a least-maximum fit of log1p(e) / e on [0, 1], 5e-9 off; with its roundings 1.6e-7).
+// polynomial (a least-maximum fit of log1p(e) / e on [0, 1], 1.8e-8 off with its fp32 coefficients; with its roundings 1.6e-7).
 __device__ __forceinline__ float2 softplus2(float2 x) {
     const float2 n = make_float2(fmaxf(-fabsf(x.x), -150.f), fmaxf(-fabsf(x.y), -150.f));   // finite: exp(-150) is 0
     const float2 t = mul2(n, all2(kLog2e));
@@ -142,7 +142,8 @@ __device__ __forceinline__ float2 logistic2(float2 x) {
 // y silu(z)
 __device__ __forceinline__ float4 gated4(float4 y, float4 z) {
     const float2 za = make_float2(z.x, z.y), zb = make_float2(z.z, z.w);
-    const float2 a = mul2(make_float2(y.x, y.y), mul2(za, logistic2(za))), b = mul2(make_float2(y.z, y.w), mul2(zb, logistic2(zb)));
+    const float2 a = mul2(make_float2(y.x, y.y), mul2(za, logistic2(za)));
+    const float2 b = mul2(make_float2(y.z, y.w), mul2(zb, logistic2(zb)));
     return make_float4(a.x, a.y, b.x, b.y);
 }
 __device__ __forceinline__ float4 add4(float4 a, float4 b) {

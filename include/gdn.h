@@ -32,9 +32,9 @@
  *   clamped to [0, T]).
  * - Thread safety: calls on different streams may run concurrently; a workspace
  *   must not be shared by calls that overlap on the device.
- * - The layout of gdn_opts_t belongs to GDN_VERSION_MAJOR.GDN_VERSION_MINOR: the library reads (and gdn_opts_init writes) the
- *   whole struct, so a program calls only a library of the minor version that it was compiled for, which
- *   gdn_version() / 100 == GDN_VERSION / 100 tells.
+ * - The layout of gdn_opts_t belongs to GDN_VERSION_MAJOR.GDN_VERSION_MINOR: the library reads (and
+ *   gdn_opts_init writes) the whole struct, so a program calls only a library of the minor version
+ *   that it was compiled for, which gdn_version() / 100 == GDN_VERSION / 100 tells.
  */
 #ifndef GDN_H_
 #define GDN_H_
@@ -484,7 +484,7 @@ gdn_status_t gdn_selective_scan_fwd(const void* u, long long u_stride, const voi
  *   slots   [rows] int32 DEVICE or NULL: row n uses state slots[n] (NULL: state n, num_slots >= rows).  A row whose slot
  *           is outside 0 .. num_slots - 1 (-1, say) is idle: its y row is zeros, no state is touched.  Two rows must not
  *           name the same state.
- * Each state is read once and written once.  opts->flags must be 0; cu_seqlens and workspace are ignored.
+ * y overlaps no input.  Each state is read once and written once.  opts->flags must be 0; cu_seqlens and workspace are ignored.
  */
 gdn_status_t gdn_selective_scan_step(const void* u, long long u_stride, const void* delta, long long delta_stride,
                                      const float* A_log, const void* Bm, long long b_stride, const void* Cm,
@@ -507,9 +507,9 @@ gdn_status_t gdn_selective_scan_step(const void* u, long long u_stride, const vo
  *   grad_A_log [D, N], grad_skip [D], grad_dt_bias [D], grad_h0 [nseq, D, N] float, each may be NULL (not computed)
  * Sums are fp32 and rounded once.  No output may overlap an input or another output.  Deterministic.
  * opts->workspace: 256-byte aligned, gdn_selective_scan_bwd_workspace_size bytes: in floats about D N for every 8 tokens
- * and every sequence (states that are kept), 3 (N + 1) D for every segment of 32 to 512 tokens and every sequence, and 2 N for
- * every token and tile of 1024 / N channels of a group (sums for grad_B and grad_C).  2 x 8192 tokens of 4096 channels of 16
- * states: 0.75 GB, where a bf16 tensor of the tokens has 0.13; the same tokens as 256 sequences 1.04 GB.
+ * and every sequence (states that are kept), 3 (N + 1) D for every segment of 32 to 512 tokens and every sequence, and 2 N
+ * for every token and tile of 1024 / N channels of a group (sums for grad_B and grad_C).  2 x 8192 tokens of 4096 channels
+ * of 16 states: 0.75 GB, where a bf16 tensor of the tokens has 0.13; the same tokens as 256 sequences 1.04 GB.
  */
 size_t gdn_selective_scan_bwd_workspace_size(int B, int T, int D, int G, int N, const gdn_opts_t* opts);
 gdn_status_t gdn_selective_scan_bwd(const void* u, long long u_stride, const void* delta, long long delta_stride,
